@@ -58,6 +58,8 @@ FAMILY_SOURCES = {
     "rownorm_tall": ("rownorm.cu",),
 }
 _ENGINE = "prm_api.cu"
+# the headers that those sources include
+_ENGINE_HEADERS = ("internal.h", "prm.h", "ptx.cuh")
 
 
 def _code_only(text: bytes) -> bytes:
@@ -74,12 +76,13 @@ def _code_only(text: bytes) -> bytes:
 
 def source_digest(family: str) -> str:
     """sha256 over the code (comments stripped) of one kernel family's
-    source, the engine and the headers: identifies the kernels and launch
+    source, the engine and their headers: identifies the kernels and launch
     plan that a stored profile of that family was taken on."""
     import hashlib
     names = set(FAMILY_SOURCES[family]) | {_ENGINE}
     h = hashlib.sha256()
-    for path in [p for p in _sources() if os.path.basename(p) in names] + _headers():
+    headers = [p for p in _headers() if os.path.basename(p) in _ENGINE_HEADERS]
+    for path in [p for p in _sources() if os.path.basename(p) in names] + headers:
         h.update(os.path.basename(path).encode())
         with open(path, "rb") as f:
             h.update(_code_only(f.read()))

@@ -1,0 +1,813 @@
+// Gated feed-forward block on the tensor cores, forward and backward:
+//   g = x Wg^T, u = x Wu^T, h = act(g) u, y = h Wd^T
+//   dh = dy Wd, dg = dh u act'(g), du = dh act(g)
+//   dx = dg Wg + du Wu, dWg = dg^T x, dWu = du^T x, dWd = dy^T h
+//
+// Four launches of one persistent tcgen05 kernel with three epilogues:
+//   GLU   : x against Wg and Wu at once. A pair of CTAs computes 256 tokens x
+//           128 features of g and of u in one accumulator (the even CTA holds
+//           the rows of Wg, the odd one those of Wu), so the activation and
+//           the product happen in registers: g and u never go to memory as
+//           GEMM outputs, only h does (and, for training, g and u once, packed)
+//   DGLU  : dh = dy Wd; dh stays in the accumulator, dg and du come out
+//   STORE : plain products: y; and dx, dWd, dWg, dWu from one tile queue
+// Operands are read in the layout the caller has: K-major or MN-major tiles
+// by TMA, without a transposed copy. dx sums over both projections in one
+// accumulator (two operand pairs, one after the other, along K).
+//
+// Rounding: products accumulate in fp32. h, dg and du are rounded to 16 bits
+// because they are operands of the next product. g and u are kept for the
+// backward pass with 16 significand bits (24-bit floats: fp32 with the low
+// byte cut off, 6 bytes for the two), so that the derivative adds no error
+// next to those roundings: with bf16 g and u the gradients were about 1.3
+// times as far from fp64.
+//
+// CTA layout, pipeline and TMEM use are those of the Newton-Schulz GEMMs
+// (ns5_gemm.cu): 320 threads, warp 0 TMA producer, warp 1 MMA issue in the
+// even CTA, warps 2-9 epilogue; 256 x 256 tiles, six 32 KB stages, two
+// accumulators.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <cmath>
+#include <mutex>
+
+#include "ffn.cuh"
+
+namespace prm {
+namespace {
+
+constexpr int PAIR_M = 256;
+constexpr int BM = 128;
+constexpr int BN = 256;
+constexpr int BN_HALF = 128;
+constexpr int BK = 64;
+constexpr int UK = 16;
+constexpr int STAGES = 6;
+constexpr uint32_t TILE_BYTES = BM * BK * 2;  // 16 KB, A and B alike
+constexpr uint32_t STAGE_BYTES = 2 * TILE_BYTES;
+constexpr uint32_t PAIR_STAGE_BYTES = 2 * STAGE_BYTES;
+constexpr uint32_t MN_CHUNK_BYTES = 64 * BK * 2;  // one 64-column MN-major box
+constexpr int NUM_THREADS = 320;
+constexpr int EPI_WARPS = 8;
+constexpr uint32_t TMEM_COLS = 2 * BN;
+constexpr uint32_t EPI_BUF_BYTES = 32 * 64;  // one 32 x 32 box of 16-bit values
+constexpr uint32_t EPI_WARP_BYTES = 2 * EPI_BUF_BYTES;
+constexpr size_t EPI_SMEM_BYTES = EPI_WARPS * EPI_WARP_BYTES;
+constexpr size_t BARRIER_BYTES = 256;
+constexpr size_t SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EPI_SMEM_BYTES + BARRIER_BYTES;
+static_assert(SMEM_BYTES <= 232448, "dynamic shared memory above the 227 KB per-block limit");
+constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;
+
+constexpr int EPI_GLU = 0, EPI_DGLU = 1, EPI_STORE = 2;
+
+// One product out = sum over its operand pairs of A B^T (B given K-major) or
+// A B (B given MN-major).
+struct FfnSegment {
+  CUtensorMap a[2];
+  CUtensorMap b[2];
+  CUtensorMap out[2];   // GLU: h; DGLU: dg, du; STORE: the product
+  int M, N;             // output extents (GLU: N = f)
+  int k_blocks[2];      // 64-long slices of each pair along K
+  int a_mn, b_mn;       // operand stored [K][M] / [K][N]
+  int tiles_m, tiles_n;
+  int splits;           // CTA pairs per tile along K
+  int64_t tile_begin;
+  float* partial;       // splits > 1: fp32 tiles
+  uint32_t* arrived;    // splits > 1: per-warp arrival counters, zero before and after the launch
+};
+
+constexpr int MAX_SEGS = 4;
+struct FfnParams {
+  FfnSegment seg[MAX_SEGS];
+  int nseg;
+  int act;
+  int64_t total;        // work items: tiles x splits
+  uint4* gu;            // packed g and u (GLU: written when not NULL; DGLU: read)
+  uint32_t* zero;       // counters to clear for the next launch
+  int zero_count;
+  int* err;
+};
+static_assert(sizeof(FfnParams) <= 4096, "kernel parameters above the 4 KB classic limit");
+
+struct Item {
+  int m0, n0;           // first output row; first output column (GLU: first feature)
+  int tile, split;
+  int kb0, kb1;
+};
+
+__device__ __forceinline__ int ffn_seg(const FfnParams& p, int64_t item) {
+  int s = 0;
+  while (s + 1 < p.nseg && item >= p.seg[s + 1].tile_begin) ++s;
+  return s;
+}
+
+template <int EPI>
+__device__ __forceinline__ Item ffn_item(const FfnSegment& sg, int64_t item) {
+  Item it;
+  const int local = static_cast<int>(item - sg.tile_begin);
+  it.split = local % sg.splits;
+  it.tile = local / sg.splits;
+  it.m0 = it.tile % sg.tiles_m * PAIR_M;
+  it.n0 = it.tile / sg.tiles_m * (EPI == EPI_GLU ? BN_HALF : BN);
+  const int kb = sg.k_blocks[0] + sg.k_blocks[1];
+  it.kb0 = static_cast<int>(static_cast<int64_t>(kb) * it.split / sg.splits);
+  it.kb1 = static_cast<int>(static_cast<int64_t>(kb) * (it.split + 1) / sg.splits);
+  return it;
+}
+
+__device__ __forceinline__ uint32_t ffn_stage_off(int row, int chunk) {
+  return static_cast<uint32_t>(row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4));
+}
+
+// Writes this lane's row of a 32 x 32 box (16 packed words) to the staging
+// box in the 64-byte swizzle of the output maps.
+__device__ __forceinline__ void ffn_stage(uint8_t* box, int lane, const uint32_t (&w)[16]) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    *reinterpret_cast<uint4*>(box + ffn_stage_off(lane, c)) =
+        make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+}
+
+// Packed g and u of one 32 x 32 box: 12 vectors of 16 bytes per lane, vector
+// k of lane l at box * 384 + k * 32 + l. Words 0..31 hold the high halves of
+// g (low 16 bits) and u (high 16 bits) of the lane's 32 columns, words 32..47
+// the next 8 bits of both, two columns to a word.
+__device__ __forceinline__ int64_t gu_box(int i0, int j0, int f) {
+  return (static_cast<int64_t>(i0 >> 5) * ((f + 31) >> 5) + (j0 >> 5)) * 384;
+}
+
+template <typename T>
+__device__ __forceinline__ void glu_chunk(const FfnParams& p, const FfnSegment& sg, int i0, int j0, uint32_t t_g,
+                                          uint32_t t_u, uint8_t* stage, int lane) {
+  float g[32], u[32];
+  tmem_load_32cols(t_g, g);
+  tmem_load_32cols(t_u, u);
+  if (i0 >= sg.M) return;
+  if (p.gu != nullptr) {
+    uint4* box = p.gu + gu_box(i0, j0, sg.N) + lane;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        w[e] = __byte_perm(__float_as_uint(g[4 * k + e]), __float_as_uint(u[4 * k + e]), 0x7632);
+      __stcs(box + k * 32, make_uint4(w[0], w[1], w[2], w[3]));
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int c = 8 * k + 2 * e;
+        const uint32_t lo = __byte_perm(__float_as_uint(g[c]), __float_as_uint(u[c]), 0x0051);
+        const uint32_t hi = __byte_perm(__float_as_uint(g[c + 1]), __float_as_uint(u[c + 1]), 0x0051);
+        w[e] = __byte_perm(lo, hi, 0x5410);
+      }
+      __stcs(box + (8 + k) * 32, make_uint4(w[0], w[1], w[2], w[3]));
+    }
+  }
+  uint32_t w[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const float a = ffn_act(p.act, g[2 * k]) * u[2 * k];
+    const float b = ffn_act(p.act, g[2 * k + 1]) * u[2 * k + 1];
+    w[k] = pack2<T>(a, b);
+  }
+  if (lane == 0) bulk_wait_group_read<0>();
+  __syncwarp();
+  ffn_stage(stage, lane, w);
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_2d(&sg.out[0], stage, j0, i0);
+    bulk_commit_group();
+  }
+}
+
+__device__ __forceinline__ void gu_load(const FfnParams& p, int i0, int j0, int f, int lane, uint4 (&raw)[12]) {
+  const uint4* box = p.gu + gu_box(i0, j0, f) + lane;
+#pragma unroll
+  for (int k = 0; k < 12; ++k) raw[k] = __ldcs(box + k * 32);
+}
+
+template <typename T>
+__device__ __forceinline__ void dglu_chunk(const FfnParams& p, const FfnSegment& sg, int i0, int j0, uint32_t t_dh,
+                                           const uint4 (&raw)[12], uint8_t* stage, int lane) {
+  float dh[32];
+  tmem_load_32cols(t_dh, dh);
+  uint32_t wg[16], wu[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    float dg[2], du[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int c = 2 * k + e;
+      const uint4 hv = raw[c >> 2];
+      const uint32_t hi = (c & 3) == 0 ? hv.x : (c & 3) == 1 ? hv.y : (c & 3) == 2 ? hv.z : hv.w;
+      const uint4 lv = raw[8 + (c >> 3)];
+      const int q = (c >> 1) & 3;
+      const uint32_t lo = q == 0 ? lv.x : q == 1 ? lv.y : q == 2 ? lv.z : lv.w;
+      // bytes: lo holds (g, u) of the even column in bytes 0, 1 and of the odd one in bytes 2, 3
+      const float g = __uint_as_float(__byte_perm(lo, hi, (c & 1) ? 0x5424 : 0x5404) & 0xFFFFFF00u);
+      const float u = __uint_as_float(__byte_perm(lo, hi, (c & 1) ? 0x7634 : 0x7614) & 0xFFFFFF00u);
+      float a, da;
+      ffn_act_grad(p.act, g, &a, &da);
+      dg[e] = dh[c] * u * da;
+      du[e] = dh[c] * a;
+    }
+    wg[k] = pack2<T>(dg[0], dg[1]);
+    wu[k] = pack2<T>(du[0], du[1]);
+  }
+  if (i0 >= sg.M) return;
+  if (lane == 0) bulk_wait_group_read<0>();
+  __syncwarp();
+  ffn_stage(stage, lane, wg);
+  ffn_stage(stage + EPI_BUF_BYTES, lane, wu);
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_2d(&sg.out[0], stage, j0, i0);
+    tma_store_2d(&sg.out[1], stage + EPI_BUF_BYTES, j0, i0);
+    bulk_commit_group();
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void store_box(const FfnSegment& sg, int i0, int j0, const float (&v)[32], uint8_t* stage,
+                                          int lane) {
+  if (i0 >= sg.M || j0 >= sg.N) return;
+  uint32_t w[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) w[k] = pack2<T>(v[2 * k], v[2 * k + 1]);
+  if (lane == 0) bulk_wait_group_read<0>();
+  __syncwarp();
+  ffn_stage(stage, lane, w);
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_2d(&sg.out[0], stage, j0, i0);
+    bulk_commit_group();
+  }
+}
+
+template <int EPI, typename T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
+    ffn_gemm_kernel(const __grid_constant__ FfnParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sA = smem;
+  uint8_t* sB = smem + STAGES * TILE_BYTES;
+  uint8_t* sEpi = smem + STAGES * STAGE_BYTES;
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(sEpi + EPI_SMEM_BYTES);
+  uint64_t* empty_bar = full_bar + STAGES;
+  uint64_t* tfull_bar = empty_bar + STAGES;
+  uint64_t* tempty_bar = tfull_bar + 2;
+  uint64_t* drain_bar = tempty_bar + 2;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain_bar + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+
+  const int warp = threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
+  const uint32_t rank = cluster_ctarank();
+  const int64_t pair_id = blockIdx.x >> 1;
+  const int64_t num_pairs = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&empty_bar[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull_bar[a], 1);
+      mbar_init(&tempty_bar[a], 2 * EPI_WARPS);
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_holder, TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  // Both CTAs' barriers must exist before either signals the other.
+  tc_fence_before_sync();
+  __syncthreads();
+  cluster_sync_all();
+  tc_fence_after_sync();
+  const uint32_t tmem_base = *tmem_holder;
+  pdl_wait();
+  if (p.zero != nullptr && blockIdx.x == 0)
+    for (int i = threadIdx.x; i < p.zero_count; i += NUM_THREADS) p.zero[i] = 0;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      uint32_t issued = 0, issued_parity = 0;
+      bool ok = true;
+      for (int64_t item = pair_id; ok && item < p.total; item += num_pairs) {
+        const FfnSegment& sg = p.seg[ffn_seg(p, item)];
+        const Item it = ffn_item<EPI>(sg, item);
+        const int m_cta = it.m0 + static_cast<int>(rank) * BM;
+        const int n_cta = EPI == EPI_GLU ? it.n0 : it.n0 + static_cast<int>(rank) * BN_HALF;
+        for (int kb = it.kb0; kb < it.kb1; ++kb) {
+          if (!wait_bounded(&empty_bar[stage], phase ^ 1u, abort_flag, p.err, WAIT_LIMIT_NS)) {
+            ok = false;
+            break;
+          }
+          if (rank == 0) mbar_arrive_expect_tx(&full_bar[stage], PAIR_STAGE_BYTES);
+          const uint32_t bar = mapa_shared(smem_u32(&full_bar[stage]), 0);
+          uint8_t* a_dst = sA + stage * TILE_BYTES;
+          uint8_t* b_dst = sB + stage * TILE_BYTES;
+          const int pair = kb >= sg.k_blocks[0] ? 1 : 0;
+          const int k = (pair ? kb - sg.k_blocks[0] : kb) * BK;
+          const CUtensorMap* ma = &sg.a[pair];
+          const CUtensorMap* mb = EPI == EPI_GLU ? &sg.b[rank] : &sg.b[pair];
+          if (EPI == EPI_STORE && sg.a_mn) {
+#pragma unroll
+            for (int q = 0; q < BM / 64; ++q)
+              tma_load_2d_pair(a_dst + q * MN_CHUNK_BYTES, ma, bar, m_cta + q * 64, k);
+          } else {
+            tma_load_2d_pair(a_dst, ma, bar, k, m_cta);
+          }
+          if (EPI == EPI_DGLU || (EPI == EPI_STORE && sg.b_mn)) {
+#pragma unroll
+            for (int q = 0; q < BN_HALF / 64; ++q)
+              tma_load_2d_pair(b_dst + q * MN_CHUNK_BYTES, mb, bar, n_cta + q * 64, k);
+          } else {
+            tma_load_2d_pair(b_dst, mb, bar, k, n_cta);
+          }
+          issued |= 1u << stage;
+          issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok && issued) {
+        // Let every load already in flight land before the CTA exits; the
+        // odd CTA's complete on the peer's barriers, so it waits an ample time.
+        if (rank == 0) {
+          for (int s = 0; s < STAGES; ++s)
+            if (issued & (1u << s)) wait_drain(&full_bar[s], (issued_parity >> s) & 1u, 50000000ull);
+        } else {
+          spin_for_ns(2000000ull);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      constexpr bool FP16 = sizeof(T) == 2 && !std::is_same<T, __nv_bfloat16>::value;
+      int stage = 0;
+      uint32_t phase = 0;
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      bool ok = true, issued_any = false;
+      for (int64_t item = pair_id; ok && item < p.total; item += num_pairs) {
+        const FfnSegment& sg = p.seg[ffn_seg(p, item)];
+        const Item it = ffn_item<EPI>(sg, item);
+        const bool a_mn = EPI == EPI_STORE && sg.a_mn;
+        const bool b_mn = EPI == EPI_DGLU || (EPI == EPI_STORE && sg.b_mn);
+        const uint32_t idesc = idesc_f16kind_f32(PAIR_M, BN, a_mn, b_mn, FP16);
+        if (!wait_bounded(&tempty_bar[acc], acc_phase ^ 1u, abort_flag, p.err, WAIT_LIMIT_NS)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
+        for (int kb = it.kb0; kb < it.kb1; ++kb) {
+          if (!wait_bounded(&full_bar[stage], phase, abort_flag, p.err, WAIT_LIMIT_NS)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const uint32_t a_addr = smem_u32(sA + stage * TILE_BYTES);
+          const uint32_t b_addr = smem_u32(sB + stage * TILE_BYTES);
+#pragma unroll
+          for (int k = 0; k < BK / UK; ++k) {
+            const uint64_t ad = a_mn ? smem_desc_sw128(a_addr + k * UK * 128, MN_CHUNK_BYTES, 1024)
+                                     : smem_desc_sw128(a_addr + k * UK * 2, 16, 1024);
+            const uint64_t bd = b_mn ? smem_desc_sw128(b_addr + k * UK * 128, MN_CHUNK_BYTES, 1024)
+                                     : smem_desc_sw128(b_addr + k * UK * 2, 16, 1024);
+            umma_bf16_pair(d_tmem, ad, bd, idesc, (kb - it.kb0) | k ? 1u : 0u);
+          }
+          issued_any = true;
+          umma_commit_pair_multicast(&empty_bar[stage], 0x3);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        umma_commit_pair_multicast(&tfull_bar[acc], 0x3);
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
+      }
+      if (!ok && issued_any) {
+        umma_commit_pair_multicast(drain_bar, 0x1);
+        wait_drain(drain_bar, 0, 50000000ull);
+      }
+    }
+  } else {
+    const int quarter = warp & 3;
+    const int ew = warp - 2;
+    const int half = ew >> 2;
+    uint8_t* stage = sEpi + ew * EPI_WARP_BYTES;
+    const uint32_t tempty_even = mapa_shared(smem_u32(&tempty_bar[0]), 0);
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int64_t item = pair_id; item < p.total; item += num_pairs) {
+      const FfnSegment& sg = p.seg[ffn_seg(p, item)];
+      const Item it = ffn_item<EPI>(sg, item);
+      const int i0 = it.m0 + static_cast<int>(rank) * BM + quarter * 32;
+      const int jh = it.n0 + half * (EPI == EPI_GLU ? BN_HALF / 2 : BN / 2);  // first column of this warp
+      uint4 raw[2][EPI == EPI_DGLU ? 12 : 1];
+      if constexpr (EPI == EPI_DGLU) {
+        if (i0 < sg.M && jh < sg.N) gu_load(p, i0, jh, sg.N, lane, raw[0]);
+      }
+      const bool got = wait_bounded(&tfull_bar[acc], acc_phase, abort_flag, p.err, WAIT_LIMIT_NS);
+      if (!__all_sync(0xffffffffu, got)) break;
+      tc_fence_after_sync();
+      const uint32_t t_row =
+          tmem_base + static_cast<uint32_t>(acc * BN) + (static_cast<uint32_t>(quarter * 32) << 16);
+      if constexpr (EPI == EPI_GLU) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int j0 = jh + q * 32;
+          if (j0 < sg.N) {
+            const uint32_t col = static_cast<uint32_t>(half * (BN_HALF / 2) + q * 32);
+            glu_chunk<T>(p, sg, i0, j0, t_row + col, t_row + BN_HALF + col, stage, lane);
+          }
+        }
+      } else if constexpr (EPI == EPI_DGLU) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int j0 = jh + q * 32;
+          if (q < 3 && i0 < sg.M && j0 + 32 < sg.N) gu_load(p, i0, j0 + 32, sg.N, lane, raw[(q + 1) & 1]);
+          if (j0 < sg.N)
+            dglu_chunk<T>(p, sg, i0, j0, t_row + static_cast<uint32_t>(half * (BN / 2) + q * 32), raw[q & 1], stage,
+                          lane);
+        }
+      } else if (sg.splits == 1) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float v[32];
+          tmem_load_32cols(t_row + static_cast<uint32_t>(half * (BN / 2) + q * 32), v);
+          store_box<T>(sg, i0, jh + q * 32, v, stage, lane);
+        }
+      } else {
+        // A part of the sum along K: this warp's 32 x 128 values go to the
+        // workspace; the warp that arrives last for them adds all parts, in
+        // order, and stores the result.
+        const int64_t region = (static_cast<int64_t>(it.tile) * 2 + rank) * EPI_WARPS + ew;
+        float4* mine = reinterpret_cast<float4*>(sg.partial) + (region * sg.splits + it.split) * (32 * 32) + lane;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float v[32];
+          tmem_load_32cols(t_row + static_cast<uint32_t>(half * (BN / 2) + q * 32), v);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            __stcg(mine + (q * 8 + k) * 32, make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]));
+        }
+        __threadfence();
+        __syncwarp();
+        uint32_t before = 0;
+        if (lane == 0) before = atomicAdd(&sg.arrived[region], 1u);
+        before = __shfl_sync(0xffffffffu, before, 0);
+        if (before + 1 == static_cast<uint32_t>(sg.splits)) {
+          __threadfence();
+          const float4* all = reinterpret_cast<const float4*>(sg.partial) + region * sg.splits * (32 * 32) + lane;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float v[32] = {};
+            for (int s = 0; s < sg.splits; ++s) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const float4 t = __ldcg(all + s * (32 * 32) + (q * 8 + k) * 32);
+                v[4 * k] += t.x;
+                v[4 * k + 1] += t.y;
+                v[4 * k + 2] += t.z;
+                v[4 * k + 3] += t.w;
+              }
+            }
+            store_box<T>(sg, i0, jh + q * 32, v, stage, lane);
+          }
+        }
+      }
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(tempty_even + static_cast<uint32_t>(acc * sizeof(uint64_t)));
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1u;
+      }
+    }
+    if (lane == 0) bulk_wait_group_all();
+  }
+  __syncwarp();
+  // No CTA may leave (or free TMEM) while its peer can still touch its
+  // barriers, shared memory or accumulators.
+  tc_fence_before_sync();
+  __syncthreads();
+  cluster_sync_all();
+  tc_fence_after_sync();
+  if (warp == 1) tmem_dealloc_pair(tmem_base, TMEM_COLS);
+}
+
+// ---------------------------------------------------------------- host side
+PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  });
+  return fn;
+}
+
+enum MapUse { MAP_ROWS, MAP_COLS, MAP_STORE };  // K-major operand, MN-major operand, output boxes
+
+// A row-major rows x cols matrix of 16-bit elements with row pitch ld.
+bool encode(CUtensorMap* map, const void* base, int dtype, int64_t rows, int64_t cols, int64_t ld, MapUse use) {
+  auto enc = map_encoder();
+  if (enc == nullptr) return false;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+  cuuint32_t box[2] = {use == MAP_STORE ? 32u : 64u, use == MAP_STORE ? 32u : use == MAP_ROWS ? 128u : 64u};
+  cuuint32_t estr[2] = {1, 1};
+  return enc(map, dtype == PRM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             use == MAP_STORE ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int EPI, typename T>
+int resident_pairs(int num_sms) {
+  static std::atomic<int> cached[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
+  const int known = cached[dev].load(std::memory_order_relaxed);
+  if (known > 0) return known;
+  if (cudaFuncSetAttribute(ffn_gemm_kernel<EPI, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(SMEM_BYTES)) != cudaSuccess)
+    return 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(num_sms & ~1));
+  cfg.blockDim = dim3(NUM_THREADS);
+  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, ffn_gemm_kernel<EPI, T>, &cfg) != cudaSuccess || n <= 0) {
+    cudaGetLastError();
+    n = num_sms / 2;
+  }
+  cached[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+template <int EPI, typename T>
+cudaError_t launch(FfnParams& p, int num_sms, cudaStream_t stream) {
+  const int pairs = resident_pairs<EPI, T>(num_sms);
+  if (pairs == 0) return cudaErrorInvalidConfiguration;
+  const unsigned grid = static_cast<unsigned>(2 * std::min<int64_t>(p.total, pairs));
+  return launch_dependent(ffn_gemm_kernel<EPI, T>, dim3(grid), dim3(NUM_THREADS), SMEM_BYTES, stream, p);
+}
+
+template <int EPI>
+cudaError_t launch(FfnParams& p, int dtype, int num_sms, cudaStream_t stream) {
+  return dtype == PRM_BF16 ? launch<EPI, __nv_bfloat16>(p, num_sms, stream)
+                           : launch<EPI, __half>(p, num_sms, stream);
+}
+
+// Extents and tile counts of one product; `splits` CTA pairs share a tile.
+void shape(FfnSegment& sg, int64_t M, int64_t N, int64_t K0, int64_t K1, bool a_mn, bool b_mn, int tile_n, int splits) {
+  sg.M = static_cast<int>(M);
+  sg.N = static_cast<int>(N);
+  sg.k_blocks[0] = static_cast<int>((K0 + BK - 1) / BK);
+  sg.k_blocks[1] = static_cast<int>((K1 + BK - 1) / BK);
+  sg.a_mn = a_mn;
+  sg.b_mn = b_mn;
+  sg.tiles_m = static_cast<int>((M + PAIR_M - 1) / PAIR_M);
+  sg.tiles_n = static_cast<int>((N + tile_n - 1) / tile_n);
+  sg.splits = splits;
+}
+
+void queue(FfnParams& p, const FfnSegment& sg) {
+  p.seg[p.nseg] = sg;
+  p.seg[p.nseg++].tile_begin = p.total;
+  p.total += static_cast<int64_t>(sg.tiles_m) * sg.tiles_n * sg.splits;
+}
+
+int64_t tiles_of(int64_t M, int64_t N) { return ((M + PAIR_M - 1) / PAIR_M) * ((N + BN - 1) / BN); }
+
+// CTA pairs per tile of an M x N product over K when it runs alone: as many
+// as leave every pair at most one item, each with at least 4 slices of K.
+constexpr int FFN_PAIRS = 76;
+int split_alone(int64_t M, int64_t N, int64_t K) {
+  const int64_t tiles = tiles_of(M, N);
+  const int64_t kb = (K + BK - 1) / BK;
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({FFN_PAIRS / tiles, kb / 4, 16})));
+}
+
+size_t partial_bytes(int64_t M, int64_t N, int splits) {
+  return splits > 1 ? static_cast<size_t>(tiles_of(M, N)) * splits * PAIR_M * BN * sizeof(float) : 0;
+}
+size_t counter_bytes(int64_t M, int64_t N) { return static_cast<size_t>(tiles_of(M, N)) * 2 * EPI_WARPS * 4; }
+
+struct FfnSizes {
+  size_t saved_h, saved;                                     // gu at saved_h
+  size_t fwd_h, fwd_partial, fwd_counters, fwd;              // offsets and size of the forward workspace
+  size_t bwd_du, bwd_partial, bwd_counters, bwd;             // dg at 0
+  int down_splits;
+  size_t bwd_counter_bytes;
+};
+
+FfnSizes sizes(int64_t T, int64_t d, int64_t f) {
+  FfnSizes s{};
+  const size_t act = round_up(static_cast<size_t>(T) * f * 2, 256);
+  s.saved_h = act;
+  s.saved = act + static_cast<size_t>((T + 31) / 32) * ((f + 31) / 32) * 384 * 16;
+  s.down_splits = split_alone(T, d, f);
+  s.fwd_partial = act;
+  s.fwd_counters = act + partial_bytes(T, d, s.down_splits);
+  s.fwd = s.fwd_counters + round_up(counter_bytes(T, d), 256);
+  s.bwd_du = act;
+  s.bwd = 2 * act;
+  return s;
+}
+
+int check(int64_t T, int64_t d, int64_t f) {
+  if (T < 0 || d < 1 || f < 1) return PRM_ERR_INVALID_ARG;
+  if (d % 8 != 0 || f % 8 != 0) return PRM_ERR_ALIGNMENT;
+  if (T >= (int64_t(1) << 31) - 256 || d >= (int64_t(1) << 24) || f >= (int64_t(1) << 24)) return PRM_ERR_UNSUPPORTED;
+  return PRM_OK;
+}
+
+}  // namespace
+}  // namespace prm
+
+extern "C" int prm_gated_ffn_sizes(int64_t tokens, int64_t d, int64_t f, size_t* saved, size_t* forward_workspace,
+                                   size_t* backward_workspace) {
+  using namespace prm;
+  if (saved == nullptr || forward_workspace == nullptr || backward_workspace == nullptr) return PRM_ERR_INVALID_ARG;
+  const int rc = check(tokens, d, f);
+  if (rc != PRM_OK) return rc;
+  const FfnSizes s = sizes(tokens, d, f);
+  *saved = s.saved;
+  *forward_workspace = s.fwd;
+  *backward_workspace = s.bwd;
+  return PRM_OK;
+}
+
+extern "C" int prm_gated_ffn_forward(const void* x, int64_t ldx, const void* w_gate, const void* w_up,
+                                     const void* w_down, void* y, void* saved, void* workspace,
+                                     size_t workspace_bytes, int64_t tokens, int64_t d, int64_t f, int act, int dtype,
+                                     void* stream) {
+  using namespace prm;
+  if ((dtype != PRM_BF16 && dtype != PRM_FP16) || act < PRM_ACT_SILU || act > PRM_ACT_GELU_TANH)
+    return PRM_ERR_INVALID_ARG;
+  int rc = check(tokens, d, f);
+  if (rc != PRM_OK || tokens == 0) return rc;
+  if (x == nullptr || w_gate == nullptr || w_up == nullptr || w_down == nullptr || y == nullptr || ldx < d)
+    return PRM_ERR_INVALID_ARG;
+  if (ldx % 8 != 0 || !aligned_to(x, 16) || !aligned_to(w_gate, 16) || !aligned_to(w_up, 16) ||
+      !aligned_to(w_down, 16) || !aligned_to(y, 16) || !aligned_to(saved, 256) || !aligned_to(workspace, 256))
+    return PRM_ERR_ALIGNMENT;
+  const FfnSizes sz = sizes(tokens, d, f);
+  if (workspace == nullptr || workspace_bytes < sz.fwd) return PRM_ERR_WORKSPACE;
+  const BlockDevice* dev;
+  if ((rc = block_device(&dev)) != PRM_OK) return rc;
+  char* ws = static_cast<char*>(workspace);
+  void* h = saved != nullptr ? saved : ws;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+
+  FfnParams p{};
+  p.err = dev->d_err;
+  p.act = act;
+  p.gu = saved != nullptr ? reinterpret_cast<uint4*>(static_cast<char*>(saved) + sz.saved_h) : nullptr;
+  uint32_t* counters = reinterpret_cast<uint32_t*>(ws + sz.fwd_counters);
+  if (sz.down_splits > 1) {
+    p.zero = counters;
+    p.zero_count = static_cast<int>(counter_bytes(tokens, d) / 4);
+  }
+  FfnSegment sg{};
+  if (!encode(&sg.a[0], x, dtype, tokens, d, ldx, MAP_ROWS) || !encode(&sg.b[0], w_gate, dtype, f, d, d, MAP_ROWS) ||
+      !encode(&sg.b[1], w_up, dtype, f, d, d, MAP_ROWS) || !encode(&sg.out[0], h, dtype, tokens, f, f, MAP_STORE))
+    return PRM_ERR_CUDA;
+  shape(sg, tokens, f, d, 0, false, false, BN_HALF, 1);
+  queue(p, sg);
+  if (launch<EPI_GLU>(p, dtype, dev->num_sms, st) != cudaSuccess) return PRM_ERR_CUDA;
+
+  FfnParams q{};
+  q.err = dev->d_err;
+  FfnSegment dn{};
+  if (!encode(&dn.a[0], h, dtype, tokens, f, f, MAP_ROWS) || !encode(&dn.b[0], w_down, dtype, d, f, f, MAP_ROWS) ||
+      !encode(&dn.out[0], y, dtype, tokens, d, d, MAP_STORE))
+    return PRM_ERR_CUDA;
+  shape(dn, tokens, d, f, 0, false, false, BN, sz.down_splits);
+  dn.partial = reinterpret_cast<float*>(ws + sz.fwd_partial);
+  dn.arrived = counters;
+  queue(q, dn);
+  return launch<EPI_STORE>(q, dtype, dev->num_sms, st) == cudaSuccess ? PRM_OK : PRM_ERR_CUDA;
+}
+
+extern "C" int prm_gated_ffn_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* w_gate,
+                                      const void* w_up, const void* w_down, const void* saved, void* dx,
+                                      void* dw_gate, void* dw_up, void* dw_down, void* workspace,
+                                      size_t workspace_bytes, int64_t tokens, int64_t d, int64_t f, int act,
+                                      int dtype, void* stream) {
+  using namespace prm;
+  if ((dtype != PRM_BF16 && dtype != PRM_FP16) || act < PRM_ACT_SILU || act > PRM_ACT_GELU_TANH)
+    return PRM_ERR_INVALID_ARG;
+  int rc = check(tokens, d, f);
+  if (rc != PRM_OK) return rc;
+  const bool weights = dw_gate != nullptr || dw_up != nullptr || dw_down != nullptr;
+  if (weights && (dw_gate == nullptr || dw_up == nullptr || dw_down == nullptr)) return PRM_ERR_INVALID_ARG;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (tokens == 0) {
+    const size_t n = static_cast<size_t>(d) * f * 2;
+    if (weights && (cudaMemsetAsync(dw_gate, 0, n, st) != cudaSuccess ||
+                    cudaMemsetAsync(dw_up, 0, n, st) != cudaSuccess ||
+                    cudaMemsetAsync(dw_down, 0, n, st) != cudaSuccess))
+      return PRM_ERR_CUDA;
+    return PRM_OK;
+  }
+  if (dy == nullptr || x == nullptr || w_gate == nullptr || w_up == nullptr || w_down == nullptr ||
+      saved == nullptr || lddy < d || ldx < d)
+    return PRM_ERR_INVALID_ARG;
+  const void* ptrs[9] = {dy, x, w_gate, w_up, w_down, dx, dw_gate, dw_up, dw_down};
+  for (const void* q : ptrs)
+    if (!aligned_to(q, 16)) return PRM_ERR_ALIGNMENT;
+  if (lddy % 8 != 0 || ldx % 8 != 0 || !aligned_to(saved, 256) || !aligned_to(workspace, 256))
+    return PRM_ERR_ALIGNMENT;
+  const FfnSizes sz = sizes(tokens, d, f);
+  if (workspace == nullptr || workspace_bytes < sz.bwd) return PRM_ERR_WORKSPACE;
+  if (dx == nullptr && !weights) return PRM_OK;
+  const BlockDevice* dev;
+  if ((rc = block_device(&dev)) != PRM_OK) return rc;
+  char* ws = static_cast<char*>(workspace);
+  void* dg = ws;
+  void* du = ws + sz.bwd_du;
+  const void* h = saved;
+
+  FfnParams p{};
+  p.err = dev->d_err;
+  p.act = act;
+  p.gu = reinterpret_cast<uint4*>(const_cast<char*>(static_cast<const char*>(saved)) + sz.saved_h);
+  FfnSegment sg{};
+  if (!encode(&sg.a[0], dy, dtype, tokens, d, lddy, MAP_ROWS) || !encode(&sg.b[0], w_down, dtype, d, f, f, MAP_COLS) ||
+      !encode(&sg.out[0], dg, dtype, tokens, f, f, MAP_STORE) ||
+      !encode(&sg.out[1], du, dtype, tokens, f, f, MAP_STORE))
+    return PRM_ERR_CUDA;
+  shape(sg, tokens, f, d, 0, false, true, BN, 1);
+  queue(p, sg);
+  if (launch<EPI_DGLU>(p, dtype, dev->num_sms, st) != cudaSuccess) return PRM_ERR_CUDA;
+
+  // dx (K = 2 f) and the weight gradients (K = tokens) from one queue, the
+  // longer sums first, so that the last tiles of the queue are short.
+  FfnParams q{};
+  q.err = dev->d_err;
+  FfnSegment segs[4] = {};
+  bool ok = true;
+  int n = 0;
+  auto add_dx = [&] {
+    if (dx == nullptr) return;
+    FfnSegment& s = segs[n++];
+    ok = ok && encode(&s.a[0], dg, dtype, tokens, f, f, MAP_ROWS) && encode(&s.a[1], du, dtype, tokens, f, f, MAP_ROWS) &&
+         encode(&s.b[0], w_gate, dtype, f, d, d, MAP_COLS) && encode(&s.b[1], w_up, dtype, f, d, d, MAP_COLS) &&
+         encode(&s.out[0], dx, dtype, tokens, d, d, MAP_STORE);
+    shape(s, tokens, d, f, f, false, true, BN, 1);
+  };
+  auto add_weight = [&](const void* a, int64_t lda, int64_t m, const void* b, int64_t ldb, int64_t nn, void* out) {
+    FfnSegment& s = segs[n++];
+    ok = ok && encode(&s.a[0], a, dtype, tokens, m, lda, MAP_COLS) &&
+         encode(&s.b[0], b, dtype, tokens, nn, ldb, MAP_COLS) && encode(&s.out[0], out, dtype, m, nn, nn, MAP_STORE);
+    shape(s, m, nn, tokens, 0, true, true, BN, 1);
+  };
+  const bool dx_first = 2 * f >= tokens;
+  if (dx_first) add_dx();
+  if (weights) {
+    add_weight(dg, f, f, x, ldx, d, dw_gate);
+    add_weight(du, f, f, x, ldx, d, dw_up);
+    add_weight(dy, lddy, d, h, f, f, dw_down);
+  }
+  if (!dx_first) add_dx();
+  if (!ok) return PRM_ERR_CUDA;
+  for (int i = 0; i < n; ++i) queue(q, segs[i]);
+  return launch<EPI_STORE>(q, dtype, dev->num_sms, st) == cudaSuccess ? PRM_OK : PRM_ERR_CUDA;
+}

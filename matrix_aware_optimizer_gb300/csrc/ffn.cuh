@@ -1,0 +1,44 @@
+// Activations of the gated feed-forward block, in fp32.
+#pragma once
+
+#include <atomic>
+#include <type_traits>
+
+#include "blocks.cuh"
+
+namespace prm {
+
+// 1 / (1 + exp(-v)).
+__device__ __forceinline__ float ffn_sigmoid(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
+
+constexpr float FFN_SQRT_2_PI = 0.7978845608028654f;      // sqrt(2 / pi)
+constexpr float FFN_SQRT_HALF = 0.7071067811865476f;
+constexpr float FFN_INV_SQRT_2PI = 0.3989422804014327f;
+
+// (1 + tanh(t)) / 2 = 1 / (1 + exp(-2 t)), so the tanh form of gelu is
+// g sigmoid(2 t): no cancellation for negative g.
+__device__ __forceinline__ float ffn_act(int act, float g) {
+  if (act == PRM_ACT_SILU) return g * ffn_sigmoid(g);
+  if (act == PRM_ACT_GELU) return 0.5f * g * (1.f + erff(g * FFN_SQRT_HALF));
+  return g * ffn_sigmoid(2.f * FFN_SQRT_2_PI * fmaf(0.044715f * g * g, g, g));
+}
+
+// act(g) and act'(g).
+__device__ __forceinline__ void ffn_act_grad(int act, float g, float* a, float* da) {
+  if (act == PRM_ACT_SILU) {
+    const float s = ffn_sigmoid(g);
+    *a = g * s;
+    *da = s * fmaf(g, 1.f - s, 1.f);
+  } else if (act == PRM_ACT_GELU) {
+    const float c = 0.5f * (1.f + erff(g * FFN_SQRT_HALF));
+    *a = g * c;
+    *da = fmaf(g * FFN_INV_SQRT_2PI, __expf(-0.5f * g * g), c);
+  } else {
+    const float t2 = 2.f * FFN_SQRT_2_PI * fmaf(0.044715f * g * g, g, g);
+    const float s = ffn_sigmoid(t2);
+    *a = g * s;
+    *da = fmaf(g * s * (1.f - s), 2.f * FFN_SQRT_2_PI * fmaf(3.f * 0.044715f * g, g, 1.f), s);
+  }
+}
+
+}  // namespace prm

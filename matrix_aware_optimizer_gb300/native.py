@@ -1,4 +1,4 @@
-"""ctypes binding of libprm (include/prm.h): the same entry points under the
+"""ctypes binding of libprm (include/prm.h, include/prm_blocks.h): the same entry points under the
 same names, argument marshalling only. Every step of the optimizer runs in the
 library's CUDA kernels; there is no Python or CPU fallback, and loading fails
 loudly when the shared library has not been built."""
@@ -37,6 +37,11 @@ PRM_MODE_PRMUON = 0
 PRM_MODE_MUONBP = 1
 PRM_NS_FORM_AUTO = 0
 PRM_NS_FORM_DIRECT = 1
+PRM_ACT_SILU = 0
+PRM_ACT_GELU = 1
+PRM_ACT_GELU_TANH = 2
+PRM_NORM_RMS = 0
+PRM_NORM_LAYER = 1
 
 ERROR_NAMES = {
     PRM_OK: "OK", PRM_ERR_INVALID_ARG: "INVALID_ARG", PRM_ERR_SHAPE: "SHAPE",
@@ -60,7 +65,29 @@ class prm_matrix_desc(ctypes.Structure):
     ]
 
 
-# name -> (restype, argtypes), mirroring include/prm.h
+class prm_block_norm_desc(ctypes.Structure):
+    _fields_ = [
+        ("rows", c_int64),
+        ("rows_per_sample", c_int64),
+        ("d", c_int64),
+        ("kind", c_int32),
+        ("stream_dtype", c_int32),
+        ("block_dtype", c_int32),
+        ("alpha", c_float),
+        ("eps", c_float),
+        ("reserved", c_int32),
+        ("post_weight", c_void_p),
+        ("pre_weight", c_void_p),
+        ("gate", c_void_p),
+        ("scale", c_void_p),
+        ("shift", c_void_p),
+        ("gate_ld", c_int64),
+        ("scale_ld", c_int64),
+        ("shift_ld", c_int64),
+    ]
+
+
+# name -> (restype, argtypes), mirroring include/prm.h and include/prm_blocks.h
 SIGNATURES = {
     "prm_create": (c_int, [POINTER(c_void_p), c_int]),
     "prm_destroy": (c_int, [c_void_p]),
@@ -92,6 +119,25 @@ SIGNATURES = {
     "prm_newton_schulz_workspace": (c_int, [c_int, c_int64, c_int64, POINTER(c_size_t)]),
     "prm_newton_schulz": (c_int, [c_void_p, c_void_p, c_int, c_int64, c_int64, POINTER(c_float), c_int,
                                   c_void_p, c_size_t, c_void_p]),
+    "prm_blocks_sync_status": (c_int, [c_void_p]),
+    "prm_gated_ffn_sizes": (c_int, [c_int64, c_int64, c_int64, POINTER(c_size_t), POINTER(c_size_t),
+                                    POINTER(c_size_t)]),
+    "prm_gated_ffn_forward": (c_int, [c_void_p, c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                      c_size_t, c_int64, c_int64, c_int64, c_int, c_int, c_void_p]),
+    "prm_gated_ffn_backward": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p, c_void_p, c_void_p,
+                                       c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_int64, c_int64,
+                                       c_int64, c_int, c_int, c_void_p]),
+    "prm_block_norm_forward": (c_int, [POINTER(prm_block_norm_desc), c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                       c_void_p]),
+    "prm_block_norm_workspace": (c_int, [POINTER(prm_block_norm_desc), POINTER(c_size_t)]),
+    "prm_block_norm_backward": (c_int, [POINTER(prm_block_norm_desc), c_void_p, c_void_p, c_void_p, c_void_p,
+                                        c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                        c_void_p, c_void_p, c_size_t, c_void_p]),
+    "prm_embedding_forward": (c_int, [c_void_p, c_int, c_void_p, c_int, c_void_p, c_int, c_int64, c_int64, c_int64,
+                                      c_float, c_void_p]),
+    "prm_embedding_backward_workspace": (c_int, [c_int64, c_int64, c_int64, POINTER(c_size_t)]),
+    "prm_embedding_backward": (c_int, [c_void_p, c_int, c_void_p, c_int, c_void_p, c_int, c_int, c_int64, c_int64,
+                                       c_int64, c_float, c_void_p, c_size_t, c_void_p]),
 }
 
 _lib = None
