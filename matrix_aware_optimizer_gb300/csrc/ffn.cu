@@ -639,6 +639,7 @@ struct FfnSizes {
 
 FfnSizes sizes(int64_t T, int64_t d, int64_t f) {
   FfnSizes s{};
+  if (T == 0) return s;
   const size_t act = round_up(static_cast<size_t>(T) * f * 2, 256);
   s.saved_h = act;
   s.saved = act + static_cast<size_t>((T + 31) / 32) * ((f + 31) / 32) * 384 * 16;
