@@ -179,8 +179,8 @@ def _norm_desc(ref, block_dtype, kind, alpha, eps, post_weight, gate, pre_weight
     """Descriptor for rows shaped like `ref` (the residual stream)."""
     if kind not in _KIND:
         raise ValueError(f"kind must be one of {sorted(_KIND)}")
-    if not ref.is_cuda or ref.dtype not in _DTYPE or block_dtype not in _DTYPE:
-        raise ValueError("tensors must be float32, bfloat16 or float16 CUDA tensors")
+    if ref.dtype not in _DTYPE or block_dtype not in _DTYPE:
+        raise ValueError("tensors must be float32, bfloat16 or float16")
     if ref.dtype != torch.float32 and ref.dtype != block_dtype:
         raise ValueError("a 16-bit residual stream needs a block of the same type")
     d = ref.shape[-1]
@@ -234,6 +234,8 @@ def block_norm(x: torch.Tensor, z: Optional[torch.Tensor] = None, kind: str = "r
 
     Returns (r, y, stats), stats for block_norm_backward.
     """
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
     block = z.dtype if z is not None else (dtype if dtype is not None else x.dtype)
     if dtype is not None and dtype != block:
         raise ValueError("dtype must be z's")
@@ -266,6 +268,8 @@ def block_norm_backward(dy: Optional[torch.Tensor], dr: Optional[torch.Tensor], 
     fp32, the others of their tensor's type."""
     if dy is None and dr is None:
         raise ValueError("dy and dr are both None")
+    if not r.is_cuda:
+        raise ValueError("r must be a CUDA tensor")
     block = z.dtype if z is not None else dy.dtype if dy is not None else r.dtype
     with _on(r.device, stream) as handle:
         desc, rows = _norm_desc(r, block, kind, alpha, 0.0, post_weight, gate, pre_weight, scale, shift)
@@ -313,8 +317,8 @@ def embedding(tokens: torch.Tensor, table: torch.Tensor, scale: float = 1.0, dty
     d] fp32, bf16 or fp16. A token outside [0, vocab) is padding: a zero row."""
     dtype = table.dtype if dtype is None else dtype
     if table.dim() != 2 or table.dtype not in _DTYPE or dtype not in _DTYPE or not table.is_contiguous() \
-            or table.device != tokens.device:
-        raise ValueError("table must be a contiguous vocab x d tensor of float32, bfloat16 or float16 with the tokens")
+            or not table.is_cuda or table.device != tokens.device:
+        raise ValueError("table must be a contiguous vocab x d CUDA tensor of float32, bfloat16 or float16")
     with _on(table.device, stream) as handle:
         tok = _tokens(tokens)
         vocab, d = table.shape

@@ -233,4 +233,8 @@ def test_tensor_api_refuses_cpu_tensors_and_wrong_shapes():
     with pytest.raises(ValueError):
         blocks.block_norm(x, alpha=0.5)
     with pytest.raises(ValueError):
+        blocks.block_norm(x, x)
+    with pytest.raises(ValueError):
+        blocks.block_norm_backward(x, None, x, x, torch.zeros(4, 4))
+    with pytest.raises(ValueError):
         blocks.block_norm_backward(None, None, x, x, torch.zeros(4, 4))
