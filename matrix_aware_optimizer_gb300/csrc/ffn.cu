@@ -82,7 +82,6 @@ constexpr int MAX_SEGS = 4;
 struct FfnParams {
   FfnSegment seg[MAX_SEGS];
   int nseg;
-  int act;
   int64_t total;        // work items: tiles x splits
   uint4* gu;            // packed g and u (GLU: written when not NULL; DGLU: read)
   uint32_t* zero;       // counters to clear for the next launch
@@ -138,7 +137,7 @@ __device__ __forceinline__ int64_t gu_box(int i0, int j0, int f) {
   return (static_cast<int64_t>(i0 >> 5) * ((f + 31) >> 5) + (j0 >> 5)) * 384;
 }
 
-template <typename T>
+template <typename T, int ACT>
 __device__ __forceinline__ void glu_chunk(const FfnParams& p, const FfnSegment& sg, int i0, int j0, uint32_t t_g,
                                           uint32_t t_u, uint8_t* stage, int lane) {
   float g[32], u[32];
@@ -171,8 +170,8 @@ __device__ __forceinline__ void glu_chunk(const FfnParams& p, const FfnSegment& 
   uint32_t w[16];
 #pragma unroll
   for (int k = 0; k < 16; ++k) {
-    const float a = ffn_act(p.act, g[2 * k]) * u[2 * k];
-    const float b = ffn_act(p.act, g[2 * k + 1]) * u[2 * k + 1];
+    const float a = ffn_act<ACT>(g[2 * k]) * u[2 * k];
+    const float b = ffn_act<ACT>(g[2 * k + 1]) * u[2 * k + 1];
     w[k] = pack2<T>(a, b);
   }
   if (lane == 0) bulk_wait_group_read<0>();
@@ -192,7 +191,7 @@ __device__ __forceinline__ void gu_load(const FfnParams& p, int i0, int j0, int 
   for (int k = 0; k < 12; ++k) raw[k] = __ldcs(box + k * 32);
 }
 
-template <typename T>
+template <typename T, int ACT>
 __device__ __forceinline__ void dglu_chunk(const FfnParams& p, const FfnSegment& sg, int i0, int j0, uint32_t t_dh,
                                            const uint4 (&raw)[12], uint8_t* stage, int lane) {
   float dh[32];
@@ -209,11 +208,12 @@ __device__ __forceinline__ void dglu_chunk(const FfnParams& p, const FfnSegment&
       const uint4 lv = raw[8 + (c >> 3)];
       const int q = (c >> 1) & 3;
       const uint32_t lo = q == 0 ? lv.x : q == 1 ? lv.y : q == 2 ? lv.z : lv.w;
-      // bytes: lo holds (g, u) of the even column in bytes 0, 1 and of the odd one in bytes 2, 3
-      const float g = __uint_as_float(__byte_perm(lo, hi, (c & 1) ? 0x5424 : 0x5404) & 0xFFFFFF00u);
-      const float u = __uint_as_float(__byte_perm(lo, hi, (c & 1) ? 0x7634 : 0x7614) & 0xFFFFFF00u);
+      // lo holds (g, u) of the even column in bytes 0, 1 and of the odd one in bytes 2, 3; the
+      // byte below the kept ones is left as it falls (below the cut of the store)
+      const float g = __uint_as_float(__byte_perm(lo, hi, (c & 1) ? 0x5424 : 0x5404));
+      const float u = __uint_as_float(__byte_perm(lo, hi, (c & 1) ? 0x7634 : 0x7614));
       float a, da;
-      ffn_act_grad(p.act, g, &a, &da);
+      ffn_act_grad<ACT>(g, &a, &da);
       dg[e] = dh[c] * u * da;
       du[e] = dh[c] * a;
     }
@@ -252,7 +252,7 @@ __device__ __forceinline__ void store_box(const FfnSegment& sg, int i0, int j0, 
   }
 }
 
-template <int EPI, typename T>
+template <int EPI, typename T, int ACT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     ffn_gemm_kernel(const __grid_constant__ FfnParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -441,7 +441,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
           const int j0 = jh + q * 32;
           if (j0 < sg.N) {
             const uint32_t col = static_cast<uint32_t>(half * (BN_HALF / 2) + q * 32);
-            glu_chunk<T>(p, sg, i0, j0, t_row + col, t_row + BN_HALF + col, stage, lane);
+            glu_chunk<T, ACT>(p, sg, i0, j0, t_row + col, t_row + BN_HALF + col, stage, lane);
           }
         }
       } else if constexpr (EPI == EPI_DGLU) {
@@ -450,7 +450,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
           const int j0 = jh + q * 32;
           if (q < 3 && i0 < sg.M && j0 + 32 < sg.N) gu_load(p, i0, j0 + 32, sg.N, lane, raw[(q + 1) & 1]);
           if (j0 < sg.N)
-            dglu_chunk<T>(p, sg, i0, j0, t_row + static_cast<uint32_t>(half * (BN / 2) + q * 32), raw[q & 1], stage,
+            dglu_chunk<T, ACT>(p, sg, i0, j0, t_row + static_cast<uint32_t>(half * (BN / 2) + q * 32), raw[q & 1], stage,
                           lane);
         }
       } else if (sg.splits == 1) {
@@ -550,14 +550,14 @@ bool encode(CUtensorMap* map, const void* base, int dtype, int64_t rows, int64_t
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int EPI, typename T>
+template <int EPI, typename T, int ACT>
 int resident_pairs(int num_sms) {
   static std::atomic<int> cached[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
   const int known = cached[dev].load(std::memory_order_relaxed);
   if (known > 0) return known;
-  if (cudaFuncSetAttribute(ffn_gemm_kernel<EPI, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  if (cudaFuncSetAttribute(ffn_gemm_kernel<EPI, T, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(SMEM_BYTES)) != cudaSuccess)
     return 0;
   cudaLaunchConfig_t cfg = {};
@@ -572,7 +572,7 @@ int resident_pairs(int num_sms) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, ffn_gemm_kernel<EPI, T>, &cfg) != cudaSuccess || n <= 0) {
+  if (cudaOccupancyMaxActiveClusters(&n, ffn_gemm_kernel<EPI, T, ACT>, &cfg) != cudaSuccess || n <= 0) {
     cudaGetLastError();
     n = num_sms / 2;
   }
@@ -580,18 +580,25 @@ int resident_pairs(int num_sms) {
   return n;
 }
 
-template <int EPI, typename T>
+template <int EPI, typename T, int ACT>
 cudaError_t launch(FfnParams& p, int num_sms, cudaStream_t stream) {
-  const int pairs = resident_pairs<EPI, T>(num_sms);
+  const int pairs = resident_pairs<EPI, T, ACT>(num_sms);
   if (pairs == 0) return cudaErrorInvalidConfiguration;
   const unsigned grid = static_cast<unsigned>(2 * std::min<int64_t>(p.total, pairs));
-  return launch_dependent(ffn_gemm_kernel<EPI, T>, dim3(grid), dim3(NUM_THREADS), SMEM_BYTES, stream, p);
+  return launch_dependent(ffn_gemm_kernel<EPI, T, ACT>, dim3(grid), dim3(NUM_THREADS), SMEM_BYTES, stream, p);
+}
+
+template <int EPI, int ACT = 0>
+cudaError_t launch(FfnParams& p, int dtype, int num_sms, cudaStream_t stream) {
+  return dtype == PRM_BF16 ? launch<EPI, __nv_bfloat16, ACT>(p, num_sms, stream)
+                           : launch<EPI, __half, ACT>(p, num_sms, stream);
 }
 
 template <int EPI>
-cudaError_t launch(FfnParams& p, int dtype, int num_sms, cudaStream_t stream) {
-  return dtype == PRM_BF16 ? launch<EPI, __nv_bfloat16>(p, num_sms, stream)
-                           : launch<EPI, __half>(p, num_sms, stream);
+cudaError_t launch_act(FfnParams& p, int act, int dtype, int num_sms, cudaStream_t stream) {
+  if (act == PRM_ACT_SILU) return launch<EPI, PRM_ACT_SILU>(p, dtype, num_sms, stream);
+  if (act == PRM_ACT_GELU) return launch<EPI, PRM_ACT_GELU>(p, dtype, num_sms, stream);
+  return launch<EPI, PRM_ACT_GELU_TANH>(p, dtype, num_sms, stream);
 }
 
 // Extents and tile counts of one product; `splits` CTA pairs share a tile.
@@ -699,7 +706,6 @@ extern "C" int prm_gated_ffn_forward(const void* x, int64_t ldx, const void* w_g
 
   FfnParams p{};
   p.err = dev->d_err;
-  p.act = act;
   p.gu = saved != nullptr ? reinterpret_cast<uint4*>(static_cast<char*>(saved) + sz.saved_h) : nullptr;
   uint32_t* counters = reinterpret_cast<uint32_t*>(ws + sz.fwd_counters);
   if (sz.down_splits > 1) {
@@ -712,7 +718,7 @@ extern "C" int prm_gated_ffn_forward(const void* x, int64_t ldx, const void* w_g
     return PRM_ERR_CUDA;
   shape(sg, tokens, f, d, 0, false, false, BN_HALF, 1);
   queue(p, sg);
-  if (launch<EPI_GLU>(p, dtype, dev->num_sms, st) != cudaSuccess) return PRM_ERR_CUDA;
+  if (launch_act<EPI_GLU>(p, act, dtype, dev->num_sms, st) != cudaSuccess) return PRM_ERR_CUDA;
 
   FfnParams q{};
   q.err = dev->d_err;
@@ -768,7 +774,6 @@ extern "C" int prm_gated_ffn_backward(const void* dy, int64_t lddy, const void* 
 
   FfnParams p{};
   p.err = dev->d_err;
-  p.act = act;
   p.gu = reinterpret_cast<uint4*>(const_cast<char*>(static_cast<const char*>(saved)) + sz.saved_h);
   FfnSegment sg{};
   if (!encode(&sg.a[0], dy, dtype, tokens, d, lddy, MAP_ROWS) || !encode(&sg.b[0], w_down, dtype, d, f, f, MAP_COLS) ||
@@ -777,7 +782,7 @@ extern "C" int prm_gated_ffn_backward(const void* dy, int64_t lddy, const void* 
     return PRM_ERR_CUDA;
   shape(sg, tokens, f, d, 0, false, true, BN, 1);
   queue(p, sg);
-  if (launch<EPI_DGLU>(p, dtype, dev->num_sms, st) != cudaSuccess) return PRM_ERR_CUDA;
+  if (launch_act<EPI_DGLU>(p, act, dtype, dev->num_sms, st) != cudaSuccess) return PRM_ERR_CUDA;
 
   // dx (K = 2 f) and the weight gradients (K = tokens) from one queue, the
   // longer sums first, so that the last tiles of the queue are short.

@@ -17,19 +17,21 @@ constexpr float FFN_INV_SQRT_2PI = 0.3989422804014327f;
 
 // (1 + tanh(t)) / 2 = 1 / (1 + exp(-2 t)), so the tanh form of gelu is
 // g sigmoid(2 t): no cancellation for negative g.
-__device__ __forceinline__ float ffn_act(int act, float g) {
-  if (act == PRM_ACT_SILU) return g * ffn_sigmoid(g);
-  if (act == PRM_ACT_GELU) return 0.5f * g * (1.f + erff(g * FFN_SQRT_HALF));
+template <int ACT>
+__device__ __forceinline__ float ffn_act(float g) {
+  if constexpr (ACT == PRM_ACT_SILU) return g * ffn_sigmoid(g);
+  if constexpr (ACT == PRM_ACT_GELU) return 0.5f * g * (1.f + erff(g * FFN_SQRT_HALF));
   return g * ffn_sigmoid(2.f * FFN_SQRT_2_PI * fmaf(0.044715f * g * g, g, g));
 }
 
 // act(g) and act'(g).
-__device__ __forceinline__ void ffn_act_grad(int act, float g, float* a, float* da) {
-  if (act == PRM_ACT_SILU) {
+template <int ACT>
+__device__ __forceinline__ void ffn_act_grad(float g, float* a, float* da) {
+  if constexpr (ACT == PRM_ACT_SILU) {
     const float s = ffn_sigmoid(g);
     *a = g * s;
     *da = s * fmaf(g, 1.f - s, 1.f);
-  } else if (act == PRM_ACT_GELU) {
+  } else if constexpr (ACT == PRM_ACT_GELU) {
     const float c = 0.5f * (1.f + erff(g * FFN_SQRT_HALF));
     *a = g * c;
     *da = fmaf(g * FFN_INV_SQRT_2PI, __expf(-0.5f * g * g), c);
