@@ -1,0 +1,880 @@
+// Backward pass of the norms around a transformer block. With n = (r - m_r) s_r,
+// q = (z - m_z) s_z, P = q post (or z), and dr arriving from r's later uses:
+//   dn  = dy (1 + scale_b) pre
+//   D   = dr + s_r (dn - n mean(dn n) [- mean(dn)])         (gradient of r in all)
+//   dx  = alpha D,   dP = gate_b D,   dq = dP post
+//   dz  = s_z (dq - q mean(dq q) [- mean(dq)])              (dP without post)
+//   dshift_b = sum dy, dscale_b = sum dy n pre, dgate_b = sum D P,
+//   dpre = sum dy (1 + scale_b) n, dpost = sum dP q         (over rows)
+// the bracketed terms for the layer norm only. Bound by memory: dy, dr, r and
+// z are read once, dx and dz written once.
+//
+// Persistent CTAs, each with a contiguous range of rows and a fixed thread
+// per column, so the column sums stay in registers and need no atomics. Rows
+// stream into a ring of shared-memory stages by bulk copies (rows are
+// contiguous, so a stage of several short rows is still one copy per array). Where a sample ends inside a CTA's range
+// the modulation sums are written out: to their place if the whole sample
+// lies in the range, else as the range's first or last partial sum, which
+// norm_join_kernel adds in order.
+//
+// Rows that bulk copies cannot fetch (d % 8 != 0, pointers off 16 bytes) or
+// of which two do not fit in shared memory are read by the consumers
+// themselves, element by element, coalesced.
+#pragma once
+
+#include <algorithm>
+#include <atomic>
+#include <type_traits>
+
+#include "block_norm.cuh"
+
+namespace prm {
+
+constexpr int SUM_GATE = 0, SUM_SCALE = 1, SUM_SHIFT = 2, SUM_POST = 3, SUM_PRE = 4, SUM_COUNT = 5;
+constexpr int MAX_STAGES = 8;
+constexpr uint64_t NORM_WAIT_NS = 2000000000ull;
+
+struct NormGradShape {
+  int size;              // see grad_threads
+  int access;
+  int tpr, groups;       // threads per row, groups of rows at once
+  int rows;              // rows per group and step
+  int stages;
+  int threads;
+  size_t smem;
+};
+
+struct NormGradParams {
+  NormParams n;
+  int64_t sample_rows;   // rows that share modulation (all rows without any)
+  int64_t ctas;
+  int groups, stages;
+  bool has[SUM_COUNT];
+  float* partial_mod;    // [cta][first, last][gate, scale, shift][d]
+  float* partial_w;      // [cta][post, pre][d]
+  int* err;
+};
+
+__device__ __forceinline__ int64_t range_begin(const NormGradParams& p, int64_t cta) {
+  return p.n.rows * cta / p.ctas;  // rows < 2^40, ctas <= 304
+}
+
+template <typename RT, typename BT>
+struct NormGradIo {
+  const BT* dy;
+  const RT* dr;
+  const RT* r;
+  const BT* z;
+  const float4* stats;
+  RT* dx;
+  BT* dz;
+  BT* mod[3];   // dgate, dscale, dshift
+};
+
+// How a thread's eight elements of a row lie: consecutive in the stage (VEC),
+// strided by the row's thread count in the stage (ELEM: d % 8 != 0, whose
+// rows start anywhere), or strided in memory (DIRECT: no ring).
+enum Access { VEC, ELEM, DIRECT };
+
+// Eight elements at p as fp32 pairs.
+__device__ __forceinline__ F8 load_f8(const float* p) {
+  const ulonglong2 a = reinterpret_cast<const ulonglong2*>(p)[0], b = reinterpret_cast<const ulonglong2*>(p)[1];
+  return {{a.x, a.y, b.x, b.y}};
+}
+template <typename T>
+__device__ __forceinline__ F8 load_f8(const T* p) {
+  const uint4 a = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+  F8 o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = unpack2<T>(w[i]);
+    o.p[i] = f2_pack(f.x, f.y);
+  }
+  return o;
+}
+// p[0], p[step], ..., zero from `left` elements on.
+template <typename T>
+__device__ __forceinline__ F8 gather_f8(const T* p, int left, int step) {
+  F8 o;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int a = 2 * k * step, b = a + step;
+    o.p[k] = f2_pack(a < left ? to_f32(p[a]) : 0.f, b < left ? to_f32(p[b]) : 0.f);
+  }
+  return o;
+}
+template <int ACCESS, typename T>
+__device__ __forceinline__ F8 read8(const T* p, int left, int step) {
+  if constexpr (ACCESS == VEC) return load_f8(p);
+  else return gather_f8(p, left, step);
+}
+template <int ACCESS, typename T>
+__device__ __forceinline__ void write8(T* p, int left, int step, const F8& v) {
+  float o[8];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 f = f2_unpack(v.p[k]);
+    o[2 * k] = f.x;
+    o[2 * k + 1] = f.y;
+  }
+  if constexpr (ACCESS == VEC) {
+    Raw8<T> raw;
+    raw.set(o);
+    raw.store(p);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e * step < left) p[e * step] = from_f32<T>(o[e]);
+  }
+}
+
+// Copies n elements from src to a stage region of `room` bytes that starts on
+// 16 bytes, at src's own offset from a 16-byte boundary; returns the bytes
+// the barrier has to wait for. The tensor starts on 16 bytes, so rounding the
+// start down stays inside it; what lies behind the last whole 16 bytes before
+// `end` (the tensor's end) is copied here element by element.
+template <typename T>
+__device__ __forceinline__ uint32_t ring_bytes(const T* src, uint32_t n, const T* end) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(src) & ~uintptr_t(15);
+  const uintptr_t last = reinterpret_cast<uintptr_t>(end) & ~uintptr_t(15);
+  uintptr_t hi = (reinterpret_cast<uintptr_t>(src + n) + 15) & ~uintptr_t(15);
+  hi = hi < last ? hi : last;
+  return hi > lo ? static_cast<uint32_t>(hi - lo) : 0u;
+}
+template <typename T>
+__device__ __forceinline__ void ring_tail(uint8_t* dst, const T* src, uint32_t n, const T* end) {
+  const T* last = reinterpret_cast<const T*>(reinterpret_cast<uintptr_t>(end) & ~uintptr_t(15));
+  const T* lo = reinterpret_cast<const T*>(reinterpret_cast<uintptr_t>(src) & ~uintptr_t(15));
+  T* out = reinterpret_cast<T*>(dst);
+  for (const T* p = last > src ? last : src; p < src + n; ++p) out[p - lo] = *p;
+}
+template <typename T>
+__device__ __forceinline__ void ring_load(uint8_t* dst, const T* src, uint32_t bytes, uint64_t* bar) {
+  if (bytes > 0)
+    bulk_load(dst, reinterpret_cast<const void*>(reinterpret_cast<uintptr_t>(src) & ~uintptr_t(15)), bytes, bar);
+}
+// Where an ELEM row that starts at src lies in its stage region.
+template <typename T>
+__device__ __forceinline__ uint32_t ring_offset(const T* src) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(src) & 15u);
+}
+
+// Threads per CTA that a kernel is compiled for: rows of up to 2048, 5120 and
+// 8192 elements.
+__host__ __device__ constexpr int grad_threads(int size) { return size == 0 ? 256 : size == 1 ? 320 : 512; }
+
+// Vectors of 8 elements per thread.
+__host__ __device__ constexpr int grad_vectors(int size) { return size == 0 ? 1 : 2; }
+
+// R: rows that a thread works on at once, to have more than one chain of
+// dependent steps and to share what a step costs besides the arithmetic.
+__host__ __device__ constexpr bool grad_far(int size, bool mod, bool w) { return w && (mod || size == 2); }
+
+template <typename RT, typename BT, int SIZE, int R, int NV, int ACCESS, bool MOD, bool W>
+__global__ void __launch_bounds__(grad_threads(SIZE), SIZE == 0 ? 2 : 1)
+    norm_backward_kernel(const __grid_constant__ NormGradParams p, const NormGradIo<RT, BT> io) {
+  constexpr bool RING = ACCESS != DIRECT;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float scratch[2][128];
+  __shared__ uint64_t full_bar[MAX_STAGES], empty_bar[MAX_STAGES];
+  __shared__ volatile int abort_flag;
+  const int tpr = p.n.tpr, d = p.n.d, groups = p.groups;
+  const int threads = tpr * groups;
+  const int step_rows = groups * R;
+  const int64_t cta = blockIdx.x;
+  // stage: rows of dy, dr, r, z and stats one after another (absent arrays
+  // take no room, ELEM regions 16 bytes more on either side of 16-byte
+  // rounding); after the ring post, pre, 1 + scale and gate of the sample at
+  // work in fp32, then the groups' exchange area
+  const uint32_t slack = ACCESS == ELEM ? 32 : 0;
+  auto region = [&](bool there, size_t size) -> uint32_t {
+    return there ? ((static_cast<uint32_t>(step_rows * d * size) + slack) & ~15u) : 0u;
+  };
+  const uint32_t by = region(io.dy != nullptr, sizeof(BT)), bdr = region(io.dr != nullptr, sizeof(RT));
+  const uint32_t br = region(io.dy != nullptr, sizeof(RT)), bz = region(io.z != nullptr, sizeof(BT));
+  const uint32_t stage_bytes = by + bdr + br + bz + (io.stats ? static_cast<uint32_t>(step_rows) * 16 : 0);
+  float* const columns = reinterpret_cast<float*>(smem + p.stages * stage_bytes);
+  const int pitch = (d + 3) & ~3;
+  float* const col_post = columns;
+  float* const col_pre = columns + (W ? pitch : 0);
+  float* const col_scale = columns + (W ? 2 * pitch : 0);
+  float* const col_gate = col_scale + (MOD ? pitch : 0);
+  uint64_t* const exchange = reinterpret_cast<uint64_t*>(columns + ((W ? 2 : 0) + (MOD ? 2 : 0)) * pitch);
+  // With both kinds of sums, or with long rows, a thread's gain sums lie in
+  // shared memory, where only it touches them: registers are short.
+  constexpr bool FAR = grad_far(SIZE, MOD, W);
+  uint64_t* const far_w = exchange + (groups > 1 ? 4 * NV * threads : 0) + threadIdx.x;
+  if constexpr (RING) {
+    if (threadIdx.x == 0) {
+      for (int s = 0; s < p.stages; ++s) {
+        mbar_init(&full_bar[s], 1);
+        mbar_init(&empty_bar[s], threads / 32);
+      }
+      abort_flag = 0;
+      fence_mbar_init();
+    }
+    __syncthreads();
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t row0 = range_begin(p, cta), row1 = range_begin(p, cta + 1);
+  const int64_t all = p.n.rows * d;
+
+  // The ring is filled by thread 0: every stage at first, then one stage per
+  // step, when every warp has left the stage before.
+  // (Its state lies in shared memory: the other threads need the registers.)
+  __shared__ struct {
+    int64_t row, sample_end;
+    int stage;
+    uint32_t phase, issued, parity;
+    bool ok;
+  } fill;
+  if (RING && threadIdx.x == 0) {
+    fill.row = row0;
+    fill.sample_end = (row0 / p.sample_rows + 1) * p.sample_rows;
+    fill.stage = 0;
+    fill.phase = fill.issued = fill.parity = 0;
+    fill.ok = true;
+  }
+  auto refill = [&] {
+    if (fill.row >= row1 || !fill.ok) return;
+    const int64_t stop = min(row1, fill.sample_end);
+    const uint32_t n = static_cast<uint32_t>(min(static_cast<int64_t>(step_rows), stop - fill.row));
+    fill.ok = wait_bounded(&empty_bar[fill.stage], fill.phase ^ 1u, &abort_flag, p.err, NORM_WAIT_NS);
+    if (!fill.ok) return;
+    uint8_t* dst = smem + fill.stage * stage_bytes;
+    uint64_t* bar = &full_bar[fill.stage];
+    const uint32_t nd = n * static_cast<uint32_t>(d);
+    const int64_t at = fill.row * d;
+    if constexpr (ACCESS == ELEM) {
+      const uint32_t ny = io.dy ? ring_bytes(io.dy + at, nd, io.dy + all) : 0u;
+      const uint32_t nr = io.dy ? ring_bytes(io.r + at, nd, io.r + all) : 0u;
+      const uint32_t ndr = io.dr ? ring_bytes(io.dr + at, nd, io.dr + all) : 0u;
+      const uint32_t nz = io.z ? ring_bytes(io.z + at, nd, io.z + all) : 0u;
+      if (fill.row + n == p.n.rows) {  // the tensors' ends
+        if (io.dy) {
+          ring_tail(dst, io.dy + at, nd, io.dy + all);
+          ring_tail(dst + by + bdr, io.r + at, nd, io.r + all);
+        }
+        if (io.dr) ring_tail(dst + by, io.dr + at, nd, io.dr + all);
+        if (io.z) ring_tail(dst + by + bdr + br, io.z + at, nd, io.z + all);
+      }
+      mbar_arrive_expect_tx(bar, ny + nr + ndr + nz + (io.stats ? n * 16 : 0u));
+      if (io.dy) {
+        ring_load(dst, io.dy + at, ny, bar);
+        ring_load(dst + by + bdr, io.r + at, nr, bar);
+      }
+      if (io.dr) ring_load(dst + by, io.dr + at, ndr, bar);
+      if (io.z) ring_load(dst + by + bdr + br, io.z + at, nz, bar);
+    } else {
+      mbar_arrive_expect_tx(bar, (io.dy ? nd * (sizeof(BT) + sizeof(RT)) : 0u) + (io.dr ? nd * sizeof(RT) : 0u) +
+                                     (io.z ? nd * sizeof(BT) : 0u) + (io.stats ? n * 16 : 0u));
+      if (io.dy) {
+        bulk_load(dst, io.dy + at, nd * sizeof(BT), bar);
+        bulk_load(dst + by + bdr, io.r + at, nd * sizeof(RT), bar);
+      }
+      if (io.dr) bulk_load(dst + by, io.dr + at, nd * sizeof(RT), bar);
+      if (io.z) bulk_load(dst + by + bdr + br, io.z + at, nd * sizeof(BT), bar);
+    }
+    if (io.stats) bulk_load(dst + by + bdr + br + bz, io.stats + fill.row, n * 16, bar);
+    fill.issued |= 1u << fill.stage;
+    fill.parity = (fill.parity & ~(1u << fill.stage)) | (fill.phase << fill.stage);
+    fill.row += n;
+    if (fill.row == fill.sample_end) fill.sample_end += p.sample_rows;
+    if (++fill.stage == p.stages) {
+      fill.stage = 0;
+      fill.phase ^= 1u;
+    }
+  };
+  if (RING && threadIdx.x == 0)
+    for (int s = 0; s < p.stages; ++s) refill();
+  const bool post = W && p.n.post != nullptr;
+  const bool pre = W && p.n.pre != nullptr;
+  const bool scale = MOD && p.has[SUM_SCALE];
+  const bool shift = MOD && p.has[SUM_SHIFT];
+  const bool gate = MOD && p.has[SUM_GATE];
+  if constexpr (W) {
+    for (int i = threadIdx.x; i < d; i += threads) {
+      if (post) col_post[i] = __ldg(p.n.post + i);
+      if (pre) col_pre[i] = __ldg(p.n.pre + i);
+    }
+  }
+
+  const int tid = tpr <= 32 ? threadIdx.x & (tpr - 1) : threadIdx.x % tpr;
+  const int group = threadIdx.x / tpr;
+  const int lane = threadIdx.x & 31;
+  int col[NV], left[NV];  // first element of each of this thread's vectors, elements from there on
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    col[v] = ACCESS == VEC ? (v * tpr + tid) * 8 : v * 8 * tpr + tid;
+    left[v] = d - col[v];
+  }
+  int turn = 0;
+  // Sums of two values per row over the row's threads. With each exchange
+  // half the lanes go on with one half of the values (6 shuffles for four
+  // values instead of 20); rows of more than a warp meet at a named barrier
+  // of their own, and each warp adds the warps' totals.
+  auto reduce = [&](float (&a)[R][2]) {
+    if (SIZE == 0 && tpr < 32) {
+      for (int o = tpr / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          a[i][0] += __shfl_xor_sync(0xffffffffu, a[i][0], o);
+          a[i][1] += __shfl_xor_sync(0xffffffffu, a[i][1], o);
+        }
+      return;
+    }
+    constexpr int VALUES = 2 * R;
+    constexpr int SPAN = 32 / VALUES;  // lanes that carry one value in the end
+    float t;
+    const bool low = lane < 16;
+    if constexpr (R == 2) {
+      const float k0 = (low ? a[0][0] : a[R - 1][0]) + __shfl_xor_sync(0xffffffffu, low ? a[R - 1][0] : a[0][0], 16);
+      const float k1 = (low ? a[0][1] : a[R - 1][1]) + __shfl_xor_sync(0xffffffffu, low ? a[R - 1][1] : a[0][1], 16);
+      const bool even = (lane & 8) == 0;
+      t = (even ? k0 : k1) + __shfl_xor_sync(0xffffffffu, even ? k1 : k0, 8);
+    } else {
+      t = (low ? a[0][0] : a[0][1]) + __shfl_xor_sync(0xffffffffu, low ? a[0][1] : a[0][0], 16);
+    }
+#pragma unroll
+    for (int o = SPAN / 2; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    int from = SPAN;  // lane distance of the values
+    if (SIZE > 0 || tpr > 32) {
+      float* s = scratch[turn];
+      turn ^= 1;
+      if ((lane & (SPAN - 1)) == 0) s[(threadIdx.x >> 5) * VALUES + lane / SPAN] = t;
+      named_barrier_sync(1 + group, tpr);
+      constexpr int MOST_WARPS = grad_threads(SIZE) / 32;
+      const int warps = tpr >> 5;
+      s += group * warps * VALUES;
+      t = 0.f;
+#pragma unroll
+      for (int k = 0; k < (MOST_WARPS + SPAN - 1) / SPAN; ++k) {
+        const int w = lane / VALUES + k * SPAN;
+        if (w < warps) t += s[w * VALUES + lane % VALUES];
+      }
+#pragma unroll
+      for (int o = 16; o >= VALUES; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+      from = 1;
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      a[i][0] = __shfl_sync(0xffffffffu, t, 2 * i * from);
+      a[i][1] = __shfl_sync(0xffffffffu, t, (2 * i + 1) * from);
+    }
+  };
+  auto join_halves = [](const uint64_t(&part)[R][2], float(&sums)[R][2]) {
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float2 f = f2_unpack(part[i][k]);
+        sums[i][k] = f.x + f.y;
+      }
+  };
+
+  F8 acc_mod[MOD ? 3 : 1][NV], acc_w[W && !FAR ? 2 : 1][NV];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+#pragma unroll
+    for (int k = 0; k < (MOD ? 3 : 1); ++k) acc_mod[k][v] = f8_zero();
+#pragma unroll
+    for (int k = 0; k < (W && !FAR ? 2 : 1); ++k) acc_w[k][v] = f8_zero();
+  }
+  if constexpr (FAR) {
+#pragma unroll
+    for (int k = 0; k < 8 * NV; ++k) far_w[k * threads] = 0;
+  }
+  // acc_w[which][v] += a b (0: post, 1: pre)
+  auto add_w = [&](int which, int v, const F8& a, const F8& b) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (FAR) {
+        uint64_t& x = far_w[((which * NV + v) * 4 + k) * threads];
+        x = f2_fma(a.p[k], b.p[k], x);
+      } else if constexpr (W) {
+        acc_w[which][v].p[k] = f2_fma(a.p[k], b.p[k], acc_w[which][v].p[k]);
+      }
+    }
+  };
+  // Adds a column sum over the CTA's row groups and hands group 0's threads
+  // the total.
+  auto across_groups = [&](F8(&acc)[NV]) {
+    if (groups == 1) return;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) exchange[(v * 4 + k) * threads + threadIdx.x] = acc[v].p[k];
+    __syncthreads();
+    if (group == 0) {
+      for (int g = 1; g < groups; ++g)
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            acc[v].p[k] = f2_add(acc[v].p[k], exchange[(v * 4 + k) * threads + g * tpr + tid]);
+    }
+    __syncthreads();
+  };
+
+  int stage = 0;
+  uint32_t phase = 0;
+  bool failed = false;
+  // The CTA's rows, sample by sample.
+  for (int64_t seg0 = row0; seg0 < row1 && !failed;) {
+    const int64_t sample = seg0 / p.sample_rows;
+    const int64_t seg1 = min(row1, (sample + 1) * p.sample_rows);
+    if constexpr (MOD) {
+      __syncthreads();  // the sample before is done with its columns
+      for (int i = threadIdx.x; i < d; i += threads) {
+        if (scale) col_scale[i] = 1.f + to_f32(static_cast<const BT*>(p.n.scale)[sample * p.n.scale_ld + i]);
+        if (gate) col_gate[i] = to_f32(static_cast<const BT*>(p.n.gate)[sample * p.n.gate_ld + i]);
+      }
+    }
+    if constexpr (MOD || W) __syncthreads();
+    const int count = static_cast<int>(seg1 - seg0);  // below 2^31: checked by the host
+    // start of this group's first row of the step
+    int64_t at0 = (seg0 + group * R) * d;
+    for (int base = 0; base < count; base += step_rows, at0 += static_cast<int64_t>(step_rows) * d) {
+      const int mine = count - base - group * R;  // rows of this step from this group's first one on
+      if constexpr (RING) {
+        if (threadIdx.x == 0 && seg0 + base != row0) refill();
+        const bool got = wait_bounded(&full_bar[stage], phase, &abort_flag, p.err, NORM_WAIT_NS);
+        failed = !__all_sync(0xffffffffu, got);
+        if (failed) break;
+      }
+      const uint8_t* src = smem + stage * stage_bytes;
+      const int in_step = group * R * d;
+      // A vector outside the row, or of a dead row, is skipped and adds
+      // nothing; the warps of long rows that are all dead skip everything.
+      if ((SIZE == 0 && tpr <= 32) || mine > 0) {
+        bool live[R][NV];
+        float4 st[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+#pragma unroll
+          for (int v = 0; v < NV; ++v) live[i][v] = left[v] > 0 && i < mine;
+          st[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (io.stats != nullptr && i < mine) {
+            if constexpr (RING)
+              st[i] = reinterpret_cast<const float4*>(src + by + bdr + br + bz)[group * R + i];
+            else
+              st[i] = __ldg(io.stats + seg0 + base + group * R + i);
+          }
+        }
+        // Vector v of row i of array `a`, whose stage region starts at `off`.
+        auto row8 = [&](auto* a, uint32_t off, int i, int v) -> F8 {
+          using T = std::remove_const_t<std::remove_pointer_t<decltype(a)>>;
+          if constexpr (ACCESS == VEC)
+            return load_f8(reinterpret_cast<const T*>(src + off) + in_step + i * d + col[v]);
+          else if constexpr (ACCESS == ELEM)
+            return gather_f8(reinterpret_cast<const T*>(src + off + ring_offset(a + (seg0 + base) * d)) + in_step +
+                                 i * d + col[v],
+                             left[v], tpr);
+          else
+            return gather_f8(a + at0 + i * d + col[v], left[v], tpr);
+        };
+        F8 D[R][NV];
+        float sums[R][2];
+        uint64_t part[R][2];
+        if (io.dy != nullptr) {
+          F8 nn[R][NV];
+#pragma unroll
+          for (int i = 0; i < R; ++i) part[i][0] = part[i][1] = 0;
+#pragma unroll
+          for (int v = 0; v < NV; ++v) {
+            F8 w, sc;
+            if (pre && left[v] > 0) w = read8<ACCESS>(col_pre + col[v], left[v], tpr);
+            if (scale && left[v] > 0) sc = read8<ACCESS>(col_scale + col[v], left[v], tpr);
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+              if (!live[i][v]) continue;
+              F8 x = row8(io.dy, 0, i, v), n = row8(io.r, by + bdr, i, v);
+              const float s0 = -st[i].x * st[i].y;
+              const uint64_t mul = f2_pack(st[i].y, st[i].y), add = f2_pack(s0, s0);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) n.p[k] = f2_fma(n.p[k], mul, add);
+              if constexpr (MOD) {
+                if (shift) {
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) acc_mod[SUM_SHIFT][v].p[k] = f2_add(acc_mod[SUM_SHIFT][v].p[k], x.p[k]);
+                }
+                if (scale) {
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    const uint64_t m = pre ? f2_mul(n.p[k], w.p[k]) : n.p[k];
+                    acc_mod[SUM_SCALE][v].p[k] = f2_fma(x.p[k], m, acc_mod[SUM_SCALE][v].p[k]);
+                    x.p[k] = f2_mul(x.p[k], sc.p[k]);
+                  }
+                }
+              }
+              if (pre) {
+                add_w(1, v, x, n);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) x.p[k] = f2_mul(x.p[k], w.p[k]);
+              }
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                part[i][0] = f2_fma(x.p[k], n.p[k], part[i][0]);
+                part[i][1] = f2_add(part[i][1], x.p[k]);
+              }
+              D[i][v] = x;
+              nn[i][v] = n;
+            }
+          }
+          join_halves(part, sums);
+          reduce(sums);
+#pragma unroll
+          for (int i = 0; i < R; ++i) {
+            const float m1 = -sums[i][0] * p.n.inv_d * st[i].y;
+            const float m2 = p.n.layer ? -sums[i][1] * p.n.inv_d * st[i].y : 0.f;
+            const uint64_t M1 = f2_pack(m1, m1), M2 = f2_pack(m2, m2), S = f2_pack(st[i].y, st[i].y);
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+              if (!live[i][v]) continue;
+              F8 x = f8_zero();
+              if (io.dr != nullptr) x = row8(io.dr, by, i, v);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                x.p[k] = f2_fma(nn[i][v].p[k], M1, x.p[k]);
+                if (p.n.layer) x.p[k] = f2_add(x.p[k], M2);
+                D[i][v].p[k] = f2_fma(S, D[i][v].p[k], x.p[k]);
+              }
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+              if (live[i][v]) D[i][v] = row8(io.dr, by, i, v);
+        }
+        if (io.dx != nullptr) {
+          const uint64_t alpha = f2_pack(p.n.alpha, p.n.alpha);
+#pragma unroll
+          for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+              if (!live[i][v]) continue;
+              F8 o;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) o.p[k] = f2_mul(alpha, D[i][v].p[k]);
+              write8<ACCESS>(io.dx + at0 + i * d + col[v], left[v], tpr, o);
+            }
+        }
+        if (io.z != nullptr) {
+          F8 q[R][NV];
+          if (post || gate) {
+#pragma unroll
+            for (int i = 0; i < R; ++i) part[i][0] = part[i][1] = 0;
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+              F8 w, g;
+              if (post && left[v] > 0) w = read8<ACCESS>(col_post + col[v], left[v], tpr);
+              if (gate && left[v] > 0) g = read8<ACCESS>(col_gate + col[v], left[v], tpr);
+#pragma unroll
+              for (int i = 0; i < R; ++i) {
+                if (!live[i][v]) continue;
+                F8 x = row8(io.z, by + bdr + br, i, v);
+                if (post) {
+                  const float s0 = -st[i].z * st[i].w;
+                  const uint64_t mul = f2_pack(st[i].w, st[i].w), add = f2_pack(s0, s0);
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) x.p[k] = f2_fma(x.p[k], mul, add);
+                }
+                if constexpr (MOD) {
+                  if (gate) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                      const uint64_t P = post ? f2_mul(x.p[k], w.p[k]) : x.p[k];
+                      acc_mod[SUM_GATE][v].p[k] = f2_fma(D[i][v].p[k], P, acc_mod[SUM_GATE][v].p[k]);
+                      D[i][v].p[k] = f2_mul(D[i][v].p[k], g.p[k]);
+                    }
+                  }
+                }
+                if (post) {
+                  add_w(0, v, D[i][v], x);
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    D[i][v].p[k] = f2_mul(D[i][v].p[k], w.p[k]);
+                    part[i][0] = f2_fma(D[i][v].p[k], x.p[k], part[i][0]);
+                    part[i][1] = f2_add(part[i][1], D[i][v].p[k]);
+                  }
+                }
+                q[i][v] = x;
+              }
+            }
+          }
+          if (post) {
+            join_halves(part, sums);
+            reduce(sums);
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+              const float m1 = -sums[i][0] * p.n.inv_d * st[i].w;
+              const float m2 = p.n.layer ? -sums[i][1] * p.n.inv_d * st[i].w : 0.f;
+              const uint64_t M1 = f2_pack(m1, m1), M2 = f2_pack(m2, m2), S = f2_pack(st[i].w, st[i].w);
+#pragma unroll
+              for (int v = 0; v < NV; ++v) {
+                if (!live[i][v]) continue;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) D[i][v].p[k] = f2_fma(S, D[i][v].p[k], f2_fma(q[i][v].p[k], M1, M2));
+              }
+            }
+          }
+          if (io.dz != nullptr) {
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+#pragma unroll
+              for (int v = 0; v < NV; ++v)
+                if (live[i][v]) write8<ACCESS>(io.dz + at0 + i * d + col[v], left[v], tpr, D[i][v]);
+          }
+        }
+      }
+      if constexpr (RING) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty_bar[stage]);
+        if (++stage == p.stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (failed) break;
+    if constexpr (MOD) {
+      // the end of the sample, or of this CTA's part of it
+      const bool before = sample * p.sample_rows < row0, after = (sample + 1) * p.sample_rows > row1;
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        if (!p.has[k]) continue;
+        across_groups(acc_mod[k]);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          if (group == 0 && left[v] > 0) {
+            if (before || after)
+              write8<ACCESS>(
+                  p.partial_mod + ((cta * 2 + (before ? 0 : 1)) * 3 + k) * static_cast<int64_t>(pitch) + col[v],
+                  left[v], tpr, acc_mod[k][v]);
+            else
+              write8<ACCESS>(io.mod[k] + sample * d + col[v], left[v], tpr, acc_mod[k][v]);
+          }
+          acc_mod[k][v] = f8_zero();
+        }
+      }
+    }
+    seg0 = seg1;
+  }
+  if (failed) {
+    // a wait gave up: let the copies in flight land before the CTA exits
+    if (RING && threadIdx.x == 0)
+      for (int s = 0; s < p.stages; ++s)
+        if (fill.issued & (1u << s)) wait_drain(&full_bar[s], (fill.parity >> s) & 1u, 50000000ull);
+    return;
+  }
+  if constexpr (W) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (!p.has[SUM_POST + k]) continue;
+      F8 total[NV];
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        if constexpr (FAR) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) total[v].p[j] = far_w[((k * NV + v) * 4 + j) * threads];
+        } else {
+          total[v] = acc_w[k][v];
+        }
+      }
+      across_groups(total);
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        if (group == 0 && left[v] > 0)
+          write8<ACCESS>(p.partial_w + (cta * 2 + k) * static_cast<int64_t>(pitch) + col[v], left[v], tpr, total[v]);
+    }
+  }
+}
+
+// out[row][column] = sum of partial sums, in CTA order. The first
+// (ctas - 1) x ceil(d / 256) blocks look after the samples that cross CTA
+// ranges: the one for range c takes the sample, if any, that began in range
+// c - 1 and goes on into c, and adds its partial sums, a thread per column
+// (a sample inside one range is complete already). The others add the gains'
+// partial sums of all CTAs, 32 columns a block: each of 8 warps adds every
+// eighth, and warp 0 adds their totals.
+template <typename BT>
+__global__ void __launch_bounds__(256) norm_join_kernel(const __grid_constant__ NormGradParams p, BT* dgate, BT* dscale,
+                                                        BT* dshift, float* dpost, float* dpre, int mod_blocks) {
+  __shared__ float part[8][33];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t d = p.n.d, pitch = (d + 3) & ~int64_t(3);
+  if (static_cast<int>(blockIdx.x) < mod_blocks) {
+    const int wide = static_cast<int>((d + 255) / 256);
+    const int64_t c = 1 + blockIdx.x / wide;
+    const int64_t row = range_begin(p, c);
+    const int64_t sample = row / p.sample_rows;
+    const int64_t begin = sample * p.sample_rows, end = begin + p.sample_rows;
+    const int64_t col = static_cast<int64_t>(blockIdx.x % wide) * 256 + threadIdx.x;
+    if (row == begin || range_begin(p, c - 1) > begin || col >= d) return;
+    BT* const out[3] = {dgate, dscale, dshift};
+    float s[3];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) s[k] = p.has[k] ? p.partial_mod[((c - 1) * 6 + 3 + k) * pitch + col] : 0.f;
+    // the last range that holds a row of the sample: range i begins at floor(rows i / ctas)
+    const int last = static_cast<int>((end * p.ctas - 1) / p.n.rows);
+    const float* from = p.partial_mod + col;
+#pragma unroll 8
+    for (int i = static_cast<int>(c); i <= last; ++i) {
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+        if (p.has[k]) s[k] += from[(i * 6 + k) * pitch];
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+      if (p.has[k]) out[k][sample * d + col] = from_f32<BT>(s[k]);
+    return;
+  }
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int job = static_cast<int>(blockIdx.x) - mod_blocks;
+  const int tiles = static_cast<int>((d + 31) / 32);
+  const int k = job / tiles;  // 0: post, 1: pre
+  const int64_t col = static_cast<int64_t>(job - k * tiles) * 32 + lane;
+  if (!p.has[SUM_POST + k]) return;
+  const float* from = p.partial_w + k * pitch + col;
+  float s = 0.f;
+  if (col < d) {
+#pragma unroll 8
+    for (int64_t i = warp; i < p.ctas; i += 8) s += from[i * 2 * pitch];
+  }
+  part[warp][lane] = s;
+  __syncthreads();
+  if (warp != 0 || col >= d) return;
+  for (int w = 1; w < 8; ++w) s += part[w][lane];
+  (k == 0 ? dpost : dpre)[col] = s;
+}
+
+struct NormGradArgs {
+  const void *dy, *dr, *r, *z;
+  const float* stats;
+  void *dx, *dz;
+  float* dpost;
+  void* dgate;
+  float* dpre;
+  void *dscale, *dshift;
+};
+
+// Geometry for rows of d elements whose `arrays` arrays take row_bytes in
+// all. Rows of up to 2048 elements: two CTAs of 256 threads per SM, each with
+// half its shared memory.
+inline NormGradShape grad_shape(int64_t d, size_t row_bytes, int arrays, bool vec, bool ring, bool w, bool mod) {
+  NormGradShape s{};
+  s.size = d <= 2048 ? 0 : d <= 5120 ? 1 : 2;
+  const int nv = grad_vectors(s.size);
+  const int vectors = static_cast<int>((d + 8 * nv - 1) / (8 * nv));
+  if (vectors <= 32) {
+    s.tpr = 2;
+    while (s.tpr < vectors) s.tpr *= 2;
+  } else {
+    s.tpr = (vectors + 31) / 32 * 32;
+  }
+  s.groups = s.size == 2 ? 1 : std::max(1, grad_threads(s.size) / s.tpr);
+  s.threads = s.tpr * s.groups;
+  // shared memory behind the ring, for a kernel with these sums
+  auto behind = [&](bool w, bool mod) {
+    return ((w ? 2 : 0) + (mod ? 2 : 0)) * ((d + 3) & ~int64_t(3)) * sizeof(float) +
+           (s.groups > 1 ? static_cast<size_t>(s.threads) * 8 * nv * sizeof(float) : 0) +
+           (grad_far(s.size, mod, w) ? static_cast<size_t>(s.threads) * 16 * nv * sizeof(float) : 0);
+  };
+  const size_t extra = behind(w, mod);
+  s.access = vec ? VEC : ELEM;
+  // two stages at least, in half an SM's shared memory, else in all of it,
+  // else one stage
+  const size_t half = 110 * 1024, whole = 220 * 1024;
+  const struct {
+    int rows, stages;
+    size_t room;
+  } tries[4] = {{2, 2, half}, {1, 2, half}, {1, 2, whole}, {1, 1, whole}};
+  for (int k = s.size == 0 ? 0 : 2; ring && k < 4; ++k) {
+    s.rows = tries[k].rows;
+    const size_t stage = row_bytes * s.groups * s.rows + (vec ? 0 : 32 * arrays);
+    s.stages =
+        extra < tries[k].room ? static_cast<int>(std::min<size_t>((tries[k].room - extra) / stage, MAX_STAGES)) : 0;
+    s.smem = stage * s.stages + extra;
+    if (s.stages >= tries[k].stages && (vec || s.rows == 1)) return s;
+  }
+  s.access = DIRECT;
+  s.rows = 1;
+  s.stages = 0;
+  s.smem = behind(true, true);  // compiled for every sum
+  return s;
+}
+
+inline size_t row_bytes(const prm_block_norm_desc& c, bool dy, bool dr, bool z, bool stats) {
+  const size_t rb = dtype_bytes(c.stream_dtype) * c.d, bb = dtype_bytes(c.block_dtype) * c.d;
+  return (dy ? rb + bb : 0) + (dr ? rb : 0) + (z ? bb : 0) + (stats ? 16 : 0);
+}
+
+template <typename RT, typename BT, int SIZE, int R, int NV, int ACCESS, bool MOD, bool W>
+cudaError_t launch_backward(NormGradParams& p, const NormGradShape& s, const NormGradArgs& a, cudaStream_t stream) {
+  auto kernel = norm_backward_kernel<RT, BT, SIZE, R, NV, ACCESS, MOD, W>;
+  if (s.smem > 40 * 1024) {
+    static std::atomic<bool> set[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!set[dev].load(std::memory_order_relaxed)) {
+      cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 224 * 1024);
+      if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+      if (e != cudaSuccess) return e;
+      set[dev].store(true, std::memory_order_relaxed);
+    }
+  }
+  const NormGradIo<RT, BT> io{static_cast<const BT*>(a.dy), static_cast<const RT*>(a.dr), static_cast<const RT*>(a.r),
+                              static_cast<const BT*>(a.z), reinterpret_cast<const float4*>(a.stats),
+                              static_cast<RT*>(a.dx), static_cast<BT*>(a.dz),
+                              {static_cast<BT*>(a.dgate), static_cast<BT*>(a.dscale), static_cast<BT*>(a.dshift)}};
+  cudaError_t e = launch_dependent(kernel, dim3(static_cast<unsigned>(p.ctas)), dim3(s.threads), s.smem, stream, p, io);
+  if (e != cudaSuccess) return e;
+  const bool mods = MOD && (p.has[SUM_GATE] || p.has[SUM_SCALE] || p.has[SUM_SHIFT]);
+  const int d = p.n.d;
+  const int mod_blocks = mods ? static_cast<int>(p.ctas - 1) * ((d + 255) / 256) : 0;
+  const int w_blocks = W && (p.has[SUM_POST] || p.has[SUM_PRE]) ? 2 * ((d + 31) / 32) : 0;
+  if (mod_blocks + w_blocks == 0) return cudaSuccess;
+  return launch_dependent(norm_join_kernel<BT>, dim3(mod_blocks + w_blocks), dim3(256), 0, stream, p, io.mod[0],
+                          io.mod[1], io.mod[2], a.dpost, a.dpre, mod_blocks);
+}
+
+template <typename RT, typename BT>
+cudaError_t launch_shape(NormGradParams& p, const NormGradShape& s, const NormGradArgs& a, cudaStream_t stream) {
+  const bool mod = p.has[SUM_GATE] || p.has[SUM_SCALE] || p.has[SUM_SHIFT];
+  const bool w = p.has[SUM_POST] || p.has[SUM_PRE];
+  using std::integral_constant;
+  auto go = [&](auto size, auto rows) {
+    constexpr int S = decltype(size)::value, R = decltype(rows)::value, V = grad_vectors(S);
+    if (mod && w) return launch_backward<RT, BT, S, R, V, VEC, true, true>(p, s, a, stream);
+    if (mod) return launch_backward<RT, BT, S, R, V, VEC, true, false>(p, s, a, stream);
+    if (w) return launch_backward<RT, BT, S, R, V, VEC, false, true>(p, s, a, stream);
+    return launch_backward<RT, BT, S, R, V, VEC, false, false>(p, s, a, stream);
+  };
+  auto strided = [&](auto size) {
+    constexpr int S = decltype(size)::value, V = grad_vectors(S);
+    return s.access == ELEM ? launch_backward<RT, BT, S, 1, V, ELEM, true, true>(p, s, a, stream)
+                            : launch_backward<RT, BT, S, 1, V, DIRECT, true, true>(p, s, a, stream);
+  };
+  if (s.access != VEC)
+    return s.size == 0   ? strided(integral_constant<int, 0>{})
+           : s.size == 1 ? strided(integral_constant<int, 1>{})
+                         : strided(integral_constant<int, 2>{});
+  if (s.size == 0)
+    return s.rows == 2 ? go(integral_constant<int, 0>{}, integral_constant<int, 2>{})
+                       : go(integral_constant<int, 0>{}, integral_constant<int, 1>{});
+  return s.size == 1 ? go(integral_constant<int, 1>{}, integral_constant<int, 1>{})
+                     : go(integral_constant<int, 2>{}, integral_constant<int, 1>{});
+}
+
+// Defined per pair of types, each pair's kernels in a translation unit of a
+// few (norm_grad_*.cu) to keep the build parallel.
+template <typename RT, typename BT>
+cudaError_t norm_grad_launch(NormGradParams& p, const NormGradShape& s, const NormGradArgs& a, cudaStream_t stream);
+
+}  // namespace prm

@@ -72,17 +72,18 @@ struct FfnSegment {
   int k_blocks[2];      // 64-long slices of each pair along K
   int a_mn, b_mn;       // operand stored [K][M] / [K][N]
   int tiles_m, tiles_n;
-  int splits;           // CTA pairs per tile along K
-  int64_t tile_begin;
-  float* partial;       // splits > 1: fp32 tiles
-  uint32_t* arrived;    // splits > 1: per-warp arrival counters, zero before and after the launch
+  int whole;            // tiles that one CTA pair computes; the rest are split
+  int splits;           // pairs per split tile, each over a part of K
+  int64_t item_begin;
+  float* partial;       // splits > 1: fp32 parts of the split tiles
+  uint32_t* arrived;    // splits > 1: arrivals per warp region, zero before the launch
 };
 
 constexpr int MAX_SEGS = 4;
 struct FfnParams {
   FfnSegment seg[MAX_SEGS];
   int nseg;
-  int64_t total;        // work items: tiles x splits
+  int64_t total;        // work items: whole tiles and parts of split ones
   uint4* gu;            // packed g and u (GLU: written when not NULL; DGLU: read)
   uint32_t* zero;       // counters to clear for the next launch
   int zero_count;
@@ -92,27 +93,44 @@ static_assert(sizeof(FfnParams) <= 4096, "kernel parameters above the 4 KB class
 
 struct Item {
   int m0, n0;           // first output row; first output column (GLU: first feature)
-  int tile, split;
+  int split_tile, split;  // split tiles: index among them and part; else -1
   int kb0, kb1;
 };
 
+// Tiles run in groups of GROUP_M row tiles, rows fastest, so that the ~76
+// pairs at work cover a block of about 8 x 9 tiles: per slice of K they share
+// half the operand bytes of a 32 x 2 block.
+constexpr int GROUP_M = 8;
+
 __device__ __forceinline__ int ffn_seg(const FfnParams& p, int64_t item) {
   int s = 0;
-  while (s + 1 < p.nseg && item >= p.seg[s + 1].tile_begin) ++s;
+  while (s + 1 < p.nseg && item >= p.seg[s + 1].item_begin) ++s;
   return s;
 }
 
 template <int EPI>
 __device__ __forceinline__ Item ffn_item(const FfnSegment& sg, int64_t item) {
   Item it;
-  const int local = static_cast<int>(item - sg.tile_begin);
-  it.split = local % sg.splits;
-  it.tile = local / sg.splits;
-  it.m0 = it.tile % sg.tiles_m * PAIR_M;
-  it.n0 = it.tile / sg.tiles_m * (EPI == EPI_GLU ? BN_HALF : BN);
+  int tile = static_cast<int>(item - sg.item_begin);
   const int kb = sg.k_blocks[0] + sg.k_blocks[1];
-  it.kb0 = static_cast<int>(static_cast<int64_t>(kb) * it.split / sg.splits);
-  it.kb1 = static_cast<int>(static_cast<int64_t>(kb) * (it.split + 1) / sg.splits);
+  it.split_tile = -1;
+  it.split = 0;
+  it.kb0 = 0;
+  it.kb1 = kb;
+  if (EPI == EPI_STORE && tile >= sg.whole) {
+    const int q = tile - sg.whole;
+    it.split_tile = q / sg.splits;
+    it.split = q - it.split_tile * sg.splits;
+    it.kb0 = static_cast<int>(static_cast<int64_t>(kb) * it.split / sg.splits);
+    it.kb1 = static_cast<int>(static_cast<int64_t>(kb) * (it.split + 1) / sg.splits);
+    tile = sg.whole + it.split_tile;
+  }
+  const int group = tile / (GROUP_M * sg.tiles_n);
+  const int rows = min(GROUP_M, sg.tiles_m - group * GROUP_M);
+  const int in_group = tile - group * GROUP_M * sg.tiles_n;
+  const int tn = in_group / rows;
+  it.m0 = (group * GROUP_M + in_group - tn * rows) * PAIR_M;
+  it.n0 = tn * (EPI == EPI_GLU ? BN_HALF : BN);
   return it;
 }
 
@@ -453,7 +471,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
             dglu_chunk<T, ACT>(p, sg, i0, j0, t_row + static_cast<uint32_t>(half * (BN / 2) + q * 32), raw[q & 1], stage,
                           lane);
         }
-      } else if (sg.splits == 1) {
+      } else if (it.split_tile < 0) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           float v[32];
@@ -464,7 +482,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         // A part of the sum along K: this warp's 32 x 128 values go to the
         // workspace; the warp that arrives last for them adds all parts, in
         // order, and stores the result.
-        const int64_t region = (static_cast<int64_t>(it.tile) * 2 + rank) * EPI_WARPS + ew;
+        const int64_t region = (static_cast<int64_t>(it.split_tile) * 2 + rank) * EPI_WARPS + ew;
         float4* mine = reinterpret_cast<float4*>(sg.partial) + (region * sg.splits + it.split) * (32 * 32) + lane;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -601,8 +619,34 @@ cudaError_t launch_act(FfnParams& p, int act, int dtype, int num_sms, cudaStream
   return launch<EPI, PRM_ACT_GELU_TANH>(p, dtype, num_sms, stream);
 }
 
-// Extents and tile counts of one product; `splits` CTA pairs share a tile.
-void shape(FfnSegment& sg, int64_t M, int64_t N, int64_t K0, int64_t K1, bool a_mn, bool b_mn, int tile_n, int splits) {
+int64_t tiles_of(int64_t M, int64_t N) { return ((M + PAIR_M - 1) / PAIR_M) * ((N + BN - 1) / BN); }
+
+// The tiles of a product that runs alone go to the pairs in waves. Where the
+// last wave is not full, its tiles are split along K over the idle pairs:
+// 256 tiles on 76 pairs take 3.5 tile times instead of 4.
+constexpr int FFN_PAIRS = 76;
+constexpr int MIN_PART = 4;  // slices of K in a part
+struct Split {
+  int64_t whole;
+  int splits;
+};
+Split split_last_wave(int64_t M, int64_t N, int64_t K) {
+  const int64_t tiles = tiles_of(M, N);
+  const int64_t rest = tiles % FFN_PAIRS;
+  const int64_t kb = (K + BK - 1) / BK;
+  const int64_t s = rest == 0 ? 1 : std::min<int64_t>({FFN_PAIRS / rest, kb / MIN_PART, 16});
+  return s < 2 ? Split{tiles, 1} : Split{tiles - rest, static_cast<int>(s)};
+}
+size_t partial_bytes(int64_t M, int64_t N, const Split& s) {
+  return static_cast<size_t>(tiles_of(M, N) - s.whole) * s.splits * PAIR_M * BN * sizeof(float);
+}
+size_t counter_bytes(int64_t M, int64_t N, const Split& s) {
+  return static_cast<size_t>(tiles_of(M, N) - s.whole) * 2 * EPI_WARPS * 4;
+}
+
+// Extents and tile counts of one product, and its place in the queue.
+void queue(FfnParams& p, FfnSegment& sg, int64_t M, int64_t N, int64_t K0, int64_t K1, bool a_mn, bool b_mn,
+           int tile_n) {
   sg.M = static_cast<int>(M);
   sg.N = static_cast<int>(N);
   sg.k_blocks[0] = static_cast<int>((K0 + BK - 1) / BK);
@@ -611,37 +655,21 @@ void shape(FfnSegment& sg, int64_t M, int64_t N, int64_t K0, int64_t K1, bool a_
   sg.b_mn = b_mn;
   sg.tiles_m = static_cast<int>((M + PAIR_M - 1) / PAIR_M);
   sg.tiles_n = static_cast<int>((N + tile_n - 1) / tile_n);
-  sg.splits = splits;
+  const int tiles = sg.tiles_m * sg.tiles_n;
+  if (sg.splits < 2) {
+    sg.whole = tiles;
+    sg.splits = 1;
+  }
+  sg.item_begin = p.total;
+  p.total += sg.whole + static_cast<int64_t>(tiles - sg.whole) * sg.splits;
+  p.seg[p.nseg++] = sg;
 }
-
-void queue(FfnParams& p, const FfnSegment& sg) {
-  p.seg[p.nseg] = sg;
-  p.seg[p.nseg++].tile_begin = p.total;
-  p.total += static_cast<int64_t>(sg.tiles_m) * sg.tiles_n * sg.splits;
-}
-
-int64_t tiles_of(int64_t M, int64_t N) { return ((M + PAIR_M - 1) / PAIR_M) * ((N + BN - 1) / BN); }
-
-// CTA pairs per tile of an M x N product over K when it runs alone: as many
-// as leave every pair at most one item, each with at least 4 slices of K.
-constexpr int FFN_PAIRS = 76;
-int split_alone(int64_t M, int64_t N, int64_t K) {
-  const int64_t tiles = tiles_of(M, N);
-  const int64_t kb = (K + BK - 1) / BK;
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({FFN_PAIRS / tiles, kb / 4, 16})));
-}
-
-size_t partial_bytes(int64_t M, int64_t N, int splits) {
-  return splits > 1 ? static_cast<size_t>(tiles_of(M, N)) * splits * PAIR_M * BN * sizeof(float) : 0;
-}
-size_t counter_bytes(int64_t M, int64_t N) { return static_cast<size_t>(tiles_of(M, N)) * 2 * EPI_WARPS * 4; }
 
 struct FfnSizes {
   size_t saved_h, saved;                                     // gu at saved_h
   size_t fwd_h, fwd_partial, fwd_counters, fwd;              // offsets and size of the forward workspace
   size_t bwd_du, bwd_partial, bwd_counters, bwd;             // dg at 0
-  int down_splits;
-  size_t bwd_counter_bytes;
+  Split down;
 };
 
 FfnSizes sizes(int64_t T, int64_t d, int64_t f) {
@@ -650,10 +678,10 @@ FfnSizes sizes(int64_t T, int64_t d, int64_t f) {
   const size_t act = round_up(static_cast<size_t>(T) * f * 2, 256);
   s.saved_h = act;
   s.saved = act + static_cast<size_t>((T + 31) / 32) * ((f + 31) / 32) * 384 * 16;
-  s.down_splits = split_alone(T, d, f);
+  s.down = split_last_wave(T, d, f);
   s.fwd_partial = act;
-  s.fwd_counters = act + partial_bytes(T, d, s.down_splits);
-  s.fwd = s.fwd_counters + round_up(counter_bytes(T, d), 256);
+  s.fwd_counters = act + partial_bytes(T, d, s.down);
+  s.fwd = s.fwd_counters + round_up(counter_bytes(T, d, s.down), 256);
   s.bwd_du = act;
   s.bwd = 2 * act;
   return s;
@@ -708,16 +736,13 @@ extern "C" int prm_gated_ffn_forward(const void* x, int64_t ldx, const void* w_g
   p.err = dev->d_err;
   p.gu = saved != nullptr ? reinterpret_cast<uint4*>(static_cast<char*>(saved) + sz.saved_h) : nullptr;
   uint32_t* counters = reinterpret_cast<uint32_t*>(ws + sz.fwd_counters);
-  if (sz.down_splits > 1) {
-    p.zero = counters;
-    p.zero_count = static_cast<int>(counter_bytes(tokens, d) / 4);
-  }
+  p.zero = counters;
+  p.zero_count = static_cast<int>(counter_bytes(tokens, d, sz.down) / 4);
   FfnSegment sg{};
   if (!encode(&sg.a[0], x, dtype, tokens, d, ldx, MAP_ROWS) || !encode(&sg.b[0], w_gate, dtype, f, d, d, MAP_ROWS) ||
       !encode(&sg.b[1], w_up, dtype, f, d, d, MAP_ROWS) || !encode(&sg.out[0], h, dtype, tokens, f, f, MAP_STORE))
     return PRM_ERR_CUDA;
-  shape(sg, tokens, f, d, 0, false, false, BN_HALF, 1);
-  queue(p, sg);
+  queue(p, sg, tokens, f, d, 0, false, false, BN_HALF);
   if (launch_act<EPI_GLU>(p, act, dtype, dev->num_sms, st) != cudaSuccess) return PRM_ERR_CUDA;
 
   FfnParams q{};
@@ -726,10 +751,11 @@ extern "C" int prm_gated_ffn_forward(const void* x, int64_t ldx, const void* w_g
   if (!encode(&dn.a[0], h, dtype, tokens, f, f, MAP_ROWS) || !encode(&dn.b[0], w_down, dtype, d, f, f, MAP_ROWS) ||
       !encode(&dn.out[0], y, dtype, tokens, d, d, MAP_STORE))
     return PRM_ERR_CUDA;
-  shape(dn, tokens, d, f, 0, false, false, BN, sz.down_splits);
+  dn.whole = static_cast<int>(sz.down.whole);
+  dn.splits = sz.down.splits;
   dn.partial = reinterpret_cast<float*>(ws + sz.fwd_partial);
   dn.arrived = counters;
-  queue(q, dn);
+  queue(q, dn, tokens, d, f, 0, false, false, BN);
   return launch<EPI_STORE>(q, dtype, dev->num_sms, st) == cudaSuccess ? PRM_OK : PRM_ERR_CUDA;
 }
 
@@ -780,30 +806,27 @@ extern "C" int prm_gated_ffn_backward(const void* dy, int64_t lddy, const void* 
       !encode(&sg.out[0], dg, dtype, tokens, f, f, MAP_STORE) ||
       !encode(&sg.out[1], du, dtype, tokens, f, f, MAP_STORE))
     return PRM_ERR_CUDA;
-  shape(sg, tokens, f, d, 0, false, true, BN, 1);
-  queue(p, sg);
+  queue(p, sg, tokens, f, d, 0, false, true, BN);
   if (launch_act<EPI_DGLU>(p, act, dtype, dev->num_sms, st) != cudaSuccess) return PRM_ERR_CUDA;
 
   // dx (K = 2 f) and the weight gradients (K = tokens) from one queue, the
   // longer sums first, so that the last tiles of the queue are short.
   FfnParams q{};
   q.err = dev->d_err;
-  FfnSegment segs[4] = {};
   bool ok = true;
-  int n = 0;
   auto add_dx = [&] {
     if (dx == nullptr) return;
-    FfnSegment& s = segs[n++];
+    FfnSegment s{};
     ok = ok && encode(&s.a[0], dg, dtype, tokens, f, f, MAP_ROWS) && encode(&s.a[1], du, dtype, tokens, f, f, MAP_ROWS) &&
          encode(&s.b[0], w_gate, dtype, f, d, d, MAP_COLS) && encode(&s.b[1], w_up, dtype, f, d, d, MAP_COLS) &&
          encode(&s.out[0], dx, dtype, tokens, d, d, MAP_STORE);
-    shape(s, tokens, d, f, f, false, true, BN, 1);
+    queue(q, s, tokens, d, f, f, false, true, BN);
   };
-  auto add_weight = [&](const void* a, int64_t lda, int64_t m, const void* b, int64_t ldb, int64_t nn, void* out) {
-    FfnSegment& s = segs[n++];
+  auto add_weight = [&](const void* a, int64_t lda, int64_t m, const void* b, int64_t ldb, int64_t n, void* out) {
+    FfnSegment s{};
     ok = ok && encode(&s.a[0], a, dtype, tokens, m, lda, MAP_COLS) &&
-         encode(&s.b[0], b, dtype, tokens, nn, ldb, MAP_COLS) && encode(&s.out[0], out, dtype, m, nn, nn, MAP_STORE);
-    shape(s, m, nn, tokens, 0, true, true, BN, 1);
+         encode(&s.b[0], b, dtype, tokens, n, ldb, MAP_COLS) && encode(&s.out[0], out, dtype, m, n, n, MAP_STORE);
+    queue(q, s, m, n, tokens, 0, true, true, BN);
   };
   const bool dx_first = 2 * f >= tokens;
   if (dx_first) add_dx();
@@ -814,6 +837,5 @@ extern "C" int prm_gated_ffn_backward(const void* dy, int64_t lddy, const void* 
   }
   if (!dx_first) add_dx();
   if (!ok) return PRM_ERR_CUDA;
-  for (int i = 0; i < n; ++i) queue(q, segs[i]);
   return launch<EPI_STORE>(q, dtype, dev->num_sms, st) == cudaSuccess ? PRM_OK : PRM_ERR_CUDA;
 }

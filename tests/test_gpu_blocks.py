@@ -306,6 +306,15 @@ def test_norm_widths(d, kind):
     _check_norm(*_norm_case(2, 7, d, kind, FP32, BF16 if d % 3 else FP32, 1, 1, 1, 1, eps=1e-3 if d <= 2 else 1e-6))
 
 
+@pytest.mark.parametrize("st,bt", [(FP32, FP32), (FP32, BF16), (BF16, BF16)])
+@pytest.mark.parametrize("d", [2040, 5112, 5128, 8184, 8192])
+def test_norm_long_rows_by_option(d, st, bt):
+    """Rows of which two may not fit in shared memory beside the option's
+    column arrays."""
+    for opts in ((1, 0, 1, 0), (0, 1, 0, 1), (0, 0, 0, 0), (1, 1, 1, 1)):
+        _check_norm(*_norm_case(2, 9, d, "layer", st, bt, *opts))
+
+
 @pytest.mark.parametrize("B,L", [(1, 1), (1, 2), (5, 1), (1300, 1), (1300, 3), (1, 5000), (7, 700), (40, 31)])
 @pytest.mark.parametrize("mod", [0, 1])
 def test_norm_row_counts(B, L, mod):
