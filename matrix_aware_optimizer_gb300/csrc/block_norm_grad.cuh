@@ -71,11 +71,6 @@ struct NormGradIo {
   BT* mod[3];   // dgate, dscale, dshift
 };
 
-// How a thread's eight elements of a row lie: consecutive in the stage (VEC),
-// strided by the row's thread count in the stage (ELEM: d % 8 != 0, whose
-// rows start anywhere), or strided in memory (DIRECT: no ring).
-enum Access { VEC, ELEM, DIRECT };
-
 // Eight elements at p as fp32 pairs.
 __device__ __forceinline__ F8 load_f8(const float* p) {
   const ulonglong2 a = reinterpret_cast<const ulonglong2*>(p)[0], b = reinterpret_cast<const ulonglong2*>(p)[1];
@@ -127,37 +122,6 @@ __device__ __forceinline__ void write8(T* p, int left, int step, const F8& v) {
     for (int e = 0; e < 8; ++e)
       if (e * step < left) p[e * step] = from_f32<T>(o[e]);
   }
-}
-
-// Copies n elements from src to a stage region of `room` bytes that starts on
-// 16 bytes, at src's own offset from a 16-byte boundary; returns the bytes
-// the barrier has to wait for. The tensor starts on 16 bytes, so rounding the
-// start down stays inside it; what lies behind the last whole 16 bytes before
-// `end` (the tensor's end) is copied here element by element.
-template <typename T>
-__device__ __forceinline__ uint32_t ring_bytes(const T* src, uint32_t n, const T* end) {
-  const uintptr_t lo = reinterpret_cast<uintptr_t>(src) & ~uintptr_t(15);
-  const uintptr_t last = reinterpret_cast<uintptr_t>(end) & ~uintptr_t(15);
-  uintptr_t hi = (reinterpret_cast<uintptr_t>(src + n) + 15) & ~uintptr_t(15);
-  hi = hi < last ? hi : last;
-  return hi > lo ? static_cast<uint32_t>(hi - lo) : 0u;
-}
-template <typename T>
-__device__ __forceinline__ void ring_tail(uint8_t* dst, const T* src, uint32_t n, const T* end) {
-  const T* last = reinterpret_cast<const T*>(reinterpret_cast<uintptr_t>(end) & ~uintptr_t(15));
-  const T* lo = reinterpret_cast<const T*>(reinterpret_cast<uintptr_t>(src) & ~uintptr_t(15));
-  T* out = reinterpret_cast<T*>(dst);
-  for (const T* p = last > src ? last : src; p < src + n; ++p) out[p - lo] = *p;
-}
-template <typename T>
-__device__ __forceinline__ void ring_load(uint8_t* dst, const T* src, uint32_t bytes, uint64_t* bar) {
-  if (bytes > 0)
-    bulk_load(dst, reinterpret_cast<const void*>(reinterpret_cast<uintptr_t>(src) & ~uintptr_t(15)), bytes, bar);
-}
-// Where an ELEM row that starts at src lies in its stage region.
-template <typename T>
-__device__ __forceinline__ uint32_t ring_offset(const T* src) {
-  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(src) & 15u);
 }
 
 // Threads per CTA that a kernel is compiled for: rows of up to 2048, 5120 and

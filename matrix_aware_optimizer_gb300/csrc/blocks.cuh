@@ -205,6 +205,42 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
+// How a thread's eight elements of a row lie: consecutive in the stage (VEC),
+// strided by the row's thread count in the stage (ELEM: d % 8 != 0, whose
+// rows start anywhere), or strided in memory (DIRECT: no ring).
+enum Access { VEC, ELEM, DIRECT };
+
+// Bulk copies of n elements from any element of a tensor that itself starts
+// on 16 bytes, to shared memory at the same offset from a 16-byte boundary.
+// ring_bytes: what the copy brings (its start rounded down, its end up, but
+// not past the last whole 16 bytes before `end`, the tensor's end);
+// ring_tail: the elements behind those, stored by this thread.
+template <typename T>
+__device__ __forceinline__ uint32_t ring_bytes(const T* src, uint32_t n, const T* end) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(src) & ~uintptr_t(15);
+  const uintptr_t last = reinterpret_cast<uintptr_t>(end) & ~uintptr_t(15);
+  uintptr_t hi = (reinterpret_cast<uintptr_t>(src + n) + 15) & ~uintptr_t(15);
+  hi = hi < last ? hi : last;
+  return hi > lo ? static_cast<uint32_t>(hi - lo) : 0u;
+}
+template <typename T>
+__device__ __forceinline__ void ring_tail(uint8_t* dst, const T* src, uint32_t n, const T* end) {
+  const T* last = reinterpret_cast<const T*>(reinterpret_cast<uintptr_t>(end) & ~uintptr_t(15));
+  const T* lo = reinterpret_cast<const T*>(reinterpret_cast<uintptr_t>(src) & ~uintptr_t(15));
+  T* out = reinterpret_cast<T*>(dst);
+  for (const T* p = last > src ? last : src; p < src + n; ++p) out[p - lo] = *p;
+}
+template <typename T>
+__device__ __forceinline__ void ring_load(uint8_t* dst, const T* src, uint32_t bytes, uint64_t* bar) {
+  if (bytes > 0)
+    bulk_load(dst, reinterpret_cast<const void*>(reinterpret_cast<uintptr_t>(src) & ~uintptr_t(15)), bytes, bar);
+}
+// Where an ELEM row that starts at src lies in its stage region.
+template <typename T>
+__device__ __forceinline__ uint32_t ring_offset(const T* src) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(src) & 15u);
+}
+
 // -------------------------------------------------------- TMA of CTA pairs
 // 2-D tile load into this CTA's shared memory whose completion is counted on
 // the mbarrier at `bar_cluster_addr`, which may belong to the peer CTA.
