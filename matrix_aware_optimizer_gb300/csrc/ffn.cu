@@ -316,6 +316,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   tc_fence_after_sync();
   const uint32_t tmem_base = *tmem_holder;
   pdl_wait();
+  pdl_launch_dependents();  // the next kernel sets up on SMs that this one leaves or does not use
   if (p.zero != nullptr && blockIdx.x == 0)
     for (int i = threadIdx.x; i < p.zero_count; i += NUM_THREADS) p.zero[i] = 0;
 
@@ -481,39 +482,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       } else {
         // A part of the sum along K: this warp's 32 x 128 values go to the
         // workspace; the warp that arrives last for them adds all parts, in
-        // order, and stores the result.
+        // order, and stores the result. Warps without rows have nothing to do.
         const int64_t region = (static_cast<int64_t>(it.split_tile) * 2 + rank) * EPI_WARPS + ew;
         float4* mine = reinterpret_cast<float4*>(sg.partial) + (region * sg.splits + it.split) * (32 * 32) + lane;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float v[32];
-          tmem_load_32cols(t_row + static_cast<uint32_t>(half * (BN / 2) + q * 32), v);
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            __stcg(mine + (q * 8 + k) * 32, make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]));
-        }
-        __threadfence();
-        __syncwarp();
-        uint32_t before = 0;
-        if (lane == 0) before = atomicAdd(&sg.arrived[region], 1u);
-        before = __shfl_sync(0xffffffffu, before, 0);
-        if (before + 1 == static_cast<uint32_t>(sg.splits)) {
-          __threadfence();
-          const float4* all = reinterpret_cast<const float4*>(sg.partial) + region * sg.splits * (32 * 32) + lane;
+        if (i0 < sg.M) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            float v[32] = {};
-            for (int s = 0; s < sg.splits; ++s) {
+            float v[32];
+            tmem_load_32cols(t_row + static_cast<uint32_t>(half * (BN / 2) + q * 32), v);
 #pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const float4 t = __ldcg(all + s * (32 * 32) + (q * 8 + k) * 32);
-                v[4 * k] += t.x;
-                v[4 * k + 1] += t.y;
-                v[4 * k + 2] += t.z;
-                v[4 * k + 3] += t.w;
+            for (int k = 0; k < 8; ++k)
+              __stcg(mine + (q * 8 + k) * 32, make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]));
+          }
+          __threadfence();
+          __syncwarp();
+          uint32_t before = 0;
+          if (lane == 0) before = atomicAdd(&sg.arrived[region], 1u);
+          before = __shfl_sync(0xffffffffu, before, 0);
+          if (before + 1 == static_cast<uint32_t>(sg.splits)) {
+            __threadfence();
+            const float4* all = reinterpret_cast<const float4*>(sg.partial) + region * sg.splits * (32 * 32) + lane;
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+              float v[32] = {};
+              for (int s = 0; s < sg.splits; s += 2) {  // two parts in flight
+                float4 a[8], b[8];
+                const bool two = s + 1 < sg.splits;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  a[k] = __ldcg(all + s * (32 * 32) + (q * 8 + k) * 32);
+                  b[k] = two ? __ldcg(all + (s + 1) * (32 * 32) + (q * 8 + k) * 32) : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  v[4 * k] = v[4 * k] + a[k].x + b[k].x;
+                  v[4 * k + 1] = v[4 * k + 1] + a[k].y + b[k].y;
+                  v[4 * k + 2] = v[4 * k + 2] + a[k].z + b[k].z;
+                  v[4 * k + 3] = v[4 * k + 3] + a[k].w + b[k].w;
+                }
               }
+              store_box<T>(sg, i0, jh + q * 32, v, stage, lane);
             }
-            store_box<T>(sg, i0, jh + q * 32, v, stage, lane);
           }
         }
       }
@@ -634,7 +643,9 @@ Split split_last_wave(int64_t M, int64_t N, int64_t K) {
   const int64_t tiles = tiles_of(M, N);
   const int64_t rest = tiles % FFN_PAIRS;
   const int64_t kb = (K + BK - 1) / BK;
-  const int64_t s = rest == 0 ? 1 : std::min<int64_t>({FFN_PAIRS / rest, kb / MIN_PART, 16});
+  // adding up the parts costs about two slices of K per part: no more parts than that pays for
+  const int64_t pays = static_cast<int64_t>(std::sqrt(static_cast<double>(kb) / 2)) + 1;
+  const int64_t s = rest == 0 ? 1 : std::min<int64_t>({FFN_PAIRS / rest, kb / MIN_PART, pays, 16});
   return s < 2 ? Split{tiles, 1} : Split{tiles - rest, static_cast<int>(s)};
 }
 size_t partial_bytes(int64_t M, int64_t N, const Split& s) {
@@ -731,6 +742,13 @@ extern "C" int prm_gated_ffn_forward(const void* x, int64_t ldx, const void* w_g
   char* ws = static_cast<char*>(workspace);
   void* h = saved != nullptr ? saved : ws;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (ffn_few(tokens, d, f))
+    return ffn_few_forward(x, ldx, w_gate, w_up, w_down, h,
+                           saved != nullptr ? reinterpret_cast<uint4*>(static_cast<char*>(saved) + sz.saved_h) : nullptr,
+                           y, static_cast<int>(tokens), static_cast<int>(d), static_cast<int>(f), act, dtype,
+                           st) == cudaSuccess
+               ? PRM_OK
+               : PRM_ERR_CUDA;
 
   FfnParams p{};
   p.err = dev->d_err;

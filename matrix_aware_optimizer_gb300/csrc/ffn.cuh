@@ -1,4 +1,5 @@
-// Activations of the gated feed-forward block, in fp32.
+// Activations of the gated feed-forward block, in fp32, and its kernels for a
+// few tokens.
 #pragma once
 
 #include <atomic>
@@ -42,5 +43,18 @@ __device__ __forceinline__ void ffn_act_grad(float g, float* a, float* da) {
     *da = fmaf(g * s * (1.f - s), 2.f * FFN_SQRT_2_PI * fmaf(3.f * 0.044715f * g, g, 1.f), s);
   }
 }
+
+// Forward pass on CUDA cores for up to FFN_FEW_TOKENS tokens: h and y, and g
+// and u in the tensor-core kernels' packed layout where gu is not NULL.
+// CUDA cores up to 4 tokens, up to 8 with small weights: at d 2048, f 8192 and
+// 4 tokens 26 us against 41 on the tensor cores, with 8 tokens 51 against 42; at
+// d 512, f 1536 and 8 tokens 8.2 against 19.
+constexpr int FFN_FEW_TOKENS = 8;
+inline bool ffn_few(int64_t tokens, int64_t d, int64_t f) {
+  return tokens <= 4 || (tokens <= FFN_FEW_TOKENS && d * f <= (int64_t(1) << 21));
+}
+cudaError_t ffn_few_forward(const void* x, int64_t ldx, const void* w_gate, const void* w_up, const void* w_down,
+                            void* h, uint4* gu, void* y, int tokens, int d, int f, int act, int dtype,
+                            cudaStream_t stream);
 
 }  // namespace prm
