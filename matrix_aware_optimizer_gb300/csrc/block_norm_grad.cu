@@ -5,14 +5,11 @@
 namespace prm {
 namespace {
 
-// Two CTAs on each of the 152 SMs; also the bound that sizes the workspace.
-constexpr int64_t NORM_GRAD_CTAS = 304;
-
 struct NormGradSpace {
   size_t mod, w;
 };
 NormGradSpace space(const prm_block_norm_desc& c) {
-  const size_t rows = static_cast<size_t>(std::min<int64_t>(c.rows, NORM_GRAD_CTAS)) * ((c.d + 3) & ~int64_t(3)) *
+  const size_t rows = static_cast<size_t>(std::min<int64_t>(c.rows, NORM_CTAS)) * ((c.d + 3) & ~int64_t(3)) *
                       sizeof(float);
   NormGradSpace s{};
   if (c.gate != nullptr || c.scale != nullptr || c.shift != nullptr) s.mod = round_up(6 * rows, 256);
@@ -66,17 +63,17 @@ extern "C" int prm_block_norm_backward(const prm_block_norm_desc* desc, const vo
   const bool mod = desc->gate != nullptr || desc->scale != nullptr || desc->shift != nullptr;
   const bool w = desc->post_weight != nullptr || desc->pre_weight != nullptr;
   const bool all = !vec;  // the strided kernels are compiled for every sum
-  const NormGradShape s =
+  const NormShape s =
       grad_shape(desc->d, row_bytes(*desc, dy != nullptr, dr != nullptr, z != nullptr, stats != nullptr),
                  (dy != nullptr ? 2 : 0) + (dr != nullptr) + (z != nullptr), vec, ring, w || all, mod || all);
   const void* present[SUM_COUNT] = {desc->gate, desc->scale, desc->shift, desc->post_weight, desc->pre_weight};
   for (int k = 0; k < SUM_COUNT; ++k) p.has[k] = present[k] != nullptr;
-  if (p.n.rows / NORM_GRAD_CTAS > (int64_t(1) << 30)) return PRM_ERR_UNSUPPORTED;
+  if (p.n.rows / NORM_CTAS > (int64_t(1) << 30)) return PRM_ERR_UNSUPPORTED;
   p.n.tpr = s.tpr;
   p.groups = s.groups;
   p.stages = s.stages;
   p.sample_rows = mod ? p.n.rps : p.n.rows;
-  const int64_t at_once = s.size == 0 && s.smem <= 112 * 1024 ? NORM_GRAD_CTAS : NORM_GRAD_CTAS / 2;
+  const int64_t at_once = s.half ? NORM_CTAS : NORM_CTAS / 2;
   p.ctas = std::min<int64_t>(at_once, (p.n.rows + s.groups * s.rows - 1) / (s.groups * s.rows));
   p.partial_mod = static_cast<float*>(workspace);
   p.partial_w = reinterpret_cast<float*>(static_cast<char*>(workspace) + sp.mod);

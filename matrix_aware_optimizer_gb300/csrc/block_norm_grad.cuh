@@ -31,19 +31,6 @@
 namespace prm {
 
 constexpr int SUM_GATE = 0, SUM_SCALE = 1, SUM_SHIFT = 2, SUM_POST = 3, SUM_PRE = 4, SUM_COUNT = 5;
-constexpr int MAX_STAGES = 8;
-constexpr uint64_t NORM_WAIT_NS = 2000000000ull;
-
-struct NormGradShape {
-  int size;              // see grad_threads
-  int access;
-  int tpr, groups;       // threads per row, groups of rows at once
-  int rows;              // rows per group and step
-  int stages;
-  int threads;
-  size_t smem;
-};
-
 struct NormGradParams {
   NormParams n;
   int64_t sample_rows;   // rows that share modulation (all rows without any)
@@ -71,72 +58,12 @@ struct NormGradIo {
   BT* mod[3];   // dgate, dscale, dshift
 };
 
-// Eight elements at p as fp32 pairs.
-__device__ __forceinline__ F8 load_f8(const float* p) {
-  const ulonglong2 a = reinterpret_cast<const ulonglong2*>(p)[0], b = reinterpret_cast<const ulonglong2*>(p)[1];
-  return {{a.x, a.y, b.x, b.y}};
-}
-template <typename T>
-__device__ __forceinline__ F8 load_f8(const T* p) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-  F8 o;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = unpack2<T>(w[i]);
-    o.p[i] = f2_pack(f.x, f.y);
-  }
-  return o;
-}
-// p[0], p[step], ..., zero from `left` elements on.
-template <typename T>
-__device__ __forceinline__ F8 gather_f8(const T* p, int left, int step) {
-  F8 o;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int a = 2 * k * step, b = a + step;
-    o.p[k] = f2_pack(a < left ? to_f32(p[a]) : 0.f, b < left ? to_f32(p[b]) : 0.f);
-  }
-  return o;
-}
-template <int ACCESS, typename T>
-__device__ __forceinline__ F8 read8(const T* p, int left, int step) {
-  if constexpr (ACCESS == VEC) return load_f8(p);
-  else return gather_f8(p, left, step);
-}
-template <int ACCESS, typename T>
-__device__ __forceinline__ void write8(T* p, int left, int step, const F8& v) {
-  float o[8];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float2 f = f2_unpack(v.p[k]);
-    o[2 * k] = f.x;
-    o[2 * k + 1] = f.y;
-  }
-  if constexpr (ACCESS == VEC) {
-    Raw8<T> raw;
-    raw.set(o);
-    raw.store(p);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e * step < left) p[e * step] = from_f32<T>(o[e]);
-  }
-}
-
-// Threads per CTA that a kernel is compiled for: rows of up to 2048, 5120 and
-// 8192 elements.
-__host__ __device__ constexpr int grad_threads(int size) { return size == 0 ? 256 : size == 1 ? 320 : 512; }
-
-// Vectors of 8 elements per thread.
-__host__ __device__ constexpr int grad_vectors(int size) { return size == 0 ? 1 : 2; }
+__host__ __device__ constexpr bool grad_far(int size, bool mod, bool w) { return w && (mod || size == 2); }
 
 // R: rows that a thread works on at once, to have more than one chain of
 // dependent steps and to share what a step costs besides the arithmetic.
-__host__ __device__ constexpr bool grad_far(int size, bool mod, bool w) { return w && (mod || size == 2); }
-
 template <typename RT, typename BT, int SIZE, int R, int NV, int ACCESS, bool MOD, bool W>
-__global__ void __launch_bounds__(grad_threads(SIZE), SIZE == 0 ? 2 : 1)
+__global__ void __launch_bounds__(norm_threads(SIZE), SIZE == 0 ? 2 : 1)
     norm_backward_kernel(const __grid_constant__ NormGradParams p, const NormGradIo<RT, BT> io) {
   constexpr bool RING = ACCESS != DIRECT;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -275,69 +202,7 @@ __global__ void __launch_bounds__(grad_threads(SIZE), SIZE == 0 ? 2 : 1)
     left[v] = d - col[v];
   }
   int turn = 0;
-  // Sums of two values per row over the row's threads. With each exchange
-  // half the lanes go on with one half of the values (6 shuffles for four
-  // values instead of 20); rows of more than a warp meet at a named barrier
-  // of their own, and each warp adds the warps' totals.
-  auto reduce = [&](float (&a)[R][2]) {
-    if (SIZE == 0 && tpr < 32) {
-      for (int o = tpr / 2; o > 0; o >>= 1)
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-          a[i][0] += __shfl_xor_sync(0xffffffffu, a[i][0], o);
-          a[i][1] += __shfl_xor_sync(0xffffffffu, a[i][1], o);
-        }
-      return;
-    }
-    constexpr int VALUES = 2 * R;
-    constexpr int SPAN = 32 / VALUES;  // lanes that carry one value in the end
-    float t;
-    const bool low = lane < 16;
-    if constexpr (R == 2) {
-      const float k0 = (low ? a[0][0] : a[R - 1][0]) + __shfl_xor_sync(0xffffffffu, low ? a[R - 1][0] : a[0][0], 16);
-      const float k1 = (low ? a[0][1] : a[R - 1][1]) + __shfl_xor_sync(0xffffffffu, low ? a[R - 1][1] : a[0][1], 16);
-      const bool even = (lane & 8) == 0;
-      t = (even ? k0 : k1) + __shfl_xor_sync(0xffffffffu, even ? k1 : k0, 8);
-    } else {
-      t = (low ? a[0][0] : a[0][1]) + __shfl_xor_sync(0xffffffffu, low ? a[0][1] : a[0][0], 16);
-    }
-#pragma unroll
-    for (int o = SPAN / 2; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    int from = SPAN;  // lane distance of the values
-    if (SIZE > 0 || tpr > 32) {
-      float* s = scratch[turn];
-      turn ^= 1;
-      if ((lane & (SPAN - 1)) == 0) s[(threadIdx.x >> 5) * VALUES + lane / SPAN] = t;
-      named_barrier_sync(1 + group, tpr);
-      constexpr int MOST_WARPS = grad_threads(SIZE) / 32;
-      const int warps = tpr >> 5;
-      s += group * warps * VALUES;
-      t = 0.f;
-#pragma unroll
-      for (int k = 0; k < (MOST_WARPS + SPAN - 1) / SPAN; ++k) {
-        const int w = lane / VALUES + k * SPAN;
-        if (w < warps) t += s[w * VALUES + lane % VALUES];
-      }
-#pragma unroll
-      for (int o = 16; o >= VALUES; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-      from = 1;
-    }
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      a[i][0] = __shfl_sync(0xffffffffu, t, 2 * i * from);
-      a[i][1] = __shfl_sync(0xffffffffu, t, (2 * i + 1) * from);
-    }
-  };
-  auto join_halves = [](const uint64_t(&part)[R][2], float(&sums)[R][2]) {
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float2 f = f2_unpack(part[i][k]);
-        sums[i][k] = f.x + f.y;
-      }
-  };
-
+  auto reduce = [&](float (&a)[R][2]) { row_sums<SIZE, R>(a, tpr, group, scratch, turn); };
   F8 acc_mod[MOD ? 3 : 1][NV], acc_w[W && !FAR ? 2 : 1][NV];
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
@@ -727,50 +592,16 @@ struct NormGradArgs {
   void *dscale, *dshift;
 };
 
-// Geometry for rows of d elements whose `arrays` arrays take row_bytes in
-// all. Rows of up to 2048 elements: two CTAs of 256 threads per SM, each with
-// half its shared memory.
-inline NormGradShape grad_shape(int64_t d, size_t row_bytes, int arrays, bool vec, bool ring, bool w, bool mod) {
-  NormGradShape s{};
-  s.size = d <= 2048 ? 0 : d <= 5120 ? 1 : 2;
-  const int nv = grad_vectors(s.size);
-  const int vectors = static_cast<int>((d + 8 * nv - 1) / (8 * nv));
-  if (vectors <= 32) {
-    s.tpr = 2;
-    while (s.tpr < vectors) s.tpr *= 2;
-  } else {
-    s.tpr = (vectors + 31) / 32 * 32;
-  }
-  s.groups = s.size == 2 ? 1 : std::max(1, grad_threads(s.size) / s.tpr);
-  s.threads = s.tpr * s.groups;
-  // shared memory behind the ring, for a kernel with these sums
-  auto behind = [&](bool w, bool mod) {
-    return ((w ? 2 : 0) + (mod ? 2 : 0)) * ((d + 3) & ~int64_t(3)) * sizeof(float) +
-           (s.groups > 1 ? static_cast<size_t>(s.threads) * 8 * nv * sizeof(float) : 0) +
-           (grad_far(s.size, mod, w) ? static_cast<size_t>(s.threads) * 16 * nv * sizeof(float) : 0);
-  };
-  const size_t extra = behind(w, mod);
-  s.access = vec ? VEC : ELEM;
-  // two stages at least, in half an SM's shared memory, else in all of it,
-  // else one stage
-  const size_t half = 110 * 1024, whole = 220 * 1024;
-  const struct {
-    int rows, stages;
-    size_t room;
-  } tries[4] = {{2, 2, half}, {1, 2, half}, {1, 2, whole}, {1, 1, whole}};
-  for (int k = s.size == 0 ? 0 : 2; ring && k < 4; ++k) {
-    s.rows = tries[k].rows;
-    const size_t stage = row_bytes * s.groups * s.rows + (vec ? 0 : 32 * arrays);
-    s.stages =
-        extra < tries[k].room ? static_cast<int>(std::min<size_t>((tries[k].room - extra) / stage, MAX_STAGES)) : 0;
-    s.smem = stage * s.stages + extra;
-    if (s.stages >= tries[k].stages && (vec || s.rows == 1)) return s;
-  }
-  s.access = DIRECT;
-  s.rows = 1;
-  s.stages = 0;
-  s.smem = behind(true, true);  // compiled for every sum
-  return s;
+// Shared memory behind the ring of a kernel with these sums: the columns'
+// arrays, the groups' exchange area, the gain sums that lie there.
+inline NormShape grad_shape(int64_t d, size_t row_bytes, int arrays, bool vec, bool ring, bool w, bool mod) {
+  return norm_shape(d, row_bytes, arrays, vec, ring, [&](int size, int threads, int groups, bool direct) {
+    const bool ww = w || direct, mm = mod || direct;  // the direct kernel is compiled for every sum
+    const int nv = norm_vectors(size);
+    return ((ww ? 2 : 0) + (mm ? 2 : 0)) * ((d + 3) & ~int64_t(3)) * sizeof(float) +
+           (groups > 1 ? static_cast<size_t>(threads) * 8 * nv * sizeof(float) : 0) +
+           (grad_far(size, mm, ww) ? static_cast<size_t>(threads) * 16 * nv * sizeof(float) : 0);
+  });
 }
 
 inline size_t row_bytes(const prm_block_norm_desc& c, bool dy, bool dr, bool z, bool stats) {
@@ -779,25 +610,16 @@ inline size_t row_bytes(const prm_block_norm_desc& c, bool dy, bool dr, bool z, 
 }
 
 template <typename RT, typename BT, int SIZE, int R, int NV, int ACCESS, bool MOD, bool W>
-cudaError_t launch_backward(NormGradParams& p, const NormGradShape& s, const NormGradArgs& a, cudaStream_t stream) {
+cudaError_t launch_backward(NormGradParams& p, const NormShape& s, const NormGradArgs& a, cudaStream_t stream) {
   auto kernel = norm_backward_kernel<RT, BT, SIZE, R, NV, ACCESS, MOD, W>;
-  if (s.smem > 40 * 1024) {
-    static std::atomic<bool> set[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!set[dev].load(std::memory_order_relaxed)) {
-      cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 224 * 1024);
-      if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
-      if (e != cudaSuccess) return e;
-      set[dev].store(true, std::memory_order_relaxed);
-    }
-  }
+  static std::atomic<bool> set[64];
+  cudaError_t e = norm_setup(kernel, set);
+  if (e != cudaSuccess) return e;
   const NormGradIo<RT, BT> io{static_cast<const BT*>(a.dy), static_cast<const RT*>(a.dr), static_cast<const RT*>(a.r),
                               static_cast<const BT*>(a.z), reinterpret_cast<const float4*>(a.stats),
                               static_cast<RT*>(a.dx), static_cast<BT*>(a.dz),
                               {static_cast<BT*>(a.dgate), static_cast<BT*>(a.dscale), static_cast<BT*>(a.dshift)}};
-  cudaError_t e = launch_dependent(kernel, dim3(static_cast<unsigned>(p.ctas)), dim3(s.threads), s.smem, stream, p, io);
+  e = launch_dependent(kernel, dim3(static_cast<unsigned>(p.ctas)), dim3(s.threads), s.smem, stream, p, io);
   if (e != cudaSuccess) return e;
   const bool mods = MOD && (p.has[SUM_GATE] || p.has[SUM_SCALE] || p.has[SUM_SHIFT]);
   const int d = p.n.d;
@@ -809,19 +631,19 @@ cudaError_t launch_backward(NormGradParams& p, const NormGradShape& s, const Nor
 }
 
 template <typename RT, typename BT>
-cudaError_t launch_shape(NormGradParams& p, const NormGradShape& s, const NormGradArgs& a, cudaStream_t stream) {
+cudaError_t launch_shape(NormGradParams& p, const NormShape& s, const NormGradArgs& a, cudaStream_t stream) {
   const bool mod = p.has[SUM_GATE] || p.has[SUM_SCALE] || p.has[SUM_SHIFT];
   const bool w = p.has[SUM_POST] || p.has[SUM_PRE];
   using std::integral_constant;
   auto go = [&](auto size, auto rows) {
-    constexpr int S = decltype(size)::value, R = decltype(rows)::value, V = grad_vectors(S);
+    constexpr int S = decltype(size)::value, R = decltype(rows)::value, V = norm_vectors(S);
     if (mod && w) return launch_backward<RT, BT, S, R, V, VEC, true, true>(p, s, a, stream);
     if (mod) return launch_backward<RT, BT, S, R, V, VEC, true, false>(p, s, a, stream);
     if (w) return launch_backward<RT, BT, S, R, V, VEC, false, true>(p, s, a, stream);
     return launch_backward<RT, BT, S, R, V, VEC, false, false>(p, s, a, stream);
   };
   auto strided = [&](auto size) {
-    constexpr int S = decltype(size)::value, V = grad_vectors(S);
+    constexpr int S = decltype(size)::value, V = norm_vectors(S);
     return s.access == ELEM ? launch_backward<RT, BT, S, 1, V, ELEM, true, true>(p, s, a, stream)
                             : launch_backward<RT, BT, S, 1, V, DIRECT, true, true>(p, s, a, stream);
   };
@@ -839,6 +661,6 @@ cudaError_t launch_shape(NormGradParams& p, const NormGradShape& s, const NormGr
 // Defined per pair of types, each pair's kernels in a translation unit of a
 // few (norm_grad_*.cu) to keep the build parallel.
 template <typename RT, typename BT>
-cudaError_t norm_grad_launch(NormGradParams& p, const NormGradShape& s, const NormGradArgs& a, cudaStream_t stream);
+cudaError_t norm_grad_launch(NormGradParams& p, const NormShape& s, const NormGradArgs& a, cudaStream_t stream);
 
 }  // namespace prm

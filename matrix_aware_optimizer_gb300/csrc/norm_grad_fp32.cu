@@ -4,7 +4,7 @@
 namespace prm {
 
 template <>
-cudaError_t norm_grad_launch<float, float>(NormGradParams& p, const NormGradShape& s, const NormGradArgs& a,
+cudaError_t norm_grad_launch<float, float>(NormGradParams& p, const NormShape& s, const NormGradArgs& a,
                                  cudaStream_t stream) {
   return launch_shape<float, float>(p, s, a, stream);
 }

@@ -4,13 +4,13 @@
 namespace prm {
 
 template <>
-cudaError_t norm_grad_launch<float, __nv_bfloat16>(NormGradParams& p, const NormGradShape& s, const NormGradArgs& a,
+cudaError_t norm_grad_launch<float, __nv_bfloat16>(NormGradParams& p, const NormShape& s, const NormGradArgs& a,
                                  cudaStream_t stream) {
   return launch_shape<float, __nv_bfloat16>(p, s, a, stream);
 }
 
 template <>
-cudaError_t norm_grad_launch<float, __half>(NormGradParams& p, const NormGradShape& s, const NormGradArgs& a,
+cudaError_t norm_grad_launch<float, __half>(NormGradParams& p, const NormShape& s, const NormGradArgs& a,
                                  cudaStream_t stream) {
   return launch_shape<float, __half>(p, s, a, stream);
 }
