@@ -83,6 +83,7 @@ constexpr int MAX_SEGS = 4;
 struct FfnParams {
   FfnSegment seg[MAX_SEGS];
   int nseg;
+  int pairs;            // of a cluster
   int64_t total;        // work items: whole tiles and parts of split ones
   uint4* gu;            // packed g and u (GLU: written when not NULL; DGLU: read)
   uint32_t* zero;       // counters to clear for the next launch
@@ -108,8 +109,9 @@ __device__ __forceinline__ int ffn_seg(const FfnParams& p, int64_t item) {
   return s;
 }
 
-template <int EPI>
-__device__ __forceinline__ Item ffn_item(const FfnSegment& sg, int64_t item) {
+// PAIRS pairs of a cluster take tiles next to each other along N.
+template <int EPI, int PAIRS>
+__device__ __forceinline__ Item ffn_item(const FfnSegment& sg, int64_t item, int pair) {
   Item it;
   int tile = static_cast<int>(item - sg.item_begin);
   const int kb = sg.k_blocks[0] + sg.k_blocks[1];
@@ -125,12 +127,12 @@ __device__ __forceinline__ Item ffn_item(const FfnSegment& sg, int64_t item) {
     it.kb1 = static_cast<int>(static_cast<int64_t>(kb) * (it.split + 1) / sg.splits);
     tile = sg.whole + it.split_tile;
   }
-  const int group = tile / (GROUP_M * sg.tiles_n);
+  const int group = tile / (GROUP_M * sg.tiles_n);  // (tiles_n counts groups of PAIRS tiles)
   const int rows = min(GROUP_M, sg.tiles_m - group * GROUP_M);
   const int in_group = tile - group * GROUP_M * sg.tiles_n;
   const int tn = in_group / rows;
   it.m0 = (group * GROUP_M + in_group - tn * rows) * PAIR_M;
-  it.n0 = tn * (EPI == EPI_GLU ? BN_HALF : BN);
+  it.n0 = (tn * PAIRS + pair) * (EPI == EPI_GLU ? BN_HALF : BN);
   return it;
 }
 
@@ -270,8 +272,8 @@ __device__ __forceinline__ void store_box(const FfnSegment& sg, int i0, int j0, 
   }
 }
 
-template <int EPI, typename T, int ACT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
+template <int EPI, typename T, int ACT, int PAIRS>
+__global__ void __cluster_dims__(2 * PAIRS, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     ffn_gemm_kernel(const __grid_constant__ FfnParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -288,14 +290,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
 
   const int warp = threadIdx.x / 32;
   const int lane = threadIdx.x % 32;
-  const uint32_t rank = cluster_ctarank();
-  const int64_t pair_id = blockIdx.x >> 1;
-  const int64_t num_pairs = gridDim.x >> 1;
+  const uint32_t rank = cluster_ctarank() & 1;  // within the pair
+  const int pair = static_cast<int>(cluster_ctarank() >> 1);
+  const uint32_t even = 2 * static_cast<uint32_t>(pair);  // cluster rank of this pair's even CTA
+  const int64_t cluster_id = blockIdx.x / (2 * PAIRS);
+  const int64_t num_clusters = gridDim.x / (2 * PAIRS);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full_bar[s], 1);
-      mbar_init(&empty_bar[s], 1);
+      mbar_init(&empty_bar[s], PAIRS);  // a stage of A is free when every pair has used it
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull_bar[a], 1);
@@ -326,9 +330,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       uint32_t phase = 0;
       uint32_t issued = 0, issued_parity = 0;
       bool ok = true;
-      for (int64_t item = pair_id; ok && item < p.total; item += num_pairs) {
+      for (int64_t item = cluster_id; ok && item < p.total; item += num_clusters) {
         const FfnSegment& sg = p.seg[ffn_seg(p, item)];
-        const Item it = ffn_item<EPI>(sg, item);
+        const Item it = ffn_item<EPI, PAIRS>(sg, item, pair);
         const int m_cta = it.m0 + static_cast<int>(rank) * BM;
         const int n_cta = EPI == EPI_GLU ? it.n0 : it.n0 + static_cast<int>(rank) * BN_HALF;
         for (int kb = it.kb0; kb < it.kb1; ++kb) {
@@ -337,14 +341,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
             break;
           }
           if (rank == 0) mbar_arrive_expect_tx(&full_bar[stage], PAIR_STAGE_BYTES);
-          const uint32_t bar = mapa_shared(smem_u32(&full_bar[stage]), 0);
+          const uint32_t bar = mapa_shared(smem_u32(&full_bar[stage]), even);
           uint8_t* a_dst = sA + stage * TILE_BYTES;
           uint8_t* b_dst = sB + stage * TILE_BYTES;
-          const int pair = kb >= sg.k_blocks[0] ? 1 : 0;
-          const int k = (pair ? kb - sg.k_blocks[0] : kb) * BK;
-          const CUtensorMap* ma = &sg.a[pair];
-          const CUtensorMap* mb = EPI == EPI_GLU ? &sg.b[rank] : &sg.b[pair];
-          if (EPI == EPI_STORE && sg.a_mn) {
+          const int second = kb >= sg.k_blocks[0] ? 1 : 0;  // operand pair
+          const int k = (second ? kb - sg.k_blocks[0] : kb) * BK;
+          const CUtensorMap* ma = &sg.a[second];
+          const CUtensorMap* mb = EPI == EPI_GLU ? &sg.b[rank] : &sg.b[second];
+          if constexpr (PAIRS == 2) {
+            // the pairs share their rows of A: each loads half of them for both
+            const uint16_t mask = static_cast<uint16_t>(0x5u << rank);
+            const int m_half = m_cta + pair * 64;
+            uint8_t* dst = a_dst + pair * MN_CHUNK_BYTES;  // 64 rows x 64 or 64 x 64 of either layout
+            if (EPI == EPI_STORE && sg.a_mn) tma_load_2d_pair_multicast(dst, ma, bar, mask, m_half, k);
+            else tma_load_2d_pair_multicast(dst, ma, bar, mask, k, m_half);
+          } else if (EPI == EPI_STORE && sg.a_mn) {
 #pragma unroll
             for (int q = 0; q < BM / 64; ++q)
               tma_load_2d_pair(a_dst + q * MN_CHUNK_BYTES, ma, bar, m_cta + q * 64, k);
@@ -385,9 +396,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       int acc = 0;
       uint32_t acc_phase = 0;
       bool ok = true, issued_any = false;
-      for (int64_t item = pair_id; ok && item < p.total; item += num_pairs) {
+      for (int64_t item = cluster_id; ok && item < p.total; item += num_clusters) {
         const FfnSegment& sg = p.seg[ffn_seg(p, item)];
-        const Item it = ffn_item<EPI>(sg, item);
+        const Item it = ffn_item<EPI, PAIRS>(sg, item, pair);
         const bool a_mn = EPI == EPI_STORE && sg.a_mn;
         const bool b_mn = EPI == EPI_DGLU || (EPI == EPI_STORE && sg.b_mn);
         const uint32_t idesc = idesc_f16kind_f32(PAIR_M, BN, a_mn, b_mn, FP16);
@@ -414,21 +425,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
             umma_bf16_pair(d_tmem, ad, bd, idesc, (kb - it.kb0) | k ? 1u : 0u);
           }
           issued_any = true;
-          umma_commit_pair_multicast(&empty_bar[stage], 0x3);
+          umma_commit_pair_multicast(&empty_bar[stage], (1u << (2 * PAIRS)) - 1);
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
           }
         }
         if (!ok) break;
-        umma_commit_pair_multicast(&tfull_bar[acc], 0x3);
+        umma_commit_pair_multicast(&tfull_bar[acc], static_cast<uint16_t>(0x3u << even));
         if (++acc == 2) {
           acc = 0;
           acc_phase ^= 1u;
         }
       }
       if (!ok && issued_any) {
-        umma_commit_pair_multicast(drain_bar, 0x1);
+        umma_commit_pair_multicast(drain_bar, static_cast<uint16_t>(0x1u << even));
         wait_drain(drain_bar, 0, 50000000ull);
       }
     }
@@ -437,12 +448,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     const int ew = warp - 2;
     const int half = ew >> 2;
     uint8_t* stage = sEpi + ew * EPI_WARP_BYTES;
-    const uint32_t tempty_even = mapa_shared(smem_u32(&tempty_bar[0]), 0);
+    const uint32_t tempty_even = mapa_shared(smem_u32(&tempty_bar[0]), even);
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (int64_t item = pair_id; item < p.total; item += num_pairs) {
+    for (int64_t item = cluster_id; item < p.total; item += num_clusters) {
       const FfnSegment& sg = p.seg[ffn_seg(p, item)];
-      const Item it = ffn_item<EPI>(sg, item);
+      const Item it = ffn_item<EPI, PAIRS>(sg, item, pair);
       const int i0 = it.m0 + static_cast<int>(rank) * BM + quarter * 32;
       const int jh = it.n0 + half * (EPI == EPI_GLU ? BN_HALF / 2 : BN / 2);  // first column of this warp
       uint4 raw[2][EPI == EPI_DGLU ? 12 : 1];
@@ -483,7 +494,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         // A part of the sum along K: this warp's 32 x 128 values go to the
         // workspace; the warp that arrives last for them adds all parts, in
         // order, and stores the result. Warps without rows have nothing to do.
-        const int64_t region = (static_cast<int64_t>(it.split_tile) * 2 + rank) * EPI_WARPS + ew;
+        const int64_t region = ((static_cast<int64_t>(it.split_tile) * PAIRS + pair) * 2 + rank) * EPI_WARPS + ew;
         float4* mine = reinterpret_cast<float4*>(sg.partial) + (region * sg.splits + it.split) * (32 * 32) + lane;
         if (i0 < sg.M) {
 #pragma unroll
@@ -561,7 +572,10 @@ PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
   return fn;
 }
 
-enum MapUse { MAP_ROWS, MAP_COLS, MAP_STORE };  // K-major operand, MN-major operand, output boxes
+enum MapUse { MAP_ROWS, MAP_COLS, MAP_STORE };  // 128 x 64 boxes, 64 x 64 boxes, 32 x 32 output boxes
+
+// Boxes of a K-major A: the two pairs of a cluster each load half its rows.
+MapUse map_a(int pairs) { return pairs == 2 ? MAP_COLS : MAP_ROWS; }
 
 // A row-major rows x cols matrix of 16-bit elements with row pitch ld.
 bool encode(CUtensorMap* map, const void* base, int dtype, int64_t rows, int64_t cols, int64_t ld, MapUse use) {
@@ -577,48 +591,51 @@ bool encode(CUtensorMap* map, const void* base, int dtype, int64_t rows, int64_t
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int EPI, typename T, int ACT>
-int resident_pairs(int num_sms) {
+template <int EPI, typename T, int ACT, int PAIRS>
+int resident_clusters(int num_sms) {
   static std::atomic<int> cached[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
   const int known = cached[dev].load(std::memory_order_relaxed);
   if (known > 0) return known;
-  if (cudaFuncSetAttribute(ffn_gemm_kernel<EPI, T, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  if (cudaFuncSetAttribute(ffn_gemm_kernel<EPI, T, ACT, PAIRS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(SMEM_BYTES)) != cudaSuccess)
     return 0;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(num_sms & ~1));
+  cfg.gridDim = dim3(static_cast<unsigned>(num_sms / (2 * PAIRS) * 2 * PAIRS));
   cfg.blockDim = dim3(NUM_THREADS);
   cfg.dynamicSmemBytes = SMEM_BYTES;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.x = 2 * PAIRS;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, ffn_gemm_kernel<EPI, T, ACT>, &cfg) != cudaSuccess || n <= 0) {
+  if (cudaOccupancyMaxActiveClusters(&n, ffn_gemm_kernel<EPI, T, ACT, PAIRS>, &cfg) != cudaSuccess || n <= 0) {
     cudaGetLastError();
-    n = num_sms / 2;
+    n = num_sms / (2 * PAIRS);
   }
   cached[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 
-template <int EPI, typename T, int ACT>
+template <int EPI, typename T, int ACT, int PAIRS>
 cudaError_t launch(FfnParams& p, int num_sms, cudaStream_t stream) {
-  const int pairs = resident_pairs<EPI, T, ACT>(num_sms);
-  if (pairs == 0) return cudaErrorInvalidConfiguration;
-  const unsigned grid = static_cast<unsigned>(2 * std::min<int64_t>(p.total, pairs));
-  return launch_dependent(ffn_gemm_kernel<EPI, T, ACT>, dim3(grid), dim3(NUM_THREADS), SMEM_BYTES, stream, p);
+  const int clusters = resident_clusters<EPI, T, ACT, PAIRS>(num_sms);
+  if (clusters == 0) return cudaErrorInvalidConfiguration;
+  const unsigned grid = static_cast<unsigned>(2 * PAIRS * std::min<int64_t>(p.total, clusters));
+  return launch_dependent(ffn_gemm_kernel<EPI, T, ACT, PAIRS>, dim3(grid), dim3(NUM_THREADS), SMEM_BYTES, stream, p);
 }
 
 template <int EPI, int ACT = 0>
 cudaError_t launch(FfnParams& p, int dtype, int num_sms, cudaStream_t stream) {
-  return dtype == PRM_BF16 ? launch<EPI, __nv_bfloat16, ACT>(p, num_sms, stream)
-                           : launch<EPI, __half, ACT>(p, num_sms, stream);
+  if (p.pairs == 2)
+    return dtype == PRM_BF16 ? launch<EPI, __nv_bfloat16, ACT, 2>(p, num_sms, stream)
+                             : launch<EPI, __half, ACT, 2>(p, num_sms, stream);
+  return dtype == PRM_BF16 ? launch<EPI, __nv_bfloat16, ACT, 1>(p, num_sms, stream)
+                           : launch<EPI, __half, ACT, 1>(p, num_sms, stream);
 }
 
 template <int EPI>
@@ -628,34 +645,48 @@ cudaError_t launch_act(FfnParams& p, int act, int dtype, int num_sms, cudaStream
   return launch<EPI, PRM_ACT_GELU_TANH>(p, dtype, num_sms, stream);
 }
 
-int64_t tiles_of(int64_t M, int64_t N) { return ((M + PAIR_M - 1) / PAIR_M) * ((N + BN - 1) / BN); }
+// Work items of an M x N product with tiles of 256 x tile_n, `pairs` of them
+// side by side to an item.
+int64_t items_of(int64_t M, int64_t N, int tile_n, int pairs) {
+  return ((M + PAIR_M - 1) / PAIR_M) * ((N + static_cast<int64_t>(tile_n) * pairs - 1) / (tile_n * pairs));
+}
+// Clusters that run at once: 76 pairs, or 36 clusters of two pairs (four CTAs
+// fit a GPC's SMs less well).
+int clusters_of(int pairs) { return pairs == 2 ? 36 : 76; }
+// Two pairs to a cluster read A once for both, a quarter less operand traffic
+// per SM: the backward pass takes 1081 us instead of 1123 at 8192 x 2048 x 8192
+// and 3410 instead of 3744 at 4096 x 5120 x 20480, with 144 of the 152 SMs. With
+// less than two waves of such items the finer ones win.
+int pairs_for(int64_t items_of_two) { return items_of_two >= 72 ? 2 : 1; }
 
-// The tiles of a product that runs alone go to the pairs in waves. Where the
-// last wave is not full, its tiles are split along K over the idle pairs:
-// 256 tiles on 76 pairs take 3.5 tile times instead of 4.
-constexpr int FFN_PAIRS = 76;
+// The items of a product that runs alone go to the clusters in waves. Where
+// the last wave is not full, its items are split along K over the idle
+// clusters: 256 tiles on 76 pairs take 3.5 tile times instead of 4.
 constexpr int MIN_PART = 4;  // slices of K in a part
 struct Split {
-  int64_t whole;
+  int pairs;
+  int64_t whole, rest;  // items computed whole and in parts
   int splits;
 };
 Split split_last_wave(int64_t M, int64_t N, int64_t K) {
-  const int64_t tiles = tiles_of(M, N);
-  const int64_t rest = tiles % FFN_PAIRS;
+  Split s{pairs_for(items_of(M, N, BN, 2)), 0, 0, 1};
+  const int64_t items = items_of(M, N, BN, s.pairs), at_once = clusters_of(s.pairs);
+  const int64_t rest = items % at_once;
   const int64_t kb = (K + BK - 1) / BK;
   // adding up the parts costs about two slices of K per part: no more parts than that pays for
   const int64_t pays = static_cast<int64_t>(std::sqrt(static_cast<double>(kb) / 2)) + 1;
-  const int64_t s = rest == 0 ? 1 : std::min<int64_t>({FFN_PAIRS / rest, kb / MIN_PART, pays, 16});
-  return s < 2 ? Split{tiles, 1} : Split{tiles - rest, static_cast<int>(s)};
+  const int64_t parts = rest == 0 ? 1 : std::min<int64_t>({at_once / rest, kb / MIN_PART, pays, 16});
+  s.whole = parts < 2 ? items : items - rest;
+  s.rest = items - s.whole;
+  s.splits = parts < 2 ? 1 : static_cast<int>(parts);
+  return s;
 }
-size_t partial_bytes(int64_t M, int64_t N, const Split& s) {
-  return static_cast<size_t>(tiles_of(M, N) - s.whole) * s.splits * PAIR_M * BN * sizeof(float);
+size_t partial_bytes(const Split& s) {
+  return static_cast<size_t>(s.rest) * s.pairs * s.splits * PAIR_M * BN * sizeof(float);
 }
-size_t counter_bytes(int64_t M, int64_t N, const Split& s) {
-  return static_cast<size_t>(tiles_of(M, N) - s.whole) * 2 * EPI_WARPS * 4;
-}
+size_t counter_bytes(const Split& s) { return static_cast<size_t>(s.rest) * s.pairs * 2 * EPI_WARPS * 4; }
 
-// Extents and tile counts of one product, and its place in the queue.
+// Extents and items of one product, and its place in the queue.
 void queue(FfnParams& p, FfnSegment& sg, int64_t M, int64_t N, int64_t K0, int64_t K1, bool a_mn, bool b_mn,
            int tile_n) {
   sg.M = static_cast<int>(M);
@@ -665,14 +696,14 @@ void queue(FfnParams& p, FfnSegment& sg, int64_t M, int64_t N, int64_t K0, int64
   sg.a_mn = a_mn;
   sg.b_mn = b_mn;
   sg.tiles_m = static_cast<int>((M + PAIR_M - 1) / PAIR_M);
-  sg.tiles_n = static_cast<int>((N + tile_n - 1) / tile_n);
-  const int tiles = sg.tiles_m * sg.tiles_n;
+  const int items = static_cast<int>(items_of(M, N, tile_n, p.pairs));
+  sg.tiles_n = items / sg.tiles_m;
   if (sg.splits < 2) {
-    sg.whole = tiles;
+    sg.whole = items;
     sg.splits = 1;
   }
   sg.item_begin = p.total;
-  p.total += sg.whole + static_cast<int64_t>(tiles - sg.whole) * sg.splits;
+  p.total += sg.whole + static_cast<int64_t>(items - sg.whole) * sg.splits;
   p.seg[p.nseg++] = sg;
 }
 
@@ -691,8 +722,8 @@ FfnSizes sizes(int64_t T, int64_t d, int64_t f) {
   s.saved = act + static_cast<size_t>((T + 31) / 32) * ((f + 31) / 32) * 384 * 16;
   s.down = split_last_wave(T, d, f);
   s.fwd_partial = act;
-  s.fwd_counters = act + partial_bytes(T, d, s.down);
-  s.fwd = s.fwd_counters + round_up(counter_bytes(T, d, s.down), 256);
+  s.fwd_counters = act + partial_bytes(s.down);
+  s.fwd = s.fwd_counters + round_up(counter_bytes(s.down), 256);
   s.bwd_du = act;
   s.bwd = 2 * act;
   return s;
@@ -755,9 +786,10 @@ extern "C" int prm_gated_ffn_forward(const void* x, int64_t ldx, const void* w_g
   p.gu = saved != nullptr ? reinterpret_cast<uint4*>(static_cast<char*>(saved) + sz.saved_h) : nullptr;
   uint32_t* counters = reinterpret_cast<uint32_t*>(ws + sz.fwd_counters);
   p.zero = counters;
-  p.zero_count = static_cast<int>(counter_bytes(tokens, d, sz.down) / 4);
+  p.zero_count = static_cast<int>(counter_bytes(sz.down) / 4);
+  p.pairs = pairs_for(items_of(tokens, f, BN_HALF, 2));
   FfnSegment sg{};
-  if (!encode(&sg.a[0], x, dtype, tokens, d, ldx, MAP_ROWS) || !encode(&sg.b[0], w_gate, dtype, f, d, d, MAP_ROWS) ||
+  if (!encode(&sg.a[0], x, dtype, tokens, d, ldx, map_a(p.pairs)) || !encode(&sg.b[0], w_gate, dtype, f, d, d, MAP_ROWS) ||
       !encode(&sg.b[1], w_up, dtype, f, d, d, MAP_ROWS) || !encode(&sg.out[0], h, dtype, tokens, f, f, MAP_STORE))
     return PRM_ERR_CUDA;
   queue(p, sg, tokens, f, d, 0, false, false, BN_HALF);
@@ -765,8 +797,9 @@ extern "C" int prm_gated_ffn_forward(const void* x, int64_t ldx, const void* w_g
 
   FfnParams q{};
   q.err = dev->d_err;
+  q.pairs = sz.down.pairs;
   FfnSegment dn{};
-  if (!encode(&dn.a[0], h, dtype, tokens, f, f, MAP_ROWS) || !encode(&dn.b[0], w_down, dtype, d, f, f, MAP_ROWS) ||
+  if (!encode(&dn.a[0], h, dtype, tokens, f, f, map_a(q.pairs)) || !encode(&dn.b[0], w_down, dtype, d, f, f, MAP_ROWS) ||
       !encode(&dn.out[0], y, dtype, tokens, d, d, MAP_STORE))
     return PRM_ERR_CUDA;
   dn.whole = static_cast<int>(sz.down.whole);
@@ -819,8 +852,9 @@ extern "C" int prm_gated_ffn_backward(const void* dy, int64_t lddy, const void* 
   FfnParams p{};
   p.err = dev->d_err;
   p.gu = reinterpret_cast<uint4*>(const_cast<char*>(static_cast<const char*>(saved)) + sz.saved_h);
+  p.pairs = pairs_for(items_of(tokens, f, BN, 2));
   FfnSegment sg{};
-  if (!encode(&sg.a[0], dy, dtype, tokens, d, lddy, MAP_ROWS) || !encode(&sg.b[0], w_down, dtype, d, f, f, MAP_COLS) ||
+  if (!encode(&sg.a[0], dy, dtype, tokens, d, lddy, map_a(p.pairs)) || !encode(&sg.b[0], w_down, dtype, d, f, f, MAP_COLS) ||
       !encode(&sg.out[0], dg, dtype, tokens, f, f, MAP_STORE) ||
       !encode(&sg.out[1], du, dtype, tokens, f, f, MAP_STORE))
     return PRM_ERR_CUDA;
@@ -831,11 +865,14 @@ extern "C" int prm_gated_ffn_backward(const void* dy, int64_t lddy, const void* 
   // longer sums first, so that the last tiles of the queue are short.
   FfnParams q{};
   q.err = dev->d_err;
+  q.pairs = pairs_for((dx != nullptr ? items_of(tokens, d, BN, 2) : 0) +
+                      (weights ? 2 * items_of(f, d, BN, 2) + items_of(d, f, BN, 2) : 0));
   bool ok = true;
   auto add_dx = [&] {
     if (dx == nullptr) return;
     FfnSegment s{};
-    ok = ok && encode(&s.a[0], dg, dtype, tokens, f, f, MAP_ROWS) && encode(&s.a[1], du, dtype, tokens, f, f, MAP_ROWS) &&
+    ok = ok && encode(&s.a[0], dg, dtype, tokens, f, f, map_a(q.pairs)) &&
+         encode(&s.a[1], du, dtype, tokens, f, f, map_a(q.pairs)) &&
          encode(&s.b[0], w_gate, dtype, f, d, d, MAP_COLS) && encode(&s.b[1], w_up, dtype, f, d, d, MAP_COLS) &&
          encode(&s.out[0], dx, dtype, tokens, d, d, MAP_STORE);
     queue(q, s, tokens, d, f, f, false, true, BN);
