@@ -193,8 +193,8 @@ inline NormShape norm_shape(int64_t d, size_t row_bytes, int arrays, bool vec, b
   const struct {
     int rows, stages;
     size_t room;
-  } tries[4] = {{2, 2, half}, {1, 2, half}, {1, 2, whole}, {1, 1, whole}};
-  for (int k = s.size == 0 ? 0 : 2; ring && k < 4; ++k) {
+  } tries[5] = {{2, 2, half}, {1, 2, half}, {2, 2, whole}, {1, 2, whole}, {1, 1, whole}};
+  for (int k = s.size == 0 ? 0 : s.size == 1 ? 2 : 3; ring && k < 5; ++k) {
     s.rows = tries[k].rows;
     const size_t stage = row_bytes * s.groups * s.rows + (vec ? 0 : 32 * arrays);
     s.stages =

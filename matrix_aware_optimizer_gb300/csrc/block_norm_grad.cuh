@@ -12,14 +12,26 @@
 // Persistent CTAs, each with a contiguous range of rows and a fixed thread
 // per column, so the column sums stay in registers and need no atomics. Rows
 // stream into a ring of shared-memory stages by bulk copies (rows are
-// contiguous, so a stage of several short rows is still one copy per array). Where a sample ends inside a CTA's range
-// the modulation sums are written out: to their place if the whole sample
-// lies in the range, else as the range's first or last partial sum, which
-// norm_join_kernel adds in order.
+// contiguous, so a stage of several short rows is still one copy per array);
+// thread 0 fills it. The gains and the sample's scale and gate lie in shared
+// memory in fp32. Where a sample ends inside a CTA's range the modulation
+// sums are written out: to their place if the whole sample lies in the range,
+// else as the range's first or last partial sum, which norm_join_kernel adds
+// in order.
 //
-// Rows that bulk copies cannot fetch (d % 8 != 0, pointers off 16 bytes) or
-// of which two do not fit in shared memory are read by the consumers
-// themselves, element by element, coalesced.
+// Rows of any width and start come through the ring: a copy's ends are
+// rounded to 16 bytes and the threads read strided elements (ELEM). Tensors
+// that do not start on 16 bytes are read from memory by the threads (DIRECT).
+//
+// Measured (device time, share of the copy bandwidth on the bytes above):
+// 32 x 1024 x 2048 modulated, fp32 stream and bf16 block, 191 us (93 %);
+// 8191 x 5120 bf16 with both gains 110 us (67 %); 65536 x 512 bf16 87 us (69
+// %); 30000 x 1001 bf16 240 us (22 %). What is left is the chain of each
+// row -- load, reduce, reduce, store -- behind which only the rows of the
+// other CTA of the SM, or the thread's second row, can hide: registers (40
+// column sums and their operands per thread) allow no more of them. Fewer
+// instructions helped most: packed pairs, two rows per thread and step
+// (139 -> 110 us at 5120), values formed again rather than held.
 #pragma once
 
 #include <algorithm>
@@ -66,6 +78,8 @@ template <typename RT, typename BT, int SIZE, int R, int NV, int ACCESS, bool MO
 __global__ void __launch_bounds__(norm_threads(SIZE), SIZE == 0 ? 2 : 1)
     norm_backward_kernel(const __grid_constant__ NormGradParams p, const NormGradIo<RT, BT> io) {
   constexpr bool RING = ACCESS != DIRECT;
+  // n and q are formed again from the stage behind the reductions instead of held across them: registers.
+  constexpr bool AGAIN = ACCESS == VEC;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float scratch[2][128];
   __shared__ uint64_t full_bar[MAX_STAGES], empty_bar[MAX_STAGES];
@@ -304,11 +318,30 @@ __global__ void __launch_bounds__(norm_threads(SIZE), SIZE == 0 ? 2 : 1)
           else
             return gather_f8(a + at0 + i * d + col[v], left[v], tpr);
         };
+        // (r - m_r) s_r, and (z - m_z) s_z where z is normed
+        auto normed_r = [&](int i, int v) -> F8 {
+          F8 n = row8(io.r, by + bdr, i, v);
+          const float s0 = -st[i].x * st[i].y;
+          const uint64_t mul = f2_pack(st[i].y, st[i].y), add = f2_pack(s0, s0);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) n.p[k] = f2_fma(n.p[k], mul, add);
+          return n;
+        };
+        auto normed_z = [&](int i, int v) -> F8 {
+          F8 q = row8(io.z, by + bdr + br, i, v);
+          if (post) {
+            const float s0 = -st[i].z * st[i].w;
+            const uint64_t mul = f2_pack(st[i].w, st[i].w), add = f2_pack(s0, s0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) q.p[k] = f2_fma(q.p[k], mul, add);
+          }
+          return q;
+        };
         F8 D[R][NV];
         float sums[R][2];
         uint64_t part[R][2];
         if (io.dy != nullptr) {
-          F8 nn[R][NV];
+          F8 nn[AGAIN ? 1 : R][NV];
 #pragma unroll
           for (int i = 0; i < R; ++i) part[i][0] = part[i][1] = 0;
 #pragma unroll
@@ -319,11 +352,8 @@ __global__ void __launch_bounds__(norm_threads(SIZE), SIZE == 0 ? 2 : 1)
 #pragma unroll
             for (int i = 0; i < R; ++i) {
               if (!live[i][v]) continue;
-              F8 x = row8(io.dy, 0, i, v), n = row8(io.r, by + bdr, i, v);
-              const float s0 = -st[i].x * st[i].y;
-              const uint64_t mul = f2_pack(st[i].y, st[i].y), add = f2_pack(s0, s0);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) n.p[k] = f2_fma(n.p[k], mul, add);
+              F8 x = row8(io.dy, 0, i, v);
+              const F8 n = normed_r(i, v);
               if constexpr (MOD) {
                 if (shift) {
 #pragma unroll
@@ -349,7 +379,7 @@ __global__ void __launch_bounds__(norm_threads(SIZE), SIZE == 0 ? 2 : 1)
                 part[i][1] = f2_add(part[i][1], x.p[k]);
               }
               D[i][v] = x;
-              nn[i][v] = n;
+              if constexpr (!AGAIN) nn[i][v] = n;
             }
           }
           join_halves(part, sums);
@@ -364,9 +394,12 @@ __global__ void __launch_bounds__(norm_threads(SIZE), SIZE == 0 ? 2 : 1)
               if (!live[i][v]) continue;
               F8 x = f8_zero();
               if (io.dr != nullptr) x = row8(io.dr, by, i, v);
+              F8 n;
+              if constexpr (AGAIN) n = normed_r(i, v);
+              else n = nn[i][v];
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
-                x.p[k] = f2_fma(nn[i][v].p[k], M1, x.p[k]);
+                x.p[k] = f2_fma(n.p[k], M1, x.p[k]);
                 if (p.n.layer) x.p[k] = f2_add(x.p[k], M2);
                 D[i][v].p[k] = f2_fma(S, D[i][v].p[k], x.p[k]);
               }
@@ -393,7 +426,7 @@ __global__ void __launch_bounds__(norm_threads(SIZE), SIZE == 0 ? 2 : 1)
             }
         }
         if (io.z != nullptr) {
-          F8 q[R][NV];
+          F8 q[AGAIN ? 1 : R][NV];
           if (post || gate) {
 #pragma unroll
             for (int i = 0; i < R; ++i) part[i][0] = part[i][1] = 0;
@@ -405,13 +438,7 @@ __global__ void __launch_bounds__(norm_threads(SIZE), SIZE == 0 ? 2 : 1)
 #pragma unroll
               for (int i = 0; i < R; ++i) {
                 if (!live[i][v]) continue;
-                F8 x = row8(io.z, by + bdr + br, i, v);
-                if (post) {
-                  const float s0 = -st[i].z * st[i].w;
-                  const uint64_t mul = f2_pack(st[i].w, st[i].w), add = f2_pack(s0, s0);
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) x.p[k] = f2_fma(x.p[k], mul, add);
-                }
+                const F8 x = normed_z(i, v);
                 if constexpr (MOD) {
                   if (gate) {
 #pragma unroll
@@ -431,7 +458,7 @@ __global__ void __launch_bounds__(norm_threads(SIZE), SIZE == 0 ? 2 : 1)
                     part[i][1] = f2_add(part[i][1], D[i][v].p[k]);
                   }
                 }
-                q[i][v] = x;
+                if constexpr (!AGAIN) q[i][v] = x;
               }
             }
           }
@@ -446,8 +473,11 @@ __global__ void __launch_bounds__(norm_threads(SIZE), SIZE == 0 ? 2 : 1)
 #pragma unroll
               for (int v = 0; v < NV; ++v) {
                 if (!live[i][v]) continue;
+                F8 x;
+                if constexpr (AGAIN) x = normed_z(i, v);
+                else x = q[i][v];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) D[i][v].p[k] = f2_fma(S, D[i][v].p[k], f2_fma(q[i][v].p[k], M1, M2));
+                for (int k = 0; k < 4; ++k) D[i][v].p[k] = f2_fma(S, D[i][v].p[k], f2_fma(x.p[k], M1, M2));
               }
             }
           }
@@ -654,8 +684,10 @@ cudaError_t launch_shape(NormGradParams& p, const NormShape& s, const NormGradAr
   if (s.size == 0)
     return s.rows == 2 ? go(integral_constant<int, 0>{}, integral_constant<int, 2>{})
                        : go(integral_constant<int, 0>{}, integral_constant<int, 1>{});
-  return s.size == 1 ? go(integral_constant<int, 1>{}, integral_constant<int, 1>{})
-                     : go(integral_constant<int, 2>{}, integral_constant<int, 1>{});
+  if (s.size == 1)
+    return s.rows == 2 ? go(integral_constant<int, 1>{}, integral_constant<int, 2>{})
+                       : go(integral_constant<int, 1>{}, integral_constant<int, 1>{});
+  return go(integral_constant<int, 2>{}, integral_constant<int, 1>{});
 }
 
 // Defined per pair of types, each pair's kernels in a translation unit of a
