@@ -516,6 +516,8 @@ template <typename DT, typename GT, int ACCESS>
 __global__ void __launch_bounds__(EMB_THREADS) piece_kernel(const EmbSum s, const DT* __restrict__ dout, GT* grad) {
   constexpr bool OUT_VEC = ACCESS == VEC;
   extern __shared__ __align__(128) uint8_t rows_smem[];  // [group][entry][pitch]
+  __shared__ uint32_t entry_key[EMB_THREADS / 2 * EMB_PIECE];  // [group][entry]
+  __shared__ uint8_t entry_off[ACCESS == ELEM ? EMB_THREADS / 2 * EMB_PIECE : 1];  // its row's offset from 16 bytes
   __shared__ uint64_t bar;
   __shared__ volatile int abort_flag;
   const int tid = threadIdx.x & (s.tpc - 1);
@@ -540,9 +542,14 @@ __global__ void __launch_bounds__(EMB_THREADS) piece_kernel(const EmbSum s, cons
     uint32_t bytes = 0;
     for (int pass = 0; pass < 2; ++pass) {
       for (int idx = threadIdx.x; idx < groups * EMB_PIECE; idx += EMB_THREADS) {
+        // (entries past the list's end: padding, so that their pieces end there)
         const int64_t entry = piece0 * EMB_PIECE + idx;
-        if (entry >= s.count || s.keys[entry] >= s.vocab) continue;
-        const DT* src = dout + static_cast<int64_t>(s.pos[entry]) * s.d + c0;
+        const uint32_t key = entry < s.count ? s.keys[entry] : s.vocab;
+        const uint32_t pos = entry < s.count ? s.pos[entry] : 0;
+        if (pass == 0) entry_key[idx] = key;
+        if (key >= s.vocab) continue;
+        const DT* src = dout + static_cast<int64_t>(pos) * s.d + c0;
+        if (ACCESS == ELEM && pass == 0) entry_off[idx] = static_cast<uint8_t>(ring_offset(src));
         uint8_t* dst = rows_smem + static_cast<size_t>(idx) * s.pitch;
         const uint32_t n = ACCESS == VEC ? width * static_cast<uint32_t>(sizeof(DT)) : ring_bytes(src, width, dout_end);
         if (pass == 0) {
@@ -555,6 +562,12 @@ __global__ void __launch_bounds__(EMB_THREADS) piece_kernel(const EmbSum s, cons
       if (pass == 0) mbar_arrive_expect_tx(&bar, bytes);
     }
   }
+  const int64_t piece = piece0 + group;
+  const bool mine = piece < s.pieces;
+  const uint32_t i0 = mine ? static_cast<uint32_t>(piece) * EMB_PIECE : 0;
+  const uint32_t n = min(s.count - i0, static_cast<uint32_t>(EMB_PIECE));
+  const uint32_t before = mine && i0 > 0 ? s.keys[i0 - 1] : 0xffffffffu;
+  const uint32_t after = mine && i0 + n < s.count ? s.keys[i0 + n] : 0xffffffffu;
   if (blockIdx.x < s.clear_ctas && blockIdx.y == 0) clear_gaps(s, grad, blockIdx.x);
   if (!sums) return;
   if constexpr (ACCESS != DIRECT) {
@@ -563,18 +576,15 @@ __global__ void __launch_bounds__(EMB_THREADS) piece_kernel(const EmbSum s, cons
       return;
     }
   }
-  const int64_t piece = piece0 + group;
-  if (piece >= s.pieces) return;
-  const uint32_t i0 = static_cast<uint32_t>(piece) * EMB_PIECE;
-  const uint32_t n = min(s.count - i0, static_cast<uint32_t>(EMB_PIECE));
-  const uint32_t before = i0 > 0 ? s.keys[i0 - 1] : 0xffffffffu;
-  const uint32_t after = i0 + n < s.count ? s.keys[i0 + n] : 0xffffffffu;
+  if (!mine) return;
   float acc[8];
   uint32_t run = 0xffffffffu;  // key of the run at work
   bool entered = false;        // it entered from the piece before
 #pragma unroll 4
   for (uint32_t j = 0; j < n; ++j) {
-    const uint32_t key = s.keys[i0 + j];
+    uint32_t key;
+    if constexpr (ACCESS == DIRECT) key = s.keys[i0 + j];
+    else key = entry_key[group * EMB_PIECE + j];
     if (key >= s.vocab) break;  // padding is sorted to the end
     float x[8];
     if constexpr (ACCESS == DIRECT) {
@@ -593,8 +603,7 @@ __global__ void __launch_bounds__(EMB_THREADS) piece_kernel(const EmbSum s, cons
           raw.get(x);
         }
       } else {
-        const DT* src = dout + static_cast<int64_t>(s.pos[i0 + j]) * s.d + c0;
-        const DT* p = reinterpret_cast<const DT*>(at + ring_offset(src)) + tid;
+        const DT* p = reinterpret_cast<const DT*>(at + entry_off[group * EMB_PIECE + j]) + tid;
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = e * s.tpc + tid < width ? to_f32(p[e * s.tpc]) : 0.f;
       }
@@ -625,10 +634,10 @@ __device__ __forceinline__ uint32_t piece_key(const EmbSum& s, int64_t piece) {
 }
 
 // Adds the head sums of pieces q, q + 1, ... up to `end` while they belong to
-// the run of key v; 8 are loaded at a time. Returns the first that does not.
+// the run of key v; AHEAD are loaded at a time. Returns the first that does not.
+template <int AHEAD>
 __device__ __forceinline__ int64_t add_heads(const EmbSum& s, uint32_t v, int64_t q, int64_t end, int64_t c0, int tid,
                                              float (&acc)[8]) {
-  constexpr int AHEAD = 8;
   for (; q < end; q += AHEAD) {
     uint32_t key[AHEAD];
     float x[AHEAD][8];
@@ -666,13 +675,13 @@ __global__ void __launch_bounds__(EMB_THREADS) block_kernel(const EmbSum s) {
   const uint32_t v = piece_key(s, q);
   if (v >= s.vocab || s.keys[q * EMB_PIECE - 1] != v || !covers_block(s, v, block)) return;
   float acc[8] = {};
-  add_heads(s, v, q, q + EMB_BLOCK, c0, tid, acc);
+  add_heads<8>(s, v, q, q + EMB_BLOCK, c0, tid, acc);
   store_partial(s.block + block * s.partial, c0, tid, acc);
 }
 
 // Adds up the run that starts in `piece` and goes on into the next ones.
 template <typename GT, bool VEC>
-__global__ void __launch_bounds__(EMB_THREADS) span_kernel(const EmbSum s, GT* grad) {
+__global__ void __launch_bounds__(EMB_THREADS, 4) span_kernel(const EmbSum s, GT* grad) {
   const int tid = threadIdx.x & (s.tpc - 1);
   const int64_t piece = static_cast<int64_t>(blockIdx.x) * (EMB_THREADS / s.tpc) + threadIdx.x / s.tpc;
   const int64_t c0 = static_cast<int64_t>(blockIdx.y) * 8 * s.tpc;
@@ -680,16 +689,16 @@ __global__ void __launch_bounds__(EMB_THREADS) span_kernel(const EmbSum s, GT* g
   pdl_launch_dependents();
   if (piece + 1 >= s.pieces) return;
   const uint32_t i1 = static_cast<uint32_t>(piece + 1) * EMB_PIECE;
-  const uint32_t v = s.keys[i1 - 1];
-  if (v >= s.vocab || s.keys[i1] != v) return;
   const uint32_t i0 = i1 - EMB_PIECE;
-  if (s.keys[i0] == v && i0 > 0 && s.keys[i0 - 1] == v) return;  // the run entered from before: an earlier piece's
+  const uint32_t v = s.keys[i1 - 1], next = s.keys[i1], own = s.keys[i0], prior = s.keys[i0 > 0 ? i0 - 1 : 0];
+  if (v >= s.vocab || next != v) return;
+  if (own == v && i0 > 0 && prior == v) return;  // the run entered from before: an earlier piece's
   float acc[8];
   load_partial(s.tail + piece * s.partial, c0, tid, acc);
   int64_t q = piece + 1;
   if (s.block != nullptr) {
     const int64_t edge = min(static_cast<int64_t>(s.pieces), (q + EMB_BLOCK - 1) / EMB_BLOCK * EMB_BLOCK);
-    q = add_heads(s, v, q, edge, c0, tid, acc);
+    q = add_heads<4>(s, v, q, edge, c0, tid, acc);
     if (q < edge) {
       finish_row<GT, VEC>(s, grad, v, c0, tid, acc);
       return;
@@ -701,7 +710,7 @@ __global__ void __launch_bounds__(EMB_THREADS) span_kernel(const EmbSum s, GT* g
       for (int e = 0; e < 8; ++e) acc[e] += x[e];
     }
   }
-  add_heads(s, v, q, s.pieces, c0, tid, acc);
+  add_heads<4>(s, v, q, s.pieces, c0, tid, acc);
   finish_row<GT, VEC>(s, grad, v, c0, tid, acc);
 }
 
@@ -952,7 +961,7 @@ extern "C" int prm_embedding_backward(const void* dout, int dout_dtype, const vo
       using DT = decltype(dt);
       using GT = decltype(gt);
       auto go = [&](auto pieces, auto block, auto span) {
-        if (smem > 48 * 1024) {
+        if (smem > 36 * 1024) {  // (with the static part, above the default limit of 48 KB)
           e = cudaFuncSetAttribute(pieces, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
           if (e != cudaSuccess) return;
         }
