@@ -13,7 +13,10 @@
  * included), work is enqueued asynchronously. Element types are PRM_FP32,
  * PRM_BF16 and PRM_FP16. Every call with nothing to do (no rows) returns
  * PRM_OK; pointers may then be NULL. Sums are held in fp32 and taken in an
- * order fixed by the sizes: the same inputs give the same bits.
+ * order fixed by the sizes: the same inputs give the same bits. The first
+ * call of each kind on a device sets kernels up (attributes, an error word):
+ * make it before any stream capture. Calls on different streams may overlap
+ * when their outputs and workspaces differ.
  */
 #ifndef PRM_BLOCKS_H
 #define PRM_BLOCKS_H
@@ -84,7 +87,7 @@ PRM_API int prm_gated_ffn_backward(const void* dy, int64_t lddy, const void* x, 
 typedef struct {
   int64_t rows;             /* all rows of all samples */
   int64_t rows_per_sample;  /* rows that share a row of gate / scale / shift; divides rows (>= 1) */
-  int64_t d;                /* 1 .. 16384 */
+  int64_t d;                /* 1 .. 8192 */
   int32_t kind;             /* PRM_NORM_* */
   int32_t stream_dtype;     /* x, r, dr, dx */
   int32_t block_dtype;      /* z, y, dy, dz and gate, scale, shift; fp32 only when the stream is, else fp32
@@ -142,6 +145,7 @@ PRM_API int prm_embedding_backward_workspace(int64_t tokens, int64_t vocab, int6
  * it is when accumulating. Tokens are sorted (stably, by a radix sort) and
  * each row's sum is taken in the order of t in fp32, long runs as sums of
  * fixed pieces: no atomics on values. tokens < 2^31 - 2^16, vocab < 2^31.
+ * workspace: 256-byte aligned, prm_embedding_backward_workspace's bytes.
  * Errors: INVALID_ARG, ALIGNMENT, WORKSPACE, UNSUPPORTED, CUDA. */
 PRM_API int prm_embedding_backward(const void* dout, int dout_dtype, const void* token, int token_bytes, void* grad,
                                    int grad_dtype, int accumulate, int64_t tokens, int64_t vocab, int64_t d,

@@ -2,7 +2,9 @@
 whose parameters the optimizer updates. Each operator is a forward and a
 backward call on tensors; PyTorch supplies memory and the stream, every
 arithmetic step runs in libprm. Outputs and workspaces are allocated on the
-stream the call runs on (`stream`, or the current one)."""
+stream the call runs on (`stream`, or the current one). Work that a call
+depends on and that runs on another stream is the caller's to order, as with
+any torch operation."""
 from __future__ import annotations
 
 import contextlib
@@ -28,11 +30,17 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 @contextlib.contextmanager
-def _elsewhere(device: int, stream: Optional[torch.cuda.Stream]):
+def _elsewhere(device: int, stream: Optional[torch.cuda.Stream], *tensors: Optional[torch.Tensor]):
     """Makes the tensors' device and the given stream the current ones, so
-    that what a call allocates belongs to the stream it runs on."""
+    that what a call allocates belongs to the stream it runs on, and tells the
+    allocator that the given stream uses the call's tensors: their memory is
+    not handed out again before its work is done."""
     with torch.cuda.device(device), torch.cuda.stream(stream):  # (a None stream changes nothing)
         yield
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
 
 
 def _is_elsewhere(device: int, stream) -> bool:
@@ -105,7 +113,7 @@ def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down:
     """
     d, f, device = _ffn_check(x, w_gate, w_up, w_down, act)
     if _is_elsewhere(device, stream):
-        with _elsewhere(device, stream):
+        with _elsewhere(device, stream, x, w_gate, w_up, w_down):
             return gated_ffn(x, w_gate, w_up, w_down, act, save)
     x2, ldx = _rows16(x, d)
     tokens = x2.shape[0]
@@ -135,7 +143,7 @@ def gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, 
     if dy.shape != x.shape or dy.dtype is not x.dtype or dy.get_device() != device:
         raise ValueError("dy must have x's shape, type and device")
     if _is_elsewhere(device, stream):
-        with _elsewhere(device, stream):
+        with _elsewhere(device, stream, dy, x, w_gate, w_up, w_down, saved.buffer, *(grads or ())):
             return gated_ffn_backward(dy, x, w_gate, w_up, w_down, saved, act, need_dx, grads)
     x2, ldx = _rows16(x, d)
     dy2, lddy = _rows16(dy, d)
@@ -249,7 +257,7 @@ def block_norm(x: torch.Tensor, z: Optional[torch.Tensor] = None, kind: str = "r
     if join_only and (pre_weight is not None or scale is not None or shift is not None):
         raise ValueError("pre_weight, scale and shift belong to the norm that join_only leaves out")
     if _is_elsewhere(device, stream):
-        with _elsewhere(device, stream):
+        with _elsewhere(device, stream, x, z, post_weight, gate, pre_weight, scale, shift):
             return block_norm(x, z, kind, alpha, post_weight, gate, pre_weight, scale, shift, eps, dtype, join_only)
     if not x.is_contiguous():
         x = x.contiguous()
@@ -282,7 +290,7 @@ def block_norm_backward(dy: Optional[torch.Tensor], dr: Optional[torch.Tensor], 
     if device < 0:
         raise ValueError("r must be a CUDA tensor")
     if _is_elsewhere(device, stream):
-        with _elsewhere(device, stream):
+        with _elsewhere(device, stream, dy, dr, r, z, stats, post_weight, gate, pre_weight, scale, shift):
             return block_norm_backward(dy, dr, r, z, stats, kind, alpha, post_weight, gate, pre_weight, scale, shift,
                                        need_dx)
     block = z.dtype if z is not None else dy.dtype if dy is not None else r.dtype
@@ -338,7 +346,7 @@ def embedding(tokens: torch.Tensor, table: torch.Tensor, scale: float = 1.0, dty
             or not table.is_contiguous() or tokens.get_device() != device:
         raise ValueError("table must be a contiguous vocab x d CUDA tensor of float32, bfloat16 or float16")
     if _is_elsewhere(device, stream):
-        with _elsewhere(device, stream):
+        with _elsewhere(device, stream, tokens, table):
             return embedding(tokens, table, scale, dtype)
     tok = _tokens(tokens)
     vocab, d = table.shape
@@ -378,7 +386,7 @@ def embedding_backward(dout: torch.Tensor, tokens: torch.Tensor, vocab: int, sca
     elif out.shape != (vocab, d) or out.dtype not in _DTYPE or out.get_device() != device or not out.is_contiguous():
         raise ValueError("out must be a contiguous vocab x d tensor of float32, bfloat16 or float16")
     if _is_elsewhere(device, stream):
-        with _elsewhere(device, stream):
+        with _elsewhere(device, stream, dout, tokens, out):
             return embedding_backward(dout, tokens, vocab, scale, dtype, out, accumulate)
     tok = _tokens(tokens)
     if not dout.is_contiguous():

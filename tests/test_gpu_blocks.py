@@ -178,6 +178,26 @@ def test_ffn_on_another_stream():
         assert torch.equal(a, b)
 
 
+def test_ffn_inputs_freed_while_another_stream_reads_them():
+    """The memory of an input that dies right after a call on another stream
+    is not handed out while that stream still has to read it."""
+    x, ws, _ = _ffn_inputs(4096, 512, 1024, BF16)
+    want = prm.gated_ffn(x, *ws)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        busy = torch.zeros(1 << 28, device="cuda")
+        for _ in range(20):
+            busy.add_(1.0)      # keeps the stream from starting the call at once
+    mine = x.clone()
+    torch.cuda.current_stream().synchronize()
+    y = prm.gated_ffn(mine, *ws, stream=s)
+    del mine
+    junk = torch.full_like(x, float("nan"))   # would take the freed block
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and torch.isnan(junk).all()
+
+
 def test_ffn_in_a_graph():
     x, ws, dy = _ffn_inputs(90, 256, 512, BF16)
     _check_ffn(x, ws, dy, "silu")
