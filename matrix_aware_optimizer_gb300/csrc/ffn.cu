@@ -733,6 +733,10 @@ int check(int64_t T, int64_t d, int64_t f) {
   if (T < 0 || d < 1 || f < 1) return PRM_ERR_INVALID_ARG;
   if (d % 8 != 0 || f % 8 != 0) return PRM_ERR_ALIGNMENT;
   if (T >= (int64_t(1) << 31) - 256 || d >= (int64_t(1) << 24) || f >= (int64_t(1) << 24)) return PRM_ERR_UNSUPPORTED;
+  // tiles are counted in 32 bits
+  constexpr int64_t MOST = int64_t(1) << 30;
+  if (items_of(T, f, BN_HALF, 1) > MOST || 3 * items_of(d, f, BN, 1) + items_of(T, d, BN, 1) > MOST)
+    return PRM_ERR_UNSUPPORTED;
   return PRM_OK;
 }
 

@@ -121,6 +121,7 @@ def test_ffn_refusals(lib):
     assert _ffn(lib, ws=None) == N.PRM_ERR_WORKSPACE
     assert _ffn(lib, n=10) == N.PRM_ERR_WORKSPACE
     assert _ffn(lib, T=1 << 31) == N.PRM_ERR_UNSUPPORTED
+    assert _ffn(lib, T=1 << 30, f=1 << 23) == N.PRM_ERR_UNSUPPORTED   # more tiles than 32 bits count
 
     def back(dy=256, lddy=64, saved=256, dx=256, dg=256, du=256, dd=256, n=1 << 30, T=4):
         return lib.prm_gated_ffn_backward(dy, lddy, 256, 64, 256, 256, 256, saved, dx, dg, du, dd, 256, n, T, 64, 64,
