@@ -38,6 +38,7 @@ constexpr int EMB_MAX_BITS = 9;  // digit of one pass
 constexpr int EMB_MAX_BINS = 1 << EMB_MAX_BITS;
 constexpr int EMB_PIECE = 16;
 constexpr int EMB_BLOCK = 32;  // pieces
+constexpr int EMB_AHEAD = 8;   // partial sums under way per thread
 constexpr int EMB_CLUSTER = 8;
 constexpr int EMB_CLUSTER_CHUNK = 8192;  // most keys per CTA of the cluster sort
 
@@ -495,15 +496,21 @@ __device__ __forceinline__ void clear_gaps(const EmbSum& s, GT* grad, uint32_t p
   uint8_t* const base = reinterpret_cast<uint8_t*>(grad);
   const int lane = threadIdx.x & 31;
   uint32_t i = lower_bound(s.keys, s.count, v0);
-  // every warp reads 32 keys of the list at a time; the CTA clears the gaps between them
-  for (uint32_t from = v0; from < v1; i += 32) {
-    const uint32_t mine = i + lane < s.count ? min(s.keys[i + lane], v1) : v1;
-#pragma unroll 1
-    for (int k = 0; k < 32 && from < v1; ++k) {
-      const uint32_t key = __shfl_sync(0xffffffffu, mine, k);
-      if (key > from) clear_bytes(base + from * row_bytes, (key - from) * row_bytes, 0, 1);
-      from = max(from, key + 1);  // (key = v1 ends the loop)
+  // Every warp reads 32 keys of the list at a time; the CTA clears the gaps in
+  // front of them. A run that fills all 32 is left by a search: stepping
+  // through a token with thousands of entries took 50 us more.
+  for (uint32_t from = v0; from < v1;) {
+    const uint32_t key = i + lane < s.count ? min(s.keys[i + lane], v1) : v1;
+    const uint32_t up = __shfl_up_sync(0xffffffffu, key, 1);
+    const uint32_t prev = lane == 0 ? from - 1 : up;
+    for (uint32_t gaps = __ballot_sync(0xffffffffu, key - prev > 1u); gaps != 0; gaps &= gaps - 1) {
+      const int k = __ffs(gaps) - 1;
+      const uint32_t to = __shfl_sync(0xffffffffu, key, k), at = __shfl_sync(0xffffffffu, prev, k) + 1;
+      clear_bytes(base + at * row_bytes, (to - at) * row_bytes, 0, 1);
     }
+    const uint32_t first = __shfl_sync(0xffffffffu, key, 0), last = __shfl_sync(0xffffffffu, key, 31);
+    from = last + 1;  // (a last of v1 ends the loop)
+    i = first == last && from < v1 ? lower_bound(s.keys, s.count, from) : i + 32;
   }
 }
 
@@ -633,22 +640,24 @@ __device__ __forceinline__ uint32_t piece_key(const EmbSum& s, int64_t piece) {
   return piece < s.pieces ? s.keys[piece * EMB_PIECE] : 0xffffffffu;
 }
 
-// Adds the head sums of pieces q, q + 1, ... up to `end` while they belong to
-// the run of key v; AHEAD are loaded at a time. Returns the first that does not.
-template <int AHEAD>
-__device__ __forceinline__ int64_t add_heads(const EmbSum& s, uint32_t v, int64_t q, int64_t end, int64_t c0, int tid,
-                                             float (&acc)[8]) {
-  for (; q < end; q += AHEAD) {
-    uint32_t key[AHEAD];
-    float x[AHEAD][8];
+// Adds the sums rows[q], rows[q + 1], ... up to `end`, each over `unit` pieces,
+// while the run of key v goes through them: `more(q)`. EMB_AHEAD are asked for at
+// a time, since the answer to each takes an L2 access. Returns the first
+// that the run does not reach.
+template <typename More>
+__device__ __forceinline__ int64_t add_sums(const float* rows, int64_t partial, int64_t q, int64_t end, int64_t c0,
+                                            int tid, float (&acc)[8], More&& more) {
+  for (; q < end; q += EMB_AHEAD) {
+    bool in[EMB_AHEAD];
+    float x[EMB_AHEAD][8];
 #pragma unroll
-    for (int k = 0; k < AHEAD; ++k) {
-      key[k] = q + k < end ? piece_key(s, q + k) : 0xffffffffu;
-      load_partial(s.head + min(q + k, static_cast<int64_t>(s.pieces) - 1) * s.partial, c0, tid, x[k]);
+    for (int k = 0; k < EMB_AHEAD; ++k) {
+      in[k] = q + k < end && more(q + k);
+      load_partial(rows + min(q + k, end - 1) * partial, c0, tid, x[k]);
     }
 #pragma unroll
-    for (int k = 0; k < AHEAD; ++k) {
-      if (key[k] != v) return q + k;
+    for (int k = 0; k < EMB_AHEAD; ++k) {
+      if (!in[k]) return q + k;
 #pragma unroll
       for (int e = 0; e < 8; ++e) acc[e] += x[k][e];
     }
@@ -675,13 +684,13 @@ __global__ void __launch_bounds__(EMB_THREADS) block_kernel(const EmbSum s) {
   const uint32_t v = piece_key(s, q);
   if (v >= s.vocab || s.keys[q * EMB_PIECE - 1] != v || !covers_block(s, v, block)) return;
   float acc[8] = {};
-  add_heads<8>(s, v, q, q + EMB_BLOCK, c0, tid, acc);
+  add_sums(s.head, s.partial, q, q + EMB_BLOCK, c0, tid, acc, [](int64_t) { return true; });
   store_partial(s.block + block * s.partial, c0, tid, acc);
 }
 
 // Adds up the run that starts in `piece` and goes on into the next ones.
 template <typename GT, bool VEC>
-__global__ void __launch_bounds__(EMB_THREADS, 4) span_kernel(const EmbSum s, GT* grad) {
+__global__ void __launch_bounds__(EMB_THREADS, 2) span_kernel(const EmbSum s, GT* grad) {
   const int tid = threadIdx.x & (s.tpc - 1);
   const int64_t piece = static_cast<int64_t>(blockIdx.x) * (EMB_THREADS / s.tpc) + threadIdx.x / s.tpc;
   const int64_t c0 = static_cast<int64_t>(blockIdx.y) * 8 * s.tpc;
@@ -695,22 +704,21 @@ __global__ void __launch_bounds__(EMB_THREADS, 4) span_kernel(const EmbSum s, GT
   if (own == v && i0 > 0 && prior == v) return;  // the run entered from before: an earlier piece's
   float acc[8];
   load_partial(s.tail + piece * s.partial, c0, tid, acc);
+  auto heads = [&](int64_t q, int64_t end) {
+    return add_sums(s.head, s.partial, q, end, c0, tid, acc, [&](int64_t p) { return piece_key(s, p) == v; });
+  };
   int64_t q = piece + 1;
   if (s.block != nullptr) {
     const int64_t edge = min(static_cast<int64_t>(s.pieces), (q + EMB_BLOCK - 1) / EMB_BLOCK * EMB_BLOCK);
-    q = add_heads<4>(s, v, q, edge, c0, tid, acc);
-    if (q < edge) {
+    q = heads(q, edge);
+    if (q < edge || edge == s.pieces) {
       finish_row<GT, VEC>(s, grad, v, c0, tid, acc);
       return;
     }
-    for (; q < s.pieces && covers_block(s, v, q / EMB_BLOCK); q += EMB_BLOCK) {
-      float x[8];
-      load_partial(s.block + q / EMB_BLOCK * s.partial, c0, tid, x);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] += x[e];
-    }
+    q = EMB_BLOCK * add_sums(s.block, s.partial, q / EMB_BLOCK, s.pieces / EMB_BLOCK, c0, tid, acc,
+                             [&](int64_t b) { return covers_block(s, v, b); });
   }
-  add_heads<4>(s, v, q, s.pieces, c0, tid, acc);
+  heads(q, s.pieces);
   finish_row<GT, VEC>(s, grad, v, c0, tid, acc);
 }
 

@@ -81,6 +81,18 @@ def test_ffn_shapes(T, d, f):
     _check_ffn(*_ffn_inputs(T, d, f, BF16, seed=T + d + f), "silu")
 
 
+# enough output tiles for clusters of two CTA pairs (one of them without a tile
+# at the end of a row), in the first products, in all of them, in the down
+# projection; few tokens with wide weights
+FFN_LARGE_SHAPES = [(300, 64, 9224), (1100, 72, 9224), (2100, 4104, 72), (2049, 2056, 2568), (6, 1032, 2064),
+                    (8, 2056, 1032)]
+
+
+@pytest.mark.parametrize("T,d,f", FFN_LARGE_SHAPES)
+def test_ffn_large_shapes(T, d, f):
+    _check_ffn(*_ffn_inputs(T, d, f, BF16, seed=T + d + f), "silu")
+
+
 @pytest.mark.parametrize("T", list(range(1, 17)))
 def test_ffn_few_tokens(T):
     _check_ffn(*_ffn_inputs(T, 264, 1032, FP16 if T % 2 else BF16, seed=T), "gelu_tanh")
@@ -538,6 +550,60 @@ def test_embedding_gradient_runs(T, pattern):
     for V in (1, 2, 300, 511, 513, 70001):
         tok = _token_set(T, V, g, pattern).cuda()
         _check_embedding_grad(tok, V, 16 if V > 1000 else 40, BF16, FP32)
+
+
+@pytest.mark.parametrize("T", [16400, 65536, 65537, 140000])
+@pytest.mark.parametrize("pattern", ["uniform", "one", "mixed"])
+def test_embedding_gradient_many_tokens(T, pattern):
+    """Above and below what one cluster sorts; runs over many blocks of pieces."""
+    g = _gen(T)
+    for V in (3, 1000, 300007):     # 300007: three passes over the digits
+        tok = _token_set(T, V, g, pattern).cuda()
+        _check_embedding_grad(tok, V, 12, BF16, FP32)
+        _check_embedding_grad(tok, V, 8, FP32, FP32, accumulate=True)
+
+
+def test_embedding_gradient_run_ends():
+    """Runs that start and end at every place around the edges of a piece and
+    of a block of pieces (of 16 entries and of 32 pieces), up to the last entry."""
+    T = 17000
+    g = _gen(8)
+    for first in (0, 1, 15, 16, 17, 511, 512, 513, 529):
+        for length in (1, 15, 16, 17, 497, 512, 1024, 1040, 5000, T - first):
+            tok = torch.arange(T) + 10
+            tok[first:first + length] = 5 + first     # sorted: below entries that come later, above those before
+            tok[:first] = torch.arange(first) % 5
+            tok = tok[torch.randperm(T, generator=g)].cuda()
+            _check_embedding_grad(tok, T + 10, 4, BF16, FP32)
+
+
+def test_embedding_gradient_off_16_bytes():
+    """dout or the gradient's buffer off 16 bytes: rows read from memory, or written element by element."""
+    g = _gen(9)
+    tok = _token_set(700, 90, g, "mixed").cuda()
+    for d in (64, 1001, 2056):
+        dout = _rand(g, 700, d, dtype=BF16)
+        want = prm.embedding_backward(dout, tok, 90)
+        odd = torch.zeros(700 * d + 1, dtype=BF16, device="cuda")[1:].view(700, d)
+        odd.copy_(dout)
+        assert torch.equal(prm.embedding_backward(odd, tok, 90), want)
+        out = torch.full((90 * d + 1,), float("nan"), device="cuda")[1:].view(90, d)
+        assert prm.embedding_backward(dout, tok, 90, out=out) is out
+        assert torch.equal(out, want)
+        table = torch.randn(90 * d + 1, device="cuda")[1:].view(90, d)
+        assert torch.equal(prm.embedding(tok, table, dtype=BF16), prm.embedding(tok, table.clone(), dtype=BF16))
+
+
+@pytest.mark.parametrize("d", [8, 64, 1001, 2048, 4104])
+def test_embedding_lookup_of_many_tokens(d):
+    g = _gen(d)
+    T = 20001 if d > 512 else 320003      # enough for several rows per thread, with a rest
+    tok = _token_set(T, 500, g, "mixed").cuda()
+    table = _rand(g, 500, d)
+    got = prm.embedding(tok, table, scale=0.5, dtype=BF16)
+    ok = (tok >= 0) & (tok < 500)
+    want = torch.where(ok[:, None], table[tok.clamp(0, 499)] * 0.5, torch.zeros(1, device="cuda")).to(BF16)
+    assert torch.equal(got, want)
 
 
 @pytest.mark.parametrize("d", [1, 5, 8, 100, 1001, 2048, 2056, 5120])
