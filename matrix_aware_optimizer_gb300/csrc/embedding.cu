@@ -21,8 +21,12 @@
 // the table meanwhile; the other rows without tokens are cleared beside the
 // pieces, in the same launch, by CTAs that find the gaps in the sorted list.
 // (Clearing everything first and summing afterwards took 108 us instead of
-// 80 at 8192 tokens, 64000 x 2048 bf16: scattered reads are slow right behind
-// a table of dirty lines in L2.)
+// 80 at 8192 tokens, 64000 x 2048 bf16, both then: scattered reads are slow
+// right behind a table of dirty lines in L2.)
+//
+// Measured, back to back: 62 us there (its bytes at the copy rate: 44) and 138
+// at 65521 tokens of 1001 bf16 into 100003 rows of fp32 (78), of which the sort
+// takes 31, the pieces about 65 and the runs' partial sums about 20.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -37,8 +41,13 @@ constexpr int EMB_TILE = 2048;   // tokens per CTA of a sorting pass
 constexpr int EMB_MAX_BITS = 9;  // digit of one pass
 constexpr int EMB_MAX_BINS = 1 << EMB_MAX_BITS;
 constexpr int EMB_PIECE = 16;
-constexpr int EMB_BLOCK = 32;  // pieces
-constexpr int EMB_AHEAD = 8;   // partial sums under way per thread
+// Partial sums of a long run: by blocks of EMB_BLOCK pieces, EMB_AHEAD under way
+// per thread. 65521 tokens, 100003 x 1001: 142 us with blocks of 32, 138 with
+// 16, 136 with 8, which doubles what the longest runs add up one by one; 8
+// under way took 1 - 3 us more than 4.
+constexpr int EMB_BLOCK = 16;
+constexpr int EMB_AHEAD = 4;
+constexpr int EMB_SPAN_CTAS = 3;  // per SM, of the kernel that adds a run's sums
 constexpr int EMB_CLUSTER = 8;
 constexpr int EMB_CLUSTER_CHUNK = 8192;  // most keys per CTA of the cluster sort
 
@@ -637,38 +646,48 @@ __global__ void __launch_bounds__(EMB_THREADS) piece_kernel(const EmbSum s, cons
 
 // Key of the first entry of a piece, or no key at all behind the last piece.
 __device__ __forceinline__ uint32_t piece_key(const EmbSum& s, int64_t piece) {
-  return piece < s.pieces ? s.keys[piece * EMB_PIECE] : 0xffffffffu;
+  const uint32_t key = s.keys[min(piece, static_cast<int64_t>(s.pieces) - 1) * EMB_PIECE];
+  return piece < s.pieces ? key : 0xffffffffu;
 }
 
-// Adds the sums rows[q], rows[q + 1], ... up to `end`, each over `unit` pieces,
-// while the run of key v goes through them: `more(q)`. EMB_AHEAD are asked for at
-// a time, since the answer to each takes an L2 access. Returns the first
-// that the run does not reach.
+// Adds the sums rows[q], rows[q + 1], ... up to `end`, while the run at work
+// goes through them: `more(q)`, asked of places that may lie behind the end.
+// EMB_AHEAD are loaded at a time, and whether the next ones belong to the run
+// is read beside them: one L2 latency for each EMB_AHEAD. Returns the first
+// place that the run does not reach.
 template <typename More>
 __device__ __forceinline__ int64_t add_sums(const float* rows, int64_t partial, int64_t q, int64_t end, int64_t c0,
                                             int tid, float (&acc)[8], More&& more) {
-  for (; q < end; q += EMB_AHEAD) {
-    bool in[EMB_AHEAD];
+  auto ask = [&](int64_t from) {  // bit k: place from + k belongs to the run
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < EMB_AHEAD; ++k) m |= static_cast<uint32_t>(more(from + k) & (from + k < end)) << k;
+    return m;
+  };
+  constexpr uint32_t ALL = (1u << EMB_AHEAD) - 1;
+  for (uint32_t in = ask(q); in != 0;) {
     float x[EMB_AHEAD][8];
 #pragma unroll
     for (int k = 0; k < EMB_AHEAD; ++k) {
-      in[k] = q + k < end && more(q + k);
-      load_partial(rows + min(q + k, end - 1) * partial, c0, tid, x[k]);
-    }
 #pragma unroll
-    for (int k = 0; k < EMB_AHEAD; ++k) {
-      if (!in[k]) return q + k;
+      for (int e = 0; e < 8; ++e) x[k][e] = 0.f;
+      if (in >> k & 1) load_partial(rows + (q + k) * partial, c0, tid, x[k]);
+    }
+    const uint32_t next = in == ALL ? ask(q + EMB_AHEAD) : 0;
+#pragma unroll
+    for (int k = 0; k < EMB_AHEAD; ++k)
 #pragma unroll
       for (int e = 0; e < 8; ++e) acc[e] += x[k][e];
-    }
+    q += __popc(in);
+    in = next;
   }
-  return end;
+  return q;
 }
 
 // Whether the run of key v, which enters block b of EMB_BLOCK pieces, goes on
-// behind it.
+// behind it (and so covers it, as equal keys stand together).
 __device__ __forceinline__ bool covers_block(const EmbSum& s, uint32_t v, int64_t block) {
-  return piece_key(s, block * EMB_BLOCK) == v && piece_key(s, (block + 1) * EMB_BLOCK) == v;
+  return piece_key(s, (block + 1) * EMB_BLOCK) == v;
 }
 
 // For very long runs: the sum of the heads of each block of pieces that a run
@@ -681,8 +700,9 @@ __global__ void __launch_bounds__(EMB_THREADS) block_kernel(const EmbSum s) {
   pdl_launch_dependents();
   const int64_t q = block * EMB_BLOCK;
   if (q == 0 || q + EMB_BLOCK >= s.pieces) return;
-  const uint32_t v = piece_key(s, q);
-  if (v >= s.vocab || s.keys[q * EMB_PIECE - 1] != v || !covers_block(s, v, block)) return;
+  const uint32_t v = piece_key(s, q), prior = s.keys[q * EMB_PIECE - 1];
+  const bool covered = covers_block(s, v, block);
+  if (v >= s.vocab || prior != v || !covered) return;
   float acc[8] = {};
   add_sums(s.head, s.partial, q, q + EMB_BLOCK, c0, tid, acc, [](int64_t) { return true; });
   store_partial(s.block + block * s.partial, c0, tid, acc);
@@ -690,7 +710,7 @@ __global__ void __launch_bounds__(EMB_THREADS) block_kernel(const EmbSum s) {
 
 // Adds up the run that starts in `piece` and goes on into the next ones.
 template <typename GT, bool VEC>
-__global__ void __launch_bounds__(EMB_THREADS, 2) span_kernel(const EmbSum s, GT* grad) {
+__global__ void __launch_bounds__(EMB_THREADS, EMB_SPAN_CTAS) span_kernel(const EmbSum s, GT* grad) {
   const int tid = threadIdx.x & (s.tpc - 1);
   const int64_t piece = static_cast<int64_t>(blockIdx.x) * (EMB_THREADS / s.tpc) + threadIdx.x / s.tpc;
   const int64_t c0 = static_cast<int64_t>(blockIdx.y) * 8 * s.tpc;
@@ -709,14 +729,13 @@ __global__ void __launch_bounds__(EMB_THREADS, 2) span_kernel(const EmbSum s, GT
   };
   int64_t q = piece + 1;
   if (s.block != nullptr) {
-    const int64_t edge = min(static_cast<int64_t>(s.pieces), (q + EMB_BLOCK - 1) / EMB_BLOCK * EMB_BLOCK);
-    q = heads(q, edge);
-    if (q < edge || edge == s.pieces) {
-      finish_row<GT, VEC>(s, grad, v, c0, tid, acc);
-      return;
-    }
-    q = EMB_BLOCK * add_sums(s.block, s.partial, q / EMB_BLOCK, s.pieces / EMB_BLOCK, c0, tid, acc,
-                             [&](int64_t b) { return covers_block(s, v, b); });
+    const int64_t whole = min(static_cast<int64_t>(s.pieces), (q + EMB_BLOCK - 1) / EMB_BLOCK * EMB_BLOCK);
+    q = heads(q, whole);
+    if (q == whole && q < s.pieces)
+      q = EMB_BLOCK * add_sums(s.block, s.partial, q / EMB_BLOCK, s.pieces / EMB_BLOCK, c0, tid, acc,
+                               [&](int64_t b) { return covers_block(s, v, b); });
+    else
+      q = s.pieces;
   }
   heads(q, s.pieces);
   finish_row<GT, VEC>(s, grad, v, c0, tid, acc);

@@ -565,11 +565,11 @@ def test_embedding_gradient_many_tokens(T, pattern):
 
 def test_embedding_gradient_run_ends():
     """Runs that start and end at every place around the edges of a piece and
-    of a block of pieces (of 16 entries and of 32 pieces), up to the last entry."""
+    of a block of pieces (16 entries, 16 pieces), up to the last entry."""
     T = 17000
     g = _gen(8)
-    for first in (0, 1, 15, 16, 17, 511, 512, 513, 529):
-        for length in (1, 15, 16, 17, 497, 512, 1024, 1040, 5000, T - first):
+    for first in (0, 1, 15, 16, 17, 239, 255, 256, 257, 511, 512, 513, 529):
+        for length in (1, 15, 16, 17, 240, 256, 272, 497, 512, 1024, 1040, 5000, T - first):
             tok = torch.arange(T) + 10
             tok[first:first + length] = 5 + first     # sorted: below entries that come later, above those before
             tok[:first] = torch.arange(first) % 5
