@@ -19,8 +19,9 @@
 // because they are operands of the next product. g and u are kept for the
 // backward pass with 16 significand bits (24-bit floats: fp32 with the low
 // byte cut off, 6 bytes for the two), so that the derivative adds no error
-// next to those roundings: with bf16 g and u the gradients were about 1.3
-// times as far from fp64.
+// next to those roundings: in an fp64 model of these steps (1024 tokens,
+// 512 x 2048) the gradients were 0.0023 from the exact ones, as with g and u
+// kept exactly, and with bf16 g and u 0.0029 - 0.0035.
 //
 // CTA layout, pipeline and TMEM use are those of the Newton-Schulz GEMMs
 // (ns5_gemm.cu): 320 threads, warp 0 TMA producer, warp 1 MMA issue in the
@@ -228,10 +229,10 @@ __device__ __forceinline__ void dglu_chunk(const FfnParams& p, const FfnSegment&
       const uint4 lv = raw[8 + (c >> 3)];
       const int q = (c >> 1) & 3;
       const uint32_t lo = q == 0 ? lv.x : q == 1 ? lv.y : q == 2 ? lv.z : lv.w;
-      // lo holds (g, u) of the even column in bytes 0, 1 and of the odd one in bytes 2, 3; the
-      // byte below the kept ones is left as it falls (below the cut of the store)
-      const float g = __uint_as_float(__byte_perm(lo, hi, (c & 1) ? 0x5424 : 0x5404));
-      const float u = __uint_as_float(__byte_perm(lo, hi, (c & 1) ? 0x7634 : 0x7614));
+      // lo holds (g, u) of the even column in bytes 0, 1 and of the odd one in bytes 2, 3; the byte
+      // below the kept ones repeats the lowest of them, which leaves an infinity what it is
+      const float g = __uint_as_float(__byte_perm(lo, hi, (c & 1) ? 0x5422 : 0x5400));
+      const float u = __uint_as_float(__byte_perm(lo, hi, (c & 1) ? 0x7633 : 0x7611));
       float a, da;
       ffn_act_grad<ACT>(g, &a, &da);
       dg[e] = dh[c] * u * da;

@@ -168,6 +168,28 @@ def test_ffn_large_values_and_non_finite_rows(T, act):
     assert torch.isnan(dx[1]).all()
 
 
+@pytest.mark.parametrize("T", [3, 40])
+def test_ffn_keeps_an_infinite_projection(T):
+    """u = inf in one place: the gradient of that feature's gate is infinite
+    of a definite sign, not a NaN, and the other features' gradients stay finite."""
+    x, (w_gate, w_up, w_down), dy = _ffn_inputs(T, 16, 64, BF16, seed=11)
+    x[:, 0] = 0.0
+    x[1, 0] = 3e38
+    w_gate[:, 0] = 0.0
+    w_up[:, 0] = 0.0
+    w_up[9, 0] = 3e38
+    y, saved = prm.gated_ffn(x, w_gate, w_up, w_down, save=True)
+    assert torch.isinf(y[1]).all() and torch.isfinite(y[[0] + list(range(2, T))]).all()
+    _, dw_gate, _, _ = prm.gated_ffn_backward(dy, x, w_gate, w_up, w_down, saved)
+    g = x.double() @ w_gate.double().t()
+    s = torch.sigmoid(g[1, 9])
+    dg = (dy[1].double() @ w_down[:, 9].double()) * (s + g[1, 9] * s * (1 - s))
+    assert torch.isinf(dw_gate[9]).all()
+    assert torch.equal(torch.sign(dw_gate[9].double()), torch.sign(dg * x[1].double()))
+    rest = [j for j in range(64) if j != 9]
+    assert torch.isfinite(dw_gate[rest, 1:]).all()
+
+
 def test_ffn_without_tokens():
     x, ws, dy = _ffn_inputs(0, 64, 128, BF16)
     y, saved = prm.gated_ffn(x, *ws, save=True)
