@@ -12,6 +12,10 @@
 // behind those of the others. The backward pass's ring of shared-memory
 // stages with two CTAs per SM was slower here (8191 x 5120 bf16 with both
 // gains 127 us, this form 70; 16384 x 4096 fp32 220 us, 126).
+//
+// 32 x 1024 x 2048, layer norm with modulation, fp32 stream and bf16 block:
+// 134 us, 6.0 TB/s (89 % of the copy rate); 12 x 256 fp32: 2.6 us on the device,
+// where the call's host time of 18 counts.
 #include <cmath>
 
 #include "block_norm.cuh"

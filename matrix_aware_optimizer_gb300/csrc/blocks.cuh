@@ -108,7 +108,6 @@ struct Raw8 {
     a = make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
   }
   __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<uint4*>(p) = a; }
-  __device__ __forceinline__ void store_cs(T* p) const { __stcs(reinterpret_cast<uint4*>(p), a); }
 };
 template <>
 struct Raw8<float> {
@@ -133,10 +132,6 @@ struct Raw8<float> {
   __device__ __forceinline__ void store(float* p) const {
     reinterpret_cast<float4*>(p)[0] = a;
     reinterpret_cast<float4*>(p)[1] = b;
-  }
-  __device__ __forceinline__ void store_cs(float* p) const {
-    __stcs(reinterpret_cast<float4*>(p), a);
-    __stcs(reinterpret_cast<float4*>(p) + 1, b);
   }
 };
 

@@ -23,6 +23,15 @@
 // 512 x 2048) the gradients were 0.0023 from the exact ones, as with g and u
 // kept exactly, and with bf16 g and u 0.0029 - 0.0035.
 //
+// Bound by the tensor cores for more than a few hundred tokens. 8192 tokens,
+// 2048 x 8192, bf16, each launch alone: GLU 322 us (1.71 PFLOP/s, with 400 MB of
+// g and u written), down 190 (1.45), DGLU 207 (1.33, 790 MB moved), gradients
+// 835 (1.65). Both passes 1.60 - 1.71 ms (1.54 - 1.45 PFLOP/s; the SM clock
+// under the power cap decides), those of 4096 tokens, 5120 x 20480 5.0 ms
+// (1.55). On the busiest SMs the tensor pipe is active 84 - 87 % of the time
+// (DGLU, where the epilogue's loads of g and u bound it, 74 %); the rest is
+// partly filled last rounds and the 8 SMs that clusters of four leave idle.
+//
 // CTA layout, pipeline and TMEM use are those of the Newton-Schulz GEMMs
 // (ns5_gemm.cu): 320 threads, warp 0 TMA producer, warp 1 MMA issue in the
 // even CTA, warps 2-9 epilogue; 256 x 256 tiles, six 32 KB stages, two

@@ -10,6 +10,10 @@
 // elements come from L1 / L2; a weight vector is unpacked once for all of
 // them. The down projection's CTAs start while the first kernel drains and
 // load their first weights before they wait for h.
+//
+// One token at d 2048, f 8192 bf16, weights not in L2: 20.5 us, 4.9 TB/s (72 %
+// of the copy rate); 17.2 back to back, where L2 keeps a part of the 101 MB.
+// What is left is the start and the end of two short launches.
 #include <algorithm>
 
 #include "ffn.cuh"
