@@ -26,9 +26,9 @@
 // Bound by the tensor cores for more than a few hundred tokens. 8192 tokens,
 // 2048 x 8192, bf16, each launch alone: GLU 322 us (1.71 PFLOP/s, with 400 MB of
 // g and u written), down 190 (1.45), DGLU 207 (1.33, 790 MB moved), gradients
-// 835 (1.65). Both passes 1.60 - 1.71 ms (1.54 - 1.45 PFLOP/s; the SM clock
-// under the power cap decides), those of 4096 tokens, 5120 x 20480 5.0 ms
-// (1.55). On the busiest SMs the tensor pipe is active 84 - 87 % of the time
+// 835 (1.65). Both passes 1.60 - 1.73 ms (1.54 - 1.43 PFLOP/s: the SM clock
+// under the power cap decides), those of 4096 tokens, 5120 x 20480 4.9 - 5.1 ms
+// (1.57 - 1.52). On the busiest SMs the tensor pipe is active 84 - 87 % of the time
 // (DGLU, where the epilogue's loads of g and u bound it, 74 %); the rest is
 // partly filled last rounds and the 8 SMs that clusters of four leave idle.
 //
@@ -125,8 +125,8 @@ __device__ __forceinline__ int ffn_seg(const FfnParams& p, int64_t item) {
 // and its items leave a last round part empty, the clusters without one take
 // that many short items more (the hole, up to hole_end), so that all come to
 // the end together (18 tile times instead of 19 at 8192 x 2048 x 8192, 112
-// instead of 117 at 4096 x 5120 x 20480: both passes 1708 us instead of 1748,
-// and 4995 instead of 5092).
+// instead of 117 at 4096 x 5120 x 20480; both passes, on one machine, 1679 us
+// instead of 1710, and 4917 instead of 5034).
 template <int EPI>
 __device__ __forceinline__ int64_t next_item(const FfnParams& p, int64_t item, int64_t c, int64_t n) {
   if (EPI != EPI_STORE || item >= p.hole_end) return item + n;
