@@ -26,7 +26,8 @@
 // Measured (device time, share of the copy bandwidth on the bytes above):
 // 32 x 1024 x 2048 modulated, fp32 stream and bf16 block, 190 us (94 %);
 // 8191 x 5120 bf16 with both gains 110 us (67 %); 65536 x 512 bf16 87 us (69
-// %); 30000 x 1001 bf16 240 us (22 %). What is left is the chain of each
+// %); 30000 x 1001 bf16 153 us (35 %; 239 from a kernel compiled for every sum,
+// as the strided ones of longer rows are). What is left is the chain of each
 // row -- load, reduce, reduce, store -- behind which only the rows of the
 // other CTA of the SM, or the thread's second row, can hide: registers (40
 // column sums and their operands per thread) allow no more of them. Fewer
@@ -665,18 +666,21 @@ cudaError_t launch_shape(NormGradParams& p, const NormShape& s, const NormGradAr
   const bool mod = p.has[SUM_GATE] || p.has[SUM_SCALE] || p.has[SUM_SHIFT];
   const bool w = p.has[SUM_POST] || p.has[SUM_PRE];
   using std::integral_constant;
-  auto go = [&](auto size, auto rows) {
-    constexpr int S = decltype(size)::value, R = decltype(rows)::value, V = norm_vectors(S);
-    if (mod && w) return launch_backward<RT, BT, S, R, V, VEC, true, true>(p, s, a, stream);
-    if (mod) return launch_backward<RT, BT, S, R, V, VEC, true, false>(p, s, a, stream);
-    if (w) return launch_backward<RT, BT, S, R, V, VEC, false, true>(p, s, a, stream);
-    return launch_backward<RT, BT, S, R, V, VEC, false, false>(p, s, a, stream);
+  auto sums = [&](auto size, auto rows, auto access) {
+    constexpr int S = decltype(size)::value, R = decltype(rows)::value, V = norm_vectors(S), A = decltype(access)::value;
+    if (mod && w) return launch_backward<RT, BT, S, R, V, A, true, true>(p, s, a, stream);
+    if (mod) return launch_backward<RT, BT, S, R, V, A, true, false>(p, s, a, stream);
+    if (w) return launch_backward<RT, BT, S, R, V, A, false, true>(p, s, a, stream);
+    return launch_backward<RT, BT, S, R, V, A, false, false>(p, s, a, stream);
   };
+  auto go = [&](auto size, auto rows) { return sums(size, rows, integral_constant<int, VEC>{}); };
   auto strided = [&](auto size) {
     constexpr int S = decltype(size)::value, V = norm_vectors(S);
     return s.access == ELEM ? launch_backward<RT, BT, S, 1, V, ELEM, true, true>(p, s, a, stream)
                             : launch_backward<RT, BT, S, 1, V, DIRECT, true, true>(p, s, a, stream);
   };
+  if (s.access == ELEM && s.size == 0)
+    return sums(integral_constant<int, 0>{}, integral_constant<int, 1>{}, integral_constant<int, ELEM>{});
   if (s.access != VEC)
     return s.size == 0   ? strided(integral_constant<int, 0>{})
            : s.size == 1 ? strided(integral_constant<int, 1>{})
