@@ -62,10 +62,9 @@ extern "C" int prm_block_norm_backward(const prm_block_norm_desc* desc, const vo
   for (int i = 0; i < 6; ++i) ring = ring && aligned_to(rows[i], 16);
   const bool mod = desc->gate != nullptr || desc->scale != nullptr || desc->shift != nullptr;
   const bool w = desc->post_weight != nullptr || desc->pre_weight != nullptr;
-  const bool all = !vec && desc->d > 2048;  // the strided kernels of long rows are compiled for every sum
   const NormShape s =
       grad_shape(desc->d, row_bytes(*desc, dy != nullptr, dr != nullptr, z != nullptr, stats != nullptr),
-                 (dy != nullptr ? 2 : 0) + (dr != nullptr) + (z != nullptr), vec, ring, w || all, mod || all);
+                 (dy != nullptr ? 2 : 0) + (dr != nullptr) + (z != nullptr), vec, ring, w, mod);
   const void* present[SUM_COUNT] = {desc->gate, desc->scale, desc->shift, desc->post_weight, desc->pre_weight};
   for (int k = 0; k < SUM_COUNT; ++k) p.has[k] = present[k] != nullptr;
   if (p.n.rows / NORM_CTAS > (int64_t(1) << 30)) return PRM_ERR_UNSUPPORTED;

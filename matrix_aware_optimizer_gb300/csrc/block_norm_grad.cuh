@@ -26,8 +26,8 @@
 // Measured (device time, share of the copy bandwidth on the bytes above):
 // 32 x 1024 x 2048 modulated, fp32 stream and bf16 block, 190 us (94 %);
 // 8191 x 5120 bf16 with both gains 110 us (67 %); 65536 x 512 bf16 87 us (69
-// %); 30000 x 1001 bf16 153 us (35 %; 239 from a kernel compiled for every sum,
-// as the strided ones of longer rows are). What is left is the chain of each
+// %); 30000 x 1001 bf16 153 us (35 %; 239 from a kernel compiled for every
+// sum), 8000 x 4999 197 us (365). What is left is the chain of each
 // row -- load, reduce, reduce, store -- behind which only the rows of the
 // other CTA of the SM, or the thread's second row, can hide: registers (40
 // column sums and their operands per thread) allow no more of them. Fewer
@@ -673,25 +673,23 @@ cudaError_t launch_shape(NormGradParams& p, const NormShape& s, const NormGradAr
     if (w) return launch_backward<RT, BT, S, R, V, A, false, true>(p, s, a, stream);
     return launch_backward<RT, BT, S, R, V, A, false, false>(p, s, a, stream);
   };
-  auto go = [&](auto size, auto rows) { return sums(size, rows, integral_constant<int, VEC>{}); };
-  auto strided = [&](auto size) {
-    constexpr int S = decltype(size)::value, V = norm_vectors(S);
-    return s.access == ELEM ? launch_backward<RT, BT, S, 1, V, ELEM, true, true>(p, s, a, stream)
-                            : launch_backward<RT, BT, S, 1, V, DIRECT, true, true>(p, s, a, stream);
-  };
-  if (s.access == ELEM && s.size == 0)
-    return sums(integral_constant<int, 0>{}, integral_constant<int, 1>{}, integral_constant<int, ELEM>{});
-  if (s.access != VEC)
-    return s.size == 0   ? strided(integral_constant<int, 0>{})
-           : s.size == 1 ? strided(integral_constant<int, 1>{})
-                         : strided(integral_constant<int, 2>{});
-  if (s.size == 0)
-    return s.rows == 2 ? go(integral_constant<int, 0>{}, integral_constant<int, 2>{})
-                       : go(integral_constant<int, 0>{}, integral_constant<int, 1>{});
-  if (s.size == 1)
-    return s.rows == 2 ? go(integral_constant<int, 1>{}, integral_constant<int, 2>{})
-                       : go(integral_constant<int, 1>{}, integral_constant<int, 1>{});
-  return go(integral_constant<int, 2>{}, integral_constant<int, 1>{});
+  const integral_constant<int, 0> small;
+  const integral_constant<int, 1> one;  // (also the size of the rows in between)
+  const integral_constant<int, 2> two;
+  if (s.access == VEC) {
+    const integral_constant<int, VEC> vec;
+    if (s.size == 2) return sums(two, one, vec);
+    if (s.size == 1) return s.rows == 2 ? sums(one, two, vec) : sums(one, one, vec);
+    return s.rows == 2 ? sums(small, two, vec) : sums(small, one, vec);
+  }
+  if (s.access == ELEM) {
+    const integral_constant<int, ELEM> elem;
+    return s.size == 0 ? sums(small, one, elem) : s.size == 1 ? sums(one, one, elem) : sums(two, one, elem);
+  }
+  // DIRECT: compiled for every sum
+  if (s.size == 0) return launch_backward<RT, BT, 0, 1, norm_vectors(0), DIRECT, true, true>(p, s, a, stream);
+  if (s.size == 1) return launch_backward<RT, BT, 1, 1, norm_vectors(1), DIRECT, true, true>(p, s, a, stream);
+  return launch_backward<RT, BT, 2, 1, norm_vectors(2), DIRECT, true, true>(p, s, a, stream);
 }
 
 // Defined per pair of types, each pair's kernels in a translation unit of a

@@ -369,6 +369,14 @@ def test_norm_long_rows_by_option(d, st, bt):
         _check_norm(*_norm_case(2, 9, d, "layer", st, bt, *opts))
 
 
+@pytest.mark.parametrize("st,bt", [(FP32, FP32), (FP32, FP16), (BF16, BF16)])
+@pytest.mark.parametrize("d", [17, 253, 1001, 2047, 2049, 3001, 5119, 5121, 7003, 8191])
+def test_norm_odd_rows_by_option(d, st, bt):
+    """Widths that are no multiple of 8, with every set of column sums."""
+    for opts in ((1, 0, 1, 0), (0, 1, 0, 1), (0, 0, 0, 0), (1, 1, 1, 1)):
+        _check_norm(*_norm_case(2, 9, d, "layer", st, bt, *opts))
+
+
 @pytest.mark.parametrize("B,L", [(1, 1), (1, 2), (5, 1), (1300, 1), (1300, 3), (1, 5000), (7, 700), (40, 31)])
 @pytest.mark.parametrize("mod", [0, 1])
 def test_norm_row_counts(B, L, mod):
