@@ -30,7 +30,7 @@ int norm_check(const prm_block_norm_desc* c, NormParams* p) {
   if (!std::isfinite(c->alpha) || !std::isfinite(c->eps) || !(c->eps >= 0.f)) return PRM_ERR_INVALID_ARG;
   if (c->rows < 0 || c->d < 1 || c->rows_per_sample < 1 || c->rows % c->rows_per_sample != 0) return PRM_ERR_SHAPE;
   if (c->d > NORM_MAX_D) return PRM_ERR_UNSUPPORTED;
-  if (c->rows / c->rows_per_sample > 0x7fffffff || c->rows > (int64_t(1) << 40)) return PRM_ERR_UNSUPPORTED;
+  if (c->rows / c->rows_per_sample > 0x7fffffff || c->rows > 0xffffffffll) return PRM_ERR_UNSUPPORTED;
   if ((c->gate != nullptr && c->gate_ld < c->d) || (c->scale != nullptr && c->scale_ld < c->d) ||
       (c->shift != nullptr && c->shift_ld < c->d))
     return PRM_ERR_SHAPE;

@@ -56,7 +56,7 @@ struct NormGradParams {
 };
 
 __device__ __forceinline__ int64_t range_begin(const NormGradParams& p, int64_t cta) {
-  return p.n.rows * cta / p.ctas;  // rows < 2^40, ctas <= 304
+  return p.n.rows * cta / p.ctas;  // rows < 2^32, ctas <= 304
 }
 
 template <typename RT, typename BT>

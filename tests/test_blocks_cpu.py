@@ -166,6 +166,7 @@ def test_norm_refusals(lib):
     assert fwd(rows_per_sample=3) == N.PRM_ERR_SHAPE
     assert fwd(d=0) == N.PRM_ERR_SHAPE
     assert fwd(d=8193) == N.PRM_ERR_UNSUPPORTED
+    assert fwd(rows=1 << 32, rows_per_sample=1 << 31) == N.PRM_ERR_UNSUPPORTED
     assert fwd(gate=16, gate_ld=63) == N.PRM_ERR_SHAPE
     assert fwd(x=None) == N.PRM_ERR_INVALID_ARG
     assert fwd(r=None) == N.PRM_ERR_INVALID_ARG
