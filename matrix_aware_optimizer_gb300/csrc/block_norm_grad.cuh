@@ -6,6 +6,8 @@
 //   dz  = s_z (dq - q mean(dq q) [- mean(dq)])              (dP without post)
 //   dshift_b = sum dy, dscale_b = sum dy n pre, dgate_b = sum D P,
 //   dpre = sum dy (1 + scale_b) n, dpost = sum dP q         (over rows)
+// (within a sample dscale_b = pre sum dy n and its part of dpre is (1 +
+// scale_b) sum dy n; so with D q, gate_b and post)
 // the bracketed terms for the layer norm only. Bound by memory: dy, dr, r and
 // z are read once, dx and dz written once.
 //
@@ -108,7 +110,9 @@ __global__ void __launch_bounds__(norm_threads(SIZE), SIZE == 0 ? 2 : 1)
   float* const col_gate = col_scale + (MOD ? pitch : 0);
   uint64_t* const exchange = reinterpret_cast<uint64_t*>(columns + ((W ? 2 : 0) + (MOD ? 2 : 0)) * pitch);
   // With both kinds of sums, or with long rows, a thread's gain sums lie in
-  // shared memory, where only it touches them: registers are short.
+  // shared memory, where only it touches them: registers are short. With both,
+  // a row adds to three sums (dy n, D q and dy) and the gains' and the
+  // modulation's are formed from them at a sample's end.
   constexpr bool FAR = grad_far(SIZE, MOD, W);
   uint64_t* const far_w = exchange + (groups > 1 ? 4 * NV * threads : 0) + threadIdx.x;
   if constexpr (RING) {
@@ -360,17 +364,18 @@ __global__ void __launch_bounds__(norm_threads(SIZE), SIZE == 0 ? 2 : 1)
 #pragma unroll
                   for (int k = 0; k < 4; ++k) acc_mod[SUM_SHIFT][v].p[k] = f2_add(acc_mod[SUM_SHIFT][v].p[k], x.p[k]);
                 }
+                if (scale || pre) {
+#pragma unroll
+                  for (int k = 0; k < 4; ++k)
+                    acc_mod[SUM_SCALE][v].p[k] = f2_fma(x.p[k], n.p[k], acc_mod[SUM_SCALE][v].p[k]);
+                }
                 if (scale) {
 #pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    const uint64_t m = pre ? f2_mul(n.p[k], w.p[k]) : n.p[k];
-                    acc_mod[SUM_SCALE][v].p[k] = f2_fma(x.p[k], m, acc_mod[SUM_SCALE][v].p[k]);
-                    x.p[k] = f2_mul(x.p[k], sc.p[k]);
-                  }
+                  for (int k = 0; k < 4; ++k) x.p[k] = f2_mul(x.p[k], sc.p[k]);
                 }
               }
               if (pre) {
-                add_w(1, v, x, n);
+                if constexpr (!MOD) add_w(1, v, x, n);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) x.p[k] = f2_mul(x.p[k], w.p[k]);
               }
@@ -441,17 +446,14 @@ __global__ void __launch_bounds__(norm_threads(SIZE), SIZE == 0 ? 2 : 1)
                 if (!live[i][v]) continue;
                 const F8 x = normed_z(i, v);
                 if constexpr (MOD) {
-                  if (gate) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                      const uint64_t P = post ? f2_mul(x.p[k], w.p[k]) : x.p[k];
-                      acc_mod[SUM_GATE][v].p[k] = f2_fma(D[i][v].p[k], P, acc_mod[SUM_GATE][v].p[k]);
-                      D[i][v].p[k] = f2_mul(D[i][v].p[k], g.p[k]);
-                    }
+                  for (int k = 0; k < 4; ++k) {
+                    acc_mod[SUM_GATE][v].p[k] = f2_fma(D[i][v].p[k], x.p[k], acc_mod[SUM_GATE][v].p[k]);
+                    if (gate) D[i][v].p[k] = f2_mul(D[i][v].p[k], g.p[k]);
                   }
                 }
                 if (post) {
-                  add_w(0, v, D[i][v], x);
+                  if constexpr (!MOD) add_w(0, v, D[i][v], x);
 #pragma unroll
                   for (int k = 0; k < 4; ++k) {
                     D[i][v].p[k] = f2_mul(D[i][v].p[k], w.p[k]);
@@ -504,9 +506,29 @@ __global__ void __launch_bounds__(norm_threads(SIZE), SIZE == 0 ? 2 : 1)
     if constexpr (MOD) {
       // the end of the sample, or of this CTA's part of it
       const bool before = sample * p.sample_rows < row0, after = (sample + 1) * p.sample_rows > row1;
+      if constexpr (W) {
+        // what the sample's sums are of the gains' gradients, and then of its own
+        const F8 one = {{f2_pack(1.f, 1.f), f2_pack(1.f, 1.f), f2_pack(1.f, 1.f), f2_pack(1.f, 1.f)}};
+        auto share = [&](int which, int v, F8& sum, bool mod, const float* mods, const float* gains) {
+          add_w(which, v, sum, mod ? read8<ACCESS>(mods + col[v], left[v], tpr) : one);
+          const F8 w = read8<ACCESS>(gains + col[v], left[v], tpr);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) sum.p[k] = f2_mul(sum.p[k], w.p[k]);
+        };
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          if (left[v] <= 0) continue;
+          if (post) share(0, v, acc_mod[SUM_GATE][v], gate, col_gate, col_post);
+          if (pre) share(1, v, acc_mod[SUM_SCALE][v], scale, col_scale, col_pre);
+        }
+      }
 #pragma unroll
       for (int k = 0; k < 3; ++k) {
-        if (!p.has[k]) continue;
+        if (!p.has[k]) {
+#pragma unroll
+          for (int v = 0; v < NV; ++v) acc_mod[k][v] = f8_zero();
+          continue;
+        }
         across_groups(acc_mod[k]);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
