@@ -93,8 +93,9 @@ __global__ void __launch_bounds__(norm_threads(SIZE), SIZE == 0 ? 2 : 1)
   const int64_t cta = blockIdx.x;
   // stage: rows of dy, dr, r, z and stats one after another (absent arrays
   // take no room, ELEM regions 16 bytes more on either side of 16-byte
-  // rounding); after the ring post, pre, 1 + scale and gate of the sample at
-  // work in fp32, then the groups' exchange area
+  // rounding); after the ring what y's and z's columns are multiplied by for
+  // the sample at work, pre (1 + scale) and post gate in fp32, then the groups'
+  // exchange area
   const uint32_t slack = ACCESS == ELEM ? 32 : 0;
   auto region = [&](bool there, size_t size) -> uint32_t {
     return there ? ((static_cast<uint32_t>(step_rows * d * size) + slack) & ~15u) : 0u;
@@ -104,11 +105,9 @@ __global__ void __launch_bounds__(norm_threads(SIZE), SIZE == 0 ? 2 : 1)
   const uint32_t stage_bytes = by + bdr + br + bz + (io.stats ? static_cast<uint32_t>(step_rows) * 16 : 0);
   float* const columns = reinterpret_cast<float*>(smem + p.stages * stage_bytes);
   const int pitch = (d + 3) & ~3;
-  float* const col_post = columns;
-  float* const col_pre = columns + (W ? pitch : 0);
-  float* const col_scale = columns + (W ? 2 * pitch : 0);
-  float* const col_gate = col_scale + (MOD ? pitch : 0);
-  uint64_t* const exchange = reinterpret_cast<uint64_t*>(columns + ((W ? 2 : 0) + (MOD ? 2 : 0)) * pitch);
+  float* const col_y = columns;
+  float* const col_z = columns + pitch;
+  uint64_t* const exchange = reinterpret_cast<uint64_t*>(columns + (W || MOD ? 2 : 0) * pitch);
   // With both kinds of sums, or with long rows, a thread's gain sums lie in
   // shared memory, where only it touches them: registers are short. With both,
   // a row adds to three sums (dy n, D q and dy) and the gains' and the
@@ -204,12 +203,15 @@ __global__ void __launch_bounds__(norm_threads(SIZE), SIZE == 0 ? 2 : 1)
   const bool scale = MOD && p.has[SUM_SCALE];
   const bool shift = MOD && p.has[SUM_SHIFT];
   const bool gate = MOD && p.has[SUM_GATE];
-  if constexpr (W) {
+  auto fill_columns = [&](int64_t sample) {
+    const BT* const sc = static_cast<const BT*>(p.n.scale) + sample * p.n.scale_ld;
+    const BT* const g = static_cast<const BT*>(p.n.gate) + sample * p.n.gate_ld;
     for (int i = threadIdx.x; i < d; i += threads) {
-      if (post) col_post[i] = __ldg(p.n.post + i);
-      if (pre) col_pre[i] = __ldg(p.n.pre + i);
+      if (pre || scale) col_y[i] = (pre ? __ldg(p.n.pre + i) : 1.f) * (scale ? 1.f + to_f32(sc[i]) : 1.f);
+      if (post || gate) col_z[i] = (post ? __ldg(p.n.post + i) : 1.f) * (gate ? to_f32(g[i]) : 1.f);
     }
-  }
+  };
+  if constexpr (W && !MOD) fill_columns(0);
 
   const int tid = tpr <= 32 ? threadIdx.x & (tpr - 1) : threadIdx.x % tpr;
   const int group = threadIdx.x / tpr;
@@ -275,10 +277,7 @@ __global__ void __launch_bounds__(norm_threads(SIZE), SIZE == 0 ? 2 : 1)
     const int64_t seg1 = min(row1, (sample + 1) * p.sample_rows);
     if constexpr (MOD) {
       __syncthreads();  // the sample before is done with its columns
-      for (int i = threadIdx.x; i < d; i += threads) {
-        if (scale) col_scale[i] = 1.f + to_f32(static_cast<const BT*>(p.n.scale)[sample * p.n.scale_ld + i]);
-        if (gate) col_gate[i] = to_f32(static_cast<const BT*>(p.n.gate)[sample * p.n.gate_ld + i]);
-      }
+      fill_columns(sample);
     }
     if constexpr (MOD || W) __syncthreads();
     const int count = static_cast<int>(seg1 - seg0);  // below 2^31: checked by the host
@@ -351,9 +350,8 @@ __global__ void __launch_bounds__(norm_threads(SIZE), SIZE == 0 ? 2 : 1)
           for (int i = 0; i < R; ++i) part[i][0] = part[i][1] = 0;
 #pragma unroll
           for (int v = 0; v < NV; ++v) {
-            F8 w, sc;
-            if (pre && left[v] > 0) w = read8<ACCESS>(col_pre + col[v], left[v], tpr);
-            if (scale && left[v] > 0) sc = read8<ACCESS>(col_scale + col[v], left[v], tpr);
+            F8 w;
+            if ((pre || scale) && left[v] > 0) w = read8<ACCESS>(col_y + col[v], left[v], tpr);
 #pragma unroll
             for (int i = 0; i < R; ++i) {
               if (!live[i][v]) continue;
@@ -369,12 +367,8 @@ __global__ void __launch_bounds__(norm_threads(SIZE), SIZE == 0 ? 2 : 1)
                   for (int k = 0; k < 4; ++k)
                     acc_mod[SUM_SCALE][v].p[k] = f2_fma(x.p[k], n.p[k], acc_mod[SUM_SCALE][v].p[k]);
                 }
-                if (scale) {
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) x.p[k] = f2_mul(x.p[k], sc.p[k]);
-                }
               }
-              if (pre) {
+              if (pre || scale) {
                 if constexpr (!MOD) add_w(1, v, x, n);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) x.p[k] = f2_mul(x.p[k], w.p[k]);
@@ -438,28 +432,24 @@ __global__ void __launch_bounds__(norm_threads(SIZE), SIZE == 0 ? 2 : 1)
             for (int i = 0; i < R; ++i) part[i][0] = part[i][1] = 0;
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-              F8 w, g;
-              if (post && left[v] > 0) w = read8<ACCESS>(col_post + col[v], left[v], tpr);
-              if (gate && left[v] > 0) g = read8<ACCESS>(col_gate + col[v], left[v], tpr);
+              F8 w;
+              if (left[v] > 0) w = read8<ACCESS>(col_z + col[v], left[v], tpr);
 #pragma unroll
               for (int i = 0; i < R; ++i) {
                 if (!live[i][v]) continue;
                 const F8 x = normed_z(i, v);
                 if constexpr (MOD) {
 #pragma unroll
-                  for (int k = 0; k < 4; ++k) {
+                  for (int k = 0; k < 4; ++k)
                     acc_mod[SUM_GATE][v].p[k] = f2_fma(D[i][v].p[k], x.p[k], acc_mod[SUM_GATE][v].p[k]);
-                    if (gate) D[i][v].p[k] = f2_mul(D[i][v].p[k], g.p[k]);
-                  }
+                } else {
+                  add_w(0, v, D[i][v], x);
                 }
-                if (post) {
-                  if constexpr (!MOD) add_w(0, v, D[i][v], x);
 #pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    D[i][v].p[k] = f2_mul(D[i][v].p[k], w.p[k]);
-                    part[i][0] = f2_fma(D[i][v].p[k], x.p[k], part[i][0]);
-                    part[i][1] = f2_add(part[i][1], D[i][v].p[k]);
-                  }
+                for (int k = 0; k < 4; ++k) {
+                  D[i][v].p[k] = f2_mul(D[i][v].p[k], w.p[k]);
+                  part[i][0] = f2_fma(D[i][v].p[k], x.p[k], part[i][0]);
+                  part[i][1] = f2_add(part[i][1], D[i][v].p[k]);
                 }
                 if constexpr (!AGAIN) q[i][v] = x;
               }
@@ -508,9 +498,15 @@ __global__ void __launch_bounds__(norm_threads(SIZE), SIZE == 0 ? 2 : 1)
       const bool before = sample * p.sample_rows < row0, after = (sample + 1) * p.sample_rows > row1;
       if constexpr (W) {
         // what the sample's sums are of the gains' gradients, and then of its own
-        const F8 one = {{f2_pack(1.f, 1.f), f2_pack(1.f, 1.f), f2_pack(1.f, 1.f), f2_pack(1.f, 1.f)}};
-        auto share = [&](int which, int v, F8& sum, bool mod, const float* mods, const float* gains) {
-          add_w(which, v, sum, mod ? read8<ACCESS>(mods + col[v], left[v], tpr) : one);
+        auto share = [&](int which, int v, F8& sum, const void* mods, int64_t ld, float plus, const float* gains) {
+          const uint64_t add = f2_pack(plus, plus);
+          F8 m = {{f2_pack(1.f, 1.f), f2_pack(1.f, 1.f), f2_pack(1.f, 1.f), f2_pack(1.f, 1.f)}};
+          if (mods != nullptr) {
+            m = read8<ACCESS>(static_cast<const BT*>(mods) + sample * ld + col[v], left[v], tpr);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) m.p[k] = f2_add(m.p[k], add);
+          }
+          add_w(which, v, sum, m);
           const F8 w = read8<ACCESS>(gains + col[v], left[v], tpr);
 #pragma unroll
           for (int k = 0; k < 4; ++k) sum.p[k] = f2_mul(sum.p[k], w.p[k]);
@@ -518,8 +514,8 @@ __global__ void __launch_bounds__(norm_threads(SIZE), SIZE == 0 ? 2 : 1)
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
           if (left[v] <= 0) continue;
-          if (post) share(0, v, acc_mod[SUM_GATE][v], gate, col_gate, col_post);
-          if (pre) share(1, v, acc_mod[SUM_SCALE][v], scale, col_scale, col_pre);
+          if (post) share(0, v, acc_mod[SUM_GATE][v], p.n.gate, p.n.gate_ld, 0.f, p.n.post);
+          if (pre) share(1, v, acc_mod[SUM_SCALE][v], p.n.scale, p.n.scale_ld, 1.f, p.n.pre);
         }
       }
 #pragma unroll
@@ -651,7 +647,7 @@ inline NormShape grad_shape(int64_t d, size_t row_bytes, int arrays, bool vec, b
   return norm_shape(d, row_bytes, arrays, vec, ring, [&](int size, int threads, int groups, bool direct) {
     const bool ww = w || direct, mm = mod || direct;  // the direct kernel is compiled for every sum
     const int nv = norm_vectors(size);
-    return ((ww ? 2 : 0) + (mm ? 2 : 0)) * ((d + 3) & ~int64_t(3)) * sizeof(float) +
+    return (ww || mm ? 2 : 0) * ((d + 3) & ~int64_t(3)) * sizeof(float) +
            (groups > 1 ? static_cast<size_t>(threads) * 8 * nv * sizeof(float) : 0) +
            (grad_far(size, mm, ww) ? static_cast<size_t>(threads) * 16 * nv * sizeof(float) : 0);
   });
