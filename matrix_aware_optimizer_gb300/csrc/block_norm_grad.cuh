@@ -73,7 +73,7 @@ struct NormGradIo {
   BT* mod[3];   // dgate, dscale, dshift
 };
 
-__host__ __device__ constexpr bool grad_far(int size, bool mod, bool w) { return w && (mod || size == 2); }
+__host__ __device__ constexpr bool grad_far(int size, bool mod, bool w) { return w && !mod && size == 2; }
 
 // R: rows that a thread works on at once, to have more than one chain of
 // dependent steps and to share what a step costs besides the arithmetic.
@@ -108,10 +108,10 @@ __global__ void __launch_bounds__(norm_threads(SIZE), SIZE == 0 ? 2 : 1)
   float* const col_y = columns;
   float* const col_z = columns + pitch;
   uint64_t* const exchange = reinterpret_cast<uint64_t*>(columns + (W || MOD ? 2 : 0) * pitch);
-  // With both kinds of sums, or with long rows, a thread's gain sums lie in
-  // shared memory, where only it touches them: registers are short. With both,
-  // a row adds to three sums (dy n, D q and dy) and the gains' and the
-  // modulation's are formed from them at a sample's end.
+  // With long rows a thread's gain sums lie in shared memory, where only it
+  // touches them: registers are short. With both kinds of sums a row adds to
+  // three (dy n, D q and dy); the gains' and the modulation's are formed from
+  // them at a sample's end, the gains' in the CTA's row of partial sums.
   constexpr bool FAR = grad_far(SIZE, MOD, W);
   uint64_t* const far_w = exchange + (groups > 1 ? 4 * NV * threads : 0) + threadIdx.x;
   if constexpr (RING) {
@@ -224,17 +224,28 @@ __global__ void __launch_bounds__(norm_threads(SIZE), SIZE == 0 ? 2 : 1)
   }
   int turn = 0;
   auto reduce = [&](float (&a)[R][2]) { row_sums<SIZE, R>(a, tpr, group, scratch, turn); };
-  F8 acc_mod[MOD ? 3 : 1][NV], acc_w[W && !FAR ? 2 : 1][NV];
+  F8 acc_mod[MOD ? 3 : 1][NV], acc_w[W && !MOD && !FAR ? 2 : 1][NV];
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
 #pragma unroll
     for (int k = 0; k < (MOD ? 3 : 1); ++k) acc_mod[k][v] = f8_zero();
 #pragma unroll
-    for (int k = 0; k < (W && !FAR ? 2 : 1); ++k) acc_w[k][v] = f8_zero();
+    for (int k = 0; k < (W && !MOD && !FAR ? 2 : 1); ++k) acc_w[k][v] = f8_zero();
   }
   if constexpr (FAR) {
 #pragma unroll
     for (int k = 0; k < 8 * NV; ++k) far_w[k * threads] = 0;
+  }
+  auto gain_sums = [&](int which, int v) {
+    return p.partial_w + (cta * 2 + which) * static_cast<int64_t>(pitch) + col[v];
+  };
+  if constexpr (W && MOD) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      if (group != 0 || left[v] <= 0) continue;
+      if (post) write8<ACCESS>(gain_sums(0, v), left[v], tpr, f8_zero());
+      if (pre) write8<ACCESS>(gain_sums(1, v), left[v], tpr, f8_zero());
+    }
   }
   // acc_w[which][v] += a b (0: post, 1: pre)
   auto add_w = [&](int which, int v, const F8& a, const F8& b) {
@@ -243,7 +254,7 @@ __global__ void __launch_bounds__(norm_threads(SIZE), SIZE == 0 ? 2 : 1)
       if constexpr (FAR) {
         uint64_t& x = far_w[((which * NV + v) * 4 + k) * threads];
         x = f2_fma(a.p[k], b.p[k], x);
-      } else if constexpr (W) {
+      } else if constexpr (W && !MOD) {
         acc_w[which][v].p[k] = f2_fma(a.p[k], b.p[k], acc_w[which][v].p[k]);
       }
     }
@@ -496,39 +507,37 @@ __global__ void __launch_bounds__(norm_threads(SIZE), SIZE == 0 ? 2 : 1)
     if constexpr (MOD) {
       // the end of the sample, or of this CTA's part of it
       const bool before = sample * p.sample_rows < row0, after = (sample + 1) * p.sample_rows > row1;
-      if constexpr (W) {
-        // what the sample's sums are of the gains' gradients, and then of its own
-        auto share = [&](int which, int v, F8& sum, const void* mods, int64_t ld, float plus, const float* gains) {
-          const uint64_t add = f2_pack(plus, plus);
-          F8 m = {{f2_pack(1.f, 1.f), f2_pack(1.f, 1.f), f2_pack(1.f, 1.f), f2_pack(1.f, 1.f)}};
-          if (mods != nullptr) {
-            m = read8<ACCESS>(static_cast<const BT*>(mods) + sample * ld + col[v], left[v], tpr);
+      // what a sum is of a gain's gradient, and then the modulation's
+      auto share = [&](int which, int v, F8& sum, const void* mods, int64_t ld, float plus, const float* gains) {
+        const uint64_t add = f2_pack(plus, plus);
+        F8 m = {{f2_pack(1.f, 1.f), f2_pack(1.f, 1.f), f2_pack(1.f, 1.f), f2_pack(1.f, 1.f)}};
+        if (mods != nullptr) {
+          m = read8<ACCESS>(static_cast<const BT*>(mods) + sample * ld + col[v], left[v], tpr);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) m.p[k] = f2_add(m.p[k], add);
-          }
-          add_w(which, v, sum, m);
-          const F8 w = read8<ACCESS>(gains + col[v], left[v], tpr);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) sum.p[k] = f2_mul(sum.p[k], w.p[k]);
-        };
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          if (left[v] <= 0) continue;
-          if (post) share(0, v, acc_mod[SUM_GATE][v], p.n.gate, p.n.gate_ld, 0.f, p.n.post);
-          if (pre) share(1, v, acc_mod[SUM_SCALE][v], p.n.scale, p.n.scale_ld, 1.f, p.n.pre);
+          for (int k = 0; k < 4; ++k) m.p[k] = f2_add(m.p[k], add);
         }
-      }
+        float* const at = gain_sums(which, v);
+        F8 t = read8<ACCESS>(at, left[v], tpr);
+        const F8 w = read8<ACCESS>(gains + col[v], left[v], tpr);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          t.p[k] = f2_fma(sum.p[k], m.p[k], t.p[k]);
+          sum.p[k] = f2_mul(sum.p[k], w.p[k]);
+        }
+        write8<ACCESS>(at, left[v], tpr, t);
+      };
 #pragma unroll
       for (int k = 0; k < 3; ++k) {
-        if (!p.has[k]) {
-#pragma unroll
-          for (int v = 0; v < NV; ++v) acc_mod[k][v] = f8_zero();
-          continue;
-        }
+        const bool gain = (k == SUM_GATE && post) || (k == SUM_SCALE && pre);
+        if (!p.has[k] && !gain) continue;
         across_groups(acc_mod[k]);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-          if (group == 0 && left[v] > 0) {
+          if (W && gain && group == 0 && left[v] > 0) {
+            if (k == SUM_GATE) share(0, v, acc_mod[k][v], p.n.gate, p.n.gate_ld, 0.f, p.n.post);
+            else share(1, v, acc_mod[k][v], p.n.scale, p.n.scale_ld, 1.f, p.n.pre);
+          }
+          if (p.has[k] && group == 0 && left[v] > 0) {
             if (before || after)
               write8<ACCESS>(
                   p.partial_mod + ((cta * 2 + (before ? 0 : 1)) * 3 + k) * static_cast<int64_t>(pitch) + col[v],
@@ -549,7 +558,7 @@ __global__ void __launch_bounds__(norm_threads(SIZE), SIZE == 0 ? 2 : 1)
         if (fill.issued & (1u << s)) wait_drain(&full_bar[s], (fill.parity >> s) & 1u, 50000000ull);
     return;
   }
-  if constexpr (W) {
+  if constexpr (W && !MOD) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       if (!p.has[SUM_POST + k]) continue;
@@ -567,7 +576,7 @@ __global__ void __launch_bounds__(norm_threads(SIZE), SIZE == 0 ? 2 : 1)
 #pragma unroll
       for (int v = 0; v < NV; ++v)
         if (group == 0 && left[v] > 0)
-          write8<ACCESS>(p.partial_w + (cta * 2 + k) * static_cast<int64_t>(pitch) + col[v], left[v], tpr, total[v]);
+          write8<ACCESS>(gain_sums(k, v), left[v], tpr, total[v]);
     }
   }
 }
