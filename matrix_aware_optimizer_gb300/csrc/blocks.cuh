@@ -248,17 +248,6 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* t
       : "memory");
 }
 
-// The same, written to the same offset in every CTA of `mask`; each is counted
-// on the barrier at bar_cluster_addr's offset in its own pair.
-__device__ __forceinline__ void tma_load_2d_pair_multicast(void* dst, const CUtensorMap* tm, uint32_t bar_cluster_addr,
-                                                           uint16_t mask, int x, int y) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster.cta_group::2"
-      " [%0], [%1, {%4, %5}], [%2], %3;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(tm)), "r"(bar_cluster_addr), "h"(mask), "r"(x), "r"(y)
-      : "memory");
-}
-
 // 2-D tile store of a box staged in shared memory, in the thread's current
 // bulk async-group. Elements outside the tensor are not written.
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* tm, const void* src, int x, int y) {

@@ -24,13 +24,11 @@
 // kept exactly, and with bf16 g and u 0.0029 - 0.0035.
 //
 // Bound by the tensor cores for more than a few hundred tokens. 8192 tokens,
-// 2048 x 8192, bf16, each launch alone: GLU 322 us (1.71 PFLOP/s, with 400 MB of
-// g and u written), down 190 (1.45), DGLU 207 (1.33, 790 MB moved), gradients
-// 835 (1.65). Both passes 1.60 - 1.73 ms (1.54 - 1.43 PFLOP/s: the SM clock
-// under the power cap decides), those of 4096 tokens, 5120 x 20480 4.9 - 5.1 ms
-// (1.57 - 1.52). On the busiest SMs the tensor pipe is active 84 - 87 % of the time
-// (DGLU, where the epilogue's loads of g and u bound it, 74 %); the rest is
-// partly filled last rounds and the 8 SMs that clusters of four leave idle.
+// 2048 x 8192, bf16: forward 488 us (1.69 PFLOP/s), with g and u saved 515,
+// backward 1185 (1.39), both passes 1.73 ms (1.43 PFLOP/s: the SM clock under
+// the power cap decides); those of 4096 tokens, 5120 x 20480 5.08 - 5.10 ms
+// (1.52). 16384 tokens, 768 x 2048: 0.43 ms (1.07); 65536 tokens, 256 x 704,
+// where the tensors' bytes weigh more: 0.66 ms.
 //
 // CTA layout, pipeline and TMEM use are those of the Newton-Schulz GEMMs
 // (ns5_gemm.cu): 320 threads, warp 0 TMA producer, warp 1 MMA issue in the
@@ -93,7 +91,6 @@ constexpr int MAX_SEGS = 4;
 struct FfnParams {
   FfnSegment seg[MAX_SEGS];
   int nseg;
-  int pairs;            // of a cluster
   int64_t total;        // work items: whole tiles and parts of split ones
   int64_t long_items, hole_end;  // see next_item
   uint4* gu;            // packed g and u (GLU: written when not NULL; DGLU: read)
@@ -109,7 +106,7 @@ struct Item {
   int kb0, kb1;
 };
 
-// Tiles run in groups of GROUP_M row tiles, rows fastest, so that the ~76
+// Tiles run in groups of GROUP_M row tiles, rows fastest, so that the 76
 // pairs at work cover a block of about 8 x 9 tiles: per slice of K they share
 // half the operand bytes of a 32 x 2 block.
 constexpr int GROUP_M = 8;
@@ -120,17 +117,16 @@ __device__ __forceinline__ int ffn_seg(const FfnParams& p, int64_t item) {
   return s;
 }
 
-// The item of cluster c of n after `item` (first: item = c - n). Items go
-// round the clusters. Where the first product has longer sums than the others
-// and its items leave a last round part empty, the clusters without one take
+// The item of CTA pair c of n after `item` (first: item = c - n). Items go
+// round the pairs. Where the first product has longer sums than the others
+// and its items leave a last round part empty, the pairs without one take
 // that many short items more (the hole, up to hole_end), so that all come to
-// the end together (18 tile times instead of 19 at 8192 x 2048 x 8192, 112
-// instead of 117 at 4096 x 5120 x 20480; both passes, on one machine, 1679 us
-// instead of 1710, and 4917 instead of 5034).
+// the end together (17 tile times instead of 18 at 8192 x 2048 x 8192, 106
+// instead of 113 at 4096 x 5120 x 20480).
 template <int EPI>
 __device__ __forceinline__ int64_t next_item(const FfnParams& p, int64_t item, int64_t c, int64_t n) {
   if (EPI != EPI_STORE || item >= p.hole_end) return item + n;
-  const int64_t rest = static_cast<uint32_t>(p.long_items) % static_cast<uint32_t>(n);  // clusters with an item then
+  const int64_t rest = static_cast<uint32_t>(p.long_items) % static_cast<uint32_t>(n);  // pairs with an item then
   int64_t to;
   if (item >= p.long_items) {
     to = item + n - rest;
@@ -143,9 +139,8 @@ __device__ __forceinline__ int64_t next_item(const FfnParams& p, int64_t item, i
   return to < p.hole_end ? to : p.hole_end + c;
 }
 
-// PAIRS pairs of a cluster take tiles next to each other along N.
-template <int EPI, int PAIRS>
-__device__ __forceinline__ Item ffn_item(const FfnSegment& sg, int64_t item, int pair) {
+template <int EPI>
+__device__ __forceinline__ Item ffn_item(const FfnSegment& sg, int64_t item) {
   Item it;
   int tile = static_cast<int>(item - sg.item_begin);
   const int kb = sg.k_blocks[0] + sg.k_blocks[1];
@@ -161,12 +156,12 @@ __device__ __forceinline__ Item ffn_item(const FfnSegment& sg, int64_t item, int
     it.kb1 = static_cast<int>(static_cast<int64_t>(kb) * (it.split + 1) / sg.splits);
     tile = sg.whole + it.split_tile;
   }
-  const int group = tile / (GROUP_M * sg.tiles_n);  // (tiles_n counts groups of PAIRS tiles)
+  const int group = tile / (GROUP_M * sg.tiles_n);
   const int rows = min(GROUP_M, sg.tiles_m - group * GROUP_M);
   const int in_group = tile - group * GROUP_M * sg.tiles_n;
   const int tn = in_group / rows;
   it.m0 = (group * GROUP_M + in_group - tn * rows) * PAIR_M;
-  it.n0 = (tn * PAIRS + pair) * (EPI == EPI_GLU ? BN_HALF : BN);
+  it.n0 = tn * (EPI == EPI_GLU ? BN_HALF : BN);
   return it;
 }
 
@@ -306,8 +301,8 @@ __device__ __forceinline__ void store_box(const FfnSegment& sg, int i0, int j0, 
   }
 }
 
-template <int EPI, typename T, int ACT, int PAIRS>
-__global__ void __cluster_dims__(2 * PAIRS, 1, 1) __launch_bounds__(NUM_THREADS, 1)
+template <int EPI, typename T, int ACT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     ffn_gemm_kernel(const __grid_constant__ FfnParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -324,16 +319,14 @@ __global__ void __cluster_dims__(2 * PAIRS, 1, 1) __launch_bounds__(NUM_THREADS,
 
   const int warp = threadIdx.x / 32;
   const int lane = threadIdx.x % 32;
-  const uint32_t rank = cluster_ctarank() & 1;  // within the pair
-  const int pair = static_cast<int>(cluster_ctarank() >> 1);
-  const uint32_t even = 2 * static_cast<uint32_t>(pair);  // cluster rank of this pair's even CTA
-  const int64_t cluster_id = blockIdx.x / (2 * PAIRS);
-  const int64_t num_clusters = gridDim.x / (2 * PAIRS);
+  const uint32_t rank = cluster_ctarank();
+  const int64_t cluster_id = blockIdx.x / 2;
+  const int64_t num_clusters = gridDim.x / 2;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full_bar[s], 1);
-      mbar_init(&empty_bar[s], PAIRS);  // a stage of A is free when every pair has used it
+      mbar_init(&empty_bar[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull_bar[a], 1);
@@ -367,7 +360,7 @@ __global__ void __cluster_dims__(2 * PAIRS, 1, 1) __launch_bounds__(NUM_THREADS,
       for (int64_t item = next_item<EPI>(p, cluster_id - num_clusters, cluster_id, num_clusters); ok && item < p.total;
          item = next_item<EPI>(p, item, cluster_id, num_clusters)) {
         const FfnSegment& sg = p.seg[ffn_seg(p, item)];
-        const Item it = ffn_item<EPI, PAIRS>(sg, item, pair);
+        const Item it = ffn_item<EPI>(sg, item);
         const int m_cta = it.m0 + static_cast<int>(rank) * BM;
         const int n_cta = EPI == EPI_GLU ? it.n0 : it.n0 + static_cast<int>(rank) * BN_HALF;
         for (int kb = it.kb0; kb < it.kb1; ++kb) {
@@ -376,21 +369,14 @@ __global__ void __cluster_dims__(2 * PAIRS, 1, 1) __launch_bounds__(NUM_THREADS,
             break;
           }
           if (rank == 0) mbar_arrive_expect_tx(&full_bar[stage], PAIR_STAGE_BYTES);
-          const uint32_t bar = mapa_shared(smem_u32(&full_bar[stage]), even);
+          const uint32_t bar = mapa_shared(smem_u32(&full_bar[stage]), 0);
           uint8_t* a_dst = sA + stage * TILE_BYTES;
           uint8_t* b_dst = sB + stage * TILE_BYTES;
           const int second = kb >= sg.k_blocks[0] ? 1 : 0;  // operand pair
           const int k = (second ? kb - sg.k_blocks[0] : kb) * BK;
           const CUtensorMap* ma = &sg.a[second];
           const CUtensorMap* mb = EPI == EPI_GLU ? &sg.b[rank] : &sg.b[second];
-          if constexpr (PAIRS == 2) {
-            // the pairs share their rows of A: each loads half of them for both
-            const uint16_t mask = static_cast<uint16_t>(0x5u << rank);
-            const int m_half = m_cta + pair * 64;
-            uint8_t* dst = a_dst + pair * MN_CHUNK_BYTES;  // 64 rows x 64 or 64 x 64 of either layout
-            if (EPI == EPI_STORE && sg.a_mn) tma_load_2d_pair_multicast(dst, ma, bar, mask, m_half, k);
-            else tma_load_2d_pair_multicast(dst, ma, bar, mask, k, m_half);
-          } else if (EPI == EPI_STORE && sg.a_mn) {
+          if (EPI == EPI_STORE && sg.a_mn) {
 #pragma unroll
             for (int q = 0; q < BM / 64; ++q)
               tma_load_2d_pair(a_dst + q * MN_CHUNK_BYTES, ma, bar, m_cta + q * 64, k);
@@ -434,7 +420,7 @@ __global__ void __cluster_dims__(2 * PAIRS, 1, 1) __launch_bounds__(NUM_THREADS,
       for (int64_t item = next_item<EPI>(p, cluster_id - num_clusters, cluster_id, num_clusters); ok && item < p.total;
          item = next_item<EPI>(p, item, cluster_id, num_clusters)) {
         const FfnSegment& sg = p.seg[ffn_seg(p, item)];
-        const Item it = ffn_item<EPI, PAIRS>(sg, item, pair);
+        const Item it = ffn_item<EPI>(sg, item);
         const bool a_mn = EPI == EPI_STORE && sg.a_mn;
         const bool b_mn = EPI == EPI_DGLU || (EPI == EPI_STORE && sg.b_mn);
         const uint32_t idesc = idesc_f16kind_f32(PAIR_M, BN, a_mn, b_mn, FP16);
@@ -461,21 +447,21 @@ __global__ void __cluster_dims__(2 * PAIRS, 1, 1) __launch_bounds__(NUM_THREADS,
             umma_bf16_pair(d_tmem, ad, bd, idesc, (kb - it.kb0) | k ? 1u : 0u);
           }
           issued_any = true;
-          umma_commit_pair_multicast(&empty_bar[stage], (1u << (2 * PAIRS)) - 1);
+          umma_commit_pair_multicast(&empty_bar[stage], 0x3);
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
           }
         }
         if (!ok) break;
-        umma_commit_pair_multicast(&tfull_bar[acc], static_cast<uint16_t>(0x3u << even));
+        umma_commit_pair_multicast(&tfull_bar[acc], 0x3);
         if (++acc == 2) {
           acc = 0;
           acc_phase ^= 1u;
         }
       }
       if (!ok && issued_any) {
-        umma_commit_pair_multicast(drain_bar, static_cast<uint16_t>(0x1u << even));
+        umma_commit_pair_multicast(drain_bar, 0x1);
         wait_drain(drain_bar, 0, 50000000ull);
       }
     }
@@ -484,13 +470,13 @@ __global__ void __cluster_dims__(2 * PAIRS, 1, 1) __launch_bounds__(NUM_THREADS,
     const int ew = warp - 2;
     const int half = ew >> 2;
     uint8_t* stage = sEpi + ew * EPI_WARP_BYTES;
-    const uint32_t tempty_even = mapa_shared(smem_u32(&tempty_bar[0]), even);
+    const uint32_t tempty_even = mapa_shared(smem_u32(&tempty_bar[0]), 0);
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int64_t item = next_item<EPI>(p, cluster_id - num_clusters, cluster_id, num_clusters); item < p.total;
          item = next_item<EPI>(p, item, cluster_id, num_clusters)) {
       const FfnSegment& sg = p.seg[ffn_seg(p, item)];
-      const Item it = ffn_item<EPI, PAIRS>(sg, item, pair);
+      const Item it = ffn_item<EPI>(sg, item);
       const int i0 = it.m0 + static_cast<int>(rank) * BM + quarter * 32;
       const int jh = it.n0 + half * (EPI == EPI_GLU ? BN_HALF / 2 : BN / 2);  // first column of this warp
       uint4 raw[2][EPI == EPI_DGLU ? 12 : 1];
@@ -531,7 +517,7 @@ __global__ void __cluster_dims__(2 * PAIRS, 1, 1) __launch_bounds__(NUM_THREADS,
         // A part of the sum along K: this warp's 32 x 128 values go to the
         // workspace; the warp that arrives last for them adds all parts, in
         // order, and stores the result. Warps without rows have nothing to do.
-        const int64_t region = ((static_cast<int64_t>(it.split_tile) * PAIRS + pair) * 2 + rank) * EPI_WARPS + ew;
+        const int64_t region = (static_cast<int64_t>(it.split_tile) * 2 + rank) * EPI_WARPS + ew;
         float4* mine = reinterpret_cast<float4*>(sg.partial) + (region * sg.splits + it.split) * (32 * 32) + lane;
         if (i0 < sg.M) {
 #pragma unroll
@@ -611,9 +597,6 @@ PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
 
 enum MapUse { MAP_ROWS, MAP_COLS, MAP_STORE };  // 128 x 64 boxes, 64 x 64 boxes, 32 x 32 output boxes
 
-// Boxes of a K-major A: the two pairs of a cluster each load half its rows.
-MapUse map_a(int pairs) { return pairs == 2 ? MAP_COLS : MAP_ROWS; }
-
 // A row-major rows x cols matrix of 16-bit elements with row pitch ld.
 bool encode(CUtensorMap* map, const void* base, int dtype, int64_t rows, int64_t cols, int64_t ld, MapUse use) {
   auto enc = map_encoder();
@@ -628,42 +611,42 @@ bool encode(CUtensorMap* map, const void* base, int dtype, int64_t rows, int64_t
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int EPI, typename T, int ACT, int PAIRS>
+template <int EPI, typename T, int ACT>
 int resident_clusters(int num_sms) {
   static std::atomic<int> cached[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
   const int known = cached[dev].load(std::memory_order_relaxed);
   if (known > 0) return known;
-  if (cudaFuncSetAttribute(ffn_gemm_kernel<EPI, T, ACT, PAIRS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  if (cudaFuncSetAttribute(ffn_gemm_kernel<EPI, T, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(SMEM_BYTES)) != cudaSuccess)
     return 0;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(num_sms / (2 * PAIRS) * 2 * PAIRS));
+  cfg.gridDim = dim3(static_cast<unsigned>(num_sms / 2 * 2));
   cfg.blockDim = dim3(NUM_THREADS);
   cfg.dynamicSmemBytes = SMEM_BYTES;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2 * PAIRS;
+  attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, ffn_gemm_kernel<EPI, T, ACT, PAIRS>, &cfg) != cudaSuccess || n <= 0) {
+  if (cudaOccupancyMaxActiveClusters(&n, ffn_gemm_kernel<EPI, T, ACT>, &cfg) != cudaSuccess || n <= 0) {
     cudaGetLastError();
-    n = num_sms / (2 * PAIRS);
+    n = num_sms / 2;
   }
   cached[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 
-template <int EPI, typename T, int ACT, int PAIRS>
+template <int EPI, typename T, int ACT>
 cudaError_t launch(FfnParams& p, int num_sms, cudaStream_t stream) {
-  const int clusters = resident_clusters<EPI, T, ACT, PAIRS>(num_sms);
+  const int clusters = resident_clusters<EPI, T, ACT>(num_sms);
   if (clusters == 0) return cudaErrorInvalidConfiguration;
   const int64_t n = std::min<int64_t>(p.total, clusters);
-  const unsigned grid = static_cast<unsigned>(2 * PAIRS * n);
+  const unsigned grid = static_cast<unsigned>(2 * n);
   p.long_items = p.hole_end = 0;
   if (p.nseg > 1) {
     const int64_t first = p.seg[1].item_begin, kb = p.seg[0].k_blocks[0] + p.seg[0].k_blocks[1];
@@ -673,16 +656,13 @@ cudaError_t launch(FfnParams& p, int num_sms, cudaStream_t stream) {
       p.hole_end = first + (n - first % n) * rounds;
     }
   }
-  return launch_dependent(ffn_gemm_kernel<EPI, T, ACT, PAIRS>, dim3(grid), dim3(NUM_THREADS), SMEM_BYTES, stream, p);
+  return launch_dependent(ffn_gemm_kernel<EPI, T, ACT>, dim3(grid), dim3(NUM_THREADS), SMEM_BYTES, stream, p);
 }
 
 template <int EPI, int ACT = 0>
 cudaError_t launch(FfnParams& p, int dtype, int num_sms, cudaStream_t stream) {
-  if (p.pairs == 2)
-    return dtype == PRM_BF16 ? launch<EPI, __nv_bfloat16, ACT, 2>(p, num_sms, stream)
-                             : launch<EPI, __half, ACT, 2>(p, num_sms, stream);
-  return dtype == PRM_BF16 ? launch<EPI, __nv_bfloat16, ACT, 1>(p, num_sms, stream)
-                           : launch<EPI, __half, ACT, 1>(p, num_sms, stream);
+  return dtype == PRM_BF16 ? launch<EPI, __nv_bfloat16, ACT>(p, num_sms, stream)
+                           : launch<EPI, __half, ACT>(p, num_sms, stream);
 }
 
 template <int EPI>
@@ -692,46 +672,35 @@ cudaError_t launch_act(FfnParams& p, int act, int dtype, int num_sms, cudaStream
   return launch<EPI, PRM_ACT_GELU_TANH>(p, dtype, num_sms, stream);
 }
 
-// Work items of an M x N product with tiles of 256 x tile_n, `pairs` of them
-// side by side to an item.
-int64_t items_of(int64_t M, int64_t N, int tile_n, int pairs) {
-  return ((M + PAIR_M - 1) / PAIR_M) * ((N + static_cast<int64_t>(tile_n) * pairs - 1) / (tile_n * pairs));
-}
-// Clusters that run at once: 76 pairs, or 36 clusters of two pairs (four CTAs
-// fit a GPC's SMs less well).
-int clusters_of(int pairs) { return pairs == 2 ? 36 : 76; }
-// Two pairs to a cluster read A once for both, a quarter less operand traffic
-// per SM: the backward pass takes 1081 us instead of 1123 at 8192 x 2048 x 8192
-// and 3410 instead of 3744 at 4096 x 5120 x 20480, with 144 of the 152 SMs. With
-// less than two waves of such items the finer ones win.
-int pairs_for(int64_t items_of_two) { return items_of_two >= 72 ? 2 : 1; }
+// Tiles of 256 x tile_n of an M x N product.
+int64_t tiles_of(int64_t M, int64_t N, int tile_n) { return ((M + PAIR_M - 1) / PAIR_M) * ((N + tile_n - 1) / tile_n); }
+constexpr int64_t AT_ONCE = 76;  // CTA pairs on the 152 SMs
 
-// The items of a product that runs alone go to the clusters in waves. Where
-// the last wave is not full, its items are split along K over the idle
-// clusters: 256 tiles on 76 pairs take 3.5 tile times instead of 4.
+// The tiles of a product that runs alone go to the pairs in waves. Where the
+// last wave is not full, its tiles are split along K over the idle pairs: 256
+// tiles on 76 pairs take 3.5 tile times instead of 4.
 constexpr int MIN_PART = 4;  // slices of K in a part
 struct Split {
-  int pairs;
-  int64_t whole, rest;  // items computed whole and in parts
+  int64_t whole, rest;  // tiles computed whole and in parts
   int splits;
 };
 Split split_last_wave(int64_t M, int64_t N, int64_t K) {
-  Split s{pairs_for(items_of(M, N, BN, 2)), 0, 0, 1};
-  const int64_t items = items_of(M, N, BN, s.pairs), at_once = clusters_of(s.pairs);
-  const int64_t rest = items % at_once;
+  Split s{0, 0, 1};
+  const int64_t items = tiles_of(M, N, BN);
+  const int64_t rest = items % AT_ONCE;
   const int64_t kb = (K + BK - 1) / BK;
   // adding up the parts costs about two slices of K per part: no more parts than that pays for
   const int64_t pays = static_cast<int64_t>(std::sqrt(static_cast<double>(kb) / 2)) + 1;
-  const int64_t parts = rest == 0 ? 1 : std::min<int64_t>({at_once / rest, kb / MIN_PART, pays, 16});
+  const int64_t parts = rest == 0 ? 1 : std::min<int64_t>({AT_ONCE / rest, kb / MIN_PART, pays, 16});
   s.whole = parts < 2 ? items : items - rest;
   s.rest = items - s.whole;
   s.splits = parts < 2 ? 1 : static_cast<int>(parts);
   return s;
 }
 size_t partial_bytes(const Split& s) {
-  return static_cast<size_t>(s.rest) * s.pairs * s.splits * PAIR_M * BN * sizeof(float);
+  return static_cast<size_t>(s.rest) * s.splits * PAIR_M * BN * sizeof(float);
 }
-size_t counter_bytes(const Split& s) { return static_cast<size_t>(s.rest) * s.pairs * 2 * EPI_WARPS * 4; }
+size_t counter_bytes(const Split& s) { return static_cast<size_t>(s.rest) * 2 * EPI_WARPS * 4; }
 
 // Extents and items of one product, and its place in the queue.
 void queue(FfnParams& p, FfnSegment& sg, int64_t M, int64_t N, int64_t K0, int64_t K1, bool a_mn, bool b_mn,
@@ -743,7 +712,7 @@ void queue(FfnParams& p, FfnSegment& sg, int64_t M, int64_t N, int64_t K0, int64
   sg.a_mn = a_mn;
   sg.b_mn = b_mn;
   sg.tiles_m = static_cast<int>((M + PAIR_M - 1) / PAIR_M);
-  const int items = static_cast<int>(items_of(M, N, tile_n, p.pairs));
+  const int items = static_cast<int>(tiles_of(M, N, tile_n));
   sg.tiles_n = items / sg.tiles_m;
   if (sg.splits < 2) {
     sg.whole = items;
@@ -782,8 +751,7 @@ int check(int64_t T, int64_t d, int64_t f) {
   if (T >= (int64_t(1) << 31) - 256 || d >= (int64_t(1) << 24) || f >= (int64_t(1) << 24)) return PRM_ERR_UNSUPPORTED;
   // tiles are counted in 32 bits
   constexpr int64_t MOST = int64_t(1) << 30;
-  if (items_of(T, f, BN_HALF, 1) > MOST || 3 * items_of(d, f, BN, 1) + items_of(T, d, BN, 1) > MOST)
-    return PRM_ERR_UNSUPPORTED;
+  if (tiles_of(T, f, BN_HALF) > MOST || 3 * tiles_of(d, f, BN) + tiles_of(T, d, BN) > MOST) return PRM_ERR_UNSUPPORTED;
   return PRM_OK;
 }
 
@@ -838,9 +806,8 @@ extern "C" int prm_gated_ffn_forward(const void* x, int64_t ldx, const void* w_g
   uint32_t* counters = reinterpret_cast<uint32_t*>(ws + sz.fwd_counters);
   p.zero = counters;
   p.zero_count = static_cast<int>(counter_bytes(sz.down) / 4);
-  p.pairs = pairs_for(items_of(tokens, f, BN_HALF, 2));
   FfnSegment sg{};
-  if (!encode(&sg.a[0], x, dtype, tokens, d, ldx, map_a(p.pairs)) || !encode(&sg.b[0], w_gate, dtype, f, d, d, MAP_ROWS) ||
+  if (!encode(&sg.a[0], x, dtype, tokens, d, ldx, MAP_ROWS) || !encode(&sg.b[0], w_gate, dtype, f, d, d, MAP_ROWS) ||
       !encode(&sg.b[1], w_up, dtype, f, d, d, MAP_ROWS) || !encode(&sg.out[0], h, dtype, tokens, f, f, MAP_STORE))
     return PRM_ERR_CUDA;
   queue(p, sg, tokens, f, d, 0, false, false, BN_HALF);
@@ -848,9 +815,8 @@ extern "C" int prm_gated_ffn_forward(const void* x, int64_t ldx, const void* w_g
 
   FfnParams q{};
   q.err = dev->d_err;
-  q.pairs = sz.down.pairs;
   FfnSegment dn{};
-  if (!encode(&dn.a[0], h, dtype, tokens, f, f, map_a(q.pairs)) || !encode(&dn.b[0], w_down, dtype, d, f, f, MAP_ROWS) ||
+  if (!encode(&dn.a[0], h, dtype, tokens, f, f, MAP_ROWS) || !encode(&dn.b[0], w_down, dtype, d, f, f, MAP_ROWS) ||
       !encode(&dn.out[0], y, dtype, tokens, d, d, MAP_STORE))
     return PRM_ERR_CUDA;
   dn.whole = static_cast<int>(sz.down.whole);
@@ -903,9 +869,8 @@ extern "C" int prm_gated_ffn_backward(const void* dy, int64_t lddy, const void* 
   FfnParams p{};
   p.err = dev->d_err;
   p.gu = reinterpret_cast<uint4*>(const_cast<char*>(static_cast<const char*>(saved)) + sz.saved_h);
-  p.pairs = pairs_for(items_of(tokens, f, BN, 2));
   FfnSegment sg{};
-  if (!encode(&sg.a[0], dy, dtype, tokens, d, lddy, map_a(p.pairs)) || !encode(&sg.b[0], w_down, dtype, d, f, f, MAP_COLS) ||
+  if (!encode(&sg.a[0], dy, dtype, tokens, d, lddy, MAP_ROWS) || !encode(&sg.b[0], w_down, dtype, d, f, f, MAP_COLS) ||
       !encode(&sg.out[0], dg, dtype, tokens, f, f, MAP_STORE) ||
       !encode(&sg.out[1], du, dtype, tokens, f, f, MAP_STORE))
     return PRM_ERR_CUDA;
@@ -916,14 +881,12 @@ extern "C" int prm_gated_ffn_backward(const void* dy, int64_t lddy, const void* 
   // longer sums first, so that the last tiles of the queue are short.
   FfnParams q{};
   q.err = dev->d_err;
-  q.pairs = pairs_for((dx != nullptr ? items_of(tokens, d, BN, 2) : 0) +
-                      (weights ? 2 * items_of(f, d, BN, 2) + items_of(d, f, BN, 2) : 0));
   bool ok = true;
   auto add_dx = [&] {
     if (dx == nullptr) return;
     FfnSegment s{};
-    ok = ok && encode(&s.a[0], dg, dtype, tokens, f, f, map_a(q.pairs)) &&
-         encode(&s.a[1], du, dtype, tokens, f, f, map_a(q.pairs)) &&
+    ok = ok && encode(&s.a[0], dg, dtype, tokens, f, f, MAP_ROWS) &&
+         encode(&s.a[1], du, dtype, tokens, f, f, MAP_ROWS) &&
          encode(&s.b[0], w_gate, dtype, f, d, d, MAP_COLS) && encode(&s.b[1], w_up, dtype, f, d, d, MAP_COLS) &&
          encode(&s.out[0], dx, dtype, tokens, d, d, MAP_STORE);
     queue(q, s, tokens, d, f, f, false, true, BN);

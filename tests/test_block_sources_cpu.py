@@ -1,0 +1,28 @@
+"""Properties of the block operators' kernels that no run may bring out --
+they would hang or fault a GPU, or depend on what another GPU maps -- read off
+the sources instead."""
+import os
+import re
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "matrix_aware_optimizer_gb300", "csrc")
+SOURCES = sorted(n for n in os.listdir(CSRC) if n.endswith((".cu", ".cuh", ".h")))
+
+
+def _code(name):
+    """A source without its comments."""
+    with open(os.path.join(CSRC, name)) as f:
+        text = f.read()
+    return re.sub(r"//[^\n]*|/\*.*?\*/", "", text, flags=re.S)
+
+
+@pytest.mark.parametrize("name", SOURCES)
+def test_no_load_is_multicast(name):
+    """The library runs in replicas on several GPUs and takes any pointer a
+    caller has, so no bulk or tensor load writes to several CTAs at once
+    (arrivals on barriers may)."""
+    joined = re.sub(r'"\s*"', "", _code(name))     # adjacent literals of one asm statement
+    for statement in re.findall(r'"[^"]*cp\.async\.bulk[^"]*"', joined):
+        assert "multicast" not in statement, statement
