@@ -295,6 +295,11 @@ __device__ __forceinline__ void st_cluster2(uint32_t addr, uint32_t a, uint32_t 
   asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
 
+// The two halves of a cluster barrier that orders no memory: all CTAs of the
+// cluster have started.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait;" ::: "memory"); }
+
 struct ClusterSort {
   const void* token;
   int token_bytes;
@@ -323,6 +328,7 @@ __global__ void __maxnreg__(48) cluster_sort_kernel(const ClusterSort s) {
   __shared__ uint32_t warp_sum[WARPS];
   const uint32_t rank_cta = cluster_ctarank();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  cluster_arrive();  // this CTA has started; met below, behind the loads of the tokens
   const uint32_t nbins = 1u << s.bits;
   const int steps = static_cast<int>(s.chunk / 1024);
   const uint32_t first = rank_cta * s.chunk;
@@ -341,6 +347,7 @@ __global__ void __maxnreg__(48) cluster_sort_kernel(const ClusterSort s) {
       pos[k] = first + i;
     }
   }
+  cluster_wait();  // all eight have: their shared memory may be written
   for (int pass = 0; pass < s.passes; ++pass) {
     const int shift = pass * s.bits;
     for (uint32_t b = threadIdx.x; b < WARPS * EMB_MAX_BINS / 2; b += 1024) reinterpret_cast<uint32_t*>(bins)[b] = 0;

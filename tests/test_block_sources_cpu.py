@@ -26,3 +26,25 @@ def test_no_load_is_multicast(name):
     joined = re.sub(r'"\s*"', "", _code(name))     # adjacent literals of one asm statement
     for statement in re.findall(r'"[^"]*cp\.async\.bulk[^"]*"', joined):
         assert "multicast" not in statement, statement
+
+
+def _kernel(name, kernel):
+    """The body of a __global__ function."""
+    text = _code(name)
+    start = text.index("{", text.index(kernel + "("))
+    depth, end = 0, start
+    while True:
+        depth += {"{": 1, "}": -1}.get(text[end], 0)
+        end += 1
+        if depth == 0:
+            return text[start:end]
+
+
+def test_cluster_sort_meets_before_it_writes_to_other_blocks():
+    """A block's shared memory may be written by another block of its cluster
+    only once it is known to have started."""
+    body = _kernel("embedding.cu", "cluster_sort_kernel")
+    first_store = re.search(r"\bst_cluster2?\(", body).start()
+    met = re.search(r"\bcluster_(sync_all|wait)\(", body).start()
+    assert met < first_store
+    assert len(re.findall(r"\bcluster_arrive\w*\(", body)) == len(re.findall(r"\bcluster_wait\(", body))
