@@ -48,3 +48,13 @@ def test_cluster_sort_meets_before_it_writes_to_other_blocks():
     met = re.search(r"\bcluster_(sync_all|wait)\(", body).start()
     assert met < first_store
     assert len(re.findall(r"\bcluster_arrive\w*\(", body)) == len(re.findall(r"\bcluster_wait\(", body))
+
+
+def test_norm_gradient_leaves_no_thread_alone_at_a_barrier():
+    """The threads of a row, and of a block, meet at barriers that have no
+    time limit; one whose bounded wait gave up must go on to them."""
+    body = _kernel("block_norm_grad.cuh", "norm_backward_kernel")
+    loop = body[body.index("int stage = 0;"):]
+    assert "wait_unless_aborted(" in loop and "row_sums" in body
+    assert not re.search(r"\b(break|return|goto)\b\s*;", loop)
+    assert not re.search(r"seg0 < row1 &&|base < count &&", loop)
