@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(norm_threads(SIZE), SIZE == 0 ? 2 : 1)
       const uint32_t nr = io.dy ? ring_bytes(io.r + at, nd, io.r + all) : 0u;
       const uint32_t ndr = io.dr ? ring_bytes(io.dr + at, nd, io.dr + all) : 0u;
       const uint32_t nz = io.z ? ring_bytes(io.z + at, nd, io.z + all) : 0u;
-      if (fill.row + n == p.n.rows) {  // the tensors' ends
+      if (all - at - nd < 8) {  // less than 16 bytes of a tensor behind these rows: its end
         if (io.dy) {
           ring_tail(dst, io.dy + at, nd, io.dy + all);
           ring_tail(dst + by + bdr, io.r + at, nd, io.r + all);

@@ -224,7 +224,8 @@ enum Access { VEC, ELEM, DIRECT };
 // on 16 bytes, to shared memory at the same offset from a 16-byte boundary.
 // ring_bytes: what the copy brings (its start rounded down, its end up, but
 // not past the last whole 16 bytes before `end`, the tensor's end);
-// ring_tail: the elements behind those, stored by this thread.
+// ring_tail: the elements behind those, stored by this thread. Any n elements
+// that end less than 16 bytes before the tensor can have some.
 template <typename T>
 __device__ __forceinline__ uint32_t ring_bytes(const T* src, uint32_t n, const T* end) {
   const uintptr_t lo = reinterpret_cast<uintptr_t>(src) & ~uintptr_t(15);
