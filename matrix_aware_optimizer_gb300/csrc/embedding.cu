@@ -30,6 +30,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <type_traits>
 
 #include "blocks.cuh"
 
@@ -827,6 +828,25 @@ cudaError_t launch_cluster_sort(const ClusterSort& s, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, cluster_sort_kernel, s);
 }
 
+// Most dynamic shared memory of a piece kernel: 256 / tpc groups of EMB_PIECE
+// rows of 8 tpc fp32 elements and 32 bytes for their ends, with tpc >= 2.
+constexpr int EMB_PIECE_SMEM = EMB_THREADS / 2 * EMB_PIECE * (2 * 8 * 4 + 32);
+
+// Allows a piece kernel that once per device. The limit belongs to the kernel,
+// not to a launch: set to what each call needs, it could fall below another
+// thread's between that one's setting and its launch.
+template <typename DT, typename GT, int ACCESS>
+cudaError_t piece_setup() {
+  static std::atomic<bool> set[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (set[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(piece_kernel<DT, GT, ACCESS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             EMB_PIECE_SMEM);
+  if (e == cudaSuccess) set[dev].store(true, std::memory_order_relaxed);
+  return e;
+}
+
 template <typename F>
 bool one_type(int dtype, F&& f) {
   if (dtype == PRM_FP32) return f(float{}), true;
@@ -994,21 +1014,20 @@ extern "C" int prm_embedding_backward(const void* dout, int dout_dtype, const vo
     one_type(grad_dtype, [&](auto gt) {
       using DT = decltype(dt);
       using GT = decltype(gt);
-      auto go = [&](auto pieces, auto block, auto span) {
-        if (smem > 36 * 1024) {  // (with the static part, above the default limit of 48 KB)
-          e = cudaFuncSetAttribute(pieces, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-          if (e != cudaSuccess) return;
-        }
-        e = launch_dependent(pieces, dim3(ctas, slabs), dim3(EMB_THREADS), smem, st, m, static_cast<const DT*>(dout),
-                             static_cast<GT*>(grad));
+      auto go = [&](auto access, auto span) {
+        constexpr int A = decltype(access)::value;
+        e = piece_setup<DT, GT, A>();
+        if (e == cudaSuccess)
+          e = launch_dependent(piece_kernel<DT, GT, A>, dim3(ctas, slabs), dim3(EMB_THREADS), smem, st, m,
+                               static_cast<const DT*>(dout), static_cast<GT*>(grad));
         if (e == cudaSuccess && pl.blocks > 0)
-          e = launch_dependent(block, dim3((pl.blocks + per - 1) / per, slabs), dim3(EMB_THREADS), 0, st, m);
+          e = launch_dependent(block_kernel, dim3((pl.blocks + per - 1) / per, slabs), dim3(EMB_THREADS), 0, st, m);
         if (e == cudaSuccess && pl.pieces > 1)
           e = launch_dependent(span, dim3(blocks, slabs), dim3(EMB_THREADS), 0, st, m, static_cast<GT*>(grad));
       };
-      if (vec) go(piece_kernel<DT, GT, VEC>, block_kernel, span_kernel<GT, true>);
-      else if (ring) go(piece_kernel<DT, GT, ELEM>, block_kernel, span_kernel<GT, false>);
-      else go(piece_kernel<DT, GT, DIRECT>, block_kernel, span_kernel<GT, false>);
+      if (vec) go(std::integral_constant<int, VEC>{}, span_kernel<GT, true>);
+      else if (ring) go(std::integral_constant<int, ELEM>{}, span_kernel<GT, false>);
+      else go(std::integral_constant<int, DIRECT>{}, span_kernel<GT, false>);
     });
   });
   return e == cudaSuccess ? PRM_OK : PRM_ERR_CUDA;

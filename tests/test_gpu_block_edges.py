@@ -1,5 +1,8 @@
 """The block operators where rows, buffers, threads and limits meet their
 edges. Comparisons and tolerances are those of test_gpu_blocks.py."""
+import ctypes
+import threading
+
 import pytest
 import torch
 
@@ -35,3 +38,45 @@ def test_norm_gradient_of_narrow_rows(B, L, d, st, bt):
 def test_norm_gradient_of_narrow_rows_without_samples(d, rows):
     """As many rows as leave one behind the last full step of 128 rows."""
     _check_norm(*_norm_case(1, rows, d, "rms", BF16, BF16, 1, 0, 1, 0, eps=1e-3))
+
+
+# ------------------------------------------------------ threads of one process
+def test_embedding_gradients_of_four_threads():
+    """Threads that run gradients of the same types and different widths at
+    once do not change each other's launches."""
+    lib = N.load()
+    T, V, kept, failures = 300, 40, [], []
+
+    def call(d):
+        """The library call for one width on a stream of its own, and its check."""
+        g = torch.Generator(device="cuda").manual_seed(d)
+        tok = torch.randint(0, V, (T,), generator=g, device="cuda")
+        dout = torch.randn(T, d, generator=g, device="cuda")
+        want = prm.embedding_backward(dout, tok, V)
+        n = ctypes.c_size_t()
+        assert lib.prm_embedding_backward_workspace(T, V, d, n) == N.PRM_OK
+        ws = torch.empty(n.value, dtype=torch.uint8, device="cuda")
+        out, stream = torch.empty_like(want), torch.cuda.Stream()
+        kept.append((tok, dout, ws, stream))
+        args = (dout.data_ptr(), N.PRM_FP32, tok.data_ptr(), 8, out.data_ptr(), N.PRM_FP32, 0, T, V, d, 1.0,
+                ws.data_ptr(), n.value, stream.cuda_stream)
+        return args, out, want
+
+    # rows in whole vectors: 128 and 65 KB of shared memory; element by element: 192 and 112 KB
+    calls = [call(d) for d in (2048, 1032, 15, 17)]
+    torch.cuda.synchronize()
+
+    def run(args):
+        codes = {lib.prm_embedding_backward(*args) for _ in range(3000)}
+        if codes != {N.PRM_OK}:
+            failures.append((args[9], codes))
+
+    threads = [threading.Thread(target=run, args=(c[0],)) for c in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failures, failures
+    for _, out, want in calls:
+        assert torch.equal(out, want)
