@@ -85,7 +85,7 @@ PRM_API int prm_gated_ffn_backward(const void* dy, int64_t lddy, const void* x, 
 #define PRM_NORM_LAYER 1
 
 typedef struct {
-  int64_t rows;             /* all rows of all samples, below 2^32 */
+  int64_t rows;             /* all rows of all samples, below 2^32, and below 2^31 where d > 256 */
   int64_t rows_per_sample;  /* rows that share a row of gate / scale / shift; divides rows (>= 1) */
   int64_t d;                /* 1 .. 8192 */
   int32_t kind;             /* PRM_NORM_* */

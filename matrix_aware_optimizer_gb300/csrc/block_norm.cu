@@ -31,6 +31,8 @@ int norm_check(const prm_block_norm_desc* c, NormParams* p) {
   if (c->rows < 0 || c->d < 1 || c->rows_per_sample < 1 || c->rows % c->rows_per_sample != 0) return PRM_ERR_SHAPE;
   if (c->d > NORM_MAX_D) return PRM_ERR_UNSUPPORTED;
   if (c->rows / c->rows_per_sample > 0x7fffffff || c->rows > 0xffffffffll) return PRM_ERR_UNSUPPORTED;
+  // the forward pass has a CTA for each row that takes more than a warp
+  if (c->rows > 0x7fffffff && c->d > 256) return PRM_ERR_UNSUPPORTED;
   if ((c->gate != nullptr && c->gate_ld < c->d) || (c->scale != nullptr && c->scale_ld < c->d) ||
       (c->shift != nullptr && c->shift_ld < c->d))
     return PRM_ERR_SHAPE;
@@ -328,7 +330,6 @@ extern "C" int prm_block_norm_forward(const prm_block_norm_desc* desc, const voi
   if (y == nullptr && (desc->pre_weight != nullptr || desc->scale != nullptr || desc->shift != nullptr))
     return PRM_ERR_INVALID_ARG;
   if (!aligned_to(stats, 16)) return PRM_ERR_ALIGNMENT;
-  if (p.rows > 0x7fffffff) return PRM_ERR_UNSUPPORTED;
   const void* rows[4] = {x, z, r, y};
   const bool vec = norm_aligned(*desc, rows, 4);
   cudaError_t e = cudaErrorInvalidValue;

@@ -1,0 +1,32 @@
+"""What the block operators' entry points refuse and which device they ask,
+on the CPU: nothing here reaches a device."""
+import ctypes
+import types
+
+import pytest
+import torch
+
+from matrix_aware_optimizer_gb300 import blocks, build, native as N
+
+from .test_blocks_cpu import _desc
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build_library()
+    return N.load()
+
+
+@pytest.mark.parametrize("rows,d", [(1 << 31, 257), ((1 << 32) - 1, 8192), (1 << 32, 1)])
+def test_norm_calls_agree_on_their_most_rows(lib, rows, d):
+    desc, n = _desc(rows=rows, rows_per_sample=rows, d=d), ctypes.c_size_t()
+    assert lib.prm_block_norm_forward(desc, 16, 16, 16, 16, 16, None) == N.PRM_ERR_UNSUPPORTED
+    assert lib.prm_block_norm_workspace(desc, n) == N.PRM_ERR_UNSUPPORTED
+    assert lib.prm_block_norm_backward(desc, 16, 16, 16, 16, 16, 16, 16, None, None, None, None, None, None, 0,
+                                       None) == N.PRM_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("rows,d", [((1 << 31) - 1, 8192), ((1 << 32) - 1, 256)])
+def test_norm_takes_the_rows_below(lib, rows, d):
+    n = ctypes.c_size_t()
+    assert lib.prm_block_norm_workspace(_desc(rows=rows, rows_per_sample=rows, d=d, pre_weight=16), n) == N.PRM_OK

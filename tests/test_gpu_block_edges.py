@@ -80,3 +80,21 @@ def test_embedding_gradients_of_four_threads():
     assert not failures, failures
     for _, out, want in calls:
         assert torch.equal(out, want)
+
+
+# ----------------------------------------------------------------- many rows
+def test_norm_of_more_rows_than_31_bits_count():
+    rows = (1 << 31) + 77
+    x = torch.zeros(rows, 1, dtype=BF16, device="cuda")
+    x[-100:, 0] = torch.linspace(-2.0, 2.0, 100, device="cuda")
+    y = torch.empty_like(x)
+    desc = N.prm_block_norm_desc(rows=rows, rows_per_sample=rows, d=1, kind=N.PRM_NORM_RMS, stream_dtype=N.PRM_BF16,
+                                 block_dtype=N.PRM_BF16, alpha=1.0, eps=0.25)
+    rc = N.load().prm_block_norm_forward(desc, x.data_ptr(), None, None, y.data_ptr(), None,
+                                         torch.cuda.current_stream().cuda_stream)
+    assert rc == N.PRM_OK
+    v = x[-100:].double()
+    want = v / torch.sqrt(v * v + 0.25)
+    # one rounding to bf16 and a few in fp32
+    assert ((y[-100:].double() - want).abs() <= (2.0 ** -8 + 2.0 ** -19) * want.abs()).all()
+    assert torch.count_nonzero(y[:-100]) == 0
