@@ -53,9 +53,10 @@ def _ptr(t: Optional[torch.Tensor]):
 
 def blocks_sync_status(stream: Optional[torch.cuda.Stream] = None) -> None:
     """Waits for the stream and raises if a device-side wait of a block
-    operator gave up."""
+    operator gave up on the stream's device."""
     s = stream if stream is not None else torch.cuda.current_stream()
-    N.check(N.load().prm_blocks_sync_status(s.cuda_stream), "prm_blocks_sync_status")
+    with torch.cuda.device(s.device):  # the error word is the current device's
+        N.check(N.load().prm_blocks_sync_status(s.cuda_stream), "prm_blocks_sync_status")
 
 
 # ---------------------------------------------------------------- gated FFN

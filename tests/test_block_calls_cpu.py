@@ -30,3 +30,40 @@ def test_norm_calls_agree_on_their_most_rows(lib, rows, d):
 def test_norm_takes_the_rows_below(lib, rows, d):
     n = ctypes.c_size_t()
     assert lib.prm_block_norm_workspace(_desc(rows=rows, rows_per_sample=rows, d=d, pre_weight=16), n) == N.PRM_OK
+
+
+# -------------------------------------------------------------------- devices
+class _Devices:
+    """Stands in for torch.cuda's notion of the current device."""
+
+    def __init__(self, monkeypatch):
+        self.current, outer = 0, self
+
+        class device:
+            def __init__(self, d):
+                self.index = d if isinstance(d, int) else d.index
+
+            def __enter__(self):
+                self.before, outer.current = outer.current, self.index
+
+            def __exit__(self, *_):
+                outer.current = self.before
+
+        monkeypatch.setattr(torch.cuda, "device", device)
+
+
+def _stream(index):
+    return types.SimpleNamespace(device=torch.device("cuda", index), cuda_stream=77)
+
+
+def test_status_is_read_on_the_streams_device(monkeypatch):
+    devices, asked = _Devices(monkeypatch), []
+
+    def status(stream):
+        asked.append((devices.current, stream))
+        return N.PRM_OK
+
+    monkeypatch.setattr(N, "load", lambda: types.SimpleNamespace(prm_blocks_sync_status=status))
+    blocks.blocks_sync_status(_stream(1))
+    blocks.blocks_sync_status(_stream(0))
+    assert asked == [(1, 77), (0, 77)] and devices.current == 0
