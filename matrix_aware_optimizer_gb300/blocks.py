@@ -2,8 +2,8 @@
 whose parameters the optimizer updates. Each operator is a forward and a
 backward call on tensors; PyTorch supplies memory and the stream, every
 arithmetic step runs in libprm. Outputs and workspaces are allocated on the
-stream the call runs on (`stream`, or the current one). Work that a call
-depends on and that runs on another stream is the caller's to order, as with
+stream the call runs on (`stream`, or the current one of the tensors' device).
+Work that a call depends on and that runs on another stream is the caller's to order, as with
 any torch operation."""
 from __future__ import annotations
 
@@ -44,6 +44,8 @@ def _elsewhere(device: int, stream: Optional[torch.cuda.Stream], *tensors: Optio
 
 
 def _is_elsewhere(device: int, stream) -> bool:
+    if stream is not None and stream.device.index != device:
+        raise ValueError("stream must be one of the tensors' device")
     return stream is not None or device != _current_device()
 
 

@@ -67,3 +67,13 @@ def test_status_is_read_on_the_streams_device(monkeypatch):
     blocks.blocks_sync_status(_stream(1))
     blocks.blocks_sync_status(_stream(0))
     assert asked == [(1, 77), (0, 77)] and devices.current == 0
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    monkeypatch.setattr(blocks, "_current_device", lambda: 0)
+    with pytest.raises(ValueError):
+        blocks._is_elsewhere(0, _stream(1))
+    with pytest.raises(ValueError):
+        blocks._is_elsewhere(1, _stream(0))
+    assert blocks._is_elsewhere(1, _stream(1)) and blocks._is_elsewhere(0, _stream(0))
+    assert blocks._is_elsewhere(1, None) and not blocks._is_elsewhere(0, None)
