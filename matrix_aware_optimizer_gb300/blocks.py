@@ -64,9 +64,13 @@ def blocks_sync_status(stream: Optional[torch.cuda.Stream] = None) -> None:
 # ---------------------------------------------------------------- gated FFN
 class FfnSaved(NamedTuple):
     """What gated_ffn leaves for gated_ffn_backward: h, g and u of one pass
-    (8 bytes per token and feature), in the library's own layout."""
+    (8 bytes per token and feature), in the library's own layout, and the
+    features, activation and type it was made with."""
     buffer: torch.Tensor
     tokens: int
+    features: Optional[int] = None
+    act: Optional[str] = None
+    dtype: Optional[torch.dtype] = None
 
 
 def _rows16(t: torch.Tensor, d: int) -> Tuple[torch.Tensor, int]:
@@ -129,7 +133,7 @@ def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down:
                                         d, f, _ACT[act], _DTYPE[x.dtype], _raw_stream(device))
     if rc:
         N.check(rc, "prm_gated_ffn_forward")
-    return (y, FfnSaved(saved, tokens)) if save else y
+    return (y, FfnSaved(saved, tokens, f, act, x.dtype)) if save else y
 
 
 def gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
@@ -145,6 +149,8 @@ def gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, 
     d, f, device = _ffn_check(x, w_gate, w_up, w_down, act)
     if dy.shape != x.shape or dy.dtype is not x.dtype or dy.get_device() != device:
         raise ValueError("dy must have x's shape, type and device")
+    if saved.features not in (None, f) or saved.act not in (None, act) or saved.dtype not in (None, x.dtype):
+        raise ValueError("saved comes from a pass with other weights, another act or another type")
     if _is_elsewhere(device, stream):
         with _elsewhere(device, stream, dy, x, w_gate, w_up, w_down, saved.buffer, *(grads or ())):
             return gated_ffn_backward(dy, x, w_gate, w_up, w_down, saved, act, need_dx, grads)

@@ -82,6 +82,24 @@ def test_embedding_gradients_of_four_threads():
         assert torch.equal(out, want)
 
 
+# ------------------------------------------------- what a forward pass left behind
+def test_ffn_backward_refuses_what_another_call_saved():
+    def inputs(f, dtype):
+        g = torch.Generator(device="cuda").manual_seed(f)
+        return [torch.randn(*s, generator=g, device="cuda").to(dtype) for s in ((1, 64), (f, 64), (f, 64), (64, f))]
+
+    x, *ws = inputs(8, BF16)
+    y, saved = prm.gated_ffn(x, *ws, act="gelu", save=True)
+    prm.gated_ffn_backward(y, x, *ws, saved, act="gelu")
+    with pytest.raises(ValueError):
+        prm.gated_ffn_backward(y, x, *ws, saved)                      # silu is not what was saved
+    with pytest.raises(ValueError):
+        prm.gated_ffn_backward(y, x, *inputs(16, BF16)[1:], saved, act="gelu")   # as many bytes, more features
+    half = inputs(8, FP16)
+    with pytest.raises(ValueError):
+        prm.gated_ffn_backward(y.half(), *half, saved, act="gelu")
+
+
 # ----------------------------------------------------------------- many rows
 def test_norm_of_more_rows_than_31_bits_count():
     rows = (1 << 31) + 77
