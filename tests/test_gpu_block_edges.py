@@ -100,6 +100,58 @@ def test_ffn_backward_refuses_what_another_call_saved():
         prm.gated_ffn_backward(y.half(), *half, saved, act="gelu")
 
 
+# ------------------------------------------------------------ buffers in place
+@pytest.mark.parametrize("st,bt", [(FP32, BF16), (BF16, BF16)])
+@pytest.mark.parametrize("d,off", [(48, 0), (2048, 0), (5120, 0), (8192, 0), (7, 0), (1001, 0), (3001, 0), (1001, 1),
+                                   (64, 1)])
+def test_norms_in_place(d, off, st, bt):
+    """r over x, dx over dr and dz over dy give the bits of separate buffers,
+    with whole vectors, odd rows and buffers off 16 bytes."""
+    lib, stream = N.load(), torch.cuda.current_stream().cuda_stream
+    B, L = 3, 211
+    x, z, par, dy, dr, kw, eps = _norm_case(B, L, d, "layer", st, bt, 1, 1, 1, 1)
+    code = {FP32: N.PRM_FP32, BF16: N.PRM_BF16}
+
+    def copy(t):
+        return torch.empty(t.numel() + off, dtype=t.dtype, device="cuda")[off:].view(t.shape).copy_(t)
+
+    p = {k: v.data_ptr() for k, v in par.items()}
+    ld = par["gate"].stride(0)
+    desc = N.prm_block_norm_desc(rows=B * L, rows_per_sample=L, d=d, kind=N.PRM_NORM_LAYER, stream_dtype=code[st],
+                                 block_dtype=code[bt], alpha=kw["alpha"], eps=eps, gate_ld=ld, scale_ld=ld,
+                                 shift_ld=ld, **p)
+    n = ctypes.c_size_t()
+    assert lib.prm_block_norm_workspace(desc, n) == N.PRM_OK
+    ws = torch.empty(n.value, dtype=torch.uint8, device="cuda")
+
+    def forward(src, dst, y, stats):
+        assert lib.prm_block_norm_forward(desc, src.data_ptr(), z.data_ptr(), dst.data_ptr(), y.data_ptr(),
+                                          stats.data_ptr(), stream) == N.PRM_OK
+
+    def backward(gy, gr, gx, gz, r, stats):
+        cols = [torch.empty(d, device="cuda"), torch.empty(B, d, dtype=bt, device="cuda"),
+                torch.empty(d, device="cuda"), torch.empty(B, d, dtype=bt, device="cuda"),
+                torch.empty(B, d, dtype=bt, device="cuda")]
+        assert lib.prm_block_norm_backward(desc, gy.data_ptr(), gr.data_ptr(), r.data_ptr(), z.data_ptr(),
+                                           stats.data_ptr(), gx.data_ptr(), gz.data_ptr(),
+                                           *(c.data_ptr() for c in cols), ws.data_ptr(), n.value, stream) == N.PRM_OK
+        return cols
+
+    x1, x2 = copy(x), copy(x)
+    r, y1, y2 = copy(x), copy(z), copy(z)
+    s1, s2 = (torch.empty(B * L, 4, device="cuda") for _ in range(2))
+    forward(x1, r, y1, s1)
+    forward(x2, x2, y2, s2)
+    assert torch.equal(r, x2) and torch.equal(y1, y2) and torch.equal(s1, s2)
+    gy, gr, gy2, gr2 = copy(dy), copy(dr), copy(dy), copy(dr)
+    gx, gz = copy(dr), copy(dy)
+    a = backward(gy, gr, gx, gz, r, s1)
+    b = backward(gy2, gr2, gr2, gy2, r, s1)
+    assert torch.equal(gx, gr2) and torch.equal(gz, gy2)
+    for u, v in zip(a, b):
+        assert torch.equal(u, v)
+
+
 # ----------------------------------------------------------------- many rows
 def test_norm_of_more_rows_than_31_bits_count():
     rows = (1 << 31) + 77
