@@ -87,6 +87,7 @@ __global__ void __launch_bounds__(norm_threads(SIZE), SIZE == 0 ? 2 : 1)
   __shared__ float scratch[2][128];
   __shared__ uint64_t full_bar[MAX_STAGES], empty_bar[MAX_STAGES];
   __shared__ volatile int abort_flag;
+  __shared__ volatile int row_failed[norm_threads(SIZE) / 64];  // [group of rows of more than a warp]
   const int tpr = p.n.tpr, d = p.n.d, groups = p.groups;
   const int threads = tpr * groups;
   const int step_rows = groups * R;
@@ -123,6 +124,7 @@ __global__ void __launch_bounds__(norm_threads(SIZE), SIZE == 0 ? 2 : 1)
       abort_flag = 0;
       fence_mbar_init();
     }
+    if (threadIdx.x < norm_threads(SIZE) / 64) row_failed[threadIdx.x] = -1;
     __syncthreads();
   }
   pdl_wait();
@@ -278,18 +280,26 @@ __global__ void __launch_bounds__(norm_threads(SIZE), SIZE == 0 ? 2 : 1)
 
   int stage = 0;
   uint32_t phase = 0;
-  // Once a wait has given up, none is waited for any more, but every thread
-  // takes part in everything else to the end: the threads of its row, and of
-  // the CTA, may have got their stage and meet it at barriers that have no time
-  // limit. (The sums are worthless then, which the error word says. Against
-  // leaving the loops: 324 us instead of 312 at 8 x 1024 x 8192 modulated,
-  // elsewhere within 1 %.)
+  // A warp whose wait gave up must not leave the other warps of its row, which
+  // may have got their stage, at a barrier that has no time limit. It names the
+  // step in its row's word and goes on to the step's reductions. Behind their
+  // barrier the whole row finds the abort flag up, and that step named, and
+  // leaves together at the next one. A row that is dead in a sample's last step
+  // meets the CTA at the next sample's start. The CTA's barriers do not wait for
+  // threads that have exited, and a step without reductions meets nobody. (At 32 x
+  // 1024 x 2048 modulated and 8 x 1024 x 8192 with gains and modulation, us: this
+  // 195 and 346; a vote at the reductions' barrier 200 and 373; a test behind it
+  // 202 and 346; going on to the end without leaving 191 and 392.)
+  bool leave = false;
   // The CTA's rows, sample by sample.
-  for (int64_t seg0 = row0; seg0 < row1;) {
+  for (int64_t seg0 = row0; seg0 < row1 && !leave;) {
     const int64_t sample = seg0 / p.sample_rows;
     const int64_t seg1 = min(row1, (sample + 1) * p.sample_rows);
     if constexpr (MOD) {
-      __syncthreads();  // the sample before is done with its columns
+      // the sample before is done with its columns
+      if constexpr (RING) leave = __syncthreads_or(abort_flag);
+      else __syncthreads();
+      if (leave) break;
       fill_columns(sample);
     }
     if constexpr (MOD || W) __syncthreads();
@@ -300,8 +310,15 @@ __global__ void __launch_bounds__(norm_threads(SIZE), SIZE == 0 ? 2 : 1)
       const int mine = count - base - group * R;  // rows of this step from this group's first one on
       if constexpr (RING) {
         if (threadIdx.x == 0 && seg0 + base != row0) refill();
-        wait_unless_aborted(&full_bar[stage], phase, &abort_flag, p.err, NORM_WAIT_NS);
-        __syncwarp();
+        const bool aborted = abort_flag != 0;
+        const bool got = wait_bounded(&full_bar[stage], phase, &abort_flag, p.err, NORM_WAIT_NS);
+        if (!__all_sync(0xffffffffu, got && !aborted)) {
+          const int first = stage == 0, p0 = static_cast<int>(phase);
+          const int before = 2 * (first ? p.stages - 1 : stage - 1) + (p0 ^ first);  // the step before
+          leave = (SIZE == 0 && tpr <= 32) || row_failed[group] == before;  // (or the row lies in this warp)
+          if (leave) break;
+          row_failed[group] = 2 * stage + p0;
+        }
       }
       const uint8_t* src = smem + stage * stage_bytes;
       const int in_step = group * R * d;
@@ -504,6 +521,7 @@ __global__ void __launch_bounds__(norm_threads(SIZE), SIZE == 0 ? 2 : 1)
         }
       }
     }
+    if (leave) break;
     if constexpr (MOD) {
       // the end of the sample, or of this CTA's part of it
       const bool before = sample * p.sample_rows < row0, after = (sample + 1) * p.sample_rows > row1;
@@ -551,6 +569,12 @@ __global__ void __launch_bounds__(norm_threads(SIZE), SIZE == 0 ? 2 : 1)
     }
     seg0 = seg1;
   }
+  if (RING && threadIdx.x == 0 && abort_flag) {
+    // a wait gave up: let the copies in flight land before the CTA exits
+    for (int s = 0; s < p.stages; ++s)
+      if (fill.issued & (1u << s)) wait_drain(&full_bar[s], (fill.parity >> s) & 1u, 50000000ull);
+  }
+  if (leave) return;
   if constexpr (W && !MOD) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -572,10 +596,6 @@ __global__ void __launch_bounds__(norm_threads(SIZE), SIZE == 0 ? 2 : 1)
           write8<ACCESS>(gain_sums(k, v), left[v], tpr, total[v]);
     }
   }
-  // After a wait that gave up: let the copies in flight land before the CTA exits.
-  if (RING && threadIdx.x == 0 && abort_flag)
-    for (int s = 0; s < p.stages; ++s)
-      if (fill.issued & (1u << s)) wait_drain(&full_bar[s], (fill.parity >> s) & 1u, 50000000ull);
 }
 
 // out[row][column] = sum of partial sums, in CTA order. The first

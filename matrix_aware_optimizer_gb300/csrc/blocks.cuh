@@ -190,21 +190,6 @@ inline cudaError_t launch_dependent(void (*kernel)(KArgs...), dim3 grid, dim3 bl
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
-// wait_bounded(), but at once without a wait where *abort is raised already:
-// a thread may go on through many stages after one wait has given up.
-__device__ __forceinline__ void wait_unless_aborted(uint64_t* bar, uint32_t parity, volatile int* abort, int* err,
-                                                    uint64_t limit_ns) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  if (ok == 0 && !*abort) wait_bounded(bar, parity, abort, err, limit_ns);
-}
-
 // ------------------------------------------------------------- bulk copies
 // Contiguous copy of `bytes` (a multiple of 16; both addresses 16-byte
 // aligned) from global to this CTA's shared memory, counted on `bar`.

@@ -51,10 +51,17 @@ def test_cluster_sort_meets_before_it_writes_to_other_blocks():
 
 
 def test_norm_gradient_leaves_no_thread_alone_at_a_barrier():
-    """The threads of a row, and of a block, meet at barriers that have no
-    time limit; one whose bounded wait gave up must go on to them."""
+    """The warps of a row meet at barriers that have no time limit, so one
+    whose bounded wait gave up says so in front of the step's reductions, and
+    the whole row, which knows behind them, leaves at the next step's wait."""
     body = _kernel("block_norm_grad.cuh", "norm_backward_kernel")
-    loop = body[body.index("int stage = 0;"):]
-    assert "wait_unless_aborted(" in loop and "row_sums" in body
-    assert not re.search(r"\b(break|return|goto)\b\s*;", loop)
-    assert not re.search(r"seg0 < row1 &&|base < count &&", loop)
+    loop = body[body.index("int stage = 0;"):body.rindex("if (leave) return;")]
+    for way in re.findall(r"[^;{}]*\b(?:break|return|goto \w+);", loop):
+        assert way.strip() == "if (leave) break;", way
+    asked, wait = loop.index("aborted = abort_flag"), loop.index("wait_bounded(")
+    agreed, said = loop.index("row_failed[group] == before"), loop.index("row_failed[group] =", loop.index("if (leave)",
+                                                                         loop.index("row_failed[group] == before")))
+    assert asked < wait < agreed < said < loop.index("reduce(sums)")
+    # the only other ways out: a row inside the warp, and the block's own agreement
+    assert [" ".join(v.split()) for v in re.findall(r"leave = ([^;=][^;]*);", loop)] == [
+        "false", "__syncthreads_or(abort_flag)", "(SIZE == 0 && tpr <= 32) || row_failed[group] == before"]
