@@ -27,9 +27,10 @@
 extern "C" {
 #endif
 
-/* Synchronises `stream` and reads the current device's error word of the
- * calls below (a bounded device-side wait that gave up). Returns PRM_OK,
- * TIMEOUT or CUDA; clears the word. */
+/* Synchronises `stream`, one of the current device, and reads that device's
+ * error word of the calls below (a bounded device-side wait that gave up; the
+ * call's outputs are then worthless). Returns PRM_OK, TIMEOUT or CUDA; clears
+ * the word. */
 PRM_API int prm_blocks_sync_status(void* stream);
 
 /* ---- gated feed-forward block ------------------------------------------
@@ -50,8 +51,9 @@ PRM_API int prm_gated_ffn_sizes(int64_t tokens, int64_t d, int64_t f, size_t* sa
 
 /* y from x. saved: prm_gated_ffn_sizes' `saved` bytes, 256-byte aligned, or
  * NULL where no backward pass follows. workspace: 256-byte aligned, at least
- * `forward_workspace` bytes. h is rounded to dtype for the second product;
- * saved holds h in dtype and g and u with 16 significand bits each.
+ * `forward_workspace` bytes. h is rounded to dtype for the second product (in
+ * fp16 an h beyond 65504 becomes infinite); saved holds h in dtype and g and u
+ * with 16 significand bits each.
  * Errors: INVALID_ARG, ALIGNMENT, WORKSPACE, UNSUPPORTED, CUDA. */
 PRM_API int prm_gated_ffn_forward(const void* x, int64_t ldx, const void* w_gate, const void* w_up,
                                   const void* w_down, void* y, void* saved, void* workspace, size_t workspace_bytes,
@@ -117,6 +119,8 @@ PRM_API int prm_block_norm_workspace(const prm_block_norm_desc* desc, size_t* by
 
 /* Gradients from dy (of y) and dr (of r, from the rows' later uses; NULL for
  * 0); r, z and stats as the forward pass left them (r: x where z was NULL).
+ * Without post_weight and gate, z may be NULL here even if the forward pass had
+ * one (dz is then not wanted); dx is alpha times r's gradient all the same.
  * dx (NULL allowed, as is dz) and dz are rows x d; dpost, dpre: d fp32;
  * dgate, dscale, dshift: samples x d contiguous of block_dtype. A gradient
  * pointer is required for each parameter that desc holds and ignored for the

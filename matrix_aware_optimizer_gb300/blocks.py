@@ -1,10 +1,12 @@
 """torch glue over include/prm_blocks.h: the operators of a transformer block
 whose parameters the optimizer updates. Each operator is a forward and a
 backward call on tensors; PyTorch supplies memory and the stream, every
-arithmetic step runs in libprm. Outputs and workspaces are allocated on the
-stream the call runs on (`stream`, or the current one of the tensors' device).
-Work that a call depends on and that runs on another stream is the caller's to order, as with
-any torch operation."""
+arithmetic step runs in libprm. The calls are outside autograd: what they
+return has no graph, whether or not the inputs require gradients, and the
+backward calls are the caller's to make. Outputs and workspaces are allocated
+on the stream the call runs on (`stream`, or the current one of the tensors'
+device). Work that a call depends on and that runs on another stream is the
+caller's to order, as with any torch operation."""
 from __future__ import annotations
 
 import contextlib
@@ -116,7 +118,8 @@ def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down:
 
     x: [..., d] bf16 or fp16; w_gate, w_up: [f, d]; w_down: [d, f], all of x's
     type; d and f multiples of 8. act: "silu", "gelu" (erf) or "gelu_tanh".
-    Returns y, or (y, saved) with save=True, saved for gated_ffn_backward.
+    Returns y, or (y, saved) with save=True, saved for gated_ffn_backward
+    (autograd does not see the call).
     """
     d, f, device = _ffn_check(x, w_gate, w_up, w_down, act)
     if _is_elsewhere(device, stream):
@@ -143,8 +146,10 @@ def gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, 
     """Gradients of gated_ffn: (dx, dw_gate, dw_up, dw_down), all of x's type.
 
     grads: three tensors of the weights' shapes and type to write the weight
-    gradients into, e.g. the buffers that PeriodicRowMuon has registered (they
-    are overwritten). dx is None with need_dx=False.
+    gradients into (they are overwritten), e.g. the buffers that PeriodicRowMuon
+    has registered where the weights are bf16; it takes no fp16 gradients, which
+    the caller converts. act and the weights are those of the pass that made
+    `saved`. dx is None with need_dx=False.
     """
     d, f, device = _ffn_check(x, w_gate, w_up, w_down, act)
     if dy.shape != x.shape or dy.dtype is not x.dtype or dy.get_device() != device:
@@ -253,7 +258,8 @@ def block_norm(x: torch.Tensor, z: Optional[torch.Tensor] = None, kind: str = "r
     or "layer". z None: r is x, y is its norm (`dtype` picks y's type).
     join_only: no norm follows; y is None.
 
-    Returns (r, y, stats), stats for block_norm_backward.
+    Returns (r, y, stats), stats for block_norm_backward (autograd does not
+    see the call).
     """
     device = x.get_device()
     if device < 0:
@@ -347,7 +353,8 @@ def _tokens(tokens: torch.Tensor) -> torch.Tensor:
 def embedding(tokens: torch.Tensor, table: torch.Tensor, scale: float = 1.0, dtype: Optional[torch.dtype] = None,
               stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """scale * table[tokens], as `dtype` (default: the table's). table: [vocab,
-    d] fp32, bf16 or fp16. A token outside [0, vocab) is padding: a zero row."""
+    d] fp32, bf16 or fp16. A token outside [0, vocab) is padding: a zero row.
+    Autograd does not see the call: embedding_backward gives table's gradient."""
     device = table.get_device()
     if dtype is None:
         dtype = table.dtype

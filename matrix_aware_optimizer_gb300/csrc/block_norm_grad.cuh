@@ -26,10 +26,12 @@
 // that do not start on 16 bytes are read from memory by the threads (DIRECT).
 //
 // Measured (device time, share of the copy bandwidth on the bytes above):
-// 32 x 1024 x 2048 modulated, fp32 stream and bf16 block, 190 us (94 %);
-// 8191 x 5120 bf16 with both gains 110 us (67 %); 65536 x 512 bf16 87 us (69
-// %); 30000 x 1001 bf16 153 us (35 %; 239 from a kernel compiled for every
-// sum), 8000 x 4999 197 us (365). What is left is the chain of each
+// 32 x 1024 x 2048 modulated, fp32 stream and bf16 block, 195 us (92 %);
+// 8191 x 5120 bf16 with both gains 112 us (66 %); 65536 x 512 bf16 89 us (67
+// %); 30000 x 1001 bf16 155 us (34 %; 239 from a kernel compiled for every
+// sum), 8000 x 4999 195 us (365); with gains and modulation 8 x 1024 x 2048 bf16
+// 69 us (43 %), 8 x 1024 x 8192 fp32 / bf16 346 us (51 %), 8 x 1024 x 3001 bf16
+// 284 us (15 %; 239 with five sums per row). What is left is the chain of each
 // row -- load, reduce, reduce, store -- behind which only the rows of the
 // other CTA of the SM, or the thread's second row, can hide: registers (40
 // column sums and their operands per thread) allow no more of them. Fewer

@@ -26,7 +26,10 @@
 //
 // Measured, back to back: 62 us there (its bytes at the copy rate: 44) and 138
 // at 65521 tokens of 1001 bf16 into 100003 rows of fp32 (78), of which the sort
-// takes 31, the pieces about 65 and the runs' partial sums about 20.
+// takes 31, the pieces about 65 and the runs' partial sums about 20. Past 65536
+// tokens, where the sort takes three launches a pass with nothing beside it:
+// 131072 tokens, 64000 x 2048 bf16 226 us (118), 1048576 tokens of 512 bf16 into
+// 64000 rows of fp32 494 (179).
 #include <algorithm>
 #include <atomic>
 #include <cmath>

@@ -28,7 +28,12 @@
 // backward 1185 (1.39), both passes 1.73 ms (1.43 PFLOP/s: the SM clock under
 // the power cap decides); those of 4096 tokens, 5120 x 20480 5.08 - 5.10 ms
 // (1.52). 16384 tokens, 768 x 2048: 0.43 ms (1.07); 65536 tokens, 256 x 704,
-// where the tensors' bytes weigh more: 0.66 ms.
+// where the tensors' bytes weigh more: 0.66 ms. Each launch alone (8192 tokens,
+// 2048 x 8192): GLU 314 us (1.75 PFLOP/s, with 400 MB of g and u written), down
+// 193 (1.43), DGLU 198 (1.39, 790 MB moved), gradients 870 (1.58); the tensor
+// pipe is active 79, 65, 67 and 68 % of the time: every pair loads all of its
+// operands itself, the last rounds are part empty, and DGLU's epilogue waits
+// for g and u.
 //
 // CTA layout, pipeline and TMEM use are those of the Newton-Schulz GEMMs
 // (ns5_gemm.cu): 320 threads, warp 0 TMA producer, warp 1 MMA issue in the
@@ -122,7 +127,8 @@ __device__ __forceinline__ int ffn_seg(const FfnParams& p, int64_t item) {
 // and its items leave a last round part empty, the pairs without one take
 // that many short items more (the hole, up to hole_end), so that all come to
 // the end together (17 tile times instead of 18 at 8192 x 2048 x 8192, 106
-// instead of 113 at 4096 x 5120 x 20480).
+// instead of 113 at 4096 x 5120 x 20480; both passes, in turn on one machine,
+// 1652 us instead of 1674 and 4898 instead of 5031).
 template <int EPI>
 __device__ __forceinline__ int64_t next_item(const FfnParams& p, int64_t item, int64_t c, int64_t n) {
   if (EPI != EPI_STORE || item >= p.hole_end) return item + n;
