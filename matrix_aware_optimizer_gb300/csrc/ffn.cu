@@ -25,9 +25,9 @@
 //
 // Bound by the tensor cores for more than a few hundred tokens. 8192 tokens,
 // 2048 x 8192, bf16: forward 488 us (1.69 PFLOP/s), with g and u saved 515,
-// backward 1185 (1.39), both passes 1.73 ms (1.43 PFLOP/s: the SM clock under
-// the power cap decides); those of 4096 tokens, 5120 x 20480 5.08 - 5.10 ms
-// (1.52). 16384 tokens, 768 x 2048: 0.43 ms (1.07); 65536 tokens, 256 x 704,
+// backward 1185 (1.39), both passes 1.65 - 1.77 ms (1.50 - 1.40 PFLOP/s: the SM
+// clock under the power cap decides); those of 4096 tokens, 5120 x 20480 4.87 -
+// 5.20 ms (1.59 - 1.49). 16384 tokens, 768 x 2048: 0.43 ms (1.07); 65536 tokens, 256 x 704,
 // where the tensors' bytes weigh more: 0.66 ms. Each launch alone (8192 tokens,
 // 2048 x 8192): GLU 314 us (1.75 PFLOP/s, with 400 MB of g and u written), down
 // 193 (1.43), DGLU 198 (1.39, 790 MB moved), gradients 870 (1.58); the tensor
