@@ -1,0 +1,82 @@
+/*
+ * prm_attention.h -- C ABI of libprm, third part: the operators of a
+ * transformer block's attention half, forward and backward, on one GB300 GPU:
+ *
+ *   projection          linear layer with bias, activation and residual; its
+ *                       matrix is PR-Muon's, its bias AdamW's
+ *   cross attention     of tokens to an encoder's states (or to the tokens
+ *                       themselves: no order among the keys is assumed)
+ *   rotary positions    of queries and keys
+ *   dropout             its mask is computed, never stored
+ *
+ * Conventions are prm.h's and prm_blocks.h's: PRM_OK or a PRM_ERR_* code,
+ * device pointers on the current device, `void*` streams, the caller owns
+ * every buffer (workspaces included), work is enqueued asynchronously. Calls
+ * with nothing to do return PRM_OK; pointers may then be NULL. Sums are held
+ * in fp32 and taken in an order fixed by the sizes: the same inputs give the
+ * same bits. The first call of each kind on a device sets kernels up: make it
+ * before any stream capture. Calls on different streams may overlap when
+ * their outputs and workspaces differ. prm_blocks_sync_status reads the error
+ * word of these calls too.
+ */
+#ifndef PRM_ATTENTION_H
+#define PRM_ATTENTION_H
+
+#include "prm_blocks.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* ---- rotary positions ---------------------------------------------------
+ * For every token and head the pairs (a, b) of the first `dim` of its `head`
+ * elements are turned by the token's angle:
+ *   (a, b) -> amplitude (a cos - b sin, b cos + a sin)
+ * and the elements behind `dim` are copied. PRM_ROTARY_HALF pairs element i
+ * with i + dim / 2, PRM_ROTARY_INTERLEAVED 2 i with 2 i + 1.
+ * The angle is position * turns[i] / 2^64 of a full turn: turns[i] is the
+ * pair's turns per position as a 64-bit fraction, and the product, taken
+ * modulo 2^64, is exact, however far the position. */
+#define PRM_ROTARY_HALF        0
+#define PRM_ROTARY_INTERLEAVED 1
+
+typedef struct {
+  int64_t samples, tokens, heads;           /* x and y: samples x tokens x heads x head */
+  int64_t head, dim;                        /* elements of a head, those of them that turn (even) */
+  int64_t x_sample, x_token, x_head;        /* strides of x in elements; a head's elements are consecutive */
+  int64_t y_sample, y_token, y_head;        /* those of y */
+  int64_t position_sample, position_token;  /* strides of the positions in elements */
+  int32_t position_bytes;                   /* 8 (int64) or 4 (int32) */
+  int32_t layout;                           /* PRM_ROTARY_* */
+  int32_t dtype;                            /* of x and y */
+  int32_t inverse;                          /* not 0: turns by minus the angle (the gradient's way back) */
+  float amplitude;
+  int32_t reserved;                         /* must be 0 */
+} prm_rotary_desc;
+
+/* y may be x (with x's strides), otherwise the two do not overlap. Any
+ * alignment; vectors are as wide as strides, dim and pointers allow.
+ * Errors: INVALID_ARG, SHAPE, UNSUPPORTED, CUDA. */
+PRM_API int prm_rotary(const prm_rotary_desc* desc, const void* x, const void* positions, const uint64_t* turns,
+                       void* y, void* stream);
+
+/* ---- dropout ------------------------------------------------------------
+ *   y[i] = residual[i] + (kept(i) ? x[i] / (1 - p) : 0)
+ * kept(i): word i % 4 of the ten-round Philox 4x32 block (Salmon, Moraes,
+ * Dror and Shaw, 2011) of counter offset + i / 4 (64 bits, the upper 64 zero)
+ * and the key seed, is at least p 2^32. The backward pass is the same call on
+ * dy without a residual. seed_device: where not NULL, the key is read from
+ * there when the kernel runs (a captured graph can have another mask at each
+ * replay) and `seed` is ignored.
+ * x: n elements of dtype; residual (or NULL) and y: of y_dtype, which is dtype,
+ * or PRM_FP32 with a residual and a 16-bit x, or 16 bits wide without one and an
+ * fp32 x (that sum's way back). y may be x or residual where the types are
+ * the same. p in [0, 1]. Any alignment. Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+PRM_API int prm_dropout(const void* x, int dtype, const void* residual, void* y, int y_dtype, int64_t n, double p,
+                        uint64_t seed, const uint64_t* seed_device, uint64_t offset, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* PRM_ATTENTION_H */

@@ -2,11 +2,12 @@
 
 Next to the optimizer, the operators of a transformer block whose parameters
 it updates, forward and backward: the gated feed-forward block, the norms
-around a block and the token embedding.
+around a block and the token embedding; and for the attention half the rotary
+positions and dropout.
 
 The compute lives in libprm.so (CUDA kernels for sm_103a behind a C ABI,
-declared in include/prm.h and include/prm_blocks.h); this package only binds it. Build the library
-with `python -m matrix_aware_optimizer_gb300.build`.
+declared in include/prm.h, include/prm_blocks.h and include/prm_attention.h);
+this package only binds it. Build the library with `python -m matrix_aware_optimizer_gb300.build`.
 """
 from . import native  # noqa: F401
 from .native import PrmError, prm_branch  # noqa: F401
@@ -14,6 +15,7 @@ from .native import PrmError, prm_branch  # noqa: F401
 
 _BLOCKS = ("gated_ffn", "gated_ffn_backward", "block_norm", "block_norm_backward", "embedding",
            "embedding_backward", "blocks_sync_status")
+_ATTENTION = ("RotaryPlan", "rotary_plan", "rotary", "rotary_backward", "dropout", "dropout_backward")
 
 
 def __getattr__(name):
@@ -22,6 +24,8 @@ def __getattr__(name):
         from . import optimizer as module
     elif name in _BLOCKS:
         from . import blocks as module
+    elif name in _ATTENTION:
+        from . import attention as module
     else:
         raise AttributeError(name)
     value = globals()[name] = getattr(module, name)

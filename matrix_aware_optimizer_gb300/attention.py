@@ -1,0 +1,224 @@
+"""torch glue over include/prm_attention.h: the operators of a transformer
+block's attention half. As in blocks.py each is a forward and a backward call
+on tensors, outside autograd, on `stream` or the current one of the tensors'
+device; PyTorch supplies memory and the stream, every arithmetic step runs in
+libprm."""
+from __future__ import annotations
+
+import functools
+import math
+import struct
+from fractions import Fraction
+from typing import NamedTuple, Optional, Union
+
+import torch
+
+from . import native as N
+from .blocks import _DTYPE, _elsewhere, _is_elsewhere, _ptr, _raw_stream
+
+_ROTARY = struct.Struct("=13q4ifi")  # prm_rotary_desc
+assert _ROTARY.size == N.ctypes.sizeof(N.prm_rotary_desc)
+_LAYOUT = {"half": N.PRM_ROTARY_HALF, "interleaved": N.PRM_ROTARY_INTERLEAVED}
+
+
+# --------------------------------------------------------- rotary positions
+class RotaryPlan(NamedTuple):
+    """What rotary needs next to the positions: every pair's turns per
+    position as a 64-bit fraction of a turn (int64 bits, on the device), the
+    elements that turn, their layout and the amplitude."""
+    turns: torch.Tensor
+    dim: int
+    layout: str
+    amplitude: float
+
+
+_TAU = 2 * Fraction(31415926535897932384626433832795028841971693993751, 10 ** 49)
+
+
+@functools.lru_cache(maxsize=64)
+def _rotary_turns(dim, base, scaling, factor, trained_length, fast, slow):
+    if scaling == "base":
+        base *= factor ** (dim / max(dim - 2, 1))
+    turns = []
+    for i in range(dim // 2):
+        f = base ** (-2.0 * i / dim)
+        if scaling == "linear":
+            f /= factor
+        elif scaling == "ramp":
+            keep = min(max((trained_length * f / (2.0 * math.pi) - slow) / (fast - slow), 0.0), 1.0)
+            f = f * keep + f / factor * (1.0 - keep)
+        bits = round(Fraction(f) / _TAU * 2 ** 64) % 2 ** 64
+        turns.append(bits - 2 ** 64 if bits >= 2 ** 63 else bits)
+    return tuple(turns)
+
+
+def rotary_plan(dim: int, base: float = 10000.0, layout: str = "half", scaling: str = "none", factor: float = 1.0,
+                trained_length: int = 2048, fast: float = 32.0, slow: float = 1.0, amplitude: Optional[float] = None,
+                device: Union[str, torch.device] = "cuda") -> RotaryPlan:
+    """Plan for rotary positions over the first `dim` elements of a head, pair
+    i turning by base^(-2 i / dim) radians per position.
+
+    layout: "half" pairs element i with i + dim / 2, "interleaved" 2 i with
+    2 i + 1. scaling, for contexts `factor` times longer than the trained one:
+    "linear" divides every frequency by factor; "base" raises the base by
+    factor^(dim / (dim - 2)), which divides the slowest pair's frequency by
+    factor and leaves the fastest; "ramp" divides those of the pairs that turn
+    less than `slow` times over trained_length, leaves those above `fast` and
+    goes evenly from one to the other between them, with an amplitude of
+    0.1 ln(factor) + 1 unless one is given (1 otherwise).
+    """
+    if dim < 2 or dim % 2:
+        raise ValueError("dim must be even and positive")
+    if layout not in _LAYOUT:
+        raise ValueError(f"layout must be one of {sorted(_LAYOUT)}")
+    if scaling not in ("none", "linear", "base", "ramp"):
+        raise ValueError("scaling must be none, linear, base or ramp")
+    if not (base > 0.0 and factor > 0.0 and math.isfinite(base) and math.isfinite(factor)):
+        raise ValueError("base and factor must be positive")
+    if scaling == "ramp" and not (0.0 <= slow < fast and trained_length > 0):
+        raise ValueError("ramp needs 0 <= slow < fast and a trained length")
+    if amplitude is None:
+        amplitude = 0.1 * math.log(factor) + 1.0 if scaling == "ramp" and factor > 1.0 else 1.0
+    if not math.isfinite(amplitude):
+        raise ValueError("amplitude must be finite")
+    turns = _rotary_turns(dim, float(base), scaling, float(factor), trained_length, fast, slow)
+    return RotaryPlan(torch.tensor(turns, dtype=torch.int64, device=device), dim, layout, float(amplitude))
+
+
+def _strides3(t):
+    """Strides of [samples, tokens, heads, head], or None where the elements
+    of a head are not consecutive."""
+    s = t.stride()
+    return s[:3] if s[3] == 1 or t.shape[3] == 1 else None
+
+
+def _distinct(t) -> bool:
+    """Whether no two elements of t share memory."""
+    reach = 1
+    for stride, extent in sorted((s, e) for s, e in zip(t.stride(), t.shape) if e > 1):
+        if stride < reach:
+            return False
+        reach = stride * (extent - 1) + reach
+    return True
+
+
+def _rotate(x, positions, plan, out, inverse, stream):
+    device = x.get_device()
+    if device < 0 or x.dtype not in _DTYPE or x.dim() not in (3, 4):
+        raise ValueError("x must be a [samples,] tokens x heads x head CUDA tensor of float32, bfloat16 or float16")
+    if positions.dtype not in (torch.int64, torch.int32) or positions.get_device() != device:
+        raise ValueError("positions must be int64 or int32, on x's device")
+    if plan.turns.get_device() != device or plan.turns.shape != (plan.dim // 2,) \
+            or plan.turns.dtype is not torch.int64 or not plan.turns.is_contiguous():
+        raise ValueError("plan must come from rotary_plan, on x's device")
+    if plan.dim > x.shape[-1]:
+        raise ValueError("the plan turns more elements than a head has")
+    if positions.dim() > x.dim() - 2 or any(a != b and a != 1 for a, b in
+                                            zip(positions.shape[::-1], x.shape[:-2][::-1])):
+        raise ValueError("positions must have x's samples and tokens, or broadcast to them")
+    if out is not None and (out.shape != x.shape or out.dtype is not x.dtype or out.get_device() != device
+                            or (out.stride(-1) != 1 and out.shape[-1] > 1) or not _distinct(out)):
+        raise ValueError("out must have x's shape, type and device, consecutive elements and no shared memory")
+    if _is_elsewhere(device, stream):
+        with _elsewhere(device, stream, x, positions, plan.turns, out):
+            return _rotate(x, positions, plan, out, inverse, None)
+    if x.numel() == 0:
+        return torch.empty_like(x) if out is None else out
+    x4 = x if x.dim() == 4 else x.unsqueeze(0)
+    xs = _strides3(x4)
+    if xs is None:
+        x4 = x4.contiguous()
+        xs = _strides3(x4)
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
+    if out is not None and out.data_ptr() == x4.data_ptr() and any(
+            a != b and e > 1 for a, b, e in zip(out.stride(), x.stride(), x.shape)):
+        raise ValueError("out shares x's memory with other strides")
+    ys = _strides3(y if x.dim() == 4 else y.unsqueeze(0))
+    samples, tokens, heads, head = x4.shape
+    ps = positions.expand(x.shape[:-2]).stride()
+    packed = _ROTARY.pack(samples, tokens, heads, head, plan.dim, *xs, *ys, ps[0] if len(ps) == 2 else 0, ps[-1],
+                          positions.element_size(), _LAYOUT[plan.layout], _DTYPE[x.dtype], 1 if inverse else 0,
+                          plan.amplitude, 0)
+    rc = N.load().prm_rotary(N.prm_rotary_desc.from_buffer_copy(packed), x4.data_ptr(), positions.data_ptr(),
+                             plan.turns.data_ptr(), y.data_ptr(), _raw_stream(device))
+    if rc:
+        N.check(rc, "prm_rotary")
+    return y
+
+
+def rotary(x: torch.Tensor, positions: torch.Tensor, plan: RotaryPlan, out: Optional[torch.Tensor] = None,
+           stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Turns the pairs of every head by its token's position.
+
+    x: [tokens, heads, head] or [samples, tokens, heads, head], fp32, bf16 or
+    fp16, with any strides (a slice of a qkv projection, say: queries and keys
+    that lie side by side are heads of one call). positions: int64 or int32 of
+    x's samples and tokens, or broadcasting to them; any 64-bit value. out: where
+    the result goes; x itself turns it in place (elements behind plan.dim are
+    then not touched), other tensors that overlap x are the caller's mistake.
+    """
+    return _rotate(x, positions, plan, out, False, stream)
+
+
+def rotary_backward(dy: torch.Tensor, positions: torch.Tensor, plan: RotaryPlan, out: Optional[torch.Tensor] = None,
+                    stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Gradient of rotary's x from that of its result: the turn back, with the
+    same amplitude. Arguments as rotary's."""
+    return _rotate(dy, positions, plan, out, True, stream)
+
+
+# ------------------------------------------------------------------ dropout
+def dropout(x: torch.Tensor, p: float, seed: Union[int, torch.Tensor], offset: int = 0,
+            residual: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """residual + x / (1 - p) where an element is kept, residual (or 0) where it
+    is dropped, which happens with probability p.
+
+    x: fp32, bf16 or fp16; residual: of x's shape and type, or fp32; the result
+    is of the residual's type. The mask follows from seed, offset and the
+    element's index in x (row-major) alone; no mask is kept: dropout_backward
+    with the same seed and offset has the same one. The next call's mask is
+    fresh with another seed, or with an offset that is larger by a quarter of x's
+    elements, rounded up. seed: an integer, or an int64 CUDA tensor of one element that
+    is read when the kernel runs, so that a captured graph can draw another mask
+    at each replay.
+    """
+    return _drop(x, p, seed, offset, residual, x.dtype if residual is None else residual.dtype, stream)
+
+
+def _drop(x, p, seed, offset, residual, dtype, stream):
+    device = x.get_device()
+    if device < 0 or x.dtype not in _DTYPE:
+        raise ValueError("x must be a CUDA tensor of float32, bfloat16 or float16")
+    if not 0.0 <= p <= 1.0:
+        raise ValueError("p must be in [0, 1]")
+    if residual is not None and (residual.shape != x.shape or residual.get_device() != device
+                                 or dtype not in (x.dtype, torch.float32)):
+        raise ValueError("residual must have x's shape and device, and its type or float32")
+    on_device = isinstance(seed, torch.Tensor)
+    if on_device and (seed.dtype is not torch.int64 or seed.numel() != 1 or seed.get_device() != device):
+        raise ValueError("a seed tensor must be one int64 element on x's device")
+    if _is_elsewhere(device, stream):
+        with _elsewhere(device, stream, x, residual, seed if on_device else None):
+            return _drop(x, p, seed, offset, residual, dtype, None)
+    if not x.is_contiguous():
+        x = x.contiguous()
+    if residual is not None and not residual.is_contiguous():
+        residual = residual.contiguous()
+    y = torch.empty(x.shape, dtype=dtype, device=x.device)
+    rc = N.load().prm_dropout(x.data_ptr(), _DTYPE[x.dtype], _ptr(residual), y.data_ptr(), _DTYPE[dtype], x.numel(), p,
+                              0 if on_device else seed & 0xFFFFFFFFFFFFFFFF, seed.data_ptr() if on_device else None,
+                              offset & 0xFFFFFFFFFFFFFFFF, _raw_stream(device))
+    if rc:
+        N.check(rc, "prm_dropout")
+    return y
+
+
+def dropout_backward(dy: torch.Tensor, p: float, seed: Union[int, torch.Tensor], offset: int = 0,
+                     dtype: Optional[torch.dtype] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Gradient of dropout's x: dy / (1 - p) where the element was kept, else 0.
+    p, seed and offset as in the forward call (a seed tensor must hold what it
+    held then). dtype: x's type where it is not dy's, a 16-bit x that joined an
+    fp32 residual. The residual's gradient is dy itself."""
+    if dtype is not None and dtype is not dy.dtype and (dtype not in _DTYPE or dy.dtype is not torch.float32):
+        raise ValueError("dtype must be dy's, or a 16-bit type where dy is float32")
+    return _drop(dy, p, seed, offset, None, dy.dtype if dtype is None else dtype, stream)

@@ -1,4 +1,4 @@
-"""ctypes binding of libprm (include/prm.h, include/prm_blocks.h): the same entry points under the
+"""ctypes binding of libprm (include/prm.h, prm_blocks.h, prm_attention.h): the same entry points under the
 same names, argument marshalling only. Every step of the optimizer runs in the
 library's CUDA kernels; there is no Python or CPU fallback, and loading fails
 loudly when the shared library has not been built."""
@@ -6,7 +6,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_char_p, c_float, c_int, c_int32, c_int64, c_size_t, c_uint16, c_void_p
+from ctypes import POINTER, c_char_p, c_float, c_int, c_int32, c_int64, c_size_t, c_uint16, c_uint64, c_void_p
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libprm.so")
 
@@ -42,6 +42,8 @@ PRM_ACT_GELU = 1
 PRM_ACT_GELU_TANH = 2
 PRM_NORM_RMS = 0
 PRM_NORM_LAYER = 1
+PRM_ROTARY_HALF = 0
+PRM_ROTARY_INTERLEAVED = 1
 
 ERROR_NAMES = {
     PRM_OK: "OK", PRM_ERR_INVALID_ARG: "INVALID_ARG", PRM_ERR_SHAPE: "SHAPE",
@@ -87,7 +89,31 @@ class prm_block_norm_desc(ctypes.Structure):
     ]
 
 
-# name -> (restype, argtypes), mirroring include/prm.h and include/prm_blocks.h
+class prm_rotary_desc(ctypes.Structure):
+    _fields_ = [
+        ("samples", c_int64),
+        ("tokens", c_int64),
+        ("heads", c_int64),
+        ("head", c_int64),
+        ("dim", c_int64),
+        ("x_sample", c_int64),
+        ("x_token", c_int64),
+        ("x_head", c_int64),
+        ("y_sample", c_int64),
+        ("y_token", c_int64),
+        ("y_head", c_int64),
+        ("position_sample", c_int64),
+        ("position_token", c_int64),
+        ("position_bytes", c_int32),
+        ("layout", c_int32),
+        ("dtype", c_int32),
+        ("inverse", c_int32),
+        ("amplitude", c_float),
+        ("reserved", c_int32),
+    ]
+
+
+# name -> (restype, argtypes), mirroring include/prm.h, include/prm_blocks.h and include/prm_attention.h
 SIGNATURES = {
     "prm_create": (c_int, [POINTER(c_void_p), c_int]),
     "prm_destroy": (c_int, [c_void_p]),
@@ -138,6 +164,9 @@ SIGNATURES = {
     "prm_embedding_backward_workspace": (c_int, [c_int64, c_int64, c_int64, POINTER(c_size_t)]),
     "prm_embedding_backward": (c_int, [c_void_p, c_int, c_void_p, c_int, c_void_p, c_int, c_int, c_int64, c_int64,
                                        c_int64, c_float, c_void_p, c_size_t, c_void_p]),
+    "prm_rotary": (c_int, [POINTER(prm_rotary_desc), c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
+    "prm_dropout": (c_int, [c_void_p, c_int, c_void_p, c_void_p, c_int, c_int64, ctypes.c_double, c_uint64, c_void_p,
+                            c_uint64, c_void_p]),
 }
 
 _lib = None

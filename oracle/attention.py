@@ -1,0 +1,55 @@
+"""fp64 restatement of the operators of a block's attention half: the
+projection, cross attention, rotary positions and dropout, forward and
+backward. Like the rest of this package it shares no code with the library."""
+import math
+from fractions import Fraction
+
+import numpy as np
+
+
+
+# ------------------------------------------------------- rotary positions
+def rotary(x, positions, inv_freq, layout, amplitude=1.0, inverse=False):
+    """x: [samples, tokens, heads, head]; positions: [samples, tokens] ints;
+    inv_freq: radians per position of every pair. Angles are reduced as exact
+    rationals, so that far positions lose nothing."""
+    out = np.array(x, dtype=np.float64)
+    two_pi = 2 * Fraction(31415926535897932384626433832795028841971693993751, 10 ** 49)
+    half = len(inv_freq)
+    for b in range(x.shape[0]):
+        for t in range(x.shape[1]):
+            for i, f in enumerate(inv_freq):
+                angle = float((int(positions[b, t]) * Fraction(float(f))) % two_pi)
+                c, s = amplitude * math.cos(angle), amplitude * math.sin(angle) * (-1.0 if inverse else 1.0)
+                p, q = (i, i + half) if layout == "half" else (2 * i, 2 * i + 1)
+                u, v = x[b, t, :, p], x[b, t, :, q]
+                out[b, t, :, p] = u * c - v * s
+                out[b, t, :, q] = v * c + u * s
+    return out
+
+
+# ---------------------------------------------------------------- dropout
+def philox(counter, key):
+    """The four words of one block: ten rounds, counter of 64 bits (the upper
+    64 zero), key of 64 bits."""
+    low = 0xFFFFFFFF
+    c = [counter & low, counter >> 32 & low, 0, 0]
+    k = [key & low, key >> 32 & low]
+    for _ in range(10):
+        p, q = 0xD2511F53 * c[0], 0xCD9E8D57 * c[2]
+        c = [q >> 32 ^ c[1] ^ k[0], q & low, p >> 32 ^ c[3] ^ k[1], p & low]
+        k = [(k[0] + 0x9E3779B9) & low, (k[1] + 0xBB67AE85) & low]
+    return c
+
+
+def kept(n, p, seed, offset=0):
+    """Which of n elements dropout keeps."""
+    words = [w for i in range((n + 3) // 4) for w in philox((offset + i) % 2 ** 64, seed % 2 ** 64)]
+    limit = int(math.floor(p * 2 ** 32 + 0.5))
+    return np.array([w >= limit for w in words[:n]], dtype=bool)
+
+
+def dropout(x, p, seed, offset=0, residual=None):
+    keep = kept(x.size, p, seed, offset).reshape(x.shape)
+    y = np.where(keep, x / (1.0 - p) if p < 1.0 else 0.0, 0.0)
+    return y if residual is None else y + residual
