@@ -75,6 +75,53 @@ PRM_API int prm_rotary(const prm_rotary_desc* desc, const void* x, const void* p
 PRM_API int prm_dropout(const void* x, int dtype, const void* residual, void* y, int y_dtype, int64_t n, double p,
                         uint64_t seed, const uint64_t* seed_device, uint64_t offset, void* stream);
 
+/* ---- cross attention ----------------------------------------------------
+ * For every sequence b, query token t and head h, over the first
+ * key_lengths[b] keys (all of them where key_lengths is NULL):
+ *   S = scale q . k,  P = softmax(S),  o = sum P v
+ * q, o: batch x queries x heads x head; k, v: batch x keys x kv_heads x head;
+ * kv_heads divides heads: heads / kv_heads query heads that lie next to each
+ * other share a key head. All of one 16-bit type; head is a multiple of 8, 8 ..
+ * 128. Each tensor has its own strides in elements, multiples of 8 (those of
+ * extents of one are ignored), and starts on 16 bytes; a head's elements are
+ * consecutive. A row without keys (key_lengths[b] <= 0, or keys 0) gives o = 0
+ * and gradients of 0. Keys and values behind the last key are not used,
+ * whatever they hold; a length above `keys` means all of them.
+ * P and (backward) dS are rounded to 16 bits as operands of the next product;
+ * the row sums are of unrounded values. */
+typedef struct {
+  int64_t batch, token, head;
+} prm_attention_strides;
+
+typedef struct {
+  int64_t batch, queries, keys, heads, kv_heads, head;
+  prm_attention_strides q, k, v, o;
+  prm_attention_strides grad_o, dq, dk, dv; /* backward only */
+  const void* key_lengths;                  /* batch integers on the device, or NULL */
+  int32_t length_bytes;                     /* 8 (int64) or 4 (int32) */
+  int32_t dtype;                            /* PRM_BF16 or PRM_FP16 */
+  float scale;                              /* > 0 */
+  int32_t reserved;                         /* must be 0 */
+} prm_attention_desc;
+
+/* Bytes of the two passes' workspaces (256-byte aligned buffers). Depends on
+ * the sizes alone. Errors: INVALID_ARG, SHAPE, UNSUPPORTED. */
+PRM_API int prm_attention_workspace(const prm_attention_desc* desc, size_t* forward, size_t* backward);
+
+/* lse: batch x heads x queries fp32, the base-2 logarithm of each row's sum of
+ * 2^(S log2 e) (-inf for a row without keys), for the backward pass, or NULL.
+ * Errors: INVALID_ARG, SHAPE, ALIGNMENT, WORKSPACE, UNSUPPORTED, CUDA. */
+PRM_API int prm_attention_forward(const prm_attention_desc* desc, const void* q, const void* k, const void* v, void* o,
+                                  float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* From grad_o (of o), with the o and lse of the forward pass:
+ *   dv = P^T grad_o,  dP = grad_o v^T,  dS = P (dP - rowsum(grad_o o)),  dq = scale dS k,  dk = scale dS^T q
+ * dk and dv of shared heads are sums over the query heads; rows behind the
+ * last key are set to zero. Nothing is added with atomics. Errors as above. */
+PRM_API int prm_attention_backward(const prm_attention_desc* desc, const void* grad_o, const void* q, const void* k,
+                                   const void* v, const void* o, const float* lse, void* dq, void* dk, void* dv,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -9,15 +9,17 @@ import functools
 import math
 import struct
 from fractions import Fraction
-from typing import NamedTuple, Optional, Union
+from typing import NamedTuple, Optional, Sequence, Union
 
 import torch
 
 from . import native as N
-from .blocks import _DTYPE, _elsewhere, _is_elsewhere, _ptr, _raw_stream
+from .blocks import _DTYPE, _HALF, _elsewhere, _is_elsewhere, _ptr, _raw_stream
 
 _ROTARY = struct.Struct("=13q4ifi")  # prm_rotary_desc
 assert _ROTARY.size == N.ctypes.sizeof(N.prm_rotary_desc)
+_ATTN = struct.Struct("=30qQ2ifi")  # prm_attention_desc
+assert _ATTN.size == N.ctypes.sizeof(N.prm_attention_desc)
 _LAYOUT = {"half": N.PRM_ROTARY_HALF, "interleaved": N.PRM_ROTARY_INTERLEAVED}
 
 
@@ -222,3 +224,161 @@ def dropout_backward(dy: torch.Tensor, p: float, seed: Union[int, torch.Tensor],
     if dtype is not None and dtype is not dy.dtype and (dtype not in _DTYPE or dy.dtype is not torch.float32):
         raise ValueError("dtype must be dy's, or a 16-bit type where dy is float32")
     return _drop(dy, p, seed, offset, None, dy.dtype if dtype is None else dtype, stream)
+
+
+# ---------------------------------------------------------- cross attention
+class AttentionSaved(NamedTuple):
+    """What cross_attention leaves for its backward pass: every row's base-2
+    logarithm of its sum [batch, heads, queries], and the scale and key count
+    of the pass."""
+    lse: torch.Tensor
+    scale: float
+    keys: int
+
+
+_NO_STRIDES = (0, 0, 0)
+
+
+def _usable(t) -> bool:
+    """Whether the library reads (or writes) t as it lies: consecutive
+    elements, rows of 16-byte units that do not overlap."""
+    if t.stride(3) != 1 or t.data_ptr() % 16:
+        return False
+    head = t.shape[3]
+    for s, e in zip(t.stride()[:3], t.shape):
+        if e > 1 and (s < head or s % 8):
+            return False
+    return True
+
+
+def _laid_out(t):
+    return t if t.numel() == 0 or _usable(t) else t.clone(memory_format=torch.contiguous_format)
+
+
+def _attention_check(q, k, v, key_lengths, scale):
+    dt, device = q.dtype, q.get_device()
+    if dt not in _HALF or device < 0:
+        raise ValueError("q must be a bfloat16 or float16 CUDA tensor")
+    if q.dim() != 4 or k.dim() != 4 or v.shape != k.shape or q.shape[0] != k.shape[0] or q.shape[3] != k.shape[3]:
+        raise ValueError("q must be batch x queries x heads x head, k and v batch x keys x kv_heads x head")
+    if k.dtype is not dt or v.dtype is not dt or k.get_device() != device or v.get_device() != device:
+        raise ValueError("k and v must be of q's type and on its device")
+    head = q.shape[3]
+    if head % 8 or not 8 <= head <= 128:
+        raise ValueError("a head must have 8 to 128 elements, a multiple of 8")
+    if k.shape[2] == 0 and q.shape[2] or k.shape[2] and q.shape[2] % k.shape[2]:
+        raise ValueError("kv_heads must divide heads")
+    if key_lengths is not None and (key_lengths.shape != (q.shape[0],) or key_lengths.get_device() != device
+                                    or key_lengths.dtype not in (torch.int32, torch.int64)):
+        raise ValueError("key_lengths must be int32 or int64, one per sequence, on q's device")
+    if scale is None:
+        scale = head ** -0.5
+    if not (scale > 0.0 and math.isfinite(scale)):
+        raise ValueError("scale must be positive")
+    return device, scale
+
+
+def _attention_desc(q, k, v, o, key_lengths, scale, grad_o=None, dq=None, dk=None, dv=None):
+    b, lq, h, d = q.shape
+    strides = []
+    for t in (q, k, v, o, grad_o, dq, dk, dv):
+        strides += _NO_STRIDES if t is None else t.stride()[:3]
+    packed = _ATTN.pack(b, lq, k.shape[1], h, k.shape[2], d, *strides,
+                        0 if key_lengths is None else key_lengths.data_ptr(),
+                        0 if key_lengths is None else key_lengths.element_size(), _DTYPE[q.dtype], scale, 0)
+    return N.prm_attention_desc.from_buffer_copy(packed)
+
+
+@functools.lru_cache(maxsize=256)
+def _attention_sizes(b, lq, lk, h, hkv, d):
+    desc = N.prm_attention_desc(batch=b, queries=lq, keys=lk, heads=h, kv_heads=hkv, head=d, dtype=N.PRM_BF16, scale=1.0)
+    forward, backward = N.c_size_t(), N.c_size_t()
+    N.check(N.load().prm_attention_workspace(desc, forward, backward), "prm_attention_workspace")
+    return forward.value, backward.value
+
+
+def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, key_lengths: Optional[torch.Tensor] = None,
+                    scale: Optional[float] = None, out: Optional[torch.Tensor] = None, save: bool = False,
+                    stream: Optional[torch.cuda.Stream] = None):
+    """softmax(scale q k^T) v of every query over its sequence's first
+    key_lengths[b] keys.
+
+    q: [batch, queries, heads, head]; k, v: [batch, keys, kv_heads, head], bf16
+    or fp16, with any strides (slices of fused projections); kv_heads divides
+    heads, heads / kv_heads neighbouring query heads share a key head; head:
+    8 to 128, a multiple of 8. The states may be of any other length than the
+    queries, one query token included; with q, k and v of the same tokens this
+    is self-attention without an order. key_lengths: int32 or int64 [batch], None
+    for all keys; what lies behind a sequence's last key is never used, and a
+    sequence without keys gives zeros. scale: head^-0.5 by default. out: where
+    the result goes.
+
+    Returns o, or (o, saved) with save=True, saved for
+    cross_attention_backward (autograd does not see the call).
+    """
+    device, scale = _attention_check(q, k, v, key_lengths, scale)
+    if out is not None and (out.shape != q.shape or out.dtype is not q.dtype or out.get_device() != device
+                            or not (_usable(out) and _distinct(out))):
+        raise ValueError("out must have q's shape, type and device, consecutive elements and 16-byte rows")
+    if _is_elsewhere(device, stream):
+        with _elsewhere(device, stream, q, k, v, key_lengths, out):
+            return cross_attention(q, k, v, key_lengths, scale, out, save)
+    b, lq, h, d = q.shape
+    lk, hkv = k.shape[1], k.shape[2]
+    q, k, v = _laid_out(q), _laid_out(k), _laid_out(v)
+    if key_lengths is not None and not key_lengths.is_contiguous():
+        key_lengths = key_lengths.contiguous()
+    o = torch.empty(q.shape, dtype=q.dtype, device=q.device) if out is None else out
+    lse = q.new_empty((b, h, lq), dtype=torch.float32) if save else None
+    n_ws = _attention_sizes(b, lq, lk, h, hkv, d)[0]
+    ws = q.new_empty(n_ws, dtype=torch.uint8) if n_ws else None
+    rc = N.load().prm_attention_forward(_attention_desc(q, k, v, o, key_lengths, scale), q.data_ptr(), k.data_ptr(),
+                                        v.data_ptr(), o.data_ptr(), _ptr(lse), _ptr(ws), n_ws, _raw_stream(device))
+    if rc:
+        N.check(rc, "prm_attention_forward")
+    return (o, AttentionSaved(lse, scale, lk)) if save else o
+
+
+def cross_attention_backward(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
+                             saved: AttentionSaved, key_lengths: Optional[torch.Tensor] = None,
+                             scale: Optional[float] = None, grads: Optional[Sequence[torch.Tensor]] = None,
+                             stream: Optional[torch.cuda.Stream] = None):
+    """Gradients of cross_attention: (dq, dk, dv), all of q's type, from that
+    of its result and the o and saved that it returned; the other arguments are
+    those of that pass. Heads that share keys add to the same dk and dv; rows
+    behind a sequence's last key are zero. grads: three tensors to write them
+    into (slices of a fused projection's gradient, say).
+    """
+    device, scale = _attention_check(q, k, v, key_lengths, scale)
+    for t in (do, o):
+        if t.shape != q.shape or t.dtype is not q.dtype or t.get_device() != device:
+            raise ValueError("do and o must have q's shape, type and device")
+    b, lq, h, d = q.shape
+    lk, hkv = k.shape[1], k.shape[2]
+    lse = saved.lse
+    if lse.shape != (b, h, lq) or lse.dtype is not torch.float32 or lse.get_device() != device             or not lse.is_contiguous() or saved.scale != scale or saved.keys != lk:
+        raise ValueError("saved does not belong to this pass")
+    if grads is not None:
+        for g, t in zip(grads, (q, k, v), strict=True):
+            if g.shape != t.shape or g.dtype is not t.dtype or g.get_device() != device                     or (g.numel() and not (_usable(g) and _distinct(g))):
+                raise ValueError("grads must have the shapes and type of q, k and v, consecutive elements and "
+                                 "16-byte rows")
+    if _is_elsewhere(device, stream):
+        with _elsewhere(device, stream, do, q, k, v, o, lse, key_lengths, *(grads or ())):
+            return cross_attention_backward(do, q, k, v, o, saved, key_lengths, scale, grads)
+    do, q, k, v, o = (_laid_out(t) for t in (do, q, k, v, o))
+    if key_lengths is not None and not key_lengths.is_contiguous():
+        key_lengths = key_lengths.contiguous()
+    if grads is None:
+        dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
+    else:
+        dq, dk, dv = grads
+    n_ws = _attention_sizes(b, lq, lk, h, hkv, d)[1]
+    ws = q.new_empty(n_ws, dtype=torch.uint8)
+    desc = _attention_desc(q, k, v, o, key_lengths, scale, do, dq, dk, dv)
+    rc = N.load().prm_attention_backward(desc, do.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+                                         lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(),
+                                         n_ws, _raw_stream(device))
+    if rc:
+        N.check(rc, "prm_attention_backward")
+    return dq, dk, dv

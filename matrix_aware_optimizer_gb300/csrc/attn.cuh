@@ -1,0 +1,230 @@
+// Shared by the attention kernels (attn_fwd.cu, attn_bwd.cu, attn_few.cu):
+// tensor memory access, products whose left operand lies in tensor memory,
+// tiles of 128 rows by TMA, and how heads and rows are laid out.
+#pragma once
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <atomic>
+
+#include "blocks.cuh"
+#include "prm_attention.h"
+
+namespace prm {
+
+// ---------------------------------------------------------- tensor memory
+// 32 lanes x n fp32 columns: thread i of the warp gets columns [col, col + n)
+// of lane (lane_base + i); load and wait are one statement.
+__device__ __forceinline__ void tmem_load_16cols(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_load_64cols(uint32_t taddr, float (&v)[64]) {
+  uint32_t r[64];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, "
+      "%20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, "
+      "%38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, "
+      "%56, %57, %58, %59, %60, %61, %62, %63"
+      "}, [%64];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// 32 lanes x n words, the other way; tmem_store_wait() before they are read.
+__device__ __forceinline__ void tmem_store_16cols(uint32_t taddr, const uint32_t (&w)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {"
+      "%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16"
+      "};" ::"r"(taddr),
+      "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"(w[8]),
+        "r"(w[9]), "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_store_32cols(uint32_t taddr, const uint32_t (&w)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {"
+      "%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, "
+      "%20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32"
+      "};" ::"r"(taddr),
+      "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"(w[8]),
+        "r"(w[9]), "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15]), "r"(w[16]),
+        "r"(w[17]), "r"(w[18]), "r"(w[19]), "r"(w[20]), "r"(w[21]), "r"(w[22]), "r"(w[23]), "r"(w[24]),
+        "r"(w[25]), "r"(w[26]), "r"(w[27]), "r"(w[28]), "r"(w[29]), "r"(w[30]), "r"(w[31])
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D[tmem] (+)= A[tmem] * B[smem]: row i of A in lane i, two 16-bit elements
+// of K to a column.
+__device__ __forceinline__ void umma_tmem_a(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* tm, uint64_t* bar, int x, int y, int z,
+                                            int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+
+// 2^v, to 2 ulp; 0 for -inf.
+__device__ __forceinline__ float exp2_fast(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// ------------------------------------------------------------------ tiles
+// A tile is 128 rows (tokens, or keys) of a head, as DP / 64 chunks of 64
+// elements; a chunk's rows are 128 bytes, swizzled by TMA. Elements from the
+// head's end to DP are zero.
+constexpr int ATT_ROWS = 128;
+constexpr uint32_t ATT_CHUNK = ATT_ROWS * 128;
+template <int DP>
+constexpr uint32_t ATT_TILE = DP / 64 * ATT_CHUNK;
+constexpr uint64_t ATT_WAIT_NS = 2000000000ull;
+
+constexpr int ATT_THREADS = 320;  // warps 0-3 and 4-7 take rows, 8 loads, 9 issues products
+
+template <int DP>
+__device__ __forceinline__ void att_load_tile(uint8_t* dst, const CUtensorMap* tm, uint64_t* bar, int head, int row,
+                                              int batch) {
+#pragma unroll
+  for (int c = 0; c < DP / 64; ++c) tma_load_4d(dst + c * ATT_CHUNK, tm, bar, c * 64, head, row, batch);
+}
+
+// D[128 x 128] = A B^T, both tiles along their elements, `steps` of 16.
+__device__ __forceinline__ void att_mma_rows(uint32_t d, const uint8_t* a, const uint8_t* b, int steps,
+                                             uint32_t idesc) {
+  const uint32_t sa = smem_u32(a), sb = smem_u32(b);
+#pragma unroll 1
+  for (int k = 0; k < steps; ++k) {
+    const uint32_t off = (k >> 2) * ATT_CHUNK + (k & 3) * 32;
+    umma_bf16(d, smem_desc_sw128(sa + off, 16, 1024), smem_desc_sw128(sb + off, 16, 1024), idesc, k > 0 ? 1u : 0u);
+  }
+}
+
+// D[128 x N] (+)= A B, A 128 x 128 in tensor memory (its first 64 columns at
+// a0, the other 64 at a1), B a tile along its rows.
+__device__ __forceinline__ void att_mma_cols(uint32_t d, uint32_t a0, uint32_t a1, const uint8_t* b, uint32_t idesc,
+                                             bool accumulate) {
+  const uint32_t sb = smem_u32(b);
+#pragma unroll
+  for (int k = 0; k < ATT_ROWS / 16; ++k)
+    umma_tmem_a(d, (k < 4 ? a0 : a1) + (k & 3) * 8, smem_desc_sw128(sb + k * 2048, ATT_CHUNK, 1024), idesc,
+                accumulate || k > 0 ? 1u : 0u);
+}
+
+// ---------------------------------------------------------- rows and heads
+// Query heads that share a key head lie next to each other. `pack` of them (a
+// power of two) share a query tile: row r is token first + r / pack of head
+// h0 + r % pack. So a tile is full with fewer tokens, and keys and values are
+// read once for all of them.
+struct AttHeads {
+  int batch, heads, kv_heads, queries, keys, head;
+  int pack_log2;
+  int groups;       // heads / pack
+  int group_heads;  // heads / kv_heads
+  __host__ __device__ __forceinline__ int tile_tokens() const { return ATT_ROWS >> pack_log2; }
+  __host__ __device__ __forceinline__ int query_tiles() const {
+    return (queries + tile_tokens() - 1) >> (7 - pack_log2);
+  }
+  __device__ __forceinline__ int kv_head(int group) const { return (group << pack_log2) / group_heads; }
+};
+
+struct AttStrides {
+  int64_t batch, token, head;
+};
+
+// Keys of sequence b.
+struct AttLengths {
+  const void* data;  // NULL: all keys
+  int bytes;
+};
+__device__ __forceinline__ int att_length(const AttLengths& l, int b, int keys) {
+  if (l.data == nullptr) return keys;
+  const int64_t n = l.bytes == 8 ? static_cast<const int64_t*>(l.data)[b] : static_cast<const int32_t*>(l.data)[b];
+  return static_cast<int>(n < 0 ? 0 : n > keys ? keys : n);
+}
+
+// ---------------------------------------------------------------- host side
+// Sets a kernel's shared memory limit, once per device.
+template <typename... Args>
+cudaError_t att_prepare(void (*kernel)(Args...), size_t smem, std::atomic<uint64_t>& ready) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && (ready.load(std::memory_order_acquire) >> dev & 1)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e == cudaSuccess && dev < 64) ready.fetch_or(uint64_t(1) << dev, std::memory_order_release);
+  return e;
+}
+
+// Map over [batch][row][head][element]; box: 64 elements x box_heads x box_rows.
+bool att_encode(CUtensorMap* map, const void* base, int dtype, int64_t batch, int64_t rows, int64_t heads,
+                int64_t head, const AttStrides& s, int box_heads, int box_rows);
+
+// One call's sizes and layouts, checked.
+struct AttCall {
+  AttHeads h;
+  AttLengths lengths;
+  AttStrides q, k, v, o, grad_o, dq, dk, dv;
+  int dtype;
+  float scale;
+  int num_sms;
+  int* err;
+};
+
+// The keys in `splits` ranges of `tiles` key tiles.
+struct AttSplit {
+  int splits, tiles;
+};
+AttSplit att_forward_split(const AttHeads& h, int num_sms);
+
+cudaError_t attn_forward(const AttCall& c, const void* q, const void* k, const void* v, void* o, float* lse,
+                         char* workspace, cudaStream_t stream);
+// Joins the parts of o that ranges of the keys left: part_o
+// [split][batch][queries][heads][head], part_lse [split][batch][heads][queries].
+cudaError_t attn_join(const AttCall& c, int splits, void* o, float* lse, const float* part_o, const float* part_lse,
+                      cudaStream_t stream);
+size_t attn_backward_workspace(const AttHeads& h, int num_sms);
+cudaError_t attn_backward(const AttCall& c, const void* grad_o, const void* q, const void* k, const void* v,
+                          const void* o, const float* lse, void* dq, void* dk, void* dv, char* workspace,
+                          cudaStream_t stream);
+// Sets a gradient of tokens x heads rows per sequence to zero.
+cudaError_t attn_zero(const AttCall& c, void* out, const AttStrides& strides, int tokens, int heads,
+                      cudaStream_t stream);
+
+}  // namespace prm

@@ -1,0 +1,175 @@
+// Entry points of cross attention: argument checks, sizes and the choice of
+// how the work is split.
+#include <algorithm>
+
+#include "attn.cuh"
+
+namespace prm {
+
+// Where there are fewer pairs of query tiles than SMs, ranges of the keys go
+// to different CTAs and their results are joined: at least two key tiles to a
+// range, so that a join's read and write of O stays below what is saved.
+AttSplit att_forward_split(const AttHeads& h, int num_sms) {
+  const int64_t blocks = (h.query_tiles() + 1) / 2;
+  const int64_t items = static_cast<int64_t>(h.batch) * h.groups * blocks;
+  const int tiles = (h.keys + ATT_ROWS - 1) / ATT_ROWS;
+  const int64_t want = std::min<int64_t>({num_sms / std::max<int64_t>(items, 1), tiles / 2, 64});
+  if (want < 2) return {1, std::max(tiles, 1)};
+  const int each = static_cast<int>((tiles + want - 1) / want);
+  return {(tiles + each - 1) / each, each};
+}
+
+namespace {
+
+constexpr int SMS = 152;  // what workspaces are sized for: one GB300
+
+struct Layout {
+  const prm_attention_strides* s;
+  int64_t rows, heads;
+};
+
+int read(const prm_attention_desc* d, AttCall* c) {
+  if (d == nullptr || d->reserved != 0 || (d->dtype != PRM_BF16 && d->dtype != PRM_FP16) || d->batch < 0 ||
+      d->queries < 0 || d->keys < 0 || d->heads < 0 || d->kv_heads < 0 ||
+      (d->key_lengths != nullptr && d->length_bytes != 4 && d->length_bytes != 8) || !(d->scale > 0.f) ||
+      !(d->scale - d->scale == 0.f))
+    return PRM_ERR_INVALID_ARG;
+  if (d->head < 8 || d->head % 8 != 0 || (d->heads > 0 && (d->kv_heads == 0 || d->heads % d->kv_heads != 0)))
+    return PRM_ERR_SHAPE;
+  // rows and tiles are counted in 31 bits
+  constexpr int64_t MOST = int64_t(1) << 30;
+  if (d->head > 128 || d->batch > (1 << 20) || d->heads > (1 << 16) || d->queries > MOST || d->keys > MOST ||
+      d->batch * d->heads > MOST)
+    return PRM_ERR_UNSUPPORTED;
+  const int64_t bh = std::max<int64_t>(d->batch * d->heads, 1);
+  if (std::max(d->queries, d->keys) > (int64_t(1) << 40) / bh) return PRM_ERR_UNSUPPORTED;
+  *c = AttCall{};
+  AttHeads& h = c->h;
+  h.batch = static_cast<int>(d->batch);
+  h.heads = static_cast<int>(d->heads);
+  h.kv_heads = static_cast<int>(d->kv_heads);
+  h.queries = static_cast<int>(d->queries);
+  h.keys = static_cast<int>(d->keys);
+  h.head = static_cast<int>(d->head);
+  h.group_heads = d->kv_heads > 0 ? static_cast<int>(d->heads / d->kv_heads) : 1;
+  while (h.pack_log2 < 5 && h.group_heads % (2 << h.pack_log2) == 0) ++h.pack_log2;
+  h.groups = h.heads >> h.pack_log2;
+  c->lengths = {d->key_lengths, d->length_bytes};
+  c->dtype = d->dtype;
+  c->scale = d->scale;
+  c->num_sms = SMS;
+  return PRM_OK;
+}
+
+// Strides whose products stay far inside 64 bits, in TMA's units.
+int layout(const prm_attention_strides& s, int64_t batch, int64_t rows, int64_t heads, int64_t head, AttStrides* out) {
+  const int64_t stride[3] = {s.batch, s.token, s.head}, extent[3] = {batch, rows, heads};
+  int64_t used[3];
+  for (int i = 0; i < 3; ++i) {
+    used[i] = extent[i] > 1 ? stride[i] : 0;
+    if (extent[i] <= 1) continue;
+    if (stride[i] < head) return PRM_ERR_SHAPE;
+    if (stride[i] % 8 != 0) return PRM_ERR_ALIGNMENT;
+    if (stride[i] >= (int64_t(1) << 38)) return PRM_ERR_UNSUPPORTED;  // TMA: 40 bits of bytes
+  }
+  *out = {used[0], used[1], used[2]};
+  return PRM_OK;
+}
+
+size_t forward_bytes(const AttHeads& h) {
+  const AttSplit sp = att_forward_split(h, SMS);
+  if (sp.splits < 2) return 0;
+  const size_t rows = static_cast<size_t>(h.batch) * h.queries * h.heads;
+  return round_up(rows * sp.splits * (h.head + 1) * sizeof(float), 256);
+}
+
+bool nothing(const AttHeads& h) { return h.batch == 0 || h.heads == 0 || (h.queries == 0 && h.keys == 0); }
+
+}  // namespace
+}  // namespace prm
+
+extern "C" int prm_attention_workspace(const prm_attention_desc* desc, size_t* forward, size_t* backward) {
+  using namespace prm;
+  if (forward == nullptr || backward == nullptr) return PRM_ERR_INVALID_ARG;
+  AttCall c;
+  const int rc = read(desc, &c);
+  if (rc != PRM_OK) return rc;
+  *forward = *backward = 0;
+  if (nothing(c.h)) return PRM_OK;
+  if (c.h.queries == 0 || c.h.keys == 0) return PRM_OK;
+  *forward = forward_bytes(c.h);
+  *backward = attn_backward_workspace(c.h, SMS);
+  return PRM_OK;
+}
+
+extern "C" int prm_attention_forward(const prm_attention_desc* desc, const void* q, const void* k, const void* v, void* o,
+                                     float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  using namespace prm;
+  AttCall c;
+  int rc = read(desc, &c);
+  if (rc != PRM_OK) return rc;
+  const AttHeads& h = c.h;
+  if (nothing(h) || h.queries == 0) return PRM_OK;
+  if (q == nullptr || o == nullptr || (h.keys > 0 && (k == nullptr || v == nullptr))) return PRM_ERR_INVALID_ARG;
+  if (!aligned_to(q, 16) || !aligned_to(k, 16) || !aligned_to(v, 16) || !aligned_to(o, 16) || !aligned_to(lse, 4) ||
+      !aligned_to(workspace, 256))
+    return PRM_ERR_ALIGNMENT;
+  if ((rc = layout(desc->q, h.batch, h.queries, h.heads, h.head, &c.q)) != PRM_OK ||
+      (rc = layout(desc->k, h.batch, h.keys, h.kv_heads, h.head, &c.k)) != PRM_OK ||
+      (rc = layout(desc->v, h.batch, h.keys, h.kv_heads, h.head, &c.v)) != PRM_OK ||
+      (rc = layout(desc->o, h.batch, h.queries, h.heads, h.head, &c.o)) != PRM_OK)
+    return rc;
+  const size_t need = h.keys == 0 ? 0 : forward_bytes(h);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return PRM_ERR_WORKSPACE;
+  const BlockDevice* dev;
+  if ((rc = block_device(&dev)) != PRM_OK) return rc;
+  c.err = dev->d_err;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = h.keys == 0 ? attn_join(c, 0, o, lse, nullptr, nullptr, st)
+                                    : attn_forward(c, q, k, v, o, lse, static_cast<char*>(workspace), st);
+  return e == cudaSuccess ? PRM_OK : PRM_ERR_CUDA;
+}
+
+extern "C" int prm_attention_backward(const prm_attention_desc* desc, const void* grad_o, const void* q, const void* k,
+                                      const void* v, const void* o, const float* lse, void* dq, void* dk, void* dv,
+                                      void* workspace, size_t workspace_bytes, void* stream) {
+  using namespace prm;
+  AttCall c;
+  int rc = read(desc, &c);
+  if (rc != PRM_OK) return rc;
+  const AttHeads& h = c.h;
+  if (nothing(h)) return PRM_OK;
+  if ((h.queries > 0 && (grad_o == nullptr || q == nullptr || o == nullptr || lse == nullptr || dq == nullptr)) ||
+      (h.keys > 0 && (k == nullptr || v == nullptr || dk == nullptr || dv == nullptr)))
+    return PRM_ERR_INVALID_ARG;
+  const void* ptrs[8] = {grad_o, q, k, v, o, dq, dk, dv};
+  for (const void* p : ptrs)
+    if (!aligned_to(p, 16)) return PRM_ERR_ALIGNMENT;
+  if (!aligned_to(lse, 4) || !aligned_to(workspace, 256)) return PRM_ERR_ALIGNMENT;
+  if ((rc = layout(desc->q, h.batch, h.queries, h.heads, h.head, &c.q)) != PRM_OK ||
+      (rc = layout(desc->k, h.batch, h.keys, h.kv_heads, h.head, &c.k)) != PRM_OK ||
+      (rc = layout(desc->v, h.batch, h.keys, h.kv_heads, h.head, &c.v)) != PRM_OK ||
+      (rc = layout(desc->o, h.batch, h.queries, h.heads, h.head, &c.o)) != PRM_OK ||
+      (rc = layout(desc->grad_o, h.batch, h.queries, h.heads, h.head, &c.grad_o)) != PRM_OK ||
+      (rc = layout(desc->dq, h.batch, h.queries, h.heads, h.head, &c.dq)) != PRM_OK ||
+      (rc = layout(desc->dk, h.batch, h.keys, h.kv_heads, h.head, &c.dk)) != PRM_OK ||
+      (rc = layout(desc->dv, h.batch, h.keys, h.kv_heads, h.head, &c.dv)) != PRM_OK)
+    return rc;
+  const bool empty = h.queries == 0 || h.keys == 0;
+  const size_t need = empty ? 0 : attn_backward_workspace(h, SMS);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return PRM_ERR_WORKSPACE;
+  const BlockDevice* dev;
+  if ((rc = block_device(&dev)) != PRM_OK) return rc;
+  c.err = dev->d_err;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  if (!empty) {
+    e = attn_backward(c, grad_o, q, k, v, o, lse, dq, dk, dv, static_cast<char*>(workspace), st);
+  } else if (h.queries > 0) {
+    e = attn_zero(c, dq, c.dq, h.queries, h.heads, st);
+  } else {
+    e = attn_zero(c, dk, c.dk, h.keys, h.kv_heads, st);
+    if (e == cudaSuccess) e = attn_zero(c, dv, c.dv, h.keys, h.kv_heads, st);
+  }
+  return e == cudaSuccess ? PRM_OK : PRM_ERR_CUDA;
+}

@@ -1,0 +1,877 @@
+// Cross attention, backward:
+//   P = 2^(S scale log2 e - lse),  dP = dO V^T,  dS = P (dP - delta),  delta = rowsum(dO o)
+//   dV = P^T dO,  dK = scale dS^T Q,  dQ = scale dS K
+// in two passes that both form S and dP anew, so that every sum is taken in
+// one place and in one order: the same inputs give the same bits, and nothing
+// is added with atomics (seven products of 128 x 128 x head per tile instead of
+// five; the five need 64 KB of dQ read and written per tile, or atomics).
+//
+//   attn_rows_kernel  -lse and -delta of every query row, in the order of the query tiles
+//   attn_dkv_kernel   a tile of 128 keys against all queries of its heads: S^T = K Q^T and
+//                     dP^T = V dO^T (rows are keys), P^T and dS^T as left operands in tensor
+//                     memory over S^T and dP^T, dV and dK in tensor memory until the end
+//   attn_dq_kernel    a tile of 128 query rows against all keys: S = Q K^T, dP = dO V^T,
+//                     dS in tensor memory over S, dQ in tensor memory
+//   attn_sum_kernel   adds parts, where few tiles were split along the other axis
+//
+// 256 threads take the elements, two to a row, each 64 columns; one thread
+// issues all products, in an order in which the tensor cores have work while
+// the elements are formed: dV and the next S^T beside dS, dK and the next dP^T
+// beside the next P. Products run through the tensor pipe in the order of
+// issue; an operand in tensor memory is overwritten only by a later product.
+//
+// P and dS are rounded to 16 bits as operands of the next product; S, dP, the
+// gradients' sums, lse and delta are fp32.
+#include <algorithm>
+#include <type_traits>
+
+#include "attn.cuh"
+
+namespace prm {
+namespace {
+
+constexpr int ROW_VALUES = 256;  // of a query tile: 128 times -lse, 128 times -delta
+constexpr size_t BWD_BARRIERS = 512;
+
+// ------------------------------------------------------------- -lse, -delta
+struct RowsParams {
+  AttHeads h;
+  AttStrides o, grad_o;
+  const void* op;
+  const void* gp;
+  const float* lse;
+  float* rows;  // [batch][group][query tile][ROW_VALUES]
+  int64_t count;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ RowsParams p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / 16;  // row, in the tiles' order
+  const int part = threadIdx.x % 16;
+  if (i >= p.count) return;  // (count is a multiple of 128: a warp's rows leave together)
+  const int r = static_cast<int>(i % ATT_ROWS);
+  int64_t tile = i / ATT_ROWS;
+  const int tiles = p.h.query_tiles();
+  const int token = static_cast<int>(tile % tiles) * p.h.tile_tokens() + (r >> p.h.pack_log2);
+  const int64_t bg = tile / tiles;
+  const int b = static_cast<int>(bg / p.h.groups);
+  const int head = (static_cast<int>(bg % p.h.groups) << p.h.pack_log2) + (r & ((1 << p.h.pack_log2) - 1));
+  float lse = INFINITY, delta = 0.f;
+  if (token < p.h.queries) {
+    lse = p.lse[(static_cast<int64_t>(b) * p.h.heads + head) * p.h.queries + token];
+    if (lse == -INFINITY) lse = INFINITY;  // a row without keys: P is zero
+    if (part * 8 < p.h.head) {
+      Raw8<T> a, g;
+      a.load(static_cast<const T*>(p.op) + b * p.o.batch + token * p.o.token + head * p.o.head + part * 8);
+      g.load(static_cast<const T*>(p.gp) + b * p.grad_o.batch + token * p.grad_o.token + head * p.grad_o.head +
+             part * 8);
+      float u[8], v[8];
+      a.get(u);
+      g.get(v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) delta = fmaf(u[e], v[e], delta);
+    }
+  }
+  __syncwarp();
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) delta += __shfl_xor_sync(0xffffffffu, delta, o);
+  if (part == 0) {
+    float* out = p.rows + tile * ROW_VALUES + r;
+    out[0] = -lse;
+    out[ATT_ROWS] = -delta;
+  }
+}
+
+// -------------------------------------------------------------- dK and dV
+template <int DP>
+struct DkvShape {
+  static constexpr uint32_t TILE = ATT_TILE<DP>;
+  static constexpr int SLOTS = DP == 128 ? 4 : 8;  // tiles of Q and dO under way
+  static constexpr int ROW_SLOTS = 4;              // -lse and -delta: never more than four query tiles under way
+  static constexpr size_t SMEM =
+      1024 + (2 + SLOTS) * TILE + ROW_SLOTS * ROW_VALUES * sizeof(float) + (BWD_BARRIERS - 256);
+};
+static_assert(DkvShape<128>::SMEM <= 232448 && DkvShape<64>::SMEM <= 232448, "shared memory above 227 KB");
+
+struct DkvParams {
+  CUtensorMap q, grad_o, k, v;
+  AttHeads h;
+  AttLengths lengths;
+  AttStrides dk_strides, dv_strides;
+  const float* rows;
+  void* dk;
+  void* dv;
+  float* part_dk;  // splits > 1: [split][batch][keys][kv_heads][head]
+  float* part_dv;
+  int key_tiles;
+  int splits, split_rounds;  // ranges of the rounds, rounds of one
+  int rounds;                // query tiles of all groups of a key head
+  int64_t items;
+  int mma_k, mma_n;
+  float scale, scale_log2;
+  int* err;
+};
+
+struct DkvItem {
+  int tile, kv_head, b, split;
+  int length;
+  int x0, n;  // first round and their number
+};
+
+__device__ __forceinline__ DkvItem dkv_item(const DkvParams& p, int64_t item) {
+  DkvItem it;
+  it.split = static_cast<int>(item % p.splits);
+  item /= p.splits;
+  it.tile = static_cast<int>(item % p.key_tiles);
+  item /= p.key_tiles;
+  it.kv_head = static_cast<int>(item % p.h.kv_heads);
+  it.b = static_cast<int>(item / p.h.kv_heads);
+  it.length = att_length(p.lengths, it.b, p.h.keys);
+  it.x0 = min(it.split * p.split_rounds, p.rounds);
+  it.n = it.tile * ATT_ROWS < it.length ? min(p.split_rounds, p.rounds - it.x0) : 0;
+  return it;
+}
+
+// Writes 32 columns of a row of a gradient, converted, from column c.
+template <typename T>
+__device__ __forceinline__ void store_row32(T* out, float* part, const float (&v)[32], int c, int head) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 8) {
+    if (c + i >= head) break;
+    float u[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) u[e] = v[i + e];
+    if (part != nullptr) {
+      Raw8<float> r;
+      r.set(u);
+      r.store(part + c + i);
+    } else {
+      Raw8<T> r;
+      r.set(u);
+      r.store(out + c + i);
+    }
+  }
+}
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(ATT_THREADS, 1) attn_dkv_kernel(const __grid_constant__ DkvParams p) {
+  using Shape = DkvShape<DP>;
+  constexpr int SLOTS = Shape::SLOTS;
+  constexpr uint32_t TILE = Shape::TILE;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sK = smem;
+  uint8_t* sV = smem + TILE;
+  uint8_t* ring = smem + 2 * TILE;  // dO_0, Q_0, dO_1, Q_1, ...: freed in that order
+  float* sRows = reinterpret_cast<float*>(ring + SLOTS * TILE);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sRows + Shape::ROW_SLOTS * ROW_VALUES);
+  uint64_t* empty = full + SLOTS;
+  uint64_t* kv_full = empty + SLOTS;
+  uint64_t* kv_empty = kv_full + 1;
+  uint64_t* s_full = kv_empty + 1;
+  uint64_t* p_ready = s_full + 1;
+  uint64_t* dp_full = p_ready + 1;
+  uint64_t* ds_ready = dp_full + 1;
+  uint64_t* acc_full = ds_ready + 1;
+  uint64_t* acc_empty = acc_full + 1;
+  uint64_t* drain_bar = acc_empty + 1;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain_bar + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+
+  const int warp = threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < SLOTS; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(kv_full, 1);
+    mbar_init(kv_empty, 1);
+    mbar_init(s_full, 1);
+    mbar_init(p_ready, 8);
+    mbar_init(dp_full, 1);
+    mbar_init(ds_ready, 8);
+    mbar_init(acc_full, 1);
+    mbar_init(acc_empty, 8);
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(tmem_holder, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_holder;
+  const uint32_t t_s = tmem, t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 256 + DP;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int tiles = p.h.query_tiles();
+
+  if (warp == 8) {
+    if (lane == 0) {
+      uint32_t n = 0, rounds = 0, items = 0;  // loads into the ring, rounds, items so far
+      bool ok = true;
+      for (int64_t item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
+        const DkvItem it = dkv_item(p, item);
+        if (it.n <= 0) continue;
+        ok = wait_bounded(kv_empty, (items & 1u) ^ 1u, abort_flag, p.err, ATT_WAIT_NS);
+        if (!ok) break;
+        mbar_arrive_expect_tx(kv_full, 2 * TILE);
+        att_load_tile<DP>(sK, &p.k, kv_full, it.kv_head, it.tile * ATT_ROWS, it.b);
+        att_load_tile<DP>(sV, &p.v, kv_full, it.kv_head, it.tile * ATT_ROWS, it.b);
+        ++items;
+        for (int x = it.x0; ok && x < it.x0 + it.n; ++x, ++rounds) {
+          const int per_head = p.rounds / tiles;  // groups of a key head
+          const int group = it.kv_head * per_head + x / tiles;
+          const int tile = x % tiles;
+          for (int which = 0; which < 2; ++which) {
+            const uint32_t slot = n % SLOTS;
+            ok = ok && wait_bounded(&empty[slot], ((n / SLOTS) & 1u) ^ 1u, abort_flag, p.err, ATT_WAIT_NS);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&full[slot], TILE + (which ? ROW_VALUES * sizeof(float) : 0));
+            att_load_tile<DP>(ring + slot * TILE, which ? &p.q : &p.grad_o, &full[slot], group << p.h.pack_log2,
+                              tile * p.h.tile_tokens(), it.b);
+            if (which)
+              bulk_load(sRows + (rounds % Shape::ROW_SLOTS) * ROW_VALUES,
+                        p.rows + ((static_cast<int64_t>(it.b) * p.h.groups + group) * tiles + tile) * ROW_VALUES,
+                        ROW_VALUES * sizeof(float), &full[slot]);
+            ++n;
+          }
+        }
+      }
+      if (!ok) {  // every load in flight lands before the CTA exits
+        for (uint32_t s = 0; s < SLOTS && s < n; ++s) wait_drain(&full[s], ((n - 1 - s) / SLOTS) & 1u, 50000000ull);
+        if (items) wait_drain(kv_full, (items - 1) & 1u, 50000000ull);
+      }
+    }
+  } else if (warp == 9) {
+    if (lane == 0) {
+      constexpr bool FP16 = !std::is_same<T, __nv_bfloat16>::value;
+      const uint32_t id_s = idesc_f16kind_f32(ATT_ROWS, ATT_ROWS, false, false, FP16);
+      const uint32_t id_acc = idesc_f16kind_f32(ATT_ROWS, p.mma_n, false, true, FP16);
+      uint32_t n = 0, rounds = 0, items = 0;  // ring tiles used up, rounds, items before this one
+      bool ok = true, issued = false;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        ok = ok && wait_bounded(bar, parity, abort_flag, p.err, ATT_WAIT_NS);
+        if (ok) tc_fence_after_sync();
+        return ok;
+      };
+      auto slot = [&](uint32_t k) { return ring + (k % SLOTS) * TILE; };
+      auto wait_slot = [&](uint32_t k) { return wait(&full[k % SLOTS], (k / SLOTS) & 1u); };
+      auto form = [&](uint32_t d, const uint8_t* a, uint32_t k, uint64_t* done) {
+        if (!wait_slot(k)) return;
+        att_mma_rows(d, a, slot(k), p.mma_k, id_s);
+        umma_commit(done);
+        issued = true;
+      };
+      for (int64_t item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
+        const DkvItem it = dkv_item(p, item);
+        if (it.n <= 0) continue;
+        if (!wait(kv_full, items & 1u)) break;
+        form(t_s, sK, n + 1, s_full);
+        if (ok) form(t_dp, sV, n, dp_full);
+        for (int i = 0; ok && i < it.n; ++i, n += 2, ++rounds) {
+          if (!wait(p_ready, rounds & 1u)) break;
+          if (i == 0 && !wait(acc_empty, (items & 1u) ^ 1u)) break;
+          att_mma_cols(t_dv, t_s, t_s + 64, slot(n), id_acc, i > 0);
+          umma_commit(&empty[n % SLOTS]);
+          if (i + 1 < it.n) form(t_s, sK, n + 3, s_full);
+          if (!ok || !wait(ds_ready, rounds & 1u)) break;
+          att_mma_cols(t_dk, t_dp, t_dp + 64, slot(n + 1), id_acc, i > 0);
+          umma_commit(&empty[(n + 1) % SLOTS]);
+          if (i + 1 < it.n)
+            form(t_dp, sV, n + 2, dp_full);
+        }
+        if (!ok) break;
+        umma_commit(kv_empty);
+        umma_commit(acc_full);
+        ++items;
+      }
+      if (!ok && issued) {
+        umma_commit(drain_bar);
+        wait_drain(drain_bar, 0, 50000000ull);
+      }
+    }
+  } else {
+    const int half = warp >> 2;  // query columns 64 half .. + 64
+    const int row = threadIdx.x & 127;
+    const uint32_t t_lane = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    uint32_t rounds = 0, items = 0, n = 1;  // n: the ring's next Q
+    const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      const bool got = wait_bounded(bar, parity, abort_flag, p.err, ATT_WAIT_NS);
+      if (!__all_sync(0xffffffffu, got)) return false;
+      tc_fence_after_sync();
+      return true;
+    };
+    auto arrive = [&](uint64_t* bar) {
+      tmem_store_wait();
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+    for (int64_t item = blockIdx.x; item < p.items; item += gridDim.x) {
+      const DkvItem it = dkv_item(p, item);
+      bool ok = true;
+      for (int i = 0; i < it.n; ++i, ++rounds, n += 2) {
+        // (S is complete once Q and its rows' values are there; the wait makes the copy visible here)
+        ok = wait(&full[n % SLOTS], (n / SLOTS) & 1u) && wait(s_full, rounds & 1u);
+        if (!ok) break;
+        const float2* values =
+            reinterpret_cast<const float2*>(sRows + (rounds % Shape::ROW_SLOTS) * ROW_VALUES + half * 64);
+        float pr[64];
+        tmem_load_64cols(t_s + t_lane + half * 64, pr);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int col = 32 * c + 2 * e;
+            const float2 lse = values[col / 2];
+            const float2 x = f2_unpack(f2_fma(f2_pack(pr[col], pr[col + 1]), sc2, f2_pack(lse.x, lse.y)));
+            pr[col] = exp2_fast(x.x);
+            pr[col + 1] = exp2_fast(x.y);
+            w[e] = pack2<T>(pr[col], pr[col + 1]);
+          }
+          tmem_store_16cols(t_s + t_lane + half * 64 + c * 16, w);
+        }
+        arrive(p_ready);
+        ok = wait(dp_full, rounds & 1u);
+        if (!ok) break;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float dp[32];
+          tmem_load_32cols(t_dp + t_lane + half * 64 + c * 32, dp);
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int col = 32 * c + 2 * e;
+            const float2 delta = values[ATT_ROWS / 2 + col / 2];
+            const float2 ds = f2_unpack(f2_mul(f2_add(f2_pack(dp[2 * e], dp[2 * e + 1]), f2_pack(delta.x, delta.y)),
+                                               f2_pack(pr[col], pr[col + 1])));
+            w[e] = pack2<T>(ds.x, ds.y);
+          }
+          // (columns 0 .. 31 of this half, which were loaded before)
+          tmem_store_16cols(t_dp + t_lane + half * 64 + c * 16, w);
+        }
+        arrive(ds_ready);
+      }
+      if (!ok) break;
+      if (it.n > 0 && !wait(acc_full, items & 1u)) break;
+      // half 0 writes dV, half 1 dK
+      const int key = it.tile * ATT_ROWS + row;
+      const bool live = key < p.h.keys;
+      const bool used = it.n > 0 && key < it.length;
+      const uint32_t t_acc = (half ? t_dk : t_dv) + t_lane;
+      const AttStrides st = half ? p.dk_strides : p.dv_strides;
+      T* out = static_cast<T*>(half ? p.dk : p.dv) + it.b * st.batch + key * st.token + it.kv_head * st.head;
+      float* part = half ? p.part_dk : p.part_dv;
+      if (part != nullptr)
+        part += (((static_cast<int64_t>(it.split) * p.h.batch + it.b) * p.h.keys + key) * p.h.kv_heads + it.kv_head) *
+                p.h.head;
+      const float factor = half ? p.scale : 1.f;
+#pragma unroll
+      for (int c = 0; c < DP; c += 32) {
+        if (c >= p.h.head) break;
+        float v[32];
+        __syncwarp();
+        if (it.n > 0) tmem_load_32cols(t_acc + c, v);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = used ? v[e] * factor : 0.f;
+        if (live) store_row32<T>(out, part, v, c, p.h.head);
+      }
+      if (it.n > 0) {
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_empty);
+        ++items;
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+// --------------------------------------------------------------------- dQ
+template <int DP>
+struct DqShape {
+  static constexpr uint32_t TILE = ATT_TILE<DP>;
+  static constexpr int KS = 3, VS = 2;  // key and value tiles under way
+  static constexpr size_t SMEM = 1024 + (2 + KS + VS) * TILE + BWD_BARRIERS;
+};
+static_assert(DqShape<128>::SMEM <= 232448, "shared memory above 227 KB");
+
+struct DqParams {
+  CUtensorMap q, grad_o, k, v;
+  AttHeads h;
+  AttLengths lengths;
+  AttStrides dq_strides;
+  const float* rows;
+  void* dq;
+  float* part_dq;  // splits > 1: [split][batch][queries][heads][head]
+  int splits, split_tiles;
+  int64_t items;
+  int mma_k, mma_n;
+  float scale, scale_log2;
+  int* err;
+};
+
+struct DqItem {
+  int tile, group, b, split;
+  int length;
+  int k0, n;
+};
+
+__device__ __forceinline__ DqItem dq_item(const DqParams& p, int64_t item) {
+  DqItem it;
+  const int tiles = p.h.query_tiles();
+  it.tile = static_cast<int>(item % tiles);
+  item /= tiles;
+  it.split = static_cast<int>(item % p.splits);
+  item /= p.splits;
+  it.group = static_cast<int>(item % p.h.groups);
+  it.b = static_cast<int>(item / p.h.groups);
+  it.length = att_length(p.lengths, it.b, p.h.keys);
+  const int key_tiles = (it.length + ATT_ROWS - 1) / ATT_ROWS;
+  it.k0 = min(it.split * p.split_tiles, key_tiles);
+  it.n = min(p.split_tiles, key_tiles - it.k0);
+  return it;
+}
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(ATT_THREADS, 1) attn_dq_kernel(const __grid_constant__ DqParams p) {
+  using Shape = DqShape<DP>;
+  constexpr int KS = Shape::KS, VS = Shape::VS;
+  constexpr uint32_t TILE = Shape::TILE;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem;
+  uint8_t* sG = smem + TILE;
+  uint8_t* sK = smem + 2 * TILE;
+  uint8_t* sV = sK + KS * TILE;
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(sV + VS * TILE);
+  uint64_t* k_empty = k_full + KS;
+  uint64_t* v_full = k_empty + KS;
+  uint64_t* v_empty = v_full + VS;
+  uint64_t* q_full = v_empty + VS;
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* s_full = q_empty + 1;  // two buffers of S
+  uint64_t* dp_full = s_full + 2;
+  uint64_t* ds_ready = dp_full + 1;
+  uint64_t* acc_full = ds_ready + 1;
+  uint64_t* acc_empty = acc_full + 1;
+  uint64_t* drain_bar = acc_empty + 1;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain_bar + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+
+  const int warp = threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < KS; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_empty[s], 1);
+    }
+    for (int s = 0; s < VS; ++s) {
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_empty[s], 1);
+    }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    mbar_init(&s_full[0], 1);
+    mbar_init(&s_full[1], 1);
+    mbar_init(dp_full, 1);
+    mbar_init(ds_ready, 8);
+    mbar_init(acc_full, 1);
+    mbar_init(acc_empty, 8);
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(tmem_holder, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_holder;
+  const uint32_t t_dp = tmem + 256, t_dq = tmem + 384;  // S at tmem and tmem + 128
+  pdl_wait();
+  pdl_launch_dependents();
+
+  if (warp == 8) {
+    if (lane == 0) {
+      uint32_t nk = 0, nv = 0, items = 0;
+      bool ok = true;
+      for (int64_t item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
+        const DqItem it = dq_item(p, item);
+        if (it.n <= 0) continue;
+        ok = wait_bounded(q_empty, (items & 1u) ^ 1u, abort_flag, p.err, ATT_WAIT_NS);
+        if (!ok) break;
+        mbar_arrive_expect_tx(q_full, 2 * TILE);
+        const int h0 = it.group << p.h.pack_log2, t0 = it.tile * p.h.tile_tokens();
+        att_load_tile<DP>(sQ, &p.q, q_full, h0, t0, it.b);
+        att_load_tile<DP>(sG, &p.grad_o, q_full, h0, t0, it.b);
+        ++items;
+        const int kv_head = p.h.kv_head(it.group);
+        for (int j = 0; j < it.n; ++j) {
+          const int key = (it.k0 + j) * ATT_ROWS;
+          ok = wait_bounded(&k_empty[nk % KS], ((nk / KS) & 1u) ^ 1u, abort_flag, p.err, ATT_WAIT_NS);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&k_full[nk % KS], TILE);
+          att_load_tile<DP>(sK + (nk % KS) * TILE, &p.k, &k_full[nk % KS], kv_head, key, it.b);
+          ++nk;
+          ok = wait_bounded(&v_empty[nv % VS], ((nv / VS) & 1u) ^ 1u, abort_flag, p.err, ATT_WAIT_NS);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&v_full[nv % VS], TILE);
+          att_load_tile<DP>(sV + (nv % VS) * TILE, &p.v, &v_full[nv % VS], kv_head, key, it.b);
+          ++nv;
+        }
+      }
+      if (!ok) {  // every load in flight lands before the CTA exits
+        for (uint32_t s = 0; s < KS && s < nk; ++s) wait_drain(&k_full[s], ((nk - 1 - s) / KS) & 1u, 50000000ull);
+        for (uint32_t s = 0; s < VS && s < nv; ++s) wait_drain(&v_full[s], ((nv - 1 - s) / VS) & 1u, 50000000ull);
+        if (items) wait_drain(q_full, (items - 1) & 1u, 50000000ull);
+      }
+    }
+  } else if (warp == 9) {
+    if (lane == 0) {
+      constexpr bool FP16 = !std::is_same<T, __nv_bfloat16>::value;
+      const uint32_t id_s = idesc_f16kind_f32(ATT_ROWS, ATT_ROWS, false, false, FP16);
+      const uint32_t id_acc = idesc_f16kind_f32(ATT_ROWS, p.mma_n, false, true, FP16);
+      uint32_t n = 0, items = 0;  // key tiles used up, items before this one
+      bool ok = true, issued = false;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        ok = ok && wait_bounded(bar, parity, abort_flag, p.err, ATT_WAIT_NS);
+        if (ok) tc_fence_after_sync();
+        return ok;
+      };
+      auto form_s = [&](uint32_t k) {
+        if (!wait(&k_full[k % KS], (k / KS) & 1u)) return;
+        att_mma_rows(tmem + (k & 1u) * 128, sQ, sK + (k % KS) * TILE, p.mma_k, id_s);
+        umma_commit(&s_full[k & 1u]);
+        issued = true;
+      };
+      auto form_dp = [&](uint32_t k) {
+        if (!wait(&v_full[k % VS], (k / VS) & 1u)) return;
+        att_mma_rows(t_dp, sG, sV + (k % VS) * TILE, p.mma_k, id_s);
+        umma_commit(dp_full);
+        umma_commit(&v_empty[k % VS]);
+      };
+      for (int64_t item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
+        const DqItem it = dq_item(p, item);
+        if (it.n <= 0) continue;
+        if (!wait(q_full, items & 1u)) break;
+        form_s(n);
+        if (ok) form_dp(n);
+        if (ok && it.n > 1) form_s(n + 1);
+        for (int j = 0; ok && j < it.n; ++j, ++n) {
+          if (!wait(ds_ready, n & 1u)) break;
+          if (j + 1 < it.n) form_dp(n + 1);
+          if (j == 0 && ok) wait(acc_empty, (items & 1u) ^ 1u);
+          if (!ok) break;
+          const uint32_t a = tmem + (n & 1u) * 128;
+          att_mma_cols(t_dq, a, a + 64, sK + (n % KS) * TILE, id_acc, j > 0);
+          umma_commit(&k_empty[n % KS]);
+          if (j + 2 < it.n) form_s(n + 2);
+        }
+        if (!ok) break;
+        umma_commit(q_empty);
+        umma_commit(acc_full);
+        ++items;
+      }
+      if (!ok && issued) {
+        umma_commit(drain_bar);
+        wait_drain(drain_bar, 0, 50000000ull);
+      }
+    }
+  } else {
+    const int half = warp >> 2;  // key columns 64 half .. + 64
+    const int row = threadIdx.x & 127;
+    const uint32_t t_lane = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    uint32_t n = 0, items = 0;
+    const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      const bool got = wait_bounded(bar, parity, abort_flag, p.err, ATT_WAIT_NS);
+      if (!__all_sync(0xffffffffu, got)) return false;
+      tc_fence_after_sync();
+      return true;
+    };
+    for (int64_t item = blockIdx.x; item < p.items; item += gridDim.x) {
+      const DqItem it = dq_item(p, item);
+      const int token = it.tile * p.h.tile_tokens() + (row >> p.h.pack_log2);
+      const int head = (it.group << p.h.pack_log2) + (row & ((1 << p.h.pack_log2) - 1));
+      const float* values =
+          p.rows + ((static_cast<int64_t>(it.b) * p.h.groups + it.group) * p.h.query_tiles() + it.tile) * ROW_VALUES;
+      const float lse = values[row], delta = values[ATT_ROWS + row];
+      const uint64_t lse2 = f2_pack(lse, lse), delta2 = f2_pack(delta, delta);
+      bool ok = true;
+      for (int j = 0; j < it.n; ++j, ++n) {
+        const uint32_t t_s = tmem + (n & 1u) * 128 + t_lane + half * 64;
+        ok = wait(&s_full[n & 1u], (n >> 1) & 1u);
+        if (!ok) break;
+        float pr[64];
+        tmem_load_64cols(t_s, pr);
+#pragma unroll
+        for (int e = 0; e < 64; e += 2) {
+          const float2 x = f2_unpack(f2_fma(f2_pack(pr[e], pr[e + 1]), sc2, lse2));
+          pr[e] = exp2_fast(x.x);
+          pr[e + 1] = exp2_fast(x.y);
+        }
+        ok = wait(dp_full, n & 1u);
+        if (!ok) break;
+        const int valid = it.length - (it.k0 + j) * ATT_ROWS;
+        const int mine = valid - half * 64;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float dp[32];
+          tmem_load_32cols(t_dp + t_lane + half * 64 + c * 32, dp);
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int col = 32 * c + 2 * e;
+            const float2 ds =
+                f2_unpack(f2_mul(f2_add(f2_pack(dp[2 * e], dp[2 * e + 1]), delta2), f2_pack(pr[col], pr[col + 1])));
+            w[e] = pack2<T>(ds.x, ds.y);
+            if (valid < ATT_ROWS) {
+              if (col >= mine) w[e] = 0u;
+              else if (col + 1 >= mine) w[e] &= 0xffffu;
+            }
+          }
+          tmem_store_16cols(t_s + c * 16, w);
+        }
+        if (valid < ATT_ROWS && half == 0) {
+          // keys behind the last one meet a dS of zero: infinities and NaN would remain. (S, which also reads the
+          // tile, is complete.)
+          uint4* k = reinterpret_cast<uint4*>(sK + (n % KS) * TILE);
+          for (int i = valid * 8 + row; i < ATT_ROWS * 8; i += 128)
+#pragma unroll
+            for (int c = 0; c < DP / 64; ++c) k[c * (ATT_CHUNK / 16) + i] = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        tmem_store_wait();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ds_ready);
+      }
+      if (!ok) break;
+      if (it.n > 0 && !wait(acc_full, items & 1u)) break;
+      const bool live = token < p.h.queries;
+      T* out = static_cast<T*>(p.dq) + it.b * p.dq_strides.batch + token * p.dq_strides.token +
+               head * p.dq_strides.head;
+      float* part = p.part_dq;
+      if (part != nullptr)
+        part += (((static_cast<int64_t>(it.split) * p.h.batch + it.b) * p.h.queries + token) * p.h.heads + head) *
+                p.h.head;
+#pragma unroll
+      for (int q = 0; q < DP / 2; q += 32) {
+        const int c = half * (DP / 2) + q;
+        if (c >= p.h.head) break;
+        float v[32];
+        __syncwarp();
+        if (it.n > 0) tmem_load_32cols(t_dq + t_lane + c, v);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = it.n > 0 ? v[e] * p.scale : 0.f;
+        if (live) store_row32<T>(out, part, v, c, p.h.head);
+      }
+      if (it.n > 0) {
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_empty);
+        ++items;
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+// -------------------------------------------------------------------- sums
+// out = sum of the parts, in order. A thread takes eight elements of a row.
+struct SumParams {
+  const float* part;  // [split][batch][tokens][heads][head]
+  void* out;
+  AttStrides out_strides;
+  int tokens, heads, head, splits;
+  int64_t rows;  // batch * tokens * heads
+};
+
+template <typename T>
+__global__ void __launch_bounds__(256) attn_sum_kernel(const __grid_constant__ SumParams p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int vectors = p.head / 8;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= p.rows * vectors) return;
+  const int64_t row = i / vectors;
+  const int vec = static_cast<int>(i - row * vectors);
+  const int64_t bt = row / p.heads;
+  const int64_t head = row - bt * p.heads, b = bt / p.tokens, token = bt - b * p.tokens;
+  float v[8] = {};
+  for (int s = 0; s < p.splits; ++s) {
+    Raw8<float> r;
+    r.load(p.part + (s * p.rows + row) * p.head + vec * 8);
+    float u[8];
+    r.get(u);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += u[e];
+  }
+  Raw8<T> r;
+  r.set(v);
+  r.store(static_cast<T*>(p.out) + b * p.out_strides.batch + token * p.out_strides.token + head * p.out_strides.head +
+          vec * 8);
+}
+
+template <typename T>
+cudaError_t add_parts(const AttCall& c, const float* part, void* out, const AttStrides& strides, int tokens, int heads,
+                      int splits, cudaStream_t stream) {
+  const SumParams p{part, out, strides, tokens, heads, c.h.head, splits,
+                    static_cast<int64_t>(c.h.batch) * tokens * heads};
+  const int64_t threads = p.rows * (c.h.head / 8);
+  return launch_dependent(attn_sum_kernel<T>, dim3(static_cast<unsigned>((threads + 255) / 256)), dim3(256), 0, stream,
+                          p);
+}
+
+// -------------------------------------------------------------------- host
+struct Plan {
+  AttSplit dkv, dq;            // ranges of rounds; ranges of key tiles
+  int rounds, key_tiles;
+  size_t dkv_at, dq_at, bytes; // workspace: rows' values, then parts of dK and dV, then of dQ
+  size_t dkv_part;             // floats of the parts of dK
+};
+
+// As forward: parts only where there are fewer tiles than SMs, of two at least.
+AttSplit split(int64_t items, int steps, int num_sms) {
+  const int64_t want = std::min<int64_t>({num_sms / std::max<int64_t>(items, 1), steps / 2, 64});
+  if (want < 2) return {1, std::max(steps, 1)};
+  const int each = static_cast<int>((steps + want - 1) / want);
+  return {(steps + each - 1) / each, each};
+}
+
+Plan plan(const AttHeads& h, int num_sms) {
+  Plan s{};
+  const int tiles = h.query_tiles();
+  s.key_tiles = (h.keys + ATT_ROWS - 1) / ATT_ROWS;
+  s.rounds = (h.group_heads >> h.pack_log2) * tiles;
+  s.dkv = split(static_cast<int64_t>(h.batch) * h.kv_heads * s.key_tiles, s.rounds, num_sms);
+  s.dq = split(static_cast<int64_t>(h.batch) * h.groups * tiles, s.key_tiles, num_sms);
+  size_t at = round_up(static_cast<size_t>(h.batch) * h.groups * tiles * ROW_VALUES * sizeof(float), 256);
+  s.dkv_at = at;
+  s.dkv_part = s.dkv.splits > 1 ? static_cast<size_t>(s.dkv.splits) * h.batch * h.keys * h.kv_heads * h.head : 0;
+  at += round_up(2 * s.dkv_part * sizeof(float), 256);
+  s.dq_at = at;
+  if (s.dq.splits > 1) at += static_cast<size_t>(s.dq.splits) * h.batch * h.queries * h.heads * h.head * sizeof(float);
+  s.bytes = round_up(at, 256);
+  return s;
+}
+
+template <typename T, int DP>
+cudaError_t launch(const AttCall& c, const Plan& s, RowsParams& rows, DkvParams& dkv, DqParams& dq,
+                   cudaStream_t stream) {
+  static std::atomic<uint64_t> dkv_ready{0}, dq_ready{0};
+  cudaError_t e;
+  if (rows.count > 0) {
+    e = launch_dependent(attn_rows_kernel<T>, dim3(static_cast<unsigned>((rows.count * 16 + 255) / 256)), dim3(256), 0,
+                         stream, rows);
+    if (e != cudaSuccess) return e;
+  }
+  if (dkv.items > 0) {
+    if ((e = att_prepare(attn_dkv_kernel<T, DP>, DkvShape<DP>::SMEM, dkv_ready)) != cudaSuccess) return e;
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(dkv.items, c.num_sms));
+    e = launch_dependent(attn_dkv_kernel<T, DP>, dim3(grid), dim3(ATT_THREADS), DkvShape<DP>::SMEM, stream, dkv);
+    if (e != cudaSuccess) return e;
+  }
+  if (dq.items > 0) {
+    if ((e = att_prepare(attn_dq_kernel<T, DP>, DqShape<DP>::SMEM, dq_ready)) != cudaSuccess) return e;
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(dq.items, c.num_sms));
+    e = launch_dependent(attn_dq_kernel<T, DP>, dim3(grid), dim3(ATT_THREADS), DqShape<DP>::SMEM, stream, dq);
+    if (e != cudaSuccess) return e;
+  }
+  if (s.dkv.splits > 1) {
+    if ((e = add_parts<T>(c, dkv.part_dk, dkv.dk, c.dk, c.h.keys, c.h.kv_heads, s.dkv.splits, stream)) != cudaSuccess)
+      return e;
+    if ((e = add_parts<T>(c, dkv.part_dv, dkv.dv, c.dv, c.h.keys, c.h.kv_heads, s.dkv.splits, stream)) != cudaSuccess)
+      return e;
+  }
+  if (s.dq.splits > 1)
+    return add_parts<T>(c, dq.part_dq, dq.dq, c.dq, c.h.queries, c.h.heads, s.dq.splits, stream);
+  return cudaSuccess;
+}
+
+}  // namespace
+
+size_t attn_backward_workspace(const AttHeads& h, int num_sms) { return plan(h, num_sms).bytes; }
+
+cudaError_t attn_backward(const AttCall& c, const void* grad_o, const void* q, const void* k, const void* v,
+                          const void* o, const float* lse, void* dq, void* dk, void* dv, char* workspace,
+                          cudaStream_t stream) {
+  const AttHeads& h = c.h;
+  const Plan s = plan(h, c.num_sms);
+  float* values = reinterpret_cast<float*>(workspace);
+  const int tiles = h.query_tiles(), pack = 1 << h.pack_log2;
+  RowsParams r{h, c.o, c.grad_o, o, grad_o, lse, values, static_cast<int64_t>(h.batch) * h.groups * tiles * ATT_ROWS};
+  DkvParams a{};
+  DqParams b{};
+  const bool q_ok = att_encode(&a.q, q, c.dtype, h.batch, h.queries, h.heads, h.head, c.q, pack, ATT_ROWS / pack) &&
+                    att_encode(&a.grad_o, grad_o, c.dtype, h.batch, h.queries, h.heads, h.head, c.grad_o, pack,
+                               ATT_ROWS / pack);
+  const bool k_ok = att_encode(&a.k, k, c.dtype, h.batch, h.keys, h.kv_heads, h.head, c.k, 1, ATT_ROWS) &&
+                    att_encode(&a.v, v, c.dtype, h.batch, h.keys, h.kv_heads, h.head, c.v, 1, ATT_ROWS);
+  if (!q_ok || !k_ok) return cudaErrorInvalidValue;
+  b.q = a.q;
+  b.grad_o = a.grad_o;
+  b.k = a.k;
+  b.v = a.v;
+  a.h = b.h = h;
+  a.lengths = b.lengths = c.lengths;
+  a.rows = b.rows = values;
+  a.mma_k = b.mma_k = (h.head + 15) / 16;
+  a.mma_n = b.mma_n = a.mma_k * 16;
+  a.scale = b.scale = c.scale;
+  a.scale_log2 = b.scale_log2 = c.scale * 1.4426950408889634f;
+  a.err = b.err = c.err;
+  a.dk_strides = c.dk;
+  a.dv_strides = c.dv;
+  a.dk = dk;
+  a.dv = dv;
+  a.key_tiles = s.key_tiles;
+  a.rounds = s.rounds;
+  a.splits = s.dkv.splits;
+  a.split_rounds = s.dkv.tiles;
+  a.items = static_cast<int64_t>(h.batch) * h.kv_heads * s.key_tiles * s.dkv.splits;
+  if (s.dkv.splits > 1) {
+    a.part_dk = reinterpret_cast<float*>(workspace + s.dkv_at);
+    a.part_dv = a.part_dk + s.dkv_part;
+  }
+  b.dq_strides = c.dq;
+  b.dq = dq;
+  b.splits = s.dq.splits;
+  b.split_tiles = s.dq.tiles;
+  b.items = static_cast<int64_t>(h.batch) * h.groups * tiles * s.dq.splits;
+  if (s.dq.splits > 1) b.part_dq = reinterpret_cast<float*>(workspace + s.dq_at);
+  const bool wide = h.head > 64;
+  if (c.dtype == PRM_BF16)
+    return wide ? launch<__nv_bfloat16, 128>(c, s, r, a, b, stream) : launch<__nv_bfloat16, 64>(c, s, r, a, b, stream);
+  return wide ? launch<__half, 128>(c, s, r, a, b, stream) : launch<__half, 64>(c, s, r, a, b, stream);
+}
+
+// Zeros, where there are no keys or no queries.
+cudaError_t attn_zero(const AttCall& c, void* out, const AttStrides& strides, int tokens, int heads,
+                      cudaStream_t stream) {
+  return c.dtype == PRM_BF16 ? add_parts<__nv_bfloat16>(c, nullptr, out, strides, tokens, heads, 0, stream)
+                             : add_parts<__half>(c, nullptr, out, strides, tokens, heads, 0, stream);
+}
+
+}  // namespace prm

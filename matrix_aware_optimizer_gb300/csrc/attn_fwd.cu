@@ -1,0 +1,561 @@
+// Cross attention, forward: o = softmax(scale q k^T over the first
+// key_lengths[b] keys) v, and the base-2 logarithm of each row's sum for the
+// backward pass.
+//
+// One pass over the keys with the running maximum and sum of the softmax. A
+// CTA takes 256 rows of queries as two tiles of 128, and walks over the keys in
+// tiles of 128. Per key tile and query tile the tensor cores form S = Q K^T in
+// tensor memory; the tile's warpgroup (a thread to a row) takes the maximum and
+// the exponentials, writes P as 16-bit values over S, and the tensor cores add
+// P V to O, both without leaving tensor memory (S 2 x 128 columns, O 2 x DP).
+// While one tile's exponentials are taken the other tile's products run. The
+// CTA is persistent: the next item's tiles are loaded, and its first S formed,
+// while the last one's rows are written.
+//
+// O is only rescaled when a row's maximum grows by more than 2^8 over the one
+// in use; until then the exponentials are taken against the old one, which
+// costs no accuracy (sums and O are in fp32, P's rounding is relative).
+//
+// P is rounded to 16 bits because it is an operand of the next product; the
+// row's sum adds the unrounded values, in fp32.
+//
+// All products of a CTA are issued by one thread and run through its tensor
+// pipe in that order: S of the next key tile overwrites P only behind the
+// product that reads it.
+#include <algorithm>
+#include <mutex>
+#include <type_traits>
+
+#include "attn.cuh"
+
+namespace prm {
+
+static PFN_cuTensorMapEncodeTiled_v12000 att_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  });
+  return fn;
+}
+
+bool att_encode(CUtensorMap* map, const void* base, int dtype, int64_t batch, int64_t rows, int64_t heads,
+                int64_t head, const AttStrides& s, int box_heads, int box_rows) {
+  auto enc = att_encoder();
+  if (enc == nullptr) return false;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(head), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows),
+                        static_cast<cuuint64_t>(batch)};
+  // the stride of an extent of one is never used, but it has to be a legal one
+  auto bytes = [&](int64_t extent, int64_t stride) {
+    return static_cast<cuuint64_t>(extent > 1 ? stride : round_up(static_cast<size_t>(head), 8)) * 2;
+  };
+  cuuint64_t strides[3] = {bytes(heads, s.head), bytes(rows, s.token), bytes(batch, s.batch)};
+  cuuint32_t box[4] = {64u, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows), 1u};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(map, dtype == PRM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+namespace {
+
+constexpr float RESCALE_ABOVE = 8.f;
+
+template <int DP>
+struct FwdShape {
+  static constexpr int STAGES = DP == 128 ? 5 : 8;  // of one key or value tile
+  static constexpr uint32_t TILE = ATT_TILE<DP>;
+  static constexpr size_t BARRIERS = 512;
+  static constexpr size_t SMEM = 1024 + (2 + STAGES) * TILE + BARRIERS;
+};
+static_assert(FwdShape<128>::SMEM <= 232448 && FwdShape<64>::SMEM <= 232448, "shared memory above 227 KB");
+
+struct FwdParams {
+  CUtensorMap q, k, v;
+  AttHeads h;
+  AttLengths lengths;
+  AttStrides o_strides;
+  void* o;
+  float* lse;       // [batch][heads][queries], or NULL
+  float* part_o;    // splits > 1: [split][batch][queries][heads][head], each part normalised
+  float* part_lse;  // splits > 1: [split][batch][heads][queries]
+  int blocks;       // pairs of query tiles
+  int splits, split_tiles;  // key ranges, key tiles of one
+  int64_t items;
+  int mma_k;        // 16-element steps of a head
+  int mma_n;        // head rounded up to 16
+  float scale_log2;
+  int* err;
+};
+
+struct FwdItem {
+  int block, split, group, b;
+  int length;   // keys of the sequence
+  int k0, n;    // first key tile and their number
+  int tiles;    // query tiles with rows: 1 or 2
+};
+
+__device__ __forceinline__ FwdItem fwd_item(const FwdParams& p, int64_t item) {
+  FwdItem it;
+  it.block = static_cast<int>(item % p.blocks);
+  item /= p.blocks;
+  it.split = static_cast<int>(item % p.splits);
+  item /= p.splits;
+  it.group = static_cast<int>(item % p.h.groups);
+  it.b = static_cast<int>(item / p.h.groups);
+  it.length = att_length(p.lengths, it.b, p.h.keys);
+  const int tiles = (it.length + ATT_ROWS - 1) / ATT_ROWS;
+  it.k0 = min(it.split * p.split_tiles, tiles);
+  it.n = min(p.split_tiles, tiles - it.k0);
+  it.tiles = (it.block * 2 + 1) * p.h.tile_tokens() < p.h.queries ? 2 : 1;
+  return it;
+}
+
+// Scores of the keys behind the last one.
+__device__ __forceinline__ void hide(float (&s)[64], int valid) {
+#pragma unroll
+  for (int i = 0; i < 64; ++i)
+    if (i >= valid) s[i] = -INFINITY;
+}
+
+// Four maxima over s, new or joined to those that are there.
+__device__ __forceinline__ void top4(const float (&s)[64], float (&mx)[4], bool first) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) mx[e] = first ? s[e] : fmaxf(mx[e], s[e]);
+#pragma unroll
+  for (int i = 4; i < 64; i += 4)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[i + e]);
+}
+
+// P = 2^(s scale - base) of 64 keys into tensor memory at t_p, and its sum.
+template <typename T>
+__device__ __forceinline__ void exponentials(const float (&s)[64], uint64_t scale2, uint64_t minus_base2,
+                                             uint64_t (&sum)[2], uint32_t t_p) {
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    uint32_t w[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float2 x = f2_unpack(f2_fma(f2_pack(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]), scale2, minus_base2));
+      const float a = exp2_fast(x.x), b = exp2_fast(x.y);
+      sum[i & 1] = f2_add(sum[i & 1], f2_pack(a, b));
+      w[i] = pack2<T>(a, b);
+    }
+    tmem_store_16cols(t_p + 16 * c, w);
+  }
+}
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(ATT_THREADS, 1) attn_fwd_kernel(const __grid_constant__ FwdParams p) {
+  using Shape = FwdShape<DP>;
+  constexpr int STAGES = Shape::STAGES;
+  constexpr uint32_t TILE = Shape::TILE;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem;
+  uint8_t* sKV = smem + 2 * TILE;
+  uint64_t* kv_full = reinterpret_cast<uint64_t*>(sKV + STAGES * TILE);
+  uint64_t* kv_empty = kv_full + STAGES;
+  uint64_t* q_full = kv_empty + STAGES;
+  uint64_t* q_empty = q_full + 2;
+  uint64_t* s_full = q_empty + 2;
+  uint64_t* p_full = s_full + 2;
+  uint64_t* pv_done = p_full + 2;
+  uint64_t* o_empty = pv_done + 2;
+  uint64_t* drain_bar = o_empty + 2;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain_bar + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+
+  const int warp = threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&kv_full[s], 1);
+      mbar_init(&kv_empty[s], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&q_full[t], 1);
+      mbar_init(&q_empty[t], 1);
+      mbar_init(&s_full[t], 1);
+      mbar_init(&p_full[t], 4);
+      mbar_init(&pv_done[t], 1);
+      mbar_init(&o_empty[t], 4);
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(tmem_holder, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_holder;
+  pdl_wait();
+  pdl_launch_dependents();
+
+  if (warp == 8) {
+    if (lane == 0) {
+      uint32_t kv = 0, q_used[2] = {0, 0};  // tiles loaded so far
+      uint32_t issued = 0;
+      bool ok = true;
+      auto load_kv = [&](const CUtensorMap* map, const FwdItem& it, int j) {
+        const uint32_t stage = kv % STAGES;
+        ok = ok && wait_bounded(&kv_empty[stage], ((kv / STAGES) & 1u) ^ 1u, abort_flag, p.err, ATT_WAIT_NS);
+        if (!ok) return;
+        mbar_arrive_expect_tx(&kv_full[stage], TILE);
+        att_load_tile<DP>(sKV + stage * TILE, map, &kv_full[stage], p.h.kv_head(it.group), (it.k0 + j) * ATT_ROWS,
+                          it.b);
+        ++kv;
+      };
+      for (int64_t item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
+        const FwdItem it = fwd_item(p, item);
+        if (it.n <= 0) continue;
+        for (int t = 0; ok && t < it.tiles; ++t) {
+          ok = wait_bounded(&q_empty[t], (q_used[t] & 1u) ^ 1u, abort_flag, p.err, ATT_WAIT_NS);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&q_full[t], TILE);
+          att_load_tile<DP>(sQ + t * TILE, &p.q, &q_full[t], it.group << p.h.pack_log2,
+                            (it.block * 2 + t) * p.h.tile_tokens(), it.b);
+          ++q_used[t];
+          issued = 1;
+        }
+        for (int j = 0; ok && j < it.n; ++j) {
+          load_kv(&p.k, it, j);
+          load_kv(&p.v, it, j);
+        }
+      }
+      if (!ok && (issued || kv)) {
+        // every load in flight lands before the CTA exits
+        for (uint32_t s = 0; s < STAGES && s < kv; ++s) {
+          const uint32_t last = (kv - 1 - s) / STAGES;  // round of the stage's latest load
+          wait_drain(&kv_full[s], last & 1u, 50000000ull);
+        }
+        for (int t = 0; t < 2; ++t)
+          if (q_used[t]) wait_drain(&q_full[t], (q_used[t] - 1) & 1u, 50000000ull);
+      }
+    }
+  } else if (warp == 9) {
+    if (lane == 0) {
+      constexpr bool FP16 = !std::is_same<T, __nv_bfloat16>::value;
+      const uint32_t id_s = idesc_f16kind_f32(ATT_ROWS, ATT_ROWS, false, false, FP16);
+      const uint32_t id_o = idesc_f16kind_f32(ATT_ROWS, p.mma_n, false, true, FP16);
+      uint32_t kv = 0;                                      // key and value tiles used up
+      uint32_t q_used[2] = {0, 0}, p_used[2] = {0, 0}, o_used[2] = {0, 0};
+      bool ok = true, issued = false;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        ok = ok && wait_bounded(bar, parity, abort_flag, p.err, ATT_WAIT_NS);
+        if (ok) tc_fence_after_sync();
+        return ok;
+      };
+      auto wait_kv = [&](uint32_t n) { return wait(&kv_full[n % STAGES], (n / STAGES) & 1u); };
+      auto form_s = [&](int t, uint32_t n, bool last) {
+        att_mma_rows(tmem + t * ATT_ROWS, sQ + t * TILE, sKV + (n % STAGES) * TILE, p.mma_k, id_s);
+        umma_commit(&s_full[t]);
+        if (last) umma_commit(&q_empty[t]);
+        issued = true;
+      };
+      for (int64_t item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
+        const FwdItem it = fwd_item(p, item);
+        if (it.n <= 0) continue;
+        for (int t = 0; t < it.tiles; ++t) {
+          if (!wait(&q_full[t], q_used[t] & 1u) || !wait_kv(kv)) break;
+          ++q_used[t];
+          form_s(t, kv, it.n == 1);
+        }
+        if (!ok) break;
+        umma_commit(&kv_empty[kv % STAGES]);
+        for (int j = 0; ok && j < it.n; ++j, kv += 2) {
+          for (int t = 0; t < it.tiles; ++t) {
+            if (!wait(&p_full[t], p_used[t] & 1u) || !wait_kv(kv + 1)) break;
+            ++p_used[t];
+            if (j == 0) {
+              if (!wait(&o_empty[t], (o_used[t] & 1u) ^ 1u)) break;
+              ++o_used[t];
+            }
+            const uint32_t a = tmem + t * ATT_ROWS;
+            att_mma_cols(tmem + 2 * ATT_ROWS + t * DP, a, a + 64, sKV + ((kv + 1) % STAGES) * TILE, id_o, j > 0);
+            umma_commit(&pv_done[t]);
+            if (j + 1 < it.n) {
+              if (!wait_kv(kv + 2)) break;
+              form_s(t, kv + 2, j + 2 == it.n);
+            }
+          }
+          if (!ok) break;
+          umma_commit(&kv_empty[(kv + 1) % STAGES]);
+          if (j + 1 < it.n) umma_commit(&kv_empty[(kv + 2) % STAGES]);
+        }
+      }
+      if (!ok && issued) {
+        umma_commit(drain_bar);
+        wait_drain(drain_bar, 0, 50000000ull);
+      }
+    }
+  } else {
+    const int t = warp >> 2;
+    const int row = threadIdx.x & 127;
+    const uint32_t t_lane = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t t_s = tmem + t * ATT_ROWS + t_lane;
+    const uint32_t t_o = tmem + 2 * ATT_ROWS + t * DP + t_lane;
+    uint32_t kv = 0, steps = 0;  // key and value tiles before this item, key tiles this tile has worked on
+    for (int64_t item = blockIdx.x; item < p.items; item += gridDim.x) {
+      const FwdItem it = fwd_item(p, item);
+      const int token = (it.block * 2 + t) * p.h.tile_tokens() + (row >> p.h.pack_log2);
+      const int head = (it.group << p.h.pack_log2) + (row & ((1 << p.h.pack_log2) - 1));
+      const bool live = token < p.h.queries;
+      float m = -INFINITY, l = 0.f;
+      bool ok = true;
+      if (it.n > 0 && t < it.tiles) {
+        for (int j = 0; j < it.n; ++j, ++steps) {
+          ok = wait_bounded(&s_full[t], steps & 1u, abort_flag, p.err, ATT_WAIT_NS);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const int valid = it.length - (it.k0 + j) * ATT_ROWS;
+          float s[64], mx[4];
+          tmem_load_64cols(t_s, s);
+          if (valid < 64) hide(s, valid);
+          top4(s, mx, true);
+          tmem_load_64cols(t_s + 64, s);
+          if (valid < ATT_ROWS) {
+            hide(s, valid - 64);
+            if (t == 0) {
+              // what lies behind the last key must not meet its P of zero: infinities and NaN would remain
+              const uint32_t n = kv + 2 * j + 1;
+              ok = wait_bounded(&kv_full[n % STAGES], (n / STAGES) & 1u, abort_flag, p.err, ATT_WAIT_NS);
+              if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+              }
+              uint4* v = reinterpret_cast<uint4*>(sKV + (n % STAGES) * TILE);
+              for (int i = valid * 8 + row; i < ATT_ROWS * 8; i += 128)
+#pragma unroll
+                for (int c = 0; c < DP / 64; ++c) v[c * (ATT_CHUNK / 16) + i] = make_uint4(0, 0, 0, 0);
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+          }
+          top4(s, mx, false);
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          if (j == 0) {
+            m = top;
+          } else {
+            const bool grows = (top - m) * p.scale_log2 > RESCALE_ABOVE;  // (from -inf: always)
+            if (__any_sync(0xffffffffu, grows)) {
+              const float factor = grows ? exp2_fast((m - top) * p.scale_log2) : 1.f;
+              if (grows) m = top;
+              l *= factor;
+              ok = wait_bounded(&pv_done[t], (steps - 1) & 1u, abort_flag, p.err, ATT_WAIT_NS);
+              if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after_sync();
+#pragma unroll
+              for (int c = 0; c < DP; c += 16) {
+                if (c >= p.mma_n) break;
+                float o[16];
+                tmem_load_16cols(t_o + c, o);
+                uint32_t w[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i] * factor);
+                tmem_store_16cols(t_o + c, w);
+              }
+            }
+          }
+          const float base = m == -INFINITY ? 0.f : m * p.scale_log2;
+          const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2), nb2 = f2_pack(-base, -base);
+          uint64_t sum[2] = {0, 0};
+          // the second half's P goes over the second half of S, which is in registers; then the first's
+          exponentials<T>(s, sc2, nb2, sum, t_s + 64);
+          tmem_load_64cols(t_s, s);
+          if (valid < 64) hide(s, valid);
+          exponentials<T>(s, sc2, nb2, sum, t_s);
+          const float2 total = f2_unpack(f2_add(sum[0], sum[1]));
+          l += total.x + total.y;
+          tmem_store_wait();
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[t]);
+        }
+        if (!ok) break;
+        ok = wait_bounded(&pv_done[t], (steps - 1) & 1u, abort_flag, p.err, ATT_WAIT_NS);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after_sync();
+      }
+      const bool some = it.n > 0;
+      kv += some ? 2 * it.n : 0;
+      if (t >= it.tiles) continue;
+      const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+      const float lse = some ? m * p.scale_log2 + log2f(l) : -INFINITY;
+      const int64_t at_lse = (static_cast<int64_t>(it.b) * p.h.heads + head) * p.h.queries + token;
+      if (live) {
+        if (p.splits > 1)
+          p.part_lse[static_cast<int64_t>(it.split) * p.h.batch * p.h.heads * p.h.queries + at_lse] = lse;
+        else if (p.lse != nullptr)
+          p.lse[at_lse] = lse;
+      }
+      T* out = static_cast<T*>(p.o) + it.b * p.o_strides.batch + token * p.o_strides.token + head * p.o_strides.head;
+      float* part = p.part_o + (((static_cast<int64_t>(it.split) * p.h.batch + it.b) * p.h.queries + token) *
+                                    p.h.heads + head) * p.h.head;
+#pragma unroll
+      for (int c = 0; c < DP; c += 32) {
+        if (c >= p.h.head) break;
+        float o[32];
+        __syncwarp();
+        if (some) {
+          tmem_load_32cols(t_o + c, o);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 32; i += 8) {
+          if (c + i >= p.h.head || !live) break;
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = some ? o[i + e] * inv : 0.f;
+          if (p.splits > 1) {
+            Raw8<float> r;
+            r.set(v);
+            r.store(part + c + i);
+          } else {
+            Raw8<T> r;
+            r.set(v);
+            r.store(out + c + i);
+          }
+        }
+      }
+      if (some) {
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&o_empty[t]);
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+// Parts of the keys joined: lse = log2 sum 2^lse_s, o = sum 2^(lse_s - lse) o_s.
+// A thread takes eight elements of a row.
+struct JoinParams {
+  AttHeads h;
+  AttStrides o_strides;
+  void* o;
+  float* lse;
+  const float* part_o;
+  const float* part_lse;
+  int splits;
+  int vectors;    // head / 8
+  int64_t count;  // rows * vectors
+};
+
+template <typename T>
+__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ JoinParams p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= p.count) return;
+  const int64_t row = i / p.vectors;  // (b * queries + token) * heads + head
+  const int vec = static_cast<int>(i - row * p.vectors);
+  const int head = static_cast<int>(row % p.h.heads);
+  const int64_t bt = row / p.h.heads;
+  const int token = static_cast<int>(bt % p.h.queries), b = static_cast<int>(bt / p.h.queries);
+  const int64_t rows = static_cast<int64_t>(p.h.batch) * p.h.queries * p.h.heads;
+  const int64_t at = (static_cast<int64_t>(b) * p.h.heads + head) * p.h.queries + token;
+  float top = -INFINITY;
+  for (int s = 0; s < p.splits; ++s) top = fmaxf(top, p.part_lse[s * rows + at]);
+  float v[8] = {}, total = 0.f;
+  for (int s = 0; s < p.splits; ++s) {
+    const float lse = p.part_lse[s * rows + at];
+    if (lse == -INFINITY) continue;  // no keys in this part
+    const float w = exp2f(lse - top);
+    total += w;
+    Raw8<float> r;
+    r.load(p.part_o + (s * rows + row) * p.h.head + vec * 8);
+    float u[8];
+    r.get(u);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = fmaf(w, u[e], v[e]);
+  }
+  const float inv = total > 0.f || total != total ? 1.f / total : 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] *= inv;
+  Raw8<T> r;
+  r.set(v);
+  r.store(static_cast<T*>(p.o) + b * p.o_strides.batch + token * p.o_strides.token + head * p.o_strides.head + vec * 8);
+  if (vec == 0 && p.lse != nullptr) p.lse[at] = total > 0.f || total != total ? top + log2f(total) : -INFINITY;
+}
+
+template <typename T, int DP>
+cudaError_t launch_fwd(const FwdParams& p, int num_sms, cudaStream_t stream) {
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = att_prepare(attn_fwd_kernel<T, DP>, FwdShape<DP>::SMEM, ready);
+  if (e != cudaSuccess) return e;
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(p.items, num_sms));
+  return launch_dependent(attn_fwd_kernel<T, DP>, dim3(grid), dim3(ATT_THREADS), FwdShape<DP>::SMEM, stream, p);
+}
+
+}  // namespace
+
+cudaError_t attn_forward(const AttCall& c, const void* q, const void* k, const void* v, void* o, float* lse,
+                         char* workspace, cudaStream_t stream) {
+  FwdParams p{};
+  p.h = c.h;
+  p.lengths = c.lengths;
+  p.o_strides = c.o;
+  p.o = o;
+  p.lse = lse;
+  p.blocks = (c.h.query_tiles() + 1) / 2;
+  const AttSplit sp = att_forward_split(c.h, c.num_sms);
+  p.splits = sp.splits;
+  p.split_tiles = sp.tiles;
+  p.items = static_cast<int64_t>(c.h.batch) * c.h.groups * p.splits * p.blocks;
+  p.mma_k = (c.h.head + 15) / 16;
+  p.mma_n = p.mma_k * 16;
+  p.scale_log2 = c.scale * 1.4426950408889634f;
+  p.err = c.err;
+  const int64_t rows = static_cast<int64_t>(c.h.batch) * c.h.queries * c.h.heads;
+  if (p.splits > 1) {
+    p.part_o = reinterpret_cast<float*>(workspace);
+    p.part_lse = p.part_o + rows * p.splits * c.h.head;
+  }
+  const int pack = 1 << c.h.pack_log2;
+  if (!att_encode(&p.q, q, c.dtype, c.h.batch, c.h.queries, c.h.heads, c.h.head, c.q, pack, ATT_ROWS / pack) ||
+      !att_encode(&p.k, k, c.dtype, c.h.batch, c.h.keys, c.h.kv_heads, c.h.head, c.k, 1, ATT_ROWS) ||
+      !att_encode(&p.v, v, c.dtype, c.h.batch, c.h.keys, c.h.kv_heads, c.h.head, c.v, 1, ATT_ROWS))
+    return cudaErrorInvalidValue;
+  const bool wide = c.h.head > 64, bf = c.dtype == PRM_BF16;
+  cudaError_t e = bf ? (wide ? launch_fwd<__nv_bfloat16, 128>(p, c.num_sms, stream)
+                             : launch_fwd<__nv_bfloat16, 64>(p, c.num_sms, stream))
+                     : (wide ? launch_fwd<__half, 128>(p, c.num_sms, stream)
+                             : launch_fwd<__half, 64>(p, c.num_sms, stream));
+  if (e != cudaSuccess || p.splits == 1) return e;
+  return attn_join(c, p.splits, o, lse, p.part_o, p.part_lse, stream);
+}
+
+cudaError_t attn_join(const AttCall& c, int splits, void* o, float* lse, const float* part_o, const float* part_lse,
+                      cudaStream_t stream) {
+  const int vectors = c.h.head / 8;
+  const int64_t count = static_cast<int64_t>(c.h.batch) * c.h.queries * c.h.heads * vectors;
+  const JoinParams p{c.h, c.o, o, lse, part_o, part_lse, splits, vectors, count};
+  return launch_dependent(c.dtype == PRM_BF16 ? attn_join_kernel<__nv_bfloat16> : attn_join_kernel<__half>,
+                          dim3(static_cast<unsigned>((count + 255) / 256)), dim3(256), 0, stream, p);
+}
+
+}  // namespace prm

@@ -113,6 +113,38 @@ class prm_rotary_desc(ctypes.Structure):
     ]
 
 
+class prm_attention_strides(ctypes.Structure):
+    _fields_ = [
+        ("batch", c_int64),
+        ("token", c_int64),
+        ("head", c_int64),
+    ]
+
+
+class prm_attention_desc(ctypes.Structure):
+    _fields_ = [
+        ("batch", c_int64),
+        ("queries", c_int64),
+        ("keys", c_int64),
+        ("heads", c_int64),
+        ("kv_heads", c_int64),
+        ("head", c_int64),
+        ("q", prm_attention_strides),
+        ("k", prm_attention_strides),
+        ("v", prm_attention_strides),
+        ("o", prm_attention_strides),
+        ("grad_o", prm_attention_strides),
+        ("dq", prm_attention_strides),
+        ("dk", prm_attention_strides),
+        ("dv", prm_attention_strides),
+        ("key_lengths", c_void_p),
+        ("length_bytes", c_int32),
+        ("dtype", c_int32),
+        ("scale", c_float),
+        ("reserved", c_int32),
+    ]
+
+
 # name -> (restype, argtypes), mirroring include/prm.h, include/prm_blocks.h and include/prm_attention.h
 SIGNATURES = {
     "prm_create": (c_int, [POINTER(c_void_p), c_int]),
@@ -167,6 +199,11 @@ SIGNATURES = {
     "prm_rotary": (c_int, [POINTER(prm_rotary_desc), c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
     "prm_dropout": (c_int, [c_void_p, c_int, c_void_p, c_void_p, c_int, c_int64, ctypes.c_double, c_uint64, c_void_p,
                             c_uint64, c_void_p]),
+    "prm_attention_workspace": (c_int, [POINTER(prm_attention_desc), POINTER(c_size_t), POINTER(c_size_t)]),
+    "prm_attention_forward": (c_int, [POINTER(prm_attention_desc), c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                      c_void_p, c_size_t, c_void_p]),
+    "prm_attention_backward": (c_int, [POINTER(prm_attention_desc), c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                       c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
 }
 
 _lib = None

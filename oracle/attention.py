@@ -53,3 +53,44 @@ def dropout(x, p, seed, offset=0, residual=None):
     keep = kept(x.size, p, seed, offset).reshape(x.shape)
     y = np.where(keep, x / (1.0 - p) if p < 1.0 else 0.0, 0.0)
     return y if residual is None else y + residual
+
+
+# -------------------------------------------------------- cross attention
+def _shared(t, heads):
+    """[keys, kv_heads, head] with every key head repeated for its query heads."""
+    return np.repeat(t, heads // t.shape[1], axis=1)
+
+
+def attention_probabilities(q, k, scale):
+    """P [heads, queries, keys] of one sequence, k cut to its keys."""
+    s = np.einsum("qhd,khd->hqk", q, _shared(k, q.shape[1])) * scale
+    p = np.exp(s - s.max(-1, keepdims=True))
+    return p / p.sum(-1, keepdims=True)
+
+
+def cross_attention(q, k, v, lengths, scale):
+    """q: [batch, queries, heads, head]; k, v: [batch, keys, kv_heads, head];
+    lengths: keys of each sequence."""
+    o = np.zeros(q.shape)
+    for b, n in enumerate(lengths):
+        if n > 0:
+            p = attention_probabilities(q[b], k[b, :n], scale)
+            o[b] = np.einsum("hqk,khd->qhd", p, _shared(v[b, :n], q.shape[2]))
+    return o
+
+
+def cross_attention_backward(do, q, k, v, lengths, scale):
+    """(dq, dk, dv)."""
+    dq, dk, dv = np.zeros(q.shape), np.zeros(k.shape), np.zeros(v.shape)
+    heads, kv_heads = q.shape[2], k.shape[2]
+    for b, n in enumerate(lengths):
+        if n <= 0:
+            continue
+        p = attention_probabilities(q[b], k[b, :n], scale)
+        dp = np.einsum("qhd,khd->hqk", do[b], _shared(v[b, :n], heads))
+        ds = p * (dp - (p * dp).sum(-1, keepdims=True)) * scale
+        dq[b] = np.einsum("hqk,khd->qhd", ds, _shared(k[b, :n], heads))
+        for out, w, t in ((dk, ds, q[b]), (dv, p, do[b])):
+            g = np.einsum("hqk,qhd->khd", w, t)
+            out[b, :n] = g.reshape(n, kv_heads, heads // kv_heads, -1).sum(2)
+    return dq, dk, dv

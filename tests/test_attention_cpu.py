@@ -152,3 +152,93 @@ def test_distinct():
     t = torch.zeros(4, 6, 8)
     assert attention._distinct(t) and attention._distinct(t.transpose(0, 2)) and attention._distinct(t[:, ::2, 1:5])
     assert not attention._distinct(t.as_strided((2, 3), (1, 1))) and not attention._distinct(t[:1].expand(3, 6, 8))
+
+
+# ---------------------------------------------------------- cross attention
+def test_attention_gradient_against_differences():
+    rng = np.random.default_rng(5)
+    q, do = rng.standard_normal((2, 3, 3, 4, 2))
+    k, v = rng.standard_normal((2, 3, 5, 2, 2))
+    lengths, scale, h = [5, 2, 0], 0.7, 1e-5
+    got = O.cross_attention_backward(do, q, k, v, lengths, scale)
+    for grad, a in zip(got, (q, k, v)):
+        for i in np.ndindex(*a.shape):
+            keep = a[i]
+            a[i] = keep + h
+            up = (O.cross_attention(q, k, v, lengths, scale) * do).sum()
+            a[i] = keep - h
+            down = (O.cross_attention(q, k, v, lengths, scale) * do).sum()
+            a[i] = keep
+            # truncation h^2 f''' / 6 ~ 1e-10 and cancellation 2^-53 |f| / h ~ 1e-10, with a margin of 100
+            assert abs(grad[i] - (up - down) / (2 * h)) <= 1e-8
+    assert not got[0][2].any() and not got[1][1, 2:].any() and not got[2][2].any()
+
+
+def _attn(strides=None, **kw):
+    v = dict(batch=2, queries=3, keys=5, heads=4, kv_heads=2, head=16, key_lengths=None, length_bytes=0,
+             dtype=N.PRM_BF16, scale=0.25, reserved=0)
+    v.update(kw)
+    names = ("q", "k", "v", "o", "grad_o", "dq", "dk", "dv")
+    rows = {n: (5, 2) if n in ("k", "v", "dk", "dv") else (3, 4) for n in names}
+    lay = {n: N.prm_attention_strides(t * h * 16, h * 16, 16) for n, (t, h) in rows.items()}
+    lay.update({n: N.prm_attention_strides(*s) for n, s in (strides or {}).items()})
+    return N.prm_attention_desc(**v, **lay)
+
+
+def test_attention_refusals(lib):
+    def fwd(q=16, k=16, v=16, o=16, lse=16, ws=None, n=0, **kw):
+        return lib.prm_attention_forward(_attn(**kw), q, k, v, o, lse, ws, n, None)
+
+    def back(g=16, q=16, k=16, v=16, o=16, lse=16, dq=16, dk=16, dv=16, ws=256, n=1 << 30, **kw):
+        return lib.prm_attention_backward(_attn(**kw), g, q, k, v, o, lse, dq, dk, dv, ws, n, None)
+
+    def sizes(**kw):
+        a, b = ctypes.c_size_t(7), ctypes.c_size_t(7)
+        rc = lib.prm_attention_workspace(_attn(**kw), a, b)
+        return rc if rc else (a.value, b.value)
+
+    for call in (fwd, back, sizes):
+        for bad in (dict(reserved=1), dict(dtype=N.PRM_FP32), dict(batch=-1), dict(queries=-1), dict(keys=-1),
+                    dict(heads=-1), dict(kv_heads=-1), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")),
+                    dict(scale=float("inf")), dict(key_lengths=16, length_bytes=2)):
+            assert call(**bad) == N.PRM_ERR_INVALID_ARG, bad
+        for bad in (dict(head=0), dict(head=12), dict(kv_heads=3), dict(kv_heads=0)):
+            assert call(**bad) == N.PRM_ERR_SHAPE, bad
+        for bad in (dict(head=136), dict(queries=1 << 31), dict(keys=1 << 31), dict(heads=1 << 17, kv_heads=1 << 17),
+                    dict(batch=1 << 21), dict(batch=1 << 20, heads=1 << 12),
+                    dict(batch=1 << 12, heads=1 << 12, queries=1 << 17)):
+            assert call(**bad) == N.PRM_ERR_UNSUPPORTED, bad
+    for call in (fwd, back):
+        for t in ("q", "k", "v", "o"):
+            assert call(**{t: None}) == N.PRM_ERR_INVALID_ARG, t
+            assert call(**{t: 8}) == N.PRM_ERR_ALIGNMENT, t
+        for t in ("q", "k", "v", "o") + (("grad_o", "dq", "dk", "dv") if call is back else ()):
+            assert call(strides={t: (640, 64, 12)}) == N.PRM_ERR_SHAPE, t      # heads overlap
+            assert call(strides={t: (640, 64, 20)}) == N.PRM_ERR_ALIGNMENT, t
+            assert call(strides={t: (1 << 38, 64, 16)}) == N.PRM_ERR_UNSUPPORTED, t
+        assert call(lse=2) == N.PRM_ERR_ALIGNMENT
+        assert call(ws=128, n=1 << 30) == N.PRM_ERR_ALIGNMENT
+        assert call(batch=0) == N.PRM_OK and call(heads=0, kv_heads=0) == N.PRM_OK
+    for t in ("g", "lse", "dq", "dk", "dv"):
+        assert back(**{t: None}) == N.PRM_ERR_INVALID_ARG, t
+    assert back(n=100) == N.PRM_ERR_WORKSPACE and back(ws=None) == N.PRM_ERR_WORKSPACE
+    assert fwd(queries=0) == N.PRM_OK
+    # a long key axis for few queries is split over CTAs, whose parts need room
+    forward, backward = sizes(batch=1, heads=1, kv_heads=1, queries=300, keys=100000)
+    assert forward > 0 and backward > 0
+    lay = {t: (1 << 30, 16, 16) for t in ("q", "k", "v", "o")}
+    assert fwd(batch=1, heads=1, kv_heads=1, queries=300, keys=100000, strides=lay) == N.PRM_ERR_WORKSPACE
+    assert sizes(queries=0) == (0, 0) and sizes(keys=0) == (0, 0) and sizes(batch=0) == (0, 0)
+    assert lib.prm_attention_workspace(_attn(), None, None) == N.PRM_ERR_INVALID_ARG
+    assert lib.prm_attention_forward(None, 16, 16, 16, 16, None, None, 0, None) == N.PRM_ERR_INVALID_ARG
+
+
+def test_attention_tensor_api_refuses():
+    q, k = torch.zeros(2, 3, 4, 16, dtype=torch.bfloat16), torch.zeros(2, 5, 2, 16, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        attention.cross_attention(q, k, k)
+    with pytest.raises(ValueError):
+        attention.cross_attention_backward(q, q, k, k, q, attention.AttentionSaved(torch.zeros(2, 4, 3), 0.25, 5))
+    assert attention._usable(q[:, :, 1:3]) and attention._usable(q.transpose(1, 2))
+    assert not attention._usable(q[..., 1:9]) and not attention._usable(q.transpose(2, 3))
+    assert not attention._usable(q[:, :1].expand(2, 3, 4, 16)) and not attention._usable(q[..., ::2])

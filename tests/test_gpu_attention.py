@@ -231,3 +231,219 @@ def test_dropout_refuses():
         args.update(bad)
         with pytest.raises(ValueError):
             prm.dropout(**args)
+
+
+# ---------------------------------------------------------- cross attention
+def _attention_inputs(B, Lq, Lk, H, Hkv, D, dtype=BF16, seed=0, size=1.5):
+    g = _gen(seed + B + Lq + 3 * Lk + 5 * H + 7 * Hkv + 11 * D)
+    return (_rand(g, B, Lq, H, D, dtype=dtype, scale=size), _rand(g, B, Lk, Hkv, D, dtype=dtype),
+            _rand(g, B, Lk, Hkv, D, dtype=dtype), _rand(g, B, Lq, H, D, dtype=dtype))
+
+
+def _tiny(u):
+    return 2.0 ** -25 if u == U[FP16] else 2.0 ** -126
+
+
+def _attention_bounds(do, q, k, v, lengths, scale, u):
+    """What o, dq, dk and dv may be off by, element by element, from the roundings that the header names and fp32
+    steps of 2^-24. S is off by (head + 3) steps of sum |q| |k|, 2^x by 2 steps more, and the row's sum and
+    maximum leave P relatively exact to that; P is rounded to 16 bits (u) as an operand, and sums over n terms in
+    fp32 add n steps. o is rounded once more (u), and delta is formed from it; dS is rounded (u). Gradients are
+    rounded once at the end (u). What lies below a type's normal range is off by half of its smallest step (fp16
+    2^-25), or left out (2^x below 2^-126)."""
+    e, tiny = 2.0 ** -24, _tiny(u)
+    out = [np.zeros(t.shape) for t in (q, q, k, v)]
+    heads, kv_heads, head = q.shape[2], k.shape[2], q.shape[3]
+    for b, n in enumerate(lengths):
+        if n <= 0:
+            continue
+        kk, vv = (np.repeat(t[b, :n], heads // kv_heads, axis=1) for t in (k, v))
+        p = O.attention_probabilities(q[b], k[b, :n], scale)
+        s_off = scale * (head + 3) * e * np.einsum("qhd,khd->hqk", np.abs(q[b]), np.abs(kk)).max(-1, keepdims=True)
+        off = 2 * s_off + (n + 40) * e                      # relative error of a normalised, unrounded P
+        pv = np.einsum("hqk,khd->qhd", p, np.abs(vv))
+        o_abs = np.abs(np.einsum("hqk,khd->qhd", p, vv))
+        off_q = off[..., 0].T[..., None]                    # [queries, heads, 1]
+        out[0][b] = (u + off_q) * pv * (1 + u) + u * o_abs + tiny * np.abs(vv).sum(0)[None]
+        dp_abs = np.einsum("qhd,khd->hqk", np.abs(do[b]), np.abs(vv))
+        delta_off = (np.abs(do[b]) * (out[0][b] + head * e * (o_abs + out[0][b]))).sum(-1).T[..., None]
+        dp = np.einsum("qhd,khd->hqk", do[b], vv)
+        ds = np.abs(p * (dp - (p * dp).sum(-1, keepdims=True)))
+        ds_off = ((u + off + 4 * e) * ds + p * (1 + off) * (head * e * dp_abs + delta_off)) * (1 + u) + tiny
+        terms = n * e
+        out[1][b] = scale * (np.einsum("hqk,khd->qhd", ds_off + terms * ds, np.abs(kk)))
+        for at, w, w_off, t in ((2, scale * ds, scale * ds_off, q[b]), (3, p, (u + off) * p + tiny, do[b])):
+            terms = heads // kv_heads * q.shape[1] * e
+            g = np.einsum("hqk,qhd->khd", w_off + terms * (w + w_off), np.abs(t))
+            out[at][b, :n] = g.reshape(n, kv_heads, heads // kv_heads, head).sum(2)
+    return out
+
+
+def _check_attention(q, k, v, do, lengths=None, scale=None, calls=None):
+    """Runs both passes and compares them; calls: (o, dq, dk, dv) made elsewhere."""
+    u = U[q.dtype]
+    n = None if lengths is None else torch.tensor(lengths, device="cuda")
+    if calls is None:
+        o, saved = prm.cross_attention(q, k, v, n, scale=scale, save=True)
+        calls = (o,) + tuple(prm.cross_attention_backward(do, q, k, v, o, saved, n, scale=scale))
+        assert torch.equal(prm.cross_attention(q, k, v, n, scale=scale), o)
+    cut = [k.shape[1]] * k.shape[0] if lengths is None else [max(0, min(x, k.shape[1])) for x in lengths]
+    scale = q.shape[3] ** -0.5 if scale is None else scale
+    host = [host64(t) for t in (do, q, k, v)]
+    for t in host[2:]:
+        for b, x in enumerate(cut):
+            t[b, x:] = 0.0
+    want = (O.cross_attention(*host[1:], cut, scale),) + O.cross_attention_backward(*host, cut, scale)
+    bounds = _attention_bounds(*host, cut, scale, u)
+    for name, got, ref, bound in zip(("o", "dq", "dk", "dv"), calls, want, bounds):
+        got = host64(got)
+        assert np.isfinite(got).all(), name
+        err = np.abs(got - ref) - (bound + u * np.abs(ref) + _tiny(u))  # (the output's own rounding)
+        assert (err <= 0).all(), (name, err.max(), np.abs(ref).max())
+    return calls
+
+
+# one of everything, edges of the query and key tiles, one and two tiles and more on both axes
+ATTENTION_SHAPES = [(1, 1, 1, 1, 1), (1, 2, 3, 1, 1), (2, 127, 129, 2, 2), (1, 128, 128, 1, 1), (1, 129, 127, 3, 3),
+                    (1, 256, 256, 2, 2), (1, 257, 130, 1, 1), (2, 300, 77, 2, 2), (1, 5, 1000, 2, 2),
+                    (1, 600, 385, 2, 1), (1, 513, 513, 1, 1)]
+
+
+@pytest.mark.parametrize("B,Lq,Lk,H,Hkv", ATTENTION_SHAPES)
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_shapes(B, Lq, Lk, H, Hkv, D):
+    _check_attention(*_attention_inputs(B, Lq, Lk, H, Hkv, D))
+
+
+@pytest.mark.parametrize("D", [8, 16, 24, 40, 56, 72, 80, 104, 120])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_attention_heads(D, dtype):
+    _check_attention(*_attention_inputs(2, 150, 140, 3, 3, D, dtype=dtype), lengths=[140, 133])
+
+
+@pytest.mark.parametrize("H,Hkv", [(2, 1), (4, 1), (8, 2), (6, 2), (12, 1), (32, 1), (64, 1), (7, 1), (40, 8)])
+@pytest.mark.parametrize("Lq", [1, 3, 70])
+def test_attention_shared_heads(H, Hkv, Lq):
+    _check_attention(*_attention_inputs(2, Lq, 200, H, Hkv, 64), lengths=[200, 65])
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_attention_lengths(dtype):
+    lengths = [0, 1, 63, 64, 65, 127, 128, 129, 191, 200, 300, -3]
+    _check_attention(*_attention_inputs(12, 40, 200, 2, 1, 64, dtype=dtype), lengths=lengths)
+    _check_attention(*_attention_inputs(12, 140, 200, 2, 1, 128, dtype=dtype), lengths=lengths)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("Lq", [1, 150])
+def test_attention_ignores_what_lies_behind_the_last_key(bad, Lq):
+    q, k, v, do = _attention_inputs(3, Lq, 300, 2, 2, 72)
+    lengths = [299, 130, 0]
+    want = _check_attention(q, k, v, do, lengths)
+    k, v = k.clone(), v.clone()
+    for b, n in enumerate(lengths):
+        k[b, n:] = bad
+        v[b, n:] = bad
+    for a, b in zip(_check_attention(q, k, v, do, lengths), want):
+        assert torch.equal(a, b)
+
+
+# long keys for few queries and long queries for few keys: ranges on different CTAs, some without work
+@pytest.mark.parametrize("B,Lq,Lk,H,Hkv,D,lengths", [(1, 9, 3000, 1, 1, 64, None), (2, 100, 2500, 2, 1, 128, [2500, 300]),
+                                                     (1, 2500, 60, 1, 1, 128, None), (2, 1500, 130, 4, 2, 64, [130, 0]),
+                                                     (1, 1200, 1300, 1, 1, 72, [1201])])
+def test_attention_in_parts(B, Lq, Lk, H, Hkv, D, lengths):
+    _check_attention(*_attention_inputs(B, Lq, Lk, H, Hkv, D), lengths=lengths)
+
+
+def test_attention_large_and_growing_scores():
+    # maxima that grow from tile to tile by more than the exponent's slack, and fall again
+    q, k, v, do = _attention_inputs(1, 200, 700, 2, 2, 64)
+    steps = torch.tensor([0.2, 3.0, 0.5, 8.0, 20.0, 1.0], device="cuda").repeat_interleave(128)[:700]
+    k = (k.float() * steps[None, :, None, None]).to(BF16)
+    _check_attention(q, k, v, do)
+    _check_attention(q, k, v, do, scale=2.0)
+    _check_attention(q, k, v, do, scale=1e-6)
+
+
+def test_attention_layouts():
+    B, Lq, Lk, H, D = 2, 90, 140, 4, 64
+    q, k, v, do = _attention_inputs(B, Lq, Lk, H, 2, D)
+    want = _check_attention(q, k, v, do, [140, 100])
+    n = torch.tensor([140, 100], device="cuda", dtype=torch.int32)
+
+    def same(q, k, v, do, n=n, **kw):
+        o, saved = prm.cross_attention(q, k, v, n, save=True, **kw)
+        got = (o,) + tuple(prm.cross_attention_backward(do, q, k, v, o, saved, n))
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+    kv = torch.stack([k, v], 2)                                      # one projection of the states
+    same(q, kv[:, :, 0], kv[:, :, 1], do)
+    qs = q.transpose(1, 2).contiguous().transpose(1, 2)              # heads before tokens
+    same(qs, k.transpose(1, 2).contiguous().transpose(1, 2), v, do.transpose(1, 2).contiguous().transpose(1, 2))
+    same(q.transpose(2, 3).contiguous().transpose(2, 3), k, v, do)   # elements apart: copied
+    wide = torch.zeros(B, Lq, H, 67, dtype=BF16, device="cuda")
+    wide[..., 1:65] = q
+    same(wide[..., 1:65], k, v, do)                                  # an odd start: copied
+    same(q, k, v, do, torch.tensor([140, 7, 100, 9], device="cuda")[::2])
+    held = torch.full((B, Lq, 3 * H, D), 3.0, dtype=BF16, device="cuda")
+    same(q, k, v, do, out=held[:, :, H:2 * H])
+    assert torch.equal(held[:, :, H:2 * H], want[0]) and (held[:, :, :H] == 3).all() and (held[:, :, 2 * H:] == 3).all()
+    # gradients into the halves of a fused projection's gradient; a gradient that is broadcast
+    o, saved = prm.cross_attention(q, k, v, n, save=True)
+    dkv, dq = torch.full_like(kv, float("nan")), torch.full_like(q, float("nan"))
+    got = prm.cross_attention_backward(do, q, k, v, o, saved, n, grads=(dq, dkv[:, :, 0], dkv[:, :, 1]))
+    assert got[0] is dq and torch.equal(dq, want[1])
+    assert torch.equal(dkv[:, :, 0], want[2]) and torch.equal(dkv[:, :, 1], want[3])
+    flat = torch.full((1,), 0.5, dtype=BF16, device="cuda").expand(B, Lq, H, D)
+    for a, b in zip(prm.cross_attention_backward(flat, q, k, v, o, saved, n),
+                    prm.cross_attention_backward(flat.contiguous(), q, k, v, o, saved, n)):
+        assert torch.equal(a, b)
+
+
+def test_attention_is_reproducible_and_leaves_its_inputs():
+    q, k, v, do = _attention_inputs(2, 700, 900, 4, 2, 128)
+    before = [t.clone() for t in (q, k, v, do)]
+    runs = []
+    for _ in range(4):
+        o, saved = prm.cross_attention(q, k, v, save=True)
+        runs.append((o,) + tuple(prm.cross_attention_backward(do, q, k, v, o, saved)) + (saved.lse,))
+    for r in runs[1:]:
+        for a, b in zip(r, runs[0]):
+            assert torch.equal(a, b)
+    for a, b in zip((q, k, v, do), before):
+        assert torch.equal(a, b)
+
+
+def test_attention_without_keys_or_queries():
+    q, k, v, do = _attention_inputs(2, 5, 7, 2, 2, 16)
+    o, saved = prm.cross_attention(q, k[:, :0], v[:, :0], save=True)
+    assert not o.any() and torch.isneginf(saved.lse).all()
+    dq, dk, dv = prm.cross_attention_backward(do, q, k[:, :0], v[:, :0], o, saved)
+    assert not dq.any() and dk.shape == (2, 0, 2, 16)
+    o, saved = prm.cross_attention(q[:, :0], k, v, save=True)
+    assert o.shape == (2, 0, 2, 16)
+    dq, dk, dv = prm.cross_attention_backward(do[:, :0], q[:, :0], k, v, o, saved)
+    assert not dk.any() and not dv.any() and dk.shape == k.shape
+    assert prm.cross_attention(q[:0], k[:0], v[:0]).shape == (0, 5, 2, 16)
+
+
+def test_attention_refuses():
+    q, k, v, do = _attention_inputs(2, 5, 7, 4, 2, 16)
+    n = torch.tensor([7, 3], device="cuda")
+    for bad in (dict(q=q.float()), dict(k=k.half()), dict(v=v[:, :6]), dict(q=q[:1]), dict(q=q[..., :12]),
+                dict(k=k[:, :, :1].expand(2, 7, 3, 16), v=v[:, :, :1].expand(2, 7, 3, 16)), dict(key_lengths=n[:1]),
+                dict(key_lengths=n.float()), dict(key_lengths=n.cpu()), dict(scale=0.0), dict(scale=-1.0),
+                dict(out=q[:1]), dict(out=q.half()), dict(out=q[:, :1].expand(2, 5, 4, 16)), dict(q=q[0])):
+        args = dict(q=q, k=k, v=v)
+        args.update(bad)
+        with pytest.raises(ValueError):
+            prm.cross_attention(**args)
+    o, saved = prm.cross_attention(q, k, v, save=True)
+    for bad in (dict(do=do[:1]), dict(o=o.half()), dict(saved=saved._replace(lse=saved.lse[:, :, :1])),
+                dict(scale=0.5), dict(k=k[:, :6], v=v[:, :6]), dict(grads=(q, k)), dict(grads=(q, k, v[:, :1]))):
+        args = dict(do=do, q=q, k=k, v=v, o=o, saved=saved)
+        args.update(bad)
+        with pytest.raises(ValueError):
+            prm.cross_attention_backward(**args)
