@@ -28,6 +28,42 @@
 extern "C" {
 #endif
 
+/* ---- linear layer -------------------------------------------------------
+ *   g = x weight^T + bias,  y = residual + act(g)
+ * x: tokens x k with row pitch ldx; weight: n x k; both of one 16-bit type
+ * `dtype` (PRM_BF16 or PRM_FP16). bias: n fp32, or NULL. residual: tokens x n
+ * with row pitch ld_residual, or NULL; y: tokens x n of y_dtype, which is the
+ * residual's type: dtype, or PRM_FP32 with a residual. n and k are multiples of
+ * 8, pitches too, pointers 16-byte aligned. act: PRM_ACT_SILU, _GELU, _GELU_TANH
+ * or PRM_ACT_NONE. tokens is any number. Products, bias, activation and residual
+ * are added in fp32 and rounded once. */
+#define PRM_ACT_NONE 3 /* y = residual + g */
+
+/* Bytes of the two passes' workspaces (256-byte aligned buffers).
+ * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED. */
+PRM_API int prm_linear_sizes(int64_t tokens, int64_t n, int64_t k, size_t* forward_workspace,
+                             size_t* backward_workspace);
+
+/* pre: tokens x n of dtype where g is left for the backward pass, or NULL;
+ * not written without an activation.
+ * Errors: INVALID_ARG, ALIGNMENT, WORKSPACE, UNSUPPORTED, CUDA. */
+PRM_API int prm_linear_forward(const void* x, int64_t ldx, const void* weight, const float* bias, const void* residual,
+                               int64_t ld_residual, void* y, int y_dtype, void* pre, void* workspace,
+                               size_t workspace_bytes, int64_t tokens, int64_t n, int64_t k, int act, int dtype,
+                               void* stream);
+
+/* From dy (of y, dy_dtype: dtype or PRM_FP32, row pitch lddy):
+ *   dg = dy act'(g)  (rounded to dtype),  dx = dg weight,  dweight = dg^T x,  dbias = sum of dg over the tokens
+ * (dbias of the unrounded dg). dx: tokens x k, dweight: n x k of dtype, dbias: n fp32;
+ * each may be NULL (not wanted), and then so may x (dweight) and weight (dx). They
+ * are written, not added to; with no tokens dweight and dbias are set to zero.
+ * The residual's gradient is dy itself. pre may be NULL without an activation.
+ * Errors as for the forward pass. */
+PRM_API int prm_linear_backward(const void* dy, int64_t lddy, int dy_dtype, const void* x, int64_t ldx,
+                                const void* weight, const void* pre, void* dx, void* dweight, float* dbias,
+                                void* workspace, size_t workspace_bytes, int64_t tokens, int64_t n, int64_t k, int act,
+                                int dtype, void* stream);
+
 /* ---- rotary positions ---------------------------------------------------
  * For every token and head the pairs (a, b) of the first `dim` of its `head`
  * elements are turned by the token's angle:

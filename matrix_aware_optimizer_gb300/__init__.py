@@ -2,8 +2,8 @@
 
 Next to the optimizer, the operators of a transformer block whose parameters
 it updates, forward and backward: the gated feed-forward block, the norms
-around a block and the token embedding; and for the attention half cross
-attention, rotary positions and dropout.
+around a block and the token embedding; and for the attention half the
+linear layer, cross attention, rotary positions and dropout.
 
 The compute lives in libprm.so (CUDA kernels for sm_103a behind a C ABI,
 declared in include/prm.h, include/prm_blocks.h and include/prm_attention.h);
@@ -15,8 +15,8 @@ from .native import PrmError, prm_branch  # noqa: F401
 
 _BLOCKS = ("gated_ffn", "gated_ffn_backward", "block_norm", "block_norm_backward", "embedding",
            "embedding_backward", "blocks_sync_status")
-_ATTENTION = ("cross_attention", "cross_attention_backward", "RotaryPlan", "rotary_plan", "rotary", "rotary_backward",
-              "dropout", "dropout_backward")
+_ATTENTION = ("linear", "linear_backward", "cross_attention", "cross_attention_backward", "RotaryPlan", "rotary_plan",
+              "rotary", "rotary_backward", "dropout", "dropout_backward")
 
 
 def __getattr__(name):

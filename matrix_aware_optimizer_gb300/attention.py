@@ -14,13 +14,136 @@ from typing import NamedTuple, Optional, Sequence, Union
 import torch
 
 from . import native as N
-from .blocks import _DTYPE, _HALF, _elsewhere, _is_elsewhere, _ptr, _raw_stream
+from .blocks import _ACT, _DTYPE, _HALF, _elsewhere, _is_elsewhere, _ptr, _raw_stream, _rows16
 
 _ROTARY = struct.Struct("=13q4ifi")  # prm_rotary_desc
 assert _ROTARY.size == N.ctypes.sizeof(N.prm_rotary_desc)
 _ATTN = struct.Struct("=30qQ2ifi")  # prm_attention_desc
 assert _ATTN.size == N.ctypes.sizeof(N.prm_attention_desc)
+_LINEAR_ACT = {None: N.PRM_ACT_NONE, **_ACT}
 _LAYOUT = {"half": N.PRM_ROTARY_HALF, "interleaved": N.PRM_ROTARY_INTERLEAVED}
+
+
+# ------------------------------------------------------------- linear layer
+class LinearSaved(NamedTuple):
+    """What linear leaves for its backward pass: x weight^T + bias in x's type
+    (None without an activation), and the sizes, activation and type of the
+    pass."""
+    pre: Optional[torch.Tensor]
+    tokens: int
+    features: int
+    act: Optional[str]
+    dtype: torch.dtype
+
+
+@functools.lru_cache(maxsize=256)
+def _linear_sizes(tokens, n, k):
+    forward, backward = N.c_size_t(), N.c_size_t()
+    N.check(N.load().prm_linear_sizes(tokens, n, k, forward, backward), "prm_linear_sizes")
+    return forward.value, backward.value
+
+
+def _linear_check(x, weight, act):
+    dt, device = x.dtype, x.get_device()
+    if act not in _LINEAR_ACT:
+        raise ValueError(f"act must be None or one of {sorted(_ACT)}")
+    if dt not in _HALF or device < 0 or x.dim() == 0:
+        raise ValueError("x must be a bfloat16 or float16 CUDA tensor")
+    k = x.shape[-1]
+    if weight.dim() != 2 or weight.shape[1] != k or weight.dtype is not dt or weight.get_device() != device \
+            or not weight.is_contiguous():
+        raise ValueError("weight must be a contiguous n x k tensor of x's type and device, k the last extent of x")
+    n = weight.shape[0]
+    if n < 1 or k < 1 or n % 8 or k % 8:
+        raise ValueError("n and k must be multiples of 8")
+    if weight.data_ptr() % 16:
+        raise ValueError("weight must start on 16 bytes")
+    return n, k, device
+
+
+def _rows(t, n):
+    """t as rows of n elements whose pitch is a multiple of 8, from a 16-byte
+    boundary: (tensor, pitch). Other layouts are copied."""
+    t, pitch = _rows16(t, n)
+    return t, pitch if t.shape[0] > 1 else n
+
+
+def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None, act: Optional[str] = None,
+           residual: Optional[torch.Tensor] = None, save: bool = False,
+           stream: Optional[torch.cuda.Stream] = None):
+    """Linear layer, y = residual + act(x weight^T + bias).
+
+    x: [..., k] bf16 or fp16; weight: [n, k] of x's type; n and k multiples of
+    8. bias: [n] fp32. act: None, "silu", "gelu" (erf) or "gelu_tanh". residual:
+    [..., n] of x's type or fp32 (the residual stream); y is of its type, else of
+    x's. Everything is added in fp32 and rounded once. Returns y, or (y, saved)
+    with save=True, saved for linear_backward (autograd does not see the call).
+    """
+    n, k, device = _linear_check(x, weight, act)
+    if bias is not None and (bias.dtype is not torch.float32 or bias.shape != (n,) or bias.get_device() != device
+                             or not bias.is_contiguous() or bias.data_ptr() % 16):
+        raise ValueError("bias must be a contiguous float32 tensor of n elements that starts on 16 bytes")
+    if residual is not None and (residual.shape[:-1] != x.shape[:-1] or residual.dim() == 0 or residual.shape[-1] != n
+                                 or residual.dtype not in (x.dtype, torch.float32)
+                                 or residual.get_device() != device):
+        raise ValueError("residual must be y's shape, x's type or float32, on x's device")
+    if _is_elsewhere(device, stream):
+        with _elsewhere(device, stream, x, weight, bias, residual):
+            return linear(x, weight, bias, act, residual, save)
+    x2, ldx = _rows(x, k)
+    r2, ldr = (None, n) if residual is None else _rows(residual, n)
+    tokens = x2.shape[0]
+    y = torch.empty((*x.shape[:-1], n), dtype=x.dtype if residual is None else residual.dtype, device=x.device)
+    pre = x.new_empty((tokens, n)) if save and act is not None else None
+    n_ws = _linear_sizes(tokens, n, k)[0]
+    ws = x.new_empty(n_ws, dtype=torch.uint8) if n_ws else None
+    rc = N.load().prm_linear_forward(x2.data_ptr(), ldx, weight.data_ptr(), _ptr(bias), _ptr(r2), ldr, y.data_ptr(),
+                                     _DTYPE[y.dtype], _ptr(pre), _ptr(ws), n_ws, tokens, n, k, _LINEAR_ACT[act],
+                                     _DTYPE[x.dtype], _raw_stream(device))
+    if rc:
+        N.check(rc, "prm_linear_forward")
+    return (y, LinearSaved(pre, tokens, n, act, x.dtype)) if save else y
+
+
+def linear_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, saved: LinearSaved,
+                    act: Optional[str] = None, need_dx: bool = True, need_dbias: bool = True,
+                    grad: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
+    """Gradients of linear: (dx, dweight, dbias), dx and dweight of x's type,
+    dbias fp32; dx and dbias None where not needed.
+
+    dy: of y, in y's type (which is fp32 after an fp32 residual; the residual's
+    gradient is dy itself). act, x and weight are those of the pass that made
+    `saved`. grad: a tensor of weight's shape and type to write dweight into (it is
+    overwritten), e.g. the buffer that PeriodicRowMuon has registered.
+    """
+    n, k, device = _linear_check(x, weight, act)
+    if dy.dim() == 0 or dy.shape[-1] != n or dy.shape[:-1] != x.shape[:-1] \
+            or dy.dtype not in (x.dtype, torch.float32) or dy.get_device() != device:
+        raise ValueError("dy must be y's shape and type, on x's device")
+    if saved.features != n or saved.act != act or saved.dtype is not x.dtype:
+        raise ValueError("saved comes from a pass with another weight, another act or another type")
+    if grad is not None and (grad.shape != weight.shape or grad.dtype is not weight.dtype
+                             or grad.get_device() != device or not grad.is_contiguous() or grad.data_ptr() % 16):
+        raise ValueError("grad must be a contiguous tensor of weight's shape and type that starts on 16 bytes")
+    if _is_elsewhere(device, stream):
+        with _elsewhere(device, stream, dy, x, weight, saved.pre, grad):
+            return linear_backward(dy, x, weight, saved, act, need_dx, need_dbias, grad)
+    x2, ldx = _rows(x, k)
+    dy2, lddy = _rows(dy, n)
+    tokens = x2.shape[0]
+    if saved.tokens != tokens:
+        raise ValueError("saved does not belong to this x")
+    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if need_dx else None
+    dweight = torch.empty_like(weight) if grad is None else grad
+    dbias = x.new_empty(n, dtype=torch.float32) if need_dbias else None
+    n_ws = _linear_sizes(tokens, n, k)[1]
+    ws = x.new_empty(n_ws, dtype=torch.uint8)
+    rc = N.load().prm_linear_backward(dy2.data_ptr(), lddy, _DTYPE[dy.dtype], x2.data_ptr(), ldx, weight.data_ptr(),
+                                      _ptr(saved.pre), _ptr(dx), dweight.data_ptr(), _ptr(dbias), ws.data_ptr(), n_ws,
+                                      tokens, n, k, _LINEAR_ACT[act], _DTYPE[x.dtype], _raw_stream(device))
+    if rc:
+        N.check(rc, "prm_linear_backward")
+    return dx, dweight, dbias
 
 
 # --------------------------------------------------------- rotary positions

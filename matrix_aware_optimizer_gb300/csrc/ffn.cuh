@@ -1,5 +1,5 @@
-// Activations of the gated feed-forward block, in fp32, and its kernels for a
-// few tokens.
+// Activations of the gated feed-forward block and of the linear layer, in
+// fp32, and their kernels for a few tokens.
 #pragma once
 
 #include <atomic>
@@ -18,8 +18,11 @@ constexpr float FFN_INV_SQRT_2PI = 0.3989422804014327f;
 
 // (1 + tanh(t)) / 2 = 1 / (1 + exp(-2 t)), so the tanh form of gelu is
 // g sigmoid(2 t): no cancellation for negative g.
+constexpr int ACT_NONE = 3;  // PRM_ACT_NONE, of the linear layer alone
+
 template <int ACT>
 __device__ __forceinline__ float ffn_act(float g) {
+  if constexpr (ACT == ACT_NONE) return g;
   if constexpr (ACT == PRM_ACT_SILU) return g * ffn_sigmoid(g);
   if constexpr (ACT == PRM_ACT_GELU) return 0.5f * g * (1.f + erff(g * FFN_SQRT_HALF));
   return g * ffn_sigmoid(2.f * FFN_SQRT_2_PI * fmaf(0.044715f * g * g, g, g));
@@ -28,7 +31,10 @@ __device__ __forceinline__ float ffn_act(float g) {
 // act(g) and act'(g).
 template <int ACT>
 __device__ __forceinline__ void ffn_act_grad(float g, float* a, float* da) {
-  if constexpr (ACT == PRM_ACT_SILU) {
+  if constexpr (ACT == ACT_NONE) {
+    *a = g;
+    *da = 1.f;
+  } else if constexpr (ACT == PRM_ACT_SILU) {
     const float s = ffn_sigmoid(g);
     *a = g * s;
     *da = s * fmaf(g, 1.f - s, 1.f);
@@ -56,5 +62,22 @@ inline bool ffn_few(int64_t tokens, int64_t d, int64_t f) {
 cudaError_t ffn_few_forward(const void* x, int64_t ldx, const void* w_gate, const void* w_up, const void* w_down,
                             void* h, uint4* gu, void* y, int tokens, int d, int f, int act, int dtype,
                             cudaStream_t stream);
+
+// The linear layer's y = act(x w^T + bias) + residual for as few tokens, and
+// x w^T + bias in pre where that is not NULL. y and residual are fp32 where
+// `wide`, else of dtype.
+struct LinearFew {
+  const void* x;
+  int64_t ldx;
+  const void* w;
+  const float* bias;
+  const void* residual;
+  int64_t ld_residual;
+  void* y;
+  void* pre;
+  int tokens, n, k;
+  bool wide;
+};
+cudaError_t linear_few_forward(const LinearFew& p, int act, int dtype, cudaStream_t stream);
 
 }  // namespace prm

@@ -1,4 +1,4 @@
-// Gated feed-forward block for a few tokens (a sampling step): the products
+// Gated feed-forward block and linear layer for a few tokens (a sampling step): the products
 // are matrix-vector products, bound by reading each weight once, and run on
 // CUDA cores. A 256-row tensor-core tile would be empty but for these rows.
 //
@@ -33,10 +33,20 @@ struct FewParams {
   uint4* gu;            // GLU: packed g and u for the backward pass, or NULL
   int tokens, rows, K;
   int split;            // warps that share a row: 1, 2, 4 or 8
+  // LINEAR alone (see LinearFew)
+  const float* bias = nullptr;
+  const void* residual = nullptr;
+  int64_t ld_residual = 0;
+  void* pre = nullptr;
+  bool wide = false;
 };
 
-template <typename T, int NT, bool GLU, int ACT>
+// What the sums become: h, y of the down projection, or a linear layer's y.
+constexpr int FEW_GLU = 0, FEW_DOWN = 1, FEW_LINEAR = 2;
+
+template <typename T, int NT, int USE, int ACT>
 __global__ void __launch_bounds__(FEW_THREADS, NT <= 4 ? 2 : 1) ffn_few_kernel(const __grid_constant__ FewParams p) {
+  constexpr bool GLU = USE == FEW_GLU;
   __shared__ float part[FEW_WARPS][NT * FEW_ROWS];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int piece = warp % p.split;  // this warp's part of K
@@ -71,7 +81,7 @@ __global__ void __launch_bounds__(FEW_THREADS, NT <= 4 ? 2 : 1) ffn_few_kernel(c
         wv[a][r] = k + a * step < p.K ? __ldcs(reinterpret_cast<const uint4*>(w[r] + k + a * step))
                                       : make_uint4(0, 0, 0, 0);
   };
-  if (GLU) {
+  if (USE != FEW_DOWN) {
     pdl_wait();  // the weights and x may be the kernels' before this one
     pdl_launch_dependents();
     load_w(k0);
@@ -143,26 +153,40 @@ __global__ void __launch_bounds__(FEW_THREADS, NT <= 4 ? 2 : 1) ffn_few_kernel(c
     }
     v = ffn_act<ACT>(v) * u;
   }
+  if constexpr (USE == FEW_LINEAR) {
+    const int64_t at = static_cast<int64_t>(t) * p.rows + row;
+    if (p.bias != nullptr) v += p.bias[row];
+    if (p.pre != nullptr) static_cast<T*>(p.pre)[at] = from_f32<T>(v);
+    v = ffn_act<ACT>(v);
+    const int64_t from = t * p.ld_residual + row;
+    if (p.residual != nullptr)
+      v += p.wide ? static_cast<const float*>(p.residual)[from] : to_f32(static_cast<const T*>(p.residual)[from]);
+    if (p.wide) {
+      static_cast<float*>(p.out)[at] = v;
+      return;
+    }
+  }
   static_cast<T*>(p.out)[static_cast<int64_t>(t) * p.rows + row] = from_f32<T>(v);
 }
 
-template <typename T, int NT, bool GLU, int ACT>
+template <typename T, int NT, int USE, int ACT>
 cudaError_t launch(FewParams p, cudaStream_t stream) {
+  constexpr bool GLU = USE == FEW_GLU;
   const int64_t groups = (static_cast<int64_t>(p.rows) * (GLU ? 2 : 1) + FEW_ROWS - 1) / FEW_ROWS;
   // about 24 warps per SM, each with a full step of K at least
   p.split = 1;
   while (p.split < FEW_WARPS && groups * p.split < 152 * 24 && p.split * 2 * 256 <= p.K) p.split *= 2;
   const int64_t per_cta = FEW_WARPS / p.split;
-  return launch_dependent(ffn_few_kernel<T, NT, GLU, ACT>, dim3(static_cast<unsigned>((groups + per_cta - 1) / per_cta)),
+  return launch_dependent(ffn_few_kernel<T, NT, USE, ACT>, dim3(static_cast<unsigned>((groups + per_cta - 1) / per_cta)),
                           dim3(FEW_THREADS), 0, stream, p);
 }
 
 template <typename T, int NT>
 cudaError_t both(const FewParams& up, const FewParams& down, int act, cudaStream_t stream) {
-  const cudaError_t e = act == PRM_ACT_SILU   ? launch<T, NT, true, PRM_ACT_SILU>(up, stream)
-                        : act == PRM_ACT_GELU ? launch<T, NT, true, PRM_ACT_GELU>(up, stream)
-                                              : launch<T, NT, true, PRM_ACT_GELU_TANH>(up, stream);
-  return e == cudaSuccess ? launch<T, NT, false, 0>(down, stream) : e;
+  const cudaError_t e = act == PRM_ACT_SILU   ? launch<T, NT, FEW_GLU, PRM_ACT_SILU>(up, stream)
+                        : act == PRM_ACT_GELU ? launch<T, NT, FEW_GLU, PRM_ACT_GELU>(up, stream)
+                                              : launch<T, NT, FEW_GLU, PRM_ACT_GELU_TANH>(up, stream);
+  return e == cudaSuccess ? launch<T, NT, FEW_DOWN, 0>(down, stream) : e;
 }
 
 template <typename T>
@@ -173,7 +197,33 @@ cudaError_t by_tokens(const FewParams& up, const FewParams& down, int act, cudaS
   return both<T, 8>(up, down, act, stream);
 }
 
+template <typename T, int ACT>
+cudaError_t linear(const FewParams& p, cudaStream_t stream) {
+  if (p.tokens == 1) return launch<T, 1, FEW_LINEAR, ACT>(p, stream);
+  if (p.tokens == 2) return launch<T, 2, FEW_LINEAR, ACT>(p, stream);
+  if (p.tokens <= 4) return launch<T, 4, FEW_LINEAR, ACT>(p, stream);
+  return launch<T, 8, FEW_LINEAR, ACT>(p, stream);
+}
+
+template <typename T>
+cudaError_t linear(const FewParams& p, int act, cudaStream_t stream) {
+  if (act == PRM_ACT_SILU) return linear<T, PRM_ACT_SILU>(p, stream);
+  if (act == PRM_ACT_GELU) return linear<T, PRM_ACT_GELU>(p, stream);
+  if (act == PRM_ACT_GELU_TANH) return linear<T, PRM_ACT_GELU_TANH>(p, stream);
+  return linear<T, ACT_NONE>(p, stream);
+}
+
 }  // namespace
+
+cudaError_t linear_few_forward(const LinearFew& p, int act, int dtype, cudaStream_t stream) {
+  FewParams q{p.x, p.ldx, {p.w, nullptr}, p.y, nullptr, p.tokens, p.n, p.k, 1};
+  q.bias = p.bias;
+  q.residual = p.residual;
+  q.ld_residual = p.ld_residual;
+  q.pre = p.pre;
+  q.wide = p.wide;
+  return dtype == PRM_BF16 ? linear<__nv_bfloat16>(q, act, stream) : linear<__half>(q, act, stream);
+}
 
 cudaError_t ffn_few_forward(const void* x, int64_t ldx, const void* w_gate, const void* w_up, const void* w_down,
                             void* h, uint4* gu, void* y, int tokens, int d, int f, int act, int dtype,

@@ -1,0 +1,360 @@
+// Linear layer with bias, activation and residual:
+//   g = x W^T + b,  y = residual + act(g)
+//   dg = dy act'(g),  dx = dg W,  dW = dg^T x,  db = sum over tokens of dg
+//
+// Forward: one launch of the block GEMM (block_gemm.cuh) whose epilogue adds
+// the bias, takes the activation and adds the residual in registers; a few
+// tokens run on CUDA cores (ffn_few.cu). Backward: dx and dW from one queue of
+// the same kernel. dg is dy itself where there is no activation and dy has
+// the operands' type; else one pass over dy (and g) forms it in 16 bits, since it
+// is the operand of both products. The same pass, or one over dy alone, takes
+// the bias' gradient as sums over blocks of rows, which a second kernel adds
+// in order.
+//
+// For an activation g is kept in the operands' type: its rounding moves dg by
+// |g act''(g) / act'(g)| of a step, less than dg's own rounding for all but the
+// few elements around a root of act'.
+#include "block_gemm.cuh"
+#include "prm_attention.h"
+
+namespace prm {
+namespace {
+
+// ---------------------------------------------------------- counters, dg, db
+__global__ void __launch_bounds__(256) clear_kernel(uint32_t* data, int n) {
+  pdl_wait();
+  pdl_launch_dependents();
+  for (int i = threadIdx.x; i < n; i += 256) data[i] = 0;
+}
+
+constexpr int DG_COLS = 256;  // columns of a CTA: 32 threads of eight, eight rows at a time
+struct DgParams {
+  const void* dy;
+  int64_t lddy;
+  const void* g;    // tokens x n, or NULL
+  void* dg;         // tokens x n, or NULL where dy is dg
+  float* partial;   // [row block][n], or NULL
+  uint32_t* zero;   // counters to clear for the products
+  int zero_count;
+  int64_t tokens;
+  int n;
+  int64_t block_rows;
+};
+
+template <typename T, typename DY, int ACT>
+__global__ void __launch_bounds__(256) linear_dg_kernel(const __grid_constant__ DgParams p) {
+  __shared__ float sums[8][DG_COLS + 8];
+  pdl_wait();
+  pdl_launch_dependents();
+  if (blockIdx.x == 0 && blockIdx.y == 0)
+    for (int i = threadIdx.x; i < p.zero_count; i += 256) p.zero[i] = 0;
+  const int lane = threadIdx.x & 31, part = threadIdx.x >> 5;
+  const int col = blockIdx.x * DG_COLS + lane * 8;
+  const int64_t r0 = blockIdx.y * p.block_rows, r1 = min(r0 + p.block_rows, p.tokens);
+  float sum[8] = {};
+  if (col < p.n) {
+    constexpr int AHEAD = 4;
+    for (int64_t r = r0 + part; r < r1; r += 8 * AHEAD) {
+      Raw8<DY> dy[AHEAD];
+      Raw8<T> g[AHEAD];
+#pragma unroll
+      for (int a = 0; a < AHEAD; ++a)
+        if (r + 8 * a < r1) {
+          dy[a].load(static_cast<const DY*>(p.dy) + (r + 8 * a) * p.lddy + col);
+          if (ACT != ACT_NONE) g[a].load(static_cast<const T*>(p.g) + (r + 8 * a) * p.n + col);
+        }
+#pragma unroll
+      for (int a = 0; a < AHEAD; ++a) {
+        if (r + 8 * a >= r1) break;
+        float v[8];
+        dy[a].get(v);
+        if constexpr (ACT != ACT_NONE) {
+          float u[8];
+          g[a].get(u);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            float act, slope;
+            ffn_act_grad<ACT>(u[e], &act, &slope);
+            v[e] *= slope;
+          }
+        }
+        if (p.dg != nullptr) {
+          Raw8<T> out;
+          out.set(v);
+          out.store(static_cast<T*>(p.dg) + (r + 8 * a) * p.n + col);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] += v[e];
+      }
+    }
+  }
+  if (p.partial == nullptr) return;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sums[part][lane * 8 + e] = sum[e];
+  __syncthreads();
+  const int c = blockIdx.x * DG_COLS + threadIdx.x;
+  if (c >= p.n) return;
+  float total = 0.f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) total += sums[k][threadIdx.x];
+  p.partial[static_cast<int64_t>(blockIdx.y) * p.n + c] = total;
+}
+
+__global__ void __launch_bounds__(128) linear_db_kernel(const float* partial, float* db, int n, int blocks) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int c = blockIdx.x * 128 + threadIdx.x;
+  if (c >= n) return;
+  float total = 0.f;
+#pragma unroll 8
+  for (int b = 0; b < blocks; ++b) total += partial[static_cast<int64_t>(b) * n + c];
+  db[c] = total;
+}
+
+template <typename T, typename DY>
+cudaError_t launch_dg(const DgParams& p, int act, dim3 grid, cudaStream_t stream) {
+  void (*kernel)(DgParams) = act == PRM_ACT_SILU        ? linear_dg_kernel<T, DY, PRM_ACT_SILU>
+                             : act == PRM_ACT_GELU      ? linear_dg_kernel<T, DY, PRM_ACT_GELU>
+                             : act == PRM_ACT_GELU_TANH ? linear_dg_kernel<T, DY, PRM_ACT_GELU_TANH>
+                                                        : linear_dg_kernel<T, DY, ACT_NONE>;
+  return launch_dependent(kernel, grid, dim3(256), 0, stream, p);
+}
+
+// -------------------------------------------------------------------- host
+template <int EPI>
+cudaError_t launch_linear(BlockGemmParams& p, int act, int dtype, int num_sms, cudaStream_t stream) {
+  if (act == ACT_NONE) return launch<EPI, ACT_NONE>(p, dtype, num_sms, stream);
+  return launch_act<EPI>(p, act, dtype, num_sms, stream);
+}
+
+// CUDA cores where they are faster: as for the feed-forward block's products.
+bool linear_few(int64_t tokens, int64_t n, int64_t k) { return ffn_few(tokens, n, k); }
+
+// Where both gradients' tiles together leave half of the CTA pairs idle, each
+// is split along K over as many as there are.
+struct GradSplit {
+  int dx, dw;  // parts of a tile
+};
+int parts_of(int64_t tiles, int64_t k) {
+  const int64_t kb = (k + BK - 1) / BK;
+  const int64_t pays = static_cast<int64_t>(std::sqrt(static_cast<double>(kb) / 2)) + 1;
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({AT_ONCE / tiles, kb / MIN_PART, pays, 16})));
+}
+GradSplit grad_split(int64_t T, int64_t n, int64_t k, bool need_dx) {
+  const int64_t tiles = tiles_of(n, k, BN) + (need_dx ? tiles_of(T, k, BN) : 0);
+  return {parts_of(tiles, n), parts_of(tiles, T)};
+}
+
+struct LinearSizes {
+  size_t fwd_counters, fwd;
+  size_t sums_at, dx_at, dw_at, counters_at, bwd;  // dg at 0
+  int dx_counters, dw_counters;
+  int row_blocks;
+  int64_t block_rows;
+  Split y;
+  GradSplit grads;
+};
+
+LinearSizes linear_sizes(int64_t T, int64_t n, int64_t k) {
+  LinearSizes s{};
+  if (T == 0) return s;
+  s.y = split_last_wave(T, n, k);
+  s.fwd_counters = partial_bytes(s.y);
+  s.fwd = s.fwd_counters + round_up(counter_bytes(s.y), 256);
+  // rows in blocks: about eight CTAs per SM over all columns, 32 rows at least
+  const int64_t strips = (n + DG_COLS - 1) / DG_COLS;
+  const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((T + 31) / 32, 8 * 152 / strips));
+  s.block_rows = (T + blocks - 1) / blocks;
+  s.row_blocks = static_cast<int>((T + s.block_rows - 1) / s.block_rows);
+  s.grads = grad_split(T, n, k, true);
+  size_t at = round_up(static_cast<size_t>(T) * n * 2, 256);
+  s.sums_at = at;
+  at += round_up(static_cast<size_t>(s.row_blocks) * n * sizeof(float), 256);
+  auto parts = [&](int64_t tiles, int splits, int* counters) {
+    const Split q{0, tiles, splits};
+    const size_t here = at;
+    if (splits > 1) {
+      at += partial_bytes(q);
+      *counters = static_cast<int>(counter_bytes(q) / 4);
+    }
+    return here;
+  };
+  s.dx_at = parts(tiles_of(T, k, BN), s.grads.dx, &s.dx_counters);
+  s.dw_at = parts(tiles_of(n, k, BN), s.grads.dw, &s.dw_counters);
+  s.counters_at = at;
+  s.bwd = round_up(at + static_cast<size_t>(s.dx_counters + s.dw_counters) * 4, 256);
+  return s;
+}
+
+int linear_check(int64_t T, int64_t n, int64_t k) {
+  if (T < 0 || n < 1 || k < 1) return PRM_ERR_INVALID_ARG;
+  if (n % 8 != 0 || k % 8 != 0) return PRM_ERR_ALIGNMENT;
+  if (T >= (int64_t(1) << 31) - 256 || n >= (int64_t(1) << 24) || k >= (int64_t(1) << 24)) return PRM_ERR_UNSUPPORTED;
+  constexpr int64_t MOST = int64_t(1) << 30;  // tiles are counted in 32 bits
+  if (tiles_of(T, n, BN) > MOST || tiles_of(T, k, BN) > MOST || tiles_of(n, k, BN) > MOST) return PRM_ERR_UNSUPPORTED;
+  return PRM_OK;
+}
+
+bool half_type(int t) { return t == PRM_BF16 || t == PRM_FP16; }
+
+}  // namespace
+}  // namespace prm
+
+extern "C" int prm_linear_sizes(int64_t tokens, int64_t n, int64_t k, size_t* forward_workspace,
+                                size_t* backward_workspace) {
+  using namespace prm;
+  if (forward_workspace == nullptr || backward_workspace == nullptr) return PRM_ERR_INVALID_ARG;
+  const int rc = linear_check(tokens, n, k);
+  if (rc != PRM_OK) return rc;
+  const LinearSizes s = linear_sizes(tokens, n, k);
+  *forward_workspace = s.fwd;
+  *backward_workspace = s.bwd;
+  return PRM_OK;
+}
+
+extern "C" int prm_linear_forward(const void* x, int64_t ldx, const void* weight, const float* bias,
+                                  const void* residual, int64_t ld_residual, void* y, int y_dtype, void* pre,
+                                  void* workspace, size_t workspace_bytes, int64_t tokens, int64_t n, int64_t k,
+                                  int act, int dtype, void* stream) {
+  using namespace prm;
+  if (!half_type(dtype) || act < PRM_ACT_SILU || act > PRM_ACT_NONE) return PRM_ERR_INVALID_ARG;
+  if (y_dtype != dtype && (y_dtype != PRM_FP32 || residual == nullptr)) return PRM_ERR_INVALID_ARG;
+  int rc = linear_check(tokens, n, k);
+  if (rc != PRM_OK || tokens == 0) return rc;
+  if (x == nullptr || weight == nullptr || y == nullptr || ldx < k || (residual != nullptr && ld_residual < n))
+    return PRM_ERR_INVALID_ARG;
+  if (ldx % 8 != 0 || (residual != nullptr && ld_residual % 8 != 0) || !aligned_to(x, 16) || !aligned_to(weight, 16) ||
+      !aligned_to(bias, 16) || !aligned_to(residual, 16) || !aligned_to(y, 16) || !aligned_to(pre, 16) ||
+      !aligned_to(workspace, 256))
+    return PRM_ERR_ALIGNMENT;
+  const LinearSizes sz = linear_sizes(tokens, n, k);
+  const bool few = linear_few(tokens, n, k);
+  if (!few && sz.fwd > 0 && (workspace == nullptr || workspace_bytes < sz.fwd)) return PRM_ERR_WORKSPACE;
+  const BlockDevice* dev;
+  if ((rc = block_device(&dev)) != PRM_OK) return rc;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool wide = y_dtype != dtype;
+  if (act == PRM_ACT_NONE) pre = nullptr;
+  if (few) {
+    const LinearFew f{x, ldx, weight, bias, residual, ld_residual, y, pre, static_cast<int>(tokens),
+                      static_cast<int>(n), static_cast<int>(k), wide};
+    return linear_few_forward(f, act, dtype, st) == cudaSuccess ? PRM_OK : PRM_ERR_CUDA;
+  }
+  char* ws = static_cast<char*>(workspace);
+  BlockGemmParams p{};
+  p.err = dev->d_err;
+  p.bias = bias;
+  p.residual = residual;
+  p.ld_residual = ld_residual;
+  p.keep = pre != nullptr;
+  GemmSegment s{};
+  if (!encode(&s.a[0], x, dtype, tokens, k, ldx, MAP_ROWS) || !encode(&s.b[0], weight, dtype, n, k, k, MAP_ROWS) ||
+      !encode(&s.out[0], y, dtype, tokens, n, n, wide ? MAP_STORE32 : MAP_STORE) ||
+      (pre != nullptr && !encode(&s.out[1], pre, dtype, tokens, n, n, MAP_STORE)))
+    return PRM_ERR_CUDA;
+  s.whole = static_cast<int>(sz.y.whole);
+  s.splits = sz.y.splits;
+  if (s.splits > 1) {
+    s.partial = reinterpret_cast<float*>(ws);
+    s.arrived = reinterpret_cast<uint32_t*>(ws + sz.fwd_counters);
+    if (launch_dependent(clear_kernel, dim3(1), dim3(256), 0, st, s.arrived,
+                         static_cast<int>(counter_bytes(sz.y) / 4)) != cudaSuccess)
+      return PRM_ERR_CUDA;
+  }
+  queue(p, s, tokens, n, k, 0, false, false, BN);
+  const cudaError_t e = wide ? launch_linear<EPI_LINEAR32>(p, act, dtype, dev->num_sms, st)
+                             : launch_linear<EPI_LINEAR>(p, act, dtype, dev->num_sms, st);
+  return e == cudaSuccess ? PRM_OK : PRM_ERR_CUDA;
+}
+
+extern "C" int prm_linear_backward(const void* dy, int64_t lddy, int dy_dtype, const void* x, int64_t ldx,
+                                   const void* weight, const void* pre, void* dx, void* dweight, float* dbias,
+                                   void* workspace, size_t workspace_bytes, int64_t tokens, int64_t n, int64_t k,
+                                   int act, int dtype, void* stream) {
+  using namespace prm;
+  if (!half_type(dtype) || (dy_dtype != dtype && dy_dtype != PRM_FP32) || act < PRM_ACT_SILU || act > PRM_ACT_NONE)
+    return PRM_ERR_INVALID_ARG;
+  int rc = linear_check(tokens, n, k);
+  if (rc != PRM_OK) return rc;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (tokens == 0) {
+    if ((dweight != nullptr && cudaMemsetAsync(dweight, 0, static_cast<size_t>(n) * k * 2, st) != cudaSuccess) ||
+        (dbias != nullptr && cudaMemsetAsync(dbias, 0, static_cast<size_t>(n) * 4, st) != cudaSuccess))
+      return PRM_ERR_CUDA;
+    return PRM_OK;
+  }
+  if (dy == nullptr || lddy < n || (dx != nullptr && weight == nullptr) ||
+      (dweight != nullptr && (x == nullptr || ldx < k)) || (act != PRM_ACT_NONE && pre == nullptr))
+    return PRM_ERR_INVALID_ARG;
+  if (!aligned_to(dy, 16) || !aligned_to(x, 16) || !aligned_to(weight, 16) || !aligned_to(pre, 16) ||
+      !aligned_to(dx, 16) || !aligned_to(dweight, 16) || !aligned_to(dbias, 4) || !aligned_to(workspace, 256) ||
+      lddy % 8 != 0 || (dweight != nullptr && ldx % 8 != 0))
+    return PRM_ERR_ALIGNMENT;
+  const LinearSizes sz = linear_sizes(tokens, n, k);
+  if (workspace == nullptr || workspace_bytes < sz.bwd) return PRM_ERR_WORKSPACE;
+  if (dx == nullptr && dweight == nullptr && dbias == nullptr) return PRM_OK;
+  const BlockDevice* dev;
+  if ((rc = block_device(&dev)) != PRM_OK) return rc;
+  char* ws = static_cast<char*>(workspace);
+  const bool products = dx != nullptr || dweight != nullptr;
+  const bool form = products && (act != PRM_ACT_NONE || dy_dtype != dtype);  // dg is not dy itself
+  // parts as they were sized with both products; one alone has fewer tiles, which only leaves pairs idle
+  const int dx_parts = sz.grads.dx, dw_parts = sz.grads.dw;
+  uint32_t* counters = reinterpret_cast<uint32_t*>(ws + sz.counters_at);
+  const int zero_count = products ? sz.dx_counters + sz.dw_counters : 0;
+  float* sums = reinterpret_cast<float*>(ws + sz.sums_at);
+  if (form || dbias != nullptr) {
+    const DgParams g{dy, lddy, act != PRM_ACT_NONE ? pre : nullptr, form ? ws : nullptr, dbias != nullptr ? sums : nullptr,
+                     counters, zero_count, tokens, static_cast<int>(n), sz.block_rows};
+    const dim3 grid(static_cast<unsigned>((n + DG_COLS - 1) / DG_COLS), static_cast<unsigned>(sz.row_blocks));
+    const bool bf = dtype == PRM_BF16, wide = dy_dtype != dtype;
+    const cudaError_t e = bf ? (wide ? launch_dg<__nv_bfloat16, float>(g, act, grid, st)
+                                     : launch_dg<__nv_bfloat16, __nv_bfloat16>(g, act, grid, st))
+                             : (wide ? launch_dg<__half, float>(g, act, grid, st)
+                                     : launch_dg<__half, __half>(g, act, grid, st));
+    if (e != cudaSuccess) return PRM_ERR_CUDA;
+  } else if (zero_count > 0) {
+    if (launch_dependent(clear_kernel, dim3(1), dim3(256), 0, st, counters, zero_count) != cudaSuccess)
+      return PRM_ERR_CUDA;
+  }
+  if (products) {
+    const void* dg = form ? static_cast<const void*>(ws) : dy;
+    const int64_t lddg = form ? n : lddy;
+    BlockGemmParams q{};
+    q.err = dev->d_err;
+    bool ok = true;
+    auto split = [&](GemmSegment& s, int parts, size_t at, uint32_t* counters) {
+      if (parts < 2) return;
+      s.whole = 0;
+      s.splits = parts;
+      s.partial = reinterpret_cast<float*>(ws + at);
+      s.arrived = counters;
+    };
+    auto add_dx = [&] {
+      if (dx == nullptr) return;
+      GemmSegment s{};
+      ok = ok && encode(&s.a[0], dg, dtype, tokens, n, lddg, MAP_ROWS) &&
+           encode(&s.b[0], weight, dtype, n, k, k, MAP_COLS) && encode(&s.out[0], dx, dtype, tokens, k, k, MAP_STORE);
+      split(s, dx_parts, sz.dx_at, counters);
+      queue(q, s, tokens, k, n, 0, false, true, BN);
+    };
+    auto add_dw = [&] {
+      if (dweight == nullptr) return;
+      GemmSegment s{};
+      ok = ok && encode(&s.a[0], dg, dtype, tokens, n, lddg, MAP_COLS) &&
+           encode(&s.b[0], x, dtype, tokens, k, ldx, MAP_COLS) && encode(&s.out[0], dweight, dtype, n, k, k, MAP_STORE);
+      split(s, dw_parts, sz.dw_at, counters + sz.dx_counters);
+      queue(q, s, n, k, tokens, 0, true, true, BN);
+    };
+    // the longer sums first, so that the last tiles of the queue are short
+    if (n >= tokens) add_dx();
+    add_dw();
+    if (n < tokens) add_dx();
+    if (!ok || launch<EPI_STORE>(q, dtype, dev->num_sms, st) != cudaSuccess) return PRM_ERR_CUDA;
+  }
+  if (dbias != nullptr &&
+      launch_dependent(linear_db_kernel, dim3(static_cast<unsigned>((n + 127) / 128)), dim3(128), 0, st, sums, dbias,
+                       static_cast<int>(n), sz.row_blocks) != cudaSuccess)
+    return PRM_ERR_CUDA;
+  return PRM_OK;
+}

@@ -40,6 +40,7 @@ PRM_NS_FORM_DIRECT = 1
 PRM_ACT_SILU = 0
 PRM_ACT_GELU = 1
 PRM_ACT_GELU_TANH = 2
+PRM_ACT_NONE = 3
 PRM_NORM_RMS = 0
 PRM_NORM_LAYER = 1
 PRM_ROTARY_HALF = 0
@@ -196,6 +197,12 @@ SIGNATURES = {
     "prm_embedding_backward_workspace": (c_int, [c_int64, c_int64, c_int64, POINTER(c_size_t)]),
     "prm_embedding_backward": (c_int, [c_void_p, c_int, c_void_p, c_int, c_void_p, c_int, c_int, c_int64, c_int64,
                                        c_int64, c_float, c_void_p, c_size_t, c_void_p]),
+    "prm_linear_sizes": (c_int, [c_int64, c_int64, c_int64, POINTER(c_size_t), POINTER(c_size_t)]),
+    "prm_linear_forward": (c_int, [c_void_p, c_int64, c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_int, c_void_p,
+                                   c_void_p, c_size_t, c_int64, c_int64, c_int64, c_int, c_int, c_void_p]),
+    "prm_linear_backward": (c_int, [c_void_p, c_int64, c_int, c_void_p, c_int64, c_void_p, c_void_p, c_void_p,
+                                    c_void_p, c_void_p, c_void_p, c_size_t, c_int64, c_int64, c_int64, c_int, c_int,
+                                    c_void_p]),
     "prm_rotary": (c_int, [POINTER(prm_rotary_desc), c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
     "prm_dropout": (c_int, [c_void_p, c_int, c_void_p, c_void_p, c_int, c_int64, ctypes.c_double, c_uint64, c_void_p,
                             c_uint64, c_void_p]),

@@ -6,6 +6,8 @@ from fractions import Fraction
 
 import numpy as np
 
+from .blocks import activation
+
 
 
 # ------------------------------------------------------- rotary positions
@@ -94,3 +96,17 @@ def cross_attention_backward(do, q, k, v, lengths, scale):
             g = np.einsum("hqk,qhd->khd", w, t)
             out[b, :n] = g.reshape(n, kv_heads, heads // kv_heads, -1).sum(2)
     return dq, dk, dv
+
+
+# ------------------------------------------------------------ linear layer
+def linear(x, w, bias, act, residual):
+    g = x @ w.T + (0.0 if bias is None else bias)
+    a = g if act is None else activation(g, act)[0]
+    return a if residual is None else residual + a
+
+
+def linear_backward(dy, x, w, bias, act):
+    """(dx, dw, dbias)."""
+    g = x @ w.T + (0.0 if bias is None else bias)
+    dg = dy if act is None else dy * activation(g, act)[1]
+    return dg @ w, dg.T @ x, dg.sum(0)
