@@ -213,6 +213,15 @@ struct AttSplit {
 };
 AttSplit att_forward_split(const AttHeads& h, int num_sms);
 
+// At most this many query rows share a key head's keys: attn_few.
+constexpr int ATT_FEW_ROWS = 16;
+inline bool att_is_few(const AttHeads& h) {
+  return static_cast<int64_t>(h.group_heads) * h.queries <= ATT_FEW_ROWS && h.kv_heads <= 65535 && h.batch <= 65535;
+}
+AttSplit att_few_split(const AttHeads& h, int num_sms);
+cudaError_t attn_few(const AttCall& c, const void* q, const void* k, const void* v, void* o, float* lse, char* workspace,
+                     cudaStream_t stream);
+
 cudaError_t attn_forward(const AttCall& c, const void* q, const void* k, const void* v, void* o, float* lse,
                          char* workspace, cudaStream_t stream);
 // Joins the parts of o that ranges of the keys left: part_o

@@ -77,7 +77,7 @@ int layout(const prm_attention_strides& s, int64_t batch, int64_t rows, int64_t 
 }
 
 size_t forward_bytes(const AttHeads& h) {
-  const AttSplit sp = att_forward_split(h, SMS);
+  const AttSplit sp = att_is_few(h) ? att_few_split(h, SMS) : att_forward_split(h, SMS);
   if (sp.splits < 2) return 0;
   const size_t rows = static_cast<size_t>(h.batch) * h.queries * h.heads;
   return round_up(rows * sp.splits * (h.head + 1) * sizeof(float), 256);
@@ -125,8 +125,10 @@ extern "C" int prm_attention_forward(const prm_attention_desc* desc, const void*
   if ((rc = block_device(&dev)) != PRM_OK) return rc;
   c.err = dev->d_err;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = h.keys == 0 ? attn_join(c, 0, o, lse, nullptr, nullptr, st)
-                                    : attn_forward(c, q, k, v, o, lse, static_cast<char*>(workspace), st);
+  char* ws = static_cast<char*>(workspace);
+  const cudaError_t e = h.keys == 0     ? attn_join(c, 0, o, lse, nullptr, nullptr, st)
+                        : att_is_few(h) ? attn_few(c, q, k, v, o, lse, ws, st)
+                                        : attn_forward(c, q, k, v, o, lse, ws, st);
   return e == cudaSuccess ? PRM_OK : PRM_ERR_CUDA;
 }
 

@@ -1,0 +1,350 @@
+// Cross attention, forward, for a few query rows per key head (a sampling
+// step's single token, with the query heads that share its keys): at most 16
+// rows, so a 128-row tensor-core tile would be empty but for them, and the time
+// is that of reading the keys and values once.
+//
+// A CTA takes a range of the keys of one key head, 64 at a time, through a ring
+// of TMA tiles; each of four warps takes 16 keys of a tile and all rows, with
+// warp-level 16 x 8 x 16 products (S = Q K^T and O += P V, the 16 rows as the
+// products' rows) and its own running maximum and sum. The warps' results are
+// joined in shared memory, the ranges' by attn_join. Two CTAs share an SM, so
+// that one's start and end are covered by the other's loads.
+#include <algorithm>
+#include <type_traits>
+
+#include "attn.cuh"
+
+namespace prm {
+namespace {
+
+constexpr int FEW_KEYS = 64;                        // of a tile
+constexpr int FEW_COMPUTE = 4;                      // warps that compute; a fifth loads
+constexpr int FEW_THREADS = 32 * (FEW_COMPUTE + 1);
+constexpr uint32_t FEW_CHUNK = FEW_KEYS * 128;      // 64 elements of each key
+template <int DP>
+struct FewShape {
+  static constexpr int STAGES = DP == 128 ? 3 : 6;
+  static constexpr uint32_t TILE = DP / 64 * FEW_CHUNK;  // keys, or values
+  static constexpr size_t RESULT = FEW_COMPUTE * ATT_FEW_ROWS * DP * sizeof(float);
+  static constexpr size_t SMEM = 1024 + STAGES * 2 * TILE + 2 * FEW_COMPUTE * ATT_FEW_ROWS * sizeof(float) + 256;
+  static_assert(RESULT <= STAGES * 2 * TILE, "the warps' results are joined where the tiles were");
+};
+
+struct FewParams {
+  CUtensorMap k, v;
+  AttHeads h;
+  AttLengths lengths;
+  AttStrides q_strides, o_strides;
+  const void* q;
+  void* o;
+  float* lse;
+  float* part_o;
+  float* part_lse;
+  int splits, split_tiles;
+  int rows;  // group_heads * queries
+  int mma_k;
+  float scale_log2;
+  int* err;
+};
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+template <typename T>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (std::is_same<T, __nv_bfloat16>::value)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
+        "%2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
+        "%2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Byte offset of 16-byte unit c of key `key` in a tile.
+__device__ __forceinline__ uint32_t unit_at(int key, int c) {
+  return (c >> 3) * FEW_CHUNK + key * 128 + (((c & 7) ^ (key & 7)) << 4);
+}
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(FEW_THREADS, 2) attn_few_kernel(const __grid_constant__ FewParams p) {
+  using Shape = FewShape<DP>;
+  constexpr int STAGES = Shape::STAGES;
+  constexpr uint32_t TILE = Shape::TILE;
+  constexpr int KSTEPS = DP / 16;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* tops = reinterpret_cast<float*>(smem + STAGES * 2 * TILE);  // [warp][row]
+  float* sums = tops + FEW_COMPUTE * ATT_FEW_ROWS;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sums + FEW_COMPUTE * ATT_FEW_ROWS);
+  uint64_t* empty = full + STAGES;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + STAGES);
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int split = blockIdx.x, kv_head = blockIdx.y, b = blockIdx.z;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], FEW_COMPUTE);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  pdl_wait();
+  pdl_launch_dependents();
+  const int length = att_length(p.lengths, b, p.h.keys);
+  const int tiles = (length + FEW_KEYS - 1) / FEW_KEYS;
+  const int k0 = min(split * p.split_tiles, tiles);
+  const int n = min(p.split_tiles, tiles - k0);
+
+  if (warp == FEW_COMPUTE) {
+    if (lane == 0) {
+      int j = 0;
+      for (; j < n; ++j) {
+        const int s = j % STAGES;
+        if (!wait_bounded(&empty[s], ((j / STAGES) & 1u) ^ 1u, abort_flag, p.err, ATT_WAIT_NS)) break;
+        uint8_t* dst = smem + s * 2 * TILE;
+        mbar_arrive_expect_tx(&full[s], 2 * TILE);
+#pragma unroll
+        for (int c = 0; c < DP / 64; ++c) {
+          tma_load_4d(dst + c * FEW_CHUNK, &p.k, &full[s], c * 64, kv_head, (k0 + j) * FEW_KEYS, b);
+          tma_load_4d(dst + TILE + c * FEW_CHUNK, &p.v, &full[s], c * 64, kv_head, (k0 + j) * FEW_KEYS, b);
+        }
+      }
+      if (j < n)  // every load in flight lands before the CTA exits
+        for (int s = 0; s < STAGES && s < j; ++s) wait_drain(&full[s], ((j - 1 - s) / STAGES) & 1u, 50000000ull);
+    }
+  } else {
+    // the rows of Q as the products' left operands: rows lane / 4 and + 8, elements 2 (lane % 4) and + 8 of a step
+    uint32_t qa[KSTEPS][4];
+    const int r0 = lane >> 2, c0 = 2 * (lane & 3);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int row = r0 + 8 * i;
+      const int token = row / p.h.group_heads, head = kv_head * p.h.group_heads + row - token * p.h.group_heads;
+      const T* q = static_cast<const T*>(p.q) + b * p.q_strides.batch + token * p.q_strides.token +
+                   head * p.q_strides.head;
+#pragma unroll
+      for (int k = 0; k < KSTEPS; ++k)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int at = 16 * k + 8 * e + c0;
+          qa[k][i + 2 * e] = row < p.rows && at < p.h.head ? *reinterpret_cast<const uint32_t*>(q + at) : 0u;
+        }
+    }
+    float o[2 * KSTEPS][4];
+#pragma unroll
+    for (int i = 0; i < 2 * KSTEPS; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    const int k_key = warp * 16 + (lane >> 4) * 8 + (lane & 7), k_unit = (lane >> 3) & 1;
+    const int v_key = warp * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), v_unit = lane >> 4;
+    for (int j = 0; j < n; ++j) {
+      const int s = j % STAGES;
+      const bool got = wait_bounded(&full[s], (j / STAGES) & 1u, abort_flag, p.err, ATT_WAIT_NS);
+      if (!__all_sync(0xffffffffu, got)) break;
+      const int valid = length - (k0 + j) * FEW_KEYS - warp * 16;
+      if (valid > 0) {
+        uint8_t* tile = smem + s * 2 * TILE;
+        const uint32_t sk = smem_u32(tile), sv = sk + TILE;
+        float acc[2][4] = {};
+#pragma unroll
+        for (int k = 0; k < KSTEPS; ++k) {
+          if (k >= p.mma_k) break;
+          uint32_t kb[4];
+          ldmatrix4(kb, sk + unit_at(k_key, 2 * k + k_unit));
+          mma16816<T>(acc[0], qa[k], kb[0], kb[1]);
+          mma16816<T>(acc[1], qa[k], kb[2], kb[3]);
+        }
+        if (valid < 16) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (8 * i + c0 + (e & 1) >= valid) acc[i][e] = -INFINITY;
+          // values behind the last key must not meet their P of zero: infinities and NaN would remain
+          for (int i = lane; i < (16 - valid) * (DP / 8); i += 32) {
+            const int key = warp * 16 + valid + i / (DP / 8);
+            *reinterpret_cast<uint4*>(tile + TILE + unit_at(key, i % (DP / 8))) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        uint32_t pa[4];
+        float factor[2];
+        bool grown = false;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float top = fmaxf(fmaxf(acc[0][2 * i], acc[0][2 * i + 1]), fmaxf(acc[1][2 * i], acc[1][2 * i + 1]));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          const bool grows = (top - m[i]) * p.scale_log2 > 8.f;  // (from -inf: always)
+          factor[i] = grows ? exp2_fast((m[i] - top) * p.scale_log2) : 1.f;
+          if (grows) m[i] = top;
+          grown |= grows;
+        }
+        if (__any_sync(0xffffffffu, grown)) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) l[i] *= factor[i];
+#pragma unroll
+          for (int i = 0; i < 2 * KSTEPS; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[i][e] *= factor[e >> 1];
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float base = m[i] == -INFINITY ? 0.f : m[i] * p.scale_log2;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const float a = exp2_fast(fmaf(acc[t][2 * i], p.scale_log2, -base));
+            const float c = exp2_fast(fmaf(acc[t][2 * i + 1], p.scale_log2, -base));
+            l[i] += a + c;
+            pa[2 * t + i] = pack2<T>(a, c);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < KSTEPS; ++k) {
+          if (k >= p.mma_k) break;
+          uint32_t vb[4];
+          ldmatrix4_trans(vb, sv + unit_at(v_key, 2 * k + v_unit));
+          mma16816<T>(o[2 * k], pa, vb[0], vb[1]);
+          mma16816<T>(o[2 * k + 1], pa, vb[2], vb[3]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[s]);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+      if ((lane & 3) == 0) {
+        tops[warp * ATT_FEW_ROWS + r0 + 8 * i] = m[i];
+        sums[warp * ATT_FEW_ROWS + r0 + 8 * i] = l[i];
+      }
+    }
+    // (every tile has been read by all warps before its memory takes results)
+    named_barrier_sync(1, 32 * FEW_COMPUTE);
+    float* mine = reinterpret_cast<float*>(smem) + warp * ATT_FEW_ROWS * DP;
+#pragma unroll
+    for (int i = 0; i < 2 * KSTEPS; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        *reinterpret_cast<float2*>(mine + (r0 + 8 * e) * DP + 8 * i + c0) = make_float2(o[i][2 * e], o[i][2 * e + 1]);
+    named_barrier_sync(1, 32 * FEW_COMPUTE);
+    const int vectors = p.h.head / 8;
+    for (int i = threadIdx.x; i < p.rows * vectors; i += 32 * FEW_COMPUTE) {
+      const int row = i / vectors, vec = i - row * vectors;
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < FEW_COMPUTE; ++w) top = fmaxf(top, tops[w * ATT_FEW_ROWS + row]);
+      float v[8] = {}, total = 0.f;
+#pragma unroll
+      for (int w = 0; w < FEW_COMPUTE; ++w) {
+        const float mw = tops[w * ATT_FEW_ROWS + row];
+        const float f = mw == top ? 1.f : exp2_fast((mw - top) * p.scale_log2);
+        total = fmaf(f, sums[w * ATT_FEW_ROWS + row], total);
+        const float* from = reinterpret_cast<const float*>(smem) + (w * ATT_FEW_ROWS + row) * DP + vec * 8;
+        float u[8];
+        Raw8<float> r;
+        r.a = *reinterpret_cast<const float4*>(from);
+        r.b = *(reinterpret_cast<const float4*>(from) + 1);
+        r.get(u);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = fmaf(f, u[e], v[e]);
+      }
+      const bool some = total > 0.f || total != total;
+      const float inv = some ? 1.f / total : 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= inv;
+      const float lse = some ? top * p.scale_log2 + log2f(total) : -INFINITY;
+      const int token = row / p.h.group_heads, head = kv_head * p.h.group_heads + row - token * p.h.group_heads;
+      const int64_t rows = static_cast<int64_t>(p.h.batch) * p.h.heads * p.h.queries;
+      const int64_t at_lse = (static_cast<int64_t>(b) * p.h.heads + head) * p.h.queries + token;
+      if (p.splits > 1) {
+        Raw8<float> r;
+        r.set(v);
+        r.store(p.part_o + (split * rows + (static_cast<int64_t>(b) * p.h.queries + token) * p.h.heads + head) * p.h.head +
+                vec * 8);
+        if (vec == 0) p.part_lse[split * rows + at_lse] = lse;
+      } else {
+        Raw8<T> r;
+        r.set(v);
+        r.store(static_cast<T*>(p.o) + b * p.o_strides.batch + token * p.o_strides.token + head * p.o_strides.head +
+                vec * 8);
+        if (vec == 0 && p.lse != nullptr) p.lse[at_lse] = lse;
+      }
+    }
+  }
+}
+
+template <typename T, int DP>
+cudaError_t launch_few(const FewParams& p, cudaStream_t stream) {
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = att_prepare(attn_few_kernel<T, DP>, FewShape<DP>::SMEM, ready);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(attn_few_kernel<T, DP>, dim3(p.splits, p.h.kv_heads, p.h.batch), dim3(FEW_THREADS),
+                          FewShape<DP>::SMEM, stream, p);
+}
+
+}  // namespace
+
+// Ranges for four CTAs per SM or so, of two tiles at least: ragged lengths
+// leave some without work.
+AttSplit att_few_split(const AttHeads& h, int num_sms) {
+  const int64_t heads = static_cast<int64_t>(h.batch) * h.kv_heads;
+  const int tiles = (h.keys + FEW_KEYS - 1) / FEW_KEYS;
+  const int64_t want = std::max<int64_t>(1, 4 * num_sms / heads);
+  const int each = static_cast<int>(std::max<int64_t>(2, (tiles + want - 1) / want));
+  return {std::max(1, (tiles + each - 1) / each), each};
+}
+
+cudaError_t attn_few(const AttCall& c, const void* q, const void* k, const void* v, void* o, float* lse, char* workspace,
+                     cudaStream_t stream) {
+  FewParams p{};
+  p.h = c.h;
+  p.lengths = c.lengths;
+  p.q_strides = c.q;
+  p.o_strides = c.o;
+  p.q = q;
+  p.o = o;
+  p.lse = lse;
+  const AttSplit sp = att_few_split(c.h, c.num_sms);
+  p.splits = sp.splits;
+  p.split_tiles = sp.tiles;
+  p.rows = c.h.group_heads * c.h.queries;
+  p.mma_k = (c.h.head + 15) / 16;
+  p.scale_log2 = c.scale * 1.4426950408889634f;
+  p.err = c.err;
+  if (p.splits > 1) {
+    p.part_o = reinterpret_cast<float*>(workspace);
+    p.part_lse = p.part_o + static_cast<int64_t>(c.h.batch) * c.h.queries * c.h.heads * p.splits * c.h.head;
+  }
+  if (!att_encode(&p.k, k, c.dtype, c.h.batch, c.h.keys, c.h.kv_heads, c.h.head, c.k, 1, FEW_KEYS) ||
+      !att_encode(&p.v, v, c.dtype, c.h.batch, c.h.keys, c.h.kv_heads, c.h.head, c.v, 1, FEW_KEYS))
+    return cudaErrorInvalidValue;
+  const bool wide = c.h.head > 64;
+  const cudaError_t e =
+      c.dtype == PRM_BF16 ? (wide ? launch_few<__nv_bfloat16, 128>(p, stream) : launch_few<__nv_bfloat16, 64>(p, stream))
+                          : (wide ? launch_few<__half, 128>(p, stream) : launch_few<__half, 64>(p, stream));
+  if (e != cudaSuccess || p.splits == 1) return e;
+  return attn_join(c, p.splits, o, lse, p.part_o, p.part_lse, stream);
+}
+
+}  // namespace prm

@@ -479,15 +479,16 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
   const int64_t rows = static_cast<int64_t>(p.h.batch) * p.h.queries * p.h.heads;
   const int64_t at = (static_cast<int64_t>(b) * p.h.heads + head) * p.h.queries + token;
   float top = -INFINITY;
+#pragma unroll 8
   for (int s = 0; s < p.splits; ++s) top = fmaxf(top, p.part_lse[s * rows + at]);
   float v[8] = {}, total = 0.f;
+#pragma unroll 4
   for (int s = 0; s < p.splits; ++s) {
     const float lse = p.part_lse[s * rows + at];
-    if (lse == -INFINITY) continue;  // no keys in this part
-    const float w = exp2f(lse - top);
-    total += w;
     Raw8<float> r;
     r.load(p.part_o + (s * rows + row) * p.h.head + vec * 8);
+    const float w = lse == -INFINITY ? 0.f : exp2f(lse - top);  // (a part without keys left zeros)
+    total += w;
     float u[8];
     r.get(u);
 #pragma unroll
