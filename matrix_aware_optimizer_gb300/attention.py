@@ -21,6 +21,7 @@ assert _ROTARY.size == N.ctypes.sizeof(N.prm_rotary_desc)
 _ATTN = struct.Struct("=30qQ2ifi")  # prm_attention_desc
 assert _ATTN.size == N.ctypes.sizeof(N.prm_attention_desc)
 _LINEAR_ACT = {None: N.PRM_ACT_NONE, **_ACT}
+_POSITION_BYTES = {torch.int64: 8, torch.int32: 4}
 _LAYOUT = {"half": N.PRM_ROTARY_HALF, "interleaved": N.PRM_ROTARY_INTERLEAVED}
 
 
@@ -210,13 +211,6 @@ def rotary_plan(dim: int, base: float = 10000.0, layout: str = "half", scaling: 
     return RotaryPlan(torch.tensor(turns, dtype=torch.int64, device=device), dim, layout, float(amplitude))
 
 
-def _strides3(t):
-    """Strides of [samples, tokens, heads, head], or None where the elements
-    of a head are not consecutive."""
-    s = t.stride()
-    return s[:3] if s[3] == 1 or t.shape[3] == 1 else None
-
-
 def _distinct(t) -> bool:
     """Whether no two elements of t share memory."""
     reach = 1
@@ -227,45 +221,56 @@ def _distinct(t) -> bool:
     return True
 
 
-def _rotate(x, positions, plan, out, inverse, stream):
-    device = x.get_device()
-    if device < 0 or x.dtype not in _DTYPE or x.dim() not in (3, 4):
-        raise ValueError("x must be a [samples,] tokens x heads x head CUDA tensor of float32, bfloat16 or float16")
-    if positions.dtype not in (torch.int64, torch.int32) or positions.get_device() != device:
-        raise ValueError("positions must be int64 or int32, on x's device")
-    if plan.turns.get_device() != device or plan.turns.shape != (plan.dim // 2,) \
-            or plan.turns.dtype is not torch.int64 or not plan.turns.is_contiguous():
-        raise ValueError("plan must come from rotary_plan, on x's device")
-    if plan.dim > x.shape[-1]:
-        raise ValueError("the plan turns more elements than a head has")
-    if positions.dim() > x.dim() - 2 or any(a != b and a != 1 for a, b in
-                                            zip(positions.shape[::-1], x.shape[:-2][::-1])):
+def _position_strides(positions, shape):
+    """Strides of the positions over x's samples and tokens."""
+    own = positions.shape
+    if own == shape:
+        st = positions.stride()
+    elif len(own) <= len(shape) and all(a == b or a == 1 for a, b in zip(own[::-1], shape[::-1])):
+        st = positions.expand(shape).stride()
+    else:
         raise ValueError("positions must have x's samples and tokens, or broadcast to them")
-    if out is not None and (out.shape != x.shape or out.dtype is not x.dtype or out.get_device() != device
-                            or (out.stride(-1) != 1 and out.shape[-1] > 1) or not _distinct(out)):
+    return st if len(st) == 2 else (0, st[0])
+
+
+def _rotate(x, positions, plan, out, inverse, stream):
+    device, dt, shape = x.get_device(), x.dtype, x.shape
+    if device < 0 or dt not in _DTYPE or len(shape) not in (3, 4):
+        raise ValueError("x must be a [samples,] tokens x heads x head CUDA tensor of float32, bfloat16 or float16")
+    if positions.dtype not in _POSITION_BYTES or positions.get_device() != device:
+        raise ValueError("positions must be int64 or int32, on x's device")
+    turns, dim, layout, amplitude = plan
+    if turns.get_device() != device or turns.dtype is not torch.int64 or turns.numel() != dim // 2 \
+            or not turns.is_contiguous():
+        raise ValueError("plan must come from rotary_plan, on x's device")
+    if dim > shape[-1]:
+        raise ValueError("the plan turns more elements than a head has")
+    ps, pt = _position_strides(positions, shape[:-2])
+    if out is not None and (out.shape != shape or out.dtype is not dt or out.get_device() != device
+                            or (out.stride(-1) != 1 and shape[-1] > 1) or not _distinct(out)):
         raise ValueError("out must have x's shape, type and device, consecutive elements and no shared memory")
     if _is_elsewhere(device, stream):
-        with _elsewhere(device, stream, x, positions, plan.turns, out):
+        with _elsewhere(device, stream, x, positions, turns, out):
             return _rotate(x, positions, plan, out, inverse, None)
     if x.numel() == 0:
         return torch.empty_like(x) if out is None else out
-    x4 = x if x.dim() == 4 else x.unsqueeze(0)
-    xs = _strides3(x4)
-    if xs is None:
-        x4 = x4.contiguous()
-        xs = _strides3(x4)
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
-    if out is not None and out.data_ptr() == x4.data_ptr() and any(
-            a != b and e > 1 for a, b, e in zip(out.stride(), x.stride(), x.shape)):
-        raise ValueError("out shares x's memory with other strides")
-    ys = _strides3(y if x.dim() == 4 else y.unsqueeze(0))
-    samples, tokens, heads, head = x4.shape
-    ps = positions.expand(x.shape[:-2]).stride()
-    packed = _ROTARY.pack(samples, tokens, heads, head, plan.dim, *xs, *ys, ps[0] if len(ps) == 2 else 0, ps[-1],
-                          positions.element_size(), _LAYOUT[plan.layout], _DTYPE[x.dtype], 1 if inverse else 0,
-                          plan.amplitude, 0)
-    rc = N.load().prm_rotary(N.prm_rotary_desc.from_buffer_copy(packed), x4.data_ptr(), positions.data_ptr(),
-                             plan.turns.data_ptr(), y.data_ptr(), _raw_stream(device))
+    if x.stride(-1) != 1 and shape[-1] > 1:
+        x = x.contiguous()
+    if out is None:
+        y = torch.empty(shape, dtype=dt, device=x.device)
+    else:
+        y = out
+        if y.data_ptr() == x.data_ptr() and any(a != b and e > 1 for a, b, e in zip(y.stride(), x.stride(), shape)):
+            raise ValueError("out shares x's memory with other strides")
+    xs, ys = x.stride(), y.stride()
+    if len(shape) == 4:
+        packed = _ROTARY.pack(*shape, dim, *xs[:3], *ys[:3], ps, pt, _POSITION_BYTES[positions.dtype],
+                              _LAYOUT[layout], _DTYPE[dt], inverse, amplitude, 0)
+    else:
+        packed = _ROTARY.pack(1, *shape, dim, 0, *xs[:2], 0, *ys[:2], ps, pt, _POSITION_BYTES[positions.dtype],
+                              _LAYOUT[layout], _DTYPE[dt], inverse, amplitude, 0)
+    rc = N.load().prm_rotary(N.prm_rotary_desc.from_buffer_copy(packed), x.data_ptr(), positions.data_ptr(),
+                             turns.data_ptr(), y.data_ptr(), _raw_stream(device))
     if rc:
         N.check(rc, "prm_rotary")
     return y

@@ -20,24 +20,28 @@ struct DropParams {
   const void* residual;
   void* y;
   int64_t n;
-  uint64_t seed, offset;
-  const uint64_t* seed_device;
+  uint64_t offset;
+  const uint64_t* seed_device;  // where not NULL the round keys come from what it holds
+  uint32_t keys[20];            // of the ten rounds
   uint32_t threshold;  // a smaller word drops its element
   int none;            // p is 1: nothing is kept
   float scale;
 };
 
-__device__ __forceinline__ uint4 philox10(uint64_t counter, uint32_t k0, uint32_t k1) {
+constexpr uint32_t KEY_STEP0 = 0x9E3779B9u, KEY_STEP1 = 0xBB67AE85u;
+
+// key(r): round r's two key words.
+template <typename Key>
+__device__ __forceinline__ uint4 philox10(uint64_t counter, Key key) {
   uint32_t c0 = static_cast<uint32_t>(counter), c1 = static_cast<uint32_t>(counter >> 32), c2 = 0, c3 = 0;
 #pragma unroll
   for (int r = 0; r < 10; ++r) {
     const uint64_t a = static_cast<uint64_t>(c0) * 0xD2511F53u, b = static_cast<uint64_t>(c2) * 0xCD9E8D57u;
-    c0 = static_cast<uint32_t>(b >> 32) ^ c1 ^ k0;
+    const uint2 k = key(r);
+    c0 = static_cast<uint32_t>(b >> 32) ^ c1 ^ k.x;
     c1 = static_cast<uint32_t>(b);
-    c2 = static_cast<uint32_t>(a >> 32) ^ c3 ^ k1;
+    c2 = static_cast<uint32_t>(a >> 32) ^ c3 ^ k.y;
     c3 = static_cast<uint32_t>(a);
-    k0 += 0x9E3779B9u;
-    k1 += 0xBB67AE85u;
   }
   return make_uint4(c0, c1, c2, c3);
 }
@@ -60,10 +64,19 @@ __global__ void __launch_bounds__(DROP_THREADS) dropout_kernel(const __grid_cons
     xv.load(x);
     if (RES) rv.load(res);
   }
-  const uint64_t seed = p.seed_device != nullptr ? *p.seed_device : p.seed;
-  const uint32_t k0 = static_cast<uint32_t>(seed), k1 = static_cast<uint32_t>(seed >> 32);
   const uint64_t block = p.offset + static_cast<uint64_t>(i0) / 4;
-  const uint4 a = philox10(block, k0, k1), b = philox10(block + 1, k0, k1);
+  uint4 a, b;
+  if (p.seed_device == nullptr) {
+    auto key = [&](int r) { return make_uint2(p.keys[2 * r], p.keys[2 * r + 1]); };
+    a = philox10(block, key);
+    b = philox10(block + 1, key);
+  } else {
+    const uint64_t seed = *p.seed_device;
+    const uint32_t k0 = static_cast<uint32_t>(seed), k1 = static_cast<uint32_t>(seed >> 32);
+    auto key = [&](int r) { return make_uint2(k0 + r * KEY_STEP0, k1 + r * KEY_STEP1); };
+    a = philox10(block, key);
+    b = philox10(block + 1, key);
+  }
   const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   if (whole) {
     float v[8], r[8];
@@ -116,7 +129,17 @@ extern "C" int prm_dropout(const void* x, int dtype, const void* residual, void*
   const int rc = block_device(&dev);
   if (rc != PRM_OK) return rc;
   const double limit = p * 4294967296.0 + 0.5;
-  DropParams q{x, residual, y, n, seed, offset, seed_device, 0, 0, 0.f};
+  DropParams q{};
+  q.x = x;
+  q.residual = residual;
+  q.y = y;
+  q.n = n;
+  q.offset = offset;
+  q.seed_device = seed_device;
+  for (uint32_t r = 0; r < 10; ++r) {
+    q.keys[2 * r] = static_cast<uint32_t>(seed) + r * KEY_STEP0;
+    q.keys[2 * r + 1] = static_cast<uint32_t>(seed >> 32) + r * KEY_STEP1;
+  }
   q.none = limit >= 4294967296.0;
   q.threshold = q.none ? 0u : static_cast<uint32_t>(limit);
   q.scale = p < 1.0 ? static_cast<float>(1.0 / (1.0 - p)) : 0.f;

@@ -100,14 +100,24 @@ __global__ void __launch_bounds__(256) linear_dg_kernel(const __grid_constant__ 
   p.partial[static_cast<int64_t>(blockIdx.y) * p.n + c] = total;
 }
 
-__global__ void __launch_bounds__(128) linear_db_kernel(const float* partial, float* db, int n, int blocks) {
+// db = the blocks' sums, in order: eight threads to a column, each with every
+// eighth block (in one round of loads), joined in the threads' order.
+__global__ void __launch_bounds__(256) linear_db_kernel(const float* partial, float* db, int n, int blocks) {
+  __shared__ float sums[8][32];
   pdl_wait();
   pdl_launch_dependents();
-  const int c = blockIdx.x * 128 + threadIdx.x;
-  if (c >= n) return;
+  const int lane = threadIdx.x & 31, part = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
   float total = 0.f;
+  if (c < n) {
 #pragma unroll 8
-  for (int b = 0; b < blocks; ++b) total += partial[static_cast<int64_t>(b) * n + c];
+    for (int b = part; b < blocks; b += 8) total += partial[static_cast<int64_t>(b) * n + c];
+  }
+  sums[part][lane] = total;
+  __syncthreads();
+  if (part > 0 || c >= n) return;
+#pragma unroll
+  for (int k = 1; k < 8; ++k) total += sums[k][lane];
   db[c] = total;
 }
 
@@ -353,7 +363,7 @@ extern "C" int prm_linear_backward(const void* dy, int64_t lddy, int dy_dtype, c
     if (!ok || launch<EPI_STORE>(q, dtype, dev->num_sms, st) != cudaSuccess) return PRM_ERR_CUDA;
   }
   if (dbias != nullptr &&
-      launch_dependent(linear_db_kernel, dim3(static_cast<unsigned>((n + 127) / 128)), dim3(128), 0, st, sums, dbias,
+      launch_dependent(linear_db_kernel, dim3(static_cast<unsigned>((n + 31) / 32)), dim3(256), 0, st, sums, dbias,
                        static_cast<int>(n), sz.row_blocks) != cudaSuccess)
     return PRM_ERR_CUDA;
   return PRM_OK;

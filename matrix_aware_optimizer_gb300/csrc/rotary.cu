@@ -176,7 +176,9 @@ cudaError_t launch(const RotParams& p, bool half, unsigned grid, cudaStream_t st
 
 template <typename T>
 cudaError_t launch(const RotParams& p, int width, bool half, unsigned grid, cudaStream_t stream) {
-  if (width == 8) return launch<T, 8>(p, half, grid, stream);
+  if constexpr (sizeof(T) == 2) {
+    if (width == 8) return launch<T, 8>(p, half, grid, stream);
+  }
   if (width == 4) return launch<T, 4>(p, half, grid, stream);
   if (width == 2) return launch<T, 2>(p, half, grid, stream);
   return launch<T, 1>(p, half, grid, stream);
