@@ -99,6 +99,22 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* tm, ui
       : "memory");
 }
 
+// True in one lane of the warp, always the same one. The warp that issues
+// products runs as a whole and has this lane issue them: what is the same in
+// all lanes then stays in uniform registers, where the products' operands have
+// to be; in a branch of one lane each operand is moved there first.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+// A value that is the same in all lanes, known as such.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 // 2^v, to 2 ulp; 0 for -inf.
 __device__ __forceinline__ float exp2_fast(float v) {
   float r;
@@ -116,7 +132,9 @@ template <int DP>
 constexpr uint32_t ATT_TILE = DP / 64 * ATT_CHUNK;
 constexpr uint64_t ATT_WAIT_NS = 2000000000ull;
 
-constexpr int ATT_THREADS = 320;  // warps 0-3 and 4-7 take rows, 8 loads, 9 issues products
+// Warps 0 .. 15 take elements, 16 loads, 17 issues products.
+constexpr int ATT_WARPS = 16;
+constexpr int ATT_THREADS = 32 * (ATT_WARPS + 2);
 
 template <int DP>
 __device__ __forceinline__ void att_load_tile(uint8_t* dst, const CUtensorMap* tm, uint64_t* bar, int head, int row,
@@ -125,25 +143,44 @@ __device__ __forceinline__ void att_load_tile(uint8_t* dst, const CUtensorMap* t
   for (int c = 0; c < DP / 64; ++c) tma_load_4d(dst + c * ATT_CHUNK, tm, bar, c * 64, head, row, batch);
 }
 
+// A descriptor's address field is its low 14 bits, in units of 16 bytes, so
+// a step along a tile is one 32-bit addition to the low word: a thread that
+// rebuilds the descriptors takes longer to issue a product than the tensor
+// cores to compute it (64 cycles).
+__device__ __forceinline__ uint64_t desc_at(uint64_t base, uint32_t bytes) {
+  return (base & 0xFFFFFFFF00000000ull) | (static_cast<uint32_t>(base) + (bytes >> 4));
+}
+
 // D[128 x 128] = A B^T, both tiles along their elements, `steps` of 16.
+template <int DP>
 __device__ __forceinline__ void att_mma_rows(uint32_t d, const uint8_t* a, const uint8_t* b, int steps,
                                              uint32_t idesc) {
-  const uint32_t sa = smem_u32(a), sb = smem_u32(b);
+  const uint64_t da = smem_desc_sw128(smem_u32(a), 16, 1024), db = smem_desc_sw128(smem_u32(b), 16, 1024);
+  if (steps == DP / 16) {
+#pragma unroll
+    for (int k = 0; k < DP / 16; ++k) {
+      const uint32_t off = (k >> 2) * ATT_CHUNK + (k & 3) * 32;
+      umma_bf16(d, desc_at(da, off), desc_at(db, off), idesc, k > 0 ? 1u : 0u);
+    }
+  } else {
 #pragma unroll 1
-  for (int k = 0; k < steps; ++k) {
-    const uint32_t off = (k >> 2) * ATT_CHUNK + (k & 3) * 32;
-    umma_bf16(d, smem_desc_sw128(sa + off, 16, 1024), smem_desc_sw128(sb + off, 16, 1024), idesc, k > 0 ? 1u : 0u);
+    for (int k = 0; k < steps; ++k) {
+      const uint32_t off = (k >> 2) * ATT_CHUNK + (k & 3) * 32;
+      umma_bf16(d, desc_at(da, off), desc_at(db, off), idesc, k > 0 ? 1u : 0u);
+    }
   }
 }
 
-// D[128 x N] (+)= A B, A 128 x 128 in tensor memory (its first 64 columns at
-// a0, the other 64 at a1), B a tile along its rows.
-__device__ __forceinline__ void att_mma_cols(uint32_t d, uint32_t a0, uint32_t a1, const uint8_t* b, uint32_t idesc,
+// D[128 x N] (+)= A B, A 128 x 128 in tensor memory, in pieces of `PIECE`
+// elements of K (PIECE / 2 columns) that start PIECE columns apart; B a tile
+// along its rows.
+template <int PIECE>
+__device__ __forceinline__ void att_mma_cols(uint32_t d, uint32_t a, const uint8_t* b, uint32_t idesc,
                                              bool accumulate) {
-  const uint32_t sb = smem_u32(b);
+  const uint64_t db = smem_desc_sw128(smem_u32(b), ATT_CHUNK, 1024);
 #pragma unroll
   for (int k = 0; k < ATT_ROWS / 16; ++k)
-    umma_tmem_a(d, (k < 4 ? a0 : a1) + (k & 3) * 8, smem_desc_sw128(sb + k * 2048, ATT_CHUNK, 1024), idesc,
+    umma_tmem_a(d, a + k * 16 / PIECE * PIECE + k * 16 % PIECE / 2, desc_at(db, k * 2048), idesc,
                 accumulate || k > 0 ? 1u : 0u);
 }
 

@@ -42,7 +42,7 @@ int read(const prm_attention_desc* d, AttCall* c) {
       d->batch * d->heads > MOST)
     return PRM_ERR_UNSUPPORTED;
   const int64_t bh = std::max<int64_t>(d->batch * d->heads, 1);
-  if (std::max(d->queries, d->keys) > (int64_t(1) << 40) / bh) return PRM_ERR_UNSUPPORTED;
+  if (std::max(d->queries, d->keys) > (int64_t(1) << 36) / bh) return PRM_ERR_UNSUPPORTED;
   *c = AttCall{};
   AttHeads& h = c->h;
   h.batch = static_cast<int>(d->batch);

@@ -14,8 +14,9 @@
 //                     dS in tensor memory over S, dQ in tensor memory
 //   attn_sum_kernel   adds parts, where few tiles were split along the other axis
 //
-// 256 threads take the elements, two to a row, each 64 columns; one thread
-// issues all products, in an order in which the tensor cores have work while
+// 512 threads take the elements, four to a row, each 32 columns (with 256 the
+// chain of load, exponential and store of each took twice the products'
+// time); one thread issues all products, in an order in which the tensor cores have work while
 // the elements are formed: dV and the next S^T beside dS, dK and the next dP^T
 // beside the next P. Products run through the tensor pipe in the order of
 // issue; an operand in tensor memory is overwritten only by a later product.
@@ -108,7 +109,7 @@ struct DkvParams {
   int key_tiles;
   int splits, split_rounds;  // ranges of the rounds, rounds of one
   int rounds;                // query tiles of all groups of a key head
-  int64_t items;
+  uint32_t items;
   int mma_k, mma_n;
   float scale, scale_log2;
   int* err;
@@ -120,25 +121,26 @@ struct DkvItem {
   int x0, n;  // first round and their number
 };
 
-__device__ __forceinline__ DkvItem dkv_item(const DkvParams& p, int64_t item) {
+__device__ __forceinline__ DkvItem dkv_item(const DkvParams& p, uint32_t item) {
   DkvItem it;
-  it.split = static_cast<int>(item % p.splits);
-  item /= p.splits;
-  it.tile = static_cast<int>(item % p.key_tiles);
-  item /= p.key_tiles;
-  it.kv_head = static_cast<int>(item % p.h.kv_heads);
-  it.b = static_cast<int>(item / p.h.kv_heads);
+  const uint32_t splits = p.splits, key_tiles = p.key_tiles, kv_heads = p.h.kv_heads;
+  it.split = static_cast<int>(item % splits);
+  item /= splits;
+  it.tile = static_cast<int>(item % key_tiles);
+  item /= key_tiles;
+  it.kv_head = static_cast<int>(item % kv_heads);
+  it.b = static_cast<int>(item / kv_heads);
   it.length = att_length(p.lengths, it.b, p.h.keys);
   it.x0 = min(it.split * p.split_rounds, p.rounds);
   it.n = it.tile * ATT_ROWS < it.length ? min(p.split_rounds, p.rounds - it.x0) : 0;
   return it;
 }
 
-// Writes 32 columns of a row of a gradient, converted, from column c.
+// Writes 16 columns of a row of a gradient, converted, from column c.
 template <typename T>
-__device__ __forceinline__ void store_row32(T* out, float* part, const float (&v)[32], int c, int head) {
+__device__ __forceinline__ void store_row16(T* out, float* part, const float (&v)[16], int c, int head) {
 #pragma unroll
-  for (int i = 0; i < 32; i += 8) {
+  for (int i = 0; i < 16; i += 8) {
     if (c + i >= head) break;
     float u[8];
 #pragma unroll
@@ -180,7 +182,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) attn_dkv_kernel(const __grid_c
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
-  const int warp = threadIdx.x / 32;
+  const int warp = uniform(threadIdx.x / 32);
   const int lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
     for (int s = 0; s < SLOTS; ++s) {
@@ -190,16 +192,16 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) attn_dkv_kernel(const __grid_c
     mbar_init(kv_full, 1);
     mbar_init(kv_empty, 1);
     mbar_init(s_full, 1);
-    mbar_init(p_ready, 8);
+    mbar_init(p_ready, ATT_WARPS);
     mbar_init(dp_full, 1);
-    mbar_init(ds_ready, 8);
+    mbar_init(ds_ready, ATT_WARPS);
     mbar_init(acc_full, 1);
-    mbar_init(acc_empty, 8);
+    mbar_init(acc_empty, ATT_WARPS);
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 9) {
+  if (warp == ATT_WARPS + 1) {
     tmem_alloc(tmem_holder, 512);
     tmem_relinquish();
   }
@@ -212,11 +214,11 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) attn_dkv_kernel(const __grid_c
   pdl_launch_dependents();
   const int tiles = p.h.query_tiles();
 
-  if (warp == 8) {
+  if (warp == ATT_WARPS) {
     if (lane == 0) {
       uint32_t n = 0, rounds = 0, items = 0;  // loads into the ring, rounds, items so far
       bool ok = true;
-      for (int64_t item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
+      for (uint32_t item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
         const DkvItem it = dkv_item(p, item);
         if (it.n <= 0) continue;
         ok = wait_bounded(kv_empty, (items & 1u) ^ 1u, abort_flag, p.err, ATT_WAIT_NS);
@@ -249,58 +251,68 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) attn_dkv_kernel(const __grid_c
         if (items) wait_drain(kv_full, (items - 1) & 1u, 50000000ull);
       }
     }
-  } else if (warp == 9) {
-    if (lane == 0) {
-      constexpr bool FP16 = !std::is_same<T, __nv_bfloat16>::value;
-      const uint32_t id_s = idesc_f16kind_f32(ATT_ROWS, ATT_ROWS, false, false, FP16);
-      const uint32_t id_acc = idesc_f16kind_f32(ATT_ROWS, p.mma_n, false, true, FP16);
-      uint32_t n = 0, rounds = 0, items = 0;  // ring tiles used up, rounds, items before this one
-      bool ok = true, issued = false;
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        ok = ok && wait_bounded(bar, parity, abort_flag, p.err, ATT_WAIT_NS);
-        if (ok) tc_fence_after_sync();
-        return ok;
-      };
-      auto slot = [&](uint32_t k) { return ring + (k % SLOTS) * TILE; };
-      auto wait_slot = [&](uint32_t k) { return wait(&full[k % SLOTS], (k / SLOTS) & 1u); };
-      auto form = [&](uint32_t d, const uint8_t* a, uint32_t k, uint64_t* done) {
-        if (!wait_slot(k)) return;
-        att_mma_rows(d, a, slot(k), p.mma_k, id_s);
+  } else if (warp == ATT_WARPS + 1) {
+    constexpr bool FP16 = !std::is_same<T, __nv_bfloat16>::value;
+    const uint32_t id_s = idesc_f16kind_f32(ATT_ROWS, ATT_ROWS, false, false, FP16);
+    const uint32_t id_acc = idesc_f16kind_f32(ATT_ROWS, p.mma_n, false, true, FP16);
+    uint32_t n = 0, rounds = 0, items = 0;  // ring tiles used up, rounds, items before this one
+    bool ok = true, issued = false;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      const bool got = wait_bounded(bar, parity, abort_flag, p.err, ATT_WAIT_NS);
+      ok = __all_sync(0xffffffffu, got);
+      tc_fence_after_sync();
+      return ok;
+    };
+    auto slot = [&](uint32_t k) { return ring + (k % SLOTS) * TILE; };
+    auto wait_slot = [&](uint32_t k) { return wait(&full[k % SLOTS], (k / SLOTS) & 1u); };
+    auto form = [&](uint32_t d, const uint8_t* a, uint32_t k, uint64_t* done) {
+      if (!wait_slot(k)) return;
+      if (elect_one()) {
+        att_mma_rows<DP>(d, a, slot(k), p.mma_k, id_s);
         umma_commit(done);
-        issued = true;
-      };
-      for (int64_t item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
-        const DkvItem it = dkv_item(p, item);
-        if (it.n <= 0) continue;
-        if (!wait(kv_full, items & 1u)) break;
-        form(t_s, sK, n + 1, s_full);
-        if (ok) form(t_dp, sV, n, dp_full);
-        for (int i = 0; ok && i < it.n; ++i, n += 2, ++rounds) {
-          if (!wait(p_ready, rounds & 1u)) break;
-          if (i == 0 && !wait(acc_empty, (items & 1u) ^ 1u)) break;
-          att_mma_cols(t_dv, t_s, t_s + 64, slot(n), id_acc, i > 0);
+      }
+      __syncwarp();
+      issued = true;
+    };
+    for (uint32_t item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
+      const DkvItem it = dkv_item(p, item);
+      const int count = uniform(it.n);
+      if (count <= 0) continue;
+      if (!wait(kv_full, items & 1u)) break;
+      form(t_s, sK, n + 1, s_full);
+      if (ok) form(t_dp, sV, n, dp_full);
+      for (int i = 0; ok && i < count; ++i, n += 2, ++rounds) {
+        if (!wait(p_ready, rounds & 1u)) break;
+        if (i == 0 && !wait(acc_empty, (items & 1u) ^ 1u)) break;
+        if (elect_one()) {
+          att_mma_cols<32>(t_dv, t_s, slot(n), id_acc, i > 0);
           umma_commit(&empty[n % SLOTS]);
-          if (i + 1 < it.n) form(t_s, sK, n + 3, s_full);
-          if (!ok || !wait(ds_ready, rounds & 1u)) break;
-          att_mma_cols(t_dk, t_dp, t_dp + 64, slot(n + 1), id_acc, i > 0);
-          umma_commit(&empty[(n + 1) % SLOTS]);
-          if (i + 1 < it.n)
-            form(t_dp, sV, n + 2, dp_full);
         }
-        if (!ok) break;
-        umma_commit(kv_empty);
-        umma_commit(acc_full);
-        ++items;
+        __syncwarp();
+        if (i + 1 < count) form(t_s, sK, n + 3, s_full);
+        if (!ok || !wait(ds_ready, rounds & 1u)) break;
+        if (elect_one()) {
+          att_mma_cols<32>(t_dk, t_dp, slot(n + 1), id_acc, i > 0);
+          umma_commit(&empty[(n + 1) % SLOTS]);
+          if (i + 1 == count) {
+            umma_commit(kv_empty);
+            umma_commit(acc_full);
+          }
+        }
+        __syncwarp();
+        if (i + 1 < count) form(t_dp, sV, n + 2, dp_full);
       }
-      if (!ok && issued) {
-        umma_commit(drain_bar);
-        wait_drain(drain_bar, 0, 50000000ull);
-      }
+      ++items;
+    }
+    if (!ok && issued) {
+      if (elect_one()) umma_commit(drain_bar);
+      wait_drain(drain_bar, 0, 50000000ull);
     }
   } else {
-    const int half = warp >> 2;  // query columns 64 half .. + 64
+    const int quarter = warp >> 2;  // query columns 32 quarter .. + 32
     const int row = threadIdx.x & 127;
     const uint32_t t_lane = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t t_mine = t_lane + quarter * 32;
     uint32_t rounds = 0, items = 0, n = 1;  // n: the ring's next Q
     const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
     auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -315,75 +327,75 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) attn_dkv_kernel(const __grid_c
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
-    for (int64_t item = blockIdx.x; item < p.items; item += gridDim.x) {
+    for (uint32_t item = blockIdx.x; item < p.items; item += gridDim.x) {
       const DkvItem it = dkv_item(p, item);
       bool ok = true;
       for (int i = 0; i < it.n; ++i, ++rounds, n += 2) {
         // (S is complete once Q and its rows' values are there; the wait makes the copy visible here)
         ok = wait(&full[n % SLOTS], (n / SLOTS) & 1u) && wait(s_full, rounds & 1u);
         if (!ok) break;
-        const float2* values =
-            reinterpret_cast<const float2*>(sRows + (rounds % Shape::ROW_SLOTS) * ROW_VALUES + half * 64);
-        float pr[64];
-        tmem_load_64cols(t_s + t_lane + half * 64, pr);
+        const float4* values =
+            reinterpret_cast<const float4*>(sRows + (rounds % Shape::ROW_SLOTS) * ROW_VALUES + quarter * 32);
+        float pr[32];
+        uint32_t w[16];
+        tmem_load_32cols(t_s + t_mine, pr);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t w[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int col = 32 * c + 2 * e;
-            const float2 lse = values[col / 2];
-            const float2 x = f2_unpack(f2_fma(f2_pack(pr[col], pr[col + 1]), sc2, f2_pack(lse.x, lse.y)));
-            pr[col] = exp2_fast(x.x);
-            pr[col + 1] = exp2_fast(x.y);
-            w[e] = pack2<T>(pr[col], pr[col + 1]);
-          }
-          tmem_store_16cols(t_s + t_lane + half * 64 + c * 16, w);
+        for (int e = 0; e < 8; ++e) {
+          const float4 lse = values[e];
+          const float2 x = f2_unpack(f2_fma(f2_pack(pr[4 * e], pr[4 * e + 1]), sc2, f2_pack(lse.x, lse.y)));
+          const float2 y = f2_unpack(f2_fma(f2_pack(pr[4 * e + 2], pr[4 * e + 3]), sc2, f2_pack(lse.z, lse.w)));
+          pr[4 * e] = exp2_fast(x.x);
+          pr[4 * e + 1] = exp2_fast(x.y);
+          pr[4 * e + 2] = exp2_fast(y.x);
+          pr[4 * e + 3] = exp2_fast(y.y);
+          w[2 * e] = pack2<T>(pr[4 * e], pr[4 * e + 1]);
+          w[2 * e + 1] = pack2<T>(pr[4 * e + 2], pr[4 * e + 3]);
         }
+        tmem_store_16cols(t_s + t_mine, w);
         arrive(p_ready);
         ok = wait(dp_full, rounds & 1u);
         if (!ok) break;
+        float dp[32];
+        tmem_load_32cols(t_dp + t_mine, dp);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float dp[32];
-          tmem_load_32cols(t_dp + t_lane + half * 64 + c * 32, dp);
-          uint32_t w[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int col = 32 * c + 2 * e;
-            const float2 delta = values[ATT_ROWS / 2 + col / 2];
-            const float2 ds = f2_unpack(f2_mul(f2_add(f2_pack(dp[2 * e], dp[2 * e + 1]), f2_pack(delta.x, delta.y)),
-                                               f2_pack(pr[col], pr[col + 1])));
-            w[e] = pack2<T>(ds.x, ds.y);
-          }
-          // (columns 0 .. 31 of this half, which were loaded before)
-          tmem_store_16cols(t_dp + t_lane + half * 64 + c * 16, w);
+        for (int e = 0; e < 8; ++e) {
+          const float4 delta = values[ATT_ROWS / 4 + e];
+          const float2 x = f2_unpack(f2_mul(f2_add(f2_pack(dp[4 * e], dp[4 * e + 1]), f2_pack(delta.x, delta.y)),
+                                            f2_pack(pr[4 * e], pr[4 * e + 1])));
+          const float2 y = f2_unpack(f2_mul(f2_add(f2_pack(dp[4 * e + 2], dp[4 * e + 3]), f2_pack(delta.z, delta.w)),
+                                            f2_pack(pr[4 * e + 2], pr[4 * e + 3])));
+          w[2 * e] = pack2<T>(x.x, x.y);
+          w[2 * e + 1] = pack2<T>(y.x, y.y);
         }
+        tmem_store_16cols(t_dp + t_mine, w);
         arrive(ds_ready);
       }
       if (!ok) break;
       if (it.n > 0 && !wait(acc_full, items & 1u)) break;
-      // half 0 writes dV, half 1 dK
+      // quarters 0 and 1 write dV, 2 and 3 dK, each half of the elements
+      const bool is_dk = quarter >= 2;
+      const int first = (quarter & 1) * (DP / 2);
       const int key = it.tile * ATT_ROWS + row;
       const bool live = key < p.h.keys;
       const bool used = it.n > 0 && key < it.length;
-      const uint32_t t_acc = (half ? t_dk : t_dv) + t_lane;
-      const AttStrides st = half ? p.dk_strides : p.dv_strides;
-      T* out = static_cast<T*>(half ? p.dk : p.dv) + it.b * st.batch + key * st.token + it.kv_head * st.head;
-      float* part = half ? p.part_dk : p.part_dv;
+      const uint32_t t_acc = (is_dk ? t_dk : t_dv) + t_lane;
+      const AttStrides st = is_dk ? p.dk_strides : p.dv_strides;
+      T* out = static_cast<T*>(is_dk ? p.dk : p.dv) + it.b * st.batch + key * st.token + it.kv_head * st.head;
+      float* part = is_dk ? p.part_dk : p.part_dv;
       if (part != nullptr)
         part += (((static_cast<int64_t>(it.split) * p.h.batch + it.b) * p.h.keys + key) * p.h.kv_heads + it.kv_head) *
                 p.h.head;
-      const float factor = half ? p.scale : 1.f;
+      const float factor = is_dk ? p.scale : 1.f;
 #pragma unroll
-      for (int c = 0; c < DP; c += 32) {
+      for (int q = 0; q < DP / 2; q += 16) {
+        const int c = first + q;
         if (c >= p.h.head) break;
-        float v[32];
+        float v[16];
         __syncwarp();
-        if (it.n > 0) tmem_load_32cols(t_acc + c, v);
+        if (it.n > 0) tmem_load_16cols(t_acc + c, v);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = used ? v[e] * factor : 0.f;
-        if (live) store_row32<T>(out, part, v, c, p.h.head);
+        for (int e = 0; e < 16; ++e) v[e] = used ? v[e] * factor : 0.f;
+        if (live) store_row16<T>(out, part, v, c, p.h.head);
       }
       if (it.n > 0) {
         tc_fence_before_sync();
@@ -397,7 +409,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) attn_dkv_kernel(const __grid_c
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  if (warp == 9) tmem_dealloc(tmem, 512);
+  if (warp == ATT_WARPS + 1) tmem_dealloc(tmem, 512);
 }
 
 // --------------------------------------------------------------------- dQ
@@ -418,7 +430,7 @@ struct DqParams {
   void* dq;
   float* part_dq;  // splits > 1: [split][batch][queries][heads][head]
   int splits, split_tiles;
-  int64_t items;
+  uint32_t items;
   int mma_k, mma_n;
   float scale, scale_log2;
   int* err;
@@ -430,15 +442,15 @@ struct DqItem {
   int k0, n;
 };
 
-__device__ __forceinline__ DqItem dq_item(const DqParams& p, int64_t item) {
+__device__ __forceinline__ DqItem dq_item(const DqParams& p, uint32_t item) {
   DqItem it;
-  const int tiles = p.h.query_tiles();
+  const uint32_t tiles = p.h.query_tiles(), splits = p.splits, groups = p.h.groups;
   it.tile = static_cast<int>(item % tiles);
   item /= tiles;
-  it.split = static_cast<int>(item % p.splits);
-  item /= p.splits;
-  it.group = static_cast<int>(item % p.h.groups);
-  it.b = static_cast<int>(item / p.h.groups);
+  it.split = static_cast<int>(item % splits);
+  item /= splits;
+  it.group = static_cast<int>(item % groups);
+  it.b = static_cast<int>(item / groups);
   it.length = att_length(p.lengths, it.b, p.h.keys);
   const int key_tiles = (it.length + ATT_ROWS - 1) / ATT_ROWS;
   it.k0 = min(it.split * p.split_tiles, key_tiles);
@@ -472,7 +484,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) attn_dq_kernel(const __grid_co
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
-  const int warp = threadIdx.x / 32;
+  const int warp = uniform(threadIdx.x / 32);
   const int lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
     for (int s = 0; s < KS; ++s) {
@@ -488,14 +500,14 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) attn_dq_kernel(const __grid_co
     mbar_init(&s_full[0], 1);
     mbar_init(&s_full[1], 1);
     mbar_init(dp_full, 1);
-    mbar_init(ds_ready, 8);
+    mbar_init(ds_ready, ATT_WARPS);
     mbar_init(acc_full, 1);
-    mbar_init(acc_empty, 8);
+    mbar_init(acc_empty, ATT_WARPS);
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 9) {
+  if (warp == ATT_WARPS + 1) {
     tmem_alloc(tmem_holder, 512);
     tmem_relinquish();
   }
@@ -507,11 +519,11 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) attn_dq_kernel(const __grid_co
   pdl_wait();
   pdl_launch_dependents();
 
-  if (warp == 8) {
+  if (warp == ATT_WARPS) {
     if (lane == 0) {
       uint32_t nk = 0, nv = 0, items = 0;
       bool ok = true;
-      for (int64_t item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
+      for (uint32_t item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
         const DqItem it = dq_item(p, item);
         if (it.n <= 0) continue;
         ok = wait_bounded(q_empty, (items & 1u) ^ 1u, abort_flag, p.err, ATT_WAIT_NS);
@@ -542,61 +554,71 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) attn_dq_kernel(const __grid_co
         if (items) wait_drain(q_full, (items - 1) & 1u, 50000000ull);
       }
     }
-  } else if (warp == 9) {
-    if (lane == 0) {
-      constexpr bool FP16 = !std::is_same<T, __nv_bfloat16>::value;
-      const uint32_t id_s = idesc_f16kind_f32(ATT_ROWS, ATT_ROWS, false, false, FP16);
-      const uint32_t id_acc = idesc_f16kind_f32(ATT_ROWS, p.mma_n, false, true, FP16);
-      uint32_t n = 0, items = 0;  // key tiles used up, items before this one
-      bool ok = true, issued = false;
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        ok = ok && wait_bounded(bar, parity, abort_flag, p.err, ATT_WAIT_NS);
-        if (ok) tc_fence_after_sync();
-        return ok;
-      };
-      auto form_s = [&](uint32_t k) {
-        if (!wait(&k_full[k % KS], (k / KS) & 1u)) return;
-        att_mma_rows(tmem + (k & 1u) * 128, sQ, sK + (k % KS) * TILE, p.mma_k, id_s);
+  } else if (warp == ATT_WARPS + 1) {
+    constexpr bool FP16 = !std::is_same<T, __nv_bfloat16>::value;
+    const uint32_t id_s = idesc_f16kind_f32(ATT_ROWS, ATT_ROWS, false, false, FP16);
+    const uint32_t id_acc = idesc_f16kind_f32(ATT_ROWS, p.mma_n, false, true, FP16);
+    uint32_t n = 0, items = 0;  // key tiles used up, items before this one
+    bool ok = true, issued = false;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      const bool got = wait_bounded(bar, parity, abort_flag, p.err, ATT_WAIT_NS);
+      ok = __all_sync(0xffffffffu, got);
+      tc_fence_after_sync();
+      return ok;
+    };
+    auto form_s = [&](uint32_t k) {
+      if (!wait(&k_full[k % KS], (k / KS) & 1u)) return;
+      if (elect_one()) {
+        att_mma_rows<DP>(tmem + (k & 1u) * 128, sQ, sK + (k % KS) * TILE, p.mma_k, id_s);
         umma_commit(&s_full[k & 1u]);
-        issued = true;
-      };
-      auto form_dp = [&](uint32_t k) {
-        if (!wait(&v_full[k % VS], (k / VS) & 1u)) return;
-        att_mma_rows(t_dp, sG, sV + (k % VS) * TILE, p.mma_k, id_s);
+      }
+      __syncwarp();
+      issued = true;
+    };
+    auto form_dp = [&](uint32_t k) {
+      if (!wait(&v_full[k % VS], (k / VS) & 1u)) return;
+      if (elect_one()) {
+        att_mma_rows<DP>(t_dp, sG, sV + (k % VS) * TILE, p.mma_k, id_s);
         umma_commit(dp_full);
         umma_commit(&v_empty[k % VS]);
-      };
-      for (int64_t item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
-        const DqItem it = dq_item(p, item);
-        if (it.n <= 0) continue;
-        if (!wait(q_full, items & 1u)) break;
-        form_s(n);
-        if (ok) form_dp(n);
-        if (ok && it.n > 1) form_s(n + 1);
-        for (int j = 0; ok && j < it.n; ++j, ++n) {
-          if (!wait(ds_ready, n & 1u)) break;
-          if (j + 1 < it.n) form_dp(n + 1);
-          if (j == 0 && ok) wait(acc_empty, (items & 1u) ^ 1u);
-          if (!ok) break;
-          const uint32_t a = tmem + (n & 1u) * 128;
-          att_mma_cols(t_dq, a, a + 64, sK + (n % KS) * TILE, id_acc, j > 0);
-          umma_commit(&k_empty[n % KS]);
-          if (j + 2 < it.n) form_s(n + 2);
-        }
+      }
+      __syncwarp();
+    };
+    for (uint32_t item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
+      const DqItem it = dq_item(p, item);
+      const int count = uniform(it.n);
+      if (count <= 0) continue;
+      if (!wait(q_full, items & 1u)) break;
+      form_s(n);
+      if (ok) form_dp(n);
+      if (ok && count > 1) form_s(n + 1);
+      for (int j = 0; ok && j < count; ++j, ++n) {
+        if (!wait(ds_ready, n & 1u)) break;
+        if (j + 1 < count) form_dp(n + 1);
+        if (j == 0 && ok) wait(acc_empty, (items & 1u) ^ 1u);
         if (!ok) break;
-        umma_commit(q_empty);
-        umma_commit(acc_full);
-        ++items;
+        if (elect_one()) {
+          att_mma_cols<32>(t_dq, tmem + (n & 1u) * 128, sK + (n % KS) * TILE, id_acc, j > 0);
+          umma_commit(&k_empty[n % KS]);
+          if (j + 1 == count) {
+            umma_commit(q_empty);
+            umma_commit(acc_full);
+          }
+        }
+        __syncwarp();
+        if (j + 2 < count) form_s(n + 2);
       }
-      if (!ok && issued) {
-        umma_commit(drain_bar);
-        wait_drain(drain_bar, 0, 50000000ull);
-      }
+      ++items;
+    }
+    if (!ok && issued) {
+      if (elect_one()) umma_commit(drain_bar);
+      wait_drain(drain_bar, 0, 50000000ull);
     }
   } else {
-    const int half = warp >> 2;  // key columns 64 half .. + 64
+    const int quarter = warp >> 2;  // key columns 32 quarter .. + 32
     const int row = threadIdx.x & 127;
     const uint32_t t_lane = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t t_mine = t_lane + quarter * 32;
     uint32_t n = 0, items = 0;
     const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
     auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -605,7 +627,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) attn_dq_kernel(const __grid_co
       tc_fence_after_sync();
       return true;
     };
-    for (int64_t item = blockIdx.x; item < p.items; item += gridDim.x) {
+    for (uint32_t item = blockIdx.x; item < p.items; item += gridDim.x) {
       const DqItem it = dq_item(p, item);
       const int token = it.tile * p.h.tile_tokens() + (row >> p.h.pack_log2);
       const int head = (it.group << p.h.pack_log2) + (row & ((1 << p.h.pack_log2) - 1));
@@ -615,49 +637,46 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) attn_dq_kernel(const __grid_co
       const uint64_t lse2 = f2_pack(lse, lse), delta2 = f2_pack(delta, delta);
       bool ok = true;
       for (int j = 0; j < it.n; ++j, ++n) {
-        const uint32_t t_s = tmem + (n & 1u) * 128 + t_lane + half * 64;
+        const uint32_t t_s = tmem + (n & 1u) * 128 + t_mine;
         ok = wait(&s_full[n & 1u], (n >> 1) & 1u);
         if (!ok) break;
-        float pr[64];
-        tmem_load_64cols(t_s, pr);
+        float pr[32];
+        tmem_load_32cols(t_s, pr);
 #pragma unroll
-        for (int e = 0; e < 64; e += 2) {
+        for (int e = 0; e < 32; e += 2) {
           const float2 x = f2_unpack(f2_fma(f2_pack(pr[e], pr[e + 1]), sc2, lse2));
           pr[e] = exp2_fast(x.x);
           pr[e + 1] = exp2_fast(x.y);
         }
         ok = wait(dp_full, n & 1u);
         if (!ok) break;
-        const int valid = it.length - (it.k0 + j) * ATT_ROWS;
-        const int mine = valid - half * 64;
+        float dp[32];
+        uint32_t w[16];
+        tmem_load_32cols(t_dp + t_mine, dp);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float dp[32];
-          tmem_load_32cols(t_dp + t_lane + half * 64 + c * 32, dp);
-          uint32_t w[16];
+        for (int e = 0; e < 16; ++e) {
+          const float2 ds = f2_unpack(f2_mul(f2_add(f2_pack(dp[2 * e], dp[2 * e + 1]), delta2),
+                                             f2_pack(pr[2 * e], pr[2 * e + 1])));
+          w[e] = pack2<T>(ds.x, ds.y);
+        }
+        const int valid = it.length - (it.k0 + j) * ATT_ROWS;
+        if (valid < ATT_ROWS) {
+          const int mine = valid - quarter * 32;
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const int col = 32 * c + 2 * e;
-            const float2 ds =
-                f2_unpack(f2_mul(f2_add(f2_pack(dp[2 * e], dp[2 * e + 1]), delta2), f2_pack(pr[col], pr[col + 1])));
-            w[e] = pack2<T>(ds.x, ds.y);
-            if (valid < ATT_ROWS) {
-              if (col >= mine) w[e] = 0u;
-              else if (col + 1 >= mine) w[e] &= 0xffffu;
-            }
+            if (2 * e >= mine) w[e] = 0u;
+            else if (2 * e + 1 >= mine) w[e] &= 0xffffu;
           }
-          tmem_store_16cols(t_s + c * 16, w);
-        }
-        if (valid < ATT_ROWS && half == 0) {
           // keys behind the last one meet a dS of zero: infinities and NaN would remain. (S, which also reads the
           // tile, is complete.)
           uint4* k = reinterpret_cast<uint4*>(sK + (n % KS) * TILE);
-          for (int i = valid * 8 + row; i < ATT_ROWS * 8; i += 128)
+          for (int i = valid * 8 + quarter * 128 + row; i < ATT_ROWS * 8; i += 512)
 #pragma unroll
             for (int c = 0; c < DP / 64; ++c) k[c * (ATT_CHUNK / 16) + i] = make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
           __syncwarp();
         }
+        tmem_store_16cols(t_s, w);
         tmem_store_wait();
         tc_fence_before_sync();
         __syncwarp();
@@ -673,15 +692,15 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) attn_dq_kernel(const __grid_co
         part += (((static_cast<int64_t>(it.split) * p.h.batch + it.b) * p.h.queries + token) * p.h.heads + head) *
                 p.h.head;
 #pragma unroll
-      for (int q = 0; q < DP / 2; q += 32) {
-        const int c = half * (DP / 2) + q;
+      for (int q = 0; q < DP / 4; q += 16) {
+        const int c = quarter * (DP / 4) + q;
         if (c >= p.h.head) break;
-        float v[32];
+        float v[16];
         __syncwarp();
-        if (it.n > 0) tmem_load_32cols(t_dq + t_lane + c, v);
+        if (it.n > 0) tmem_load_16cols(t_dq + t_lane + c, v);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = it.n > 0 ? v[e] * p.scale : 0.f;
-        if (live) store_row32<T>(out, part, v, c, p.h.head);
+        for (int e = 0; e < 16; ++e) v[e] = it.n > 0 ? v[e] * p.scale : 0.f;
+        if (live) store_row16<T>(out, part, v, c, p.h.head);
       }
       if (it.n > 0) {
         tc_fence_before_sync();
@@ -695,7 +714,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) attn_dq_kernel(const __grid_co
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  if (warp == 9) tmem_dealloc(tmem, 512);
+  if (warp == ATT_WARPS + 1) tmem_dealloc(tmem, 512);
 }
 
 // -------------------------------------------------------------------- sums
@@ -789,13 +808,13 @@ cudaError_t launch(const AttCall& c, const Plan& s, RowsParams& rows, DkvParams&
   }
   if (dkv.items > 0) {
     if ((e = att_prepare(attn_dkv_kernel<T, DP>, DkvShape<DP>::SMEM, dkv_ready)) != cudaSuccess) return e;
-    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(dkv.items, c.num_sms));
+    const unsigned grid = static_cast<unsigned>(std::min<uint32_t>(dkv.items, c.num_sms));
     e = launch_dependent(attn_dkv_kernel<T, DP>, dim3(grid), dim3(ATT_THREADS), DkvShape<DP>::SMEM, stream, dkv);
     if (e != cudaSuccess) return e;
   }
   if (dq.items > 0) {
     if ((e = att_prepare(attn_dq_kernel<T, DP>, DqShape<DP>::SMEM, dq_ready)) != cudaSuccess) return e;
-    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(dq.items, c.num_sms));
+    const unsigned grid = static_cast<unsigned>(std::min<uint32_t>(dq.items, c.num_sms));
     e = launch_dependent(attn_dq_kernel<T, DP>, dim3(grid), dim3(ATT_THREADS), DqShape<DP>::SMEM, stream, dq);
     if (e != cudaSuccess) return e;
   }
@@ -850,7 +869,7 @@ cudaError_t attn_backward(const AttCall& c, const void* grad_o, const void* q, c
   a.rounds = s.rounds;
   a.splits = s.dkv.splits;
   a.split_rounds = s.dkv.tiles;
-  a.items = static_cast<int64_t>(h.batch) * h.kv_heads * s.key_tiles * s.dkv.splits;
+  a.items = static_cast<uint32_t>(static_cast<int64_t>(h.batch) * h.kv_heads * s.key_tiles * s.dkv.splits);
   if (s.dkv.splits > 1) {
     a.part_dk = reinterpret_cast<float*>(workspace + s.dkv_at);
     a.part_dv = a.part_dk + s.dkv_part;
@@ -859,7 +878,7 @@ cudaError_t attn_backward(const AttCall& c, const void* grad_o, const void* q, c
   b.dq = dq;
   b.splits = s.dq.splits;
   b.split_tiles = s.dq.tiles;
-  b.items = static_cast<int64_t>(h.batch) * h.groups * tiles * s.dq.splits;
+  b.items = static_cast<uint32_t>(static_cast<int64_t>(h.batch) * h.groups * tiles * s.dq.splits);
   if (s.dq.splits > 1) b.part_dq = reinterpret_cast<float*>(workspace + s.dq_at);
   const bool wide = h.head > 64;
   if (c.dtype == PRM_BF16)

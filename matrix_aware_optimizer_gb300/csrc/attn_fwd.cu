@@ -69,10 +69,11 @@ constexpr float RESCALE_ABOVE = 8.f;
 
 template <int DP>
 struct FwdShape {
-  static constexpr int STAGES = DP == 128 ? 5 : 8;  // of one key or value tile
+  static constexpr int STAGES = DP == 128 ? 4 : 8;  // of one key or value tile
   static constexpr uint32_t TILE = ATT_TILE<DP>;
-  static constexpr size_t BARRIERS = 512;
-  static constexpr size_t SMEM = 1024 + (2 + STAGES) * TILE + BARRIERS;
+  // barriers, and what the halves of a row tell each other
+  static constexpr size_t REST = 512 + 2 * 2 * 2 * ATT_ROWS * sizeof(float);
+  static constexpr size_t SMEM = 1024 + (2 + STAGES) * TILE + REST;
 };
 static_assert(FwdShape<128>::SMEM <= 232448 && FwdShape<64>::SMEM <= 232448, "shared memory above 227 KB");
 
@@ -87,7 +88,7 @@ struct FwdParams {
   float* part_lse;  // splits > 1: [split][batch][heads][queries]
   int blocks;       // pairs of query tiles
   int splits, split_tiles;  // key ranges, key tiles of one
-  int64_t items;
+  uint32_t items;
   int mma_k;        // 16-element steps of a head
   int mma_n;        // head rounded up to 16
   float scale_log2;
@@ -101,14 +102,18 @@ struct FwdItem {
   int tiles;    // query tiles with rows: 1 or 2
 };
 
-__device__ __forceinline__ FwdItem fwd_item(const FwdParams& p, int64_t item) {
+__device__ __forceinline__ FwdItem fwd_item(const FwdParams& p, uint32_t item) {
   FwdItem it;
-  it.block = static_cast<int>(item % p.blocks);
-  item /= p.blocks;
-  it.split = static_cast<int>(item % p.splits);
-  item /= p.splits;
-  it.group = static_cast<int>(item % p.h.groups);
-  it.b = static_cast<int>(item / p.h.groups);
+  const uint32_t blocks = p.blocks, splits = p.splits, groups = p.h.groups;
+  it.block = static_cast<int>(item % blocks);
+  item /= blocks;
+  it.split = 0;
+  if (splits > 1) {
+    it.split = static_cast<int>(item % splits);
+    item /= splits;
+  }
+  it.group = static_cast<int>(item % groups);
+  it.b = static_cast<int>(item / groups);
   it.length = att_length(p.lengths, it.b, p.h.keys);
   const int tiles = (it.length + ATT_ROWS - 1) / ATT_ROWS;
   it.k0 = min(it.split * p.split_tiles, tiles);
@@ -124,10 +129,10 @@ __device__ __forceinline__ void hide(float (&s)[64], int valid) {
     if (i >= valid) s[i] = -INFINITY;
 }
 
-// Four maxima over s, new or joined to those that are there.
-__device__ __forceinline__ void top4(const float (&s)[64], float (&mx)[4], bool first) {
+// Four maxima over s.
+__device__ __forceinline__ void top4(const float (&s)[64], float (&mx)[4]) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) mx[e] = first ? s[e] : fmaxf(mx[e], s[e]);
+  for (int e = 0; e < 4; ++e) mx[e] = s[e];
 #pragma unroll
   for (int i = 4; i < 64; i += 4)
 #pragma unroll
@@ -170,10 +175,12 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) attn_fwd_kernel(const __grid_c
   uint64_t* pv_done = p_full + 2;
   uint64_t* o_empty = pv_done + 2;
   uint64_t* drain_bar = o_empty + 2;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain_bar + 1);
+  uint64_t* pair_bar = drain_bar + 1;  // of the two warps that share 32 rows of a tile
+  float* sPair = reinterpret_cast<float*>(pair_bar + 8);  // [step parity][tile][half][row]
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sPair + 2 * 2 * 2 * ATT_ROWS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
-  const int warp = threadIdx.x / 32;
+  const int warp = uniform(threadIdx.x / 32);
   const int lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -184,15 +191,16 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) attn_fwd_kernel(const __grid_c
       mbar_init(&q_full[t], 1);
       mbar_init(&q_empty[t], 1);
       mbar_init(&s_full[t], 1);
-      mbar_init(&p_full[t], 4);
+      mbar_init(&p_full[t], ATT_WARPS / 2);
       mbar_init(&pv_done[t], 1);
-      mbar_init(&o_empty[t], 4);
+      mbar_init(&o_empty[t], ATT_WARPS / 2);
     }
+    for (int i = 0; i < 8; ++i) mbar_init(&pair_bar[i], 2);
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 9) {
+  if (warp == ATT_WARPS + 1) {
     tmem_alloc(tmem_holder, 512);
     tmem_relinquish();
   }
@@ -203,7 +211,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) attn_fwd_kernel(const __grid_c
   pdl_wait();
   pdl_launch_dependents();
 
-  if (warp == 8) {
+  if (warp == ATT_WARPS) {
     if (lane == 0) {
       uint32_t kv = 0, q_used[2] = {0, 0};  // tiles loaded so far
       uint32_t issued = 0;
@@ -217,7 +225,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) attn_fwd_kernel(const __grid_c
                           it.b);
         ++kv;
       };
-      for (int64_t item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
+      for (uint32_t item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
         const FwdItem it = fwd_item(p, item);
         if (it.n <= 0) continue;
         for (int t = 0; ok && t < it.tiles; ++t) {
@@ -244,163 +252,113 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) attn_fwd_kernel(const __grid_c
           if (q_used[t]) wait_drain(&q_full[t], (q_used[t] - 1) & 1u, 50000000ull);
       }
     }
-  } else if (warp == 9) {
-    if (lane == 0) {
-      constexpr bool FP16 = !std::is_same<T, __nv_bfloat16>::value;
-      const uint32_t id_s = idesc_f16kind_f32(ATT_ROWS, ATT_ROWS, false, false, FP16);
-      const uint32_t id_o = idesc_f16kind_f32(ATT_ROWS, p.mma_n, false, true, FP16);
-      uint32_t kv = 0;                                      // key and value tiles used up
-      uint32_t q_used[2] = {0, 0}, p_used[2] = {0, 0}, o_used[2] = {0, 0};
-      bool ok = true, issued = false;
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        ok = ok && wait_bounded(bar, parity, abort_flag, p.err, ATT_WAIT_NS);
-        if (ok) tc_fence_after_sync();
-        return ok;
-      };
-      auto wait_kv = [&](uint32_t n) { return wait(&kv_full[n % STAGES], (n / STAGES) & 1u); };
-      auto form_s = [&](int t, uint32_t n, bool last) {
-        att_mma_rows(tmem + t * ATT_ROWS, sQ + t * TILE, sKV + (n % STAGES) * TILE, p.mma_k, id_s);
+  } else if (warp == ATT_WARPS + 1) {
+    constexpr bool FP16 = !std::is_same<T, __nv_bfloat16>::value;
+    const uint32_t id_s = idesc_f16kind_f32(ATT_ROWS, ATT_ROWS, false, false, FP16);
+    const uint32_t id_o = idesc_f16kind_f32(ATT_ROWS, p.mma_n, false, true, FP16);
+    uint32_t kv = 0;                                      // key and value tiles used up
+    uint32_t q_used[2] = {0, 0}, p_used[2] = {0, 0}, o_used[2] = {0, 0};
+    bool ok = true, issued = false;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      const bool got = wait_bounded(bar, parity, abort_flag, p.err, ATT_WAIT_NS);
+      ok = __all_sync(0xffffffffu, got);
+      tc_fence_after_sync();
+      return ok;
+    };
+    auto wait_kv = [&](uint32_t n) { return wait(&kv_full[n % STAGES], (n / STAGES) & 1u); };
+    auto form_s = [&](int t, uint32_t n, bool last, bool free_k) {
+      if (elect_one()) {
+        att_mma_rows<DP>(tmem + t * ATT_ROWS, sQ + t * TILE, sKV + (n % STAGES) * TILE, p.mma_k, id_s);
         umma_commit(&s_full[t]);
         if (last) umma_commit(&q_empty[t]);
-        issued = true;
-      };
-      for (int64_t item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
-        const FwdItem it = fwd_item(p, item);
-        if (it.n <= 0) continue;
-        for (int t = 0; t < it.tiles; ++t) {
-          if (!wait(&q_full[t], q_used[t] & 1u) || !wait_kv(kv)) break;
-          ++q_used[t];
-          form_s(t, kv, it.n == 1);
-        }
-        if (!ok) break;
-        umma_commit(&kv_empty[kv % STAGES]);
-        for (int j = 0; ok && j < it.n; ++j, kv += 2) {
-          for (int t = 0; t < it.tiles; ++t) {
-            if (!wait(&p_full[t], p_used[t] & 1u) || !wait_kv(kv + 1)) break;
-            ++p_used[t];
-            if (j == 0) {
-              if (!wait(&o_empty[t], (o_used[t] & 1u) ^ 1u)) break;
-              ++o_used[t];
-            }
-            const uint32_t a = tmem + t * ATT_ROWS;
-            att_mma_cols(tmem + 2 * ATT_ROWS + t * DP, a, a + 64, sKV + ((kv + 1) % STAGES) * TILE, id_o, j > 0);
-            umma_commit(&pv_done[t]);
-            if (j + 1 < it.n) {
-              if (!wait_kv(kv + 2)) break;
-              form_s(t, kv + 2, j + 2 == it.n);
-            }
-          }
-          if (!ok) break;
-          umma_commit(&kv_empty[(kv + 1) % STAGES]);
-          if (j + 1 < it.n) umma_commit(&kv_empty[(kv + 2) % STAGES]);
-        }
+        if (free_k) umma_commit(&kv_empty[n % STAGES]);
       }
-      if (!ok && issued) {
-        umma_commit(drain_bar);
-        wait_drain(drain_bar, 0, 50000000ull);
+      __syncwarp();
+      issued = true;
+    };
+    for (uint32_t item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
+      const FwdItem it = fwd_item(p, item);
+      const int n = uniform(it.n), tiles = uniform(it.tiles);
+      if (n <= 0) continue;
+      for (int t = 0; t < tiles; ++t) {
+        if (!wait(&q_full[t], q_used[t] & 1u) || !wait_kv(kv)) break;
+        ++q_used[t];
+        form_s(t, kv, n == 1, t + 1 == tiles);
+      }
+      for (int j = 0; ok && j < n; ++j, kv += 2) {
+        for (int t = 0; t < tiles; ++t) {
+          if (!wait(&p_full[t], p_used[t] & 1u) || !wait_kv(kv + 1)) break;
+          ++p_used[t];
+          if (j == 0) {
+            if (!wait(&o_empty[t], (o_used[t] & 1u) ^ 1u)) break;
+            ++o_used[t];
+          }
+          if (elect_one()) {
+            att_mma_cols<64>(tmem + 2 * ATT_ROWS + t * DP, tmem + t * ATT_ROWS, sKV + ((kv + 1) % STAGES) * TILE, id_o,
+                             j > 0);
+            umma_commit(&pv_done[t]);
+            if (t + 1 == tiles) umma_commit(&kv_empty[(kv + 1) % STAGES]);
+          }
+          __syncwarp();
+          if (j + 1 < n) {
+            if (!wait_kv(kv + 2)) break;
+            form_s(t, kv + 2, j + 2 == n, t + 1 == tiles);
+          }
+        }
       }
     }
+    if (!ok && issued) {
+      if (elect_one()) umma_commit(drain_bar);
+      wait_drain(drain_bar, 0, 50000000ull);
+    }
   } else {
-    const int t = warp >> 2;
+    // Two threads to a row: keys 64 half .. + 64 of a tile, and the same half of O's elements.
+    const int t = warp >> 3, half = (warp >> 2) & 1;
     const int row = threadIdx.x & 127;
     const uint32_t t_lane = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t t_s = tmem + t * ATT_ROWS + t_lane;
-    const uint32_t t_o = tmem + 2 * ATT_ROWS + t * DP + t_lane;
+    const uint32_t t_s = tmem + t * ATT_ROWS + half * 64 + t_lane;
+    const uint32_t t_o = tmem + 2 * ATT_ROWS + t * DP + half * (DP / 2) + t_lane;
+    uint64_t* pair = &pair_bar[t * 4 + (warp & 3)];
+    float* told = sPair + (t * 2 + half) * ATT_ROWS + row;
+    const float* heard = sPair + (t * 2 + 1 - half) * ATT_ROWS + row;
     uint32_t kv = 0, steps = 0;  // key and value tiles before this item, key tiles this tile has worked on
-    for (int64_t item = blockIdx.x; item < p.items; item += gridDim.x) {
+    uint32_t meetings = 0;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      const bool got = wait_bounded(bar, parity, abort_flag, p.err, ATT_WAIT_NS);
+      if (!__all_sync(0xffffffffu, got)) return false;
+      tc_fence_after_sync();
+      return true;
+    };
+    // Exchanges one value with the thread of the row's other half.
+    auto meet = [&](float mine, float* other) {
+      const uint32_t at = (meetings & 1u) * (4 * ATT_ROWS);
+      told[at] = mine;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pair);
+      const bool got = wait_bounded(pair, meetings & 1u, abort_flag, p.err, ATT_WAIT_NS);
+      if (!__all_sync(0xffffffffu, got)) return false;
+      *other = heard[at];
+      ++meetings;
+      return true;
+    };
+    // The last item's rows are written behind the next one's first exponentials, so that its last product has
+    // ended by then.
+    uint32_t held = 0, held_step = 0;  // its number + 1, its last step
+    float held_m = 0.f, held_l = 0.f;
+    auto finish = [&](uint32_t item, bool some, float m, float l, uint32_t step) {
       const FwdItem it = fwd_item(p, item);
       const int token = (it.block * 2 + t) * p.h.tile_tokens() + (row >> p.h.pack_log2);
       const int head = (it.group << p.h.pack_log2) + (row & ((1 << p.h.pack_log2) - 1));
       const bool live = token < p.h.queries;
-      float m = -INFINITY, l = 0.f;
-      bool ok = true;
-      if (it.n > 0 && t < it.tiles) {
-        for (int j = 0; j < it.n; ++j, ++steps) {
-          ok = wait_bounded(&s_full[t], steps & 1u, abort_flag, p.err, ATT_WAIT_NS);
-          if (!__all_sync(0xffffffffu, ok)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after_sync();
-          const int valid = it.length - (it.k0 + j) * ATT_ROWS;
-          float s[64], mx[4];
-          tmem_load_64cols(t_s, s);
-          if (valid < 64) hide(s, valid);
-          top4(s, mx, true);
-          tmem_load_64cols(t_s + 64, s);
-          if (valid < ATT_ROWS) {
-            hide(s, valid - 64);
-            if (t == 0) {
-              // what lies behind the last key must not meet its P of zero: infinities and NaN would remain
-              const uint32_t n = kv + 2 * j + 1;
-              ok = wait_bounded(&kv_full[n % STAGES], (n / STAGES) & 1u, abort_flag, p.err, ATT_WAIT_NS);
-              if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                break;
-              }
-              uint4* v = reinterpret_cast<uint4*>(sKV + (n % STAGES) * TILE);
-              for (int i = valid * 8 + row; i < ATT_ROWS * 8; i += 128)
-#pragma unroll
-                for (int c = 0; c < DP / 64; ++c) v[c * (ATT_CHUNK / 16) + i] = make_uint4(0, 0, 0, 0);
-              fence_proxy_async_smem();
-              __syncwarp();
-            }
-          }
-          top4(s, mx, false);
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          if (j == 0) {
-            m = top;
-          } else {
-            const bool grows = (top - m) * p.scale_log2 > RESCALE_ABOVE;  // (from -inf: always)
-            if (__any_sync(0xffffffffu, grows)) {
-              const float factor = grows ? exp2_fast((m - top) * p.scale_log2) : 1.f;
-              if (grows) m = top;
-              l *= factor;
-              ok = wait_bounded(&pv_done[t], (steps - 1) & 1u, abort_flag, p.err, ATT_WAIT_NS);
-              if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after_sync();
-#pragma unroll
-              for (int c = 0; c < DP; c += 16) {
-                if (c >= p.mma_n) break;
-                float o[16];
-                tmem_load_16cols(t_o + c, o);
-                uint32_t w[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i] * factor);
-                tmem_store_16cols(t_o + c, w);
-              }
-            }
-          }
-          const float base = m == -INFINITY ? 0.f : m * p.scale_log2;
-          const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2), nb2 = f2_pack(-base, -base);
-          uint64_t sum[2] = {0, 0};
-          // the second half's P goes over the second half of S, which is in registers; then the first's
-          exponentials<T>(s, sc2, nb2, sum, t_s + 64);
-          tmem_load_64cols(t_s, s);
-          if (valid < 64) hide(s, valid);
-          exponentials<T>(s, sc2, nb2, sum, t_s);
-          const float2 total = f2_unpack(f2_add(sum[0], sum[1]));
-          l += total.x + total.y;
-          tmem_store_wait();
-          tc_fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[t]);
-        }
-        if (!ok) break;
-        ok = wait_bounded(&pv_done[t], (steps - 1) & 1u, abort_flag, p.err, ATT_WAIT_NS);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        tc_fence_after_sync();
+      if (some) {
+        float other;
+        if (!meet(l, &other) || !wait(&pv_done[t], step & 1u)) return false;
+        l = half ? other + l : l + other;
       }
-      const bool some = it.n > 0;
-      kv += some ? 2 * it.n : 0;
-      if (t >= it.tiles) continue;
       const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-      const float lse = some ? m * p.scale_log2 + log2f(l) : -INFINITY;
       const int64_t at_lse = (static_cast<int64_t>(it.b) * p.h.heads + head) * p.h.queries + token;
-      if (live) {
+      if (live && half == 0) {
+        const float lse = some ? m * p.scale_log2 + log2f(l) : -INFINITY;
         if (p.splits > 1)
           p.part_lse[static_cast<int64_t>(it.split) * p.h.batch * p.h.heads * p.h.queries + at_lse] = lse;
         else if (p.lse != nullptr)
@@ -410,16 +368,12 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) attn_fwd_kernel(const __grid_c
       float* part = p.part_o + (((static_cast<int64_t>(it.split) * p.h.batch + it.b) * p.h.queries + token) *
                                     p.h.heads + head) * p.h.head;
 #pragma unroll
-      for (int c = 0; c < DP; c += 32) {
+      for (int q = 0; q < DP / 2; q += 32) {
+        const int c = half * (DP / 2) + q;
         if (c >= p.h.head) break;
         float o[32];
         __syncwarp();
-        if (some) {
-          tmem_load_32cols(t_o + c, o);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = 0.f;
-        }
+        if (some) tmem_load_32cols(t_o + q, o);
 #pragma unroll
         for (int i = 0; i < 32; i += 8) {
           if (c + i >= p.h.head || !live) break;
@@ -442,13 +396,91 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) attn_fwd_kernel(const __grid_c
         __syncwarp();
         if (lane == 0) mbar_arrive(&o_empty[t]);
       }
+      return true;
+    };
+    bool ok = true;
+    for (uint32_t item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
+      const FwdItem it = fwd_item(p, item);
+      if (it.n <= 0) {
+        if (t < it.tiles) finish(item, false, -INFINITY, 0.f, 0);
+        continue;
+      }
+      if (t >= it.tiles) {
+        kv += 2 * it.n;
+        continue;
+      }
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < it.n; ++j, ++steps) {
+        if (!(ok = wait(&s_full[t], steps & 1u))) break;
+        const int valid = it.length - (it.k0 + j) * ATT_ROWS;
+        float s[64], mx[4];
+        tmem_load_64cols(t_s, s);
+        if (valid < ATT_ROWS) {
+          hide(s, valid - half * 64);
+          if (t == 0) {
+            // what lies behind the last key must not meet its P of zero: infinities and NaN would remain
+            const uint32_t n = kv + 2 * j + 1;
+            if (!(ok = wait(&kv_full[n % STAGES], (n / STAGES) & 1u))) break;
+            uint4* v = reinterpret_cast<uint4*>(sKV + (n % STAGES) * TILE);
+            for (int i = valid * 8 + half * 128 + row; i < ATT_ROWS * 8; i += 256)
+#pragma unroll
+              for (int c = 0; c < DP / 64; ++c) v[c * (ATT_CHUNK / 16) + i] = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+        }
+        top4(s, mx);
+        float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), other;
+        if (!(ok = meet(top, &other))) break;
+        top = fmaxf(top, other);
+        if (j == 0) {
+          m = top;
+        } else {
+          const bool grows = (top - m) * p.scale_log2 > RESCALE_ABOVE;  // (from -inf: always)
+          if (__any_sync(0xffffffffu, grows)) {
+            const float factor = grows ? exp2_fast((m - top) * p.scale_log2) : 1.f;
+            if (grows) m = top;
+            l *= factor;
+            if (!(ok = wait(&pv_done[t], (steps - 1) & 1u))) break;
+#pragma unroll
+            for (int c = 0; c < DP / 2; c += 16) {
+              float o[16];
+              tmem_load_16cols(t_o + c, o);
+              uint32_t w[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i] * factor);
+              tmem_store_16cols(t_o + c, w);
+            }
+          }
+        }
+        const float base = m == -INFINITY ? 0.f : m * p.scale_log2;
+        const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2), nb2 = f2_pack(-base, -base);
+        uint64_t sum[2] = {0, 0};
+        exponentials<T>(s, sc2, nb2, sum, t_s);
+        const float2 total = f2_unpack(f2_add(sum[0], sum[1]));
+        l += total.x + total.y;
+        tmem_store_wait();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[t]);
+        if (j == 0 && held > 0) {
+          if (!(ok = finish(held - 1, true, held_m, held_l, held_step))) break;
+          held = 0;
+        }
+      }
+      kv += 2 * it.n;
+      held = item + 1;
+      held_m = m;
+      held_l = l;
+      held_step = steps - 1;
     }
+    if (ok && held > 0) finish(held - 1, true, held_m, held_l, held_step);
   }
   __syncwarp();
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  if (warp == 9) tmem_dealloc(tmem, 512);
+  if (warp == ATT_WARPS + 1) tmem_dealloc(tmem, 512);
 }
 
 // Parts of the keys joined: lse = log2 sum 2^lse_s, o = sum 2^(lse_s - lse) o_s.
@@ -532,7 +564,7 @@ cudaError_t launch_fwd(const FwdParams& p, int num_sms, cudaStream_t stream) {
   static std::atomic<uint64_t> ready{0};
   const cudaError_t e = att_prepare(attn_fwd_kernel<T, DP>, FwdShape<DP>::SMEM, ready);
   if (e != cudaSuccess) return e;
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(p.items, num_sms));
+  const unsigned grid = static_cast<unsigned>(std::min<uint32_t>(p.items, num_sms));
   return launch_dependent(attn_fwd_kernel<T, DP>, dim3(grid), dim3(ATT_THREADS), FwdShape<DP>::SMEM, stream, p);
 }
 
@@ -550,7 +582,7 @@ cudaError_t attn_forward(const AttCall& c, const void* q, const void* k, const v
   const AttSplit sp = att_forward_split(c.h, c.num_sms);
   p.splits = sp.splits;
   p.split_tiles = sp.tiles;
-  p.items = static_cast<int64_t>(c.h.batch) * c.h.groups * p.splits * p.blocks;
+  p.items = static_cast<uint32_t>(static_cast<int64_t>(c.h.batch) * c.h.groups * p.splits * p.blocks);
   p.mma_k = (c.h.head + 15) / 16;
   p.mma_n = p.mma_k * 16;
   p.scale_log2 = c.scale * 1.4426950408889634f;
