@@ -132,9 +132,6 @@ template <int DP>
 constexpr uint32_t ATT_TILE = DP / 64 * ATT_CHUNK;
 constexpr uint64_t ATT_WAIT_NS = 2000000000ull;
 
-// Warps 0 .. 15 take elements, 16 loads, 17 issues products.
-constexpr int ATT_WARPS = 16;
-constexpr int ATT_THREADS = 32 * (ATT_WARPS + 2);
 
 template <int DP>
 __device__ __forceinline__ void att_load_tile(uint8_t* dst, const CUtensorMap* tm, uint64_t* bar, int head, int row,
@@ -171,15 +168,15 @@ __device__ __forceinline__ void att_mma_rows(uint32_t d, const uint8_t* a, const
   }
 }
 
-// D[128 x N] (+)= A B, A 128 x 128 in tensor memory, in pieces of `PIECE`
-// elements of K (PIECE / 2 columns) that start PIECE columns apart; B a tile
-// along its rows.
-template <int PIECE>
+// D[128 x N] (+)= A B over rows 16 FIRST .. 16 LAST of B, A 128 x 128 in
+// tensor memory, in pieces of `PIECE` elements of K (PIECE / 2 columns) that
+// start PIECE columns apart; B a tile along its rows.
+template <int PIECE, int FIRST = 0, int LAST = ATT_ROWS / 16>
 __device__ __forceinline__ void att_mma_cols(uint32_t d, uint32_t a, const uint8_t* b, uint32_t idesc,
                                              bool accumulate) {
   const uint64_t db = smem_desc_sw128(smem_u32(b), ATT_CHUNK, 1024);
 #pragma unroll
-  for (int k = 0; k < ATT_ROWS / 16; ++k)
+  for (int k = FIRST; k < LAST; ++k)
     umma_tmem_a(d, a + k * 16 / PIECE * PIECE + k * 16 % PIECE / 2, desc_at(db, k * 2048), idesc,
                 accumulate || k > 0 ? 1u : 0u);
 }

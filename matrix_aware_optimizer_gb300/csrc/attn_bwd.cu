@@ -31,6 +31,9 @@
 namespace prm {
 namespace {
 
+// Warps 0 .. 15 take elements, 16 loads, 17 issues products.
+constexpr int BWD_WARPS = 16;
+constexpr int BWD_THREADS = 32 * (BWD_WARPS + 2);
 constexpr int ROW_VALUES = 256;  // of a query tile: 128 times -lse, 128 times -delta
 constexpr size_t BWD_BARRIERS = 512;
 
@@ -158,7 +161,7 @@ __device__ __forceinline__ void store_row16(T* out, float* part, const float (&v
 }
 
 template <typename T, int DP>
-__global__ void __launch_bounds__(ATT_THREADS, 1) attn_dkv_kernel(const __grid_constant__ DkvParams p) {
+__global__ void __launch_bounds__(BWD_THREADS, 1) attn_dkv_kernel(const __grid_constant__ DkvParams p) {
   using Shape = DkvShape<DP>;
   constexpr int SLOTS = Shape::SLOTS;
   constexpr uint32_t TILE = Shape::TILE;
@@ -192,16 +195,16 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) attn_dkv_kernel(const __grid_c
     mbar_init(kv_full, 1);
     mbar_init(kv_empty, 1);
     mbar_init(s_full, 1);
-    mbar_init(p_ready, ATT_WARPS);
+    mbar_init(p_ready, BWD_WARPS);
     mbar_init(dp_full, 1);
-    mbar_init(ds_ready, ATT_WARPS);
+    mbar_init(ds_ready, BWD_WARPS);
     mbar_init(acc_full, 1);
-    mbar_init(acc_empty, ATT_WARPS);
+    mbar_init(acc_empty, BWD_WARPS);
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == ATT_WARPS + 1) {
+  if (warp == BWD_WARPS + 1) {
     tmem_alloc(tmem_holder, 512);
     tmem_relinquish();
   }
@@ -214,7 +217,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) attn_dkv_kernel(const __grid_c
   pdl_launch_dependents();
   const int tiles = p.h.query_tiles();
 
-  if (warp == ATT_WARPS) {
+  if (warp == BWD_WARPS) {
     if (lane == 0) {
       uint32_t n = 0, rounds = 0, items = 0;  // loads into the ring, rounds, items so far
       bool ok = true;
@@ -251,7 +254,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) attn_dkv_kernel(const __grid_c
         if (items) wait_drain(kv_full, (items - 1) & 1u, 50000000ull);
       }
     }
-  } else if (warp == ATT_WARPS + 1) {
+  } else if (warp == BWD_WARPS + 1) {
     constexpr bool FP16 = !std::is_same<T, __nv_bfloat16>::value;
     const uint32_t id_s = idesc_f16kind_f32(ATT_ROWS, ATT_ROWS, false, false, FP16);
     const uint32_t id_acc = idesc_f16kind_f32(ATT_ROWS, p.mma_n, false, true, FP16);
@@ -409,7 +412,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) attn_dkv_kernel(const __grid_c
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  if (warp == ATT_WARPS + 1) tmem_dealloc(tmem, 512);
+  if (warp == BWD_WARPS + 1) tmem_dealloc(tmem, 512);
 }
 
 // --------------------------------------------------------------------- dQ
@@ -459,7 +462,7 @@ __device__ __forceinline__ DqItem dq_item(const DqParams& p, uint32_t item) {
 }
 
 template <typename T, int DP>
-__global__ void __launch_bounds__(ATT_THREADS, 1) attn_dq_kernel(const __grid_constant__ DqParams p) {
+__global__ void __launch_bounds__(BWD_THREADS, 1) attn_dq_kernel(const __grid_constant__ DqParams p) {
   using Shape = DqShape<DP>;
   constexpr int KS = Shape::KS, VS = Shape::VS;
   constexpr uint32_t TILE = Shape::TILE;
@@ -500,14 +503,14 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) attn_dq_kernel(const __grid_co
     mbar_init(&s_full[0], 1);
     mbar_init(&s_full[1], 1);
     mbar_init(dp_full, 1);
-    mbar_init(ds_ready, ATT_WARPS);
+    mbar_init(ds_ready, BWD_WARPS);
     mbar_init(acc_full, 1);
-    mbar_init(acc_empty, ATT_WARPS);
+    mbar_init(acc_empty, BWD_WARPS);
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == ATT_WARPS + 1) {
+  if (warp == BWD_WARPS + 1) {
     tmem_alloc(tmem_holder, 512);
     tmem_relinquish();
   }
@@ -519,7 +522,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) attn_dq_kernel(const __grid_co
   pdl_wait();
   pdl_launch_dependents();
 
-  if (warp == ATT_WARPS) {
+  if (warp == BWD_WARPS) {
     if (lane == 0) {
       uint32_t nk = 0, nv = 0, items = 0;
       bool ok = true;
@@ -554,7 +557,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) attn_dq_kernel(const __grid_co
         if (items) wait_drain(q_full, (items - 1) & 1u, 50000000ull);
       }
     }
-  } else if (warp == ATT_WARPS + 1) {
+  } else if (warp == BWD_WARPS + 1) {
     constexpr bool FP16 = !std::is_same<T, __nv_bfloat16>::value;
     const uint32_t id_s = idesc_f16kind_f32(ATT_ROWS, ATT_ROWS, false, false, FP16);
     const uint32_t id_acc = idesc_f16kind_f32(ATT_ROWS, p.mma_n, false, true, FP16);
@@ -714,7 +717,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) attn_dq_kernel(const __grid_co
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  if (warp == ATT_WARPS + 1) tmem_dealloc(tmem, 512);
+  if (warp == BWD_WARPS + 1) tmem_dealloc(tmem, 512);
 }
 
 // -------------------------------------------------------------------- sums
@@ -809,13 +812,13 @@ cudaError_t launch(const AttCall& c, const Plan& s, RowsParams& rows, DkvParams&
   if (dkv.items > 0) {
     if ((e = att_prepare(attn_dkv_kernel<T, DP>, DkvShape<DP>::SMEM, dkv_ready)) != cudaSuccess) return e;
     const unsigned grid = static_cast<unsigned>(std::min<uint32_t>(dkv.items, c.num_sms));
-    e = launch_dependent(attn_dkv_kernel<T, DP>, dim3(grid), dim3(ATT_THREADS), DkvShape<DP>::SMEM, stream, dkv);
+    e = launch_dependent(attn_dkv_kernel<T, DP>, dim3(grid), dim3(BWD_THREADS), DkvShape<DP>::SMEM, stream, dkv);
     if (e != cudaSuccess) return e;
   }
   if (dq.items > 0) {
     if ((e = att_prepare(attn_dq_kernel<T, DP>, DqShape<DP>::SMEM, dq_ready)) != cudaSuccess) return e;
     const unsigned grid = static_cast<unsigned>(std::min<uint32_t>(dq.items, c.num_sms));
-    e = launch_dependent(attn_dq_kernel<T, DP>, dim3(grid), dim3(ATT_THREADS), DqShape<DP>::SMEM, stream, dq);
+    e = launch_dependent(attn_dq_kernel<T, DP>, dim3(grid), dim3(BWD_THREADS), DqShape<DP>::SMEM, stream, dq);
     if (e != cudaSuccess) return e;
   }
   if (s.dkv.splits > 1) {

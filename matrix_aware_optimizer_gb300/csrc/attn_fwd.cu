@@ -65,15 +65,17 @@ bool att_encode(CUtensorMap* map, const void* base, int dtype, int64_t batch, in
 
 namespace {
 
+// Warps 0 .. 3 and 4 .. 7 take the two tiles' rows, 8 loads, 9 issues products.
+constexpr int FWD_WARPS = 8;
+constexpr int FWD_THREADS = 32 * (FWD_WARPS + 2);
 constexpr float RESCALE_ABOVE = 8.f;
 
 template <int DP>
 struct FwdShape {
-  static constexpr int STAGES = DP == 128 ? 4 : 8;  // of one key or value tile
+  static constexpr int STAGES = DP == 128 ? 5 : 8;  // of one key or value tile
   static constexpr uint32_t TILE = ATT_TILE<DP>;
-  // barriers, and what the halves of a row tell each other
-  static constexpr size_t REST = 512 + 2 * 2 * 2 * ATT_ROWS * sizeof(float);
-  static constexpr size_t SMEM = 1024 + (2 + STAGES) * TILE + REST;
+  static constexpr size_t BARRIERS = 512;
+  static constexpr size_t SMEM = 1024 + (2 + STAGES) * TILE + BARRIERS;
 };
 static_assert(FwdShape<128>::SMEM <= 232448 && FwdShape<64>::SMEM <= 232448, "shared memory above 227 KB");
 
@@ -129,10 +131,10 @@ __device__ __forceinline__ void hide(float (&s)[64], int valid) {
     if (i >= valid) s[i] = -INFINITY;
 }
 
-// Four maxima over s.
-__device__ __forceinline__ void top4(const float (&s)[64], float (&mx)[4]) {
+// Four maxima over s, new or joined to those that are there.
+__device__ __forceinline__ void top4(const float (&s)[64], float (&mx)[4], bool first) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) mx[e] = s[e];
+  for (int e = 0; e < 4; ++e) mx[e] = first ? s[e] : fmaxf(mx[e], s[e]);
 #pragma unroll
   for (int i = 4; i < 64; i += 4)
 #pragma unroll
@@ -158,7 +160,7 @@ __device__ __forceinline__ void exponentials(const float (&s)[64], uint64_t scal
 }
 
 template <typename T, int DP>
-__global__ void __launch_bounds__(ATT_THREADS, 1) attn_fwd_kernel(const __grid_constant__ FwdParams p) {
+__global__ void __launch_bounds__(FWD_THREADS, 1) attn_fwd_kernel(const __grid_constant__ FwdParams p) {
   using Shape = FwdShape<DP>;
   constexpr int STAGES = Shape::STAGES;
   constexpr uint32_t TILE = Shape::TILE;
@@ -171,13 +173,11 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) attn_fwd_kernel(const __grid_c
   uint64_t* q_full = kv_empty + STAGES;
   uint64_t* q_empty = q_full + 2;
   uint64_t* s_full = q_empty + 2;
-  uint64_t* p_full = s_full + 2;
-  uint64_t* pv_done = p_full + 2;
+  uint64_t* p_full = s_full + 2;  // [tile][half]: of the keys 0 .. 63, 64 .. 127
+  uint64_t* pv_done = p_full + 4;
   uint64_t* o_empty = pv_done + 2;
   uint64_t* drain_bar = o_empty + 2;
-  uint64_t* pair_bar = drain_bar + 1;  // of the two warps that share 32 rows of a tile
-  float* sPair = reinterpret_cast<float*>(pair_bar + 8);  // [step parity][tile][half][row]
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sPair + 2 * 2 * 2 * ATT_ROWS);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
   const int warp = uniform(threadIdx.x / 32);
@@ -191,16 +191,16 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) attn_fwd_kernel(const __grid_c
       mbar_init(&q_full[t], 1);
       mbar_init(&q_empty[t], 1);
       mbar_init(&s_full[t], 1);
-      mbar_init(&p_full[t], ATT_WARPS / 2);
+      mbar_init(&p_full[2 * t], FWD_WARPS / 2);
+      mbar_init(&p_full[2 * t + 1], FWD_WARPS / 2);
       mbar_init(&pv_done[t], 1);
-      mbar_init(&o_empty[t], ATT_WARPS / 2);
+      mbar_init(&o_empty[t], FWD_WARPS / 2);
     }
-    for (int i = 0; i < 8; ++i) mbar_init(&pair_bar[i], 2);
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == ATT_WARPS + 1) {
+  if (warp == FWD_WARPS + 1) {
     tmem_alloc(tmem_holder, 512);
     tmem_relinquish();
   }
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) attn_fwd_kernel(const __grid_c
   pdl_wait();
   pdl_launch_dependents();
 
-  if (warp == ATT_WARPS) {
+  if (warp == FWD_WARPS) {
     if (lane == 0) {
       uint32_t kv = 0, q_used[2] = {0, 0};  // tiles loaded so far
       uint32_t issued = 0;
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) attn_fwd_kernel(const __grid_c
           if (q_used[t]) wait_drain(&q_full[t], (q_used[t] - 1) & 1u, 50000000ull);
       }
     }
-  } else if (warp == ATT_WARPS + 1) {
+  } else if (warp == FWD_WARPS + 1) {
     constexpr bool FP16 = !std::is_same<T, __nv_bfloat16>::value;
     const uint32_t id_s = idesc_f16kind_f32(ATT_ROWS, ATT_ROWS, false, false, FP16);
     const uint32_t id_o = idesc_f16kind_f32(ATT_ROWS, p.mma_n, false, true, FP16);
@@ -281,27 +281,30 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) attn_fwd_kernel(const __grid_c
       const int n = uniform(it.n), tiles = uniform(it.tiles);
       if (n <= 0) continue;
       for (int t = 0; t < tiles; ++t) {
-        if (!wait(&q_full[t], q_used[t] & 1u) || !wait_kv(kv)) break;
+        if ((t == 0 && !wait_kv(kv)) || !wait(&q_full[t], q_used[t] & 1u)) break;
         ++q_used[t];
         form_s(t, kv, n == 1, t + 1 == tiles);
       }
       for (int j = 0; ok && j < n; ++j, kv += 2) {
         for (int t = 0; t < tiles; ++t) {
-          if (!wait(&p_full[t], p_used[t] & 1u) || !wait_kv(kv + 1)) break;
-          ++p_used[t];
-          if (j == 0) {
-            if (!wait(&o_empty[t], (o_used[t] & 1u) ^ 1u)) break;
-            ++o_used[t];
-          }
+          // (the first tile's waits for keys and values hold for the second)
+          if ((t == 0 && !wait_kv(kv + 1)) || (j == 0 && !wait(&o_empty[t], (o_used[t] & 1u) ^ 1u))) break;
+          if (j == 0) ++o_used[t];
+          const uint32_t t_p = tmem + t * ATT_ROWS, t_o = tmem + 2 * ATT_ROWS + t * DP;
+          const uint8_t* v = sKV + ((kv + 1) % STAGES) * TILE;
+          if (!wait(&p_full[2 * t], p_used[t] & 1u)) break;
+          if (elect_one()) att_mma_cols<64, 0, 4>(t_o, t_p, v, id_o, j > 0);
+          __syncwarp();
+          if (!wait(&p_full[2 * t + 1], p_used[t] & 1u)) break;
           if (elect_one()) {
-            att_mma_cols<64>(tmem + 2 * ATT_ROWS + t * DP, tmem + t * ATT_ROWS, sKV + ((kv + 1) % STAGES) * TILE, id_o,
-                             j > 0);
+            att_mma_cols<64, 4, 8>(t_o, t_p, v, id_o, true);
             umma_commit(&pv_done[t]);
             if (t + 1 == tiles) umma_commit(&kv_empty[(kv + 1) % STAGES]);
           }
           __syncwarp();
+          ++p_used[t];
           if (j + 1 < n) {
-            if (!wait_kv(kv + 2)) break;
+            if (t == 0 && !wait_kv(kv + 2)) break;
             form_s(t, kv + 2, j + 2 == n, t + 1 == tiles);
           }
         }
@@ -312,52 +315,36 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) attn_fwd_kernel(const __grid_c
       wait_drain(drain_bar, 0, 50000000ull);
     }
   } else {
-    // Two threads to a row: keys 64 half .. + 64 of a tile, and the same half of O's elements.
-    const int t = warp >> 3, half = (warp >> 2) & 1;
+    const int t = warp >> 2;
     const int row = threadIdx.x & 127;
     const uint32_t t_lane = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t t_s = tmem + t * ATT_ROWS + half * 64 + t_lane;
-    const uint32_t t_o = tmem + 2 * ATT_ROWS + t * DP + half * (DP / 2) + t_lane;
-    uint64_t* pair = &pair_bar[t * 4 + (warp & 3)];
-    float* told = sPair + (t * 2 + half) * ATT_ROWS + row;
-    const float* heard = sPair + (t * 2 + 1 - half) * ATT_ROWS + row;
+    const uint32_t t_s = tmem + t * ATT_ROWS + t_lane;
+    const uint32_t t_o = tmem + 2 * ATT_ROWS + t * DP + t_lane;
     uint32_t kv = 0, steps = 0;  // key and value tiles before this item, key tiles this tile has worked on
-    uint32_t meetings = 0;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       const bool got = wait_bounded(bar, parity, abort_flag, p.err, ATT_WAIT_NS);
       if (!__all_sync(0xffffffffu, got)) return false;
       tc_fence_after_sync();
       return true;
     };
-    // Exchanges one value with the thread of the row's other half.
-    auto meet = [&](float mine, float* other) {
-      const uint32_t at = (meetings & 1u) * (4 * ATT_ROWS);
-      told[at] = mine;
+    auto arrive = [&](uint64_t* bar) {
+      tmem_store_wait();
+      tc_fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(pair);
-      const bool got = wait_bounded(pair, meetings & 1u, abort_flag, p.err, ATT_WAIT_NS);
-      if (!__all_sync(0xffffffffu, got)) return false;
-      *other = heard[at];
-      ++meetings;
-      return true;
+      if (lane == 0) mbar_arrive(bar);
     };
     // The last item's rows are written behind the next one's first exponentials, so that its last product has
     // ended by then.
-    uint32_t held = 0, held_step = 0;  // its number + 1, its last step
+    uint32_t held = 0;  // its number + 1
     float held_m = 0.f, held_l = 0.f;
-    auto finish = [&](uint32_t item, bool some, float m, float l, uint32_t step) {
+    auto finish = [&](uint32_t item, bool some, float m, float l) {
       const FwdItem it = fwd_item(p, item);
       const int token = (it.block * 2 + t) * p.h.tile_tokens() + (row >> p.h.pack_log2);
       const int head = (it.group << p.h.pack_log2) + (row & ((1 << p.h.pack_log2) - 1));
       const bool live = token < p.h.queries;
-      if (some) {
-        float other;
-        if (!meet(l, &other) || !wait(&pv_done[t], step & 1u)) return false;
-        l = half ? other + l : l + other;
-      }
       const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
       const int64_t at_lse = (static_cast<int64_t>(it.b) * p.h.heads + head) * p.h.queries + token;
-      if (live && half == 0) {
+      if (live) {
         const float lse = some ? m * p.scale_log2 + log2f(l) : -INFINITY;
         if (p.splits > 1)
           p.part_lse[static_cast<int64_t>(it.split) * p.h.batch * p.h.heads * p.h.queries + at_lse] = lse;
@@ -368,12 +355,11 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) attn_fwd_kernel(const __grid_c
       float* part = p.part_o + (((static_cast<int64_t>(it.split) * p.h.batch + it.b) * p.h.queries + token) *
                                     p.h.heads + head) * p.h.head;
 #pragma unroll
-      for (int q = 0; q < DP / 2; q += 32) {
-        const int c = half * (DP / 2) + q;
+      for (int c = 0; c < DP; c += 32) {
         if (c >= p.h.head) break;
         float o[32];
         __syncwarp();
-        if (some) tmem_load_32cols(t_o + q, o);
+        if (some) tmem_load_32cols(t_o + c, o);
 #pragma unroll
         for (int i = 0; i < 32; i += 8) {
           if (c + i >= p.h.head || !live) break;
@@ -396,13 +382,12 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) attn_fwd_kernel(const __grid_c
         __syncwarp();
         if (lane == 0) mbar_arrive(&o_empty[t]);
       }
-      return true;
     };
     bool ok = true;
     for (uint32_t item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
       const FwdItem it = fwd_item(p, item);
       if (it.n <= 0) {
-        if (t < it.tiles) finish(item, false, -INFINITY, 0.f, 0);
+        if (t < it.tiles) finish(item, false, -INFINITY, 0.f);
         continue;
       }
       if (t >= it.tiles) {
@@ -414,25 +399,26 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) attn_fwd_kernel(const __grid_c
         if (!(ok = wait(&s_full[t], steps & 1u))) break;
         const int valid = it.length - (it.k0 + j) * ATT_ROWS;
         float s[64], mx[4];
-        tmem_load_64cols(t_s, s);
+        tmem_load_64cols(t_s + 64, s);
         if (valid < ATT_ROWS) {
-          hide(s, valid - half * 64);
+          hide(s, valid - 64);
           if (t == 0) {
             // what lies behind the last key must not meet its P of zero: infinities and NaN would remain
             const uint32_t n = kv + 2 * j + 1;
             if (!(ok = wait(&kv_full[n % STAGES], (n / STAGES) & 1u))) break;
             uint4* v = reinterpret_cast<uint4*>(sKV + (n % STAGES) * TILE);
-            for (int i = valid * 8 + half * 128 + row; i < ATT_ROWS * 8; i += 256)
+            for (int i = valid * 8 + row; i < ATT_ROWS * 8; i += 128)
 #pragma unroll
               for (int c = 0; c < DP / 64; ++c) v[c * (ATT_CHUNK / 16) + i] = make_uint4(0, 0, 0, 0);
             fence_proxy_async_smem();
             __syncwarp();
           }
         }
-        top4(s, mx);
-        float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), other;
-        if (!(ok = meet(top, &other))) break;
-        top = fmaxf(top, other);
+        top4(s, mx, true);
+        tmem_load_64cols(t_s, s);
+        if (valid < 64) hide(s, valid);
+        top4(s, mx, false);
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         if (j == 0) {
           m = top;
         } else {
@@ -443,7 +429,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) attn_fwd_kernel(const __grid_c
             l *= factor;
             if (!(ok = wait(&pv_done[t], (steps - 1) & 1u))) break;
 #pragma unroll
-            for (int c = 0; c < DP / 2; c += 16) {
+            for (int c = 0; c < DP; c += 16) {
               float o[16];
               tmem_load_16cols(t_o + c, o);
               uint32_t w[16];
@@ -456,15 +442,18 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) attn_fwd_kernel(const __grid_c
         const float base = m == -INFINITY ? 0.f : m * p.scale_log2;
         const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2), nb2 = f2_pack(-base, -base);
         uint64_t sum[2] = {0, 0};
+        // the first 64 keys' P goes over their S, and its product begins; then the others'
         exponentials<T>(s, sc2, nb2, sum, t_s);
+        arrive(&p_full[2 * t]);
+        tmem_load_64cols(t_s + 64, s);
+        if (valid < ATT_ROWS) hide(s, valid - 64);
+        exponentials<T>(s, sc2, nb2, sum, t_s + 64);
+        arrive(&p_full[2 * t + 1]);
         const float2 total = f2_unpack(f2_add(sum[0], sum[1]));
         l += total.x + total.y;
-        tmem_store_wait();
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[t]);
         if (j == 0 && held > 0) {
-          if (!(ok = finish(held - 1, true, held_m, held_l, held_step))) break;
+          if (!(ok = wait(&pv_done[t], (steps - 1) & 1u))) break;
+          finish(held - 1, true, held_m, held_l);
           held = 0;
         }
       }
@@ -472,15 +461,14 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) attn_fwd_kernel(const __grid_c
       held = item + 1;
       held_m = m;
       held_l = l;
-      held_step = steps - 1;
     }
-    if (ok && held > 0) finish(held - 1, true, held_m, held_l, held_step);
+    if (ok && held > 0 && wait(&pv_done[t], (steps - 1) & 1u)) finish(held - 1, true, held_m, held_l);
   }
   __syncwarp();
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  if (warp == ATT_WARPS + 1) tmem_dealloc(tmem, 512);
+  if (warp == FWD_WARPS + 1) tmem_dealloc(tmem, 512);
 }
 
 // Parts of the keys joined: lse = log2 sum 2^lse_s, o = sum 2^(lse_s - lse) o_s.
@@ -565,7 +553,7 @@ cudaError_t launch_fwd(const FwdParams& p, int num_sms, cudaStream_t stream) {
   const cudaError_t e = att_prepare(attn_fwd_kernel<T, DP>, FwdShape<DP>::SMEM, ready);
   if (e != cudaSuccess) return e;
   const unsigned grid = static_cast<unsigned>(std::min<uint32_t>(p.items, num_sms));
-  return launch_dependent(attn_fwd_kernel<T, DP>, dim3(grid), dim3(ATT_THREADS), FwdShape<DP>::SMEM, stream, p);
+  return launch_dependent(attn_fwd_kernel<T, DP>, dim3(grid), dim3(FWD_THREADS), FwdShape<DP>::SMEM, stream, p);
 }
 
 }  // namespace
