@@ -168,17 +168,43 @@ __device__ __forceinline__ void att_mma_rows(uint32_t d, const uint8_t* a, const
   }
 }
 
-// D[128 x N] (+)= A B over rows 16 FIRST .. 16 LAST of B, A 128 x 128 in
-// tensor memory, in pieces of `PIECE` elements of K (PIECE / 2 columns) that
-// start PIECE columns apart; B a tile along its rows.
+// D[128 x N] (+)= A B over rows 16 FIRST .. 16 LAST of B (no further than row
+// 16 `steps`), A 128 x 128 in tensor memory, in pieces of `PIECE` elements of K
+// (PIECE / 2 columns) that start PIECE columns apart; B a tile along its rows.
 template <int PIECE, int FIRST = 0, int LAST = ATT_ROWS / 16>
 __device__ __forceinline__ void att_mma_cols(uint32_t d, uint32_t a, const uint8_t* b, uint32_t idesc,
-                                             bool accumulate) {
+                                             bool accumulate, int steps = ATT_ROWS / 16) {
   const uint64_t db = smem_desc_sw128(smem_u32(b), ATT_CHUNK, 1024);
+  if (steps >= LAST) {
 #pragma unroll
-  for (int k = FIRST; k < LAST; ++k)
-    umma_tmem_a(d, a + k * 16 / PIECE * PIECE + k * 16 % PIECE / 2, desc_at(db, k * 2048), idesc,
-                accumulate || k > 0 ? 1u : 0u);
+    for (int k = FIRST; k < LAST; ++k)
+      umma_tmem_a(d, a + k * 16 / PIECE * PIECE + k * 16 % PIECE / 2, desc_at(db, k * 2048), idesc,
+                  accumulate || k > 0 ? 1u : 0u);
+  } else {
+#pragma unroll 1
+    for (int k = FIRST; k < steps; ++k)
+      umma_tmem_a(d, a + k * 16 / PIECE * PIECE + k * 16 % PIECE / 2, desc_at(db, k * 2048), idesc,
+                  accumulate || k > 0 ? 1u : 0u);
+  }
+}
+
+// ------------------------------------------------------------------ output
+// A warp's 32 rows x 64 elements of a result go through 4 KB of shared memory
+// (1024-byte aligned, in the swizzle of a 128-byte box) and out as one TMA
+// store: rows stored by their threads cost 32 cache lines an instruction (the
+// last 128 x 128 block of a forward item 6000 cycles that way, 700 this way).
+// Rows outside the tensor and elements behind the head are not written.
+constexpr uint32_t ATT_STAGE = 32 * 128;
+
+// Eight elements of the lane's row, the unit-th of its 128 bytes.
+__device__ __forceinline__ void att_stage_row8(uint8_t* stage, int lane, int unit, const uint4& v) {
+  *reinterpret_cast<uint4*>(stage + lane * 128 + ((unit ^ (lane & 7)) << 4)) = v;
+}
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* tm, const void* src, int x, int y, int z, int w) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(tm)),
+               "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
 }
 
 // ---------------------------------------------------------- rows and heads

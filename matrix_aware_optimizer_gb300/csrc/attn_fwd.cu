@@ -72,19 +72,17 @@ constexpr float RESCALE_ABOVE = 8.f;
 
 template <int DP>
 struct FwdShape {
-  static constexpr int STAGES = DP == 128 ? 5 : 8;  // of one key or value tile
+  static constexpr int STAGES = DP == 128 ? 4 : 8;  // of one key or value tile
   static constexpr uint32_t TILE = ATT_TILE<DP>;
   static constexpr size_t BARRIERS = 512;
-  static constexpr size_t SMEM = 1024 + (2 + STAGES) * TILE + BARRIERS;
+  static constexpr size_t SMEM = 1024 + (2 + STAGES) * TILE + FWD_WARPS * ATT_STAGE + BARRIERS;
 };
 static_assert(FwdShape<128>::SMEM <= 232448 && FwdShape<64>::SMEM <= 232448, "shared memory above 227 KB");
 
 struct FwdParams {
-  CUtensorMap q, k, v;
+  CUtensorMap q, k, v, o;  // o: a warp's rows
   AttHeads h;
   AttLengths lengths;
-  AttStrides o_strides;
-  void* o;
   float* lse;       // [batch][heads][queries], or NULL
   float* part_o;    // splits > 1: [split][batch][queries][heads][head], each part normalised
   float* part_lse;  // splits > 1: [split][batch][heads][queries]
@@ -127,26 +125,29 @@ __device__ __forceinline__ FwdItem fwd_item(const FwdParams& p, uint32_t item) {
 // Scores of the keys behind the last one.
 __device__ __forceinline__ void hide(float (&s)[64], int valid) {
 #pragma unroll
-  for (int i = 0; i < 64; ++i)
-    if (i >= valid) s[i] = -INFINITY;
+  for (int c = 0; c < 64; c += 16) {
+    if (c + 16 <= valid) continue;  // (the same in all threads)
+#pragma unroll
+    for (int i = c; i < c + 16; ++i) s[i] = i < valid ? s[i] : -INFINITY;
+  }
 }
 
-// Four maxima over s, new or joined to those that are there.
-__device__ __forceinline__ void top4(const float (&s)[64], float (&mx)[4], bool first) {
+// Four maxima, joined by those over s.
+__device__ __forceinline__ void top4(const float (&s)[64], float (&mx)[4]) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) mx[e] = first ? s[e] : fmaxf(mx[e], s[e]);
-#pragma unroll
-  for (int i = 4; i < 64; i += 4)
+  for (int i = 0; i < 64; i += 4)
 #pragma unroll
     for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[i + e]);
 }
 
-// P = 2^(s scale - base) of 64 keys into tensor memory at t_p, and its sum.
-template <typename T>
+// P = 2^(s scale - base) of 64 keys, of which `valid` are there, into tensor
+// memory at t_p, and its sum.
+template <typename T, bool ALL>
 __device__ __forceinline__ void exponentials(const float (&s)[64], uint64_t scale2, uint64_t minus_base2,
-                                             uint64_t (&sum)[2], uint32_t t_p) {
+                                             uint64_t (&sum)[2], uint32_t t_p, int valid) {
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
+    if (!ALL && 32 * c >= valid) return;  // P of keys that no product reads
     uint32_t w[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -168,7 +169,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) attn_fwd_kernel(const __grid_c
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
   uint8_t* sKV = smem + 2 * TILE;
-  uint64_t* kv_full = reinterpret_cast<uint64_t*>(sKV + STAGES * TILE);
+  uint8_t* sOut = sKV + STAGES * TILE;
+  uint64_t* kv_full = reinterpret_cast<uint64_t*>(sOut + FWD_WARPS * ATT_STAGE);
   uint64_t* kv_empty = kv_full + STAGES;
   uint64_t* q_full = kv_empty + STAGES;
   uint64_t* q_empty = q_full + 2;
@@ -213,8 +215,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) attn_fwd_kernel(const __grid_c
 
   if (warp == FWD_WARPS) {
     if (lane == 0) {
-      uint32_t kv = 0, q_used[2] = {0, 0};  // tiles loaded so far
-      uint32_t issued = 0;
+      uint32_t kv = 0;                 // key and value tiles loaded so far
+      uint32_t q_turn = 0, q_any = 0;  // bit t: phase of tile t's next load; whether there was one
       bool ok = true;
       auto load_kv = [&](const CUtensorMap* map, const FwdItem& it, int j) {
         const uint32_t stage = kv % STAGES;
@@ -229,35 +231,36 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) attn_fwd_kernel(const __grid_c
         const FwdItem it = fwd_item(p, item);
         if (it.n <= 0) continue;
         for (int t = 0; ok && t < it.tiles; ++t) {
-          ok = wait_bounded(&q_empty[t], (q_used[t] & 1u) ^ 1u, abort_flag, p.err, ATT_WAIT_NS);
+          ok = wait_bounded(&q_empty[t], ((q_turn >> t) & 1u) ^ 1u, abort_flag, p.err, ATT_WAIT_NS);
           if (!ok) break;
           mbar_arrive_expect_tx(&q_full[t], TILE);
           att_load_tile<DP>(sQ + t * TILE, &p.q, &q_full[t], it.group << p.h.pack_log2,
                             (it.block * 2 + t) * p.h.tile_tokens(), it.b);
-          ++q_used[t];
-          issued = 1;
+          q_turn ^= 1u << t;
+          q_any |= 1u << t;
         }
         for (int j = 0; ok && j < it.n; ++j) {
           load_kv(&p.k, it, j);
           load_kv(&p.v, it, j);
         }
       }
-      if (!ok && (issued || kv)) {
+      if (!ok) {
         // every load in flight lands before the CTA exits
         for (uint32_t s = 0; s < STAGES && s < kv; ++s) {
           const uint32_t last = (kv - 1 - s) / STAGES;  // round of the stage's latest load
           wait_drain(&kv_full[s], last & 1u, 50000000ull);
         }
         for (int t = 0; t < 2; ++t)
-          if (q_used[t]) wait_drain(&q_full[t], (q_used[t] - 1) & 1u, 50000000ull);
+          if (q_any >> t & 1u) wait_drain(&q_full[t], ((q_turn >> t) & 1u) ^ 1u, 50000000ull);
       }
     }
   } else if (warp == FWD_WARPS + 1) {
     constexpr bool FP16 = !std::is_same<T, __nv_bfloat16>::value;
-    const uint32_t id_s = idesc_f16kind_f32(ATT_ROWS, ATT_ROWS, false, false, FP16);
+    const uint32_t id_s = idesc_f16kind_f32(ATT_ROWS, 0, false, false, FP16);  // (N: the keys of the tile)
     const uint32_t id_o = idesc_f16kind_f32(ATT_ROWS, p.mma_n, false, true, FP16);
-    uint32_t kv = 0;                                      // key and value tiles used up
-    uint32_t q_used[2] = {0, 0}, p_used[2] = {0, 0}, o_used[2] = {0, 0};
+    uint32_t kv = 0;                             // key and value tiles used up
+    // bit t: phase of tile t's next wait. (An array indexed by t would lie in local memory, some hundred cycles away.)
+    uint32_t q_turn = 0, p_turn = 0, o_turn = 3;
     bool ok = true, issued = false;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       const bool got = wait_bounded(bar, parity, abort_flag, p.err, ATT_WAIT_NS);
@@ -266,9 +269,11 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) attn_fwd_kernel(const __grid_c
       return ok;
     };
     auto wait_kv = [&](uint32_t n) { return wait(&kv_full[n % STAGES], (n / STAGES) & 1u); };
-    auto form_s = [&](int t, uint32_t n, bool last, bool free_k) {
+    // keys: those of the tile that are there, in steps of 16
+    auto form_s = [&](int t, uint32_t n, int keys, bool last, bool free_k) {
       if (elect_one()) {
-        att_mma_rows<DP>(tmem + t * ATT_ROWS, sQ + t * TILE, sKV + (n % STAGES) * TILE, p.mma_k, id_s);
+        att_mma_rows<DP>(tmem + t * ATT_ROWS, sQ + t * TILE, sKV + (n % STAGES) * TILE, p.mma_k,
+                         id_s | static_cast<uint32_t>(keys * 2) << 17);
         umma_commit(&s_full[t]);
         if (last) umma_commit(&q_empty[t]);
         if (free_k) umma_commit(&kv_empty[n % STAGES]);
@@ -276,38 +281,64 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) attn_fwd_kernel(const __grid_c
       __syncwarp();
       issued = true;
     };
-    for (uint32_t item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
-      const FwdItem it = fwd_item(p, item);
-      const int n = uniform(it.n), tiles = uniform(it.tiles);
-      if (n <= 0) continue;
-      for (int t = 0; t < tiles; ++t) {
-        if ((t == 0 && !wait_kv(kv)) || !wait(&q_full[t], q_used[t] & 1u)) break;
-        ++q_used[t];
-        form_s(t, kv, n == 1, t + 1 == tiles);
+    // The first S of an item is formed behind the last one's last product of the same tile.
+    uint32_t item = blockIdx.x;
+    int next_n = 0, next_tiles = 0, next_left = 0;  // key tiles, query tiles, keys from the first key tile on
+    auto advance = [&] {  // to the next item with keys, if there is one
+      next_n = next_tiles = 0;
+      while (item < p.items && next_n == 0) {
+        const FwdItem it = fwd_item(p, item);
+        item += gridDim.x;
+        next_n = uniform(max(it.n, 0));
+        next_left = uniform(it.length - it.k0 * ATT_ROWS);
+        if (next_n > 0) next_tiles = uniform(it.tiles);
       }
-      for (int j = 0; ok && j < n; ++j, kv += 2) {
-        for (int t = 0; t < tiles; ++t) {
+    };
+    auto steps_of = [](int left) { return min(ATT_ROWS / 16, (left + 15) / 16); };
+    auto first_s = [&](int t, uint32_t k) {
+      if ((t > 0 || wait_kv(k)) && wait(&q_full[t], (q_turn >> t) & 1u)) {
+        q_turn ^= 1u << t;
+        form_s(t, k, steps_of(next_left), next_n == 1, t + 1 == next_tiles);
+      }
+    };
+    advance();
+    for (int t = 0; ok && t < next_tiles; ++t) first_s(t, kv);
+    while (ok && next_n > 0) {
+      const int n = next_n, tiles = next_tiles;
+      int left = next_left;
+      advance();
+      for (int j = 0; ok && j < n; ++j, kv += 2, left -= ATT_ROWS) {
+        const int steps = steps_of(left);
+        for (int t = 0; ok && t < tiles; ++t) {
           // (the first tile's waits for keys and values hold for the second)
-          if ((t == 0 && !wait_kv(kv + 1)) || (j == 0 && !wait(&o_empty[t], (o_used[t] & 1u) ^ 1u))) break;
-          if (j == 0) ++o_used[t];
+          if (t == 0 && !wait_kv(kv + 1)) break;
+          if (j == 0) {
+            if (!wait(&o_empty[t], (o_turn >> t) & 1u)) break;
+            o_turn ^= 1u << t;
+          }
           const uint32_t t_p = tmem + t * ATT_ROWS, t_o = tmem + 2 * ATT_ROWS + t * DP;
           const uint8_t* v = sKV + ((kv + 1) % STAGES) * TILE;
-          if (!wait(&p_full[2 * t], p_used[t] & 1u)) break;
-          if (elect_one()) att_mma_cols<64, 0, 4>(t_o, t_p, v, id_o, j > 0);
+          const uint32_t turn = (p_turn >> t) & 1u;
+          if (!wait(&p_full[2 * t], turn)) break;
+          if (elect_one()) att_mma_cols<64, 0, 4>(t_o, t_p, v, id_o, j > 0, steps);
           __syncwarp();
-          if (!wait(&p_full[2 * t + 1], p_used[t] & 1u)) break;
+          if (!wait(&p_full[2 * t + 1], turn)) break;
+          p_turn ^= 1u << t;
           if (elect_one()) {
-            att_mma_cols<64, 4, 8>(t_o, t_p, v, id_o, true);
+            if (steps > 4) att_mma_cols<64, 4, 8>(t_o, t_p, v, id_o, true, steps);
             umma_commit(&pv_done[t]);
             if (t + 1 == tiles) umma_commit(&kv_empty[(kv + 1) % STAGES]);
           }
           __syncwarp();
-          ++p_used[t];
           if (j + 1 < n) {
             if (t == 0 && !wait_kv(kv + 2)) break;
-            form_s(t, kv + 2, j + 2 == n, t + 1 == tiles);
+            form_s(t, kv + 2, steps_of(left - ATT_ROWS), j + 2 == n, t + 1 == tiles);
+          } else if (t < next_tiles) {
+            first_s(t, kv + 2);
           }
         }
+        if (j + 1 == n)
+          for (int t = tiles; ok && t < next_tiles; ++t) first_s(t, kv + 2);
       }
     }
     if (!ok && issued) {
@@ -334,135 +365,175 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) attn_fwd_kernel(const __grid_c
       if (lane == 0) mbar_arrive(bar);
     };
     // The last item's rows are written behind the next one's first exponentials, so that its last product has
-    // ended by then.
+    // ended by then; its O is read first, so that the next product may begin.
+    // (A single place writes rows, also those of items without keys and, in a last round without an item, the last
+    // one's: a second copy of that code costs registers that spill where there is hardly any L1.)
     uint32_t held = 0;  // its number + 1
     float held_m = 0.f, held_l = 0.f;
-    auto finish = [&](uint32_t item, bool some, float m, float l) {
-      const FwdItem it = fwd_item(p, item);
-      const int token = (it.block * 2 + t) * p.h.tile_tokens() + (row >> p.h.pack_log2);
-      const int head = (it.group << p.h.pack_log2) + (row & ((1 << p.h.pack_log2) - 1));
-      const bool live = token < p.h.queries;
-      const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-      const int64_t at_lse = (static_cast<int64_t>(it.b) * p.h.heads + head) * p.h.queries + token;
-      if (live) {
-        const float lse = some ? m * p.scale_log2 + log2f(l) : -INFINITY;
-        if (p.splits > 1)
-          p.part_lse[static_cast<int64_t>(it.split) * p.h.batch * p.h.heads * p.h.queries + at_lse] = lse;
-        else if (p.lse != nullptr)
-          p.lse[at_lse] = lse;
-      }
-      T* out = static_cast<T*>(p.o) + it.b * p.o_strides.batch + token * p.o_strides.token + head * p.o_strides.head;
-      float* part = p.part_o + (((static_cast<int64_t>(it.split) * p.h.batch + it.b) * p.h.queries + token) *
-                                    p.h.heads + head) * p.h.head;
-#pragma unroll
-      for (int c = 0; c < DP; c += 32) {
-        if (c >= p.h.head) break;
-        float o[32];
-        __syncwarp();
-        if (some) tmem_load_32cols(t_o + c, o);
-#pragma unroll
-        for (int i = 0; i < 32; i += 8) {
-          if (c + i >= p.h.head || !live) break;
-          float v[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = some ? o[i + e] * inv : 0.f;
-          if (p.splits > 1) {
-            Raw8<float> r;
-            r.set(v);
-            r.store(part + c + i);
-          } else {
-            Raw8<T> r;
-            r.set(v);
-            r.store(out + c + i);
-          }
+    bool ok = true;
+    for (uint32_t item = blockIdx.x; ok; item += gridDim.x) {
+      const bool end = item >= p.items;
+      int n = 0, valid = 0;
+      bool mine = false;  // the item has rows of this tile
+      if (!end) {
+        const FwdItem it = fwd_item(p, item);
+        mine = t < it.tiles;
+        n = max(it.n, 0);
+        valid = it.length - it.k0 * ATT_ROWS;
+        if (!mine) {
+          kv += 2 * n;
+          continue;
         }
       }
-      if (some) {
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&o_empty[t]);
-      }
-    };
-    bool ok = true;
-    for (uint32_t item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
-      const FwdItem it = fwd_item(p, item);
-      if (it.n <= 0) {
-        if (t < it.tiles) finish(item, false, -INFINITY, 0.f);
-        continue;
-      }
-      if (t >= it.tiles) {
-        kv += 2 * it.n;
-        continue;
-      }
       float m = -INFINITY, l = 0.f;
-      for (int j = 0; j < it.n; ++j, ++steps) {
-        if (!(ok = wait(&s_full[t], steps & 1u))) break;
-        const int valid = it.length - (it.k0 + j) * ATT_ROWS;
-        float s[64], mx[4];
-        tmem_load_64cols(t_s + 64, s);
-        if (valid < ATT_ROWS) {
-          hide(s, valid - 64);
-          if (t == 0) {
+      int j = 0;
+      do {
+        if (n > 0) {
+          if (!(ok = wait(&s_full[t], steps & 1u))) break;
+          const bool whole = valid >= ATT_ROWS;  // (the same in all threads; most tiles are)
+          float s[64], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          if (whole || valid > 64) {
+            tmem_load_64cols(t_s + 64, s);
+            if (!whole) hide(s, valid - 64);
+            top4(s, mx);
+          }
+          if (!whole && t == 0) {
             // what lies behind the last key must not meet its P of zero: infinities and NaN would remain
-            const uint32_t n = kv + 2 * j + 1;
-            if (!(ok = wait(&kv_full[n % STAGES], (n / STAGES) & 1u))) break;
-            uint4* v = reinterpret_cast<uint4*>(sKV + (n % STAGES) * TILE);
-            for (int i = valid * 8 + row; i < ATT_ROWS * 8; i += 128)
+            const uint32_t at = kv + 1;
+            if (!(ok = wait(&kv_full[at % STAGES], (at / STAGES) & 1u))) break;
+            uint4* v = reinterpret_cast<uint4*>(sKV + (at % STAGES) * TILE);
+            for (int i = valid * 8 + row; i < (valid + 15) / 16 * 128; i += 128)
 #pragma unroll
               for (int c = 0; c < DP / 64; ++c) v[c * (ATT_CHUNK / 16) + i] = make_uint4(0, 0, 0, 0);
             fence_proxy_async_smem();
             __syncwarp();
           }
-        }
-        top4(s, mx, true);
-        tmem_load_64cols(t_s, s);
-        if (valid < 64) hide(s, valid);
-        top4(s, mx, false);
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        if (j == 0) {
-          m = top;
-        } else {
-          const bool grows = (top - m) * p.scale_log2 > RESCALE_ABOVE;  // (from -inf: always)
-          if (__any_sync(0xffffffffu, grows)) {
-            const float factor = grows ? exp2_fast((m - top) * p.scale_log2) : 1.f;
-            if (grows) m = top;
-            l *= factor;
-            if (!(ok = wait(&pv_done[t], (steps - 1) & 1u))) break;
+          tmem_load_64cols(t_s, s);
+          if (!whole) hide(s, valid);
+          top4(s, mx);
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          if (j == 0) {
+            m = top;
+          } else {
+            const bool grows = (top - m) * p.scale_log2 > RESCALE_ABOVE;  // (from -inf: always)
+            if (__any_sync(0xffffffffu, grows)) {
+              const float factor = grows ? exp2_fast((m - top) * p.scale_log2) : 1.f;
+              if (grows) m = top;
+              l *= factor;
+              if (!(ok = wait(&pv_done[t], (steps - 1) & 1u))) break;
+#pragma unroll 1
+              for (int c = 0; c < p.mma_n; c += 16) {
+                float o[16];
+                tmem_load_16cols(t_o + c, o);
+                uint32_t w[16];
 #pragma unroll
-            for (int c = 0; c < DP; c += 16) {
-              float o[16];
-              tmem_load_16cols(t_o + c, o);
-              uint32_t w[16];
-#pragma unroll
-              for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i] * factor);
-              tmem_store_16cols(t_o + c, w);
+                for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i] * factor);
+                tmem_store_16cols(t_o + c, w);
+              }
+              tmem_load_64cols(t_s, s);  // (not held meanwhile)
+              if (!whole) hide(s, valid);
             }
           }
+          const float base = m == -INFINITY ? 0.f : m * p.scale_log2;
+          const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2), nb2 = f2_pack(-base, -base);
+          uint64_t sum[2] = {0, 0};
+          // the first 64 keys' P goes over their S, and its product begins; then the others'
+          if (whole) {
+            exponentials<T, true>(s, sc2, nb2, sum, t_s, 64);
+            arrive(&p_full[2 * t]);
+            tmem_load_64cols(t_s + 64, s);
+            exponentials<T, true>(s, sc2, nb2, sum, t_s + 64, 64);
+          } else {
+            exponentials<T, false>(s, sc2, nb2, sum, t_s, valid);
+            arrive(&p_full[2 * t]);
+            if (valid > 64) {
+              tmem_load_64cols(t_s + 64, s);
+              hide(s, valid - 64);
+              exponentials<T, false>(s, sc2, nb2, sum, t_s + 64, valid - 64);
+            }
+          }
+          arrive(&p_full[2 * t + 1]);
+          const float2 total = f2_unpack(f2_add(sum[0], sum[1]));
+          l += total.x + total.y;
+          kv += 2;
+          valid -= ATT_ROWS;
+          ++steps;
         }
-        const float base = m == -INFINITY ? 0.f : m * p.scale_log2;
-        const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2), nb2 = f2_pack(-base, -base);
-        uint64_t sum[2] = {0, 0};
-        // the first 64 keys' P goes over their S, and its product begins; then the others'
-        exponentials<T>(s, sc2, nb2, sum, t_s);
-        arrive(&p_full[2 * t]);
-        tmem_load_64cols(t_s + 64, s);
-        if (valid < ATT_ROWS) hide(s, valid - 64);
-        exponentials<T>(s, sc2, nb2, sum, t_s + 64);
-        arrive(&p_full[2 * t + 1]);
-        const float2 total = f2_unpack(f2_add(sum[0], sum[1]));
-        l += total.x + total.y;
         if (j == 0 && held > 0) {
-          if (!(ok = wait(&pv_done[t], (steps - 1) & 1u))) break;
-          finish(held - 1, true, held_m, held_l);
+          const FwdItem it = fwd_item(p, held - 1);
+          const bool some = it.n > 0;
+          // (with keys in this item its first step was counted already)
+          if (some && !(ok = wait(&pv_done[t], (steps - (n > 0 ? 2 : 1)) & 1u))) break;
+          const int token = (it.block * 2 + t) * p.h.tile_tokens() + (row >> p.h.pack_log2);
+          const int head = (it.group << p.h.pack_log2) + (row & ((1 << p.h.pack_log2) - 1));
+          const bool live = token < p.h.queries;
+          const float inv = held_l > 0.f || held_l != held_l ? 1.f / held_l : 0.f;
+          if (live) {
+            const int64_t at = (static_cast<int64_t>(it.b) * p.h.heads + head) * p.h.queries + token;
+            const float lse = some ? held_m * p.scale_log2 + log2f(held_l) : -INFINITY;
+            if (p.splits > 1)
+              p.part_lse[static_cast<int64_t>(it.split) * p.h.batch * p.h.heads * p.h.queries + at] = lse;
+            else if (p.lse != nullptr)
+              p.lse[at] = lse;
+          }
+          float* part = p.part_o + (((static_cast<int64_t>(it.split) * p.h.batch + it.b) * p.h.queries + token) *
+                                        p.h.heads + head) * p.h.head;
+          uint8_t* stage = sOut + warp * ATT_STAGE;
+          const int first = token - (lane >> p.h.pack_log2);  // the warp's first token
+#pragma unroll 1
+          for (int c = 0; c < p.h.head; c += 64) {
+            uint4 u[8];
+#pragma unroll
+            for (int q = 0; q < 64; q += 16) {
+              if (c + q >= p.h.head) break;
+              float o[16];
+              __syncwarp();
+              if (some) tmem_load_16cols(t_o + c + q, o);
+#pragma unroll
+              for (int i = 0; i < 16; i += 8) {
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = some ? o[i + e] * inv : 0.f;
+                if (p.splits > 1) {
+                  Raw8<float> r;
+                  r.set(v);
+                  if (live && c + q + i < p.h.head) r.store(part + c + q + i);
+                } else {
+                  Raw8<T> r;
+                  r.set(v);
+                  u[(q + i) / 8] = r.a;
+                }
+              }
+            }
+            if (some && c + 64 >= p.h.head) {  // O has been read
+              tc_fence_before_sync();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&o_empty[t]);
+            }
+            if (p.splits > 1) continue;
+            if (lane == 0) bulk_wait_group_read<0>();
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              if (c + 8 * i >= p.h.head) break;
+              att_stage_row8(stage, lane, i, u[i]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && first < p.h.queries) {
+              tma_store_4d(&p.o, stage, c, it.group << p.h.pack_log2, first, it.b);
+              bulk_commit_group();
+            }
+          }
           held = 0;
         }
-      }
-      kv += 2 * it.n;
+      } while (++j < n);
+      if (end || !ok) break;
       held = item + 1;
       held_m = m;
       held_l = l;
     }
-    if (ok && held > 0 && wait(&pv_done[t], (steps - 1) & 1u)) finish(held - 1, true, held_m, held_l);
+    if (lane == 0) bulk_wait_group_all();
   }
   __syncwarp();
   tc_fence_before_sync();
@@ -563,8 +634,6 @@ cudaError_t attn_forward(const AttCall& c, const void* q, const void* k, const v
   FwdParams p{};
   p.h = c.h;
   p.lengths = c.lengths;
-  p.o_strides = c.o;
-  p.o = o;
   p.lse = lse;
   p.blocks = (c.h.query_tiles() + 1) / 2;
   const AttSplit sp = att_forward_split(c.h, c.num_sms);
@@ -582,6 +651,7 @@ cudaError_t attn_forward(const AttCall& c, const void* q, const void* k, const v
   }
   const int pack = 1 << c.h.pack_log2;
   if (!att_encode(&p.q, q, c.dtype, c.h.batch, c.h.queries, c.h.heads, c.h.head, c.q, pack, ATT_ROWS / pack) ||
+      !att_encode(&p.o, o, c.dtype, c.h.batch, c.h.queries, c.h.heads, c.h.head, c.o, pack, 32 / pack) ||
       !att_encode(&p.k, k, c.dtype, c.h.batch, c.h.keys, c.h.kv_heads, c.h.head, c.k, 1, ATT_ROWS) ||
       !att_encode(&p.v, v, c.dtype, c.h.batch, c.h.keys, c.h.kv_heads, c.h.head, c.v, 1, ATT_ROWS))
     return cudaErrorInvalidValue;
