@@ -19,9 +19,9 @@
 // P is rounded to 16 bits because it is an operand of the next product; the
 // row's sum adds the unrounded values, in fp32.
 //
-// All products of a CTA are issued by one thread and run through its tensor
-// pipe in that order: S of the next key tile overwrites P only behind the
-// product that reads it.
+// All products of a query tile are issued by one thread and run through the
+// tensor pipe in that order: S of the next key tile overwrites P only behind
+// the product that reads it.
 #include <algorithm>
 #include <mutex>
 #include <type_traits>
@@ -65,9 +65,12 @@ bool att_encode(CUtensorMap* map, const void* base, int dtype, int64_t batch, in
 
 namespace {
 
-// Warps 0 .. 3 and 4 .. 7 take the two tiles' rows, 8 loads, 9 issues products.
+// Warps 0 .. 3 and 4 .. 7 take the two tiles' rows, 8 loads, 9 and 10 issue the
+// two tiles' products: a wait that is already over costs 100 cycles, in which
+// the other warp's products run (with one warp for both tiles a key tile took
+// 3700 cycles at 8192 x 8192, the tensor cores at work 2400 of them).
 constexpr int FWD_WARPS = 8;
-constexpr int FWD_THREADS = 32 * (FWD_WARPS + 2);
+constexpr int FWD_THREADS = 32 * (FWD_WARPS + 3);
 constexpr float RESCALE_ABOVE = 8.f;
 
 template <int DP>
@@ -179,7 +182,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) attn_fwd_kernel(const __grid_c
   uint64_t* pv_done = p_full + 4;
   uint64_t* o_empty = pv_done + 2;
   uint64_t* drain_bar = o_empty + 2;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain_bar + 1);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain_bar + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
   const int warp = uniform(threadIdx.x / 32);
@@ -187,7 +190,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) attn_fwd_kernel(const __grid_c
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&kv_full[s], 1);
-      mbar_init(&kv_empty[s], 1);
+      mbar_init(&kv_empty[s], 2);  // both tiles are done with it
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&q_full[t], 1);
@@ -198,7 +201,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) attn_fwd_kernel(const __grid_c
       mbar_init(&pv_done[t], 1);
       mbar_init(&o_empty[t], FWD_WARPS / 2);
     }
-    mbar_init(drain_bar, 1);
+    mbar_init(&drain_bar[0], 1);
+    mbar_init(&drain_bar[1], 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -254,13 +258,15 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) attn_fwd_kernel(const __grid_c
           if (q_any >> t & 1u) wait_drain(&q_full[t], ((q_turn >> t) & 1u) ^ 1u, 50000000ull);
       }
     }
-  } else if (warp == FWD_WARPS + 1) {
+  } else if (warp > FWD_WARPS) {
     constexpr bool FP16 = !std::is_same<T, __nv_bfloat16>::value;
     const uint32_t id_s = idesc_f16kind_f32(ATT_ROWS, 0, false, false, FP16);  // (N: the keys of the tile)
     const uint32_t id_o = idesc_f16kind_f32(ATT_ROWS, p.mma_n, false, true, FP16);
-    uint32_t kv = 0;                             // key and value tiles used up
-    // bit t: phase of tile t's next wait. (An array indexed by t would lie in local memory, some hundred cycles away.)
-    uint32_t q_turn = 0, p_turn = 0, o_turn = 3;
+    const int t = warp - (FWD_WARPS + 1);  // this warp's query tile
+    const uint32_t t_s = tmem + t * ATT_ROWS, t_o = tmem + 2 * ATT_ROWS + t * DP;
+    const uint8_t* q = sQ + t * TILE;
+    uint32_t kv = 0;                                // key and value tiles used up
+    uint32_t q_turn = 0, p_turn = 0, o_turn = 1;    // phases of the next waits
     bool ok = true, issued = false;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       const bool got = wait_bounded(bar, parity, abort_flag, p.err, ATT_WAIT_NS);
@@ -270,80 +276,77 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) attn_fwd_kernel(const __grid_c
     };
     auto wait_kv = [&](uint32_t n) { return wait(&kv_full[n % STAGES], (n / STAGES) & 1u); };
     // keys: those of the tile that are there, in steps of 16
-    auto form_s = [&](int t, uint32_t n, int keys, bool last, bool free_k) {
+    auto form_s = [&](uint32_t n, int keys, bool last) {
+      if (!wait_kv(n)) return;
       if (elect_one()) {
-        att_mma_rows<DP>(tmem + t * ATT_ROWS, sQ + t * TILE, sKV + (n % STAGES) * TILE, p.mma_k,
-                         id_s | static_cast<uint32_t>(keys * 2) << 17);
+        att_mma_rows<DP>(t_s, q, sKV + (n % STAGES) * TILE, p.mma_k, id_s | static_cast<uint32_t>(keys * 2) << 17);
         umma_commit(&s_full[t]);
+        umma_commit(&kv_empty[n % STAGES]);
         if (last) umma_commit(&q_empty[t]);
-        if (free_k) umma_commit(&kv_empty[n % STAGES]);
       }
       __syncwarp();
       issued = true;
     };
-    // The first S of an item is formed behind the last one's last product of the same tile.
+    // An item without rows of this tile: its keys and values are free as soon as they are there.
+    auto pass = [&](int n) {
+      for (int j = 0; ok && j < 2 * n; ++j, ++kv) {
+        if (!wait_kv(kv)) return;
+        if (elect_one()) mbar_arrive(&kv_empty[kv % STAGES]);
+        __syncwarp();
+      }
+    };
+    // The first S of an item is formed behind the last one's last product; items without rows of this tile that lie
+    // between are passed first.
     uint32_t item = blockIdx.x;
-    int next_n = 0, next_tiles = 0, next_left = 0;  // key tiles, query tiles, keys from the first key tile on
-    auto advance = [&] {  // to the next item with keys, if there is one
-      next_n = next_tiles = 0;
-      while (item < p.items && next_n == 0) {
+    int next_n = 0, next_left = 0;  // key tiles, keys from the first key tile on
+    auto first_s = [&] {
+      next_n = 0;
+      while (ok && item < p.items && next_n == 0) {
         const FwdItem it = fwd_item(p, item);
         item += gridDim.x;
-        next_n = uniform(max(it.n, 0));
-        next_left = uniform(it.length - it.k0 * ATT_ROWS);
-        if (next_n > 0) next_tiles = uniform(it.tiles);
-      }
-    };
-    auto steps_of = [](int left) { return min(ATT_ROWS / 16, (left + 15) / 16); };
-    auto first_s = [&](int t, uint32_t k) {
-      if ((t > 0 || wait_kv(k)) && wait(&q_full[t], (q_turn >> t) & 1u)) {
-        q_turn ^= 1u << t;
-        form_s(t, k, steps_of(next_left), next_n == 1, t + 1 == next_tiles);
-      }
-    };
-    advance();
-    for (int t = 0; ok && t < next_tiles; ++t) first_s(t, kv);
-    while (ok && next_n > 0) {
-      const int n = next_n, tiles = next_tiles;
-      int left = next_left;
-      advance();
-      for (int j = 0; ok && j < n; ++j, kv += 2, left -= ATT_ROWS) {
-        const int steps = steps_of(left);
-        for (int t = 0; ok && t < tiles; ++t) {
-          // (the first tile's waits for keys and values hold for the second)
-          if (t == 0 && !wait_kv(kv + 1)) break;
-          if (j == 0) {
-            if (!wait(&o_empty[t], (o_turn >> t) & 1u)) break;
-            o_turn ^= 1u << t;
-          }
-          const uint32_t t_p = tmem + t * ATT_ROWS, t_o = tmem + 2 * ATT_ROWS + t * DP;
-          const uint8_t* v = sKV + ((kv + 1) % STAGES) * TILE;
-          const uint32_t turn = (p_turn >> t) & 1u;
-          if (!wait(&p_full[2 * t], turn)) break;
-          if (elect_one()) att_mma_cols<64, 0, 4>(t_o, t_p, v, id_o, j > 0, steps);
-          __syncwarp();
-          if (!wait(&p_full[2 * t + 1], turn)) break;
-          p_turn ^= 1u << t;
-          if (elect_one()) {
-            if (steps > 4) att_mma_cols<64, 4, 8>(t_o, t_p, v, id_o, true, steps);
-            umma_commit(&pv_done[t]);
-            if (t + 1 == tiles) umma_commit(&kv_empty[(kv + 1) % STAGES]);
-          }
-          __syncwarp();
-          if (j + 1 < n) {
-            if (t == 0 && !wait_kv(kv + 2)) break;
-            form_s(t, kv + 2, steps_of(left - ATT_ROWS), j + 2 == n, t + 1 == tiles);
-          } else if (t < next_tiles) {
-            first_s(t, kv + 2);
-          }
+        const int n = uniform(max(it.n, 0));
+        if (n > 0 && t >= uniform(it.tiles)) {
+          pass(n);
+        } else {
+          next_n = n;
+          next_left = uniform(it.length - it.k0 * ATT_ROWS);
         }
-        if (j + 1 == n)
-          for (int t = tiles; ok && t < next_tiles; ++t) first_s(t, kv + 2);
+      }
+      if (next_n > 0 && ok && wait(&q_full[t], q_turn)) {
+        q_turn ^= 1u;
+        form_s(kv, min(ATT_ROWS / 16, (next_left + 15) / 16), next_n == 1);
+      }
+    };
+    first_s();
+    while (ok && next_n > 0) {
+      const int n = next_n;
+      int left = next_left;
+      for (int j = 0; ok && j < n; ++j, left -= ATT_ROWS) {
+        const int steps = min(ATT_ROWS / 16, (left + 15) / 16);
+        if (!wait_kv(kv + 1) || (j == 0 && !wait(&o_empty[t], o_turn)) || !wait(&p_full[2 * t], p_turn)) break;
+        if (j == 0) o_turn ^= 1u;
+        const uint32_t stage = (kv + 1) % STAGES;
+        const uint8_t* v = sKV + stage * TILE;
+        if (elect_one()) att_mma_cols<64, 0, 4>(t_o, t_s, v, id_o, j > 0, steps);
+        __syncwarp();
+        if (!wait(&p_full[2 * t + 1], p_turn)) break;
+        p_turn ^= 1u;
+        if (elect_one()) {
+          if (steps > 4) att_mma_cols<64, 4, 8>(t_o, t_s, v, id_o, true, steps);
+          umma_commit(&pv_done[t]);
+          umma_commit(&kv_empty[stage]);
+        }
+        __syncwarp();
+        kv += 2;
+        if (j + 1 < n)
+          form_s(kv, min(ATT_ROWS / 16, (left - ATT_ROWS + 15) / 16), j + 2 == n);
+        else
+          first_s();
       }
     }
     if (!ok && issued) {
-      if (elect_one()) umma_commit(drain_bar);
-      wait_drain(drain_bar, 0, 50000000ull);
+      if (elect_one()) umma_commit(&drain_bar[t]);
+      wait_drain(&drain_bar[t], 0, 50000000ull);
     }
   } else {
     const int t = warp >> 2;
@@ -397,8 +400,9 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) attn_fwd_kernel(const __grid_c
             if (!whole) hide(s, valid - 64);
             top4(s, mx);
           }
-          if (!whole && t == 0) {
-            // what lies behind the last key must not meet its P of zero: infinities and NaN would remain
+          if (!whole) {
+            // what lies behind the last key must not meet its P of zero: infinities and NaN would remain. (Both
+            // tiles' threads write the same zeros, each before its own product.)
             const uint32_t at = kv + 1;
             if (!(ok = wait(&kv_full[at % STAGES], (at / STAGES) & 1u))) break;
             uint4* v = reinterpret_cast<uint4*>(sKV + (at % STAGES) * TILE);
