@@ -54,6 +54,12 @@ __device__ __forceinline__ void tmem_load_64cols(uint32_t taddr, float (&v)[64])
 }
 
 // 32 lanes x n words, the other way; tmem_store_wait() before they are read.
+__device__ __forceinline__ void tmem_store_8cols(uint32_t taddr, const uint32_t (&w)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+      "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+      : "memory");
+}
 __device__ __forceinline__ void tmem_store_16cols(uint32_t taddr, const uint32_t (&w)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {"
@@ -63,19 +69,6 @@ __device__ __forceinline__ void tmem_store_16cols(uint32_t taddr, const uint32_t
         "r"(w[9]), "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15])
       : "memory");
 }
-__device__ __forceinline__ void tmem_store_32cols(uint32_t taddr, const uint32_t (&w)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {"
-      "%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, "
-      "%20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32"
-      "};" ::"r"(taddr),
-      "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"(w[8]),
-        "r"(w[9]), "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15]), "r"(w[16]),
-        "r"(w[17]), "r"(w[18]), "r"(w[19]), "r"(w[20]), "r"(w[21]), "r"(w[22]), "r"(w[23]), "r"(w[24]),
-        "r"(w[25]), "r"(w[26]), "r"(w[27]), "r"(w[28]), "r"(w[29]), "r"(w[30]), "r"(w[31])
-      : "memory");
-}
-
 __device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // D[tmem] (+)= A[tmem] * B[smem]: row i of A in lane i, two 16-bit elements
@@ -252,9 +245,10 @@ cudaError_t att_prepare(void (*kernel)(Args...), size_t smem, std::atomic<uint64
   return e;
 }
 
-// Map over [batch][row][head][element]; box: 64 elements x box_heads x box_rows.
+// Map over [batch][row][head][element]; box: 64 or 32 elements (in the swizzle
+// of as many bytes) x box_heads x box_rows.
 bool att_encode(CUtensorMap* map, const void* base, int dtype, int64_t batch, int64_t rows, int64_t heads,
-                int64_t head, const AttStrides& s, int box_heads, int box_rows);
+                int64_t head, const AttStrides& s, int box_heads, int box_rows, int box_elements = 64);
 
 // One call's sizes and layouts, checked.
 struct AttCall {

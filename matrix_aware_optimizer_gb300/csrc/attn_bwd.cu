@@ -31,13 +31,15 @@
 namespace prm {
 namespace {
 
-// Warps 0 .. 15 take elements, 16 loads, 17 issues products.
+// Warps 0 .. 15 take elements, 16 loads, 17 and 18 issue products.
 constexpr int BWD_WARPS = 16;
-constexpr int BWD_THREADS = 32 * (BWD_WARPS + 2);
+constexpr int BWD_THREADS = 32 * (BWD_WARPS + 3);
 constexpr int ROW_VALUES = 256;  // of a query tile: 128 times -lse, 128 times -delta
 constexpr size_t BWD_BARRIERS = 512;
 
 // ------------------------------------------------------------- -lse, -delta
+// A block takes a query tile: eight threads to a row, which they read 16 bytes
+// at a time, four rows each.
 struct RowsParams {
   AttHeads h;
   AttStrides o, grad_o;
@@ -45,62 +47,81 @@ struct RowsParams {
   const void* gp;
   const float* lse;
   float* rows;  // [batch][group][query tile][ROW_VALUES]
-  int64_t count;
 };
 
-template <typename T>
+template <typename T, int DP>
 __global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ RowsParams p) {
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / 16;  // row, in the tiles' order
-  const int part = threadIdx.x % 16;
-  if (i >= p.count) return;  // (count is a multiple of 128: a warp's rows leave together)
-  const int r = static_cast<int>(i % ATT_ROWS);
-  int64_t tile = i / ATT_ROWS;
-  const int tiles = p.h.query_tiles();
-  const int token = static_cast<int>(tile % tiles) * p.h.tile_tokens() + (r >> p.h.pack_log2);
-  const int64_t bg = tile / tiles;
-  const int b = static_cast<int>(bg / p.h.groups);
-  const int head = (static_cast<int>(bg % p.h.groups) << p.h.pack_log2) + (r & ((1 << p.h.pack_log2) - 1));
-  float lse = INFINITY, delta = 0.f;
-  if (token < p.h.queries) {
-    lse = p.lse[(static_cast<int64_t>(b) * p.h.heads + head) * p.h.queries + token];
-    if (lse == -INFINITY) lse = INFINITY;  // a row without keys: P is zero
-    if (part * 8 < p.h.head) {
-      Raw8<T> a, g;
-      a.load(static_cast<const T*>(p.op) + b * p.o.batch + token * p.o.token + head * p.o.head + part * 8);
-      g.load(static_cast<const T*>(p.gp) + b * p.grad_o.batch + token * p.grad_o.token + head * p.grad_o.head +
-             part * 8);
-      float u[8], v[8];
-      a.get(u);
-      g.get(v);
+  constexpr int VECTORS = DP / 64, ROWS = 4;
+  const uint32_t tiles = p.h.query_tiles(), groups = p.h.groups;
+  const uint32_t bg = blockIdx.x / tiles, tile = blockIdx.x - bg * tiles;
+  const int b = static_cast<int>(bg / groups), group = static_cast<int>(bg - b * groups);
+  const int part = threadIdx.x & 7, r0 = threadIdx.x >> 3;
+  const int first = static_cast<int>(tile) * p.h.tile_tokens(), pack = 1 << p.h.pack_log2;
+  const T* o = static_cast<const T*>(p.op) + b * p.o.batch + part * 8;
+  const T* g = static_cast<const T*>(p.gp) + b * p.grad_o.batch + part * 8;
+  Raw8<T> ov[ROWS][VECTORS], gv[ROWS][VECTORS];
+  float lse[ROWS];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) delta = fmaf(u[e], v[e], delta);
+  for (int k = 0; k < ROWS; ++k) {
+    const int r = r0 + 32 * k;
+    const int token = first + (r >> p.h.pack_log2), head = group * pack + (r & (pack - 1));
+    const bool live = token < p.h.queries;
+    lse[k] = -INFINITY;
+    if (live && part == 0) lse[k] = p.lse[(static_cast<int64_t>(b) * p.h.heads + head) * p.h.queries + token];
+#pragma unroll
+    for (int v = 0; v < VECTORS; ++v) {
+      ov[k][v].zero();
+      gv[k][v].zero();
+      if (live && (v * 8 + part) * 8 < p.h.head) {
+        ov[k][v].load(o + token * p.o.token + head * p.o.head + v * 64);
+        gv[k][v].load(g + token * p.grad_o.token + head * p.grad_o.head + v * 64);
+      }
     }
   }
-  __syncwarp();
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) delta += __shfl_xor_sync(0xffffffffu, delta, o);
-  if (part == 0) {
-    float* out = p.rows + tile * ROW_VALUES + r;
-    out[0] = -lse;
-    out[ATT_ROWS] = -delta;
+  for (int k = 0; k < ROWS; ++k) {
+    float delta = 0.f;
+#pragma unroll
+    for (int v = 0; v < VECTORS; ++v) {
+      float a[8], c[8];
+      ov[k][v].get(a);
+      gv[k][v].get(c);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) delta = fmaf(a[e], c[e], delta);
+    }
+#pragma unroll
+    for (int i = 4; i > 0; i >>= 1) delta += __shfl_xor_sync(0xffffffffu, delta, i);
+    if (part == 0) {
+      float* out = p.rows + static_cast<int64_t>(blockIdx.x) * ROW_VALUES + r0 + 32 * k;
+      out[0] = lse[k] == -INFINITY ? -INFINITY : -lse[k];  // a row without keys: P is zero
+      out[ATT_ROWS] = -delta;
+    }
   }
 }
 
-// -------------------------------------------------------------- dK and dV
-template <int DP>
+// -------------------------------------------------------- dK and dV (and dQ)
+// DQ: there is one key tile per sequence, so its pass over the queries can form
+// dQ = dS K as well (five products instead of seven, exponentials taken once,
+// Q and dO read once): dS^T then goes to shared memory, where it is the left
+// operand of dK as it lies and that of dQ along its columns.
+template <int DP, bool DQ>
 struct DkvShape {
   static constexpr uint32_t TILE = ATT_TILE<DP>;
-  static constexpr int SLOTS = DP == 128 ? 4 : 8;  // tiles of Q and dO under way
-  static constexpr int ROW_SLOTS = 4;              // -lse and -delta: never more than four query tiles under way
-  static constexpr size_t SMEM =
-      1024 + (2 + SLOTS) * TILE + ROW_SLOTS * ROW_VALUES * sizeof(float) + (BWD_BARRIERS - 256);
+  static constexpr int SLOTS = DP == 128 ? 4 : 8;  // tiles of dO and Q under way
+  static constexpr int ROW_SLOTS = SLOTS / 2;      // -lse and -delta of as many query tiles
+  static constexpr uint32_t DS = DQ ? 2 * ATT_CHUNK : 0;
+  static constexpr size_t USED = (2 + SLOTS) * TILE + DS + ROW_SLOTS * ROW_VALUES * sizeof(float) + 256;
+  // up to 1024 bytes go to the alignment of the tiles; a kernel that has fewer checks what it got
+  static constexpr size_t SMEM = USED + 1024 <= 232448 ? USED + 1024 : 232448;
 };
-static_assert(DkvShape<128>::SMEM <= 232448 && DkvShape<64>::SMEM <= 232448, "shared memory above 227 KB");
 
 struct DkvParams {
   CUtensorMap q, grad_o, k, v;
+  CUtensorMap dq;  // DQ: a warp's 32 columns of 32 rows
+  void* dq_out;
+  AttStrides dq_strides;
   AttHeads h;
   AttLengths lengths;
   AttStrides dk_strides, dv_strides;
@@ -127,15 +148,22 @@ struct DkvItem {
 __device__ __forceinline__ DkvItem dkv_item(const DkvParams& p, uint32_t item) {
   DkvItem it;
   const uint32_t splits = p.splits, key_tiles = p.key_tiles, kv_heads = p.h.kv_heads;
-  it.split = static_cast<int>(item % splits);
-  item /= splits;
-  it.tile = static_cast<int>(item % key_tiles);
-  item /= key_tiles;
+  it.split = 0;
+  if (splits > 1) {
+    it.split = static_cast<int>(item % splits);
+    item /= splits;
+  }
+  it.tile = 0;
+  if (key_tiles > 1) {
+    it.tile = static_cast<int>(item % key_tiles);
+    item /= key_tiles;
+  }
   it.kv_head = static_cast<int>(item % kv_heads);
   it.b = static_cast<int>(item / kv_heads);
   it.length = att_length(p.lengths, it.b, p.h.keys);
   it.x0 = min(it.split * p.split_rounds, p.rounds);
-  it.n = it.tile * ATT_ROWS < it.length ? min(p.split_rounds, p.rounds - it.x0) : 0;
+  it.n = min(p.split_rounds, p.rounds - it.x0);
+  if (it.tile * ATT_ROWS >= it.length) it.n = 0;
   return it;
 }
 
@@ -160,17 +188,28 @@ __device__ __forceinline__ void store_row16(T* out, float* part, const float (&v
   }
 }
 
-template <typename T, int DP>
+// Where a thread's row of 32 gradient elements lies in its warp's 2 KB, in the
+// swizzle of a 64-byte box.
+__device__ __forceinline__ uint32_t dq_stage_at(int lane, int unit) {
+  return static_cast<uint32_t>(lane * 64 + ((unit ^ ((lane >> 1) & 3)) << 4));
+}
+
+template <typename T, int DP, bool DQ>
 __global__ void __launch_bounds__(BWD_THREADS, 1) attn_dkv_kernel(const __grid_constant__ DkvParams p) {
-  using Shape = DkvShape<DP>;
+  using Shape = DkvShape<DP, DQ>;
   constexpr int SLOTS = Shape::SLOTS;
   constexpr uint32_t TILE = Shape::TILE;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  if (smem + Shape::USED > smem_raw + Shape::SMEM) {  // (dynamic shared memory starts on 1024 bytes as it is)
+    if (threadIdx.x == 0) atomicExch(p.err, DEV_ERR_TIMEOUT);
+    return;
+  }
   uint8_t* sK = smem;
   uint8_t* sV = smem + TILE;
   uint8_t* ring = smem + 2 * TILE;  // dO_0, Q_0, dO_1, Q_1, ...: freed in that order
-  float* sRows = reinterpret_cast<float*>(ring + SLOTS * TILE);
+  uint8_t* sDS = ring + SLOTS * TILE;
+  float* sRows = reinterpret_cast<float*>(sDS + Shape::DS);
   uint64_t* full = reinterpret_cast<uint64_t*>(sRows + Shape::ROW_SLOTS * ROW_VALUES);
   uint64_t* empty = full + SLOTS;
   uint64_t* kv_full = empty + SLOTS;
@@ -179,10 +218,12 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) attn_dkv_kernel(const __grid_c
   uint64_t* p_ready = s_full + 1;
   uint64_t* dp_full = p_ready + 1;
   uint64_t* ds_ready = dp_full + 1;
-  uint64_t* acc_full = ds_ready + 1;
+  uint64_t* dq_full = ds_ready + 1;
+  uint64_t* dq_read = dq_full + 1;
+  uint64_t* acc_full = dq_read + 1;
   uint64_t* acc_empty = acc_full + 1;
   uint64_t* drain_bar = acc_empty + 1;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain_bar + 1);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain_bar + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
   const int warp = uniform(threadIdx.x / 32);
@@ -190,17 +231,21 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) attn_dkv_kernel(const __grid_c
   if (threadIdx.x == 0) {
     for (int s = 0; s < SLOTS; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      // two products each; with DQ a tile of Q is freed by the warps, which send rows of dQ out of its memory
+      mbar_init(&empty[s], DQ && s % 2 == 1 ? BWD_WARPS : 2);
     }
     mbar_init(kv_full, 1);
-    mbar_init(kv_empty, 1);
+    mbar_init(kv_empty, 2);
     mbar_init(s_full, 1);
     mbar_init(p_ready, BWD_WARPS);
     mbar_init(dp_full, 1);
     mbar_init(ds_ready, BWD_WARPS);
-    mbar_init(acc_full, 1);
+    mbar_init(dq_full, 1);
+    mbar_init(dq_read, BWD_WARPS);
+    mbar_init(acc_full, 2);
     mbar_init(acc_empty, BWD_WARPS);
-    mbar_init(drain_bar, 1);
+    mbar_init(&drain_bar[0], 1);
+    mbar_init(&drain_bar[1], 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -212,10 +257,15 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) attn_dkv_kernel(const __grid_c
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_holder;
-  const uint32_t t_s = tmem, t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 256 + DP;
+  // Where three accumulators and the two tiles fit, dQ has columns of its own; else it takes those of dP, which then
+  // waits until dQ has been read.
+  const bool apart = 3 * p.mma_n <= 256;
+  const uint32_t t_s = tmem, t_dp = tmem + 128, t_dv = tmem + 256, t_dk = t_dv + p.mma_n;
+  const uint32_t t_dq = apart ? t_dk + p.mma_n : t_dp;
   pdl_wait();
   pdl_launch_dependents();
   const int tiles = p.h.query_tiles();
+  const int per_head = p.rounds / tiles;  // groups of a key head
 
   if (warp == BWD_WARPS) {
     if (lane == 0) {
@@ -230,10 +280,8 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) attn_dkv_kernel(const __grid_c
         att_load_tile<DP>(sK, &p.k, kv_full, it.kv_head, it.tile * ATT_ROWS, it.b);
         att_load_tile<DP>(sV, &p.v, kv_full, it.kv_head, it.tile * ATT_ROWS, it.b);
         ++items;
-        for (int x = it.x0; ok && x < it.x0 + it.n; ++x, ++rounds) {
-          const int per_head = p.rounds / tiles;  // groups of a key head
-          const int group = it.kv_head * per_head + x / tiles;
-          const int tile = x % tiles;
+        int group = it.kv_head * per_head + it.x0 / tiles, tile = it.x0 % tiles;
+        for (int x = 0; ok && x < it.n; ++x, ++rounds) {
           for (int which = 0; which < 2; ++which) {
             const uint32_t slot = n % SLOTS;
             ok = ok && wait_bounded(&empty[slot], ((n / SLOTS) & 1u) ^ 1u, abort_flag, p.err, ATT_WAIT_NS);
@@ -247,6 +295,10 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) attn_dkv_kernel(const __grid_c
                         ROW_VALUES * sizeof(float), &full[slot]);
             ++n;
           }
+          if (++tile == tiles) {
+            tile = 0;
+            ++group;
+          }
         }
       }
       if (!ok) {  // every load in flight lands before the CTA exits
@@ -254,10 +306,14 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) attn_dkv_kernel(const __grid_c
         if (items) wait_drain(kv_full, (items - 1) & 1u, 50000000ull);
       }
     }
-  } else if (warp == BWD_WARPS + 1) {
+  } else if (warp > BWD_WARPS) {
+    // Two warps issue products: one S^T and dV, the other dP^T, dK and dQ. A wait that is already over costs 100
+    // cycles, in which the other's products run.
     constexpr bool FP16 = !std::is_same<T, __nv_bfloat16>::value;
     const uint32_t id_s = idesc_f16kind_f32(ATT_ROWS, ATT_ROWS, false, false, FP16);
     const uint32_t id_acc = idesc_f16kind_f32(ATT_ROWS, p.mma_n, false, true, FP16);
+    const uint32_t id_dq = idesc_f16kind_f32(ATT_ROWS, p.mma_n, true, true, FP16);
+    const int mine = warp - (BWD_WARPS + 1);
     uint32_t n = 0, rounds = 0, items = 0;  // ring tiles used up, rounds, items before this one
     bool ok = true, issued = false;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -268,48 +324,106 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) attn_dkv_kernel(const __grid_c
     };
     auto slot = [&](uint32_t k) { return ring + (k % SLOTS) * TILE; };
     auto wait_slot = [&](uint32_t k) { return wait(&full[k % SLOTS], (k / SLOTS) & 1u); };
-    auto form = [&](uint32_t d, const uint8_t* a, uint32_t k, uint64_t* done) {
-      if (!wait_slot(k)) return;
-      if (elect_one()) {
-        att_mma_rows<DP>(d, a, slot(k), p.mma_k, id_s);
-        umma_commit(done);
-      }
-      __syncwarp();
-      issued = true;
-    };
     for (uint32_t item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
       const DkvItem it = dkv_item(p, item);
       const int count = uniform(it.n);
       if (count <= 0) continue;
+      const int key_steps = min(ATT_ROWS / 16, (uniform(it.length) - uniform(it.tile) * ATT_ROWS + 15) / 16);
       if (!wait(kv_full, items & 1u)) break;
-      form(t_s, sK, n + 1, s_full);
-      if (ok) form(t_dp, sV, n, dp_full);
-      for (int i = 0; ok && i < count; ++i, n += 2, ++rounds) {
-        if (!wait(p_ready, rounds & 1u)) break;
-        if (i == 0 && !wait(acc_empty, (items & 1u) ^ 1u)) break;
-        if (elect_one()) {
-          att_mma_cols<32>(t_dv, t_s, slot(n), id_acc, i > 0);
-          umma_commit(&empty[n % SLOTS]);
+      if (mine == 0) {
+        auto form_s = [&](uint32_t k) {
+          if (!wait_slot(k)) return;
+          if (elect_one()) {
+            att_mma_rows<DP>(t_s, sK, slot(k), p.mma_k, id_s);
+            umma_commit(s_full);
+            if (!DQ) umma_commit(&empty[k % SLOTS]);
+          }
+          __syncwarp();
+          issued = true;
+        };
+        form_s(n + 1);
+        for (int i = 0; ok && i < count; ++i, n += 2, ++rounds) {
+          if (i == 0 && !wait(acc_empty, (items & 1u) ^ 1u)) break;
+          if (!wait_slot(n) || !wait(p_ready, rounds & 1u)) break;
+          if (elect_one()) {
+            att_mma_cols<32>(t_dv, t_s, slot(n), id_acc, i > 0);
+            umma_commit(&empty[n % SLOTS]);
+            if (i + 1 == count) {
+              umma_commit(kv_empty);
+              umma_commit(acc_full);
+            }
+          }
+          __syncwarp();
+          if (i + 1 < count) form_s(n + 3);
         }
-        __syncwarp();
-        if (i + 1 < count) form(t_s, sK, n + 3, s_full);
-        if (!ok || !wait(ds_ready, rounds & 1u)) break;
-        if (elect_one()) {
-          att_mma_cols<32>(t_dk, t_dp, slot(n + 1), id_acc, i > 0);
-          umma_commit(&empty[(n + 1) % SLOTS]);
-          if (i + 1 == count) {
-            umma_commit(kv_empty);
-            umma_commit(acc_full);
+      } else {
+        auto form_dp = [&](uint32_t k) {
+          if (!wait_slot(k)) return;
+          if (elect_one()) {
+            att_mma_rows<DP>(t_dp, sV, slot(k), p.mma_k, id_s);
+            umma_commit(dp_full);
+            umma_commit(&empty[k % SLOTS]);
+          }
+          __syncwarp();
+          issued = true;
+        };
+        // dQ of the last round has been read (its columns are dP's, or those of the next dQ)
+        auto wait_read = [&] { return rounds == 0 || wait(dq_read, (rounds - 1) & 1u); };
+        if (DQ && !apart && !wait_read()) break;
+        form_dp(n);
+        for (int i = 0; ok && i < count; ++i, n += 2) {
+          if (i == 0 && !wait(acc_empty, (items & 1u) ^ 1u)) break;
+          if (!wait_slot(n + 1) || !wait(ds_ready, rounds & 1u)) break;
+          if constexpr (DQ) {
+            if (apart) {
+              if (i + 1 < count) form_dp(n + 2);
+              if (!ok || !wait_read()) break;
+            }
+            if (elect_one()) {
+              // dS^T lies [key][query]: along its rows for dK, along its columns for dQ
+              const uint64_t ds_q = smem_desc_sw128(smem_u32(sDS), ATT_CHUNK, 1024);
+              const uint64_t keys = smem_desc_sw128(smem_u32(sK), ATT_CHUNK, 1024);
+#pragma unroll 1
+              for (int k = 0; k < key_steps; ++k)
+                umma_bf16(t_dq, desc_at(ds_q, k * 2048), desc_at(keys, k * 2048), id_dq, k > 0 ? 1u : 0u);
+              const uint64_t ds_k = smem_desc_sw128(smem_u32(sDS), 16, 1024);
+              const uint64_t q = smem_desc_sw128(smem_u32(slot(n + 1)), ATT_CHUNK, 1024);
+#pragma unroll
+              for (int k = 0; k < ATT_ROWS / 16; ++k)
+                umma_bf16(t_dk, desc_at(ds_k, (k >> 2) * ATT_CHUNK + (k & 3) * 32), desc_at(q, k * 2048), id_acc,
+                          i > 0 || k > 0 ? 1u : 0u);
+              umma_commit(dq_full);
+              if (i + 1 == count) {
+                umma_commit(kv_empty);
+                umma_commit(acc_full);
+              }
+            }
+            __syncwarp();
+            ++rounds;
+            if (!apart && i + 1 < count) {
+              if (!wait_read()) break;
+              form_dp(n + 2);
+            }
+          } else {
+            if (elect_one()) {
+              att_mma_cols<32>(t_dk, t_dp, slot(n + 1), id_acc, i > 0);
+              umma_commit(&empty[(n + 1) % SLOTS]);
+              if (i + 1 == count) {
+                umma_commit(kv_empty);
+                umma_commit(acc_full);
+              }
+            }
+            __syncwarp();
+            ++rounds;
+            if (i + 1 < count) form_dp(n + 2);
           }
         }
-        __syncwarp();
-        if (i + 1 < count) form(t_dp, sV, n + 2, dp_full);
       }
       ++items;
     }
     if (!ok && issued) {
-      if (elect_one()) umma_commit(drain_bar);
-      wait_drain(drain_bar, 0, 50000000ull);
+      if (elect_one()) umma_commit(&drain_bar[mine]);
+      wait_drain(&drain_bar[mine], 0, 50000000ull);
     }
   } else {
     const int quarter = warp >> 2;  // query columns 32 quarter .. + 32
@@ -317,7 +431,6 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) attn_dkv_kernel(const __grid_c
     const uint32_t t_lane = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t t_mine = t_lane + quarter * 32;
     uint32_t rounds = 0, items = 0, n = 1;  // n: the ring's next Q
-    const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       const bool got = wait_bounded(bar, parity, abort_flag, p.err, ATT_WAIT_NS);
       if (!__all_sync(0xffffffffu, got)) return false;
@@ -325,56 +438,150 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) attn_dkv_kernel(const __grid_c
       return true;
     };
     auto arrive = [&](uint64_t* bar) {
-      tmem_store_wait();
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
-    for (uint32_t item = blockIdx.x; item < p.items; item += gridDim.x) {
+    bool ok = true;
+    for (uint32_t item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
       const DkvItem it = dkv_item(p, item);
-      bool ok = true;
-      for (int i = 0; i < it.n; ++i, ++rounds, n += 2) {
-        // (S is complete once Q and its rows' values are there; the wait makes the copy visible here)
-        ok = wait(&full[n % SLOTS], (n / SLOTS) & 1u) && wait(s_full, rounds & 1u);
-        if (!ok) break;
-        const float4* values =
-            reinterpret_cast<const float4*>(sRows + (rounds % Shape::ROW_SLOTS) * ROW_VALUES + quarter * 32);
+      int group = 0, tile = 0;
+      if (DQ) {
+        group = it.kv_head * per_head + it.x0 / tiles;
+        tile = it.x0 % tiles;
+      }
+      // With DQ a round's rows of dQ are sent behind the next round's P, and the last one's in a round without P.
+      for (int i = 0; i < it.n + (DQ ? 1 : 0); ++i) {
+        const float* values = sRows + (rounds % Shape::ROW_SLOTS) * ROW_VALUES + quarter * 32;
         float pr[32];
-        uint32_t w[16];
-        tmem_load_32cols(t_s + t_mine, pr);
+        if (!DQ || i < it.n) {
+          // (S is complete once Q and its rows' values are there; the wait makes the copy visible here)
+          if (!(ok = wait(&full[n % SLOTS], (n / SLOTS) & 1u) && wait(s_full, rounds & 1u))) break;
+          const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
+          tmem_load_32cols(t_s + t_mine, pr);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float4 lse = values[e];
-          const float2 x = f2_unpack(f2_fma(f2_pack(pr[4 * e], pr[4 * e + 1]), sc2, f2_pack(lse.x, lse.y)));
-          const float2 y = f2_unpack(f2_fma(f2_pack(pr[4 * e + 2], pr[4 * e + 3]), sc2, f2_pack(lse.z, lse.w)));
-          pr[4 * e] = exp2_fast(x.x);
-          pr[4 * e + 1] = exp2_fast(x.y);
-          pr[4 * e + 2] = exp2_fast(y.x);
-          pr[4 * e + 3] = exp2_fast(y.y);
-          w[2 * e] = pack2<T>(pr[4 * e], pr[4 * e + 1]);
-          w[2 * e + 1] = pack2<T>(pr[4 * e + 2], pr[4 * e + 3]);
-        }
-        tmem_store_16cols(t_s + t_mine, w);
-        arrive(p_ready);
-        ok = wait(dp_full, rounds & 1u);
-        if (!ok) break;
-        float dp[32];
-        tmem_load_32cols(t_dp + t_mine, dp);
+          for (int c = 0; c < 32; c += 16) {
+            uint32_t w[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float4 delta = values[ATT_ROWS / 4 + e];
-          const float2 x = f2_unpack(f2_mul(f2_add(f2_pack(dp[4 * e], dp[4 * e + 1]), f2_pack(delta.x, delta.y)),
-                                            f2_pack(pr[4 * e], pr[4 * e + 1])));
-          const float2 y = f2_unpack(f2_mul(f2_add(f2_pack(dp[4 * e + 2], dp[4 * e + 3]), f2_pack(delta.z, delta.w)),
-                                            f2_pack(pr[4 * e + 2], pr[4 * e + 3])));
-          w[2 * e] = pack2<T>(x.x, x.y);
-          w[2 * e + 1] = pack2<T>(y.x, y.y);
+            for (int e = c; e < c + 16; e += 4) {
+              const float4 lse = *reinterpret_cast<const float4*>(values + e);
+              const float2 x = f2_unpack(f2_fma(f2_pack(pr[e], pr[e + 1]), sc2, f2_pack(lse.x, lse.y)));
+              const float2 y = f2_unpack(f2_fma(f2_pack(pr[e + 2], pr[e + 3]), sc2, f2_pack(lse.z, lse.w)));
+              pr[e] = exp2_fast(x.x);
+              pr[e + 1] = exp2_fast(x.y);
+              pr[e + 2] = exp2_fast(y.x);
+              pr[e + 3] = exp2_fast(y.y);
+              w[(e - c) / 2] = pack2<T>(pr[e], pr[e + 1]);
+              w[(e - c) / 2 + 1] = pack2<T>(pr[e + 2], pr[e + 3]);
+            }
+            tmem_store_8cols(t_s + t_mine + c / 2, w);
+          }
+          tmem_store_wait();
+          arrive(p_ready);
         }
-        tmem_store_16cols(t_dp + t_mine, w);
+        if constexpr (DQ) {
+          if (i > 0) {
+            // These 32 columns of 32 rows of the last round's dQ go out of the memory of its Q.
+            if (!(ok = wait(dq_full, (rounds - 1) & 1u))) break;
+            const uint32_t slot = (n - 2) % SLOTS;
+            uint8_t* stage = ring + slot * TILE + warp * 2048;
+            const bool some = quarter * 32 < p.h.head;  // (the same in all threads of a warp)
+            if (some) {
+#pragma unroll
+              for (int c = 0; c < 32; c += 16) {
+                float v[16];
+                tmem_load_16cols(t_dq + t_mine + c, v);
+#pragma unroll
+                for (int u = 0; u < 16; u += 8) {
+                  float x[8];
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) x[e] = v[u + e] * p.scale;
+                  Raw8<T> r;
+                  r.set(x);
+                  *reinterpret_cast<uint4*>(stage + dq_stage_at(lane, (c + u) / 8)) = r.a;
+                }
+              }
+              fence_proxy_async_smem();
+            }
+            arrive(dq_read);
+            if (some && lane == 0) {
+              const int last_tile = tile > 0 ? tile - 1 : tiles - 1, last_group = tile > 0 ? group : group - 1;
+              const int first = last_tile * p.h.tile_tokens() + (((warp & 3) * 32) >> p.h.pack_log2);
+              if (first < p.h.queries) {
+                tma_store_4d(&p.dq, stage, quarter * 32, last_group << p.h.pack_log2, first, it.b);
+                bulk_commit_group();
+                bulk_wait_group_read<0>();
+              }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[slot]);
+          }
+          if (i == it.n) break;
+        }
+        if (!(ok = wait(dp_full, rounds & 1u))) break;
+        // keys behind the last one may hold anything: dQ sums over keys, so their dS is zero
+        const bool used = !DQ || row < it.length;
+#pragma unroll
+        for (int c = 0; c < 32; c += 16) {
+          float dp[16];
+          uint32_t w[8];
+          tmem_load_16cols(t_dp + t_mine + c, dp);
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) {
+            const float4 delta = *reinterpret_cast<const float4*>(values + ATT_ROWS + c + e);
+            const float2 x = f2_unpack(f2_mul(f2_add(f2_pack(dp[e], dp[e + 1]), f2_pack(delta.x, delta.y)),
+                                              f2_pack(pr[c + e], pr[c + e + 1])));
+            const float2 y = f2_unpack(f2_mul(f2_add(f2_pack(dp[e + 2], dp[e + 3]), f2_pack(delta.z, delta.w)),
+                                              f2_pack(pr[c + e + 2], pr[c + e + 3])));
+            w[e / 2] = used ? pack2<T>(x.x, x.y) : 0u;
+            w[e / 2 + 1] = used ? pack2<T>(y.x, y.y) : 0u;
+          }
+          if constexpr (DQ) {
+            uint8_t* ds = sDS + (quarter >> 1) * ATT_CHUNK + row * 128;
+            const int unit = (quarter & 1) * 4 + c / 8;
+            *reinterpret_cast<uint4*>(ds + ((unit ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(ds + (((unit + 1) ^ (row & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+          } else {
+            tmem_store_8cols(t_dp + t_mine + c / 2, w);  // (over columns that have been read)
+          }
+        }
+        if constexpr (DQ) {
+          if (i == 0 && it.length < ATT_ROWS) {
+            // as above, in K
+            uint4* k = reinterpret_cast<uint4*>(sK);
+            for (int c = it.length * 8 + static_cast<int>(threadIdx.x); c < (it.length + 15) / 16 * 128; c += 512)
+#pragma unroll
+              for (int q = 0; q < DP / 64; ++q) k[q * (ATT_CHUNK / 16) + c] = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          if (++tile == tiles) {
+            tile = 0;
+            ++group;
+          }
+        } else {
+          tmem_store_wait();
+        }
         arrive(ds_ready);
+        ++rounds;
+        n += 2;
       }
       if (!ok) break;
-      if (it.n > 0 && !wait(acc_full, items & 1u)) break;
+      if (DQ && it.n <= 0 && it.length <= 0) {
+        // no keys: dQ is zero
+        for (int x = 0, g = group, q = tile; x < min(p.split_rounds, p.rounds - it.x0); ++x) {
+          const int token = q * p.h.tile_tokens() + (row >> p.h.pack_log2);
+          T* out = static_cast<T*>(p.dq_out) + it.b * p.dq_strides.batch + token * p.dq_strides.token +
+                   ((g << p.h.pack_log2) + (row & ((1 << p.h.pack_log2) - 1))) * p.dq_strides.head;
+          if (token < p.h.queries)
+            for (int c = quarter * 32; c < min(p.h.head, quarter * 32 + 32); c += 8)
+              *reinterpret_cast<uint4*>(out + c) = make_uint4(0, 0, 0, 0);
+          if (++q == tiles) {
+            q = 0;
+            ++g;
+          }
+        }
+      }
+      if (it.n > 0 && !(ok = wait(acc_full, items & 1u))) break;
       // quarters 0 and 1 write dV, 2 and 3 dK, each half of the elements
       const bool is_dk = quarter >= 2;
       const int first = (quarter & 1) * (DP / 2);
@@ -389,10 +596,8 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) attn_dkv_kernel(const __grid_c
         part += (((static_cast<int64_t>(it.split) * p.h.batch + it.b) * p.h.keys + key) * p.h.kv_heads + it.kv_head) *
                 p.h.head;
       const float factor = is_dk ? p.scale : 1.f;
-#pragma unroll
-      for (int q = 0; q < DP / 2; q += 16) {
-        const int c = first + q;
-        if (c >= p.h.head) break;
+#pragma unroll 1
+      for (int c = first; c < min(first + DP / 2, p.h.head); c += 16) {
         float v[16];
         __syncwarp();
         if (it.n > 0) tmem_load_16cols(t_acc + c, v);
@@ -401,12 +606,11 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) attn_dkv_kernel(const __grid_c
         if (live) store_row16<T>(out, part, v, c, p.h.head);
       }
       if (it.n > 0) {
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(acc_empty);
+        arrive(acc_empty);
         ++items;
       }
     }
+    if (DQ && lane == 0) bulk_wait_group_all();
   }
   __syncwarp();
   tc_fence_before_sync();
@@ -483,8 +687,9 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) attn_dq_kernel(const __grid_co
   uint64_t* ds_ready = dp_full + 1;
   uint64_t* acc_full = ds_ready + 1;
   uint64_t* acc_empty = acc_full + 1;
-  uint64_t* drain_bar = acc_empty + 1;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain_bar + 1);
+  uint64_t* dq_done = acc_empty + 1;  // of each buffer of S, which holds dS
+  uint64_t* drain_bar = dq_done + 2;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain_bar + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
   const int warp = uniform(threadIdx.x / 32);
@@ -506,7 +711,10 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) attn_dq_kernel(const __grid_co
     mbar_init(ds_ready, BWD_WARPS);
     mbar_init(acc_full, 1);
     mbar_init(acc_empty, BWD_WARPS);
-    mbar_init(drain_bar, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&dq_done[i], 1);
+      mbar_init(&drain_bar[i], 1);
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -557,10 +765,12 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) attn_dq_kernel(const __grid_co
         if (items) wait_drain(q_full, (items - 1) & 1u, 50000000ull);
       }
     }
-  } else if (warp == BWD_WARPS + 1) {
+  } else if (warp > BWD_WARPS) {
+    // Two warps issue products: one S, up to two key tiles ahead, the other dP and dQ.
     constexpr bool FP16 = !std::is_same<T, __nv_bfloat16>::value;
     const uint32_t id_s = idesc_f16kind_f32(ATT_ROWS, ATT_ROWS, false, false, FP16);
     const uint32_t id_acc = idesc_f16kind_f32(ATT_ROWS, p.mma_n, false, true, FP16);
+    const int mine = warp - (BWD_WARPS + 1);
     uint32_t n = 0, items = 0;  // key tiles used up, items before this one
     bool ok = true, issued = false;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -568,15 +778,6 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) attn_dq_kernel(const __grid_co
       ok = __all_sync(0xffffffffu, got);
       tc_fence_after_sync();
       return ok;
-    };
-    auto form_s = [&](uint32_t k) {
-      if (!wait(&k_full[k % KS], (k / KS) & 1u)) return;
-      if (elect_one()) {
-        att_mma_rows<DP>(tmem + (k & 1u) * 128, sQ, sK + (k % KS) * TILE, p.mma_k, id_s);
-        umma_commit(&s_full[k & 1u]);
-      }
-      __syncwarp();
-      issued = true;
     };
     auto form_dp = [&](uint32_t k) {
       if (!wait(&v_full[k % VS], (k / VS) & 1u)) return;
@@ -586,36 +787,50 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) attn_dq_kernel(const __grid_co
         umma_commit(&v_empty[k % VS]);
       }
       __syncwarp();
+      issued = true;
     };
     for (uint32_t item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
       const DqItem it = dq_item(p, item);
       const int count = uniform(it.n);
       if (count <= 0) continue;
       if (!wait(q_full, items & 1u)) break;
-      form_s(n);
-      if (ok) form_dp(n);
-      if (ok && count > 1) form_s(n + 1);
-      for (int j = 0; ok && j < count; ++j, ++n) {
-        if (!wait(ds_ready, n & 1u)) break;
-        if (j + 1 < count) form_dp(n + 1);
-        if (j == 0 && ok) wait(acc_empty, (items & 1u) ^ 1u);
-        if (!ok) break;
-        if (elect_one()) {
-          att_mma_cols<32>(t_dq, tmem + (n & 1u) * 128, sK + (n % KS) * TILE, id_acc, j > 0);
-          umma_commit(&k_empty[n % KS]);
-          if (j + 1 == count) {
-            umma_commit(q_empty);
-            umma_commit(acc_full);
+      if (mine == 0) {
+        for (int j = 0; ok && j < count; ++j, ++n) {
+          // (dS of two tiles ago has been read)
+          if (n >= 2 && !wait(&dq_done[n & 1u], ((n - 2) >> 1) & 1u)) break;
+          if (!wait(&k_full[n % KS], (n / KS) & 1u)) break;
+          if (elect_one()) {
+            att_mma_rows<DP>(tmem + (n & 1u) * 128, sQ, sK + (n % KS) * TILE, p.mma_k, id_s);
+            umma_commit(&s_full[n & 1u]);
           }
+          __syncwarp();
+          issued = true;
         }
-        __syncwarp();
-        if (j + 2 < count) form_s(n + 2);
+      } else {
+        form_dp(n);
+        for (int j = 0; ok && j < count; ++j, ++n) {
+          if (!wait(&k_full[n % KS], (n / KS) & 1u)) break;
+          if (j == 0 && !wait(acc_empty, (items & 1u) ^ 1u)) break;
+          if (!wait(ds_ready, n & 1u)) break;
+          if (j + 1 < count) form_dp(n + 1);
+          if (!ok) break;
+          if (elect_one()) {
+            att_mma_cols<32>(t_dq, tmem + (n & 1u) * 128, sK + (n % KS) * TILE, id_acc, j > 0);
+            umma_commit(&dq_done[n & 1u]);
+            umma_commit(&k_empty[n % KS]);
+            if (j + 1 == count) {
+              umma_commit(q_empty);
+              umma_commit(acc_full);
+            }
+          }
+          __syncwarp();
+        }
       }
       ++items;
     }
     if (!ok && issued) {
-      if (elect_one()) umma_commit(drain_bar);
-      wait_drain(drain_bar, 0, 50000000ull);
+      if (elect_one()) umma_commit(&drain_bar[mine]);
+      wait_drain(&drain_bar[mine], 0, 50000000ull);
     }
   } else {
     const int quarter = warp >> 2;  // key columns 32 quarter .. + 32
@@ -653,23 +868,29 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) attn_dq_kernel(const __grid_co
         }
         ok = wait(dp_full, n & 1u);
         if (!ok) break;
-        float dp[32];
-        uint32_t w[16];
-        tmem_load_32cols(t_dp + t_mine, dp);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float2 ds = f2_unpack(f2_mul(f2_add(f2_pack(dp[2 * e], dp[2 * e + 1]), delta2),
-                                             f2_pack(pr[2 * e], pr[2 * e + 1])));
-          w[e] = pack2<T>(ds.x, ds.y);
-        }
         const int valid = it.length - (it.k0 + j) * ATT_ROWS;
-        if (valid < ATT_ROWS) {
-          const int mine = valid - quarter * 32;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            if (2 * e >= mine) w[e] = 0u;
-            else if (2 * e + 1 >= mine) w[e] &= 0xffffu;
+        for (int c = 0; c < 32; c += 16) {
+          float dp[16];
+          uint32_t w[8];
+          tmem_load_16cols(t_dp + t_mine + c, dp);
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            const float2 ds = f2_unpack(f2_mul(f2_add(f2_pack(dp[e], dp[e + 1]), delta2),
+                                               f2_pack(pr[c + e], pr[c + e + 1])));
+            w[e / 2] = pack2<T>(ds.x, ds.y);
           }
+          if (valid < ATT_ROWS) {
+            const int mine = valid - quarter * 32 - c;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              if (2 * e >= mine) w[e] = 0u;
+              else if (2 * e + 1 >= mine) w[e] &= 0xffffu;
+            }
+          }
+          tmem_store_8cols(t_s + c / 2, w);
+        }
+        if (valid < ATT_ROWS) {
           // keys behind the last one meet a dS of zero: infinities and NaN would remain. (S, which also reads the
           // tile, is complete.)
           uint4* k = reinterpret_cast<uint4*>(sK + (n % KS) * TILE);
@@ -679,7 +900,6 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) attn_dq_kernel(const __grid_co
           fence_proxy_async_smem();
           __syncwarp();
         }
-        tmem_store_16cols(t_s, w);
         tmem_store_wait();
         tc_fence_before_sync();
         __syncwarp();
@@ -694,10 +914,8 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) attn_dq_kernel(const __grid_co
       if (part != nullptr)
         part += (((static_cast<int64_t>(it.split) * p.h.batch + it.b) * p.h.queries + token) * p.h.heads + head) *
                 p.h.head;
-#pragma unroll
-      for (int q = 0; q < DP / 4; q += 16) {
-        const int c = quarter * (DP / 4) + q;
-        if (c >= p.h.head) break;
+#pragma unroll 1
+      for (int c = quarter * (DP / 4); c < min((quarter + 1) * (DP / 4), p.h.head); c += 16) {
         float v[16];
         __syncwarp();
         if (it.n > 0) tmem_load_16cols(t_dq + t_lane + c, v);
@@ -769,6 +987,7 @@ cudaError_t add_parts(const AttCall& c, const float* part, void* out, const AttS
 // -------------------------------------------------------------------- host
 struct Plan {
   AttSplit dkv, dq;            // ranges of rounds; ranges of key tiles
+  bool one;                    // one key tile: dQ comes out of dK's and dV's pass
   int rounds, key_tiles;
   size_t dkv_at, dq_at, bytes; // workspace: rows' values, then parts of dK and dV, then of dQ
   size_t dkv_part;             // floats of the parts of dK
@@ -788,6 +1007,7 @@ Plan plan(const AttHeads& h, int num_sms) {
   s.key_tiles = (h.keys + ATT_ROWS - 1) / ATT_ROWS;
   s.rounds = (h.group_heads >> h.pack_log2) * tiles;
   s.dkv = split(static_cast<int64_t>(h.batch) * h.kv_heads * s.key_tiles, s.rounds, num_sms);
+  s.one = s.key_tiles == 1;
   s.dq = split(static_cast<int64_t>(h.batch) * h.groups * tiles, s.key_tiles, num_sms);
   size_t at = round_up(static_cast<size_t>(h.batch) * h.groups * tiles * ROW_VALUES * sizeof(float), 256);
   s.dkv_at = at;
@@ -799,24 +1019,28 @@ Plan plan(const AttHeads& h, int num_sms) {
   return s;
 }
 
+template <typename T, int DP, bool DQ>
+cudaError_t launch_dkv(const DkvParams& p, int num_sms, cudaStream_t stream) {
+  static std::atomic<uint64_t> ready{0};
+  constexpr size_t SMEM = DkvShape<DP, DQ>::SMEM;
+  static_assert(DkvShape<DP, DQ>::USED <= 232448, "shared memory above 227 KB");
+  const cudaError_t e = att_prepare(attn_dkv_kernel<T, DP, DQ>, SMEM, ready);
+  if (e != cudaSuccess) return e;
+  const unsigned grid = static_cast<unsigned>(std::min<uint32_t>(p.items, num_sms));
+  return launch_dependent(attn_dkv_kernel<T, DP, DQ>, dim3(grid), dim3(BWD_THREADS), SMEM, stream, p);
+}
+
 template <typename T, int DP>
-cudaError_t launch(const AttCall& c, const Plan& s, RowsParams& rows, DkvParams& dkv, DqParams& dq,
+cudaError_t launch(const AttCall& c, const Plan& s, const RowsParams& rows, const DkvParams& dkv, const DqParams& dq,
                    cudaStream_t stream) {
-  static std::atomic<uint64_t> dkv_ready{0}, dq_ready{0};
-  cudaError_t e;
-  if (rows.count > 0) {
-    e = launch_dependent(attn_rows_kernel<T>, dim3(static_cast<unsigned>((rows.count * 16 + 255) / 256)), dim3(256), 0,
-                         stream, rows);
-    if (e != cudaSuccess) return e;
-  }
-  if (dkv.items > 0) {
-    if ((e = att_prepare(attn_dkv_kernel<T, DP>, DkvShape<DP>::SMEM, dkv_ready)) != cudaSuccess) return e;
-    const unsigned grid = static_cast<unsigned>(std::min<uint32_t>(dkv.items, c.num_sms));
-    e = launch_dependent(attn_dkv_kernel<T, DP>, dim3(grid), dim3(BWD_THREADS), DkvShape<DP>::SMEM, stream, dkv);
-    if (e != cudaSuccess) return e;
-  }
-  if (dq.items > 0) {
-    if ((e = att_prepare(attn_dq_kernel<T, DP>, DqShape<DP>::SMEM, dq_ready)) != cudaSuccess) return e;
+  static std::atomic<uint64_t> ready{0};
+  const unsigned tiles = static_cast<unsigned>(c.h.batch) * c.h.groups * c.h.query_tiles();
+  cudaError_t e = launch_dependent(attn_rows_kernel<T, DP>, dim3(tiles), dim3(256), 0, stream, rows);
+  if (e != cudaSuccess) return e;
+  e = s.one ? launch_dkv<T, DP, true>(dkv, c.num_sms, stream) : launch_dkv<T, DP, false>(dkv, c.num_sms, stream);
+  if (e != cudaSuccess) return e;
+  if (!s.one) {
+    if ((e = att_prepare(attn_dq_kernel<T, DP>, DqShape<DP>::SMEM, ready)) != cudaSuccess) return e;
     const unsigned grid = static_cast<unsigned>(std::min<uint32_t>(dq.items, c.num_sms));
     e = launch_dependent(attn_dq_kernel<T, DP>, dim3(grid), dim3(BWD_THREADS), DqShape<DP>::SMEM, stream, dq);
     if (e != cudaSuccess) return e;
@@ -843,7 +1067,7 @@ cudaError_t attn_backward(const AttCall& c, const void* grad_o, const void* q, c
   const Plan s = plan(h, c.num_sms);
   float* values = reinterpret_cast<float*>(workspace);
   const int tiles = h.query_tiles(), pack = 1 << h.pack_log2;
-  RowsParams r{h, c.o, c.grad_o, o, grad_o, lse, values, static_cast<int64_t>(h.batch) * h.groups * tiles * ATT_ROWS};
+  const RowsParams r{h, c.o, c.grad_o, o, grad_o, lse, values};
   DkvParams a{};
   DqParams b{};
   const bool q_ok = att_encode(&a.q, q, c.dtype, h.batch, h.queries, h.heads, h.head, c.q, pack, ATT_ROWS / pack) &&
@@ -851,7 +1075,11 @@ cudaError_t attn_backward(const AttCall& c, const void* grad_o, const void* q, c
                                ATT_ROWS / pack);
   const bool k_ok = att_encode(&a.k, k, c.dtype, h.batch, h.keys, h.kv_heads, h.head, c.k, 1, ATT_ROWS) &&
                     att_encode(&a.v, v, c.dtype, h.batch, h.keys, h.kv_heads, h.head, c.v, 1, ATT_ROWS);
-  if (!q_ok || !k_ok) return cudaErrorInvalidValue;
+  if (!q_ok || !k_ok ||
+      (s.one && !att_encode(&a.dq, dq, c.dtype, h.batch, h.queries, h.heads, h.head, c.dq, pack, 32 / pack, 32)))
+    return cudaErrorInvalidValue;
+  a.dq_out = dq;
+  a.dq_strides = c.dq;
   b.q = a.q;
   b.grad_o = a.grad_o;
   b.k = a.k;

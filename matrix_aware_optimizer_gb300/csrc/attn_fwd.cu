@@ -45,7 +45,7 @@ static PFN_cuTensorMapEncodeTiled_v12000 att_encoder() {
 }
 
 bool att_encode(CUtensorMap* map, const void* base, int dtype, int64_t batch, int64_t rows, int64_t heads,
-                int64_t head, const AttStrides& s, int box_heads, int box_rows) {
+                int64_t head, const AttStrides& s, int box_heads, int box_rows, int box_elements) {
   auto enc = att_encoder();
   if (enc == nullptr) return false;
   cuuint64_t dims[4] = {static_cast<cuuint64_t>(head), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows),
@@ -55,11 +55,11 @@ bool att_encode(CUtensorMap* map, const void* base, int dtype, int64_t batch, in
     return static_cast<cuuint64_t>(extent > 1 ? stride : round_up(static_cast<size_t>(head), 8)) * 2;
   };
   cuuint64_t strides[3] = {bytes(heads, s.head), bytes(rows, s.token), bytes(batch, s.batch)};
-  cuuint32_t box[4] = {64u, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows), 1u};
+  cuuint32_t box[4] = {static_cast<cuuint32_t>(box_elements), static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows), 1u};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   return enc(map, dtype == PRM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
              const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             box_elements == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
