@@ -487,19 +487,16 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) attn_dkv_kernel(const __grid_c
             uint8_t* stage = ring + slot * TILE + warp * 2048;
             const bool some = quarter * 32 < p.h.head;  // (the same in all threads of a warp)
             if (some) {
+              float v[32];
+              tmem_load_32cols(t_dq + t_mine, v);
 #pragma unroll
-              for (int c = 0; c < 32; c += 16) {
-                float v[16];
-                tmem_load_16cols(t_dq + t_mine + c, v);
+              for (int u = 0; u < 32; u += 8) {
+                float x[8];
 #pragma unroll
-                for (int u = 0; u < 16; u += 8) {
-                  float x[8];
-#pragma unroll
-                  for (int e = 0; e < 8; ++e) x[e] = v[u + e] * p.scale;
-                  Raw8<T> r;
-                  r.set(x);
-                  *reinterpret_cast<uint4*>(stage + dq_stage_at(lane, (c + u) / 8)) = r.a;
-                }
+                for (int e = 0; e < 8; ++e) x[e] = v[u + e] * p.scale;
+                Raw8<T> r;
+                r.set(x);
+                *reinterpret_cast<uint4*>(stage + dq_stage_at(lane, u / 8)) = r.a;
               }
               fence_proxy_async_smem();
             }

@@ -377,12 +377,14 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) attn_fwd_kernel(const __grid_c
     for (uint32_t item = blockIdx.x; ok; item += gridDim.x) {
       const bool end = item >= p.items;
       int n = 0, valid = 0;
-      bool mine = false;  // the item has rows of this tile
+      bool mine = false;        // the item has rows of this tile
+      bool valid_ends = false;  // its sequence ends before the tensor
       if (!end) {
         const FwdItem it = fwd_item(p, item);
         mine = t < it.tiles;
         n = max(it.n, 0);
         valid = it.length - it.k0 * ATT_ROWS;
+        valid_ends = it.length < p.h.keys;
         if (!mine) {
           kv += 2 * n;
           continue;
@@ -400,9 +402,9 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) attn_fwd_kernel(const __grid_c
             if (!whole) hide(s, valid - 64);
             top4(s, mx);
           }
-          if (!whole) {
+          if (!whole && valid_ends) {
             // what lies behind the last key must not meet its P of zero: infinities and NaN would remain. (Both
-            // tiles' threads write the same zeros, each before its own product.)
+            // tiles' threads write the same zeros, each before its own product. Behind the tensor's end TMA did.)
             const uint32_t at = kv + 1;
             if (!(ok = wait(&kv_full[at % STAGES], (at / STAGES) & 1u))) break;
             uint4* v = reinterpret_cast<uint4*>(sKV + (at % STAGES) * TILE);
@@ -486,41 +488,34 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) attn_fwd_kernel(const __grid_c
           const int first = token - (lane >> p.h.pack_log2);  // the warp's first token
 #pragma unroll 1
           for (int c = 0; c < p.h.head; c += 64) {
-            uint4 u[8];
-#pragma unroll
-            for (int q = 0; q < 64; q += 16) {
-              if (c + q >= p.h.head) break;
-              float o[16];
-              __syncwarp();
-              if (some) tmem_load_16cols(t_o + c + q, o);
-#pragma unroll
-              for (int i = 0; i < 16; i += 8) {
-                float v[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = some ? o[i + e] * inv : 0.f;
-                if (p.splits > 1) {
-                  Raw8<float> r;
-                  r.set(v);
-                  if (live && c + q + i < p.h.head) r.store(part + c + q + i);
-                } else {
-                  Raw8<T> r;
-                  r.set(v);
-                  u[(q + i) / 8] = r.a;
-                }
-              }
-            }
+            // (one load: with four of 16 columns, each waited for, this took 1060 cycles)
+            float o[64];
+            __syncwarp();
+            if (some) tmem_load_64cols(t_o + c, o);
             if (some && c + 64 >= p.h.head) {  // O has been read
               tc_fence_before_sync();
               __syncwarp();
               if (lane == 0) mbar_arrive(&o_empty[t]);
             }
-            if (p.splits > 1) continue;
+#pragma unroll
+            for (int i = 0; i < 64; ++i) o[i] = some ? o[i] * inv : 0.f;
+            if (p.splits > 1) {
+#pragma unroll
+              for (int i = 0; i < 64; i += 8) {
+                if (c + i >= p.h.head || !live) break;
+                float4* to = reinterpret_cast<float4*>(part + c + i);
+                to[0] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                to[1] = make_float4(o[i + 4], o[i + 5], o[i + 6], o[i + 7]);
+              }
+              continue;
+            }
             if (lane == 0) bulk_wait_group_read<0>();
             __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              if (c + 8 * i >= p.h.head) break;
-              att_stage_row8(stage, lane, i, u[i]);
+            for (int i = 0; i < 64; i += 8) {
+              if (c + i >= p.h.head) break;
+              att_stage_row8(stage, lane, i / 8, make_uint4(pack2<T>(o[i], o[i + 1]), pack2<T>(o[i + 2], o[i + 3]),
+                                                            pack2<T>(o[i + 4], o[i + 5]), pack2<T>(o[i + 6], o[i + 7])));
             }
             fence_proxy_async_smem();
             __syncwarp();
