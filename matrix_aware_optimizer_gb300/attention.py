@@ -95,9 +95,9 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] =
     r2, ldr = (None, n) if residual is None else _rows(residual, n)
     tokens = x2.shape[0]
     y = torch.empty((*x.shape[:-1], n), dtype=x.dtype if residual is None else residual.dtype, device=x.device)
-    pre = x.new_empty((tokens, n)) if save and act is not None else None
+    pre = torch.empty((tokens, n), dtype=x.dtype, device=x.device) if save and act is not None else None
     n_ws = _linear_sizes(tokens, n, k)[0]
-    ws = x.new_empty(n_ws, dtype=torch.uint8) if n_ws else None
+    ws = torch.empty(n_ws, dtype=torch.uint8, device=x.device) if n_ws else None
     rc = N.load().prm_linear_forward(x2.data_ptr(), ldx, weight.data_ptr(), _ptr(bias), _ptr(r2), ldr, y.data_ptr(),
                                      _DTYPE[y.dtype], _ptr(pre), _ptr(ws), n_ws, tokens, n, k, _LINEAR_ACT[act],
                                      _DTYPE[x.dtype], _raw_stream(device))
@@ -136,9 +136,9 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, sav
         raise ValueError("saved does not belong to this x")
     dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if need_dx else None
     dweight = torch.empty_like(weight) if grad is None else grad
-    dbias = x.new_empty(n, dtype=torch.float32) if need_dbias else None
+    dbias = torch.empty(n, dtype=torch.float32, device=x.device) if need_dbias else None
     n_ws = _linear_sizes(tokens, n, k)[1]
-    ws = x.new_empty(n_ws, dtype=torch.uint8)
+    ws = torch.empty(n_ws, dtype=torch.uint8, device=x.device)
     rc = N.load().prm_linear_backward(dy2.data_ptr(), lddy, _DTYPE[dy.dtype], x2.data_ptr(), ldx, weight.data_ptr(),
                                       _ptr(saved.pre), _ptr(dx), dweight.data_ptr(), _ptr(dbias), ws.data_ptr(), n_ws,
                                       tokens, n, k, _LINEAR_ACT[act], _DTYPE[x.dtype], _raw_stream(device))
@@ -226,6 +226,8 @@ def _position_strides(positions, shape):
     own = positions.shape
     if own == shape:
         st = positions.stride()
+    elif len(own) == 1 and own[0] == shape[-1]:
+        return 0, positions.stride(0)
     elif len(own) <= len(shape) and all(a == b or a == 1 for a, b in zip(own[::-1], shape[::-1])):
         st = positions.expand(shape).stride()
     else:
@@ -364,13 +366,17 @@ class AttentionSaved(NamedTuple):
     keys: int
 
 
-_NO_STRIDES = (0, 0, 0)
+_NO_STRIDES = (0,) * 12
 
 
 def _usable(t) -> bool:
     """Whether the library reads (or writes) t as it lies: consecutive
     elements, rows of 16-byte units that do not overlap."""
-    if t.stride(3) != 1 or t.data_ptr() % 16:
+    if t.data_ptr() & 15:
+        return False
+    if t.is_contiguous():  # (a head is a multiple of 8)
+        return True
+    if t.stride(3) != 1:
         return False
     head = t.shape[3]
     for s, e in zip(t.stride()[:3], t.shape):
@@ -380,41 +386,47 @@ def _usable(t) -> bool:
 
 
 def _laid_out(t):
-    return t if t.numel() == 0 or _usable(t) else t.clone(memory_format=torch.contiguous_format)
+    return t if _usable(t) or t.numel() == 0 else t.clone(memory_format=torch.contiguous_format)
 
 
 def _attention_check(q, k, v, key_lengths, scale):
-    dt, device = q.dtype, q.get_device()
+    dt, device, shape, kv = q.dtype, q.get_device(), q.shape, k.shape
     if dt not in _HALF or device < 0:
         raise ValueError("q must be a bfloat16 or float16 CUDA tensor")
-    if q.dim() != 4 or k.dim() != 4 or v.shape != k.shape or q.shape[0] != k.shape[0] or q.shape[3] != k.shape[3]:
+    if len(shape) != 4 or len(kv) != 4 or v.shape != kv or shape[0] != kv[0] or shape[3] != kv[3]:
         raise ValueError("q must be batch x queries x heads x head, k and v batch x keys x kv_heads x head")
     if k.dtype is not dt or v.dtype is not dt or k.get_device() != device or v.get_device() != device:
         raise ValueError("k and v must be of q's type and on its device")
-    head = q.shape[3]
+    head, heads, kv_heads = shape[3], shape[2], kv[2]
     if head % 8 or not 8 <= head <= 128:
         raise ValueError("a head must have 8 to 128 elements, a multiple of 8")
-    if k.shape[2] == 0 and q.shape[2] or k.shape[2] and q.shape[2] % k.shape[2]:
+    if heads % kv_heads if kv_heads else heads:
         raise ValueError("kv_heads must divide heads")
-    if key_lengths is not None and (key_lengths.shape != (q.shape[0],) or key_lengths.get_device() != device
-                                    or key_lengths.dtype not in (torch.int32, torch.int64)):
+    if key_lengths is not None and (key_lengths.shape != (shape[0],) or key_lengths.get_device() != device
+                                    or key_lengths.dtype not in _POSITION_BYTES):
         raise ValueError("key_lengths must be int32 or int64, one per sequence, on q's device")
     if scale is None:
         scale = head ** -0.5
-    if not (scale > 0.0 and math.isfinite(scale)):
+    elif not 0.0 < scale < math.inf:
         raise ValueError("scale must be positive")
     return device, scale
 
 
-def _attention_desc(q, k, v, o, key_lengths, scale, grad_o=None, dq=None, dk=None, dv=None):
+def _attention_desc(q, k, v, o, key_lengths, scale, backward=()):
     b, lq, h, d = q.shape
-    strides = []
-    for t in (q, k, v, o, grad_o, dq, dk, dv):
-        strides += _NO_STRIDES if t is None else t.stride()[:3]
-    packed = _ATTN.pack(b, lq, k.shape[1], h, k.shape[2], d, *strides,
-                        0 if key_lengths is None else key_lengths.data_ptr(),
-                        0 if key_lengths is None else key_lengths.element_size(), _DTYPE[q.dtype], scale, 0)
-    return N.prm_attention_desc.from_buffer_copy(packed)
+    kv = k.shape
+    if key_lengths is None:
+        lengths, length_bytes = 0, 0
+    else:
+        lengths, length_bytes = key_lengths.data_ptr(), key_lengths.element_size()
+    if backward:
+        do, dq, dk, dv = backward
+        later = (*do.stride()[:3], *dq.stride()[:3], *dk.stride()[:3], *dv.stride()[:3])
+    else:
+        later = _NO_STRIDES
+    return N.prm_attention_desc.from_buffer_copy(
+        _ATTN.pack(b, lq, kv[1], h, kv[2], d, *q.stride()[:3], *k.stride()[:3], *v.stride()[:3], *o.stride()[:3],
+                   *later, lengths, length_bytes, _DTYPE[q.dtype], scale, 0))
 
 
 @functools.lru_cache(maxsize=256)
@@ -457,9 +469,9 @@ def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, key_lengt
     if key_lengths is not None and not key_lengths.is_contiguous():
         key_lengths = key_lengths.contiguous()
     o = torch.empty(q.shape, dtype=q.dtype, device=q.device) if out is None else out
-    lse = q.new_empty((b, h, lq), dtype=torch.float32) if save else None
+    lse = torch.empty((b, h, lq), dtype=torch.float32, device=q.device) if save else None
     n_ws = _attention_sizes(b, lq, lk, h, hkv, d)[0]
-    ws = q.new_empty(n_ws, dtype=torch.uint8) if n_ws else None
+    ws = torch.empty(n_ws, dtype=torch.uint8, device=q.device) if n_ws else None
     rc = N.load().prm_attention_forward(_attention_desc(q, k, v, o, key_lengths, scale), q.data_ptr(), k.data_ptr(),
                                         v.data_ptr(), o.data_ptr(), _ptr(lse), _ptr(ws), n_ws, _raw_stream(device))
     if rc:
@@ -494,16 +506,19 @@ def cross_attention_backward(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
     if _is_elsewhere(device, stream):
         with _elsewhere(device, stream, do, q, k, v, o, lse, key_lengths, *(grads or ())):
             return cross_attention_backward(do, q, k, v, o, saved, key_lengths, scale, grads)
-    do, q, k, v, o = (_laid_out(t) for t in (do, q, k, v, o))
+    do, q, k, v, o = _laid_out(do), _laid_out(q), _laid_out(k), _laid_out(v), _laid_out(o)
     if key_lengths is not None and not key_lengths.is_contiguous():
         key_lengths = key_lengths.contiguous()
     if grads is None:
-        dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
+        dt, device_ = q.dtype, q.device
+        dq = torch.empty(q.shape, dtype=dt, device=device_)
+        dk = torch.empty(k.shape, dtype=dt, device=device_)
+        dv = torch.empty(k.shape, dtype=dt, device=device_)
     else:
         dq, dk, dv = grads
     n_ws = _attention_sizes(b, lq, lk, h, hkv, d)[1]
-    ws = q.new_empty(n_ws, dtype=torch.uint8)
-    desc = _attention_desc(q, k, v, o, key_lengths, scale, do, dq, dk, dv)
+    ws = torch.empty(n_ws, dtype=torch.uint8, device=q.device)
+    desc = _attention_desc(q, k, v, o, key_lengths, scale, (do, dq, dk, dv))
     rc = N.load().prm_attention_backward(desc, do.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
                                          lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(),
                                          n_ws, _raw_stream(device))

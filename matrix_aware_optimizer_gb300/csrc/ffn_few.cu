@@ -45,7 +45,7 @@ struct FewParams {
 constexpr int FEW_GLU = 0, FEW_DOWN = 1, FEW_LINEAR = 2;
 
 template <typename T, int NT, int USE, int ACT>
-__global__ void __launch_bounds__(FEW_THREADS, NT <= 4 ? 2 : 1) ffn_few_kernel(const __grid_constant__ FewParams p) {
+__global__ void __launch_bounds__(FEW_THREADS, USE == FEW_LINEAR && NT == 1 ? 4 : NT <= 4 ? 2 : 1) ffn_few_kernel(const __grid_constant__ FewParams p) {
   constexpr bool GLU = USE == FEW_GLU;
   __shared__ float part[FEW_WARPS][NT * FEW_ROWS];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -71,7 +71,8 @@ __global__ void __launch_bounds__(FEW_THREADS, NT <= 4 ? 2 : 1) ffn_few_kernel(c
     for (int r = 0; r < FEW_ROWS; ++r) acc[t][r] = 0;
   const int step = p.split * 256;
   const int k0 = (piece * 32 + lane) * 8;
-  constexpr int AHEAD = NT == 1 ? 4 : 2;  // steps whose weights are in flight
+  // steps whose weights are in flight
+  constexpr int AHEAD = NT == 1 && USE != FEW_LINEAR ? 4 : 2;
   uint4 wv[AHEAD][FEW_ROWS];
   auto load_w = [&](int k) {
 #pragma unroll

@@ -168,9 +168,11 @@ struct LinearSizes {
 LinearSizes linear_sizes(int64_t T, int64_t n, int64_t k) {
   LinearSizes s{};
   if (T == 0) return s;
-  s.y = split_last_wave(T, n, k);
-  s.fwd_counters = partial_bytes(s.y);
-  s.fwd = s.fwd_counters + round_up(counter_bytes(s.y), 256);
+  if (!linear_few(T, n, k)) {
+    s.y = split_last_wave(T, n, k);
+    s.fwd_counters = partial_bytes(s.y);
+    s.fwd = s.fwd_counters + round_up(counter_bytes(s.y), 256);
+  }
   // rows in blocks: about eight CTAs per SM over all columns, 32 rows at least
   const int64_t strips = (n + DG_COLS - 1) / DG_COLS;
   const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((T + 31) / 32, 8 * 152 / strips));
