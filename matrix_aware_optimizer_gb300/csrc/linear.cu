@@ -15,7 +15,7 @@
 // |g act''(g) / act'(g)| of a step, less than dg's own rounding for all but the
 // few elements around a root of act'.
 #include "block_gemm.cuh"
-#include "prm_attention.h"
+#include "linear.cuh"
 
 namespace prm {
 namespace {
@@ -155,6 +155,8 @@ GradSplit grad_split(int64_t T, int64_t n, int64_t k, bool need_dx) {
   return {parts_of(tiles, n), parts_of(tiles, T)};
 }
 
+constexpr int LINEAR_SMS = 152;  // what plans are made for: one GB300
+
 struct LinearSizes {
   size_t fwd_counters, fwd;
   size_t sums_at, dx_at, dw_at, counters_at, bwd;  // dg at 0
@@ -163,12 +165,15 @@ struct LinearSizes {
   int64_t block_rows;
   Split y;
   GradSplit grads;
+  SkinnyPlan y_skinny, dx_skinny;
 };
 
 LinearSizes linear_sizes(int64_t T, int64_t n, int64_t k) {
   LinearSizes s{};
   if (T == 0) return s;
-  if (!linear_few(T, n, k)) {
+  s.y_skinny = skinny_plan(T, n, k, LINEAR_SMS);
+  s.dx_skinny = skinny_plan(T, k, n, LINEAR_SMS);
+  if (!linear_few(T, n, k) && !s.y_skinny.use) {
     s.y = split_last_wave(T, n, k);
     s.fwd_counters = partial_bytes(s.y);
     s.fwd = s.fwd_counters + round_up(counter_bytes(s.y), 256);
@@ -178,7 +183,7 @@ LinearSizes linear_sizes(int64_t T, int64_t n, int64_t k) {
   const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((T + 31) / 32, 8 * 152 / strips));
   s.block_rows = (T + blocks - 1) / blocks;
   s.row_blocks = static_cast<int>((T + s.block_rows - 1) / s.block_rows);
-  s.grads = grad_split(T, n, k, true);
+  s.grads = grad_split(T, n, k, !s.dx_skinny.use);
   size_t at = round_up(static_cast<size_t>(T) * n * 2, 256);
   s.sums_at = at;
   at += round_up(static_cast<size_t>(s.row_blocks) * n * sizeof(float), 256);
@@ -191,7 +196,7 @@ LinearSizes linear_sizes(int64_t T, int64_t n, int64_t k) {
     }
     return here;
   };
-  s.dx_at = parts(tiles_of(T, k, BN), s.grads.dx, &s.dx_counters);
+  s.dx_at = parts(tiles_of(T, k, BN), s.dx_skinny.use ? 1 : s.grads.dx, &s.dx_counters);
   s.dw_at = parts(tiles_of(n, k, BN), s.grads.dw, &s.dw_counters);
   s.counters_at = at;
   s.bwd = round_up(at + static_cast<size_t>(s.dx_counters + s.dw_counters) * 4, 256);
@@ -251,6 +256,11 @@ extern "C" int prm_linear_forward(const void* x, int64_t ldx, const void* weight
     const LinearFew f{x, ldx, weight, bias, residual, ld_residual, y, pre, static_cast<int>(tokens),
                       static_cast<int>(n), static_cast<int>(k), wide};
     return linear_few_forward(f, act, dtype, st) == cudaSuccess ? PRM_OK : PRM_ERR_CUDA;
+  }
+  if (sz.y_skinny.use) {
+    const SkinnyCall call{weight, x, ldx, tokens, n, k, 0, bias, residual, ld_residual, y, pre, act, dtype, wide,
+                          dev->d_err};
+    return skinny_product(sz.y_skinny, call, st) == cudaSuccess ? PRM_OK : PRM_ERR_CUDA;
   }
   char* ws = static_cast<char*>(workspace);
   BlockGemmParams p{};
@@ -343,7 +353,7 @@ extern "C" int prm_linear_backward(const void* dy, int64_t lddy, int dy_dtype, c
       s.arrived = counters;
     };
     auto add_dx = [&] {
-      if (dx == nullptr) return;
+      if (dx == nullptr || sz.dx_skinny.use) return;
       GemmSegment s{};
       ok = ok && encode(&s.a[0], dg, dtype, tokens, n, lddg, MAP_ROWS) &&
            encode(&s.b[0], weight, dtype, n, k, k, MAP_COLS) && encode(&s.out[0], dx, dtype, tokens, k, k, MAP_STORE);
@@ -362,7 +372,13 @@ extern "C" int prm_linear_backward(const void* dy, int64_t lddy, int dy_dtype, c
     if (n >= tokens) add_dx();
     add_dw();
     if (n < tokens) add_dx();
-    if (!ok || launch<EPI_STORE>(q, dtype, dev->num_sms, st) != cudaSuccess) return PRM_ERR_CUDA;
+    if (!ok) return PRM_ERR_CUDA;
+    if (dx != nullptr && sz.dx_skinny.use) {
+      const SkinnyCall call{weight, dg, lddg, tokens, k, n, 1, nullptr, nullptr, 0, dx, nullptr, ACT_NONE, dtype, false,
+                            dev->d_err};
+      if (skinny_product(sz.dx_skinny, call, st) != cudaSuccess) return PRM_ERR_CUDA;
+    }
+    if (q.nseg > 0 && launch<EPI_STORE>(q, dtype, dev->num_sms, st) != cudaSuccess) return PRM_ERR_CUDA;
   }
   if (dbias != nullptr &&
       launch_dependent(linear_db_kernel, dim3(static_cast<unsigned>((n + 31) / 32)), dim3(256), 0, st, sums, dbias,

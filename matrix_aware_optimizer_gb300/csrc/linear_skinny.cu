@@ -1,0 +1,362 @@
+// Products of the linear layer with few tokens: D^T = A B^T with the features
+// as the tensor cores' rows (128 to a CTA) and all tokens, up to 256, as their
+// columns, in steps of 16. So a tile is full however few tokens there are, each
+// weight is read once for every 256 of them, and the sum over K is split over
+// the CTAs of a cluster, which add their parts through distributed shared
+// memory, in order, each for its share of the tokens.
+//
+// Used where the 256 x 256 tiles of block_gemm.cuh would leave most SMs idle:
+// 777 tokens, 8192 -> 2048 bf16 with an fp32 residual 53 us there; 64 tokens,
+// 2048 -> 6144 20 us. Per 64 of K a CTA loads 16 KB of weights and 128 bytes
+// per token for 2 cycles of products per token: bound by these loads, which is
+// why many tokens go to the larger tiles.
+#include <algorithm>
+#include <type_traits>
+
+#include "linear.cuh"
+
+namespace prm {
+namespace {
+
+constexpr int SK_ROWS = 128;       // features of a CTA
+constexpr int SK_K = 64;           // K of a stage
+constexpr int SK_MAX_COLS = 256;   // tokens of a CTA
+constexpr int SK_THREADS = 192;    // warp 0 loads, warp 1 issues products, 2 - 5 take rows
+constexpr uint32_t SK_A = SK_ROWS * SK_K * 2;
+constexpr size_t SK_SMEM = 232448 - 2048;  // (each of two CTAs on an SM takes 1 KB more)
+constexpr size_t SK_REST = 1024 + 256;
+constexpr uint64_t SK_WAIT_NS = 2000000000ull;
+
+struct SkinnyParams {
+  CUtensorMap a, b;
+  int rows, tokens, k_blocks;
+  int cols;       // tokens of a CTA, a multiple of 16
+  int stages;
+  int a_mn;       // A stored [K][rows]
+  uint32_t tmem_cols;
+  const float* bias;
+  const void* residual;
+  int64_t ld_residual;
+  void* y;        // tokens x rows
+  void* pre;      // act's argument, or NULL
+  int* err;
+};
+
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* tm, uint64_t* bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+          smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(smem_u32(bar)), "r"(x), "r"(y)
+      : "memory");
+}
+
+// Four neighbouring features of a token: the residual, and the result from
+// their sums.
+template <typename T, bool WIDE>
+__device__ __forceinline__ float4 skinny_residual(const SkinnyParams& p, int token, int row) {
+  if (p.residual == nullptr) return make_float4(0.f, 0.f, 0.f, 0.f);
+  const int64_t from = token * p.ld_residual + row;
+  if (WIDE) return __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(p.residual) + from));
+  const uint2 r = __ldcs(reinterpret_cast<const uint2*>(static_cast<const T*>(p.residual) + from));
+  const float2 a = unpack2<T>(r.x), b = unpack2<T>(r.y);
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+template <typename T, int ACT, bool WIDE>
+__device__ __forceinline__ void skinny_out(const SkinnyParams& p, int token, int row, float4 v, const float4& bias,
+                                           const float4& res) {
+  const int64_t at = static_cast<int64_t>(token) * p.rows + row;
+  v.x += bias.x, v.y += bias.y, v.z += bias.z, v.w += bias.w;
+  if (ACT != ACT_NONE && p.pre != nullptr)
+    *reinterpret_cast<uint2*>(static_cast<T*>(p.pre) + at) = make_uint2(pack2<T>(v.x, v.y), pack2<T>(v.z, v.w));
+  v = make_float4(ffn_act<ACT>(v.x) + res.x, ffn_act<ACT>(v.y) + res.y, ffn_act<ACT>(v.z) + res.z,
+                  ffn_act<ACT>(v.w) + res.w);
+  if (WIDE) *reinterpret_cast<float4*>(static_cast<float*>(p.y) + at) = v;
+  else *reinterpret_cast<uint2*>(static_cast<T*>(p.y) + at) = make_uint2(pack2<T>(v.x, v.y), pack2<T>(v.z, v.w));
+}
+
+template <typename T, int ACT, bool WIDE>
+__global__ void __launch_bounds__(SK_THREADS, 1) skinny_kernel(const __grid_constant__ SkinnyParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t b_bytes = static_cast<uint32_t>(p.cols) * SK_K * 2;
+  uint8_t* sA = smem;
+  uint8_t* sB = smem + p.stages * SK_A;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sB + p.stages * b_bytes);
+  uint64_t* empty = full + p.stages;
+  uint64_t* done = empty + p.stages;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int parts = static_cast<int>(cluster_size()), part = static_cast<int>(cluster_ctarank());
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_holder, p.tmem_cols);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_holder;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int row0 = blockIdx.x * SK_ROWS, token0 = blockIdx.y * p.cols;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(p.k_blocks) * part / parts);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(p.k_blocks) * (part + 1) / parts);
+
+  bool ok = true;
+  if (warp == 0) {
+    if (lane == 0) {
+      int s = 0;
+      uint32_t phase = 0, issued = 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!wait_bounded(&empty[s], phase ^ 1u, abort_flag, p.err, SK_WAIT_NS)) {
+          ok = false;
+          break;
+        }
+        mbar_arrive_expect_tx(&full[s], SK_A + b_bytes);
+        uint8_t* a = sA + s * SK_A;
+        if (p.a_mn) {
+          tma_load_2d(a, &p.a, &full[s], row0, kb * SK_K);
+          tma_load_2d(a + SK_A / 2, &p.a, &full[s], row0 + 64, kb * SK_K);
+        } else {
+          tma_load_2d(a, &p.a, &full[s], kb * SK_K, row0);
+        }
+        tma_load_2d(sB + s * b_bytes, &p.b, &full[s], kb * SK_K, token0);
+        ++issued;
+        if (++s == p.stages) {
+          s = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!ok)  // every load in flight lands before the CTA exits
+        for (uint32_t q = 0; q < static_cast<uint32_t>(p.stages) && q < issued; ++q)
+          wait_drain(&full[q], ((issued - 1 - q) / p.stages) & 1u, 50000000ull);
+    }
+  } else if (warp == 1) {
+    constexpr bool FP16 = !std::is_same<T, __nv_bfloat16>::value;
+    const uint32_t idesc = idesc_f16kind_f32(SK_ROWS, 0, p.a_mn, false, FP16) | (static_cast<uint32_t>(p.cols) >> 3) << 17;
+    int s = 0;
+    uint32_t phase = 0;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      ok = __all_sync(0xffffffffu, wait_bounded(&full[s], phase, abort_flag, p.err, SK_WAIT_NS));
+      if (!ok) break;
+      tc_fence_after_sync();
+      if (elect_one()) {
+        const uint32_t a = smem_u32(sA + s * SK_A);
+        const uint64_t da = p.a_mn ? smem_desc_sw128(a, SK_A / 2, 1024) : smem_desc_sw128(a, 16, 1024);
+        const uint64_t db = smem_desc_sw128(smem_u32(sB + s * b_bytes), 16, 1024);
+        const uint32_t step = p.a_mn ? 2048 : 32;
+#pragma unroll
+        for (int k = 0; k < SK_K / 16; ++k)
+          umma_bf16(tmem, desc_at(da, k * step), desc_at(db, k * 32), idesc, kb > kb0 || k > 0 ? 1u : 0u);
+        umma_commit(&empty[s]);
+        if (kb + 1 == kb1) umma_commit(done);
+      }
+      __syncwarp();
+      if (++s == p.stages) {
+        s = 0;
+        phase ^= 1u;
+      }
+    }
+    if (!ok && kb1 > kb0) {
+      if (elect_one()) umma_commit(done);
+      wait_drain(done, 0, 50000000ull);
+    }
+  } else {
+    ok = __all_sync(0xffffffffu, wait_bounded(done, 0, abort_flag, p.err, SK_WAIT_NS));
+    tc_fence_after_sync();
+  }
+
+  // The sums go to where the stages were (every product has read its tiles), [token][feature]; then each CTA of the
+  // cluster adds the parts of its share of the tokens, four features to a thread.
+  float* mine = reinterpret_cast<float*>(smem);
+  if (warp >= 2 && ok) {
+    const int lane_row = (warp & 3) * 32 + lane;  // warps 2 - 5: each a quarter of tensor memory
+    const uint32_t t_row = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    for (int c = 0; c < p.cols; c += 32) {
+      float v[32];
+      tmem_load_32cols(t_row + c, v);
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (c + i < p.cols) mine[(c + i) * SK_ROWS + lane_row] = v[i];
+    }
+  }
+  __syncthreads();
+  if (parts > 1) cluster_sync_all();
+  if (warp >= 2) {
+    const int first = p.cols * part / parts, last = min(p.cols * (part + 1) / parts, p.tokens - token0);
+    const int q4 = (threadIdx.x & 31) * 4, row = row0 + q4;
+    if (row < p.rows) {  // (rows are a multiple of 8)
+      const float4 bias = p.bias != nullptr ? *reinterpret_cast<const float4*>(p.bias + row) : make_float4(0.f, 0.f, 0.f, 0.f);
+      const uint32_t base = smem_u32(mine) + q4 * 4;
+      constexpr int AHEAD = 4;  // tokens of a thread under way
+      for (int c = first + warp - 2; c < last; c += 4 * AHEAD) {
+        float4 v[AHEAD], res[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+          v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          res[i] = skinny_residual<T, WIDE>(p, token0 + min(c + 4 * i, last - 1), row);
+        }
+#pragma unroll 4
+        for (int q = 0; q < parts; ++q) {
+          const uint32_t from = mapa_shared(base, q);
+#pragma unroll
+          for (int i = 0; i < AHEAD; ++i) {
+            const int token = min(c + 4 * i, last - 1);
+            const float4 u = ld_cluster_f32x4(from + token * (SK_ROWS * 4));
+            v[i].x += u.x, v[i].y += u.y, v[i].z += u.z, v[i].w += u.w;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+          if (c + 4 * i < last) skinny_out<T, ACT, WIDE>(p, token0 + c + 4 * i, row, v[i], bias, res[i]);
+      }
+    }
+  }
+  if (parts > 1) {
+    __syncthreads();
+    cluster_sync_all();  // no CTA leaves while another reads its part
+  }
+  __syncwarp();
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  if (warp == 1) tmem_dealloc(tmem, p.tmem_cols);
+}
+
+template <typename T, int ACT, bool WIDE>
+cudaError_t launch(const SkinnyParams& p, const SkinnyPlan& s, cudaStream_t stream) {
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(ready.load(std::memory_order_acquire) >> dev & 1)) {
+    e = cudaFuncSetAttribute(skinny_kernel<T, ACT, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(SK_SMEM));
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready.fetch_or(uint64_t(1) << dev, std::memory_order_release);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((p.rows + SK_ROWS - 1) / SK_ROWS),
+                     static_cast<unsigned>((p.tokens + p.cols - 1) / p.cols), static_cast<unsigned>(s.parts));
+  cfg.blockDim = dim3(SK_THREADS);
+  cfg.dynamicSmemBytes = p.stages * (SK_A + static_cast<size_t>(p.cols) * SK_K * 2) + SK_REST;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 1;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = static_cast<unsigned>(s.parts);
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, skinny_kernel<T, ACT, WIDE>, p);
+}
+
+template <typename T, int ACT>
+cudaError_t launch(const SkinnyParams& p, const SkinnyPlan& s, bool wide, cudaStream_t stream) {
+  return wide ? launch<T, ACT, true>(p, s, stream) : launch<T, ACT, false>(p, s, stream);
+}
+
+template <typename T>
+cudaError_t launch(const SkinnyParams& p, const SkinnyPlan& s, int act, bool wide, cudaStream_t stream) {
+  if (act == PRM_ACT_SILU) return launch<T, PRM_ACT_SILU>(p, s, wide, stream);
+  if (act == PRM_ACT_GELU) return launch<T, PRM_ACT_GELU>(p, s, wide, stream);
+  if (act == PRM_ACT_GELU_TANH) return launch<T, PRM_ACT_GELU_TANH>(p, s, wide, stream);
+  return launch<T, ACT_NONE>(p, s, wide, stream);
+}
+
+}  // namespace
+
+// Time of a product in cycles, for either kernel: rounds of clusters (or of
+// CTA pairs) times the slices of K of one, and what a launch costs besides. A
+// slice costs a CTA its loads, 64 bytes a cycle, and a pair 650 cycles; the
+// rest is fitted to what was measured (64 tokens 2048 -> 6144: 10.8 us, 256
+// tokens 8192 -> 2048: 19, 777 tokens 8192 -> 2048: 26; with pairs 20, 30, 41).
+SkinnyPlan skinny_plan(int64_t tokens, int64_t rows, int64_t k, int num_sms) {
+  // Clusters of one to eight CTAs that run at once, one CTA or (with half of the shared memory) two to an SM: not all
+  // SMs of a GPC fit a cluster's size. With one cluster more than that a second round begins: 48 clusters of three
+  // took 54 us where 46 fit.
+  static constexpr int FIT[2][8] = {{152, 76, 46, 36, 28, 23, 15, 15}, {304, 152, 97, 74, 58, 46, 38, 36}};
+  SkinnyPlan s{};
+  const int64_t kb = (k + SK_K - 1) / SK_K;
+  const int64_t fewest = (tokens + SK_MAX_COLS - 1) / SK_MAX_COLS;
+  int64_t best = 0;
+  for (int64_t col_tiles = fewest; col_tiles <= fewest + 2; ++col_tiles) {
+    const int64_t cols = ((tokens + col_tiles - 1) / col_tiles + 15) / 16 * 16;
+    const int64_t units = (rows + SK_ROWS - 1) / SK_ROWS * ((tokens + cols - 1) / cols);
+    const bool two = cols <= 128;
+    for (int parts = 1; parts <= 8 && (parts == 1 || kb / parts >= 4); ++parts) {
+      const int64_t rounds = (units + FIT[two][parts - 1] - 1) / FIT[two][parts - 1];
+      const int64_t share = two && units * parts > num_sms ? 2 : 1;  // of an SM's loads
+      const int64_t cycles = rounds * ((kb + parts - 1) / parts * (256 + 2 * cols) * share + 3000 + 8 * cols) + 6000 +
+                             (parts > 1 ? 2000 : 0);
+      if (best == 0 || cycles < best) {
+        best = cycles;
+        s.cols = static_cast<int>(cols);
+        s.parts = parts;
+        s.two = two;
+      }
+    }
+  }
+  const int64_t tiles = (tokens + 255) / 256 * ((rows + 255) / 256);
+  const int64_t pairs = num_sms / 2;
+  const int64_t split = std::max<int64_t>(1, std::min<int64_t>({pairs / tiles, kb / 4, 8}));
+  const int64_t rounds = (tiles + pairs - 1) / pairs;
+  s.use = best < rounds * ((kb + split - 1) / split) * 650 + 28000 && rows <= (int64_t(1) << 30) &&
+          (tokens + s.cols - 1) / s.cols <= 65535;
+  return s;
+}
+
+cudaError_t skinny_product(const SkinnyPlan& s, const SkinnyCall& c, cudaStream_t stream) {
+  SkinnyParams p{};
+  p.rows = static_cast<int>(c.rows);
+  p.tokens = static_cast<int>(c.tokens);
+  p.k_blocks = static_cast<int>((c.k + SK_K - 1) / SK_K);
+  p.cols = s.cols;
+  const size_t stage = SK_A + static_cast<size_t>(s.cols) * SK_K * 2;
+  // no more than a part of the sum needs: with less shared memory the next kernel's CTAs set up beside these
+  p.stages = static_cast<int>(std::min<size_t>({size_t(10), (SK_SMEM / (s.two ? 2 : 1) - SK_REST) / stage,
+                                                static_cast<size_t>((p.k_blocks + s.parts - 1) / s.parts)}));
+  // the sums take the stages' place
+  while (p.stages * stage < static_cast<size_t>(s.cols) * SK_ROWS * 4) ++p.stages;
+  p.a_mn = c.a_mn;
+  p.tmem_cols = 32;
+  while (p.tmem_cols < static_cast<uint32_t>(s.cols)) p.tmem_cols *= 2;
+  p.bias = c.bias;
+  p.residual = c.residual;
+  p.ld_residual = c.ld_residual;
+  p.y = c.y;
+  p.pre = c.pre;
+  p.err = c.err;
+  const bool maps = c.a_mn ? encode_box(&p.a, c.a, c.dtype, c.k, c.rows, c.rows, 64)
+                           : encode_box(&p.a, c.a, c.dtype, c.rows, c.k, c.k, SK_ROWS);
+  if (!maps || !encode_box(&p.b, c.b, c.dtype, c.tokens, c.k, c.ldb, s.cols)) return cudaErrorInvalidValue;
+  return c.dtype == PRM_BF16 ? launch<__nv_bfloat16>(p, s, c.act, c.wide, stream)
+                             : launch<__half>(p, s, c.act, c.wide, stream);
+}
+
+}  // namespace prm
