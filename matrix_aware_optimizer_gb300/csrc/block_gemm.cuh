@@ -77,6 +77,7 @@ struct BlockGemmParams {
   const float* bias;    // LINEAR: N, or NULL
   const void* residual; // LINEAR: M x N with row pitch ld_residual, or NULL
   int64_t ld_residual;
+  void* y;              // LINEAR: M x N, contiguous
   int keep;             // LINEAR: product + bias is wanted
   uint32_t* zero;       // counters to clear for the next launch
   int zero_count;
@@ -286,24 +287,34 @@ __device__ __forceinline__ void store_box(const GemmSegment& sg, int i0, int j0,
   }
 }
 
-// A lane's row of the residual, 32 columns from j0; zeros outside.
+// A 32 x 32 box of the residual from (i0, j0), zeros outside, as a warp reads
+// it whole cache lines at a time: lanes along a row, rows one after another.
+// (With a row to a lane, 8192 x 6144 with an fp32 residual took 280 us.)
 template <int EPI>
-struct ResidualRow {
-  static constexpr int BYTES = EPI == EPI_LINEAR32 ? 4 : 2, VECTORS = EPI == EPI_LINEAR32 ? 8 : 4;
+struct ResidualBox {
+  static constexpr bool WIDE = EPI == EPI_LINEAR32;
+  static constexpr int VECTORS = WIDE ? 8 : 4;         // of 16 bytes, in each lane
+  static constexpr int UNITS = WIDE ? 8 : 4;           // of a row
+  static constexpr int ELEMENTS = 32 / UNITS;          // of a unit
   uint4 v[VECTORS];
-  __device__ __forceinline__ void load(const BlockGemmParams& p, const GemmSegment& sg, int row, int j0) {
-    const char* src = static_cast<const char*>(p.residual) + (row * p.ld_residual + j0) * BYTES;
+  static __device__ __forceinline__ int row(int lane, int k) { return lane / UNITS + k * (32 / UNITS); }
+  static __device__ __forceinline__ int col(int lane) { return lane % UNITS * ELEMENTS; }
+  __device__ __forceinline__ void load(const BlockGemmParams& p, const GemmSegment& sg, int i0, int j0, int lane) {
+    if (p.residual == nullptr) return;
+    const int j = j0 + col(lane);
+    const char* src = static_cast<const char*>(p.residual) + (i0 * p.ld_residual + j) * (WIDE ? 4 : 2);
 #pragma unroll
     for (int k = 0; k < VECTORS; ++k)
-      v[k] = p.residual != nullptr && row < sg.M && j0 + k * (16 / BYTES) < sg.N
-                 ? __ldcs(reinterpret_cast<const uint4*>(src) + k)
+      v[k] = i0 + row(lane, k) < sg.M && j < sg.N
+                 ? __ldcs(reinterpret_cast<const uint4*>(src + row(lane, k) * p.ld_residual * (WIDE ? 4 : 2)))
                  : make_uint4(0, 0, 0, 0);
   }
 };
 
 template <int EPI, typename T, int ACT>
 __device__ __forceinline__ void linear_box(const BlockGemmParams& p, const GemmSegment& sg, int i0, int j0,
-                                           float (&v)[32], const ResidualRow<EPI>& res, uint8_t* stage, int lane) {
+                                           float (&v)[32], const ResidualBox<EPI>& res, uint8_t* stage, int lane) {
+  using Box = ResidualBox<EPI>;
   if (i0 >= sg.M || j0 >= sg.N) return;
   if (p.bias != nullptr) {
 #pragma unroll
@@ -318,13 +329,14 @@ __device__ __forceinline__ void linear_box(const BlockGemmParams& p, const GemmS
   }
   if (lane == 0) bulk_wait_group_read<0>();
   __syncwarp();
+  const bool joined = EPI == EPI_LINEAR32 || p.residual != nullptr;
   if (ACT != ACT_NONE && p.keep) {
     uint32_t w[16];
 #pragma unroll
     for (int k = 0; k < 16; ++k) w[k] = pack2<T>(v[2 * k], v[2 * k + 1]);
-    uint8_t* box = EPI == EPI_LINEAR32 ? stage : stage + EPI_BUF_BYTES;
+    uint8_t* box = joined ? stage : stage + EPI_BUF_BYTES;
     stage_box(box, lane, w);
-    if (EPI == EPI_LINEAR32) {  // an fp32 box takes all of the warp's staging memory
+    if (joined) {  // the sums take all of the warp's staging memory
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
@@ -337,30 +349,48 @@ __device__ __forceinline__ void linear_box(const BlockGemmParams& p, const GemmS
   }
 #pragma unroll
   for (int k = 0; k < 32; ++k) v[k] = ffn_act<ACT>(v[k]);
-  if constexpr (EPI == EPI_LINEAR32) {
+  if (joined) {
+    // act(g) in fp32 through shared memory (16-byte units swizzled by the row), to the residual's order and out
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float4 r = make_float4(v[4 * k] + __uint_as_float(res.v[k].x), v[4 * k + 1] + __uint_as_float(res.v[k].y),
-                                   v[4 * k + 2] + __uint_as_float(res.v[k].z),
-                                   v[4 * k + 3] + __uint_as_float(res.v[k].w));
-      // 128-byte rows in the 128-byte swizzle of the fp32 map
-      *reinterpret_cast<float4*>(stage + lane * 128 + ((k ^ (lane & 7)) << 4)) = r;
-    }
-  } else {
-    uint32_t w[16];
+    for (int k = 0; k < 8; ++k)
+      *reinterpret_cast<float4*>(stage + lane * 128 + ((k ^ (lane & 7)) << 4)) =
+          make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+    __syncwarp();
+    const int j = j0 + Box::col(lane);
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const uint4 q = res.v[k >> 2];
-      const float2 r = unpack2<T>((k & 3) == 0 ? q.x : (k & 3) == 1 ? q.y : (k & 3) == 2 ? q.z : q.w);
-      w[k] = pack2<T>(v[2 * k] + r.x, v[2 * k + 1] + r.y);
+    for (int k = 0; k < Box::VECTORS; ++k) {
+      const int r = Box::row(lane, k), unit = lane % Box::UNITS;
+      const uint8_t* from = stage + r * 128;
+      const uint4 q = p.residual != nullptr ? res.v[k] : make_uint4(0, 0, 0, 0);
+      uint4 out;
+      if constexpr (Box::WIDE) {
+        const float4 a = *reinterpret_cast<const float4*>(from + ((unit ^ (r & 7)) << 4));
+        out = make_uint4(__float_as_uint(a.x + __uint_as_float(q.x)), __float_as_uint(a.y + __uint_as_float(q.y)),
+                         __float_as_uint(a.z + __uint_as_float(q.z)), __float_as_uint(a.w + __uint_as_float(q.w)));
+      } else {
+        const float4 a = *reinterpret_cast<const float4*>(from + (((2 * unit) ^ (r & 7)) << 4));
+        const float4 b = *reinterpret_cast<const float4*>(from + (((2 * unit + 1) ^ (r & 7)) << 4));
+        const float2 q0 = unpack2<T>(q.x), q1 = unpack2<T>(q.y), q2 = unpack2<T>(q.z), q3 = unpack2<T>(q.w);
+        out = make_uint4(pack2<T>(a.x + q0.x, a.y + q0.y), pack2<T>(a.z + q1.x, a.w + q1.y),
+                         pack2<T>(b.x + q2.x, b.y + q2.y), pack2<T>(b.z + q3.x, b.w + q3.y));
+      }
+      if (i0 + r < sg.M && j < sg.N)
+        __stcs(reinterpret_cast<uint4*>(static_cast<char*>(p.y) +
+                                        (static_cast<int64_t>(i0 + r) * sg.N + j) * (Box::WIDE ? 4 : 2)),
+               out);
     }
-    stage_box(stage, lane, w);
+    __syncwarp();
+    return;
   }
+  uint32_t w[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) w[k] = pack2<T>(v[2 * k], v[2 * k + 1]);
+  stage_box(stage, lane, w);
   fence_proxy_async_smem();
   __syncwarp();
   if (lane == 0) {
     tma_store_2d(&sg.out[0], stage, j0, i0);
-    if (EPI == EPI_LINEAR && ACT != ACT_NONE && p.keep) tma_store_2d(&sg.out[1], stage + EPI_BUF_BYTES, j0, i0);
+    if (ACT != ACT_NONE && p.keep) tma_store_2d(&sg.out[1], stage + EPI_BUF_BYTES, j0, i0);
     bulk_commit_group();
   }
 }
@@ -547,9 +577,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       if constexpr (EPI == EPI_DGLU) {
         if (i0 < sg.M && jh < sg.N) gu_load(p, i0, jh, sg.N, lane, raw[0]);
       }
-      ResidualRow<EPI> res[2];
+      ResidualBox<EPI> res;
       if constexpr (epi_linear(EPI)) {
-        if (it.split_tile < 0) res[0].load(p, sg, i0 + lane, jh);
+        if (it.split_tile < 0) res.load(p, sg, i0, jh, lane);
       }
       const bool got = wait_bounded(&tfull_bar[acc], acc_phase, abort_flag, p.err, WAIT_LIMIT_NS);
       if (!__all_sync(0xffffffffu, got)) break;
@@ -578,14 +608,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           float v[32];
-          if constexpr (epi_linear(EPI)) {
-            if (q < 3) res[(q + 1) & 1].load(p, sg, i0 + lane, jh + (q + 1) * 32);
-          }
           tmem_load_32cols(t_row + static_cast<uint32_t>(half * (BN / 2) + q * 32), v);
           if constexpr (epi_linear(EPI))
-            linear_box<EPI, T, ACT>(p, sg, i0, jh + q * 32, v, res[q & 1], stage, lane);
+            linear_box<EPI, T, ACT>(p, sg, i0, jh + q * 32, v, res, stage, lane);
           else
             store_box<T>(sg, i0, jh + q * 32, v, stage, lane);
+          if constexpr (epi_linear(EPI)) {
+            if (q < 3) res.load(p, sg, i0, jh + (q + 1) * 32, lane);
+          }
         }
       } else {
         // A part of the sum along K: this warp's 32 x 128 values go to the
@@ -630,8 +660,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                 }
               }
               if constexpr (epi_linear(EPI)) {
-                res[0].load(p, sg, i0 + lane, jh + q * 32);
-                linear_box<EPI, T, ACT>(p, sg, i0, jh + q * 32, v, res[0], stage, lane);
+                res.load(p, sg, i0, jh + q * 32, lane);
+                linear_box<EPI, T, ACT>(p, sg, i0, jh + q * 32, v, res, stage, lane);
               } else {
                 store_box<T>(sg, i0, jh + q * 32, v, stage, lane);
               }
@@ -674,20 +704,17 @@ PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
   return fn;
 }
 
-// 128 x 64 boxes, 64 x 64 boxes, 32 x 32 output boxes of 16 bits and of fp32
-enum MapUse { MAP_ROWS, MAP_COLS, MAP_STORE, MAP_STORE32 };
+enum MapUse { MAP_ROWS, MAP_COLS, MAP_STORE };  // 128 x 64 boxes, 64 x 64 boxes, 32 x 32 output boxes
 
-// A row-major rows x cols matrix of 16-bit elements (MAP_STORE32: fp32) with
-// row pitch ld.
+// A row-major rows x cols matrix of 16-bit elements with row pitch ld.
 bool encode(CUtensorMap* map, const void* base, int dtype, int64_t rows, int64_t cols, int64_t ld, MapUse use) {
   auto enc = map_encoder();
   if (enc == nullptr) return false;
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  const bool wide = use == MAP_STORE32, out = use == MAP_STORE || wide;
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * (wide ? 4 : 2)};
-  cuuint32_t box[2] = {out ? 32u : 64u, out ? 32u : use == MAP_ROWS ? 128u : 64u};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+  cuuint32_t box[2] = {use == MAP_STORE ? 32u : 64u, use == MAP_STORE ? 32u : use == MAP_ROWS ? 128u : 64u};
   cuuint32_t estr[2] = {1, 1};
-  return enc(map, wide ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : dtype == PRM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+  return enc(map, dtype == PRM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
              const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
              use == MAP_STORE ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;

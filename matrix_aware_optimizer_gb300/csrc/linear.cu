@@ -268,10 +268,11 @@ extern "C" int prm_linear_forward(const void* x, int64_t ldx, const void* weight
   p.bias = bias;
   p.residual = residual;
   p.ld_residual = ld_residual;
+  p.y = y;
   p.keep = pre != nullptr;
   GemmSegment s{};
   if (!encode(&s.a[0], x, dtype, tokens, k, ldx, MAP_ROWS) || !encode(&s.b[0], weight, dtype, n, k, k, MAP_ROWS) ||
-      !encode(&s.out[0], y, dtype, tokens, n, n, wide ? MAP_STORE32 : MAP_STORE) ||
+      (!wide && !encode(&s.out[0], y, dtype, tokens, n, n, MAP_STORE)) ||
       (pre != nullptr && !encode(&s.out[1], pre, dtype, tokens, n, n, MAP_STORE)))
     return PRM_ERR_CUDA;
   s.whole = static_cast<int>(sz.y.whole);
