@@ -141,6 +141,17 @@ __device__ __forceinline__ uint64_t desc_at(uint64_t base, uint32_t bytes) {
   return (base & 0xFFFFFFFF00000000ull) | (static_cast<uint32_t>(base) + (bytes >> 4));
 }
 
+// Brings a tile into L2.
+template <int DP>
+__device__ __forceinline__ void att_prefetch_tile(const CUtensorMap* tm, int head, int row, int batch) {
+#pragma unroll
+  for (int c = 0; c < DP / 64; ++c)
+    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
+                     reinterpret_cast<uint64_t>(tm)),
+                 "r"(c * 64), "r"(head), "r"(row), "r"(batch)
+                 : "memory");
+}
+
 // D[128 x 128] = A B^T, both tiles along their elements, `steps` of 16.
 template <int DP>
 __device__ __forceinline__ void att_mma_rows(uint32_t d, const uint8_t* a, const uint8_t* b, int steps,

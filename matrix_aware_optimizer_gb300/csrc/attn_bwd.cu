@@ -299,6 +299,11 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) attn_dkv_kernel(const __grid_c
             tile = 0;
             ++group;
           }
+          if (DQ && x + 1 < it.n) {
+            // a slot is free for less than a round before its tile is needed: too short for memory, not for L2
+            att_prefetch_tile<DP>(&p.grad_o, group << p.h.pack_log2, tile * p.h.tile_tokens(), it.b);
+            att_prefetch_tile<DP>(&p.q, group << p.h.pack_log2, tile * p.h.tile_tokens(), it.b);
+          }
         }
       }
       if (!ok) {  // every load in flight lands before the CTA exits
@@ -442,6 +447,14 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) attn_dkv_kernel(const __grid_c
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
+    // Once the last store has read its memory (which takes as long as forming dS does).
+    auto free_q = [&](uint32_t slot) {
+      if (lane == 0) {
+        bulk_wait_group_read<0>();
+        mbar_arrive(&empty[slot]);
+      }
+      __syncwarp();
+    };
     bool ok = true;
     for (uint32_t item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
       const DkvItem it = dkv_item(p, item);
@@ -507,11 +520,10 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) attn_dkv_kernel(const __grid_c
               if (first < p.h.queries) {
                 tma_store_4d(&p.dq, stage, quarter * 32, last_group << p.h.pack_log2, first, it.b);
                 bulk_commit_group();
-                bulk_wait_group_read<0>();
               }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[slot]);
+            if (i == it.n) free_q(slot);
           }
           if (i == it.n) break;
         }
@@ -559,6 +571,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) attn_dkv_kernel(const __grid_c
           tmem_store_wait();
         }
         arrive(ds_ready);
+        if (DQ && i > 0) free_q((n - 2) % SLOTS);
         ++rounds;
         n += 2;
       }
