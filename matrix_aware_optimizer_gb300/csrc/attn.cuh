@@ -276,7 +276,28 @@ struct AttCall {
 struct AttSplit {
   int splits, tiles;
 };
-AttSplit att_forward_split(const AttHeads& h, int num_sms);
+
+// Units of work (a pair of query tiles against all keys, say) over the SMs:
+// whole rounds of them are computed whole, and those of a last round that would
+// leave SMs idle in `parts` of `each` steps, whose results are joined. So 512
+// units on 152 SMs take 3.5 units' time instead of 4.
+struct AttShare {
+  uint32_t whole, rest;  // units computed whole, and in parts
+  int parts, each;
+  __host__ __device__ __forceinline__ uint32_t items() const { return whole + rest * parts; }
+};
+AttShare att_share(int64_t units, int steps, int num_sms);
+struct AttUnit {
+  uint32_t unit;
+  int first, most;  // step that its part begins with, and the most that it has
+  int slot;         // where its part goes; -1: the unit is whole
+};
+__device__ __forceinline__ AttUnit att_unit(const AttShare& s, uint32_t item) {
+  if (item < s.whole) return {item, 0, 1 << 30, -1};
+  const uint32_t q = item - s.whole, unit = q / static_cast<uint32_t>(s.parts);
+  return {s.whole + unit, static_cast<int>(q - unit * s.parts) * s.each, s.each, static_cast<int>(q)};
+}
+AttShare att_forward_share(const AttHeads& h, int num_sms);
 
 // At most this many query rows share a key head's keys: attn_few.
 constexpr int ATT_FEW_ROWS = 16;

@@ -6,17 +6,26 @@
 
 namespace prm {
 
-// Where there are fewer pairs of query tiles than SMs, ranges of the keys go
-// to different CTAs and their results are joined: at least two key tiles to a
-// range, so that a join's read and write of O stays below what is saved.
-AttSplit att_forward_split(const AttHeads& h, int num_sms) {
+AttShare att_share(int64_t units, int steps, int num_sms) {
+  AttShare s{static_cast<uint32_t>(units), 0, 1, std::max(steps, 1)};
+  const int64_t rest = units % num_sms;
+  if (rest == 0) return s;
+  // a part is two steps at least, and has to save more than writing and joining the parts costs: about four
+  const int64_t want = std::min<int64_t>({num_sms / rest, steps / 2, 64});
+  if (want < 2) return s;
+  const int each = static_cast<int>((steps + want - 1) / want);
+  if (steps - each <= 4 && units > num_sms) return s;
+  s.whole = static_cast<uint32_t>(units - rest);
+  s.rest = static_cast<uint32_t>(rest);
+  s.parts = (steps + each - 1) / each;
+  s.each = each;
+  if (s.parts < 2) return {static_cast<uint32_t>(units), 0, 1, std::max(steps, 1)};
+  return s;
+}
+
+AttShare att_forward_share(const AttHeads& h, int num_sms) {
   const int64_t blocks = (h.query_tiles() + 1) / 2;
-  const int64_t items = static_cast<int64_t>(h.batch) * h.groups * blocks;
-  const int tiles = (h.keys + ATT_ROWS - 1) / ATT_ROWS;
-  const int64_t want = std::min<int64_t>({num_sms / std::max<int64_t>(items, 1), tiles / 2, 64});
-  if (want < 2) return {1, std::max(tiles, 1)};
-  const int each = static_cast<int>((tiles + want - 1) / want);
-  return {(tiles + each - 1) / each, each};
+  return att_share(static_cast<int64_t>(h.batch) * h.groups * blocks, (h.keys + ATT_ROWS - 1) / ATT_ROWS, num_sms);
 }
 
 namespace {
@@ -77,10 +86,13 @@ int layout(const prm_attention_strides& s, int64_t batch, int64_t rows, int64_t 
 }
 
 size_t forward_bytes(const AttHeads& h) {
-  const AttSplit sp = att_is_few(h) ? att_few_split(h, SMS) : att_forward_split(h, SMS);
-  if (sp.splits < 2) return 0;
-  const size_t rows = static_cast<size_t>(h.batch) * h.queries * h.heads;
-  return round_up(rows * sp.splits * (h.head + 1) * sizeof(float), 256);
+  if (att_is_few(h)) {
+    const AttSplit sp = att_few_split(h, SMS);
+    const size_t rows = static_cast<size_t>(h.batch) * h.queries * h.heads;
+    return sp.splits < 2 ? 0 : round_up(rows * sp.splits * (h.head + 1) * sizeof(float), 256);
+  }
+  const AttShare sh = att_forward_share(h, SMS);
+  return round_up(static_cast<size_t>(sh.rest) * sh.parts * 2 * ATT_ROWS * (h.head + 1) * sizeof(float), 256);
 }
 
 bool nothing(const AttHeads& h) { return h.batch == 0 || h.heads == 0 || (h.queries == 0 && h.keys == 0); }

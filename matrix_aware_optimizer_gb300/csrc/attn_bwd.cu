@@ -12,7 +12,7 @@
 //                     memory over S^T and dP^T, dV and dK in tensor memory until the end
 //   attn_dq_kernel    a tile of 128 query rows against all keys: S = Q K^T, dP = dO V^T,
 //                     dS in tensor memory over S, dQ in tensor memory
-//   attn_sum_kernel   adds parts, where few tiles were split along the other axis
+//   attn_sum_kernel   adds parts, of tiles whose other axis was split to fill a last round
 //
 // 512 threads take the elements, four to a row, each 32 columns (with 256 the
 // chain of load, exponential and store of each took twice the products'
@@ -128,11 +128,11 @@ struct DkvParams {
   const float* rows;
   void* dk;
   void* dv;
-  float* part_dk;  // splits > 1: [split][batch][keys][kv_heads][head]
+  float* part_dk;  // [slot][ATT_ROWS][head]
   float* part_dv;
   int key_tiles;
-  int splits, split_rounds;  // ranges of the rounds, rounds of one
-  int rounds;                // query tiles of all groups of a key head
+  int rounds;      // query tiles of all groups of a key head: the steps of a unit
+  AttShare share;
   uint32_t items;
   int mma_k, mma_n;
   float scale, scale_log2;
@@ -140,29 +140,24 @@ struct DkvParams {
 };
 
 struct DkvItem {
-  int tile, kv_head, b, split;
+  int tile, kv_head, b, slot;
   int length;
-  int x0, n;  // first round and their number
+  int x0, n;  // first round and their number, none where there are no keys
+  int all;    // their number all the same
 };
 
 __device__ __forceinline__ DkvItem dkv_item(const DkvParams& p, uint32_t item) {
   DkvItem it;
-  const uint32_t splits = p.splits, key_tiles = p.key_tiles, kv_heads = p.h.kv_heads;
-  it.split = 0;
-  if (splits > 1) {
-    it.split = static_cast<int>(item % splits);
-    item /= splits;
-  }
-  it.tile = 0;
-  if (key_tiles > 1) {
-    it.tile = static_cast<int>(item % key_tiles);
-    item /= key_tiles;
-  }
-  it.kv_head = static_cast<int>(item % kv_heads);
-  it.b = static_cast<int>(item / kv_heads);
+  const uint32_t key_tiles = p.key_tiles, kv_heads = p.h.kv_heads;
+  const AttUnit u = att_unit(p.share, item);
+  it.slot = u.slot;
+  it.tile = static_cast<int>(u.unit % key_tiles);
+  const uint32_t bh = u.unit / key_tiles;
+  it.kv_head = static_cast<int>(bh % kv_heads);
+  it.b = static_cast<int>(bh / kv_heads);
   it.length = att_length(p.lengths, it.b, p.h.keys);
-  it.x0 = min(it.split * p.split_rounds, p.rounds);
-  it.n = min(p.split_rounds, p.rounds - it.x0);
+  it.x0 = min(u.first, p.rounds);
+  it.all = it.n = min(u.most, p.rounds - it.x0);
   if (it.tile * ATT_ROWS >= it.length) it.n = 0;
   return it;
 }
@@ -578,7 +573,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) attn_dkv_kernel(const __grid_c
       if (!ok) break;
       if (DQ && it.n <= 0 && it.length <= 0) {
         // no keys: dQ is zero
-        for (int x = 0, g = group, q = tile; x < min(p.split_rounds, p.rounds - it.x0); ++x) {
+        for (int x = 0, g = group, q = tile; x < it.all; ++x) {
           const int token = q * p.h.tile_tokens() + (row >> p.h.pack_log2);
           T* out = static_cast<T*>(p.dq_out) + it.b * p.dq_strides.batch + token * p.dq_strides.token +
                    ((g << p.h.pack_log2) + (row & ((1 << p.h.pack_log2) - 1))) * p.dq_strides.head;
@@ -601,10 +596,8 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) attn_dkv_kernel(const __grid_c
       const uint32_t t_acc = (is_dk ? t_dk : t_dv) + t_lane;
       const AttStrides st = is_dk ? p.dk_strides : p.dv_strides;
       T* out = static_cast<T*>(is_dk ? p.dk : p.dv) + it.b * st.batch + key * st.token + it.kv_head * st.head;
-      float* part = is_dk ? p.part_dk : p.part_dv;
-      if (part != nullptr)
-        part += (((static_cast<int64_t>(it.split) * p.h.batch + it.b) * p.h.keys + key) * p.h.kv_heads + it.kv_head) *
-                p.h.head;
+      float* part = nullptr;
+      if (it.slot >= 0) part = (is_dk ? p.part_dk : p.part_dv) + static_cast<int64_t>(it.slot * ATT_ROWS + row) * p.h.head;
       const float factor = is_dk ? p.scale : 1.f;
 #pragma unroll 1
       for (int c = first; c < min(first + DP / 2, p.h.head); c += 16) {
@@ -645,8 +638,8 @@ struct DqParams {
   AttStrides dq_strides;
   const float* rows;
   void* dq;
-  float* part_dq;  // splits > 1: [split][batch][queries][heads][head]
-  int splits, split_tiles;
+  float* part_dq;  // [slot][ATT_ROWS][head]
+  AttShare share;
   uint32_t items;
   int mma_k, mma_n;
   float scale, scale_log2;
@@ -654,24 +647,24 @@ struct DqParams {
 };
 
 struct DqItem {
-  int tile, group, b, split;
+  int tile, group, b, slot;
   int length;
   int k0, n;
 };
 
 __device__ __forceinline__ DqItem dq_item(const DqParams& p, uint32_t item) {
   DqItem it;
-  const uint32_t tiles = p.h.query_tiles(), splits = p.splits, groups = p.h.groups;
-  it.tile = static_cast<int>(item % tiles);
-  item /= tiles;
-  it.split = static_cast<int>(item % splits);
-  item /= splits;
-  it.group = static_cast<int>(item % groups);
-  it.b = static_cast<int>(item / groups);
+  const uint32_t tiles = p.h.query_tiles(), groups = p.h.groups;
+  const AttUnit u = att_unit(p.share, item);
+  it.slot = u.slot;
+  it.tile = static_cast<int>(u.unit % tiles);
+  const uint32_t bg = u.unit / tiles;
+  it.group = static_cast<int>(bg % groups);
+  it.b = static_cast<int>(bg / groups);
   it.length = att_length(p.lengths, it.b, p.h.keys);
   const int key_tiles = (it.length + ATT_ROWS - 1) / ATT_ROWS;
-  it.k0 = min(it.split * p.split_tiles, key_tiles);
-  it.n = min(p.split_tiles, key_tiles - it.k0);
+  it.k0 = min(u.first, key_tiles);
+  it.n = min(u.most, key_tiles - it.k0);
   return it;
 }
 
@@ -920,10 +913,8 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) attn_dq_kernel(const __grid_co
       const bool live = token < p.h.queries;
       T* out = static_cast<T*>(p.dq) + it.b * p.dq_strides.batch + token * p.dq_strides.token +
                head * p.dq_strides.head;
-      float* part = p.part_dq;
-      if (part != nullptr)
-        part += (((static_cast<int64_t>(it.split) * p.h.batch + it.b) * p.h.queries + token) * p.h.heads + head) *
-                p.h.head;
+      float* part = nullptr;
+      if (it.slot >= 0) part = p.part_dq + static_cast<int64_t>(it.slot * ATT_ROWS + row) * p.h.head;
 #pragma unroll 1
       for (int c = quarter * (DP / 4); c < min((quarter + 1) * (DP / 4), p.h.head); c += 16) {
         float v[16];
@@ -949,30 +940,38 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) attn_dq_kernel(const __grid_co
 }
 
 // -------------------------------------------------------------------- sums
-// out = sum of the parts, in order. A thread takes eight elements of a row.
+// The units that were computed in parts: out = sum of the parts, in order. A
+// thread takes eight elements of a row.
 struct SumParams {
-  const float* part;  // [split][batch][tokens][heads][head]
-  void* out;
-  AttStrides out_strides;
-  int tokens, heads, head, splits;
-  int64_t rows;  // batch * tokens * heads
+  const float* part[2];  // [slot][ATT_ROWS][head]: dK and dV, or dQ
+  void* out[2];
+  AttStrides strides[2];
+  AttHeads h;
+  AttShare share;
+  int tiles;  // of a head
+  int keys;   // rows are keys of a key head, not queries of a group
 };
 
 template <typename T>
 __global__ void __launch_bounds__(256) attn_sum_kernel(const __grid_constant__ SumParams p) {
   pdl_wait();
   pdl_launch_dependents();
-  const int vectors = p.head / 8;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= p.rows * vectors) return;
-  const int64_t row = i / vectors;
-  const int vec = static_cast<int>(i - row * vectors);
-  const int64_t bt = row / p.heads;
-  const int64_t head = row - bt * p.heads, b = bt / p.tokens, token = bt - b * p.tokens;
+  const int vectors = p.h.head / 8, which = blockIdx.z;
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  if (i >= ATT_ROWS * vectors) return;
+  const int row = i / vectors, vec = i - row * vectors;
+  const uint32_t unit = p.share.whole + blockIdx.y, tiles = p.tiles, heads = p.keys ? p.h.kv_heads : p.h.groups;
+  const int tile = static_cast<int>(unit % tiles), g = static_cast<int>(unit / tiles % heads);
+  const int b = static_cast<int>(unit / tiles / heads);
+  const int token = p.keys ? tile * ATT_ROWS + row : tile * p.h.tile_tokens() + (row >> p.h.pack_log2);
+  const int head = p.keys ? g : (g << p.h.pack_log2) + (row & ((1 << p.h.pack_log2) - 1));
+  if (token >= (p.keys ? p.h.keys : p.h.queries)) return;
+  const float* from = p.part[which] + (static_cast<int64_t>(blockIdx.y) * p.share.parts * ATT_ROWS + row) * p.h.head + vec * 8;
   float v[8] = {};
-  for (int s = 0; s < p.splits; ++s) {
+#pragma unroll 4
+  for (int s = 0; s < p.share.parts; ++s) {
     Raw8<float> r;
-    r.load(p.part + (s * p.rows + row) * p.head + vec * 8);
+    r.load(from + static_cast<int64_t>(s) * ATT_ROWS * p.h.head);
     float u[8];
     r.get(u);
 #pragma unroll
@@ -980,51 +979,60 @@ __global__ void __launch_bounds__(256) attn_sum_kernel(const __grid_constant__ S
   }
   Raw8<T> r;
   r.set(v);
-  r.store(static_cast<T*>(p.out) + b * p.out_strides.batch + token * p.out_strides.token + head * p.out_strides.head +
-          vec * 8);
+  const AttStrides& st = p.strides[which];
+  r.store(static_cast<T*>(p.out[which]) + b * st.batch + token * st.token + head * st.head + vec * 8);
 }
 
 template <typename T>
-cudaError_t add_parts(const AttCall& c, const float* part, void* out, const AttStrides& strides, int tokens, int heads,
-                      int splits, cudaStream_t stream) {
-  const SumParams p{part, out, strides, tokens, heads, c.h.head, splits,
-                    static_cast<int64_t>(c.h.batch) * tokens * heads};
-  const int64_t threads = p.rows * (c.h.head / 8);
-  return launch_dependent(attn_sum_kernel<T>, dim3(static_cast<unsigned>((threads + 255) / 256)), dim3(256), 0, stream,
-                          p);
+cudaError_t add_parts(const SumParams& p, int outputs, cudaStream_t stream) {
+  return launch_dependent(attn_sum_kernel<T>,
+                          dim3(static_cast<unsigned>((ATT_ROWS * (p.h.head / 8) + 255) / 256), p.share.rest,
+                               static_cast<unsigned>(outputs)),
+                          dim3(256), 0, stream, p);
+}
+
+// A gradient of tokens x heads rows per sequence, all zero.
+struct ZeroParams {
+  void* out;
+  AttStrides strides;
+  int tokens, heads, vectors;
+  int64_t count;
+};
+
+__global__ void __launch_bounds__(256) attn_zero_kernel(const __grid_constant__ ZeroParams p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= p.count) return;
+  const int64_t row = i / p.vectors, vec = i - row * p.vectors;
+  const int64_t bt = row / p.heads, head = row - bt * p.heads, b = bt / p.tokens, token = bt - b * p.tokens;
+  uint16_t* out = static_cast<uint16_t*>(p.out) + b * p.strides.batch + token * p.strides.token + head * p.strides.head;
+  *reinterpret_cast<uint4*>(out + vec * 8) = make_uint4(0, 0, 0, 0);
 }
 
 // -------------------------------------------------------------------- host
 struct Plan {
-  AttSplit dkv, dq;            // ranges of rounds; ranges of key tiles
+  AttShare dkv, dq;            // of the rounds; of the key tiles
   bool one;                    // one key tile: dQ comes out of dK's and dV's pass
   int rounds, key_tiles;
   size_t dkv_at, dq_at, bytes; // workspace: rows' values, then parts of dK and dV, then of dQ
   size_t dkv_part;             // floats of the parts of dK
 };
 
-// As forward: parts only where there are fewer tiles than SMs, of two at least.
-AttSplit split(int64_t items, int steps, int num_sms) {
-  const int64_t want = std::min<int64_t>({num_sms / std::max<int64_t>(items, 1), steps / 2, 64});
-  if (want < 2) return {1, std::max(steps, 1)};
-  const int each = static_cast<int>((steps + want - 1) / want);
-  return {(steps + each - 1) / each, each};
-}
-
 Plan plan(const AttHeads& h, int num_sms) {
   Plan s{};
   const int tiles = h.query_tiles();
   s.key_tiles = (h.keys + ATT_ROWS - 1) / ATT_ROWS;
   s.rounds = (h.group_heads >> h.pack_log2) * tiles;
-  s.dkv = split(static_cast<int64_t>(h.batch) * h.kv_heads * s.key_tiles, s.rounds, num_sms);
+  s.dkv = att_share(static_cast<int64_t>(h.batch) * h.kv_heads * s.key_tiles, s.rounds, num_sms);
   s.one = s.key_tiles == 1;
-  s.dq = split(static_cast<int64_t>(h.batch) * h.groups * tiles, s.key_tiles, num_sms);
+  s.dq = att_share(static_cast<int64_t>(h.batch) * h.groups * tiles, s.key_tiles, num_sms);
   size_t at = round_up(static_cast<size_t>(h.batch) * h.groups * tiles * ROW_VALUES * sizeof(float), 256);
   s.dkv_at = at;
-  s.dkv_part = s.dkv.splits > 1 ? static_cast<size_t>(s.dkv.splits) * h.batch * h.keys * h.kv_heads * h.head : 0;
+  s.dkv_part = static_cast<size_t>(s.dkv.rest) * s.dkv.parts * ATT_ROWS * h.head;
   at += round_up(2 * s.dkv_part * sizeof(float), 256);
   s.dq_at = at;
-  if (s.dq.splits > 1) at += static_cast<size_t>(s.dq.splits) * h.batch * h.queries * h.heads * h.head * sizeof(float);
+  at += static_cast<size_t>(s.dq.rest) * s.dq.parts * ATT_ROWS * h.head * sizeof(float);
   s.bytes = round_up(at, 256);
   return s;
 }
@@ -1055,14 +1063,14 @@ cudaError_t launch(const AttCall& c, const Plan& s, const RowsParams& rows, cons
     e = launch_dependent(attn_dq_kernel<T, DP>, dim3(grid), dim3(BWD_THREADS), DqShape<DP>::SMEM, stream, dq);
     if (e != cudaSuccess) return e;
   }
-  if (s.dkv.splits > 1) {
-    if ((e = add_parts<T>(c, dkv.part_dk, dkv.dk, c.dk, c.h.keys, c.h.kv_heads, s.dkv.splits, stream)) != cudaSuccess)
-      return e;
-    if ((e = add_parts<T>(c, dkv.part_dv, dkv.dv, c.dv, c.h.keys, c.h.kv_heads, s.dkv.splits, stream)) != cudaSuccess)
-      return e;
+  if (s.dkv.rest > 0) {
+    const SumParams sum{{dkv.part_dk, dkv.part_dv}, {dkv.dk, dkv.dv}, {c.dk, c.dv}, c.h, s.dkv, s.key_tiles, 1};
+    if ((e = add_parts<T>(sum, 2, stream)) != cudaSuccess) return e;
   }
-  if (s.dq.splits > 1)
-    return add_parts<T>(c, dq.part_dq, dq.dq, c.dq, c.h.queries, c.h.heads, s.dq.splits, stream);
+  if (!s.one && s.dq.rest > 0) {
+    const SumParams sum{{dq.part_dq, nullptr}, {dq.dq, nullptr}, {c.dq, {}}, c.h, s.dq, c.h.query_tiles(), 0};
+    return add_parts<T>(sum, 1, stream);
+  }
   return cudaSuccess;
 }
 
@@ -1108,30 +1116,26 @@ cudaError_t attn_backward(const AttCall& c, const void* grad_o, const void* q, c
   a.dv = dv;
   a.key_tiles = s.key_tiles;
   a.rounds = s.rounds;
-  a.splits = s.dkv.splits;
-  a.split_rounds = s.dkv.tiles;
-  a.items = static_cast<uint32_t>(static_cast<int64_t>(h.batch) * h.kv_heads * s.key_tiles * s.dkv.splits);
-  if (s.dkv.splits > 1) {
-    a.part_dk = reinterpret_cast<float*>(workspace + s.dkv_at);
-    a.part_dv = a.part_dk + s.dkv_part;
-  }
+  a.share = s.dkv;
+  a.items = s.dkv.items();
+  a.part_dk = reinterpret_cast<float*>(workspace + s.dkv_at);
+  a.part_dv = a.part_dk + s.dkv_part;
   b.dq_strides = c.dq;
   b.dq = dq;
-  b.splits = s.dq.splits;
-  b.split_tiles = s.dq.tiles;
-  b.items = static_cast<uint32_t>(static_cast<int64_t>(h.batch) * h.groups * tiles * s.dq.splits);
-  if (s.dq.splits > 1) b.part_dq = reinterpret_cast<float*>(workspace + s.dq_at);
+  b.share = s.dq;
+  b.items = s.dq.items();
+  b.part_dq = reinterpret_cast<float*>(workspace + s.dq_at);
   const bool wide = h.head > 64;
   if (c.dtype == PRM_BF16)
     return wide ? launch<__nv_bfloat16, 128>(c, s, r, a, b, stream) : launch<__nv_bfloat16, 64>(c, s, r, a, b, stream);
   return wide ? launch<__half, 128>(c, s, r, a, b, stream) : launch<__half, 64>(c, s, r, a, b, stream);
 }
 
-// Zeros, where there are no keys or no queries.
 cudaError_t attn_zero(const AttCall& c, void* out, const AttStrides& strides, int tokens, int heads,
                       cudaStream_t stream) {
-  return c.dtype == PRM_BF16 ? add_parts<__nv_bfloat16>(c, nullptr, out, strides, tokens, heads, 0, stream)
-                             : add_parts<__half>(c, nullptr, out, strides, tokens, heads, 0, stream);
+  const int vectors = c.h.head / 8;
+  const ZeroParams p{out, strides, tokens, heads, vectors, static_cast<int64_t>(c.h.batch) * tokens * heads * vectors};
+  return launch_dependent(attn_zero_kernel, dim3(static_cast<unsigned>((p.count + 255) / 256)), dim3(256), 0, stream, p);
 }
 
 }  // namespace prm

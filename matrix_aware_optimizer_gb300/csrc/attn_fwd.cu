@@ -101,10 +101,10 @@ struct FwdParams {
   AttHeads h;
   AttLengths lengths;
   float* lse;       // [batch][heads][queries], or NULL
-  float* part_o;    // splits > 1: [split][batch][queries][heads][head], each part normalised
-  float* part_lse;  // splits > 1: [split][batch][heads][queries]
+  float* part_o;    // [slot][2 ATT_ROWS][head], each part normalised
+  float* part_lse;  // [slot][2 ATT_ROWS]
   int blocks;       // pairs of query tiles
-  int splits, split_tiles;  // key ranges, key tiles of one
+  AttShare share;
   uint32_t items;
   int mma_k;        // 16-element steps of a head
   int mma_n;        // head rounded up to 16
@@ -113,7 +113,7 @@ struct FwdParams {
 };
 
 struct FwdItem {
-  int block, split, group, b;
+  int block, slot, group, b;
   int length;   // keys of the sequence
   int k0, n;    // first key tile and their number
   int tiles;    // query tiles with rows: 1 or 2
@@ -121,20 +121,17 @@ struct FwdItem {
 
 __device__ __forceinline__ FwdItem fwd_item(const FwdParams& p, uint32_t item) {
   FwdItem it;
-  const uint32_t blocks = p.blocks, splits = p.splits, groups = p.h.groups;
-  it.block = static_cast<int>(item % blocks);
-  item /= blocks;
-  it.split = 0;
-  if (splits > 1) {
-    it.split = static_cast<int>(item % splits);
-    item /= splits;
-  }
-  it.group = static_cast<int>(item % groups);
-  it.b = static_cast<int>(item / groups);
+  const uint32_t blocks = p.blocks, groups = p.h.groups;
+  const AttUnit u = att_unit(p.share, item);
+  it.slot = u.slot;
+  it.block = static_cast<int>(u.unit % blocks);
+  const uint32_t bg = u.unit / blocks;
+  it.group = static_cast<int>(bg % groups);
+  it.b = static_cast<int>(bg / groups);
   it.length = att_length(p.lengths, it.b, p.h.keys);
   const int tiles = (it.length + ATT_ROWS - 1) / ATT_ROWS;
-  it.k0 = min(it.split * p.split_tiles, tiles);
-  it.n = min(p.split_tiles, tiles - it.k0);
+  it.k0 = min(u.first, tiles);
+  it.n = min(u.most, tiles - it.k0);
   it.tiles = (it.block * 2 + 1) * p.h.tile_tokens() < p.h.queries ? 2 : 1;
   return it;
 }
@@ -491,13 +488,12 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) attn_fwd_kernel(const __grid_c
           if (live) {
             const int64_t at = (static_cast<int64_t>(it.b) * p.h.heads + head) * p.h.queries + token;
             const float lse = some ? held_m * p.scale_log2 + log2f(held_l) : -INFINITY;
-            if (p.splits > 1)
-              p.part_lse[static_cast<int64_t>(it.split) * p.h.batch * p.h.heads * p.h.queries + at] = lse;
+            if (it.slot >= 0)
+              p.part_lse[it.slot * (2 * ATT_ROWS) + t * ATT_ROWS + row] = lse;
             else if (p.lse != nullptr)
               p.lse[at] = lse;
           }
-          float* part = p.part_o + (((static_cast<int64_t>(it.split) * p.h.batch + it.b) * p.h.queries + token) *
-                                        p.h.heads + head) * p.h.head;
+          float* part = p.part_o + static_cast<int64_t>(it.slot * (2 * ATT_ROWS) + t * ATT_ROWS + row) * p.h.head;
           uint8_t* stage = sOut + warp * ATT_STAGE;
           const int first = token - (lane >> p.h.pack_log2);  // the warp's first token
 #pragma unroll 1
@@ -513,7 +509,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) attn_fwd_kernel(const __grid_c
             }
 #pragma unroll
             for (int i = 0; i < 64; ++i) o[i] = some ? o[i] * inv : 0.f;
-            if (p.splits > 1) {
+            if (it.slot >= 0) {
 #pragma unroll
               for (int i = 0; i < 64; i += 8) {
                 if (c + i >= p.h.head || !live) break;
@@ -631,6 +627,59 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
   if (vec == 0 && p.lse != nullptr) p.lse[at] = total > 0.f || total != total ? top + log2f(total) : -INFINITY;
 }
 
+// The same for the units that were computed in parts: a thread takes eight
+// elements of a row.
+struct UnitJoinParams {
+  FwdParams f;
+  AttStrides o_strides;
+  void* o;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(256) attn_join_units_kernel(const __grid_constant__ UnitJoinParams p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const AttHeads& h = p.f.h;
+  const int vectors = h.head / 8, parts = p.f.share.parts;
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  if (i >= 2 * ATT_ROWS * vectors) return;
+  const int row = i / vectors, vec = i - row * vectors;
+  const uint32_t unit = p.f.share.whole + blockIdx.y, blocks = p.f.blocks, groups = h.groups;
+  const int block = static_cast<int>(unit % blocks), group = static_cast<int>(unit / blocks % groups);
+  const int b = static_cast<int>(unit / blocks / groups);
+  const int tile = block * 2 + row / ATT_ROWS, in_tile = row % ATT_ROWS;
+  const int token = tile * h.tile_tokens() + (in_tile >> h.pack_log2);
+  const int head = (group << h.pack_log2) + (in_tile & ((1 << h.pack_log2) - 1));
+  if (token >= h.queries) return;
+  const int64_t first = static_cast<int64_t>(blockIdx.y) * parts * (2 * ATT_ROWS) + row;
+  float top = -INFINITY;
+#pragma unroll 8
+  for (int s = 0; s < parts; ++s) top = fmaxf(top, p.f.part_lse[first + s * (2 * ATT_ROWS)]);
+  float v[8] = {}, total = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < parts; ++s) {
+    const int64_t at = first + s * (2 * ATT_ROWS);
+    const float lse = p.f.part_lse[at];
+    Raw8<float> r;
+    r.load(p.f.part_o + at * h.head + vec * 8);
+    const float w = lse == -INFINITY ? 0.f : exp2f(lse - top);  // (a part without keys left zeros)
+    total += w;
+    float u[8];
+    r.get(u);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = fmaf(w, u[e], v[e]);
+  }
+  const bool some = total > 0.f || total != total;
+  const float inv = some ? 1.f / total : 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] *= inv;
+  Raw8<T> r;
+  r.set(v);
+  r.store(static_cast<T*>(p.o) + b * p.o_strides.batch + token * p.o_strides.token + head * p.o_strides.head + vec * 8);
+  if (vec == 0 && p.f.lse != nullptr)
+    p.f.lse[(static_cast<int64_t>(b) * h.heads + head) * h.queries + token] = some ? top + log2f(total) : -INFINITY;
+}
+
 template <typename T, int DP>
 cudaError_t launch_fwd(const FwdParams& p, int num_sms, cudaStream_t stream) {
   static std::atomic<uint64_t> ready{0};
@@ -649,19 +698,15 @@ cudaError_t attn_forward(const AttCall& c, const void* q, const void* k, const v
   p.lengths = c.lengths;
   p.lse = lse;
   p.blocks = (c.h.query_tiles() + 1) / 2;
-  const AttSplit sp = att_forward_split(c.h, c.num_sms);
-  p.splits = sp.splits;
-  p.split_tiles = sp.tiles;
-  p.items = static_cast<uint32_t>(static_cast<int64_t>(c.h.batch) * c.h.groups * p.splits * p.blocks);
+  p.share = att_forward_share(c.h, c.num_sms);
+  p.items = p.share.items();
   p.mma_k = (c.h.head + 15) / 16;
   p.mma_n = p.mma_k * 16;
   p.scale_log2 = c.scale * 1.4426950408889634f;
   p.err = c.err;
-  const int64_t rows = static_cast<int64_t>(c.h.batch) * c.h.queries * c.h.heads;
-  if (p.splits > 1) {
-    p.part_o = reinterpret_cast<float*>(workspace);
-    p.part_lse = p.part_o + rows * p.splits * c.h.head;
-  }
+  p.part_o = reinterpret_cast<float*>(workspace);
+  if (p.share.rest > 0)
+    p.part_lse = p.part_o + static_cast<int64_t>(p.share.rest) * p.share.parts * 2 * ATT_ROWS * c.h.head;
   const int pack = 1 << c.h.pack_log2;
   if (!att_encode(&p.q, q, c.dtype, c.h.batch, c.h.queries, c.h.heads, c.h.head, c.q, pack, ATT_ROWS / pack) ||
       !att_encode(&p.o, o, c.dtype, c.h.batch, c.h.queries, c.h.heads, c.h.head, c.o, pack, 32 / pack) ||
@@ -673,8 +718,10 @@ cudaError_t attn_forward(const AttCall& c, const void* q, const void* k, const v
                              : launch_fwd<__nv_bfloat16, 64>(p, c.num_sms, stream))
                      : (wide ? launch_fwd<__half, 128>(p, c.num_sms, stream)
                              : launch_fwd<__half, 64>(p, c.num_sms, stream));
-  if (e != cudaSuccess || p.splits == 1) return e;
-  return attn_join(c, p.splits, o, lse, p.part_o, p.part_lse, stream);
+  if (e != cudaSuccess || p.share.rest == 0) return e;
+  const UnitJoinParams j{p, c.o, o};
+  return launch_dependent(bf ? attn_join_units_kernel<__nv_bfloat16> : attn_join_units_kernel<__half>,
+                          dim3(static_cast<unsigned>(c.h.head / 8), p.share.rest), dim3(256), 0, stream, j);
 }
 
 cudaError_t attn_join(const AttCall& c, int splits, void* o, float* lse, const float* part_o, const float* part_lse,

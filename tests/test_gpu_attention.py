@@ -356,6 +356,13 @@ def test_attention_in_parts(B, Lq, Lk, H, Hkv, D, lengths):
     _check_attention(*_attention_inputs(B, Lq, Lk, H, Hkv, D), lengths=lengths)
 
 
+# more tiles than SMs, and a last round of them that leaves SMs idle: its tiles in parts, the others whole
+@pytest.mark.parametrize("B,Lq,Lk,H,Hkv,lengths", [(1, 1030, 1100, 40, 40, None), (2, 1030, 1100, 40, 20, [1100, 700]),
+                                                   (3, 1030, 100, 60, 60, [100, 0, 37])])
+def test_attention_last_round_in_parts(B, Lq, Lk, H, Hkv, lengths):
+    _check_attention(*_attention_inputs(B, Lq, Lk, H, Hkv, 16), lengths=lengths)
+
+
 def test_attention_large_and_growing_scores():
     # maxima that grow from tile to tile by more than the exponent's slack, and fall again
     q, k, v, do = _attention_inputs(1, 200, 700, 2, 2, 64)
