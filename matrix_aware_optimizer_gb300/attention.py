@@ -451,7 +451,7 @@ def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, key_lengt
     is self-attention without an order. key_lengths: int32 or int64 [batch], None
     for all keys; what lies behind a sequence's last key is never used, and a
     sequence without keys gives zeros. scale: head^-0.5 by default. out: where
-    the result goes.
+    the result goes; it does not overlap the inputs.
 
     Returns o, or (o, saved) with save=True, saved for
     cross_attention_backward (autograd does not see the call).
@@ -487,7 +487,8 @@ def cross_attention_backward(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
     of its result and the o and saved that it returned; the other arguments are
     those of that pass. Heads that share keys add to the same dk and dv; rows
     behind a sequence's last key are zero. grads: three tensors to write them
-    into (slices of a fused projection's gradient, say).
+    into (slices of a fused projection's gradient, say), which do not overlap
+    each other or the inputs.
     """
     device, scale = _attention_check(q, k, v, key_lengths, scale)
     for t in (do, o):
@@ -503,6 +504,8 @@ def cross_attention_backward(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
             if g.shape != t.shape or g.dtype is not t.dtype or g.get_device() != device                     or (g.numel() and not (_usable(g) and _distinct(g))):
                 raise ValueError("grads must have the shapes and type of q, k and v, consecutive elements and "
                                  "16-byte rows")
+        if len({g.data_ptr() for g in grads if g.numel()}) < sum(g.numel() > 0 for g in grads):
+            raise ValueError("grads must be three different tensors")
     if _is_elsewhere(device, stream):
         with _elsewhere(device, stream, do, q, k, v, o, lse, key_lengths, *(grads or ())):
             return cross_attention_backward(do, q, k, v, o, saved, key_lengths, scale, grads)
