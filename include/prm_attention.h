@@ -44,11 +44,11 @@ extern "C" {
 PRM_API int prm_linear_sizes(int64_t tokens, int64_t n, int64_t k, size_t* forward_workspace,
                              size_t* backward_workspace);
 
-/* pre: tokens x n of dtype where g is left for the backward pass, or NULL;
- * not written without an activation.
+/* pre: tokens x n fp32 where g is left for the backward pass, or NULL; not
+ * written without an activation.
  * Errors: INVALID_ARG, ALIGNMENT, WORKSPACE, UNSUPPORTED, CUDA. */
 PRM_API int prm_linear_forward(const void* x, int64_t ldx, const void* weight, const float* bias, const void* residual,
-                               int64_t ld_residual, void* y, int y_dtype, void* pre, void* workspace,
+                               int64_t ld_residual, void* y, int y_dtype, float* pre, void* workspace,
                                size_t workspace_bytes, int64_t tokens, int64_t n, int64_t k, int act, int dtype,
                                void* stream);
 
@@ -60,7 +60,7 @@ PRM_API int prm_linear_forward(const void* x, int64_t ldx, const void* weight, c
  * The residual's gradient is dy itself. pre may be NULL without an activation.
  * Errors as for the forward pass. */
 PRM_API int prm_linear_backward(const void* dy, int64_t lddy, int dy_dtype, const void* x, int64_t ldx,
-                                const void* weight, const void* pre, void* dx, void* dweight, float* dbias,
+                                const void* weight, const float* pre, void* dx, void* dweight, float* dbias,
                                 void* workspace, size_t workspace_bytes, int64_t tokens, int64_t n, int64_t k, int act,
                                 int dtype, void* stream);
 

@@ -27,9 +27,8 @@ _LAYOUT = {"half": N.PRM_ROTARY_HALF, "interleaved": N.PRM_ROTARY_INTERLEAVED}
 
 # ------------------------------------------------------------- linear layer
 class LinearSaved(NamedTuple):
-    """What linear leaves for its backward pass: x weight^T + bias in x's type
-    (None without an activation), and the sizes, activation and type of the
-    pass."""
+    """What linear leaves for its backward pass: x weight^T + bias in fp32 (None
+    without an activation), and the sizes, activation and type of the pass."""
     pre: Optional[torch.Tensor]
     tokens: int
     features: int
@@ -95,7 +94,7 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] =
     r2, ldr = (None, n) if residual is None else _rows(residual, n)
     tokens = x2.shape[0]
     y = torch.empty((*x.shape[:-1], n), dtype=x.dtype if residual is None else residual.dtype, device=x.device)
-    pre = torch.empty((tokens, n), dtype=x.dtype, device=x.device) if save and act is not None else None
+    pre = torch.empty((tokens, n), dtype=torch.float32, device=x.device) if save and act is not None else None
     n_ws = _linear_sizes(tokens, n, k)[0]
     ws = torch.empty(n_ws, dtype=torch.uint8, device=x.device) if n_ws else None
     rc = N.load().prm_linear_forward(x2.data_ptr(), ldx, weight.data_ptr(), _ptr(bias), _ptr(r2), ldr, y.data_ptr(),

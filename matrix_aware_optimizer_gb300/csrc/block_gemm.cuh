@@ -47,7 +47,7 @@ constexpr int EPI_GLU = 0, EPI_DGLU = 1, EPI_STORE = 2, EPI_LINEAR = 3, EPI_LINE
 // Epilogues that take plain products, in parts along K where the queue says so.
 __host__ __device__ constexpr bool epi_plain(int epi) { return epi >= EPI_STORE; }
 // LINEAR: out = act(product + bias) + residual in 16 bits, LINEAR32: in fp32
-// with an fp32 residual; where asked for, product + bias goes out in 16 bits too.
+// with an fp32 residual; where asked for, product + bias goes out in fp32 too.
 __host__ __device__ constexpr bool epi_linear(int epi) { return epi >= EPI_LINEAR; }
 
 // One product out = sum over its operand pairs of A B^T (B given K-major) or
@@ -55,7 +55,7 @@ __host__ __device__ constexpr bool epi_linear(int epi) { return epi >= EPI_LINEA
 struct GemmSegment {
   CUtensorMap a[2];
   CUtensorMap b[2];
-  CUtensorMap out[2];   // GLU: h; DGLU: dg, du; STORE: the product; LINEAR: y, product + bias
+  CUtensorMap out[2];   // GLU: h; DGLU: dg, du; STORE: the product; LINEAR: y
   int M, N;             // output extents (GLU: N = f)
   int k_blocks[2];      // 64-long slices of each pair along K
   int a_mn, b_mn;       // operand stored [K][M] / [K][N]
@@ -78,7 +78,7 @@ struct BlockGemmParams {
   const void* residual; // LINEAR: M x N with row pitch ld_residual, or NULL
   int64_t ld_residual;
   void* y;              // LINEAR: M x N, contiguous
-  int keep;             // LINEAR: product + bias is wanted
+  float* pre;           // LINEAR: where product + bias is kept, M x N, or NULL
   uint32_t* zero;       // counters to clear for the next launch
   int zero_count;
   int* err;
@@ -329,28 +329,9 @@ __device__ __forceinline__ void linear_box(const BlockGemmParams& p, const GemmS
   }
   if (lane == 0) bulk_wait_group_read<0>();
   __syncwarp();
-  const bool joined = EPI == EPI_LINEAR32 || p.residual != nullptr;
-  if (ACT != ACT_NONE && p.keep) {
-    uint32_t w[16];
-#pragma unroll
-    for (int k = 0; k < 16; ++k) w[k] = pack2<T>(v[2 * k], v[2 * k + 1]);
-    uint8_t* box = joined ? stage : stage + EPI_BUF_BYTES;
-    stage_box(box, lane, w);
-    if (joined) {  // the sums take all of the warp's staging memory
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        tma_store_2d(&sg.out[1], box, j0, i0);
-        bulk_commit_group();
-        bulk_wait_group_read<0>();
-      }
-      __syncwarp();
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < 32; ++k) v[k] = ffn_act<ACT>(v[k]);
-  if (joined) {
-    // act(g) in fp32 through shared memory (16-byte units swizzled by the row), to the residual's order and out
+  const bool keep = ACT != ACT_NONE && p.pre != nullptr;
+  if (EPI == EPI_LINEAR32 || p.residual != nullptr || keep) {
+    // g in fp32 through shared memory (16-byte units swizzled by the row) into the residual's order, and out
 #pragma unroll
     for (int k = 0; k < 8; ++k)
       *reinterpret_cast<float4*>(stage + lane * 128 + ((k ^ (lane & 7)) << 4)) =
@@ -360,28 +341,34 @@ __device__ __forceinline__ void linear_box(const BlockGemmParams& p, const GemmS
 #pragma unroll
     for (int k = 0; k < Box::VECTORS; ++k) {
       const int r = Box::row(lane, k), unit = lane % Box::UNITS;
+      const bool live = i0 + r < sg.M && j < sg.N;
+      const int64_t at = static_cast<int64_t>(i0 + r) * sg.N + j;
       const uint8_t* from = stage + r * 128;
       const uint4 q = p.residual != nullptr ? res.v[k] : make_uint4(0, 0, 0, 0);
+      constexpr int QUADS = Box::ELEMENTS / 4;
+      float4 g[QUADS];
+#pragma unroll
+      for (int e = 0; e < QUADS; ++e) {
+        g[e] = *reinterpret_cast<const float4*>(from + (((QUADS * unit + e) ^ (r & 7)) << 4));
+        if (keep && live) __stcs(reinterpret_cast<float4*>(p.pre + at) + e, g[e]);
+        g[e] = make_float4(ffn_act<ACT>(g[e].x), ffn_act<ACT>(g[e].y), ffn_act<ACT>(g[e].z), ffn_act<ACT>(g[e].w));
+      }
       uint4 out;
       if constexpr (Box::WIDE) {
-        const float4 a = *reinterpret_cast<const float4*>(from + ((unit ^ (r & 7)) << 4));
-        out = make_uint4(__float_as_uint(a.x + __uint_as_float(q.x)), __float_as_uint(a.y + __uint_as_float(q.y)),
-                         __float_as_uint(a.z + __uint_as_float(q.z)), __float_as_uint(a.w + __uint_as_float(q.w)));
+        out = make_uint4(__float_as_uint(g[0].x + __uint_as_float(q.x)), __float_as_uint(g[0].y + __uint_as_float(q.y)),
+                         __float_as_uint(g[0].z + __uint_as_float(q.z)), __float_as_uint(g[0].w + __uint_as_float(q.w)));
       } else {
-        const float4 a = *reinterpret_cast<const float4*>(from + (((2 * unit) ^ (r & 7)) << 4));
-        const float4 b = *reinterpret_cast<const float4*>(from + (((2 * unit + 1) ^ (r & 7)) << 4));
         const float2 q0 = unpack2<T>(q.x), q1 = unpack2<T>(q.y), q2 = unpack2<T>(q.z), q3 = unpack2<T>(q.w);
-        out = make_uint4(pack2<T>(a.x + q0.x, a.y + q0.y), pack2<T>(a.z + q1.x, a.w + q1.y),
-                         pack2<T>(b.x + q2.x, b.y + q2.y), pack2<T>(b.z + q3.x, b.w + q3.y));
+        out = make_uint4(pack2<T>(g[0].x + q0.x, g[0].y + q0.y), pack2<T>(g[0].z + q1.x, g[0].w + q1.y),
+                         pack2<T>(g[1].x + q2.x, g[1].y + q2.y), pack2<T>(g[1].z + q3.x, g[1].w + q3.y));
       }
-      if (i0 + r < sg.M && j < sg.N)
-        __stcs(reinterpret_cast<uint4*>(static_cast<char*>(p.y) +
-                                        (static_cast<int64_t>(i0 + r) * sg.N + j) * (Box::WIDE ? 4 : 2)),
-               out);
+      if (live) __stcs(reinterpret_cast<uint4*>(static_cast<char*>(p.y) + at * (Box::WIDE ? 4 : 2)), out);
     }
     __syncwarp();
     return;
   }
+#pragma unroll
+  for (int k = 0; k < 32; ++k) v[k] = ffn_act<ACT>(v[k]);
   uint32_t w[16];
 #pragma unroll
   for (int k = 0; k < 16; ++k) w[k] = pack2<T>(v[2 * k], v[2 * k + 1]);
@@ -390,7 +377,6 @@ __device__ __forceinline__ void linear_box(const BlockGemmParams& p, const GemmS
   __syncwarp();
   if (lane == 0) {
     tma_store_2d(&sg.out[0], stage, j0, i0);
-    if (ACT != ACT_NONE && p.keep) tma_store_2d(&sg.out[1], stage + EPI_BUF_BYTES, j0, i0);
     bulk_commit_group();
   }
 }

@@ -64,7 +64,7 @@ cudaError_t ffn_few_forward(const void* x, int64_t ldx, const void* w_gate, cons
                             cudaStream_t stream);
 
 // The linear layer's y = act(x w^T + bias) + residual for as few tokens, and
-// x w^T + bias in pre where that is not NULL. y and residual are fp32 where
+// x w^T + bias in fp32 in pre where that is not NULL. y and residual are fp32 where
 // `wide`, else of dtype.
 struct LinearFew {
   const void* x;
@@ -74,7 +74,7 @@ struct LinearFew {
   const void* residual;
   int64_t ld_residual;
   void* y;
-  void* pre;
+  float* pre;
   int tokens, n, k;
   bool wide;
 };

@@ -37,7 +37,7 @@ struct FewParams {
   const float* bias = nullptr;
   const void* residual = nullptr;
   int64_t ld_residual = 0;
-  void* pre = nullptr;
+  float* pre = nullptr;
   bool wide = false;
 };
 
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(FEW_THREADS, USE == FEW_LINEAR && NT == 1 ? 4 
   if constexpr (USE == FEW_LINEAR) {
     const int64_t at = static_cast<int64_t>(t) * p.rows + row;
     if (p.bias != nullptr) v += p.bias[row];
-    if (p.pre != nullptr) static_cast<T*>(p.pre)[at] = from_f32<T>(v);
+    if (p.pre != nullptr) p.pre[at] = v;
     v = ffn_act<ACT>(v);
     const int64_t from = t * p.ld_residual + row;
     if (p.residual != nullptr)

@@ -11,9 +11,10 @@
 // the bias' gradient as sums over blocks of rows, which a second kernel adds
 // in order.
 //
-// For an activation g is kept in the operands' type: its rounding moves dg by
-// |g act''(g) / act'(g)| of a step, less than dg's own rounding for all but the
-// few elements around a root of act'.
+// For an activation g is kept in fp32: the bias' gradient is an fp32 sum, and
+// with g in 16 bits it was off by 0.0026 (bf16), a thousand times its own
+// rounding. dg is rounded to 16 bits only as an operand; db sums what it was
+// before.
 #include "block_gemm.cuh"
 #include "linear.cuh"
 
@@ -31,7 +32,7 @@ constexpr int DG_COLS = 256;  // columns of a CTA: 32 threads of eight, eight ro
 struct DgParams {
   const void* dy;
   int64_t lddy;
-  const void* g;    // tokens x n, or NULL
+  const float* g;   // tokens x n, or NULL
   void* dg;         // tokens x n, or NULL where dy is dg
   float* partial;   // [row block][n], or NULL
   uint32_t* zero;   // counters to clear for the products
@@ -56,12 +57,12 @@ __global__ void __launch_bounds__(256) linear_dg_kernel(const __grid_constant__ 
     constexpr int AHEAD = 4;
     for (int64_t r = r0 + part; r < r1; r += 8 * AHEAD) {
       Raw8<DY> dy[AHEAD];
-      Raw8<T> g[AHEAD];
+      Raw8<float> g[AHEAD];
 #pragma unroll
       for (int a = 0; a < AHEAD; ++a)
         if (r + 8 * a < r1) {
           dy[a].load(static_cast<const DY*>(p.dy) + (r + 8 * a) * p.lddy + col);
-          if (ACT != ACT_NONE) g[a].load(static_cast<const T*>(p.g) + (r + 8 * a) * p.n + col);
+          if (ACT != ACT_NONE) g[a].load(p.g + (r + 8 * a) * p.n + col);
         }
 #pragma unroll
       for (int a = 0; a < AHEAD; ++a) {
@@ -230,7 +231,7 @@ extern "C" int prm_linear_sizes(int64_t tokens, int64_t n, int64_t k, size_t* fo
 }
 
 extern "C" int prm_linear_forward(const void* x, int64_t ldx, const void* weight, const float* bias,
-                                  const void* residual, int64_t ld_residual, void* y, int y_dtype, void* pre,
+                                  const void* residual, int64_t ld_residual, void* y, int y_dtype, float* pre,
                                   void* workspace, size_t workspace_bytes, int64_t tokens, int64_t n, int64_t k,
                                   int act, int dtype, void* stream) {
   using namespace prm;
@@ -269,11 +270,10 @@ extern "C" int prm_linear_forward(const void* x, int64_t ldx, const void* weight
   p.residual = residual;
   p.ld_residual = ld_residual;
   p.y = y;
-  p.keep = pre != nullptr;
+  p.pre = pre;
   GemmSegment s{};
   if (!encode(&s.a[0], x, dtype, tokens, k, ldx, MAP_ROWS) || !encode(&s.b[0], weight, dtype, n, k, k, MAP_ROWS) ||
-      (!wide && !encode(&s.out[0], y, dtype, tokens, n, n, MAP_STORE)) ||
-      (pre != nullptr && !encode(&s.out[1], pre, dtype, tokens, n, n, MAP_STORE)))
+      (!wide && !encode(&s.out[0], y, dtype, tokens, n, n, MAP_STORE)))
     return PRM_ERR_CUDA;
   s.whole = static_cast<int>(sz.y.whole);
   s.splits = sz.y.splits;
@@ -291,7 +291,7 @@ extern "C" int prm_linear_forward(const void* x, int64_t ldx, const void* weight
 }
 
 extern "C" int prm_linear_backward(const void* dy, int64_t lddy, int dy_dtype, const void* x, int64_t ldx,
-                                   const void* weight, const void* pre, void* dx, void* dweight, float* dbias,
+                                   const void* weight, const float* pre, void* dx, void* dweight, float* dbias,
                                    void* workspace, size_t workspace_bytes, int64_t tokens, int64_t n, int64_t k,
                                    int act, int dtype, void* stream) {
   using namespace prm;

@@ -25,7 +25,7 @@ struct SkinnyCall {
   const void* residual;
   int64_t ld_residual;
   void* y;
-  void* pre;
+  float* pre;
   int act, dtype;
   bool wide;           // y and residual are fp32
   int* err;

@@ -38,7 +38,7 @@ struct SkinnyParams {
   const void* residual;
   int64_t ld_residual;
   void* y;        // tokens x rows
-  void* pre;      // act's argument, or NULL
+  float* pre;     // act's argument, or NULL
   int* err;
 };
 
@@ -80,7 +80,7 @@ __device__ __forceinline__ void skinny_out(const SkinnyParams& p, int token, int
   const int64_t at = static_cast<int64_t>(token) * p.rows + row;
   v.x += bias.x, v.y += bias.y, v.z += bias.z, v.w += bias.w;
   if (ACT != ACT_NONE && p.pre != nullptr)
-    *reinterpret_cast<uint2*>(static_cast<T*>(p.pre) + at) = make_uint2(pack2<T>(v.x, v.y), pack2<T>(v.z, v.w));
+    *reinterpret_cast<float4*>(p.pre + at) = v;
   v = make_float4(ffn_act<ACT>(v.x) + res.x, ffn_act<ACT>(v.y) + res.y, ffn_act<ACT>(v.z) + res.z,
                   ffn_act<ACT>(v.w) + res.w);
   if (WIDE) *reinterpret_cast<float4*>(static_cast<float*>(p.y) + at) = v;

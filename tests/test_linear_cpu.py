@@ -57,7 +57,7 @@ def test_linear_refusals(lib):
     assert fwd(r=16, ldr=56) == N.PRM_ERR_INVALID_ARG and fwd(r=16, ldr=68) == N.PRM_ERR_ALIGNMENT
     assert fwd(y=None) == N.PRM_ERR_INVALID_ARG and fwd(b=8) == N.PRM_ERR_ALIGNMENT
     # some tiles behind a full round, split along k
-    assert fwd(T=2304, n=2304, k=2304, ldx=2304, size=10) == N.PRM_ERR_WORKSPACE
+    assert fwd(T=5120, n=4096, k=2048, ldx=2048, size=10) == N.PRM_ERR_WORKSPACE
     assert back(dy=None) == N.PRM_ERR_INVALID_ARG and back(lddy=56) == N.PRM_ERR_INVALID_ARG
     assert back(pre=None) == N.PRM_ERR_INVALID_ARG and back(dyt=N.PRM_FP16) == N.PRM_ERR_INVALID_ARG
     assert back(lddy=68) == N.PRM_ERR_ALIGNMENT and back(dx=8) == N.PRM_ERR_ALIGNMENT
