@@ -15,7 +15,8 @@
  * with nothing to do return PRM_OK; pointers may then be NULL. Sums are held
  * in fp32 and taken in an order fixed by the sizes: the same inputs give the
  * same bits. The first call of each kind on a device sets kernels up: make it
- * before any stream capture. Calls on different streams may overlap when
+ * before any stream capture. An output overlaps no input and no other output,
+ * except where its section allows it. Calls on different streams may overlap when
  * their outputs and workspaces differ. prm_blocks_sync_status reads the error
  * word of these calls too.
  */

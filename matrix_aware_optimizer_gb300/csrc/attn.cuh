@@ -196,7 +196,8 @@ __device__ __forceinline__ void att_mma_cols(uint32_t d, uint32_t a, const uint8
 // A warp's 32 rows x 64 elements of a result go through 4 KB of shared memory
 // (1024-byte aligned, in the swizzle of a 128-byte box) and out as one TMA
 // store: rows stored by their threads cost 32 cache lines an instruction (the
-// last 128 x 128 block of a forward item 6000 cycles that way, 700 this way).
+// last 128 x 128 block of a forward item 3600 - 6000 cycles that way, 2100 -
+// 2500 this way, its loads from tensor memory included).
 // Rows outside the tensor and elements behind the head are not written.
 constexpr uint32_t ATT_STAGE = 32 * 128;
 

@@ -9,6 +9,11 @@
 // products' rows) and its own running maximum and sum. The warps' results are
 // joined in shared memory, the ranges' by attn_join. Two CTAs share an SM, so
 // that one's start and end are covered by the other's loads.
+//
+// 16 tokens, 16 heads of 128 on 4 key heads, 1 .. 4096 keys each (67 MB), bf16:
+// 22 - 23 us with the join, this kernel 17 of them (3.9 TB/s, 58 % of the copy
+// rate: the sequences' lengths differ, and a launch this short starts and ends
+// its loads at half speed).
 #include <algorithm>
 #include <type_traits>
 

