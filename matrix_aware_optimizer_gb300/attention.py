@@ -20,6 +20,7 @@ _ROTARY = struct.Struct("=13q4ifi")  # prm_rotary_desc
 assert _ROTARY.size == N.ctypes.sizeof(N.prm_rotary_desc)
 _ATTN = struct.Struct("=30qQ2ifi")  # prm_attention_desc
 assert _ATTN.size == N.ctypes.sizeof(N.prm_attention_desc)
+_FLOAT_END = 2.0 ** 128 * (1.0 - 2.0 ** -25)  # rounds to an infinity of fp32
 _LINEAR_ACT = {None: N.PRM_ACT_NONE, **_ACT}
 _POSITION_BYTES = {torch.int64: 8, torch.int32: 4}
 _LAYOUT = {"half": N.PRM_ROTARY_HALF, "interleaved": N.PRM_ROTARY_INTERLEAVED}
@@ -204,8 +205,8 @@ def rotary_plan(dim: int, base: float = 10000.0, layout: str = "half", scaling: 
         raise ValueError("ramp needs 0 <= slow < fast and a trained length")
     if amplitude is None:
         amplitude = 0.1 * math.log(factor) + 1.0 if scaling == "ramp" and factor > 1.0 else 1.0
-    if not math.isfinite(amplitude):
-        raise ValueError("amplitude must be finite")
+    if not abs(amplitude) < _FLOAT_END:
+        raise ValueError("amplitude must be finite in fp32")
     turns = _rotary_turns(dim, float(base), scaling, float(factor), trained_length, fast, slow)
     return RotaryPlan(torch.tensor(turns, dtype=torch.int64, device=device), dim, layout, float(amplitude))
 
@@ -406,8 +407,8 @@ def _attention_check(q, k, v, key_lengths, scale):
         raise ValueError("key_lengths must be int32 or int64, one per sequence, on q's device")
     if scale is None:
         scale = head ** -0.5
-    elif not 0.0 < scale < math.inf:
-        raise ValueError("scale must be positive")
+    elif not 1.0 / _FLOAT_END < scale < _FLOAT_END:
+        raise ValueError("scale must be positive and finite in fp32")
     return device, scale
 
 
@@ -485,7 +486,8 @@ def cross_attention_backward(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
     """Gradients of cross_attention: (dq, dk, dv), all of q's type, from that
     of its result and the o and saved that it returned; the other arguments are
     those of that pass. Heads that share keys add to the same dk and dv; rows
-    behind a sequence's last key are zero. grads: three tensors to write them
+    behind a sequence's last key are zero. P (do v^T - sum of do o) is rounded to
+    q's type on the way: fp16 gradients are scaled so that it stays below 65504. grads: three tensors to write them
     into (slices of a fused projection's gradient, say), which do not overlap
     each other or the inputs.
     """
@@ -496,11 +498,13 @@ def cross_attention_backward(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
     b, lq, h, d = q.shape
     lk, hkv = k.shape[1], k.shape[2]
     lse = saved.lse
-    if lse.shape != (b, h, lq) or lse.dtype is not torch.float32 or lse.get_device() != device             or not lse.is_contiguous() or saved.scale != scale or saved.keys != lk:
+    if lse.shape != (b, h, lq) or lse.dtype is not torch.float32 or lse.get_device() != device \
+            or not lse.is_contiguous() or saved.scale != scale or saved.keys != lk:
         raise ValueError("saved does not belong to this pass")
     if grads is not None:
         for g, t in zip(grads, (q, k, v), strict=True):
-            if g.shape != t.shape or g.dtype is not t.dtype or g.get_device() != device                     or (g.numel() and not (_usable(g) and _distinct(g))):
+            if g.shape != t.shape or g.dtype is not t.dtype or g.get_device() != device \
+                    or (g.numel() and not (_usable(g) and _distinct(g))):
                 raise ValueError("grads must have the shapes and type of q, k and v, consecutive elements and "
                                  "16-byte rows")
         if len({g.data_ptr() for g in grads if g.numel()}) < sum(g.numel() > 0 for g in grads):

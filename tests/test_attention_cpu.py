@@ -86,6 +86,14 @@ def _rotary(**kw):
     return N.prm_rotary_desc(*(v[k] for k, _ in N.prm_rotary_desc._fields_))
 
 
+def test_amplitudes_beyond_fp32_are_refused():
+    assert attention.rotary_plan(8, amplitude=3.4e38, device="cpu").amplitude == 3.4e38
+    for amplitude in (3.5e38, -1e300, float("inf")):
+        with pytest.raises(ValueError):
+            attention.rotary_plan(8, amplitude=amplitude, device="cpu")
+
+
+
 def test_rotary_refusals(lib):
     def call(x=16, pos=16, turns=16, y=32, **kw):
         return lib.prm_rotary(_rotary(**kw), x, pos, turns, y, None)

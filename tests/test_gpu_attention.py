@@ -6,6 +6,8 @@ Tolerances. U is the largest relative error of one rounding to a type: half a
 step, 2^-9 of the value's power of two, so at most 2^-8 of the value for bf16
 (2^-11 for fp16, 2^-24 for fp32). fp32 arithmetic adds its own steps of 2^-24,
 counted where they matter."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -454,3 +456,28 @@ def test_attention_refuses():
         args.update(bad)
         with pytest.raises(ValueError):
             prm.cross_attention_backward(**args)
+
+
+def test_scales_beyond_fp32_are_refused():
+    q, k, v = (torch.zeros(1, n, 1, 8, dtype=torch.bfloat16, device="cuda") for n in (2, 3, 3))
+    for scale in (0.0, -1.0, 1e-50, 3.5e38, 1e300, math.inf, math.nan):
+        with pytest.raises(ValueError):
+            prm.cross_attention(q, k, v, scale=scale)
+
+
+def test_attention_gradients_of_one_key():
+    # softmax of one score is one: o is v, dv the sum of do, dq and dk zero but for delta's rounding
+    q, k, v, do = _attention_inputs(3, 70, 1, 4, 2, 64)
+    o, saved = prm.cross_attention(q, k, v, save=True)
+    assert torch.equal(o, v.repeat_interleave(2, 2).expand_as(o))
+    dq, dk, dv = prm.cross_attention_backward(do, q, k, v, o, saved)
+    want = do.double().sum(1, keepdim=True).unflatten(2, (2, 2)).sum(3)
+    # 140 additions in fp32 and the rounding to bf16
+    size = do.double().abs().sum(1, keepdim=True).unflatten(2, (2, 2)).sum(3)
+    assert ((dv.double() - want).abs() <= 2.0 ** -8 * want.abs() + 140 * 2.0 ** -23 * size).all()
+    # do . v is summed twice, in two orders: 64 additions each, of products of up to 16 sizes (P is one to 2^-22)
+    off = 2 * 65 * 2.0 ** -23 * (do.double().abs() * v.repeat_interleave(2, 2).double().abs()).sum(3)
+    scale = 64 ** -0.5
+    assert (dq.double().abs() <= 1.01 * scale * off[..., None] * k.repeat_interleave(2, 2).double().abs() + 1e-30).all()
+    bound = (off[..., None] * q.double().abs()).sum(1, keepdim=True).unflatten(2, (2, 2)).sum(3)
+    assert (dk.double().abs() <= 1.01 * scale * bound + 1e-30).all()
