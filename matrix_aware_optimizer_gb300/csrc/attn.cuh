@@ -193,17 +193,17 @@ __device__ __forceinline__ void att_mma_cols(uint32_t d, uint32_t a, const uint8
 }
 
 // ------------------------------------------------------------------ output
-// A warp's 32 rows x 64 elements of a result go through 4 KB of shared memory
-// (1024-byte aligned, in the swizzle of a 128-byte box) and out as one TMA
-// store: rows stored by their threads cost 32 cache lines an instruction (the
-// last 128 x 128 block of a forward item 3600 - 6000 cycles that way, 2100 -
-// 2500 this way, its loads from tensor memory included).
-// Rows outside the tensor and elements behind the head are not written.
-constexpr uint32_t ATT_STAGE = 32 * 128;
+// A warp's 32 rows x 32 elements of a result go through 2 KB of shared memory
+// (in the swizzle of a 64-byte box) and out as one TMA store: rows stored by
+// their threads cost 32 cache lines an instruction (128 x 128 elements 3600 -
+// 6000 cycles that way). Rows outside the tensor and elements behind the head
+// are not written.
+constexpr uint32_t ATT_STAGE = 32 * 64;
+constexpr int ATT_STAGE_COLS = 32;
 
-// Eight elements of the lane's row, the unit-th of its 128 bytes.
-__device__ __forceinline__ void att_stage_row8(uint8_t* stage, int lane, int unit, const uint4& v) {
-  *reinterpret_cast<uint4*>(stage + lane * 128 + ((unit ^ (lane & 7)) << 4)) = v;
+// Where the unit-th eight elements of the lane's row lie.
+__device__ __forceinline__ uint32_t att_stage_at(int lane, int unit) {
+  return static_cast<uint32_t>(lane * 64 + ((unit ^ ((lane >> 1) & 3)) << 4));
 }
 __device__ __forceinline__ void tma_store_4d(const CUtensorMap* tm, const void* src, int x, int y, int z, int w) {
   asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(

@@ -194,12 +194,6 @@ __device__ __forceinline__ void store_row16(T* out, float* part, const float (&v
   }
 }
 
-// Where a thread's row of 32 gradient elements lies in its warp's 2 KB, in the
-// swizzle of a 64-byte box.
-__device__ __forceinline__ uint32_t dq_stage_at(int lane, int unit) {
-  return static_cast<uint32_t>(lane * 64 + ((unit ^ ((lane >> 1) & 3)) << 4));
-}
-
 template <typename T, int DP, bool DQ>
 __global__ void __launch_bounds__(BWD_THREADS, 1) attn_dkv_kernel(const __grid_constant__ DkvParams p) {
   using Shape = DkvShape<DP, DQ>;
@@ -503,7 +497,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) attn_dkv_kernel(const __grid_c
             // These 32 columns of 32 rows of the last round's dQ go out of the memory of its Q.
             if (!(ok = wait(dq_full, (rounds - 1) & 1u))) break;
             const uint32_t slot = (n - 2) % SLOTS;
-            uint8_t* stage = ring + slot * TILE + warp * 2048;
+            uint8_t* stage = ring + slot * TILE + warp * ATT_STAGE;
             const bool some = quarter * 32 < p.h.head;  // (the same in all threads of a warp)
             if (some) {
               float v[32];
@@ -515,7 +509,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) attn_dkv_kernel(const __grid_c
                 for (int e = 0; e < 8; ++e) x[e] = v[u + e] * p.scale;
                 Raw8<T> r;
                 r.set(x);
-                *reinterpret_cast<uint4*>(stage + dq_stage_at(lane, u / 8)) = r.a;
+                *reinterpret_cast<uint4*>(stage + att_stage_at(lane, u / 8)) = r.a;
               }
               fence_proxy_async_smem();
             }
@@ -1105,7 +1099,7 @@ cudaError_t attn_backward(const AttCall& c, const void* grad_o, const void* q, c
   const bool k_ok = att_encode(&a.k, k, c.dtype, h.batch, h.keys, h.kv_heads, h.head, c.k, 1, ATT_ROWS) &&
                     att_encode(&a.v, v, c.dtype, h.batch, h.keys, h.kv_heads, h.head, c.v, 1, ATT_ROWS);
   if (!q_ok || !k_ok ||
-      (s.one && !att_encode(&a.dq, dq, c.dtype, h.batch, h.queries, h.heads, h.head, c.dq, pack, 32 / pack, 32)))
+      (s.one && !att_encode(&a.dq, dq, c.dtype, h.batch, h.queries, h.heads, h.head, c.dq, pack, 32 / pack, ATT_STAGE_COLS)))
     return cudaErrorInvalidValue;
   a.dq_out = dq;
   a.dq_strides = c.dq;

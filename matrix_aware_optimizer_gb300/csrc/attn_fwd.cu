@@ -101,7 +101,7 @@ struct FwdShape {
   static constexpr int STAGES = DP == 128 ? 4 : 8;  // of one key or value tile
   static constexpr uint32_t TILE = ATT_TILE<DP>;
   static constexpr size_t BARRIERS = 512;
-  static constexpr size_t SMEM = 1024 + (2 + STAGES) * TILE + FWD_WARPS * ATT_STAGE + BARRIERS;
+  static constexpr size_t SMEM = 1024 + (2 + STAGES) * TILE + FWD_WARPS * 2 * ATT_STAGE + BARRIERS;
 };
 static_assert(FwdShape<128>::SMEM <= 232448 && FwdShape<64>::SMEM <= 232448, "shared memory above 227 KB");
 
@@ -112,7 +112,8 @@ struct FwdParams {
   float* lse;       // [batch][heads][queries], or NULL
   float* part_o;    // [slot][2 ATT_ROWS][head], each part normalised
   float* part_lse;  // [slot][2 ATT_ROWS]
-  int blocks;       // pairs of query tiles
+  Divisor blocks;   // pairs of query tiles
+  Divisor groups;
   AttShare share;
   uint32_t items;
   int mma_k;        // 16-element steps of a head
@@ -130,13 +131,12 @@ struct FwdItem {
 
 __device__ __forceinline__ FwdItem fwd_item(const FwdParams& p, uint32_t item) {
   FwdItem it;
-  const uint32_t blocks = p.blocks, groups = p.h.groups;
   const AttUnit u = att_unit(p.share, item);
   it.slot = u.slot;
-  it.block = static_cast<int>(u.unit % blocks);
-  const uint32_t bg = u.unit / blocks;
-  it.group = static_cast<int>(bg % groups);
-  it.b = static_cast<int>(bg / groups);
+  const uint32_t bg = p.blocks.quotient(u.unit), b = p.groups.quotient(bg);
+  it.block = static_cast<int>(u.unit - bg * p.blocks.d);
+  it.group = static_cast<int>(bg - b * p.groups.d);
+  it.b = static_cast<int>(b);
   it.length = att_length(p.lengths, it.b, p.h.keys);
   const int tiles = (it.length + ATT_ROWS - 1) / ATT_ROWS;
   it.k0 = min(u.first, tiles);
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) attn_fwd_kernel(const __grid_c
   uint8_t* sQ = smem;
   uint8_t* sKV = smem + 2 * TILE;
   uint8_t* sOut = sKV + STAGES * TILE;
-  uint64_t* kv_full = reinterpret_cast<uint64_t*>(sOut + FWD_WARPS * ATT_STAGE);
+  uint64_t* kv_full = reinterpret_cast<uint64_t*>(sOut + FWD_WARPS * 2 * ATT_STAGE);
   uint64_t* kv_empty = kv_full + STAGES;
   uint64_t* q_full = kv_empty + STAGES;
   uint64_t* q_empty = q_full + 2;
@@ -391,16 +391,20 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) attn_fwd_kernel(const __grid_c
     // ended by then; its O is read first, so that the next product may begin.
     // (A single place writes rows, also those of items without keys and, in a last round without an item, the last
     // one's: a second copy of that code costs registers that spill where there is hardly any L1.)
-    uint32_t held = 0;  // its number + 1
+    bool held = false;
+    FwdItem last{};
     float held_m = 0.f, held_l = 0.f;
+    uint32_t pieces = 0;  // stores so far, from two buffers in turn
     bool ok = true;
     for (uint32_t item = blockIdx.x; ok; item += gridDim.x) {
       const bool end = item >= p.items;
       int n = 0, valid = 0;
       bool mine = false;        // the item has rows of this tile
       bool valid_ends = false;  // its sequence ends before the tensor
+      FwdItem now{};
       if (!end) {
-        const FwdItem it = fwd_item(p, item);
+        now = fwd_item(p, item);
+        const FwdItem& it = now;
         mine = t < it.tiles;
         n = max(it.n, 0);
         valid = it.length - it.k0 * ATT_ROWS;
@@ -485,8 +489,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) attn_fwd_kernel(const __grid_c
           valid -= ATT_ROWS;
           ++steps;
         }
-        if (j == 0 && held > 0) {
-          const FwdItem it = fwd_item(p, held - 1);
+        if (j == 0 && held) {
+          const FwdItem& it = last;
           const bool some = it.n > 0;
           // (with keys in this item its first step was counted already)
           if (some && !(ok = wait(&pv_done[t], (steps - (n > 0 ? 2 : 1)) & 1u))) break;
@@ -503,24 +507,22 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) attn_fwd_kernel(const __grid_c
               p.lse[at] = lse;
           }
           float* part = p.part_o + static_cast<int64_t>(it.slot * (2 * ATT_ROWS) + t * ATT_ROWS + row) * p.h.head;
-          uint8_t* stage = sOut + warp * ATT_STAGE;
           const int first = token - (lane >> p.h.pack_log2);  // the warp's first token
 #pragma unroll 1
-          for (int c = 0; c < p.h.head; c += 64) {
-            // (one load: with four of 16 columns, each waited for, this took 1060 cycles)
-            float o[64];
+          for (int c = 0; c < p.h.head; c += ATT_STAGE_COLS) {
+            float o[ATT_STAGE_COLS];
             __syncwarp();
-            if (some) tmem_load_64cols(t_o + c, o);
-            if (some && c + 64 >= p.h.head) {  // O has been read
+            if (some) tmem_load_32cols(t_o + c, o);
+            if (some && c + ATT_STAGE_COLS >= p.h.head) {  // O has been read
               tc_fence_before_sync();
               __syncwarp();
               if (lane == 0) mbar_arrive(&o_empty[t]);
             }
 #pragma unroll
-            for (int i = 0; i < 64; ++i) o[i] = some ? o[i] * inv : 0.f;
+            for (int i = 0; i < ATT_STAGE_COLS; ++i) o[i] = some ? o[i] * inv : 0.f;
             if (it.slot >= 0) {
 #pragma unroll
-              for (int i = 0; i < 64; i += 8) {
+              for (int i = 0; i < ATT_STAGE_COLS; i += 8) {
                 if (c + i >= p.h.head || !live) break;
                 float4* to = reinterpret_cast<float4*>(part + c + i);
                 to[0] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
@@ -528,26 +530,30 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) attn_fwd_kernel(const __grid_c
               }
               continue;
             }
-            if (lane == 0) bulk_wait_group_read<0>();
+            uint8_t* stage = sOut + (warp * 2 + (pieces & 1u)) * ATT_STAGE;
+            if (lane == 0) bulk_wait_group_read<1>();  // the store before the last one has read this buffer
             __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 64; i += 8) {
+            for (int i = 0; i < ATT_STAGE_COLS; i += 8) {
               if (c + i >= p.h.head) break;
-              att_stage_row8(stage, lane, i / 8, make_uint4(pack2<T>(o[i], o[i + 1]), pack2<T>(o[i + 2], o[i + 3]),
-                                                            pack2<T>(o[i + 4], o[i + 5]), pack2<T>(o[i + 6], o[i + 7])));
+              *reinterpret_cast<uint4*>(stage + att_stage_at(lane, i / 8)) =
+                  make_uint4(pack2<T>(o[i], o[i + 1]), pack2<T>(o[i + 2], o[i + 3]), pack2<T>(o[i + 4], o[i + 5]),
+                             pack2<T>(o[i + 6], o[i + 7]));
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0 && first < p.h.queries) {
-              tma_store_4d(&p.o, stage, c, it.group << p.h.pack_log2, first, it.b);
+            if (lane == 0) {
+              if (first < p.h.queries) tma_store_4d(&p.o, stage, c, it.group << p.h.pack_log2, first, it.b);
               bulk_commit_group();
             }
+            ++pieces;
           }
-          held = 0;
+          held = false;
         }
       } while (++j < n);
       if (end || !ok) break;
-      held = item + 1;
+      held = true;
+      last = now;
       held_m = m;
       held_l = l;
     }
@@ -653,7 +659,7 @@ __global__ void __launch_bounds__(256) attn_join_units_kernel(const __grid_const
   const int i = blockIdx.x * 256 + threadIdx.x;
   if (i >= 2 * ATT_ROWS * vectors) return;
   const int row = i / vectors, vec = i - row * vectors;
-  const uint32_t unit = p.f.share.whole + blockIdx.y, blocks = p.f.blocks, groups = h.groups;
+  const uint32_t unit = p.f.share.whole + blockIdx.y, blocks = p.f.blocks.d, groups = h.groups;
   const int block = static_cast<int>(unit % blocks), group = static_cast<int>(unit / blocks % groups);
   const int b = static_cast<int>(unit / blocks / groups);
   const int tile = block * 2 + row / ATT_ROWS, in_tile = row % ATT_ROWS;
@@ -706,7 +712,8 @@ cudaError_t attn_forward(const AttCall& c, const void* q, const void* k, const v
   p.h = c.h;
   p.lengths = c.lengths;
   p.lse = lse;
-  p.blocks = (c.h.query_tiles() + 1) / 2;
+  p.blocks = Divisor::of(static_cast<uint32_t>((c.h.query_tiles() + 1) / 2));
+  p.groups = Divisor::of(static_cast<uint32_t>(c.h.groups));
   p.share = att_forward_share(c.h, c.num_sms);
   p.items = p.share.items();
   p.mma_k = (c.h.head + 15) / 16;
@@ -718,7 +725,7 @@ cudaError_t attn_forward(const AttCall& c, const void* q, const void* k, const v
     p.part_lse = p.part_o + static_cast<int64_t>(p.share.rest) * p.share.parts * 2 * ATT_ROWS * c.h.head;
   const int pack = 1 << c.h.pack_log2;
   if (!att_encode(&p.q, q, c.dtype, c.h.batch, c.h.queries, c.h.heads, c.h.head, c.q, pack, ATT_ROWS / pack) ||
-      !att_encode(&p.o, o, c.dtype, c.h.batch, c.h.queries, c.h.heads, c.h.head, c.o, pack, 32 / pack) ||
+      !att_encode(&p.o, o, c.dtype, c.h.batch, c.h.queries, c.h.heads, c.h.head, c.o, pack, 32 / pack, ATT_STAGE_COLS) ||
       !att_encode(&p.k, k, c.dtype, c.h.batch, c.h.keys, c.h.kv_heads, c.h.head, c.k, 1, ATT_ROWS) ||
       !att_encode(&p.v, v, c.dtype, c.h.batch, c.h.keys, c.h.kv_heads, c.h.head, c.v, 1, ATT_ROWS))
     return cudaErrorInvalidValue;

@@ -258,4 +258,17 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* tm, const void* 
                : "memory");
 }
 
+// Quotient of n < 2^31 by a divisor of 1 .. 2^31: floor(n m / 2^(32 + s)) with
+// s = ceil(log2 d) - 1 and m = floor(2^(32 + s) / d) + 1 (Granlund and
+// Montgomery, 1994: exact as m d - 2^(32 + s) <= d <= 2^(s + 1)).
+struct Divisor {
+  uint32_t d, m, s;
+  static Divisor of(uint32_t d) {
+    uint32_t s = 0;
+    while ((uint64_t(1) << (s + 1)) < d) ++s;
+    return {d, d == 1 ? 0u : static_cast<uint32_t>((uint64_t(1) << (32 + s)) / d + 1), s};
+  }
+  __device__ __forceinline__ uint32_t quotient(uint32_t n) const { return d == 1 ? n : __umulhi(n, m) >> s; }
+};
+
 }  // namespace prm
