@@ -387,175 +387,150 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) attn_fwd_kernel(const __grid_c
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
-    // The last item's rows are written behind the next one's first exponentials, so that its last product has
-    // ended by then; its O is read first, so that the next product may begin.
-    // (A single place writes rows, also those of items without keys and, in a last round without an item, the last
-    // one's: a second copy of that code costs registers that spill where there is hardly any L1.)
-    bool held = false;
-    FwdItem last{};
-    float held_m = 0.f, held_l = 0.f;
     uint32_t pieces = 0;  // stores so far, from two buffers in turn
     bool ok = true;
-    for (uint32_t item = blockIdx.x; ok; item += gridDim.x) {
-      const bool end = item >= p.items;
-      int n = 0, valid = 0;
-      bool mine = false;        // the item has rows of this tile
-      bool valid_ends = false;  // its sequence ends before the tensor
-      FwdItem now{};
-      if (!end) {
-        now = fwd_item(p, item);
-        const FwdItem& it = now;
-        mine = t < it.tiles;
-        n = max(it.n, 0);
-        valid = it.length - it.k0 * ATT_ROWS;
-        valid_ends = it.length < p.h.keys;
-        if (!mine) {
-          kv += 2 * n;
+    for (uint32_t item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
+      const FwdItem it = fwd_item(p, item);
+      const int n = max(it.n, 0);
+      if (t >= it.tiles) {
+        kv += 2 * n;
+        continue;
+      }
+      int valid = it.length - it.k0 * ATT_ROWS;
+      const bool valid_ends = it.length < p.h.keys;  // the sequence ends before the tensor
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < n; ++j) {
+        if (!(ok = wait(&s_full[t], steps & 1u))) break;
+        const bool whole = valid >= ATT_ROWS;  // (the same in all threads; most tiles are)
+        float s[64], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if (whole || valid > 64) {
+          tmem_load_64cols(t_s + 64, s);
+          if (!whole) hide(s, valid - 64);
+          top4(s, mx);
+        }
+        if (!whole && valid_ends) {
+          // what lies behind the last key must not meet its P of zero: infinities and NaN would remain. (Both
+          // tiles' threads write the same zeros, each before its own product. Behind the tensor's end TMA did.)
+          const uint32_t at = kv + 1;
+          if (!(ok = wait(&kv_full[at % STAGES], (at / STAGES) & 1u))) break;
+          uint4* v = reinterpret_cast<uint4*>(sKV + (at % STAGES) * TILE);
+          for (int i = valid * 8 + row; i < (valid + 15) / 16 * 128; i += 128)
+#pragma unroll
+            for (int c = 0; c < DP / 64; ++c) v[c * (ATT_CHUNK / 16) + i] = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        tmem_load_64cols(t_s, s);
+        if (!whole) hide(s, valid);
+        top4(s, mx);
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        if (j == 0) {
+          m = top;
+        } else {
+          const bool grows = (top - m) * p.scale_log2 > RESCALE_ABOVE;  // (from -inf: always)
+          if (__any_sync(0xffffffffu, grows)) {
+            const float factor = grows ? exp2_fast((m - top) * p.scale_log2) : 1.f;
+            if (grows) m = top;
+            l *= factor;
+            if (!(ok = wait(&pv_done[t], (steps - 1) & 1u))) break;
+#pragma unroll 1
+            for (int c = 0; c < p.mma_n; c += 16) {
+              float o[16];
+              tmem_load_16cols(t_o + c, o);
+              uint32_t w[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i] * factor);
+              tmem_store_16cols(t_o + c, w);
+            }
+            tmem_load_64cols(t_s, s);  // (not held meanwhile)
+            if (!whole) hide(s, valid);
+          }
+        }
+        const float base = m == -INFINITY ? 0.f : m * p.scale_log2;
+        const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2), nb2 = f2_pack(-base, -base);
+        uint64_t sum[2] = {0, 0};
+        // the first 64 keys' P goes over their S, and its product begins; then the others'
+        if (whole) {
+          exponentials<T, true>(s, sc2, nb2, sum, t_s, 64);
+          arrive(&p_full[2 * t]);
+          tmem_load_64cols(t_s + 64, s);
+          exponentials<T, true>(s, sc2, nb2, sum, t_s + 64, 64);
+        } else {
+          exponentials<T, false>(s, sc2, nb2, sum, t_s, valid);
+          arrive(&p_full[2 * t]);
+          if (valid > 64) {
+            tmem_load_64cols(t_s + 64, s);
+            hide(s, valid - 64);
+            exponentials<T, false>(s, sc2, nb2, sum, t_s + 64, valid - 64);
+          }
+        }
+        arrive(&p_full[2 * t + 1]);
+        const float2 total = f2_unpack(f2_add(sum[0], sum[1]));
+        l += total.x + total.y;
+        kv += 2;
+        valid -= ATT_ROWS;
+        ++steps;
+      }
+      if (!ok) break;
+      // The rows are written while the next item's first S is formed. (Written behind that item's first exponentials
+      // they hide the last product, but its own first product then waits for O: 16 x 1024 queries of 16 x 128 on 256
+      // keys 56 us that way, 50 this way.)
+      const bool some = n > 0;
+      if (some && !(ok = wait(&pv_done[t], (steps - 1) & 1u))) break;
+      const int token = (it.block * 2 + t) * p.h.tile_tokens() + (row >> p.h.pack_log2);
+      const int head = (it.group << p.h.pack_log2) + (row & ((1 << p.h.pack_log2) - 1));
+      const bool live = token < p.h.queries;
+      const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+      if (live) {
+        const int64_t at = (static_cast<int64_t>(it.b) * p.h.heads + head) * p.h.queries + token;
+        const float lse = some ? m * p.scale_log2 + log2f(l) : -INFINITY;
+        if (it.slot >= 0)
+          p.part_lse[it.slot * (2 * ATT_ROWS) + t * ATT_ROWS + row] = lse;
+        else if (p.lse != nullptr)
+          p.lse[at] = lse;
+      }
+      float* part = p.part_o + static_cast<int64_t>(it.slot * (2 * ATT_ROWS) + t * ATT_ROWS + row) * p.h.head;
+      const int first = token - (lane >> p.h.pack_log2);  // the warp's first token
+#pragma unroll 1
+      for (int c = 0; c < p.h.head; c += ATT_STAGE_COLS) {
+        float o[ATT_STAGE_COLS];
+        __syncwarp();
+        if (some) tmem_load_32cols(t_o + c, o);
+        if (some && c + ATT_STAGE_COLS >= p.h.head) {  // O has been read
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&o_empty[t]);
+        }
+#pragma unroll
+        for (int i = 0; i < ATT_STAGE_COLS; ++i) o[i] = some ? o[i] * inv : 0.f;
+        if (it.slot >= 0) {
+#pragma unroll
+          for (int i = 0; i < ATT_STAGE_COLS; i += 8) {
+            if (c + i >= p.h.head || !live) break;
+            float4* to = reinterpret_cast<float4*>(part + c + i);
+            to[0] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            to[1] = make_float4(o[i + 4], o[i + 5], o[i + 6], o[i + 7]);
+          }
           continue;
         }
+        uint8_t* stage = sOut + (warp * 2 + (pieces & 1u)) * ATT_STAGE;
+        if (lane == 0) bulk_wait_group_read<1>();  // the store before the last one has read this buffer
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < ATT_STAGE_COLS; i += 8) {
+          if (c + i >= p.h.head) break;
+          *reinterpret_cast<uint4*>(stage + att_stage_at(lane, i / 8)) =
+              make_uint4(pack2<T>(o[i], o[i + 1]), pack2<T>(o[i + 2], o[i + 3]), pack2<T>(o[i + 4], o[i + 5]),
+                         pack2<T>(o[i + 6], o[i + 7]));
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (first < p.h.queries) tma_store_4d(&p.o, stage, c, it.group << p.h.pack_log2, first, it.b);
+          bulk_commit_group();
+        }
+        ++pieces;
       }
-      float m = -INFINITY, l = 0.f;
-      int j = 0;
-      do {
-        if (n > 0) {
-          if (!(ok = wait(&s_full[t], steps & 1u))) break;
-          const bool whole = valid >= ATT_ROWS;  // (the same in all threads; most tiles are)
-          float s[64], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          if (whole || valid > 64) {
-            tmem_load_64cols(t_s + 64, s);
-            if (!whole) hide(s, valid - 64);
-            top4(s, mx);
-          }
-          if (!whole && valid_ends) {
-            // what lies behind the last key must not meet its P of zero: infinities and NaN would remain. (Both
-            // tiles' threads write the same zeros, each before its own product. Behind the tensor's end TMA did.)
-            const uint32_t at = kv + 1;
-            if (!(ok = wait(&kv_full[at % STAGES], (at / STAGES) & 1u))) break;
-            uint4* v = reinterpret_cast<uint4*>(sKV + (at % STAGES) * TILE);
-            for (int i = valid * 8 + row; i < (valid + 15) / 16 * 128; i += 128)
-#pragma unroll
-              for (int c = 0; c < DP / 64; ++c) v[c * (ATT_CHUNK / 16) + i] = make_uint4(0, 0, 0, 0);
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
-          tmem_load_64cols(t_s, s);
-          if (!whole) hide(s, valid);
-          top4(s, mx);
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          if (j == 0) {
-            m = top;
-          } else {
-            const bool grows = (top - m) * p.scale_log2 > RESCALE_ABOVE;  // (from -inf: always)
-            if (__any_sync(0xffffffffu, grows)) {
-              const float factor = grows ? exp2_fast((m - top) * p.scale_log2) : 1.f;
-              if (grows) m = top;
-              l *= factor;
-              if (!(ok = wait(&pv_done[t], (steps - 1) & 1u))) break;
-#pragma unroll 1
-              for (int c = 0; c < p.mma_n; c += 16) {
-                float o[16];
-                tmem_load_16cols(t_o + c, o);
-                uint32_t w[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i] * factor);
-                tmem_store_16cols(t_o + c, w);
-              }
-              tmem_load_64cols(t_s, s);  // (not held meanwhile)
-              if (!whole) hide(s, valid);
-            }
-          }
-          const float base = m == -INFINITY ? 0.f : m * p.scale_log2;
-          const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2), nb2 = f2_pack(-base, -base);
-          uint64_t sum[2] = {0, 0};
-          // the first 64 keys' P goes over their S, and its product begins; then the others'
-          if (whole) {
-            exponentials<T, true>(s, sc2, nb2, sum, t_s, 64);
-            arrive(&p_full[2 * t]);
-            tmem_load_64cols(t_s + 64, s);
-            exponentials<T, true>(s, sc2, nb2, sum, t_s + 64, 64);
-          } else {
-            exponentials<T, false>(s, sc2, nb2, sum, t_s, valid);
-            arrive(&p_full[2 * t]);
-            if (valid > 64) {
-              tmem_load_64cols(t_s + 64, s);
-              hide(s, valid - 64);
-              exponentials<T, false>(s, sc2, nb2, sum, t_s + 64, valid - 64);
-            }
-          }
-          arrive(&p_full[2 * t + 1]);
-          const float2 total = f2_unpack(f2_add(sum[0], sum[1]));
-          l += total.x + total.y;
-          kv += 2;
-          valid -= ATT_ROWS;
-          ++steps;
-        }
-        if (j == 0 && held) {
-          const FwdItem& it = last;
-          const bool some = it.n > 0;
-          // (with keys in this item its first step was counted already)
-          if (some && !(ok = wait(&pv_done[t], (steps - (n > 0 ? 2 : 1)) & 1u))) break;
-          const int token = (it.block * 2 + t) * p.h.tile_tokens() + (row >> p.h.pack_log2);
-          const int head = (it.group << p.h.pack_log2) + (row & ((1 << p.h.pack_log2) - 1));
-          const bool live = token < p.h.queries;
-          const float inv = held_l > 0.f || held_l != held_l ? 1.f / held_l : 0.f;
-          if (live) {
-            const int64_t at = (static_cast<int64_t>(it.b) * p.h.heads + head) * p.h.queries + token;
-            const float lse = some ? held_m * p.scale_log2 + log2f(held_l) : -INFINITY;
-            if (it.slot >= 0)
-              p.part_lse[it.slot * (2 * ATT_ROWS) + t * ATT_ROWS + row] = lse;
-            else if (p.lse != nullptr)
-              p.lse[at] = lse;
-          }
-          float* part = p.part_o + static_cast<int64_t>(it.slot * (2 * ATT_ROWS) + t * ATT_ROWS + row) * p.h.head;
-          const int first = token - (lane >> p.h.pack_log2);  // the warp's first token
-#pragma unroll 1
-          for (int c = 0; c < p.h.head; c += ATT_STAGE_COLS) {
-            float o[ATT_STAGE_COLS];
-            __syncwarp();
-            if (some) tmem_load_32cols(t_o + c, o);
-            if (some && c + ATT_STAGE_COLS >= p.h.head) {  // O has been read
-              tc_fence_before_sync();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&o_empty[t]);
-            }
-#pragma unroll
-            for (int i = 0; i < ATT_STAGE_COLS; ++i) o[i] = some ? o[i] * inv : 0.f;
-            if (it.slot >= 0) {
-#pragma unroll
-              for (int i = 0; i < ATT_STAGE_COLS; i += 8) {
-                if (c + i >= p.h.head || !live) break;
-                float4* to = reinterpret_cast<float4*>(part + c + i);
-                to[0] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-                to[1] = make_float4(o[i + 4], o[i + 5], o[i + 6], o[i + 7]);
-              }
-              continue;
-            }
-            uint8_t* stage = sOut + (warp * 2 + (pieces & 1u)) * ATT_STAGE;
-            if (lane == 0) bulk_wait_group_read<1>();  // the store before the last one has read this buffer
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < ATT_STAGE_COLS; i += 8) {
-              if (c + i >= p.h.head) break;
-              *reinterpret_cast<uint4*>(stage + att_stage_at(lane, i / 8)) =
-                  make_uint4(pack2<T>(o[i], o[i + 1]), pack2<T>(o[i + 2], o[i + 3]), pack2<T>(o[i + 4], o[i + 5]),
-                             pack2<T>(o[i + 6], o[i + 7]));
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              if (first < p.h.queries) tma_store_4d(&p.o, stage, c, it.group << p.h.pack_log2, first, it.b);
-              bulk_commit_group();
-            }
-            ++pieces;
-          }
-          held = false;
-        }
-      } while (++j < n);
-      if (end || !ok) break;
-      held = true;
-      last = now;
-      held_m = m;
-      held_l = l;
     }
     if (lane == 0) bulk_wait_group_all();
   }
