@@ -117,8 +117,11 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ 
 // dQ = dS K as well (five products instead of seven, exponentials taken once,
 // Q and dO read once): dS^T then goes to shared memory, where it is the left
 // operand of dK as it lies and that of dQ along its columns.
+constexpr int DKV_OUT_WARPS = 4;
 template <int DP, bool DQ>
 struct DkvShape {
+  static constexpr int LOADER = BWD_WARPS + (DQ ? DKV_OUT_WARPS : 0);  // the warp that loads; two more issue products
+  static constexpr int THREADS = 32 * (LOADER + 3);
   static constexpr uint32_t TILE = ATT_TILE<DP>;
   static constexpr int SLOTS = DP == 128 ? 4 : 8;  // tiles of dO and Q under way
   static constexpr int ROW_SLOTS = SLOTS / 2;      // -lse and -delta of as many query tiles
@@ -195,9 +198,9 @@ __device__ __forceinline__ void store_row16(T* out, float* part, const float (&v
 }
 
 template <typename T, int DP, bool DQ>
-__global__ void __launch_bounds__(BWD_THREADS, 1) attn_dkv_kernel(const __grid_constant__ DkvParams p) {
+__global__ void __launch_bounds__(DkvShape<DP, DQ>::THREADS, 1) attn_dkv_kernel(const __grid_constant__ DkvParams p) {
   using Shape = DkvShape<DP, DQ>;
-  constexpr int SLOTS = Shape::SLOTS;
+  constexpr int SLOTS = Shape::SLOTS, LOADER = Shape::LOADER;
   constexpr uint32_t TILE = Shape::TILE;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -231,8 +234,8 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) attn_dkv_kernel(const __grid_c
   if (threadIdx.x == 0) {
     for (int s = 0; s < SLOTS; ++s) {
       mbar_init(&full[s], 1);
-      // two products each; with DQ a tile of Q is freed by the warps, which send rows of dQ out of its memory
-      mbar_init(&empty[s], DQ && s % 2 == 1 ? BWD_WARPS : 2);
+      // two products each; with DQ a tile of Q is freed by the warps that send rows of dQ out of its memory
+      mbar_init(&empty[s], DQ && s % 2 == 1 ? DKV_OUT_WARPS : 2);
     }
     mbar_init(kv_full, 1);
     mbar_init(kv_empty, 2);
@@ -241,7 +244,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) attn_dkv_kernel(const __grid_c
     mbar_init(dp_full, 1);
     mbar_init(ds_ready, BWD_WARPS);
     mbar_init(dq_full, 1);
-    mbar_init(dq_read, BWD_WARPS);
+    mbar_init(dq_read, DKV_OUT_WARPS);
     mbar_init(acc_full, 2);
     mbar_init(acc_empty, BWD_WARPS);
     mbar_init(&drain_bar[0], 1);
@@ -249,7 +252,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) attn_dkv_kernel(const __grid_c
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == BWD_WARPS + 1) {
+  if (warp == LOADER + 1) {
     tmem_alloc(tmem_holder, 512);
     tmem_relinquish();
   }
@@ -267,7 +270,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) attn_dkv_kernel(const __grid_c
   const int tiles = p.h.query_tiles();
   const int per_head = p.rounds / tiles;  // groups of a key head
 
-  if (warp == BWD_WARPS) {
+  if (warp == LOADER) {
     if (lane == 0) {
       uint32_t n = 0, rounds = 0, items = 0;  // loads into the ring, rounds, items so far
       bool ok = true;
@@ -311,14 +314,14 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) attn_dkv_kernel(const __grid_c
         if (items) wait_drain(kv_full, (items - 1) & 1u, 50000000ull);
       }
     }
-  } else if (warp > BWD_WARPS) {
+  } else if (warp > LOADER) {
     // Two warps issue products: one S^T and dV, the other dP^T, dK and dQ. A wait that is already over costs 100
     // cycles, in which the other's products run.
     constexpr bool FP16 = !std::is_same<T, __nv_bfloat16>::value;
     const uint32_t id_s = idesc_f16kind_f32(ATT_ROWS, ATT_ROWS, false, false, FP16);
     const uint32_t id_acc = idesc_f16kind_f32(ATT_ROWS, p.mma_n, false, true, FP16);
     const uint32_t id_dq = idesc_f16kind_f32(ATT_ROWS, p.mma_n, true, true, FP16);
-    const int mine = warp - (BWD_WARPS + 1);
+    const int mine = warp - (LOADER + 1);
     uint32_t n = 0, rounds = 0, items = 0;  // ring tiles used up, rounds, items before this one
     bool ok = true, issued = false;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -430,6 +433,56 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) attn_dkv_kernel(const __grid_c
       if (elect_one()) umma_commit(&drain_bar[mine]);
       wait_drain(&drain_bar[mine], 0, 50000000ull);
     }
+  } else if (DQ && warp >= BWD_WARPS) {
+    // Four warps take rows of dQ out, by way of the memory of their Q, while the others form the next round's P and dS.
+    const uint32_t t_mine = t_dq + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    uint32_t rounds = 0, n = 1;  // n: the ring's next Q
+    bool ok = true;
+    for (uint32_t item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
+      const DkvItem it = dkv_item(p, item);
+      int group = it.kv_head * per_head + it.x0 / tiles, tile = it.x0 % tiles;
+      for (int i = 0; i < it.n; ++i, ++rounds, n += 2) {
+        const bool got = wait_bounded(dq_full, rounds & 1u, abort_flag, p.err, ATT_WAIT_NS);
+        if (!(ok = __all_sync(0xffffffffu, got))) break;
+        tc_fence_after_sync();
+        const uint32_t slot = n % SLOTS;
+        uint8_t* stage = ring + slot * TILE + (warp & 3) * (TILE / 4);
+#pragma unroll 1
+        for (int c = 0; c < p.h.head; c += ATT_STAGE_COLS) {
+          float v[ATT_STAGE_COLS];
+          tmem_load_32cols(t_mine + c, v);
+#pragma unroll
+          for (int u = 0; u < ATT_STAGE_COLS; u += 8) {
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = v[u + e] * p.scale;
+            Raw8<T> r;
+            r.set(x);
+            *reinterpret_cast<uint4*>(stage + c / ATT_STAGE_COLS * ATT_STAGE + att_stage_at(lane, u / 8)) = r.a;
+          }
+        }
+        tc_fence_before_sync();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(dq_read);
+          const int first = tile * p.h.tile_tokens() + (((warp & 3) * 32) >> p.h.pack_log2);
+          if (first < p.h.queries) {
+            for (int c = 0; c < p.h.head; c += ATT_STAGE_COLS)
+              tma_store_4d(&p.dq, stage + c / ATT_STAGE_COLS * ATT_STAGE, c, group << p.h.pack_log2, first, it.b);
+            bulk_commit_group();
+            bulk_wait_group_read<0>();
+          }
+          mbar_arrive(&empty[slot]);
+        }
+        __syncwarp();
+        if (++tile == tiles) {
+          tile = 0;
+          ++group;
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_group_all();
   } else {
     const int quarter = warp >> 2;  // query columns 32 quarter .. + 32
     const int row = threadIdx.x & 127;
@@ -447,87 +500,38 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) attn_dkv_kernel(const __grid_c
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
-    // Once the last store has read its memory (which takes as long as forming dS does).
-    auto free_q = [&](uint32_t slot) {
-      if (lane == 0) {
-        bulk_wait_group_read<0>();
-        mbar_arrive(&empty[slot]);
-      }
-      __syncwarp();
-    };
     bool ok = true;
     for (uint32_t item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
       const DkvItem it = dkv_item(p, item);
-      int group = 0, tile = 0;
-      if (DQ) {
-        group = it.kv_head * per_head + it.x0 / tiles;
-        tile = it.x0 % tiles;
-      }
-      // With DQ a round's rows of dQ are sent behind the next round's P, and the last one's in a round without P.
-      for (int i = 0; i < it.n + (DQ ? 1 : 0); ++i) {
+      for (int i = 0; i < it.n; ++i) {
         const float* values = sRows + (rounds % Shape::ROW_SLOTS) * ROW_VALUES + quarter * 32;
         float pr[32];
-        if (!DQ || i < it.n) {
-          // (S is complete once Q and its rows' values are there; the wait makes the copy visible here)
-          if (!(ok = wait(&full[n % SLOTS], (n / SLOTS) & 1u) && wait(s_full, rounds & 1u))) break;
-          const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
-          tmem_load_32cols(t_s + t_mine, pr);
+        // (S is complete once Q and its rows' values are there; the wait makes the copy visible here)
+        if (!(ok = wait(&full[n % SLOTS], (n / SLOTS) & 1u) && wait(s_full, rounds & 1u))) break;
+        const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
+        tmem_load_32cols(t_s + t_mine, pr);
 #pragma unroll
-          for (int c = 0; c < 32; c += 16) {
-            uint32_t w[8];
+        for (int c = 0; c < 32; c += 16) {
+          uint32_t w[8];
 #pragma unroll
-            for (int e = c; e < c + 16; e += 4) {
-              const float4 lse = *reinterpret_cast<const float4*>(values + e);
-              const float2 x = f2_unpack(f2_fma(f2_pack(pr[e], pr[e + 1]), sc2, f2_pack(lse.x, lse.y)));
-              const float2 y = f2_unpack(f2_fma(f2_pack(pr[e + 2], pr[e + 3]), sc2, f2_pack(lse.z, lse.w)));
-              pr[e] = exp2_fast(x.x);
-              pr[e + 1] = exp2_fast(x.y);
-              pr[e + 2] = exp2_fast(y.x);
-              pr[e + 3] = exp2_fast(y.y);
-              w[(e - c) / 2] = pack2<T>(pr[e], pr[e + 1]);
-              w[(e - c) / 2 + 1] = pack2<T>(pr[e + 2], pr[e + 3]);
-            }
-            tmem_store_8cols(t_s + t_mine + c / 2, w);
+          for (int e = c; e < c + 16; e += 4) {
+            const float4 lse = *reinterpret_cast<const float4*>(values + e);
+            const float2 x = f2_unpack(f2_fma(f2_pack(pr[e], pr[e + 1]), sc2, f2_pack(lse.x, lse.y)));
+            const float2 y = f2_unpack(f2_fma(f2_pack(pr[e + 2], pr[e + 3]), sc2, f2_pack(lse.z, lse.w)));
+            pr[e] = exp2_fast(x.x);
+            pr[e + 1] = exp2_fast(x.y);
+            pr[e + 2] = exp2_fast(y.x);
+            pr[e + 3] = exp2_fast(y.y);
+            w[(e - c) / 2] = pack2<T>(pr[e], pr[e + 1]);
+            w[(e - c) / 2 + 1] = pack2<T>(pr[e + 2], pr[e + 3]);
           }
-          tmem_store_wait();
-          arrive(p_ready);
+          tmem_store_8cols(t_s + t_mine + c / 2, w);
         }
-        if constexpr (DQ) {
-          if (i > 0) {
-            // These 32 columns of 32 rows of the last round's dQ go out of the memory of its Q.
-            if (!(ok = wait(dq_full, (rounds - 1) & 1u))) break;
-            const uint32_t slot = (n - 2) % SLOTS;
-            uint8_t* stage = ring + slot * TILE + warp * ATT_STAGE;
-            const bool some = quarter * 32 < p.h.head;  // (the same in all threads of a warp)
-            if (some) {
-              float v[32];
-              tmem_load_32cols(t_dq + t_mine, v);
-#pragma unroll
-              for (int u = 0; u < 32; u += 8) {
-                float x[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = v[u + e] * p.scale;
-                Raw8<T> r;
-                r.set(x);
-                *reinterpret_cast<uint4*>(stage + att_stage_at(lane, u / 8)) = r.a;
-              }
-              fence_proxy_async_smem();
-            }
-            arrive(dq_read);
-            if (some && lane == 0) {
-              const int last_tile = tile > 0 ? tile - 1 : tiles - 1, last_group = tile > 0 ? group : group - 1;
-              const int first = last_tile * p.h.tile_tokens() + (((warp & 3) * 32) >> p.h.pack_log2);
-              if (first < p.h.queries) {
-                tma_store_4d(&p.dq, stage, quarter * 32, last_group << p.h.pack_log2, first, it.b);
-                bulk_commit_group();
-              }
-            }
-            __syncwarp();
-            if (i == it.n) free_q(slot);
-          }
-          if (i == it.n) break;
-        }
+        tmem_store_wait();
+        arrive(p_ready);
         if (!(ok = wait(dp_full, rounds & 1u))) break;
+        // (the last round's products have read dS)
+        if (DQ && rounds > 0 && !(ok = wait(dq_full, (rounds - 1) & 1u))) break;
         // keys behind the last one may hold anything: dQ sums over keys, so their dS is zero
         const bool used = !DQ || row < it.length;
 #pragma unroll
@@ -563,22 +567,18 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) attn_dkv_kernel(const __grid_c
               for (int q = 0; q < DP / 64; ++q) k[q * (ATT_CHUNK / 16) + c] = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
-          if (++tile == tiles) {
-            tile = 0;
-            ++group;
-          }
         } else {
           tmem_store_wait();
         }
         arrive(ds_ready);
-        if (DQ && i > 0) free_q((n - 2) % SLOTS);
         ++rounds;
         n += 2;
       }
       if (!ok) break;
       if (DQ && it.n <= 0 && it.length <= 0) {
         // no keys: dQ is zero
-        for (int x = 0, g = group, q = tile; x < it.all; ++x) {
+        int g = it.kv_head * per_head + it.x0 / tiles, q = it.x0 % tiles;
+        for (int x = 0; x < it.all; ++x) {
           const int token = q * p.h.tile_tokens() + (row >> p.h.pack_log2);
           T* out = static_cast<T*>(p.dq_out) + it.b * p.dq_strides.batch + token * p.dq_strides.token +
                    ((g << p.h.pack_log2) + (row & ((1 << p.h.pack_log2) - 1))) * p.dq_strides.head;
@@ -618,13 +618,12 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) attn_dkv_kernel(const __grid_c
         ++items;
       }
     }
-    if (DQ && lane == 0) bulk_wait_group_all();
   }
   __syncwarp();
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  if (warp == BWD_WARPS + 1) tmem_dealloc(tmem, 512);
+  if (warp == LOADER + 1) tmem_dealloc(tmem, 512);
 }
 
 // --------------------------------------------------------------------- dQ
@@ -1050,7 +1049,7 @@ cudaError_t launch_dkv(const DkvParams& p, int num_sms, cudaStream_t stream) {
   const cudaError_t e = att_prepare(attn_dkv_kernel<T, DP, DQ>, SMEM, ready);
   if (e != cudaSuccess) return e;
   const unsigned grid = static_cast<unsigned>(std::min<uint32_t>(p.items, num_sms));
-  return launch_dependent(attn_dkv_kernel<T, DP, DQ>, dim3(grid), dim3(BWD_THREADS), SMEM, stream, p);
+  return launch_dependent(attn_dkv_kernel<T, DP, DQ>, dim3(grid), dim3(DkvShape<DP, DQ>::THREADS), SMEM, stream, p);
 }
 
 template <typename T, int DP>
