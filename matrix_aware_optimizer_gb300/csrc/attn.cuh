@@ -193,17 +193,18 @@ __device__ __forceinline__ void att_mma_cols(uint32_t d, uint32_t a, const uint8
 }
 
 // ------------------------------------------------------------------ output
-// A warp's 32 rows x 32 elements of a result go through 2 KB of shared memory
-// (in the swizzle of a 64-byte box) and out as one TMA store: rows stored by
+// A warp's 32 rows x 64 elements of a result go through 4 KB of shared memory
+// (in the swizzle of a 128-byte box) and out as one TMA store: rows stored by
 // their threads cost 32 cache lines an instruction (128 x 128 elements 3600 -
 // 6000 cycles that way). Rows outside the tensor and elements behind the head
 // are not written.
-constexpr uint32_t ATT_STAGE = 32 * 64;
-constexpr int ATT_STAGE_COLS = 32;
+constexpr uint32_t ATT_STAGE = 32 * 128;
+constexpr int ATT_PIECE = 32;  // elements of a row that are taken from tensor memory at a time
 
-// Where the unit-th eight elements of the lane's row lie.
-__device__ __forceinline__ uint32_t att_stage_at(int lane, int unit) {
-  return static_cast<uint32_t>(lane * 64 + ((unit ^ ((lane >> 1) & 3)) << 4));
+// Where eight elements of the lane's row lie, `element` of it the first, in
+// as many stages as the head has 64 elements.
+__device__ __forceinline__ uint32_t att_stage_at(int lane, int element) {
+  return (element >> 6) * ATT_STAGE + lane * 128 + (((element >> 3 & 7) ^ (lane & 7)) << 4);
 }
 __device__ __forceinline__ void tma_store_4d(const CUtensorMap* tm, const void* src, int x, int y, int z, int w) {
   asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(
@@ -257,10 +258,9 @@ cudaError_t att_prepare(void (*kernel)(Args...), size_t smem, std::atomic<uint64
   return e;
 }
 
-// Map over [batch][row][head][element]; box: 64 or 32 elements (in the swizzle
-// of as many bytes) x box_heads x box_rows.
+// Map over [batch][row][head][element]; box: 64 elements x box_heads x box_rows.
 bool att_encode(CUtensorMap* map, const void* base, int dtype, int64_t batch, int64_t rows, int64_t heads,
-                int64_t head, const AttStrides& s, int box_heads, int box_rows, int box_elements = 64);
+                int64_t head, const AttStrides& s, int box_heads, int box_rows);
 
 // One call's sizes and layouts, checked.
 struct AttCall {

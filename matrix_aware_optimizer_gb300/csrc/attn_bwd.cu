@@ -448,17 +448,17 @@ __global__ void __launch_bounds__(DkvShape<DP, DQ>::THREADS, 1) attn_dkv_kernel(
         const uint32_t slot = n % SLOTS;
         uint8_t* stage = ring + slot * TILE + (warp & 3) * (TILE / 4);
 #pragma unroll 1
-        for (int c = 0; c < p.h.head; c += ATT_STAGE_COLS) {
-          float v[ATT_STAGE_COLS];
+        for (int c = 0; c < p.h.head; c += ATT_PIECE) {
+          float v[ATT_PIECE];
           tmem_load_32cols(t_mine + c, v);
 #pragma unroll
-          for (int u = 0; u < ATT_STAGE_COLS; u += 8) {
+          for (int u = 0; u < ATT_PIECE; u += 8) {
             float x[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] = v[u + e] * p.scale;
             Raw8<T> r;
             r.set(x);
-            *reinterpret_cast<uint4*>(stage + c / ATT_STAGE_COLS * ATT_STAGE + att_stage_at(lane, u / 8)) = r.a;
+            *reinterpret_cast<uint4*>(stage + att_stage_at(lane, c + u)) = r.a;
           }
         }
         tc_fence_before_sync();
@@ -468,8 +468,8 @@ __global__ void __launch_bounds__(DkvShape<DP, DQ>::THREADS, 1) attn_dkv_kernel(
           mbar_arrive(dq_read);
           const int first = tile * p.h.tile_tokens() + (((warp & 3) * 32) >> p.h.pack_log2);
           if (first < p.h.queries) {
-            for (int c = 0; c < p.h.head; c += ATT_STAGE_COLS)
-              tma_store_4d(&p.dq, stage + c / ATT_STAGE_COLS * ATT_STAGE, c, group << p.h.pack_log2, first, it.b);
+            for (int c = 0; c < p.h.head; c += 64)
+              tma_store_4d(&p.dq, stage + c / 64 * ATT_STAGE, c, group << p.h.pack_log2, first, it.b);
             bulk_commit_group();
             bulk_wait_group_read<0>();
           }
@@ -1098,7 +1098,7 @@ cudaError_t attn_backward(const AttCall& c, const void* grad_o, const void* q, c
   const bool k_ok = att_encode(&a.k, k, c.dtype, h.batch, h.keys, h.kv_heads, h.head, c.k, 1, ATT_ROWS) &&
                     att_encode(&a.v, v, c.dtype, h.batch, h.keys, h.kv_heads, h.head, c.v, 1, ATT_ROWS);
   if (!q_ok || !k_ok ||
-      (s.one && !att_encode(&a.dq, dq, c.dtype, h.batch, h.queries, h.heads, h.head, c.dq, pack, 32 / pack, ATT_STAGE_COLS)))
+      (s.one && !att_encode(&a.dq, dq, c.dtype, h.batch, h.queries, h.heads, h.head, c.dq, pack, 32 / pack)))
     return cudaErrorInvalidValue;
   a.dq_out = dq;
   a.dq_strides = c.dq;

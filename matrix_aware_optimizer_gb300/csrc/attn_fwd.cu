@@ -55,7 +55,7 @@ static PFN_cuTensorMapEncodeTiled_v12000 att_encoder() {
 }
 
 bool att_encode(CUtensorMap* map, const void* base, int dtype, int64_t batch, int64_t rows, int64_t heads,
-                int64_t head, const AttStrides& s, int box_heads, int box_rows, int box_elements) {
+                int64_t head, const AttStrides& s, int box_heads, int box_rows) {
   auto enc = att_encoder();
   if (enc == nullptr) return false;
   cuuint64_t dims[4] = {static_cast<cuuint64_t>(head), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows),
@@ -65,11 +65,11 @@ bool att_encode(CUtensorMap* map, const void* base, int dtype, int64_t batch, in
     return static_cast<cuuint64_t>(extent > 1 ? stride : round_up(static_cast<size_t>(head), 8)) * 2;
   };
   cuuint64_t strides[3] = {bytes(heads, s.head), bytes(rows, s.token), bytes(batch, s.batch)};
-  cuuint32_t box[4] = {static_cast<cuuint32_t>(box_elements), static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows), 1u};
+  cuuint32_t box[4] = {64u, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows), 1u};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   return enc(map, dtype == PRM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
              const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             box_elements == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -88,12 +88,15 @@ bool encode_box(CUtensorMap* map, const void* base, int dtype, int64_t rows, int
 
 namespace {
 
-// Warps 0 .. 3 and 4 .. 7 take the two tiles' rows, 8 loads, 9 and 10 issue the
-// two tiles' products: a wait that is already over costs 100 cycles, in which
-// the other warp's products run (with one warp for both tiles a key tile took
-// 3700 cycles at 8192 x 8192, the tensor cores at work 2400 of them).
+// Warps 0 .. 3 and 4 .. 7 take the two tiles' exponentials, 8 .. 11 write rows
+// of O, 12 loads, 13 and 14 issue the two tiles' products: a wait that is
+// already over costs 100 cycles, in which the other warp's products run (with
+// one warp for both tiles a key tile took 3700 cycles at 8192 x 8192, the tensor
+// cores at work 2400 of them).
 constexpr int FWD_WARPS = 8;
-constexpr int FWD_THREADS = 32 * (FWD_WARPS + 3);
+constexpr int FWD_OUT_WARPS = 4;
+constexpr int FWD_LOADER = FWD_WARPS + FWD_OUT_WARPS;
+constexpr int FWD_THREADS = 32 * (FWD_LOADER + 3);
 constexpr float RESCALE_ABOVE = 8.f;
 
 template <int DP>
@@ -101,7 +104,9 @@ struct FwdShape {
   static constexpr int STAGES = DP == 128 ? 4 : 8;  // of one key or value tile
   static constexpr uint32_t TILE = ATT_TILE<DP>;
   static constexpr size_t BARRIERS = 512;
-  static constexpr size_t SMEM = 1024 + (2 + STAGES) * TILE + FWD_WARPS * 2 * ATT_STAGE + BARRIERS;
+  static constexpr uint32_t OUT = DP / 64 * ATT_STAGE;  // a warp's rows of O
+  static constexpr size_t SMEM =
+      1024 + (2 + STAGES) * TILE + FWD_OUT_WARPS * OUT + 2 * ATT_ROWS * sizeof(float) + BARRIERS;
 };
 static_assert(FwdShape<128>::SMEM <= 232448 && FwdShape<64>::SMEM <= 232448, "shared memory above 227 KB");
 
@@ -193,7 +198,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) attn_fwd_kernel(const __grid_c
   uint8_t* sQ = smem;
   uint8_t* sKV = smem + 2 * TILE;
   uint8_t* sOut = sKV + STAGES * TILE;
-  uint64_t* kv_full = reinterpret_cast<uint64_t*>(sOut + FWD_WARPS * 2 * ATT_STAGE);
+  float* sInv = reinterpret_cast<float*>(sOut + FWD_OUT_WARPS * Shape::OUT);  // [tile][row] one over the row's sum
+  uint64_t* kv_full = reinterpret_cast<uint64_t*>(sInv + 2 * ATT_ROWS);
   uint64_t* kv_empty = kv_full + STAGES;
   uint64_t* q_full = kv_empty + STAGES;
   uint64_t* q_empty = q_full + 2;
@@ -201,7 +207,9 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) attn_fwd_kernel(const __grid_c
   uint64_t* p_full = s_full + 2;  // [tile][half]: of the keys 0 .. 63, 64 .. 127
   uint64_t* pv_done = p_full + 4;
   uint64_t* o_empty = pv_done + 2;
-  uint64_t* drain_bar = o_empty + 2;
+  uint64_t* o_full = o_empty + 2;    // an item's last product is done
+  uint64_t* inv_full = o_full + 2;
+  uint64_t* drain_bar = inv_full + 2;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain_bar + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
@@ -219,14 +227,16 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) attn_fwd_kernel(const __grid_c
       mbar_init(&p_full[2 * t], FWD_WARPS / 2);
       mbar_init(&p_full[2 * t + 1], FWD_WARPS / 2);
       mbar_init(&pv_done[t], 1);
-      mbar_init(&o_empty[t], FWD_WARPS / 2);
+      mbar_init(&o_empty[t], FWD_OUT_WARPS);
+      mbar_init(&o_full[t], 1);
+      mbar_init(&inv_full[t], FWD_WARPS / 2);
     }
     mbar_init(&drain_bar[0], 1);
     mbar_init(&drain_bar[1], 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == FWD_WARPS + 1) {
+  if (warp == FWD_LOADER + 1) {
     tmem_alloc(tmem_holder, 512);
     tmem_relinquish();
   }
@@ -237,7 +247,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) attn_fwd_kernel(const __grid_c
   pdl_wait();
   pdl_launch_dependents();
 
-  if (warp == FWD_WARPS) {
+  if (warp == FWD_LOADER) {
     if (lane == 0) {
       uint32_t kv = 0;                 // key and value tiles loaded so far
       uint32_t q_turn = 0, q_any = 0;  // bit t: phase of tile t's next load; whether there was one
@@ -278,11 +288,11 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) attn_fwd_kernel(const __grid_c
           if (q_any >> t & 1u) wait_drain(&q_full[t], ((q_turn >> t) & 1u) ^ 1u, 50000000ull);
       }
     }
-  } else if (warp > FWD_WARPS) {
+  } else if (warp > FWD_LOADER) {
     constexpr bool FP16 = !std::is_same<T, __nv_bfloat16>::value;
     const uint32_t id_s = idesc_f16kind_f32(ATT_ROWS, 0, false, false, FP16);  // (N: the keys of the tile)
     const uint32_t id_o = idesc_f16kind_f32(ATT_ROWS, p.mma_n, false, true, FP16);
-    const int t = warp - (FWD_WARPS + 1);  // this warp's query tile
+    const int t = warp - (FWD_LOADER + 1);  // this warp's query tile
     const uint32_t t_s = tmem + t * ATT_ROWS, t_o = tmem + 2 * ATT_ROWS + t * DP;
     const uint8_t* q = sQ + t * TILE;
     uint32_t kv = 0;                                // key and value tiles used up
@@ -354,6 +364,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) attn_fwd_kernel(const __grid_c
         if (elect_one()) {
           if (steps > 4) att_mma_cols<64, 4, 8>(t_o, t_s, v, id_o, true, steps);
           umma_commit(&pv_done[t]);
+          if (j + 1 == n) umma_commit(&o_full[t]);
           umma_commit(&kv_empty[stage]);
         }
         __syncwarp();
@@ -368,6 +379,73 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) attn_fwd_kernel(const __grid_c
       if (elect_one()) umma_commit(&drain_bar[t]);
       wait_drain(&drain_bar[t], 0, 50000000ull);
     }
+  } else if (warp >= FWD_WARPS) {
+    // Rows of O, while the others take the next item's exponentials.
+    const int row = (warp & 3) * 32 + lane;
+    uint8_t* stage = sOut + (warp & 3) * Shape::OUT;
+    uint32_t turn = 0;  // bit t: phase of tile t's next waits
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      const bool got = wait_bounded(bar, parity, abort_flag, p.err, ATT_WAIT_NS);
+      if (!__all_sync(0xffffffffu, got)) return false;
+      tc_fence_after_sync();
+      return true;
+    };
+    for (uint32_t item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
+      const FwdItem it = fwd_item(p, item);
+      const bool some = it.n > 0;  // (else its rows are zero)
+      for (int t = 0; t < it.tiles; ++t) {
+        float inv = 0.f;
+        if (some) {
+          if (!(ok = wait(&inv_full[t], turn >> t & 1u) && wait(&o_full[t], turn >> t & 1u))) break;
+          turn ^= 1u << t;
+          inv = sInv[t * ATT_ROWS + row];
+        }
+        const int token = (it.block * 2 + t) * p.h.tile_tokens() + (row >> p.h.pack_log2);
+        const int first = token - (lane >> p.h.pack_log2);  // the warp's first token
+        const uint32_t t_o = tmem + 2 * ATT_ROWS + t * DP + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        float* part = it.slot < 0 ? nullptr
+                                  : p.part_o + static_cast<int64_t>(it.slot * (2 * ATT_ROWS) + t * ATT_ROWS + row) * p.h.head;
+        if (lane == 0) bulk_wait_group_read<0>();  // the last tile's stores have read their memory
+        __syncwarp();
+#pragma unroll 1
+        for (int c = 0; c < p.h.head; c += ATT_PIECE) {
+          float o[ATT_PIECE];
+          if (some) tmem_load_32cols(t_o + c, o);
+#pragma unroll
+          for (int i = 0; i < ATT_PIECE; ++i) o[i] = some ? o[i] * inv : 0.f;
+          if (part != nullptr) {
+#pragma unroll
+            for (int i = 0; i < ATT_PIECE; i += 8) {
+              if (c + i >= p.h.head || token >= p.h.queries) break;
+              float4* to = reinterpret_cast<float4*>(part + c + i);
+              to[0] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+              to[1] = make_float4(o[i + 4], o[i + 5], o[i + 6], o[i + 7]);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < ATT_PIECE; i += 8)
+              *reinterpret_cast<uint4*>(stage + att_stage_at(lane, c + i)) =
+                  make_uint4(pack2<T>(o[i], o[i + 1]), pack2<T>(o[i + 2], o[i + 3]), pack2<T>(o[i + 4], o[i + 5]),
+                             pack2<T>(o[i + 6], o[i + 7]));
+          }
+          __syncwarp();
+        }
+        tc_fence_before_sync();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (some) mbar_arrive(&o_empty[t]);
+          if (part == nullptr && first < p.h.queries) {
+            for (int c = 0; c < p.h.head; c += 64)
+              tma_store_4d(&p.o, stage + c / 64 * ATT_STAGE, c, it.group << p.h.pack_log2, first, it.b);
+            bulk_commit_group();
+          }
+        }
+        __syncwarp();
+      }
+    }
+    if (lane == 0) bulk_wait_group_all();
   } else {
     const int t = warp >> 2;
     const int row = threadIdx.x & 127;
@@ -387,7 +465,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) attn_fwd_kernel(const __grid_c
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
-    uint32_t pieces = 0;  // stores so far, from two buffers in turn
+    uint32_t o_turn = 1;  // phase of the next wait for O's way out
     bool ok = true;
     for (uint32_t item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
       const FwdItem it = fwd_item(p, item);
@@ -472,73 +550,31 @@ __global__ void __launch_bounds__(FWD_THREADS, 1) attn_fwd_kernel(const __grid_c
         ++steps;
       }
       if (!ok) break;
-      // The rows are written while the next item's first S is formed. (Written behind that item's first exponentials
-      // they hide the last product, but its own first product then waits for O: 16 x 1024 queries of 16 x 128 on 256
-      // keys 56 us that way, 50 this way.)
       const bool some = n > 0;
-      if (some && !(ok = wait(&pv_done[t], (steps - 1) & 1u))) break;
       const int token = (it.block * 2 + t) * p.h.tile_tokens() + (row >> p.h.pack_log2);
       const int head = (it.group << p.h.pack_log2) + (row & ((1 << p.h.pack_log2) - 1));
-      const bool live = token < p.h.queries;
-      const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-      if (live) {
-        const int64_t at = (static_cast<int64_t>(it.b) * p.h.heads + head) * p.h.queries + token;
+      if (some) {
+        // (the last item's have been read once its O has)
+        if (!(ok = wait(&o_empty[t], o_turn))) break;
+        o_turn ^= 1u;
+        sInv[t * ATT_ROWS + row] = l > 0.f || l != l ? 1.f / l : 0.f;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&inv_full[t]);
+      }
+      if (token < p.h.queries) {
         const float lse = some ? m * p.scale_log2 + log2f(l) : -INFINITY;
         if (it.slot >= 0)
           p.part_lse[it.slot * (2 * ATT_ROWS) + t * ATT_ROWS + row] = lse;
         else if (p.lse != nullptr)
-          p.lse[at] = lse;
-      }
-      float* part = p.part_o + static_cast<int64_t>(it.slot * (2 * ATT_ROWS) + t * ATT_ROWS + row) * p.h.head;
-      const int first = token - (lane >> p.h.pack_log2);  // the warp's first token
-#pragma unroll 1
-      for (int c = 0; c < p.h.head; c += ATT_STAGE_COLS) {
-        float o[ATT_STAGE_COLS];
-        __syncwarp();
-        if (some) tmem_load_32cols(t_o + c, o);
-        if (some && c + ATT_STAGE_COLS >= p.h.head) {  // O has been read
-          tc_fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&o_empty[t]);
-        }
-#pragma unroll
-        for (int i = 0; i < ATT_STAGE_COLS; ++i) o[i] = some ? o[i] * inv : 0.f;
-        if (it.slot >= 0) {
-#pragma unroll
-          for (int i = 0; i < ATT_STAGE_COLS; i += 8) {
-            if (c + i >= p.h.head || !live) break;
-            float4* to = reinterpret_cast<float4*>(part + c + i);
-            to[0] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-            to[1] = make_float4(o[i + 4], o[i + 5], o[i + 6], o[i + 7]);
-          }
-          continue;
-        }
-        uint8_t* stage = sOut + (warp * 2 + (pieces & 1u)) * ATT_STAGE;
-        if (lane == 0) bulk_wait_group_read<1>();  // the store before the last one has read this buffer
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < ATT_STAGE_COLS; i += 8) {
-          if (c + i >= p.h.head) break;
-          *reinterpret_cast<uint4*>(stage + att_stage_at(lane, i / 8)) =
-              make_uint4(pack2<T>(o[i], o[i + 1]), pack2<T>(o[i + 2], o[i + 3]), pack2<T>(o[i + 4], o[i + 5]),
-                         pack2<T>(o[i + 6], o[i + 7]));
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          if (first < p.h.queries) tma_store_4d(&p.o, stage, c, it.group << p.h.pack_log2, first, it.b);
-          bulk_commit_group();
-        }
-        ++pieces;
+          p.lse[(static_cast<int64_t>(it.b) * p.h.heads + head) * p.h.queries + token] = lse;
       }
     }
-    if (lane == 0) bulk_wait_group_all();
   }
   __syncwarp();
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  if (warp == FWD_WARPS + 1) tmem_dealloc(tmem, 512);
+  if (warp == FWD_LOADER + 1) tmem_dealloc(tmem, 512);
 }
 
 // Parts of the keys joined: lse = log2 sum 2^lse_s, o = sum 2^(lse_s - lse) o_s.
@@ -700,7 +736,7 @@ cudaError_t attn_forward(const AttCall& c, const void* q, const void* k, const v
     p.part_lse = p.part_o + static_cast<int64_t>(p.share.rest) * p.share.parts * 2 * ATT_ROWS * c.h.head;
   const int pack = 1 << c.h.pack_log2;
   if (!att_encode(&p.q, q, c.dtype, c.h.batch, c.h.queries, c.h.heads, c.h.head, c.q, pack, ATT_ROWS / pack) ||
-      !att_encode(&p.o, o, c.dtype, c.h.batch, c.h.queries, c.h.heads, c.h.head, c.o, pack, 32 / pack, ATT_STAGE_COLS) ||
+      !att_encode(&p.o, o, c.dtype, c.h.batch, c.h.queries, c.h.heads, c.h.head, c.o, pack, 32 / pack) ||
       !att_encode(&p.k, k, c.dtype, c.h.batch, c.h.keys, c.h.kv_heads, c.h.head, c.k, 1, ATT_ROWS) ||
       !att_encode(&p.v, v, c.dtype, c.h.batch, c.h.keys, c.h.kv_heads, c.h.head, c.v, 1, ATT_ROWS))
     return cudaErrorInvalidValue;
