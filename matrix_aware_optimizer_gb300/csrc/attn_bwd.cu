@@ -51,6 +51,15 @@ constexpr size_t BWD_BARRIERS = 512;
 // ------------------------------------------------------------- -lse, -delta
 // A block takes a query tile: eight threads to a row, which they read 16 bytes
 // at a time, four rows each.
+//
+// delta is the sum of dO o, with o as the forward pass rounded it, or for a
+// sequence of up to four keys that of P dP, formed here: there dS is a small
+// difference, and o's rounding was half of the gradients' error (2 keys, heads
+// of 128, bf16: dQ 0.0047 off with o, 0.0024 with P dP, which are dS' and dQ's
+// own roundings; 4 keys 0.0034 and 0.0025, 8 keys 0.0031 and 0.0025). Each key
+// costs two products of every row on CUDA cores: with a limit of 16 keys 32 x
+// 1024 queries on ragged captions took 260 us instead of 223, both passes.
+constexpr int ROWS_FEW_KEYS = 4;
 struct RowsParams {
   AttHeads h;
   AttStrides o, grad_o;
@@ -58,10 +67,33 @@ struct RowsParams {
   const void* gp;
   const float* lse;
   float* rows;  // [batch][group][query tile][ROW_VALUES]
+  AttStrides q, k, v;
+  const void* qp;
+  const void* kp;
+  const void* vp;
+  AttLengths lengths;
+  float scale_log2;
 };
 
+// Sum of x y over the eight threads of a row.
+template <typename T, int VECTORS>
+__device__ __forceinline__ float row_dot(const Raw8<T> (&x)[VECTORS], const Raw8<T> (&y)[VECTORS]) {
+  float sum = 0.f;
+#pragma unroll
+  for (int v = 0; v < VECTORS; ++v) {
+    float a[8], c[8];
+    x[v].get(a);
+    y[v].get(c);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum = fmaf(a[e], c[e], sum);
+  }
+#pragma unroll
+  for (int i = 4; i > 0; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
+  return sum;
+}
+
 template <typename T, int DP>
-__global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ RowsParams p) {
+__global__ void __launch_bounds__(256, 3) attn_rows_kernel(const __grid_constant__ RowsParams p) {
   pdl_wait();
   pdl_launch_dependents();
   constexpr int VECTORS = DP / 64, ROWS = 4;
@@ -70,8 +102,46 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ 
   const int b = static_cast<int>(bg / groups), group = static_cast<int>(bg - b * groups);
   const int part = threadIdx.x & 7, r0 = threadIdx.x >> 3;
   const int first = static_cast<int>(tile) * p.h.tile_tokens(), pack = 1 << p.h.pack_log2;
-  const T* o = static_cast<const T*>(p.op) + b * p.o.batch + part * 8;
   const T* g = static_cast<const T*>(p.gp) + b * p.grad_o.batch + part * 8;
+  float* out = p.rows + static_cast<int64_t>(blockIdx.x) * ROW_VALUES + r0;
+  const int length = att_length(p.lengths, b, p.h.keys);
+  if (length <= ROWS_FEW_KEYS) {  // (the same in all threads)
+    const int kv = p.h.kv_head(group);
+    const T* q = static_cast<const T*>(p.qp) + b * p.q.batch + part * 8;
+    const T* keys = static_cast<const T*>(p.kp) + b * p.k.batch + kv * p.k.head + part * 8;
+    const T* values = static_cast<const T*>(p.vp) + b * p.v.batch + kv * p.v.head + part * 8;
+    auto load = [&](Raw8<T>(&x)[VECTORS], const T* from, bool live) {
+#pragma unroll
+      for (int v = 0; v < VECTORS; ++v) {
+        x[v].zero();
+        if (live && (v * 8 + part) * 8 < p.h.head) x[v].load(from + v * 64);
+      }
+    };
+#pragma unroll 1
+    for (int r = r0; r < ATT_ROWS; r += 32) {
+      const int token = first + (r >> p.h.pack_log2), head = group * pack + (r & (pack - 1));
+      const bool live = token < p.h.queries && length > 0;
+      float lse = -INFINITY, delta = 0.f;
+      if (live) lse = p.lse[(static_cast<int64_t>(b) * p.h.heads + head) * p.h.queries + token];
+      Raw8<T> qv[VECTORS], gv[VECTORS];
+      load(qv, q + token * p.q.token + head * p.q.head, live);
+      load(gv, g + token * p.grad_o.token + head * p.grad_o.head, live);
+#pragma unroll 2
+      for (int j = 0; j < length; ++j) {
+        Raw8<T> kj[VECTORS], vj[VECTORS];
+        load(kj, keys + j * p.k.token, true);
+        load(vj, values + j * p.v.token, true);
+        const float s = row_dot(qv, kj), dp = row_dot(gv, vj);
+        if (live) delta = fmaf(exp2f(fmaf(s, p.scale_log2, -lse)), dp, delta);
+      }
+      if (part == 0) {
+        out[r - r0] = lse == -INFINITY ? -INFINITY : -lse;  // a row without keys: P is zero
+        out[r - r0 + ATT_ROWS] = -delta;
+      }
+    }
+    return;
+  }
+  const T* o = static_cast<const T*>(p.op) + b * p.o.batch + part * 8;
   Raw8<T> ov[ROWS][VECTORS], gv[ROWS][VECTORS];
   float lse[ROWS];
 #pragma unroll
@@ -93,21 +163,10 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ 
   }
 #pragma unroll
   for (int k = 0; k < ROWS; ++k) {
-    float delta = 0.f;
-#pragma unroll
-    for (int v = 0; v < VECTORS; ++v) {
-      float a[8], c[8];
-      ov[k][v].get(a);
-      gv[k][v].get(c);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) delta = fmaf(a[e], c[e], delta);
-    }
-#pragma unroll
-    for (int i = 4; i > 0; i >>= 1) delta += __shfl_xor_sync(0xffffffffu, delta, i);
+    const float delta = row_dot(ov[k], gv[k]);
     if (part == 0) {
-      float* out = p.rows + static_cast<int64_t>(blockIdx.x) * ROW_VALUES + r0 + 32 * k;
-      out[0] = lse[k] == -INFINITY ? -INFINITY : -lse[k];  // a row without keys: P is zero
-      out[ATT_ROWS] = -delta;
+      out[32 * k] = lse[k] == -INFINITY ? -INFINITY : -lse[k];
+      out[32 * k + ATT_ROWS] = -delta;
     }
   }
 }
@@ -1089,7 +1148,7 @@ cudaError_t attn_backward(const AttCall& c, const void* grad_o, const void* q, c
   const Plan s = plan(h, c.num_sms);
   float* values = reinterpret_cast<float*>(workspace);
   const int tiles = h.query_tiles(), pack = 1 << h.pack_log2;
-  const RowsParams r{h, c.o, c.grad_o, o, grad_o, lse, values};
+  const RowsParams r{h,   c.o, c.grad_o, o, grad_o, lse, values, c.q, c.k, c.v, q, k, v, c.lengths, c.scale * 1.4426950408889634f};
   DkvParams a{};
   DqParams b{};
   const bool q_ok = att_encode(&a.q, q, c.dtype, h.batch, h.queries, h.heads, h.head, c.q, pack, ATT_ROWS / pack) &&

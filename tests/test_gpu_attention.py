@@ -481,3 +481,35 @@ def test_attention_gradients_of_one_key():
     assert (dq.double().abs() <= 1.01 * scale * off[..., None] * k.repeat_interleave(2, 2).double().abs() + 1e-30).all()
     bound = (off[..., None] * q.double().abs()).sum(1, keepdim=True).unflatten(2, (2, 2)).sum(3)
     assert (dk.double().abs() <= 1.01 * scale * bound + 1e-30).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, torch.float16])
+@pytest.mark.parametrize("Lk, Hkv, D", [(1, 2, 64), (2, 4, 128), (3, 1, 32), (4, 2, 72), (5, 4, 128), (300, 2, 64)])
+def test_attention_gradients_of_few_keys(Lk, Hkv, D, dtype):
+    """With up to four keys delta has no rounding of o in it: what is left are dS'
+    rounding, a half step of each of its values, and the result's own."""
+    q, k, v, do = _attention_inputs(5, 130, Lk, 4, Hkv, D, dtype)
+    lengths = torch.tensor([Lk, min(Lk, 2), 1, min(Lk, 4), 0], device="cuda")
+    o, saved = prm.cross_attention(q, k, v, lengths, save=True)
+    dq, dk, dv = prm.cross_attention_backward(do, q, k, v, o, saved, lengths)
+    half = torch.finfo(dtype).eps / 2
+    tiny = torch.finfo(dtype).tiny * torch.finfo(dtype).eps  # the least step
+    scale = D ** -0.5
+    for b, n in enumerate(lengths.tolist()):
+        if n == 0 or n > 4:
+            continue
+        Q, G = (t[b].double().transpose(0, 1) for t in (q, do))
+        K, V = (t[b, :n].double().transpose(0, 1).repeat_interleave(4 // Hkv, 0) for t in (k, v))
+        P = (scale * Q @ K.transpose(1, 2)).softmax(-1)
+        dP = G @ V.transpose(1, 2)
+        dS = P * (dP - (P * dP).sum(-1, keepdim=True))
+        # fp32: P to 2^-20 of its value (scores below 100, their logarithm's rounding), sums of up to 128 products
+        small = 2.0 ** -14 * P * (G.abs() @ V.abs().transpose(1, 2)).amax(-1, keepdim=True)
+        off = half * dS.abs() + small + tiny
+        want, bound = scale * dS @ K, scale * off @ K.abs()
+        err = (dq[b].double().transpose(0, 1) - want).abs()
+        assert (err <= 1.01 * (bound + half * (want.abs() + bound)) + tiny).all()
+        want = (scale * dS.transpose(1, 2) @ Q).unflatten(0, (Hkv, 4 // Hkv)).sum(1)
+        bound = (scale * off.transpose(1, 2) @ Q.abs()).unflatten(0, (Hkv, 4 // Hkv)).sum(1)
+        err = (dk[b, :n].double().transpose(0, 1) - want).abs()
+        assert (err <= 1.01 * (bound + half * (want.abs() + bound)) + tiny).all()
