@@ -25,15 +25,16 @@
 //
 // P and dS are rounded to 16 bits as operands of the next product; S, dP, the
 // gradients' sums, lse and delta are fp32. delta takes o as the forward pass
-// rounded it.
+// rounded it, or comes from P dP (a few keys, below).
 //
 // Measured, bf16, 16 heads: 2 x 4096 queries and keys of 128 705 us (0.98
 // PFLOP/s of the five products that are needed, 1.37 of the seven that are
 // formed: rows 14, dK and dV 408, dQ 275, the tensor pipe active 59 and 66 % of
 // the time), 2 x 8192 2553 (1.08). Bound by the chain S - P - dV, dP - dS - dK of
 // each tile, whose two halves cover each other's waits. 32 x 1024 queries of 72
-// on up to 120 keys 182 us (rows 32, the one pass 127 - 129) where the bytes
-// take 38: a round's steps follow one another (about 6500 cycles).
+// on 120 keys 165 us (rows 32, the one pass 113) where the bytes take 38: a
+// round's steps follow one another (about 5500 cycles; 6500, and 184 us, where
+// the warps that form P and dS also take dQ out).
 #include <algorithm>
 #include <type_traits>
 

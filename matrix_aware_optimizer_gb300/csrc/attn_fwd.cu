@@ -23,14 +23,16 @@
 // tensor pipe in that order: S of the next key tile overwrites P only behind
 // the product that reads it.
 //
-// Measured, bf16, 16 heads of 128: 2 x 8192 queries and keys 814 - 845 us
-// (1.30 - 1.35 PFLOP/s, 0.68 - 0.70 of the measured rate of a large product),
-// 2 x 4096 236 us (1.16; the tensor pipe is active 53 % of the time). Bound by
-// the exponentials' warps: per key tile and pair of query tiles the products
-// take 2048 cycles, a warpgroup's load, maximum, exponentials and store of its
-// 128 x 128 about as many, with the waits between them. 16 x 1024 queries on up
-// to 250 keys 45 - 51 us where the bytes take 22: two key tiles to an item, of
-// which the first S, the last product and the rows' way out are not covered.
+// Measured, bf16, 16 heads of 128: 2 x 8192 queries and keys 795 - 804 us
+// (1.37 - 1.38 PFLOP/s, 0.72 of the measured rate of a large product), 2 x 4096
+// 221 (1.24; the tensor pipe is active 58 % of the time). Bound by the chain S -
+// exponentials - P V of each tile: per key tile the products take 1024 cycles, a
+// warpgroup's maximum, exponentials and stores 1500, its wait for the next S
+// 1500, in which the other tile's products run. 16 x 1024 queries on up to 250
+// keys 44 - 46 us where the bytes take 22; 32 x 1024 of 72 elements on 120 keys
+// 62 - 65 where they take 24: an item is one or two key tiles, and its
+// exponentials, its rows' way out (2700 cycles a tile) and the products between
+// them follow one another.
 #include <algorithm>
 #include <mutex>
 #include <type_traits>
